@@ -1,0 +1,438 @@
+// kvpool_window.cu -- attention of a ragged batch of queries over raw K/V
+// tokens with a sliding window and a few first tokens that stay visible: what
+// computes a prompt's own outputs in a window layer while append takes its
+// tokens into the cache ("Why does V4 split pools? ..." s3.3: the window is
+// the exact local part of attention).
+//
+//   out = sum_t softmax_t(scale <q, k_t>) v_t over t <= p with t > p - window
+//   or t < n_sink;  lse = log sum_t exp(scale <q, k_t>);  a query that sees
+//   nothing gives zeros and -inf.
+#include <algorithm>
+#include <cmath>
+#include <cstddef>
+#include <memory>
+#include <new>
+
+#include <cuda_runtime.h>
+
+#include "kvpool_window.h"
+
+namespace kvp {
+namespace {
+
+__device__ uint32_t g_ops_error;  // device error word of the calls that have no pool
+
+__device__ __forceinline__ float ex2f(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <int T>
+__device__ __forceinline__ float4 load4(const uint8_t* base, int64_t i) {
+  if constexpr (T == KVPOOL_F32) {
+    return *reinterpret_cast<const float4*>(base + 4 * i);
+  } else {
+    const uint2 r = *reinterpret_cast<const uint2*>(base + 2 * i);
+    return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xFFFF0000u), __uint_as_float(r.y << 16),
+                       __uint_as_float(r.y & 0xFFFF0000u));
+  }
+}
+template <int T>
+__device__ __forceinline__ void store4(uint8_t* base, int64_t i, float4 x) {
+  if constexpr (T == KVPOOL_F32) {
+    *reinterpret_cast<float4*>(base + 4 * i) = x;
+  } else {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
+    *reinterpret_cast<uint2*>(base + 2 * i) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  }
+}
+
+// ---- fp32 FMA tiles -----------------------------------------------------------
+// 64 rows x 32 keys per step in fp32 shared memory, 256 threads: thread (ty,
+// tx) owns rows 4 ty .. 4 ty + 3, keys tx and tx + 16 of the scores, and dims
+// 4 tx .. 4 tx + 3 (and 64 more) of the outputs.  The running maximum and sum
+// live in registers, the same in a row's 16 threads.
+constexpr int kFmaRows = 64, kFmaKeys = 32, kFmaThreads = 256;
+
+template <int D>
+struct FmaSmem {
+  float q[kFmaRows][D + 4];
+  float k[kFmaKeys][D + 4];
+  float v[kFmaKeys][D];
+  float p[kFmaRows][kFmaKeys + 4];
+};
+
+template <int T, int D>
+__global__ void __launch_bounds__(kFmaThreads) window_fma_kernel(const __grid_constant__ WinParams P) {
+  pdl_start();
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  FmaSmem<D>& sm = *reinterpret_cast<FmaSmem<D>*>(smem_raw);
+  const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
+  const WinItem w = win_item(P, blockIdx.x);
+  const WinSeg& S = P.segs[w.seg];
+  const int rows = w.n_tok * P.group;
+  for (int i = tid; i < kFmaRows * (D / 4); i += kFmaThreads) {
+    const int r = i / (D / 4), c = 4 * (i % (D / 4));
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < rows)
+      x = load4<T>(P.q, (S.q_row0 + w.tok0 + r / P.group) * P.q_tok +
+                            (int64_t)(w.hk * P.group + r % P.group) * P.q_head + c);
+    *reinterpret_cast<float4*>(&sm.q[r][c]) = x;
+  }
+  int pos[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) pos[r] = 4 * ty + r < rows ? w.pos0 + (4 * ty + r) / P.group : -1;
+  float m[4], l[4], o[4][D / 16];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    m[r] = -INFINITY;
+    l[r] = 0.0f;
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) o[r][c] = 0.0f;
+  }
+  // steps over the first n_s tokens, then over the window's; this split's share
+  const int st_s = (w.n_s + kFmaKeys - 1) / kFmaKeys, st_w = (w.n_w + kFmaKeys - 1) / kFmaKeys;
+  const int n_st = st_s + st_w;
+  const int a = (int)((int64_t)n_st * w.split / w.n_split), b = (int)((int64_t)n_st * (w.split + 1) / w.n_split);
+  for (int st = a; st < b; ++st) {
+    const bool sink = st < st_s;
+    const int t0 = sink ? st * kFmaKeys : w.lo + (st - st_s) * kFmaKeys;
+    const int end = sink ? w.n_s : w.lo + w.n_w;  // tokens from here on are nobody's: read as zeros
+    __syncthreads();
+    for (int i = tid; i < kFmaKeys * (D / 4); i += kFmaThreads) {
+      const int r = i / (D / 4), c = 4 * (i % (D / 4));
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+      if (t0 + r < end) {
+        x = load4<T>(P.k, (S.k_start + t0 + r) * P.k_tok + w.hk * P.k_head + c);
+        y = load4<T>(P.v, (S.k_start + t0 + r) * P.v_tok + w.hk * P.v_head + c);
+      }
+      *reinterpret_cast<float4*>(&sm.k[r][c]) = x;
+      *reinterpret_cast<float4*>(&sm.v[r][c]) = y;
+    }
+    __syncthreads();
+    float s[4][2];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) s[r][0] = s[r][1] = 0.0f;
+#pragma unroll 4
+    for (int c = 0; c < D; c += 4) {
+      const float4 k0 = *reinterpret_cast<const float4*>(&sm.k[tx][c]);
+      const float4 k1 = *reinterpret_cast<const float4*>(&sm.k[tx + 16][c]);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float4 x = *reinterpret_cast<const float4*>(&sm.q[4 * ty + r][c]);
+        s[r][0] = fmaf(x.x, k0.x, fmaf(x.y, k0.y, fmaf(x.z, k0.z, fmaf(x.w, k0.w, s[r][0]))));
+        s[r][1] = fmaf(x.x, k1.x, fmaf(x.y, k1.y, fmaf(x.z, k1.z, fmaf(x.w, k1.w, s[r][1]))));
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int t = t0 + tx + 16 * j;
+        const bool see = t < end && (sink ? pos[r] >= 0 : win_sees(P, pos[r], t));
+        s[r][j] = see ? s[r][j] * P.scale_log2 : -INFINITY;
+      }
+      float mx = fmaxf(s[r][0], s[r][1]);
+#pragma unroll
+      for (int off = 8; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+      mx = fmaxf(mx, m[r]);
+      const float base = mx == -INFINITY ? 0.0f : mx;
+      const float corr = ex2f(m[r] - base);
+      const float p0 = ex2f(s[r][0] - base), p1 = ex2f(s[r][1] - base);
+      float ps = p0 + p1;
+#pragma unroll
+      for (int off = 8; off > 0; off >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, off);
+      l[r] = l[r] * corr + ps;
+      m[r] = mx;
+      sm.p[4 * ty + r][tx] = p0;
+      sm.p[4 * ty + r][tx + 16] = p1;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) o[r][c] *= corr;
+    }
+    __syncwarp();  // a row's weights are written and read by the same half-warp
+#pragma unroll 2
+    for (int j = 0; j < kFmaKeys; j += 4) {
+      float p[4][4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float4 x = *reinterpret_cast<const float4*>(&sm.p[4 * ty + r][j]);
+        p[r][0] = x.x, p[r][1] = x.y, p[r][2] = x.z, p[r][3] = x.w;
+      }
+#pragma unroll
+      for (int jj = 0; jj < 4; ++jj)
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          const float4 y = *reinterpret_cast<const float4*>(&sm.v[j + jj][64 * c + 4 * tx]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            o[r][4 * c] = fmaf(p[r][jj], y.x, o[r][4 * c]);
+            o[r][4 * c + 1] = fmaf(p[r][jj], y.y, o[r][4 * c + 1]);
+            o[r][4 * c + 2] = fmaf(p[r][jj], y.z, o[r][4 * c + 2]);
+            o[r][4 * c + 3] = fmaf(p[r][jj], y.w, o[r][4 * c + 3]);
+          }
+        }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int row = 4 * ty + r;
+    if (row >= rows) continue;
+    if (w.n_split > 1) {
+      const int64_t pr = (int64_t)w.slot * P.tile_rows + row;
+      if (tx == 0) P.part_ml[pr] = make_float2(m[r], l[r]);
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c)
+        *reinterpret_cast<float4*>(P.part_o + pr * D + 64 * c + 4 * tx) =
+            make_float4(o[r][4 * c], o[r][4 * c + 1], o[r][4 * c + 2], o[r][4 * c + 3]);
+      continue;
+    }
+    const float inv = l[r] > 0.0f ? 1.0f / l[r] : 0.0f;
+    const int64_t tok = S.q_row0 + w.tok0 + row / P.group;
+    const int h = w.hk * P.group + row % P.group;
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c)
+      store4<T>(P.out, tok * P.o_tok + h * P.o_head + 64 * c + 4 * tx,
+                make_float4(o[r][4 * c] * inv, o[r][4 * c + 1] * inv, o[r][4 * c + 2] * inv, o[r][4 * c + 3] * inv));
+    if (P.lse && tx == 0)
+      P.lse[tok * P.q_heads + h] = l[r] > 0.0f ? (m[r] + log2f(l[r])) * 0.69314718055994531f : -INFINITY;
+  }
+}
+
+// ---- merge of the splits ------------------------------------------------------
+// One warp per row of a tile whose keys were split: out = sum_s 2^(m_s - M)
+// o_s / sum_s 2^(m_s - M) l_s, splits in order (the same sum on every run).
+template <int T, int D>
+__global__ void __launch_bounds__(128) window_merge_kernel(const __grid_constant__ WinParams P) {
+  pdl_start();
+  const int lane = threadIdx.x & 31;
+  const int row = blockIdx.y * 4 + (threadIdx.x >> 5);
+  // items of a split tile come in runs of n_split * kv_heads; the tile's
+  // first run (split 0) stands for it
+  const WinItem w = win_item(P, blockIdx.x);
+  if (w.n_split == 1 || w.split != 0 || row >= w.n_tok * P.group) return;
+  const WinSeg& S = P.segs[w.seg];
+  constexpr int V = D / 32;
+  float m = -INFINITY, l = 0.0f, acc[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+#pragma unroll 4
+  for (int s = 0; s < w.n_split; ++s) {
+    const int64_t pr = ((int64_t)w.slot + (int64_t)s * P.kv_heads) * P.tile_rows + row;
+    const float2 ml = P.part_ml[pr];
+    float x[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = P.part_o[pr * D + lane * V + i];
+    const float mx = fmaxf(m, ml.x);
+    const float base = mx == -INFINITY ? 0.0f : mx;
+    const float fa = ex2f(m - base), fb = ex2f(ml.x - base);
+    l = l * fa + ml.y * fb;
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = acc[i] * fa + x[i] * fb;
+    m = mx;
+  }
+  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  const int64_t tok = S.q_row0 + w.tok0 + row / P.group;
+  const int h = w.hk * P.group + row % P.group;
+  const int64_t at = tok * P.o_tok + h * P.o_head + lane * V;
+  if constexpr (T == KVPOOL_F32) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) reinterpret_cast<float*>(P.out)[at + i] = acc[i] * inv;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i += 2)
+      *reinterpret_cast<__nv_bfloat162*>(P.out + 2 * (at + i)) = __floats2bfloat162_rn(acc[i] * inv, acc[i + 1] * inv);
+  }
+  if (P.lse && lane == 0) P.lse[tok * P.q_heads + h] = l > 0.0f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+}
+
+// ---- host plan ------------------------------------------------------------------
+constexpr int32_t kMaxLen = 1 << 30;
+
+bool strides_ok(const kvpool_heads& h, int32_t dtype) {
+  const int64_t unit = dtype == KVPOOL_BF16 ? 8 : 4;  // values in 16 bytes
+  return reinterpret_cast<uintptr_t>(h.data) % 16 == 0 && h.token_stride % unit == 0 && h.head_stride % unit == 0 &&
+         h.token_stride >= 0 && h.head_stride >= 0;
+}
+
+int check_args(const kvpool_window_args* a, int32_t n, const int32_t* q_len, const int64_t* k_start,
+               const int32_t* k_len, int64_t* total_q) {
+  if (!a || n < 0) return KVPOOL_ERR_INVALID_ARG;
+  if (a->dtype != KVPOOL_F32 && a->dtype != KVPOOL_BF16) return KVPOOL_ERR_INVALID_ARG;
+  if (a->head_dim != 64 && a->head_dim != 128) return KVPOOL_ERR_INVALID_ARG;
+  if (a->k.heads < 1 || a->v.heads != a->k.heads || a->out.heads != a->q.heads || a->q.heads < a->k.heads ||
+      a->q.heads > 1024 || a->q.heads % a->k.heads != 0 || a->q.heads / a->k.heads > kWinMaxGroup)
+    return KVPOOL_ERR_INVALID_ARG;
+  if (a->window < 0 || a->n_sink < 0 || !std::isfinite(a->scale) || a->q_rows < 0 || a->kv_rows < 0)
+    return KVPOOL_ERR_INVALID_ARG;
+  if (a->q_rows > 0x7FFFFFFF || a->kv_rows > 0x7FFFFFFF) return KVPOOL_ERR_INVALID_ARG;
+  if (!strides_ok(a->q, a->dtype) || !strides_ok(a->k, a->dtype) || !strides_ok(a->v, a->dtype) ||
+      !strides_ok(a->out, a->dtype))
+    return KVPOOL_ERR_INVALID_ARG;
+  if (n > 0 && (!q_len || !k_start || !k_len)) return KVPOOL_ERR_INVALID_ARG;
+  int64_t q = 0;
+  bool keys = false;
+  for (int i = 0; i < n; ++i) {
+    if (q_len[i] < 0 || q_len[i] > kMaxLen || k_len[i] < 0 || k_len[i] > kMaxLen) return KVPOOL_ERR_INVALID_ARG;
+    if (k_len[i] > 0 && (k_start[i] < 0 || k_start[i] > a->kv_rows - k_len[i])) return KVPOOL_ERR_INVALID_ARG;
+    q += q_len[i];
+    keys |= q_len[i] > 0 && k_len[i] > 0;
+  }
+  if (q > a->q_rows) return KVPOOL_ERR_INVALID_ARG;
+  if (q > 0 && (!a->q.data || !a->out.data)) return KVPOOL_ERR_INVALID_ARG;
+  if (keys && (!a->k.data || !a->v.data)) return KVPOOL_ERR_INVALID_ARG;
+  *total_q = q;
+  return KVPOOL_OK;
+}
+
+// the most keys that a tile of the segment sees
+int64_t tile_keys(const kvpool_window_args* a, int32_t q_len, int32_t k_len, int tile_tokens) {
+  const int64_t w = (int64_t)a->window + std::min(tile_tokens, q_len) + a->n_sink;
+  return std::min<int64_t>(k_len, w);
+}
+
+// Fill segments [i0, n) of one launch (at most kMaxWinSegs with queries);
+// returns the next segment.  A launch with few tiles cuts each tile's keys
+// into parts (merged by a second kernel) so that the GPU is filled.
+int plan_launch(const kvpool_window_args* a, int32_t i0, int32_t n, const int32_t* q_len, const int64_t* k_start,
+                const int32_t* k_len, int64_t q_row0, int n_sms, WinParams* P, int64_t* next_row, int64_t* slots) {
+  const int Hk = a->k.heads;
+  int i = i0;
+  P->n_segs = 0;
+  int64_t tiles = 0;
+  for (; i < n && P->n_segs < kMaxWinSegs; ++i) {
+    if (q_len[i] > 0) {
+      WinSeg& S = P->segs[P->n_segs++];
+      S = WinSeg{};
+      S.q_row0 = q_row0;
+      S.k_start = k_len[i] > 0 ? k_start[i] : 0;
+      S.q_len = q_len[i];
+      S.k_len = k_len[i];
+      tiles += (int64_t)((q_len[i] + P->tile_tokens - 1) / P->tile_tokens) * Hk;
+    }
+    q_row0 += q_len[i];
+  }
+  *next_row = q_row0;
+  constexpr int kMinSplitKeys = 128;
+  const int64_t want = 2LL * n_sms;  // work items
+  int64_t items = 0, slot = 0;
+  for (int s = 0; s < P->n_segs; ++s) {
+    WinSeg& S = P->segs[s];
+    const int64_t st = (int64_t)((S.q_len + P->tile_tokens - 1) / P->tile_tokens) * Hk;
+    int64_t split = 1;
+    if (tiles < want)
+      split = std::max<int64_t>(
+          1, std::min<int64_t>((want + tiles - 1) / tiles,
+                               (tile_keys(a, S.q_len, S.k_len, P->tile_tokens) + kMinSplitKeys - 1) / kMinSplitKeys));
+    S.n_split = (int32_t)split;
+    S.item_base = (int32_t)items;
+    S.part_base = (int32_t)(slot);
+    items += st * split;
+    if (split > 1) slot += st * split;
+  }
+  P->n_items = items <= 0x7FFFFFFF ? (int32_t)items : -1;
+  *slots = slot;
+  return i;
+}
+
+void fill_params(const kvpool_window_args* a, WinParams* P) {
+  P->q = static_cast<const uint8_t*>(a->q.data);
+  P->k = static_cast<const uint8_t*>(a->k.data);
+  P->v = static_cast<const uint8_t*>(a->v.data);
+  P->out = static_cast<uint8_t*>(const_cast<void*>(a->out.data));
+  P->lse = a->d_lse;
+  P->q_tok = a->q.token_stride;
+  P->q_head = a->q.head_stride;
+  P->k_tok = a->k.token_stride;
+  P->k_head = a->k.head_stride;
+  P->v_tok = a->v.token_stride;
+  P->v_head = a->v.head_stride;
+  P->o_tok = a->out.token_stride;
+  P->o_head = a->out.head_stride;
+  P->q_heads = a->q.heads;
+  P->kv_heads = a->k.heads;
+  P->group = a->q.heads / a->k.heads;
+  P->window = std::min(a->window, kMaxLen);
+  P->n_sink = std::min(a->n_sink, kMaxLen);
+  P->scale_log2 = a->scale * 1.4426950408889634f;
+  P->tile_tokens = kFmaRows / P->group;
+  P->tile_rows = P->tile_tokens * P->group;
+}
+
+int64_t slot_bytes(const WinParams& P, int head_dim) { return (int64_t)P.tile_rows * (head_dim + 2) * 4; }
+
+int device_sms() {
+  int dev = 0, v = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  return v;
+}
+
+template <int T, int D>
+cudaError_t launch_window(const WinParams& P, bool merge, cudaStream_t s) {
+  constexpr int smem = (int)sizeof(FmaSmem<D>);
+  auto* kern = window_fma_kernel<T, D>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) e = launch_kernel(true, kern, dim3(P.n_items), dim3(kFmaThreads), smem, s, P);
+  if (e == cudaSuccess && merge)
+    e = launch_kernel(true, window_merge_kernel<T, D>, dim3(P.n_items, (P.tile_rows + 3) / 4), dim3(128), 0, s, P);
+  return e;
+}
+
+}  // namespace
+}  // namespace kvp
+
+extern "C" int64_t kvpool_window_workspace(const kvpool_window_args* a, int32_t n, const int32_t* h_q_len,
+                                           const int64_t* h_k_start, const int32_t* h_k_len) {
+  using namespace kvp;
+  int64_t total = 0;
+  const int rc = check_args(a, n, h_q_len, h_k_start, h_k_len, &total);
+  if (rc != KVPOOL_OK) return rc;
+  if (total == 0) return 0;
+  const int sms = device_sms();
+  if (sms <= 0) return KVPOOL_ERR_CUDA;
+  std::unique_ptr<WinParams> P(new (std::nothrow) WinParams);
+  if (!P) return KVPOOL_ERR_INVALID_ARG;
+  fill_params(a, P.get());
+  int64_t most = 0, row = 0, slots = 0;
+  for (int i = 0; i < n;) {
+    i = plan_launch(a, i, n, h_q_len, h_k_start, h_k_len, row, sms, P.get(), &row, &slots);
+    most = std::max(most, slots * slot_bytes(*P, a->head_dim));
+  }
+  return most;
+}
+
+extern "C" int kvpool_window_attend(const kvpool_window_args* a, int32_t n, const int32_t* h_q_len,
+                                    const int64_t* h_k_start, const int32_t* h_k_len, void* d_workspace,
+                                    int64_t workspace_bytes, void* stream) {
+  using namespace kvp;
+  int64_t total = 0;
+  const int rc = check_args(a, n, h_q_len, h_k_start, h_k_len, &total);
+  if (rc != KVPOOL_OK) return rc;
+  if (total == 0) return KVPOOL_OK;
+  const int64_t need = kvpool_window_workspace(a, n, h_q_len, h_k_start, h_k_len);
+  if (need < 0) return (int)need;
+  if (need > 0 && (!d_workspace || workspace_bytes < need || reinterpret_cast<uintptr_t>(d_workspace) % 16 != 0))
+    return KVPOOL_ERR_INVALID_ARG;
+  const int sms = device_sms();
+  std::unique_ptr<WinParams> P(new (std::nothrow) WinParams);
+  if (!P) return KVPOOL_ERR_INVALID_ARG;
+  fill_params(a, P.get());
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int64_t row = 0, slots = 0;
+  for (int i = 0; i < n;) {
+    i = plan_launch(a, i, n, h_q_len, h_k_start, h_k_len, row, sms, P.get(), &row, &slots);
+    if (P->n_segs == 0) continue;
+    if (P->n_items < 0) return KVPOOL_ERR_INVALID_ARG;
+    P->part_o = static_cast<float*>(d_workspace);
+    P->part_ml = reinterpret_cast<float2*>(P->part_o + slots * P->tile_rows * a->head_dim);
+    cudaError_t e;
+    if (a->dtype == KVPOOL_F32)
+      e = a->head_dim == 128 ? launch_window<KVPOOL_F32, 128>(*P, slots > 0, s) : launch_window<KVPOOL_F32, 64>(*P, slots > 0, s);
+    else
+      e = a->head_dim == 128 ? launch_window<KVPOOL_BF16, 128>(*P, slots > 0, s) : launch_window<KVPOOL_BF16, 64>(*P, slots > 0, s);
+    if (e != cudaSuccess) return KVPOOL_ERR_CUDA;
+  }
+  return KVPOOL_OK;
+}

@@ -32,7 +32,8 @@ EXPORTS = ["kvpool_required_bytes", "kvpool_create", "kvpool_destroy", "kvpool_a
            "kvpool_topk_static", "kvpool_profile_timeline", "kvpool_fingerprint", "kvpool_image_bytes",
            "kvpool_export_prefix", "kvpool_import_prefix", "kvpool_host_slot_bytes", "kvpool_set_host_pool",
            "kvpool_offload", "kvpool_fetch", "kvpool_block_location", "kvpool_epoch", "kvpool_block_activity",
-           "kvpool_inactive_blocks", "kvpool_wait_selftest", "kvpool_topk_static_check"]
+           "kvpool_inactive_blocks", "kvpool_wait_selftest", "kvpool_topk_static_check", "kvpool_rope_table",
+           "kvpool_qk_norm_rope", "kvpool_window_workspace", "kvpool_window_attend"]
 
 
 class KvpoolError(RuntimeError):
@@ -70,6 +71,17 @@ class _LayerLayout(C.Structure):
                 ("hca_offset", C.c_int64), ("hca_block_bytes", C.c_int64), ("ring_offset", C.c_int64),
                 ("ring_request_bytes", C.c_int64), ("acc_offset", C.c_int64), ("acc_request_bytes", C.c_int64),
                 ("csa_host_offset", C.c_int64)]
+
+
+class _Heads(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("token_stride", C.c_int64), ("head_stride", C.c_int64), ("heads", C.c_int32),
+                ("pad", C.c_int32)]
+
+
+class _WindowArgs(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("head_dim", C.c_int32), ("q", _Heads), ("k", _Heads), ("v", _Heads),
+                ("out", _Heads), ("q_rows", C.c_int64), ("kv_rows", C.c_int64), ("d_lse", C.c_void_p),
+                ("window", C.c_int32), ("n_sink", C.c_int32), ("scale", C.c_float), ("pad", C.c_int32)]
 
 
 _lib = None
@@ -120,6 +132,12 @@ def lib():
         L.kvpool_inactive_blocks.restype = i32
         L.kvpool_inactive_blocks.argtypes = [vp, C.c_uint32, vp, i32, vp]
         L.kvpool_wait_selftest.argtypes = [vp, vp]
+        hp = C.POINTER(_Heads)
+        L.kvpool_rope_table.argtypes = [i32, vp, vp]
+        L.kvpool_qk_norm_rope.argtypes = [i32, i32, i64, hp, hp, hp, hp, vp, vp, C.c_float, i32, i32, vp, vp, vp]
+        L.kvpool_window_workspace.restype = i64
+        L.kvpool_window_workspace.argtypes = [C.POINTER(_WindowArgs), i32, vp, vp, vp]
+        L.kvpool_window_attend.argtypes = [C.POINTER(_WindowArgs), i32, vp, vp, vp, vp, i64, vp]
         L.kvpool_last_error.restype = C.c_char_p
         L.kvpool_last_error.argtypes = [vp]
         _lib = L
@@ -226,6 +244,182 @@ def _i32(a) -> np.ndarray:
     if type(a) is np.ndarray and a.dtype == np.int32 and a.flags.c_contiguous:
         return a
     return np.ascontiguousarray(a, dtype=np.int32)
+
+
+def _dtype(t) -> int:
+    import torch
+    if t.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("tensors must be float32 or bfloat16")
+    return F32 if t.dtype == torch.float32 else BF16
+
+
+def _heads(t, what: str, like=None) -> _Heads:
+    """A [tokens][heads][dim] CUDA tensor as the C ABI takes it."""
+    if t.dim() != 3 or not t.is_cuda or t.stride(2) != 1 and t.shape[2] > 1:
+        raise ValueError(f"{what} must be a [tokens][heads][dim] CUDA tensor with adjacent values")
+    if like is not None and (t.dtype != like.dtype or t.device != like.device or t.shape[2] != like.shape[2]):
+        raise ValueError(f"{what} must have the type, device and head dim of the other tensors")
+    unit = 16 // t.element_size()
+    # the stride of an axis of length 1 is never used
+    ts, hs = (t.stride(i) if t.shape[i] > 1 else 0 for i in (0, 1))
+    if t.numel() and t.data_ptr() % 16 or ts % unit or hs % unit:
+        raise ValueError(f"{what}: data and strides must be whole multiples of 16 bytes")
+    return _Heads(t.data_ptr() if t.numel() else None, ts, hs, t.shape[1], 0)
+
+
+def _out_heads(t, what: str, like) -> _Heads:
+    """_heads of an output: no two of its values share a place."""
+    if any(t.shape[i] > 1 and t.stride(i) < t.shape[2] for i in (0, 1)):
+        raise ValueError(f"{what}: two values share a place")
+    return _heads(t, what, like)
+
+
+def _empty(shape, dtype, device, stream: int):
+    """torch.empty whose memory belongs to `stream`, the one that will use it."""
+    import torch
+    if stream == torch.cuda.current_stream(device).cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _need(t, what: str, dtype, shape, device):
+    if t.dtype != dtype or t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+
+
+def rope_table(rot_dim: int, theta: float = 10000.0, inv_freq=None, device="cuda"):
+    """The rotation table of qk_norm_rope on `device`: int64 [rot_dim / 2], the
+    frequencies theta ** (-2i / rot_dim) (or inv_freq, radians per position) as
+    64-bit fractions of a turn; see kvpool_rope_table in include/kvpool.h."""
+    import torch
+    if inv_freq is None:
+        inv_freq = theta ** (-np.arange(0, rot_dim, 2, dtype=np.float64) / max(rot_dim, 1))
+    f = np.ascontiguousarray(inv_freq, dtype=np.float64)
+    if f.shape != (rot_dim // 2,):
+        raise ValueError("rope_table: inv_freq must have rot_dim / 2 values")
+    out = np.empty(max(f.size, 1), np.uint64)
+    rc = lib().kvpool_rope_table(rot_dim, f.ctypes.data, out.ctypes.data)
+    if rc != OK:
+        raise KvpoolError(rc, "rope_table: rot_dim must be a multiple of 16 up to 256, the frequencies finite")
+    return torch.from_numpy(out[:f.size].view(np.int64)).to(device)
+
+
+def qk_norm_rope(q, k, positions, table, q_weight=None, k_weight=None, eps: float = 1e-6, interleaved: bool = False,
+                 out_q=None, out_k=None, stream=None):
+    """Norm every head of q and k ([tokens][heads][dim], float32 or bfloat16,
+    either may be None) and rotate it by its token's position (int64
+    [tokens]) with the table of rope_table (None: norms only); returns (out_q,
+    out_k), which may be given and may be q and k themselves.  See
+    kvpool_qk_norm_rope in include/kvpool.h."""
+    import torch
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("qk_norm_rope: neither q nor k")
+    if not x.is_cuda:
+        raise ValueError("qk_norm_rope: the tensors must be on a CUDA device")
+    T, D = x.shape[0], x.shape[-1]
+    with torch.cuda.device(x.device):
+        s = _stream(stream)
+    hs, outs = [], []
+    for t, o, what in ((q, out_q, "q"), (k, out_k, "k")):
+        if t is None:
+            hs += [None, None]
+            outs.append(None)
+            continue
+        a = _heads(t, what, x)
+        if t.shape[0] != T:
+            raise ValueError("qk_norm_rope: q and k must have the same tokens")
+        if o is None:
+            o = _empty(t.shape, t.dtype, t.device, s)
+        elif o.shape != t.shape:
+            raise ValueError(f"qk_norm_rope: out_{what} must have the shape of {what}")
+        hs += [a, _out_heads(o, "out_" + what, x)]
+        outs.append(o)
+    rot = 0
+    if table is not None:
+        rot = 2 * table.numel()
+        _need(table, "table", torch.int64, (rot // 2,), x.device)
+        _need(positions, "positions", torch.int64, (T,), x.device)
+    for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _need(w, what, torch.float32, (D,), x.device)
+    ref = [C.byref(h) if h is not None else None for h in hs]
+    with torch.cuda.device(x.device):
+        rc = lib().kvpool_qk_norm_rope(_dtype(x), D, T, ref[0], ref[2], ref[1], ref[3], _ptr(q_weight), _ptr(k_weight),
+                                       eps, rot, int(bool(interleaved)), _ptr(table) if rot else None,
+                                       _ptr(positions) if rot else None, s)
+    if rc != OK:
+        raise KvpoolError(rc, "qk_norm_rope refused its arguments" if rc == ERR_INVALID_ARG else "qk_norm_rope: CUDA error")
+    return outs[0], outs[1]
+
+
+def window_attend(q, k, v, q_len, k_start, k_len, window: int, n_sink: int = 0, scale=None, out=None, lse=None,
+                  workspace=None, stream=None):
+    """Attention of a ragged batch over raw K/V rows with a sliding window and
+    n_sink first tokens that stay visible; returns out ([rows][q heads][dim],
+    like q).  q_len, k_start, k_len: host integers per segment; lse: a float32
+    [rows][q heads] tensor to fill, or None; workspace: a uint8 CUDA tensor of
+    window_workspace bytes (one is allocated when None).  See
+    kvpool_window_attend in include/kvpool.h."""
+    import torch
+    if not q.is_cuda:
+        raise ValueError("window_attend: the tensors must be on a CUDA device")
+    with torch.cuda.device(q.device):
+        s = _stream(stream)
+        if out is None:
+            out = _empty(q.shape, q.dtype, q.device, s)
+        a, ql, ks, kl = _window_args(q, k, v, q_len, k_start, k_len, window, n_sink, scale, out, lse)
+        call = (C.byref(a), ql.size, ql.ctypes.data, ks.ctypes.data, kl.ctypes.data)
+        rc = int(lib().kvpool_window_workspace(*call))
+        if rc >= 0:
+            if workspace is None and rc > 0:
+                workspace = _empty((rc,), torch.uint8, q.device, s)
+            if workspace is not None and (workspace.device != q.device or not workspace.is_contiguous()):
+                raise ValueError("window_attend: workspace must be a contiguous tensor on the queries' device")
+            nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+            rc = lib().kvpool_window_attend(*call, _ptr(workspace), nbytes, s)
+    if rc != OK:
+        raise KvpoolError(rc, "window_attend refused its arguments" if rc == ERR_INVALID_ARG else "window_attend: CUDA error")
+    return out
+
+
+def window_workspace(q, k, v, q_len, k_start, k_len, window: int, n_sink: int = 0) -> int:
+    """Workspace bytes of window_attend with these arguments."""
+    import torch
+    a, ql, ks, kl = _window_args(q, k, v, q_len, k_start, k_len, window, n_sink, None, q, None)
+    with torch.cuda.device(q.device):
+        rc = int(lib().kvpool_window_workspace(C.byref(a), ql.size, ql.ctypes.data, ks.ctypes.data, kl.ctypes.data))
+    if rc < 0:
+        raise KvpoolError(rc, "window_workspace refused its arguments")
+    return rc
+
+
+def _window_args(q, k, v, q_len, k_start, k_len, window, n_sink, scale, out, lse):
+    import torch
+    qh, kh, vh = _heads(q, "q"), _heads(k, "k", q), _heads(v, "v", q)
+    if k.shape != v.shape:
+        raise ValueError("window_attend: k and v must have the same shape")
+    if out.shape != q.shape:
+        raise ValueError("window_attend: out must have the shape of q")
+    oh = _out_heads(out, "out", q)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, q.shape[:2], q.device)
+    ql, ks, kl = (_ints(x, t) for x, t in ((q_len, np.int32), (k_start, np.int64), (k_len, np.int32)))
+    if not ql.shape == ks.shape == kl.shape or ql.ndim != 1:
+        raise ValueError("window_attend: q_len, k_start and k_len must have one value per segment")
+    a = _WindowArgs(_dtype(q), q.shape[2], qh, kh, vh, oh, q.shape[0], k.shape[0], _ptr(lse), window, n_sink,
+                    1.0 / float(np.sqrt(q.shape[2])) if scale is None else scale, 0)
+    return a, ql, ks, kl
+
+
+def _ints(x, dtype) -> np.ndarray:
+    a = np.asarray(x)
+    if a.size and a.dtype.kind not in "iu":
+        raise ValueError("lengths and starts must be integers")
+    if a.size and (a.min() < np.iinfo(dtype).min or a.max() > np.iinfo(dtype).max):
+        raise ValueError("a length or start is out of range")
+    return np.ascontiguousarray(a, dtype=dtype)
 
 
 class Pool:

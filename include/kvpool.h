@@ -360,6 +360,84 @@ int kvpool_topk_static(const float* d_scores, int32_t n_rows, int32_t n_cols, in
  * kvpool_topk_static, which clears the word. */
 int kvpool_topk_static_check(void* stream, uint32_t* h_flags);
 
+/* ---- around the pool: what a model does to its rows before and beside the
+ * cache calls.  These entry points have no pool: they take the caller's
+ * tensors as they are, need no arena, and work on the current device, in
+ * stream order on `stream`.  The design pages have no counterpart. ---- */
+
+/* The heads of a run of tokens: value j of head h of token t is at element
+ * t * token_stride + h * head_stride + j of data (a head's values are
+ * adjacent).  data and both strides are whole multiples of 16 bytes; strides
+ * are in elements and not negative. */
+typedef struct kvpool_heads {
+  const void* data;
+  int64_t token_stride, head_stride;
+  int32_t heads;
+  int32_t pad;
+} kvpool_heads;
+
+/* Rotation table of kvpool_qk_norm_rope, on the host: h_table[i] =
+ * h_inv_freq[i] / (2 pi) modulo 1 as a 64-bit fraction of a turn, i <
+ * rot_dim / 2.  Copy it to the device once.  Errors: INVALID_ARG (rot_dim
+ * negative, above 256 or not a multiple of 16; a frequency that is not
+ * finite). */
+int kvpool_rope_table(int32_t rot_dim, const double* h_inv_freq, uint64_t* h_table);
+
+/* Norm every head of the queries and keys and rotate it by its token's
+ * position, in one pass: y = x / sqrt(mean(x^2) + eps) * weight over head_dim
+ * values, then over the first rot_dim of them (a, b) -> (a cos - b sin, b cos
+ * + a sin) with angle position * inv_freq[i]; pair i is (i, i + rot_dim / 2),
+ * or (2i, 2i + 1) when interleaved is 1.  fp32 inside, one rounding to dtype.
+ * The result is what kvpool_append takes as keys and kvpool_decode_attend as
+ * queries.  dtype: KVPOOL_F32 or KVPOOL_BF16.  head_dim: a multiple of 8 up to
+ * 256; rot_dim: a multiple of 16 up to head_dim (0: norms only, no table or
+ * positions needed).  q or k may be NULL or have no heads.  An output may be
+ * its own input (same data and strides); otherwise they must not overlap.
+ * Weights: [head_dim] fp32 or NULL (ones).  d_positions: [n_tokens], any sign
+ * and size.  Errors: INVALID_ARG, CUDA. */
+int kvpool_qk_norm_rope(int32_t dtype, int32_t head_dim, int64_t n_tokens, const kvpool_heads* q,
+                        const kvpool_heads* k, const kvpool_heads* q_out, const kvpool_heads* k_out,
+                        const float* d_q_weight, const float* d_k_weight, float eps, int32_t rot_dim,
+                        int32_t interleaved, const uint64_t* d_table, const int64_t* d_positions, void* stream);
+
+/* Attention of a ragged batch over raw K/V tokens with a sliding window and a
+ * few first tokens that stay visible: a prompt's own outputs in a window
+ * layer (kvpool_append takes the same tokens into the cache), or single
+ * tokens over a caller's K/V rows.  Segment i has the next h_q_len[i] query
+ * rows (segments in order) and K/V rows h_k_start[i] .. h_k_start[i] +
+ * h_k_len[i] - 1, its tokens at positions 0 .. h_k_len[i] - 1; its queries are
+ * the last ones: query j is at position p = h_k_len[i] - h_q_len[i] + j and
+ * sees the token at t when t <= p and (t > p - window or t < n_sink).  A query
+ * that sees nothing gives zeros and -inf.  q.heads must be a multiple (up to
+ * 16) of k.heads: query head h reads key head h / (q.heads / k.heads).
+ * out: like q, in dtype; d_lse: [q_rows][q.heads] fp32 natural-log sums of
+ * the exponentials, or NULL.  Query rows behind the last segment are left as
+ * they were.  K/V rows outside the segments are never let into a result; the
+ * values of a segment's own rows should be finite (a NaN or infinity in a
+ * value row may reach queries of the same tile that do not see it).
+ * dtype: KVPOOL_F32 (fp32 throughout) or KVPOOL_BF16 (softmax statistics and
+ * sums in fp32); head_dim 64 or 128; window and n_sink >= 0.
+ * d_workspace: kvpool_window_workspace bytes (16-byte aligned, may be NULL
+ * when that is 0); calls that overlap on the GPU need one each.  The lengths
+ * are read during the call: a captured call replays with the same ones.
+ * Errors: INVALID_ARG, CUDA. */
+typedef struct kvpool_window_args {
+  int32_t dtype, head_dim;
+  kvpool_heads q, k, v, out;
+  int64_t q_rows, kv_rows; /* rows of q and out, of k and v */
+  float* d_lse;
+  int32_t window, n_sink;
+  float scale; /* of the scores, e.g. 1 / sqrt(head_dim) */
+  int32_t pad;
+} kvpool_window_args;
+
+/* Workspace bytes of that call on the current device (a negative error code
+ * if its arguments are refused). */
+int64_t kvpool_window_workspace(const kvpool_window_args* args, int32_t n, const int32_t* h_q_len,
+                                const int64_t* h_k_start, const int32_t* h_k_len);
+int kvpool_window_attend(const kvpool_window_args* args, int32_t n, const int32_t* h_q_len, const int64_t* h_k_start,
+                         const int32_t* h_k_len, void* d_workspace, int64_t workspace_bytes, void* stream);
+
 /* ---- host-side queries (no device access) ---- */
 typedef struct kvpool_info {
   int64_t length;   /* tokens appended (or shared) so far */

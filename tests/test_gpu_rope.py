@@ -1,0 +1,139 @@
+"""Head norms with the position rotation against the formula in 64 bits."""
+import numpy as np
+import pytest
+import torch
+
+from heterogeneous_compressed_kv_gb300 import kvpool as K
+
+pytestmark = pytest.mark.gpu
+
+
+def formula(x, pos, freq, w, eps, inter):
+    """The rotated norms in 64 bits, and each value's pair magnitude."""
+    x = x.double().cpu()
+    rot = 2 * len(freq)
+    y = x / torch.sqrt((x * x).mean(-1, keepdim=True) + eps)
+    if w is not None:
+        y = y * w.double().cpu()
+    ang = pos.double().cpu()[:, None, None] * torch.tensor(freq, dtype=torch.float64)
+    a, b = (y[..., 0:rot:2], y[..., 1:rot:2]) if inter else (y[..., :rot // 2], y[..., rot // 2:rot])
+    p, q = a * torch.cos(ang) - b * torch.sin(ang), b * torch.cos(ang) + a * torch.sin(ang)
+    mag = torch.sqrt(a * a + b * b)
+    if inter:
+        r, g = torch.stack([p, q], -1).flatten(-2), torch.stack([mag, mag], -1).flatten(-2)
+    else:
+        r, g = torch.cat([p, q], -1), torch.cat([mag, mag], -1)
+    return torch.cat([r, y[..., rot:]], -1), torch.cat([g, y[..., rot:].abs()], -1)
+
+
+def check(got, want):
+    ref, mag = want
+    # one rounding to the type (half a step of the value), and in fp32: the sum of squares and its root (a few steps),
+    # the sine's and cosine's place (2^-25 turns, 2 pi of it: 2^-22.3) and two products: under 2^-20 of the pair
+    tol = torch.finfo(got.dtype).eps / 2 * ref.abs() + 2.0 ** -20 * mag + 1e-30
+    err = (got.double().cpu() - ref).abs()
+    assert bool((err <= tol).all()), float((err / tol).max())
+
+
+def freqs(rot):
+    return 10000.0 ** (-np.arange(0, rot, 2) / max(rot, 1))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("T,hq,hk,d,rot", [(1, 1, 1, 64, 64), (3, 4, 1, 128, 128), (33, 16, 16, 128, 64), (5, 3, 2, 96, 32),
+                                           (7, 5, 1, 256, 256), (2, 2, 2, 8, 0), (4, 9, 3, 80, 80), (700, 16, 2, 64, 48),
+                                           (3000, 16, 4, 128, 128)])
+def test_formula(T, hq, hk, d, rot, inter, dtype):
+    g = torch.Generator(device="cuda").manual_seed(T * 7 + d)
+    q = torch.randn((T, hq, d), device="cuda", generator=g).to(dtype)
+    k = (3 * torch.randn((T, hk, d), device="cuda", generator=g)).to(dtype)
+    pos = torch.randint(0, 1 << 20, (T,), device="cuda", generator=g)
+    qw = torch.randn((d,), device="cuda", generator=g)
+    tab = K.rope_table(rot) if rot else None
+    oq, ok = K.qk_norm_rope(q, k, pos, tab, qw, None, eps=1e-5, interleaved=inter)
+    check(oq, formula(q, pos, freqs(rot), qw, 1e-5, inter))
+    check(ok, formula(k, pos, freqs(rot), None, 1e-5, inter))
+
+
+def test_far_and_negative_positions():
+    # the turn is exact modulo 2^64, so a position far away is as good as a near one; the formula's own angle in 64 bits
+    # is good to 2^-53 of itself, which holds 2^20 radians to 2^-33
+    pos = torch.tensor([0, 1, -1, 1 << 20, -(1 << 20), (1 << 20) + 1], device="cuda")
+    q = torch.randn((6, 2, 128), device="cuda")
+    oq, _ = K.qk_norm_rope(q, None, pos, K.rope_table(128))
+    check(oq, formula(q, pos, freqs(128), None, 1e-6, False))
+    # exact periods: a frequency of a quarter turn comes back after 4 positions, at any distance
+    tab = K.rope_table(16, inv_freq=np.full(8, np.pi / 2))
+    far = torch.tensor([0, 4, 1 << 40, -(1 << 40), (1 << 62) + 4, 2], device="cuda")
+    x = torch.randn((1, 1, 16), device="cuda").expand(6, 1, 16).contiguous()
+    y, _ = K.qk_norm_rope(x, None, far, tab)
+    for i in range(1, 5):
+        assert torch.equal(y[0], y[i])
+    assert torch.equal(y[5], -y[0])
+
+
+def test_zeros_and_extremes():
+    x = torch.zeros((2, 2, 64), device="cuda", dtype=torch.bfloat16)
+    pos = torch.tensor([0, 5], device="cuda")
+    y, _ = K.qk_norm_rope(x, None, pos, K.rope_table(64))
+    assert torch.equal(y, x)
+    big = torch.full((1, 1, 64), 1e18, device="cuda")
+    y, _ = K.qk_norm_rope(big, None, pos[:1], K.rope_table(64))  # squares of 1e36 still sum in fp32
+    check(y, formula(big, pos[:1], freqs(64), None, 1e-6, False))
+
+
+def test_views_in_place_and_rows_behind():
+    g = torch.Generator(device="cuda").manual_seed(3)
+    rows = torch.randn((9, 8 + 2 * 2, 128), device="cuda", generator=g).bfloat16()
+    keep = rows.clone()
+    pos = torch.arange(100, 107, device="cuda")
+    tab = K.rope_table(128)
+    q, k = rows[:7, :8], rows[:7, 8:10]
+    wq, wk = K.qk_norm_rope(q, k, pos, tab)
+    oq, ok = K.qk_norm_rope(q, k, pos, tab, out_q=q, out_k=k)  # in place, inside a fused projection's rows
+    assert oq.data_ptr() == q.data_ptr() and torch.equal(oq, wq) and torch.equal(ok, wk)
+    assert torch.equal(rows[:, 10:], keep[:, 10:]) and torch.equal(rows[7:], keep[7:])
+    # heads outermost
+    x = torch.randn((4, 7, 64), device="cuda", generator=g).transpose(0, 1)
+    y, _ = K.qk_norm_rope(x, None, pos, K.rope_table(64))
+    check(y, formula(x, pos, freqs(64), None, 1e-6, False))
+
+
+def test_no_tokens():
+    q = torch.empty((0, 4, 64), device="cuda", dtype=torch.bfloat16)
+    oq, ok = K.qk_norm_rope(q, None, torch.empty((0,), dtype=torch.int64, device="cuda"), K.rope_table(64))
+    assert oq.shape == q.shape and ok is None
+
+
+def test_refusals():
+    q = torch.randn((4, 2, 64), device="cuda")
+    pos, tab = torch.arange(4, device="cuda"), K.rope_table(64)
+    for bad in (dict(q=q.half()), dict(q=q.cpu()), dict(q=q[:, :, ::2]), dict(q=torch.randn((4, 2, 66), device="cuda")[:, :, 1:65]),
+                dict(positions=pos.int()), dict(positions=pos[:3]), dict(table=tab.float()), dict(q_weight=pos),
+                dict(k=q.bfloat16()), dict(k=q[:3]), dict(out_q=q[:3]), dict(out_q=q[:, :1].expand(4, 2, 64))):
+        with pytest.raises(ValueError):
+            K.qk_norm_rope(**{**dict(q=q, k=None, positions=pos, table=tab), **bad})
+    with pytest.raises(K.KvpoolError):
+        K.qk_norm_rope(q, None, pos, K.rope_table(128))  # rot_dim above head_dim
+    with pytest.raises(ValueError):
+        K.qk_norm_rope(None, None, pos, tab)
+
+
+def test_stream_and_graph():
+    q = torch.randn((40, 16, 128), device="cuda").bfloat16()
+    pos, tab = torch.arange(40, device="cuda"), K.rope_table(128)
+    want, _ = K.qk_norm_rope(q, None, pos, tab)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got, _ = K.qk_norm_rope(q, None, pos, tab, stream=side)
+    side.synchronize()
+    assert torch.equal(got, want)
+    out = torch.zeros_like(q)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        K.qk_norm_rope(q, None, pos, tab, out_q=out)
+    pos += 11
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, K.qk_norm_rope(q, None, pos, tab)[0])

@@ -1,0 +1,196 @@
+"""Window attention with first tokens that stay visible against the formula in
+64 bits."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from heterogeneous_compressed_kv_gb300 import kvpool as K
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def formula(q, k, v, ql, ks, kl, window, sink, scale):
+    """(out, lse, mass) in 64 bits: mass = sum of p |v|, which the tolerances count in."""
+    q, k, v = q.double(), k.double(), v.double()
+    group = q.shape[1] // k.shape[1]
+    out, mass = torch.zeros_like(q), torch.zeros_like(q)
+    lse = torch.full(q.shape[:2], -math.inf, dtype=torch.float64, device=q.device)
+    at = 0
+    for n, k0, m in zip(ql, ks, kl):
+        p = torch.arange(m - n, m, device=q.device)[:, None]
+        t = torch.arange(m, device=q.device)[None]
+        see = (t <= p) & ((t > p - window) | (t < sink))
+        kk, vv = (x[k0:k0 + m].repeat_interleave(group, 1) for x in (k, v))
+        s = torch.einsum("nhd,mhd->hnm", q[at:at + n], kk) * scale
+        s = torch.where(see, s, -math.inf)
+        z = torch.logsumexp(s, -1, keepdim=True)
+        w = torch.where(see, torch.exp(s - torch.where(z == -math.inf, 0.0, z)), 0.0)
+        vv = torch.where(see.any(0)[:, None, None], vv, 0.0)
+        out[at:at + n] = torch.einsum("hnm,mhd->nhd", w, vv)
+        mass[at:at + n] = torch.einsum("hnm,mhd->nhd", w, vv.abs())
+        lse[at:at + n] = z[..., 0].T if m else -math.inf
+        at += n
+    return out, lse, mass
+
+
+def check(got, lse, want, q, k, scale, dtype, n_keys):
+    ref, z, mass = want
+    # a score's sum of D products in fp32 is off by at most D 2^-24 |q||k|, twice for products and order; a weight by
+    # that, by 2^-20 (its exponential and the rescaling) and by the sum over the keys; with bf16 each weight is rounded
+    # once more (half a step), and the output too
+    fin = torch.finfo(dtype).eps / 2
+    qk = scale * float(q.double().norm(dim=-1).max() * k.double().nan_to_num(0, 0, 0).norm(dim=-1).max())
+    s_err = 2 * (q.shape[-1] + 4) * 2.0 ** -24 * qk
+    rel = 2 * s_err + 2.0 ** -20 + n_keys * 2.0 ** -24
+    tol = fin * ref.abs() + (rel + (fin if dtype == BF else 0)) * mass * 1.01 + 1e-30
+    err = (got.double() - ref).abs()
+    assert bool((err <= tol).all()), float((err / tol).max())
+    if lse is not None:
+        dead = z == -math.inf
+        assert torch.equal(dead, lse == -math.inf)
+        e = (lse.double() - z)[~dead].abs()
+        tol = (rel + 2.0 ** -23 * z.abs())[~dead]
+        assert bool((e <= tol).all()), float((e / tol).max())
+
+
+def inputs(ql, kl, hq, hk, d, dtype, seed=0, gap=0):
+    """Rows of all segments, `gap` rows of NaN between their cached tokens."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    q = torch.randn((int(sum(ql)), hq, d), device="cuda", generator=g).to(dtype)
+    ks, rows = [], gap
+    for m in kl:
+        ks.append(rows)
+        rows += m + gap
+    k, v = (torch.full((rows, hk, d), math.nan, device="cuda", dtype=dtype) for _ in range(2))
+    for k0, m in zip(ks, kl):
+        k[k0:k0 + m] = torch.randn((m, hk, d), device="cuda", generator=g).to(dtype)
+        v[k0:k0 + m] = torch.randn((m, hk, d), device="cuda", generator=g).to(dtype)
+    return q, k, v, ks
+
+
+def run(ql, kl, hq, hk, d, dtype, window, sink, seed=0, gap=3):
+    q, k, v, ks = inputs(ql, kl, hq, hk, d, dtype, seed, gap)
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    out = K.window_attend(q, k, v, ql, ks, kl, window, sink, lse=lse)
+    scale = 1 / math.sqrt(d)
+    check(out, lse, formula(q, k, v, ql, ks, kl, window, sink, scale), q, k, scale, dtype, max(max(kl), 1))
+
+
+SHAPES = [  # q_len, k_len, window, sinks
+    ([1], [1], 1, 0), ([1], [1], 0, 0), ([1], [1], 0, 1), ([2], [2], 1, 0), ([5], [5], 16, 2),
+    ([1, 1, 1], [1, 77, 300], 64, 4), ([1] * 9, [1, 2, 31, 32, 33, 127, 128, 129, 1000], 128, 0),
+    ([64], [64], 64, 0), ([65], [200], 33, 3), ([130], [130], 1000, 0), ([127, 128, 129], [127, 128, 129], 128, 1),
+    ([300], [1000], 128, 130), ([257, 1, 0, 40], [700, 513, 9, 40], 100, 5), ([10], [4], 8, 2), ([3], [0], 4, 4),
+    ([0, 6], [5, 6], 4, 0), ([513], [2000], 256, 64), ([17], [4000], 3000, 1), ([200], [260], 0, 7), ([40], [40], 2 ** 31 - 1, 0),
+]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("shape", SHAPES, ids=[str(i) for i in range(len(SHAPES))])
+def test_formula(shape, d, dtype):
+    ql, kl, window, sink = shape
+    run(ql, kl, 4, 2, d, dtype, window, sink, seed=len(ql) + sum(kl))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("hq,hk", [(1, 1), (3, 3), (6, 2), (5, 1), (8, 1), (14, 2), (16, 1)])
+@pytest.mark.parametrize("ql,kl", [([1, 1], [90, 700]), ([5, 2], [5, 640]), ([150], [400])])
+def test_groups(ql, kl, hq, hk, dtype):
+    run(ql, kl, hq, hk, 64, dtype, 100, 3, seed=hq)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_many_segments(dtype):
+    r = np.random.RandomState(0)
+    kl = r.randint(0, 90, 600).tolist()
+    ql = [int(min(m, x)) for m, x in zip(kl, r.randint(0, 4, 600))]
+    run(ql, kl, 2, 1, 64, dtype, 20, 2, gap=1)
+
+
+def test_long_single_tokens_split_and_merge():
+    run([1], [70001], 4, 1, 128, BF, 1 << 20, 0)
+    run([1, 1], [20000, 5], 2, 2, 64, F32, 1 << 20, 0)
+    run([2], [9000], 4, 4, 128, BF, 4096, 500)
+
+
+def test_large_scores_keep_the_softmax_finite():
+    q, k, v, ks = inputs([40], [40], 2, 2, 64, BF)
+    q, k = q * 40, k * 40  # scores in the thousands: one key has all the weight
+    out = K.window_attend(q, k, v, [40], ks, [40], 16)
+    want = formula(q, k, v, [40], ks, [40], 16, 0, 0.125)
+    assert bool(torch.isfinite(out).all())
+    near = (out.double() - want[0]).abs() <= 2.0 ** -6 * want[2] + 1e-6
+    assert float(near.double().mean()) > 0.999  # ties between two keys within a score's rounding may fall either way
+
+
+def test_views_other_rows_and_scale():
+    g = torch.Generator(device="cuda").manual_seed(5)
+    rows = torch.randn((300, 8 + 2 * 2, 64), device="cuda", generator=g).to(BF)
+    q, k, v = rows[:, :8], rows[:, 8:10], rows[:, 10:]
+    out = torch.full((310, 8, 64), 3.0, device="cuda", dtype=BF)
+    got = K.window_attend(q[40:200], k, v, [100], [50], [180], 70, 2, scale=0.3, out=out[:160])
+    assert got.data_ptr() == out.data_ptr()
+    want = formula(q[40:140], k, v, [100], [50], [180], 70, 2, 0.3)
+    check(got[:100], None, want, q, k, 0.3, BF, 180)
+    assert bool((out[100:] == 3.0).all())  # rows behind the last segment
+    # heads outermost
+    kt = torch.randn((2, 300, 64), device="cuda", generator=g).to(BF).transpose(0, 1)
+    got = K.window_attend(q, kt, v, [300], [0], [300], 64)
+    check(got, None, formula(q, kt, v, [300], [0], [300], 64, 0, 0.125), q, kt, 0.125, BF, 300)
+
+
+def test_overlapping_segments_read_the_same_rows():
+    # two requests over one shared prompt's rows
+    q, k, v, _ = inputs([3, 50], [100], 2, 1, 128, BF, gap=0)
+    out = K.window_attend(q, k, v, [3, 50], [0, 10], [100, 90], 33, 1)
+    scale = 1 / math.sqrt(128)
+    check(out, None, formula(q, k, v, [3, 50], [0, 10], [100, 90], 33, 1, scale), q, k, scale, BF, 100)
+
+
+@pytest.mark.parametrize("ql,kl", [([1, 1], [5000, 300]), ([400], [900])])
+def test_same_bits_again_streams_and_graphs(ql, kl):
+    q, k, v, ks = inputs(ql, kl, 4, 2, 128, BF, gap=0)
+    args = (q, k, v, ql, ks, kl, 2048, 4)
+    want = K.window_attend(*args)
+    assert torch.equal(want, K.window_attend(*args))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = K.window_attend(*args, stream=side)
+    side.synchronize()
+    assert torch.equal(got, want)
+    ws = [torch.empty(max(K.window_workspace(*args), 16), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    outs, graphs = [torch.zeros_like(q) for _ in range(2)], []
+    for o, w in zip(outs, ws):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            K.window_attend(*args, out=o, workspace=w)
+    q.mul_(-0.5)
+    graphs[0].replay()
+    graphs[1].replay()
+    torch.cuda.synchronize()
+    want = K.window_attend(*args)
+    assert torch.equal(outs[0], want) and torch.equal(outs[1], want)
+
+
+def test_refusals():
+    q, k, v, ks = inputs([4], [10], 4, 2, 64, BF, gap=0)
+    ok = dict(q=q, k=k, v=v, q_len=[4], k_start=[0], k_len=[10], window=4)
+    K.window_attend(**ok)
+    for bad in (dict(q=q.half()), dict(k=k.float()), dict(v=v[:5]), dict(q=q.cpu()), dict(out=q[:3]),
+                dict(out=q[:1].expand(4, 4, 64)), dict(lse=torch.empty((4, 4), device="cuda", dtype=BF)),
+                dict(q_len=[4, 1]), dict(q_len=[1.5]), dict(k_start=[2 ** 70]), dict(q=q[..., :32])):
+        with pytest.raises((ValueError, OverflowError)):
+            K.window_attend(**{**ok, **bad})
+    for bad in (dict(q_len=[5]), dict(k_len=[11]), dict(k_start=[1]), dict(window=-1), dict(n_sink=-1),
+                dict(scale=math.inf)):
+        with pytest.raises(K.KvpoolError):
+            K.window_attend(**{**ok, **bad})
+    qs, kss, vs, st = inputs([1], [3000], 4, 2, 64, BF, gap=0)
+    call = dict(q=qs, k=kss, v=vs, q_len=[1], k_start=st, k_len=[3000], window=3000)
+    if K.window_workspace(**call):
+        with pytest.raises(K.KvpoolError):
+            K.window_attend(**call, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))

@@ -1,0 +1,103 @@
+"""Refusals and host parts of the entry points without a pool (no GPU)."""
+import ctypes as C
+
+import numpy as np
+import pytest
+
+from heterogeneous_compressed_kv_gb300 import kvpool as K
+
+P16 = 1 << 20  # a plausible, aligned address that nothing reads
+
+
+def heads(n=4, d=64, data=P16, ts=None, hs=None):
+    return K._Heads(data, n * d if ts is None else ts, d if hs is None else hs, n, 0)
+
+
+def table(rot, f):
+    f = np.ascontiguousarray(f, np.float64)
+    out = np.zeros(max(rot // 2, 1), np.uint64)
+    return K.lib().kvpool_rope_table(rot, f.ctypes.data, out.ctypes.data), out
+
+
+def test_rope_table_is_the_fraction_of_a_turn():
+    rot = 128
+    f = 10000.0 ** (-np.arange(0, rot, 2) / rot)
+    rc, t = table(rot, f)
+    assert rc == K.OK
+    # a double's half step (2^-53 relative) of f / (2 pi) < 1, twice (quotient, 2 pi itself)
+    got = t.astype(np.longdouble) / np.longdouble(2) ** 64
+    want = f.astype(np.longdouble) / (2 * np.longdouble(np.pi))
+    assert np.max(np.abs(got - want)) <= 2.0 ** -52
+
+
+def test_rope_table_whole_turns_and_negative_frequencies():
+    rc, t = table(16, [2 * np.pi, -0.25 * 2 * np.pi, 0.0, 1e-30, -1e-30, 3.5 * 2 * np.pi, 1.0, -1.0])
+    assert rc == K.OK
+    turns = t.astype(np.float64) / 2.0 ** 64
+    assert turns[0] in (0.0,) and turns[1] == 0.75 and turns[2] == 0.0 and turns[5] == 0.5
+    assert int(t[6]) + int(t[7]) in range(2 ** 64 - 4096, 2 ** 64 + 4097)  # f and -f are a whole turn together
+    assert t[4] == 0
+
+
+@pytest.mark.parametrize("rot", [-16, 8, 24, 272])
+def test_rope_table_refuses_sizes(rot):
+    assert table(rot, np.ones(max(rot // 2, 1)))[0] == K.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("bad", [np.inf, -np.inf, np.nan])
+def test_rope_table_refuses_frequencies(bad):
+    assert table(16, [1, 1, 1, 1, 1, 1, 1, bad])[0] == K.ERR_INVALID_ARG
+
+
+def rope(dtype=K.BF16, d=64, T=2, q=None, k=None, qo=None, ko=None, eps=1e-6, rot=64, inter=0, tab=P16, pos=P16):
+    q, k = q or heads(), k or heads()
+    qo, ko = qo or q, ko or k
+    r = C.byref
+    return K.lib().kvpool_qk_norm_rope(dtype, d, T, r(q), r(k), r(qo), r(ko), None, None, eps, rot, inter, tab, pos, None)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(dtype=K.FP8_E4M3), dict(d=0), dict(d=60), dict(d=264), dict(rot=-16), dict(rot=24), dict(rot=128), dict(T=-1),
+    dict(eps=-1.0), dict(eps=float("nan")), dict(eps=float("inf")), dict(inter=2), dict(tab=None), dict(pos=None),
+    dict(q=heads(data=P16 + 2)), dict(q=heads(ts=257)), dict(k=heads(hs=68)), dict(k=heads(data=None)),
+    dict(q=heads(n=-1)), dict(qo=heads(n=3)), dict(q=heads(n=70000)), dict(qo=heads(data=None))])
+def test_rope_refuses(bad):
+    assert rope(**bad) == K.ERR_INVALID_ARG
+
+
+def test_rope_without_work():
+    assert rope(T=0) == K.OK
+    none = heads(n=0)
+    assert rope(q=none, k=none) == K.OK
+
+
+def window(q_len, k_start, k_len, n=None, ws=None, ws_bytes=0, **kw):
+    a = K._WindowArgs(kw.get("dtype", K.BF16), kw.get("d", 64), kw.get("q", heads(8)), kw.get("k", heads(4)),
+                      kw.get("v", heads(4)), kw.get("out", heads(8)), kw.get("q_rows", 100), kw.get("kv_rows", 1000), None,
+                      kw.get("window", 16), kw.get("sink", 0), kw.get("scale", 0.125), 0)
+    ql, ks, kl = (np.array(x, t) for x, t in ((q_len, np.int32), (k_start, np.int64), (k_len, np.int32)))
+    call = (C.byref(a), ql.size if n is None else n, ql.ctypes.data, ks.ctypes.data, kl.ctypes.data)
+    got = K.lib().kvpool_window_attend(*call, ws, ws_bytes, None)
+    assert K.lib().kvpool_window_workspace(*call) == (got if got else 0)
+    return got
+
+
+@pytest.mark.parametrize("bad", [
+    dict(dtype=K.FP8_E4M3), dict(d=96), dict(q=heads(3)), dict(q=heads(6)), dict(q=heads(68)), dict(out=heads(4)),
+    dict(v=heads(8)), dict(k=heads(0), v=heads(0)), dict(window=-1), dict(sink=-1), dict(scale=float("nan")),
+    dict(q_rows=1), dict(q_rows=-1), dict(q_rows=1 << 31), dict(kv_rows=1 << 31), dict(q=heads(8, data=None)),
+    dict(k=heads(4, data=None)), dict(v=heads(4, data=P16 + 8)), dict(k=heads(4, ts=257)), dict(out=heads(8, hs=-64))])
+def test_window_refuses_arguments(bad):
+    assert window([2], [0], [5], **bad) == K.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("seg", [([-1], [0], [5]), ([1], [0], [-1]), ([1], [-1], [5]), ([1], [996], [5]),
+                                 ([1], [1 << 40], [5]), ([60, 60], [0, 0], [60, 60]), ([1], [0], [(1 << 30) + 1])])
+def test_window_refuses_segments(seg):
+    assert window(*seg) == K.ERR_INVALID_ARG
+
+
+def test_window_without_work():
+    assert window([], [], []) == K.OK
+    assert window([0, 0], [0, 5], [10, 0]) == K.OK
+    assert window([1], [0], [5], n=-1) == K.ERR_INVALID_ARG
