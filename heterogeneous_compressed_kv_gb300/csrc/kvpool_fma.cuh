@@ -1,0 +1,116 @@
+// kvpool_fma.cuh -- attention of a tile of 64 query rows over steps of 32 keys
+// in fp32 FMAs: the step that the fp32 forms of the attention kernels share.
+#pragma once
+
+#include "device_util.cuh"
+
+namespace kvp {
+
+__device__ __forceinline__ float ex2f(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+constexpr int kFmaRows = 64, kFmaKeys = 32, kFmaThreads = 256;
+
+template <int D>
+struct FmaSmem {
+  float q[kFmaRows][D + 4];
+  float k[kFmaKeys][D + 4];
+  float v[kFmaKeys][D];
+  float p[kFmaRows][kFmaKeys + 4];
+};
+
+// The state of thread (ty, tx) = (tid / 16, tid % 16): rows 4 ty .. 4 ty + 3,
+// keys tx and tx + 16 of a step's scores, dims 4 tx .. 4 tx + 3 (and 64 more)
+// of the outputs.  The running maximum (log2 domain) and sum are the same in
+// the 16 threads of a row.
+template <int D>
+struct FmaTile {
+  float m[4], l[4], o[4][D / 16];
+
+  __device__ __forceinline__ void init() {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      m[r] = -INFINITY;
+      l[r] = 0.0f;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) o[r][c] = 0.0f;
+    }
+  }
+
+  // scores of the staged keys times ks(key), masked by see(row of the thread,
+  // key of the step); weights times vs(key) for the values
+  template <class See, class KScale, class VScale>
+  __device__ __forceinline__ void step(FmaSmem<D>& sm, int ty, int tx, See see, KScale ks, VScale vs) {
+    float s[4][2];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) s[r][0] = s[r][1] = 0.0f;
+#pragma unroll 4
+    for (int c = 0; c < D; c += 4) {
+      const float4 k0 = *reinterpret_cast<const float4*>(&sm.k[tx][c]);
+      const float4 k1 = *reinterpret_cast<const float4*>(&sm.k[tx + 16][c]);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float4 x = *reinterpret_cast<const float4*>(&sm.q[4 * ty + r][c]);
+        s[r][0] = fmaf(x.x, k0.x, fmaf(x.y, k0.y, fmaf(x.z, k0.z, fmaf(x.w, k0.w, s[r][0]))));
+        s[r][1] = fmaf(x.x, k1.x, fmaf(x.y, k1.y, fmaf(x.z, k1.z, fmaf(x.w, k1.w, s[r][1]))));
+      }
+    }
+    const float ks0 = ks(tx), ks1 = ks(tx + 16), vs0 = vs(tx), vs1 = vs(tx + 16);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      s[r][0] = see(r, tx) ? s[r][0] * ks0 : -INFINITY;
+      s[r][1] = see(r, tx + 16) ? s[r][1] * ks1 : -INFINITY;
+      float mx = fmaxf(s[r][0], s[r][1]);
+#pragma unroll
+      for (int off = 8; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+      mx = fmaxf(mx, m[r]);
+      const float base = mx == -INFINITY ? 0.0f : mx;
+      const float corr = ex2f(m[r] - base);
+      const float p0 = ex2f(s[r][0] - base), p1 = ex2f(s[r][1] - base);
+      float ps = p0 + p1;
+#pragma unroll
+      for (int off = 8; off > 0; off >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, off);
+      l[r] = l[r] * corr + ps;
+      m[r] = mx;
+      sm.p[4 * ty + r][tx] = p0 * vs0;
+      sm.p[4 * ty + r][tx + 16] = p1 * vs1;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) o[r][c] *= corr;
+    }
+    __syncwarp();  // a row's weights are written and read by the same half-warp
+#pragma unroll 2
+    for (int j = 0; j < kFmaKeys; j += 4) {
+      float p[4][4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float4 x = *reinterpret_cast<const float4*>(&sm.p[4 * ty + r][j]);
+        p[r][0] = x.x, p[r][1] = x.y, p[r][2] = x.z, p[r][3] = x.w;
+      }
+#pragma unroll
+      for (int jj = 0; jj < 4; ++jj)
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          const float4 y = *reinterpret_cast<const float4*>(&sm.v[j + jj][64 * c + 4 * tx]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            o[r][4 * c] = fmaf(p[r][jj], y.x, o[r][4 * c]);
+            o[r][4 * c + 1] = fmaf(p[r][jj], y.y, o[r][4 * c + 1]);
+            o[r][4 * c + 2] = fmaf(p[r][jj], y.z, o[r][4 * c + 2]);
+            o[r][4 * c + 3] = fmaf(p[r][jj], y.w, o[r][4 * c + 3]);
+          }
+        }
+    }
+  }
+
+  __device__ __forceinline__ void put(float* row_o, int r, int tx) const {
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c)
+      *reinterpret_cast<float4*>(row_o + 64 * c + 4 * tx) =
+          make_float4(o[r][4 * c], o[r][4 * c + 1], o[r][4 * c + 2], o[r][4 * c + 3]);
+  }
+};
+
+}  // namespace kvp

@@ -1211,9 +1211,11 @@ int kvpool_append(kvpool_t* p, int32_t n, const int32_t* h_req_ids, const int32_
   return KVPOOL_OK;
 }
 
-int kvpool_decode_attend(kvpool_t* p, int32_t layer, int32_t n, const int32_t* h_req_ids, const void* d_q,
-                         const void* d_q_idx, int32_t top_k, float* d_out, int32_t* d_topk_out, void* stream) {
-  if (!p) return KVPOOL_ERR_INVALID_ARG;
+// decode_attend; with n_shared > 0 the HCA entries of the first n_shared tokens
+// (the same blocks in every request) are read once for all requests.
+static int decode_attend(kvpool_t* p, int32_t layer, int32_t n, const int32_t* h_req_ids, int64_t n_shared,
+                         const void* d_q, const void* d_q_idx, int32_t top_k, float* d_out, int32_t* d_topk_out,
+                         void* stream) {
   if (layer < 0 || layer >= p->cfg.n_layers || n < 0 || top_k < 0)
     return p->fail(KVPOOL_ERR_INVALID_ARG, "decode_attend: bad layer, n or top_k");
   if (n > p->cfg.max_batch) return p->fail(KVPOOL_ERR_INVALID_ARG, "decode_attend: n > max_batch");
@@ -1225,6 +1227,19 @@ int kvpool_decode_attend(kvpool_t* p, int32_t layer, int32_t n, const int32_t* h
     if (!p->req_ok(h_req_ids[i])) return p->fail(KVPOOL_ERR_BAD_REQUEST, "decode_attend: bad request id");
     if (p->reqs[h_req_ids[i]].length == 0) return p->fail(KVPOOL_ERR_INVALID_ARG, "decode_attend: empty request");
   }
+  if (n_shared < 0) return p->fail(KVPOOL_ERR_INVALID_ARG, "decode_attend: negative shared prefix");
+  if (n_shared % p->cfg.m_prime != 0) return p->fail(KVPOOL_ERR_NOT_SHAREABLE, "decode_attend: shared prefix not whole blocks");
+  const int64_t sh_blocks = n_shared / p->cfg.m_prime;
+  // A block id is drawn once, at one place of one request's table, and gets
+  // into others only with all ids before it (share_prefix copies a prefix; an
+  // import draws new ids).  So requests whose prefixes end in the same id have
+  // the same prefix.
+  for (int i = 0; i < n && sh_blocks > 0; ++i) {
+    const std::vector<int32_t>& t = p->reqs[h_req_ids[i]].table;
+    if ((int64_t)t.size() < sh_blocks || t[sh_blocks - 1] != p->reqs[h_req_ids[0]].table[sh_blocks - 1])
+      return p->fail(KVPOOL_ERR_NOT_SHAREABLE, "decode_attend: the requests do not share that prefix");
+  }
+  const int n_sh = p->lay.layers[layer].has_hca ? (int)sh_blocks : 0;  // shared HCA entries
   if (!p->device()) return p->fail(KVPOOL_ERR_INVALID_ARG, "decode_attend: pool has no device");
   if (n == 0) return KVPOOL_OK;
   if (reinterpret_cast<uintptr_t>(d_q) % 16 != 0) return p->fail(KVPOOL_ERR_INVALID_ARG, "decode_attend: q not 16-byte aligned");
@@ -1296,7 +1311,7 @@ int kvpool_decode_attend(kvpool_t* p, int32_t layer, int32_t n, const int32_t* h
       R.n_cand = Ld.has_csa ? (int32_t)(q.length / p->cfg.m) : 0;
       R.k = std::min(top_k, R.n_cand);
       R.select_all = (R.k == R.n_cand) ? 1 : 0;
-      R.n_hca = Ld.has_hca ? (int32_t)(q.length / p->cfg.m_prime) : 0;
+      R.n_hca = Ld.has_hca ? (int32_t)(q.length / p->cfg.m_prime) - n_sh : 0;  // its own, behind the shared ones
       R.w = (int32_t)std::min<int64_t>(q.length, p->cfg.n_win);
       R.score_base = score_ctas;
       const int nseg = (R.n_cand + EPS - 1) / EPS;
@@ -1334,6 +1349,7 @@ int kvpool_decode_attend(kvpool_t* p, int32_t layer, int32_t n, const int32_t* h
     }
     len0 = fit_one_wave(src_0, len0, max_split_len, target0);
     len1 = fit_one_wave(src_1, len1, max_split_len, attend_target);
+    int split2 = n_sh > 0 ? shared_splits(pd, gn, n_sh, p->n_sms) : 0;
     int splits0 = 0, splits1 = 0, parts = 0;
     for (int pass = 0; pass < 2; ++pass) {
       splits0 = splits1 = parts = 0;
@@ -1348,10 +1364,11 @@ int kvpool_decode_attend(kvpool_t* p, int32_t layer, int32_t n, const int32_t* h
         R.part_base = parts;
         splits0 += R.n_split0;
         splits1 += R.n_split1;
-        parts += R.n_split0 + R.n_split1;
+        parts += R.n_split0 + R.n_split1 + split2;
       }
       if (parts <= kMaxSplits) break;
       len0 = len1 = max_split_len;
+      split2 = std::min(split2, 4);  // of at most 256 requests
     }
     if (parts > kMaxSplits) {
       rc = -1;
@@ -1366,6 +1383,7 @@ int kvpool_decode_attend(kvpool_t* p, int32_t layer, int32_t n, const int32_t* h
     int64_t bytes1 = 0;
     for (int i = 0; i < gn; ++i) bytes1 += (int64_t)P.reqs[i].k * (entry_algo + 4);
     const int64_t bytes0 = attend_bytes - bytes1;
+    const int64_t bytes2 = (int64_t)n_sh * (entry_algo + 4) + (int64_t)gn * pd.HD * pd.isz;
     // [HCA | window] attention needs no top-k: after the indexer scan (which
     // wants every SM) it runs on the side stream, beside the latency-bound
     // select passes; the [selected CSA] part follows the select
@@ -1378,8 +1396,12 @@ int kvpool_decode_attend(kvpool_t* p, int32_t layer, int32_t n, const int32_t* h
       if (e == cudaSuccess) e = cudaStreamWaitEvent(p->side, p->ev_fork, 0);
       if (e != cudaSuccess) rc = (int)e;
     }
+    if (rc == 0 && n_sh > 0)
+      rc = p->launch(KVPOOL_KERNEL_ATTEND, bytes2, s0, [&](int* nk) { return launch_shared(P, n_sh, split2, s0, nk); });
+    P.pool.table = pd.table + 4LL * n_sh;  // part 0 sees the tables from each request's own blocks on
     if (rc == 0)
       rc = p->launch(KVPOOL_KERNEL_ATTEND, bytes0, s0, [&](int* nk) { return launch_attend(P, 0, ctas0, s0, nk); });
+    P.pool.table = pd.table;
     if (rc == 0 && key_ctas > 0)
       rc = p->launch(KVPOOL_KERNEL_SELECT, 0, stream, [&](int* nk) { return launch_select(P, stream, nk, !fork); });
     if (rc == 0)
@@ -1389,12 +1411,26 @@ int kvpool_decode_attend(kvpool_t* p, int32_t layer, int32_t n, const int32_t* h
       if (e == cudaSuccess) e = cudaStreamWaitEvent((cudaStream_t)stream, p->ev_join, 0);
       if (e != cudaSuccess && rc == 0) rc = (int)e;
     }
+    for (int i = 0; i < gn; ++i) P.reqs[i].n_split1 += split2;  // the merge takes a request's partials as one run
     if (rc == 0) rc = p->launch(KVPOOL_KERNEL_COMBINE, out_bytes, stream, [&](int* nk) { return launch_combine(P, stream, nk); });
   }
   if (rc != 0) p->epoch -= 1;
   if (rc == -1) return KVPOOL_ERR_INVALID_ARG;
   if (rc != 0) return p->cuda_fail((cudaError_t)rc, "decode_attend launch");
   return KVPOOL_OK;
+}
+
+int kvpool_decode_attend(kvpool_t* p, int32_t layer, int32_t n, const int32_t* h_req_ids, const void* d_q,
+                         const void* d_q_idx, int32_t top_k, float* d_out, int32_t* d_topk_out, void* stream) {
+  if (!p) return KVPOOL_ERR_INVALID_ARG;
+  return decode_attend(p, layer, n, h_req_ids, 0, d_q, d_q_idx, top_k, d_out, d_topk_out, stream);
+}
+
+int kvpool_decode_attend_shared(kvpool_t* p, int32_t layer, int32_t n, const int32_t* h_req_ids, int64_t n_shared,
+                                const void* d_q, const void* d_q_idx, int32_t top_k, float* d_out, int32_t* d_topk_out,
+                                void* stream) {
+  if (!p) return KVPOOL_ERR_INVALID_ARG;
+  return decode_attend(p, layer, n, h_req_ids, n_shared, d_q, d_q_idx, top_k, d_out, d_topk_out, stream);
 }
 
 int kvpool_request_info(const kvpool_t* p, int32_t r, kvpool_info* info, int32_t* ids, int32_t cap) {

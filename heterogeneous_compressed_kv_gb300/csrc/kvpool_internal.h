@@ -220,5 +220,10 @@ size_t attend_smem_bytes(const PoolDesc& pd);
 int launch_select(const AttendParams& p, void* stream, int* n_kernels, bool alone);
 int launch_attend(const AttendParams& p, int part, int ctas, void* stream, int* n_kernels);
 int launch_combine(const AttendParams& p, void* stream, int* n_kernels);
+// the first n_entries HCA entries of every request of the launch (the same
+// blocks in all of them), cut into n_split runs: partials in the slots behind
+// each request's n_split0 + n_split1 others
+int shared_splits(const PoolDesc& pd, int n, int n_entries, int n_sms);
+int launch_shared(const AttendParams& p, int n_entries, int n_split, void* stream, int* n_kernels);
 
 }  // namespace kvp

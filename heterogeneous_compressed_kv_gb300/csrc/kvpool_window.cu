@@ -15,18 +15,13 @@
 
 #include <cuda_runtime.h>
 
+#include "kvpool_fma.cuh"
 #include "kvpool_window.h"
 
 namespace kvp {
 namespace {
 
 __device__ uint32_t g_ops_error;  // device error word of the calls that have no pool
-
-__device__ __forceinline__ float ex2f(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 template <int T>
 __device__ __forceinline__ float4 load4(const uint8_t* base, int64_t i) {
@@ -49,21 +44,7 @@ __device__ __forceinline__ void store4(uint8_t* base, int64_t i, float4 x) {
   }
 }
 
-// ---- fp32 FMA tiles -----------------------------------------------------------
-// 64 rows x 32 keys per step in fp32 shared memory, 256 threads: thread (ty,
-// tx) owns rows 4 ty .. 4 ty + 3, keys tx and tx + 16 of the scores, and dims
-// 4 tx .. 4 tx + 3 (and 64 more) of the outputs.  The running maximum and sum
-// live in registers, the same in a row's 16 threads.
-constexpr int kFmaRows = 64, kFmaKeys = 32, kFmaThreads = 256;
-
-template <int D>
-struct FmaSmem {
-  float q[kFmaRows][D + 4];
-  float k[kFmaKeys][D + 4];
-  float v[kFmaKeys][D];
-  float p[kFmaRows][kFmaKeys + 4];
-};
-
+// ---- fp32 FMA tiles: 64 rows, 32 keys per step ----------------------------------
 template <int T, int D>
 __global__ void __launch_bounds__(kFmaThreads) window_fma_kernel(const __grid_constant__ WinParams P) {
   pdl_start();
@@ -84,14 +65,8 @@ __global__ void __launch_bounds__(kFmaThreads) window_fma_kernel(const __grid_co
   int pos[4];
 #pragma unroll
   for (int r = 0; r < 4; ++r) pos[r] = 4 * ty + r < rows ? w.pos0 + (4 * ty + r) / P.group : -1;
-  float m[4], l[4], o[4][D / 16];
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    m[r] = -INFINITY;
-    l[r] = 0.0f;
-#pragma unroll
-    for (int c = 0; c < D / 16; ++c) o[r][c] = 0.0f;
-  }
+  FmaTile<D> f;
+  f.init();
   // steps over the first n_s tokens, then over the window's; this split's share
   const int st_s = (w.n_s + kFmaKeys - 1) / kFmaKeys, st_w = (w.n_w + kFmaKeys - 1) / kFmaKeys;
   const int n_st = st_s + st_w;
@@ -112,68 +87,12 @@ __global__ void __launch_bounds__(kFmaThreads) window_fma_kernel(const __grid_co
       *reinterpret_cast<float4*>(&sm.v[r][c]) = y;
     }
     __syncthreads();
-    float s[4][2];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) s[r][0] = s[r][1] = 0.0f;
-#pragma unroll 4
-    for (int c = 0; c < D; c += 4) {
-      const float4 k0 = *reinterpret_cast<const float4*>(&sm.k[tx][c]);
-      const float4 k1 = *reinterpret_cast<const float4*>(&sm.k[tx + 16][c]);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float4 x = *reinterpret_cast<const float4*>(&sm.q[4 * ty + r][c]);
-        s[r][0] = fmaf(x.x, k0.x, fmaf(x.y, k0.y, fmaf(x.z, k0.z, fmaf(x.w, k0.w, s[r][0]))));
-        s[r][1] = fmaf(x.x, k1.x, fmaf(x.y, k1.y, fmaf(x.z, k1.z, fmaf(x.w, k1.w, s[r][1]))));
-      }
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int t = t0 + tx + 16 * j;
-        const bool see = t < end && (sink ? pos[r] >= 0 : win_sees(P, pos[r], t));
-        s[r][j] = see ? s[r][j] * P.scale_log2 : -INFINITY;
-      }
-      float mx = fmaxf(s[r][0], s[r][1]);
-#pragma unroll
-      for (int off = 8; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-      mx = fmaxf(mx, m[r]);
-      const float base = mx == -INFINITY ? 0.0f : mx;
-      const float corr = ex2f(m[r] - base);
-      const float p0 = ex2f(s[r][0] - base), p1 = ex2f(s[r][1] - base);
-      float ps = p0 + p1;
-#pragma unroll
-      for (int off = 8; off > 0; off >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, off);
-      l[r] = l[r] * corr + ps;
-      m[r] = mx;
-      sm.p[4 * ty + r][tx] = p0;
-      sm.p[4 * ty + r][tx + 16] = p1;
-#pragma unroll
-      for (int c = 0; c < D / 16; ++c) o[r][c] *= corr;
-    }
-    __syncwarp();  // a row's weights are written and read by the same half-warp
-#pragma unroll 2
-    for (int j = 0; j < kFmaKeys; j += 4) {
-      float p[4][4];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float4 x = *reinterpret_cast<const float4*>(&sm.p[4 * ty + r][j]);
-        p[r][0] = x.x, p[r][1] = x.y, p[r][2] = x.z, p[r][3] = x.w;
-      }
-#pragma unroll
-      for (int jj = 0; jj < 4; ++jj)
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          const float4 y = *reinterpret_cast<const float4*>(&sm.v[j + jj][64 * c + 4 * tx]);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            o[r][4 * c] = fmaf(p[r][jj], y.x, o[r][4 * c]);
-            o[r][4 * c + 1] = fmaf(p[r][jj], y.y, o[r][4 * c + 1]);
-            o[r][4 * c + 2] = fmaf(p[r][jj], y.z, o[r][4 * c + 2]);
-            o[r][4 * c + 3] = fmaf(p[r][jj], y.w, o[r][4 * c + 3]);
-          }
-        }
-    }
+    f.step(
+        sm, ty, tx,
+        [&](int r, int j) {
+          return t0 + j < end && (sink ? pos[r] >= 0 : win_sees(P, pos[r], t0 + j));
+        },
+        [&](int) { return P.scale_log2; }, [](int) { return 1.0f; });
   }
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
@@ -181,22 +100,20 @@ __global__ void __launch_bounds__(kFmaThreads) window_fma_kernel(const __grid_co
     if (row >= rows) continue;
     if (w.n_split > 1) {
       const int64_t pr = (int64_t)w.slot * P.tile_rows + row;
-      if (tx == 0) P.part_ml[pr] = make_float2(m[r], l[r]);
-#pragma unroll
-      for (int c = 0; c < D / 64; ++c)
-        *reinterpret_cast<float4*>(P.part_o + pr * D + 64 * c + 4 * tx) =
-            make_float4(o[r][4 * c], o[r][4 * c + 1], o[r][4 * c + 2], o[r][4 * c + 3]);
+      if (tx == 0) P.part_ml[pr] = make_float2(f.m[r], f.l[r]);
+      f.put(P.part_o + pr * D, r, tx);
       continue;
     }
-    const float inv = l[r] > 0.0f ? 1.0f / l[r] : 0.0f;
+    const float inv = f.l[r] > 0.0f ? 1.0f / f.l[r] : 0.0f;
     const int64_t tok = S.q_row0 + w.tok0 + row / P.group;
     const int h = w.hk * P.group + row % P.group;
 #pragma unroll
     for (int c = 0; c < D / 64; ++c)
       store4<T>(P.out, tok * P.o_tok + h * P.o_head + 64 * c + 4 * tx,
-                make_float4(o[r][4 * c] * inv, o[r][4 * c + 1] * inv, o[r][4 * c + 2] * inv, o[r][4 * c + 3] * inv));
+                make_float4(f.o[r][4 * c] * inv, f.o[r][4 * c + 1] * inv, f.o[r][4 * c + 2] * inv,
+                            f.o[r][4 * c + 3] * inv));
     if (P.lse && tx == 0)
-      P.lse[tok * P.q_heads + h] = l[r] > 0.0f ? (m[r] + log2f(l[r])) * 0.69314718055994531f : -INFINITY;
+      P.lse[tok * P.q_heads + h] = f.l[r] > 0.0f ? (f.m[r] + log2f(f.l[r])) * 0.69314718055994531f : -INFINITY;
   }
 }
 

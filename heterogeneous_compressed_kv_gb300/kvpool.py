@@ -33,7 +33,8 @@ EXPORTS = ["kvpool_required_bytes", "kvpool_create", "kvpool_destroy", "kvpool_a
            "kvpool_export_prefix", "kvpool_import_prefix", "kvpool_host_slot_bytes", "kvpool_set_host_pool",
            "kvpool_offload", "kvpool_fetch", "kvpool_block_location", "kvpool_epoch", "kvpool_block_activity",
            "kvpool_inactive_blocks", "kvpool_wait_selftest", "kvpool_topk_static_check", "kvpool_rope_table",
-           "kvpool_qk_norm_rope", "kvpool_window_workspace", "kvpool_window_attend"]
+           "kvpool_qk_norm_rope", "kvpool_window_workspace", "kvpool_window_attend",
+           "kvpool_decode_attend_shared"]
 
 
 class KvpoolError(RuntimeError):
@@ -104,6 +105,7 @@ def lib():
         L.kvpool_share_prefix.argtypes = [vp, i32, i32, i64, vp, vp, vp]
         L.kvpool_append.argtypes = [vp, i32, vp, vp, vp, vp, vp, vp]
         L.kvpool_decode_attend.argtypes = [vp, i32, i32, vp, vp, vp, i32, vp, vp, vp]
+        L.kvpool_decode_attend_shared.argtypes = [vp, i32, i32, vp, i64, vp, vp, i32, vp, vp, vp]
         L.kvpool_request_info.argtypes = [vp, i32, C.POINTER(_Info), vp, i32]
         L.kvpool_block_refcount.argtypes = [vp, i32]
         L.kvpool_free_block_count.argtypes = [vp]
@@ -562,6 +564,15 @@ class Pool:
         rc = self.L.kvpool_decode_attend(self.h, layer, req.size, req.ctypes.data, _ptr(q),
                                          _ptr(q_idx), top_k, _ptr(out), _ptr(topk_out), _stream(stream))
         return self._check(rc, "decode_attend") if check else rc
+
+    def decode_attend_shared(self, layer, req_ids, n_shared, q, q_idx, top_k, out, topk_out=None, stream=None,
+                             check=True) -> int:
+        """decode_attend of requests whose first n_shared tokens are the same
+        blocks, whose HCA entries are read once for all of them."""
+        req = _i32(req_ids)
+        rc = self.L.kvpool_decode_attend_shared(self.h, layer, req.size, req.ctypes.data, n_shared, _ptr(q), _ptr(q_idx),
+                                                top_k, _ptr(out), _ptr(topk_out), _stream(stream))
+        return self._check(rc, "decode_attend_shared") if check else rc
 
     # ---- queries ----
     def request_info(self, req: int, cap: int = 1 << 16):

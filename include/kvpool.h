@@ -323,6 +323,21 @@ int kvpool_append(kvpool_t* pool, int32_t n, const int32_t* h_req_ids, const int
 int kvpool_decode_attend(kvpool_t* pool, int32_t layer, int32_t n, const int32_t* h_req_ids, const void* d_q,
                          const void* d_q_idx, int32_t top_k, float* d_out, int32_t* d_topk_out, void* stream);
 
+/* kvpool_decode_attend of requests whose first n_shared tokens are the same
+ * sealed blocks ([P3] s2.2; kvpool_share_prefix): the HCA entries of those
+ * blocks are read once for the whole batch instead of once per request, as a
+ * dense product of all requests' queries per head.  Same arguments, outputs
+ * and selected entries as kvpool_decode_attend; outputs differ from its by
+ * the order of the fp32 sums (and, with an fp8 cache, by being closer to the
+ * decoded values).  The indexer scan, the selected CSA entries and the window
+ * stay per request.  n_shared: a multiple of m' (0: nothing is shared).
+ * Errors: as kvpool_decode_attend; INVALID_ARG (n_shared negative),
+ * NOT_SHAREABLE (n_shared not a multiple of m', or requests whose first
+ * n_shared / m' blocks are not the same). */
+int kvpool_decode_attend_shared(kvpool_t* pool, int32_t layer, int32_t n, const int32_t* h_req_ids, int64_t n_shared,
+                                const void* d_q, const void* d_q_idx, int32_t top_k, float* d_out, int32_t* d_topk_out,
+                                void* stream);
+
 /* Top-k selection over a caller's score matrix that allocates nothing.  The
  * design pages have no counterpart of this entry point: it is the indexer's
  * selection step (same rule as decode_attend: k = min(top_k, n_cols) largest

@@ -101,3 +101,27 @@ def test_window_without_work():
     assert window([], [], []) == K.OK
     assert window([0, 0], [0, 5], [10, 0]) == K.OK
     assert window([1], [0], [5], n=-1) == K.ERR_INVALID_ARG
+
+
+def test_shared_decode_refuses_what_is_not_shared():
+    from tests.test_abi_host import base_workload, cfg_of
+    p = K.Pool(cfg_of(base_workload(layer_kinds=[K.HCA])))
+    a, b, c = (p.alloc_request() for _ in range(3))
+    buf = np.zeros(16, np.float32).ctypes.data
+
+    def call(ids, n_shared, layer=0):
+        return p.decode_attend_shared(layer, ids, n_shared, buf, buf, 0, buf, stream=0, check=False)
+
+    p.append([a], [600], 1, 1, 1, stream=0)
+    p.append([c], [600], 1, 1, 1, stream=0)
+    p.share_prefix(b, a, 256, 1, 1, stream=0)
+    p.append([b], [300], 1, 1, 1, stream=0)
+    assert call([a, b], 256) == K.ERR_INVALID_ARG and "no device" in p.last_error()  # shared: only the device is missing
+    assert call([b, a, b], 128) == K.ERR_INVALID_ARG and "no device" in p.last_error()
+    assert call([a], 512) == K.ERR_INVALID_ARG and "no device" in p.last_error()
+    for ids, n in (([a, b], 384), ([a, b], 512), ([a, c], 128), ([a, b], 100), ([a], 640), ([a, b], 1 << 40), ([c, b], 256)):
+        assert call(ids, n) == K.ERR_NOT_SHAREABLE, (ids, n)
+    assert call([a, b], -128) == K.ERR_INVALID_ARG
+    assert call([a, 7], 128) == K.ERR_BAD_REQUEST
+    assert call([a], 0, layer=1) == K.ERR_INVALID_ARG
+    assert p.L.kvpool_decode_attend_shared(None, 0, 0, None, 0, None, None, 0, None, None, None) == K.ERR_INVALID_ARG
