@@ -173,8 +173,8 @@ bool strides_ok(const kvpool_heads& h, int32_t dtype) {
          h.token_stride >= 0 && h.head_stride >= 0;
 }
 
-int check_args(const kvpool_window_args* a, int32_t n, const int32_t* q_len, const int64_t* k_start,
-               const int32_t* k_len, int64_t* total_q) {
+int check_args(const kvpool_window_args* a, int32_t n, const int64_t* q_len, const int64_t* k_start,
+               const int64_t* k_len, int64_t* total_q) {
   if (!a || n < 0) return KVPOOL_ERR_INVALID_ARG;
   if (a->dtype != KVPOOL_F32 && a->dtype != KVPOOL_BF16) return KVPOOL_ERR_INVALID_ARG;
   if (a->head_dim != 64 && a->head_dim != 128) return KVPOOL_ERR_INVALID_ARG;
@@ -203,36 +203,57 @@ int check_args(const kvpool_window_args* a, int32_t n, const int32_t* q_len, con
   return KVPOOL_OK;
 }
 
+// ---- which kernel takes a segment ------------------------------------------------
+enum Form { kFormTc, kFormFma, kForms };
+
+// The tensor copies' limits: strides of used axes positive and below 2^40
+// bytes; the softmax takes the maximum before the scale, so that is positive.
+bool tc_able(const kvpool_window_args* a) {
+  if (a->dtype != KVPOOL_BF16 || !(a->scale > 0.0f)) return false;
+  auto ok = [](int64_t stride, int64_t extent) { return extent <= 1 || (stride > 0 && stride < (1ll << 38)); };
+  return ok(a->q.token_stride, a->q_rows) && ok(a->q.head_stride, a->q.heads) && ok(a->q.head_stride * 16, a->k.heads) &&
+         ok(a->k.token_stride, a->kv_rows) && ok(a->k.head_stride, a->k.heads) && ok(a->v.token_stride, a->kv_rows) &&
+         ok(a->v.head_stride, a->v.heads);
+}
+
+Form form_of(const kvpool_window_args* a, bool tc, int64_t q_len, int64_t k_len) {
+  const int64_t rows = q_len * (a->q.heads / a->k.heads);
+  return tc && k_len > 0 && rows > 16 ? kFormTc : kFormFma;
+}
+
 // the most keys that a tile of the segment sees
-int64_t tile_keys(const kvpool_window_args* a, int32_t q_len, int32_t k_len, int tile_tokens) {
-  const int64_t w = (int64_t)a->window + std::min(tile_tokens, q_len) + a->n_sink;
+int64_t tile_keys(const kvpool_window_args* a, int64_t q_len, int64_t k_len, int tile_tokens) {
+  const int64_t w = (int64_t)a->window + std::min<int64_t>(tile_tokens, q_len) + a->n_sink;
   return std::min<int64_t>(k_len, w);
 }
 
 // Fill segments [i0, n) of one launch (at most kMaxWinSegs with queries);
 // returns the next segment.  A launch with few tiles cuts each tile's keys
 // into parts (merged by a second kernel) so that the GPU is filled.
-int plan_launch(const kvpool_window_args* a, int32_t i0, int32_t n, const int32_t* q_len, const int64_t* k_start,
-                const int32_t* k_len, int64_t q_row0, int n_sms, WinParams* P, int64_t* next_row, int64_t* slots) {
+int plan_launch(const kvpool_window_args* a, Form form, bool tc, int32_t i0, int32_t n, const int64_t* q_len,
+                const int64_t* k_start, const int64_t* k_len, int64_t q_row0, int n_sms, WinParams* P, int64_t* next_row,
+                int64_t* slots) {
   const int Hk = a->k.heads;
+  P->tile_tokens = form == kFormTc ? 2 * (kTcTileRows / P->group) : kFmaRows / P->group;
+  P->tile_rows = P->tile_tokens * P->group;
   int i = i0;
   P->n_segs = 0;
   int64_t tiles = 0;
   for (; i < n && P->n_segs < kMaxWinSegs; ++i) {
-    if (q_len[i] > 0) {
+    if (q_len[i] > 0 && form_of(a, tc, q_len[i], k_len[i]) == form) {
       WinSeg& S = P->segs[P->n_segs++];
       S = WinSeg{};
       S.q_row0 = q_row0;
       S.k_start = k_len[i] > 0 ? k_start[i] : 0;
-      S.q_len = q_len[i];
-      S.k_len = k_len[i];
+      S.q_len = (int32_t)q_len[i];
+      S.k_len = (int32_t)k_len[i];
       tiles += (int64_t)((q_len[i] + P->tile_tokens - 1) / P->tile_tokens) * Hk;
     }
     q_row0 += q_len[i];
   }
   *next_row = q_row0;
   constexpr int kMinSplitKeys = 128;
-  const int64_t want = 2LL * n_sms;  // work items
+  const int64_t want = form == kFormTc ? n_sms : 2LL * n_sms;  // work items
   int64_t items = 0, slot = 0;
   for (int s = 0; s < P->n_segs; ++s) {
     WinSeg& S = P->segs[s];
@@ -248,7 +269,7 @@ int plan_launch(const kvpool_window_args* a, int32_t i0, int32_t n, const int32_
     items += st * split;
     if (split > 1) slot += st * split;
   }
-  P->n_items = items <= 0x7FFFFFFF ? (int32_t)items : -1;
+  P->n_items = items <= (1 << 30) ? (int32_t)items : -1;
   *slots = slot;
   return i;
 }
@@ -273,8 +294,6 @@ void fill_params(const kvpool_window_args* a, WinParams* P) {
   P->window = std::min(a->window, kMaxLen);
   P->n_sink = std::min(a->n_sink, kMaxLen);
   P->scale_log2 = a->scale * 1.4426950408889634f;
-  P->tile_tokens = kFmaRows / P->group;
-  P->tile_rows = P->tile_tokens * P->group;
 }
 
 int64_t slot_bytes(const WinParams& P, int head_dim) { return (int64_t)P.tile_rows * (head_dim + 2) * 4; }
@@ -287,21 +306,23 @@ int device_sms() {
 }
 
 template <int T, int D>
-cudaError_t launch_window(const WinParams& P, bool merge, cudaStream_t s) {
+cudaError_t launch_fma(const WinParams& P, cudaStream_t s) {
   constexpr int smem = (int)sizeof(FmaSmem<D>);
   auto* kern = window_fma_kernel<T, D>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e == cudaSuccess) e = launch_kernel(true, kern, dim3(P.n_items), dim3(kFmaThreads), smem, s, P);
-  if (e == cudaSuccess && merge)
-    e = launch_kernel(true, window_merge_kernel<T, D>, dim3(P.n_items, (P.tile_rows + 3) / 4), dim3(128), 0, s, P);
-  return e;
+  return e == cudaSuccess ? launch_kernel(true, kern, dim3(P.n_items), dim3(kFmaThreads), smem, s, P) : e;
+}
+
+template <int T, int D>
+cudaError_t launch_merge(const WinParams& P, cudaStream_t s) {
+  return launch_kernel(true, window_merge_kernel<T, D>, dim3(P.n_items, (P.tile_rows + 3) / 4), dim3(128), 0, s, P);
 }
 
 }  // namespace
 }  // namespace kvp
 
-extern "C" int64_t kvpool_window_workspace(const kvpool_window_args* a, int32_t n, const int32_t* h_q_len,
-                                           const int64_t* h_k_start, const int32_t* h_k_len) {
+extern "C" int64_t kvpool_window_workspace(const kvpool_window_args* a, int32_t n, const int64_t* h_q_len,
+                                           const int64_t* h_k_start, const int64_t* h_k_len) {
   using namespace kvp;
   int64_t total = 0;
   const int rc = check_args(a, n, h_q_len, h_k_start, h_k_len, &total);
@@ -312,16 +333,19 @@ extern "C" int64_t kvpool_window_workspace(const kvpool_window_args* a, int32_t 
   std::unique_ptr<WinParams> P(new (std::nothrow) WinParams);
   if (!P) return KVPOOL_ERR_INVALID_ARG;
   fill_params(a, P.get());
-  int64_t most = 0, row = 0, slots = 0;
-  for (int i = 0; i < n;) {
-    i = plan_launch(a, i, n, h_q_len, h_k_start, h_k_len, row, sms, P.get(), &row, &slots);
-    most = std::max(most, slots * slot_bytes(*P, a->head_dim));
-  }
+  const bool tc = tc_able(a);
+  int64_t most = 0;
+  for (int f = 0; f < kForms; ++f)
+    for (int64_t i = 0, row = 0, slots = 0; i < n;) {
+      i = plan_launch(a, (Form)f, tc, (int32_t)i, n, h_q_len, h_k_start, h_k_len, row, sms, P.get(), &row, &slots);
+      if (P->n_items < 0) return KVPOOL_ERR_INVALID_ARG;
+      most = std::max(most, slots * slot_bytes(*P, a->head_dim));
+    }
   return most;
 }
 
-extern "C" int kvpool_window_attend(const kvpool_window_args* a, int32_t n, const int32_t* h_q_len,
-                                    const int64_t* h_k_start, const int32_t* h_k_len, void* d_workspace,
+extern "C" int kvpool_window_attend(const kvpool_window_args* a, int32_t n, const int64_t* h_q_len,
+                                    const int64_t* h_k_start, const int64_t* h_k_len, void* d_workspace,
                                     int64_t workspace_bytes, void* stream) {
   using namespace kvp;
   int64_t total = 0;
@@ -336,20 +360,44 @@ extern "C" int kvpool_window_attend(const kvpool_window_args* a, int32_t n, cons
   std::unique_ptr<WinParams> P(new (std::nothrow) WinParams);
   if (!P) return KVPOOL_ERR_INVALID_ARG;
   fill_params(a, P.get());
+  uint32_t* err = nullptr;
+  if (cudaGetSymbolAddress(reinterpret_cast<void**>(&err), g_ops_error) != cudaSuccess) return KVPOOL_ERR_CUDA;
+  P->err = err;
+  const bool tc = tc_able(a);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  int64_t row = 0, slots = 0;
-  for (int i = 0; i < n;) {
-    i = plan_launch(a, i, n, h_q_len, h_k_start, h_k_len, row, sms, P.get(), &row, &slots);
-    if (P->n_segs == 0) continue;
-    if (P->n_items < 0) return KVPOOL_ERR_INVALID_ARG;
-    P->part_o = static_cast<float*>(d_workspace);
-    P->part_ml = reinterpret_cast<float2*>(P->part_o + slots * P->tile_rows * a->head_dim);
-    cudaError_t e;
-    if (a->dtype == KVPOOL_F32)
-      e = a->head_dim == 128 ? launch_window<KVPOOL_F32, 128>(*P, slots > 0, s) : launch_window<KVPOOL_F32, 64>(*P, slots > 0, s);
-    else
-      e = a->head_dim == 128 ? launch_window<KVPOOL_BF16, 128>(*P, slots > 0, s) : launch_window<KVPOOL_BF16, 64>(*P, slots > 0, s);
-    if (e != cudaSuccess) return KVPOOL_ERR_CUDA;
-  }
+  for (int f = 0; f < kForms; ++f)
+    for (int64_t i = 0, row = 0, slots = 0; i < n;) {
+      i = plan_launch(a, (Form)f, tc, (int32_t)i, n, h_q_len, h_k_start, h_k_len, row, sms, P.get(), &row, &slots);
+      if (P->n_segs == 0) continue;
+      P->part_o = static_cast<float*>(d_workspace);
+      P->part_ml = reinterpret_cast<float2*>(P->part_o + slots * P->tile_rows * a->head_dim);
+      cudaError_t e = cudaSuccess;
+      if (f == kFormTc) e = (cudaError_t)launch_window_tc(*P, a->head_dim, a->q_rows, a->kv_rows, sms, stream);
+      else if (a->dtype == KVPOOL_F32)
+        e = a->head_dim == 128 ? launch_fma<KVPOOL_F32, 128>(*P, s) : launch_fma<KVPOOL_F32, 64>(*P, s);
+      else
+        e = a->head_dim == 128 ? launch_fma<KVPOOL_BF16, 128>(*P, s) : launch_fma<KVPOOL_BF16, 64>(*P, s);
+      if (e == cudaSuccess && slots > 0) {
+        if (a->dtype == KVPOOL_F32)
+          e = a->head_dim == 128 ? launch_merge<KVPOOL_F32, 128>(*P, s) : launch_merge<KVPOOL_F32, 64>(*P, s);
+        else
+          e = a->head_dim == 128 ? launch_merge<KVPOOL_BF16, 128>(*P, s) : launch_merge<KVPOOL_BF16, 64>(*P, s);
+      }
+      if (e != cudaSuccess) return KVPOOL_ERR_CUDA;
+    }
   return KVPOOL_OK;
+}
+
+extern "C" int kvpool_window_check(void* stream, uint32_t* h_flags) {
+  using namespace kvp;
+  uint32_t word = 0;
+  void* err = nullptr;
+  if (cudaGetSymbolAddress(&err, g_ops_error) != cudaSuccess) return KVPOOL_ERR_CUDA;
+  const uint32_t zero = 0;
+  if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess ||
+      cudaMemcpy(&word, err, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess ||
+      (word && cudaMemcpy(err, &zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess))
+    return KVPOOL_ERR_CUDA;
+  if (h_flags) *h_flags = word;
+  return word == 0 ? KVPOOL_OK : KVPOOL_ERR_DEVICE_CHECK;
 }

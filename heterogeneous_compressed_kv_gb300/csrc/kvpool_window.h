@@ -84,4 +84,9 @@ __device__ __forceinline__ bool win_sees(const WinParams& P, int p, int t) {
   return t <= p && (t > p - P.window || t < P.n_sink);
 }
 
+// Tensor-core form of a launch of prompts (bf16); tiles of two times
+// tile_tokens / 2 tokens.  Returns a cudaError_t.
+constexpr int kTcTileRows = 128;
+int launch_window_tc(const WinParams& P, int head_dim, int64_t q_rows, int64_t kv_rows, int n_sms, void* stream);
+
 }  // namespace kvp

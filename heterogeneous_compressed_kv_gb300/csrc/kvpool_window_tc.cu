@@ -1,0 +1,526 @@
+// kvpool_window_tc.cu -- window attention of prompts on the 5th-generation
+// tensor cores (bf16).
+//
+// A work item is 256 query rows (token, query head of the group) of one key
+// head: two tiles of 128 rows that share every K and V tile of 128 keys.
+// Persistent CTAs, one per SM, of ten warps: one issues the tensor copies
+// (Q tiles, and a ring of K and V tiles), one the matrix products, and a group
+// of four per query tile does its softmax, a thread per row.  Scores S = Q K^T
+// go to tensor memory; the softmax reads a row, keeps the running maximum and
+// sum in fp32, and writes the weights back as bf16 over the scores; O += P V
+// accumulates in tensor memory.  While one tile's rows go through the softmax
+// the products of the other tile run, so the tensor core and the exponentials
+// (both about 1,024 cycles per 128 x 128 x 128 tile pair and side) overlap.
+//
+// The outputs are rescaled only when a row's maximum grows by more than 2^8:
+// until then its weights are taken against the older maximum (bf16 keeps its
+// relative precision up to 2^8, the sums are fp32), so the read-modify-write
+// of O leaves the critical path.
+//
+// Rows of K and V behind what any row of the item sees never count: scores are
+// masked, and such V rows are zeroed in shared memory before the product (0
+// times a NaN there would reach every row).
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "kvpool_fma.cuh"
+#include "kvpool_tcgen05.cuh"
+#include "kvpool_window.h"
+
+namespace kvp {
+namespace {
+
+constexpr int kTcKeys = 128;
+constexpr int kTcThreads = 320;
+constexpr float kRescale = 8.0f;  // log2 growth of the maximum that rescales O
+
+template <int D>
+struct TcShape {
+  static constexpr int kTileBytes = 128 * D * 2;  // a Q, K or V tile: D / 64 runs of 128 rows x 128 bytes
+  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kBarOff = (2 + kStages) * kTileBytes;
+  static constexpr int kSmem = kBarOff + 256 + 1024;  // + slack to align the tiles to 1,024 bytes
+};
+
+struct TcMaps {
+  CUtensorMap q, k, v;
+};
+
+// Step st of an item: 128 keys from token t0 on, of which those before `end` count.
+struct TcStep {
+  int t0, end;
+  bool sink;
+};
+__device__ __forceinline__ TcStep tc_step(const WinItem& w, int st) {
+  const int st_s = (w.n_s + kTcKeys - 1) / kTcKeys;
+  TcStep s;
+  s.sink = st < st_s;
+  s.t0 = s.sink ? st * kTcKeys : w.lo + (st - st_s) * kTcKeys;
+  s.end = s.sink ? w.n_s : w.lo + w.n_w;
+  return s;
+}
+// this split's steps [a, b) of an item
+__device__ __forceinline__ void tc_range(const WinItem& w, int& a, int& b) {
+  const int n = (w.n_s + kTcKeys - 1) / kTcKeys + (w.n_w + kTcKeys - 1) / kTcKeys;
+  a = (int)((int64_t)n * w.split / w.n_split);
+  b = (int)((int64_t)n * (w.split + 1) / w.n_split);
+}
+// A query tile of an item: tokens at positions p0 .. p1 (n of them)
+struct TcTile {
+  int n, p0, p1;
+};
+__device__ __forceinline__ TcTile tc_tile(const WinParams& P, const WinItem& w, int t) {
+  const int tt = P.tile_tokens / 2;
+  TcTile q;
+  q.n = max(0, min(tt, w.n_tok - t * tt));
+  q.p0 = w.pos0 + t * tt;
+  q.p1 = q.p0 + q.n - 1;
+  return q;
+}
+// does some row of the tile see some key of the step?
+__device__ __forceinline__ bool tc_need(const WinParams& P, const TcTile& q, const TcStep& s) {
+  if (q.n <= 0) return false;
+  return s.sink || (s.t0 <= q.p1 && (s.t0 + kTcKeys - 1 > q.p0 - P.window || s.t0 < P.n_sink));
+}
+
+// k-th item of a CTA: back and forth over the CTAs, the last (longest) tiles first
+__device__ __forceinline__ int tc_nth(const WinParams& P, int k) {
+  const int g = gridDim.x, c = blockIdx.x;
+  const int i = k * g + ((k & 1) ? g - 1 - c : c);
+  return i < P.n_items ? P.n_items - 1 - i : -1;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_constant__ WinParams P,
+                                                                  const __grid_constant__ TcMaps M) {
+  pdl_start();
+  using Sh = TcShape<D>;
+  constexpr int NS = Sh::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+  uint8_t* q_tile = smem;
+  uint8_t* ring = smem + 2 * Sh::kTileBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Sh::kBarOff);
+  uint64_t *kv_full = bars, *kv_free = kv_full + NS, *q_full = kv_free + NS, *q_free = q_full + 2, *s_full = q_free + 2,
+           *p_ready = s_full + 2, *o_full = p_ready + 2, *o_free = o_full + 2, *drain = o_free + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&kv_full[i], 1);
+      mbar_init(&kv_free[i], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&q_full[t], 1);
+      mbar_init(&q_free[t], 1);
+      mbar_init(&s_full[t], 1);
+      mbar_init(&p_ready[t], 4);
+      mbar_init(&o_full[t], 1);
+      mbar_init(&o_free[t], 4);
+    }
+    mbar_init(drain, 1);
+    mbar_fence_init();
+  }
+  if (warp == 9) tmem_alloc(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;  // columns: S0, S1 (128 each), O0, O1 (128 each)
+
+  if (warp == 8) {
+    // ---- tensor copies ----
+    int stage = 0, n_q[2] = {0, 0};
+    uint32_t round = 0;  // of the ring
+    int issued = 0;
+    bool ok = true;
+    auto load = [&](const CUtensorMap* map, int hk, int row) {
+      if (round > 0) ok = ok && warp_wait(&kv_free[stage], (round - 1) & 1, P.err);
+      if (!ok) return;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&kv_full[stage], Sh::kTileBytes);
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+          tma_load_3d(ring + stage * Sh::kTileBytes + c * 16384, map, 64 * c, hk, row, &kv_full[stage]);
+      }
+      __syncwarp();
+      ++issued;
+      if (++stage == NS) {
+        stage = 0;
+        ++round;
+      }
+    };
+    for (int k = 0; ok; ++k) {
+      const int item = tc_nth(P, k);
+      if (item < 0) break;
+      const WinItem w = win_item(P, item);
+      const WinSeg& S = P.segs[w.seg];
+      int a, b;
+      tc_range(w, a, b);
+      if (a >= b) continue;
+      const int tt = P.tile_tokens / 2;
+      for (int t = 0; t < 2; ++t) {
+        if (w.n_tok <= t * tt) break;
+        if (n_q[t] > 0) ok = ok && warp_wait(&q_free[t], (n_q[t] - 1) & 1, P.err);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&q_full[t], tt * P.group * D * 2);
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_4d(q_tile + t * Sh::kTileBytes + c * 16384, &M.q, 64 * c, 0, w.hk, (int)S.q_row0 + w.tok0 + t * tt,
+                        &q_full[t]);
+        }
+        __syncwarp();
+        ++n_q[t];
+        if (t == 0 && ok) load(&M.k, w.hk, (int)S.k_start + tc_step(w, a).t0);  // the first K between the Q tiles
+      }
+      for (int st = a; st < b && ok; ++st) {
+        const int row = (int)S.k_start + tc_step(w, st).t0;
+        if (st > a) load(&M.k, w.hk, row);
+        if (ok) load(&M.v, w.hk, row);
+      }
+    }
+    // the CTA does not end while copies land in its shared memory
+    for (int i = issued > NS ? issued - NS : 0; i < issued; ++i) warp_wait(&kv_full[i % NS], (i / NS) & 1, P.err);
+    for (int t = 0; t < 2; ++t)
+      if (n_q[t] > 0) warp_wait(&q_full[t], (n_q[t] - 1) & 1, P.err);
+  } else if (warp == 9) {
+    // ---- matrix products (lane 0 issues) ----
+    constexpr uint32_t kIdQK = bf16_idesc(128, kTcKeys, false), kIdPV = bf16_idesc(128, D, true);
+    const uint32_t q_addr = smem_addr(q_tile), ring_addr = smem_addr(ring);
+    int stage = 0;
+    uint32_t round = 0;
+    int n_q[2] = {0, 0}, n_p[2] = {0, 0}, n_o[2] = {0, 0};
+    bool ok = true;
+    auto next = [&]() {
+      if (++stage == NS) {
+        stage = 0;
+        ++round;
+      }
+    };
+    auto qk = [&](int t, int s) {
+      if (lane == 0) {
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          const uint32_t off = (c / 4) * 16384 + (c % 4) * 32;
+          mma_ss(tmem + 128 * t, smem_desc(q_addr + t * Sh::kTileBytes + off, 16),
+                 smem_desc(ring_addr + s * Sh::kTileBytes + off, 16), kIdQK, c > 0);
+        }
+        mma_commit(&s_full[t]);
+      }
+    };
+    for (int k = 0; ok; ++k) {
+      const int item = tc_nth(P, k);
+      if (item < 0) break;
+      const WinItem w = win_item(P, item);
+      int a, b;
+      tc_range(w, a, b);
+      if (a >= b) continue;
+      const TcTile q[2] = {tc_tile(P, w, 0), tc_tile(P, w, 1)};
+      int last[2] = {-1, -1};  // the last step that the tile needs
+      for (int t = 0; t < 2; ++t)
+        for (int st = b - 1; st >= a && last[t] < 0; --st)
+          if (tc_need(P, q[t], tc_step(w, st))) last[t] = st;
+      bool first_qk[2] = {true, true}, first_pv[2] = {true, true};
+      // scores of step st against the K tile in ring stage s
+      auto scores = [&](int t, int st, int s) {
+        if (!tc_need(P, q[t], tc_step(w, st))) return;
+        if (first_qk[t]) {
+          ok = ok && warp_wait(&q_full[t], n_q[t] & 1, P.err);
+          if (!ok) return;
+          tc_fence_after();
+          ++n_q[t];
+          first_qk[t] = false;
+        }
+        qk(t, s);
+        if (lane == 0 && st == last[t]) mma_commit(&q_free[t]);
+      };
+      ok = ok && warp_wait(&kv_full[stage], round & 1, P.err);
+      if (!ok) break;
+      tc_fence_after();
+      for (int t = 0; t < 2 && ok; ++t) scores(t, a, stage);
+      if (!ok) break;
+      if (lane == 0) mma_commit(&kv_free[stage]);
+      next();
+      for (int st = a; st < b && ok; ++st) {
+        const TcStep cur = tc_step(w, st);
+        const int vs = stage;
+        ok = warp_wait(&kv_full[vs], round & 1, P.err);
+        if (!ok) break;
+        tc_fence_after();
+        next();
+        if (cur.t0 + kTcKeys > cur.end) {  // rows that nobody sees: zeros
+          const int r0 = cur.end - cur.t0;
+          for (int c = 0; c < D / 64; ++c) {
+            uint4* base = reinterpret_cast<uint4*>(ring + vs * Sh::kTileBytes + c * 16384);
+            for (int i = r0 * 8 + lane; i < 128 * 8; i += 32) base[i] = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async();
+          __syncwarp();
+        }
+        const int ks = stage;
+        if (st + 1 < b) {
+          ok = warp_wait(&kv_full[ks], round & 1, P.err);
+          if (!ok) break;
+          tc_fence_after();
+        }
+        for (int t = 0; t < 2; ++t) {
+          if (tc_need(P, q[t], cur)) {
+            ok = ok && warp_wait(&p_ready[t], n_p[t] & 1, P.err);
+            ++n_p[t];
+            if (ok && first_pv[t] && n_o[t] > 0) ok = warp_wait(&o_free[t], (n_o[t] - 1) & 1, P.err);
+            if (!ok) break;
+            tc_fence_after();
+            if (lane == 0) {
+#pragma unroll
+              for (int c = 0; c < kTcKeys / 16; ++c)
+                mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * c,
+                       smem_desc(ring_addr + vs * Sh::kTileBytes + c * 2048, 16384), kIdPV, !first_pv[t] || c > 0);
+              if (st == last[t]) mma_commit(&o_full[t]);
+            }
+            first_pv[t] = false;
+            if (st == last[t]) ++n_o[t];
+          }
+          if (st + 1 < b) scores(t, st + 1, ks);
+          if (!ok) break;
+        }
+        if (!ok) break;
+        if (lane == 0) {
+          mma_commit(&kv_free[vs]);
+          if (st + 1 < b) mma_commit(&kv_free[ks]);
+        }
+        if (st + 1 < b) next();
+      }
+      // a tile whose rows need no step was loaded all the same: take its Q
+      for (int t = 0; t < 2 && ok; ++t)
+        if (q[t].n > 0 && first_qk[t]) {
+          ok = warp_wait(&q_full[t], n_q[t] & 1, P.err);
+          ++n_q[t];
+          if (lane == 0) mma_commit(&q_free[t]);
+        }
+      __syncwarp();
+    }
+    if (lane == 0) {  // every product and its arrivals are done before the CTA ends
+      mma_commit(drain);
+      mbar_wait_word(drain, 0, P.err);
+    }
+    __syncwarp();
+  } else {
+    // ---- softmax of query tile t: a thread per row ----
+    const int t = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t lane_base = (uint32_t)(warp & 3) << 21;  // 32 lanes per warp, lane in bits 16..
+    const uint32_t ts = tmem + lane_base + 128 * t, to = tmem + lane_base + 256 + 128 * t;
+    const int r_tok = row / P.group, r_head = row % P.group;
+    const int tt = P.tile_tokens / 2;
+    const float scale = P.scale_log2;
+    int n_s = 0, n_o = 0;
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      const int item = tc_nth(P, k);
+      if (item < 0) break;
+      const WinItem w = win_item(P, item);
+      const WinSeg& S = P.segs[w.seg];
+      int a, b;
+      tc_range(w, a, b);
+      const TcTile q = tc_tile(P, w, t);
+      const int pos = q.p0 + r_tok;
+      float m = -INFINITY, l = 0.0f;  // m: of the scaled scores (log2)
+      bool first = true;
+      for (int st = a; st < b; ++st) {
+        const TcStep c = tc_step(w, st);
+        if (!tc_need(P, q, c)) continue;
+        if (!warp_wait(&s_full[t], n_s & 1, P.err)) {
+          ok = false;
+          break;
+        }
+        ++n_s;
+        tc_fence_after();
+        uint32_t s[128];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, s + 32 * i);
+        tmem_wait_ld();
+        // columns that the row does not see (none in a tile in the middle)
+        const bool whole = c.t0 + kTcKeys <= c.end &&
+                           (c.sink || (c.t0 + kTcKeys - 1 <= q.p0 &&
+                                       (c.t0 > q.p1 - P.window || c.t0 + kTcKeys <= P.n_sink)));
+        if (!whole) {
+          const int hi = min(c.sink ? c.end - 1 : pos, c.end - 1) - c.t0;         // last column
+          const int lo = c.sink ? 0 : pos - P.window + 1 - c.t0;                   // first of the window
+          const int sk = c.sink ? 0 : P.n_sink - c.t0;                            // columns before it: first tokens
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int h = hi - 32 * i, g = lo - 32 * i, f = sk - 32 * i;
+            const uint32_t le = h < 0 ? 0u : h >= 31 ? ~0u : (2u << h) - 1u;
+            const uint32_t ge = g <= 0 ? ~0u : g >= 32 ? 0u : ~((1u << g) - 1u);
+            const uint32_t lt = f <= 0 ? 0u : f >= 32 ? ~0u : (1u << f) - 1u;
+            const uint32_t see = le & (ge | lt);
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (!((see >> j) & 1u)) s[32 * i + j] = 0xFF800000u;  // -inf
+          }
+        }
+        float mx[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(s[i]);
+#pragma unroll
+        for (int i = 4; i < 128; i += 4)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], __uint_as_float(s[i + j]));
+        const float mn = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+        if (first) {
+          m = mn;
+          first = false;
+        } else if (__any_sync(0xffffffffu, mn > m + kRescale)) {
+          const float m2 = fmaxf(m, mn);
+          const float f = m2 == -INFINITY ? 1.0f : ex2f(m - m2);
+          m = m2;
+          l *= f;
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            uint32_t o[32];
+            tmem_ld32(to + 32 * i, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+            tmem_st32(to + 32 * i, o);
+          }
+        }
+        const float base = m == -INFINITY ? 0.0f : m;
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float p0 = ex2f(fmaf(__uint_as_float(s[64 * i + 2 * j]), scale, -base));
+            const float p1 = ex2f(fmaf(__uint_as_float(s[64 * i + 2 * j + 1]), scale, -base));
+            sum[(2 * j) & 3] += p0;
+            sum[(2 * j + 1) & 3] += p1;
+            const __nv_bfloat162 x = __floats2bfloat162_rn(p0, p1);
+            pk[j] = *reinterpret_cast<const uint32_t*>(&x);
+          }
+          tmem_st32(ts + 32 * i, pk);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_ready[t]);
+      }
+      if (!ok) break;
+      // ---- outputs of the tile ----
+      const bool mine = r_tok < q.n && row < tt * P.group;
+      const int64_t tok = S.q_row0 + w.tok0 + t * tt + r_tok;
+      const int head = w.hk * P.group + r_head;
+      const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+      if (!first) {
+        if (!warp_wait(&o_full[t], n_o & 1, P.err)) break;
+        ++n_o;
+        tc_fence_after();
+      }
+      const int64_t pr = (int64_t)w.slot * P.tile_rows + t * tt * P.group + row;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        uint32_t o[32];
+        __syncwarp();
+        if (!first) {
+          tmem_ld32(to + 32 * i, o);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = 0u;
+        }
+        if (i == D / 32 - 1 && !first) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&o_free[t]);
+        }
+        if (mine && w.n_split > 1) {
+          float4* dst = reinterpret_cast<float4*>(P.part_o + pr * D + 32 * i);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            dst[j] = make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]), __uint_as_float(o[4 * j + 2]),
+                                 __uint_as_float(o[4 * j + 3]));
+        } else if (mine) {
+          uint4* dst = reinterpret_cast<uint4*>(P.out + 2 * (tok * P.o_tok + head * P.o_head + 32 * i));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const __nv_bfloat162 y = __floats2bfloat162_rn(__uint_as_float(o[8 * j + 2 * e]) * inv,
+                                                             __uint_as_float(o[8 * j + 2 * e + 1]) * inv);
+              x[e] = *reinterpret_cast<const uint32_t*>(&y);
+            }
+            dst[j] = make_uint4(x[0], x[1], x[2], x[3]);
+          }
+        }
+      }
+      if (mine) {
+        if (w.n_split > 1) P.part_ml[pr] = make_float2(l > 0.0f ? m : -INFINITY, l);
+        else if (P.lse) P.lse[tok * P.q_heads + head] = l > 0.0f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) tmem_free(tmem, 512);
+}
+
+// ---- host ---------------------------------------------------------------------
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+  static const EncodeFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeFn>(p);
+  }();
+  return fn;
+}
+
+bool encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+            const cuuint32_t* box) {
+  const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
+  return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, ones,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// a stride in bytes; an axis of length 1 takes any legal one
+cuuint64_t stride_bytes(int64_t values, int64_t extent) { return extent > 1 ? (cuuint64_t)values * 2 : 16; }
+
+template <int D>
+cudaError_t launch_tc(const WinParams& P, const TcMaps& M, int ctas, cudaStream_t s) {
+  auto* kern = window_tc_kernel<D>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TcShape<D>::kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(true, kern, dim3(ctas), dim3(kTcThreads), TcShape<D>::kSmem, s, P, M);
+}
+
+}  // namespace
+
+int launch_window_tc(const WinParams& P, int head_dim, int64_t q_rows, int64_t kv_rows, int n_sms, void* stream) {
+  if (!encode_fn()) return (int)cudaErrorNotSupported;
+  TcMaps M;
+  const cuuint64_t d = head_dim, g = P.group, hk = P.kv_heads;
+  const cuuint64_t qd[4] = {d, g, hk, (cuuint64_t)q_rows};
+  const cuuint64_t qs[3] = {stride_bytes(P.q_head, g), stride_bytes(P.q_head * P.group, hk), stride_bytes(P.q_tok, q_rows)};
+  const cuuint32_t qb[4] = {64, (cuuint32_t)g, 1, (cuuint32_t)(P.tile_tokens / 2)};
+  const cuuint64_t kd[3] = {d, hk, (cuuint64_t)kv_rows};
+  const cuuint64_t ks[2] = {stride_bytes(P.k_head, hk), stride_bytes(P.k_tok, kv_rows)};
+  const cuuint64_t vs[2] = {stride_bytes(P.v_head, hk), stride_bytes(P.v_tok, kv_rows)};
+  const cuuint32_t kb[3] = {64, 1, kTcKeys};
+  if (!encode(&M.q, P.q, 4, qd, qs, qb) || !encode(&M.k, P.k, 3, kd, ks, kb) || !encode(&M.v, P.v, 3, kd, vs, kb))
+    return (int)cudaErrorInvalidValue;
+  const int ctas = P.n_items < n_sms ? P.n_items : n_sms;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return (int)(head_dim == 128 ? launch_tc<128>(P, M, ctas, s) : launch_tc<64>(P, M, ctas, s));
+}
+
+}  // namespace kvp

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 from dataclasses import dataclass, field
 from typing import Optional, Sequence
 
@@ -34,7 +35,7 @@ EXPORTS = ["kvpool_required_bytes", "kvpool_create", "kvpool_destroy", "kvpool_a
            "kvpool_offload", "kvpool_fetch", "kvpool_block_location", "kvpool_epoch", "kvpool_block_activity",
            "kvpool_inactive_blocks", "kvpool_wait_selftest", "kvpool_topk_static_check", "kvpool_rope_table",
            "kvpool_qk_norm_rope", "kvpool_window_workspace", "kvpool_window_attend",
-           "kvpool_decode_attend_shared"]
+           "kvpool_decode_attend_shared", "kvpool_window_check"]
 
 
 class KvpoolError(RuntimeError):
@@ -72,17 +73,6 @@ class _LayerLayout(C.Structure):
                 ("hca_offset", C.c_int64), ("hca_block_bytes", C.c_int64), ("ring_offset", C.c_int64),
                 ("ring_request_bytes", C.c_int64), ("acc_offset", C.c_int64), ("acc_request_bytes", C.c_int64),
                 ("csa_host_offset", C.c_int64)]
-
-
-class _Heads(C.Structure):
-    _fields_ = [("data", C.c_void_p), ("token_stride", C.c_int64), ("head_stride", C.c_int64), ("heads", C.c_int32),
-                ("pad", C.c_int32)]
-
-
-class _WindowArgs(C.Structure):
-    _fields_ = [("dtype", C.c_int32), ("head_dim", C.c_int32), ("q", _Heads), ("k", _Heads), ("v", _Heads),
-                ("out", _Heads), ("q_rows", C.c_int64), ("kv_rows", C.c_int64), ("d_lse", C.c_void_p),
-                ("window", C.c_int32), ("n_sink", C.c_int32), ("scale", C.c_float), ("pad", C.c_int32)]
 
 
 _lib = None
@@ -134,12 +124,13 @@ def lib():
         L.kvpool_inactive_blocks.restype = i32
         L.kvpool_inactive_blocks.argtypes = [vp, C.c_uint32, vp, i32, vp]
         L.kvpool_wait_selftest.argtypes = [vp, vp]
-        hp = C.POINTER(_Heads)
         L.kvpool_rope_table.argtypes = [i32, vp, vp]
-        L.kvpool_qk_norm_rope.argtypes = [i32, i32, i64, hp, hp, hp, hp, vp, vp, C.c_float, i32, i32, vp, vp, vp]
+        cp = C.c_char_p  # a packed structure
+        L.kvpool_qk_norm_rope.argtypes = [i32, i32, i64, cp, cp, cp, cp, vp, vp, C.c_float, i32, i32, vp, vp, vp]
         L.kvpool_window_workspace.restype = i64
-        L.kvpool_window_workspace.argtypes = [C.POINTER(_WindowArgs), i32, vp, vp, vp]
-        L.kvpool_window_attend.argtypes = [C.POINTER(_WindowArgs), i32, vp, vp, vp, vp, i64, vp]
+        L.kvpool_window_workspace.argtypes = [cp, i32, vp, vp, vp]
+        L.kvpool_window_attend.argtypes = [cp, i32, vp, vp, vp, vp, i64, vp]
+        L.kvpool_window_check.argtypes = [vp, C.POINTER(C.c_uint32)]
         L.kvpool_last_error.restype = C.c_char_p
         L.kvpool_last_error.argtypes = [vp]
         _lib = L
@@ -250,44 +241,82 @@ def _i32(a) -> np.ndarray:
 
 def _dtype(t) -> int:
     import torch
-    if t.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError("tensors must be float32 or bfloat16")
-    return F32 if t.dtype == torch.float32 else BF16
+    if t.dtype is torch.bfloat16:
+        return BF16
+    if t.dtype is torch.float32:
+        return F32
+    raise ValueError("tensors must be float32 or bfloat16")
 
 
-def _heads(t, what: str, like=None) -> _Heads:
-    """A [tokens][heads][dim] CUDA tensor as the C ABI takes it."""
-    if t.dim() != 3 or not t.is_cuda or t.stride(2) != 1 and t.shape[2] > 1:
-        raise ValueError(f"{what} must be a [tokens][heads][dim] CUDA tensor with adjacent values")
-    if like is not None and (t.dtype != like.dtype or t.device != like.device or t.shape[2] != like.shape[2]):
+# kvpool_heads and kvpool_window_args of include/kvpool.h, packed in one go
+# (filling ctypes structures field by field takes longer than a small launch)
+_HEADS = struct.Struct("@Pqqii")
+_WINDOW_ARGS = struct.Struct("@ii" + 4 * "Pqqii" + "qqPiifi")
+
+
+def _rows(t, what: str, like=None, out: bool = False) -> tuple:
+    """The kvpool_heads fields of a [tokens][heads][dim] CUDA tensor."""
+    shape = t.shape
+    if len(shape) != 3 or not t.is_cuda:
+        raise ValueError(f"{what} must be a [tokens][heads][dim] CUDA tensor")
+    if like is not None and (t.dtype is not like.dtype or shape[2] != like.shape[2] or t.device != like.device):
         raise ValueError(f"{what} must have the type, device and head dim of the other tensors")
-    unit = 16 // t.element_size()
+    ts, hs, vs = t.stride()
     # the stride of an axis of length 1 is never used
-    ts, hs = (t.stride(i) if t.shape[i] > 1 else 0 for i in (0, 1))
-    if t.numel() and t.data_ptr() % 16 or ts % unit or hs % unit:
-        raise ValueError(f"{what}: data and strides must be whole multiples of 16 bytes")
-    return _Heads(t.data_ptr() if t.numel() else None, ts, hs, t.shape[1], 0)
-
-
-def _out_heads(t, what: str, like) -> _Heads:
-    """_heads of an output: no two of its values share a place."""
-    if any(t.shape[i] > 1 and t.stride(i) < t.shape[2] for i in (0, 1)):
+    ts, hs = ts if shape[0] > 1 else 0, hs if shape[1] > 1 else 0
+    ptr = t.data_ptr()
+    if (ptr | ts * t.element_size() | hs * t.element_size()) & 15 and t.numel() or vs != 1 and shape[2] > 1:
+        raise ValueError(f"{what}: a head's values must be adjacent, data and strides whole multiples of 16 bytes")
+    if out and (shape[0] > 1 and ts < shape[2] or shape[1] > 1 and hs < shape[2]):
         raise ValueError(f"{what}: two values share a place")
-    return _heads(t, what, like)
+    return ptr, ts, hs, shape[1], 0
 
 
-def _empty(shape, dtype, device, stream: int):
+class _on:
+    """The tensors' device as the current one, entered only where it is not."""
+
+    def __init__(self, index: int):
+        import torch
+        self.ctx = None if torch.cuda.current_device() == index else torch.cuda.device(index)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+
+    def __exit__(self, *e):
+        if self.ctx is not None:
+            self.ctx.__exit__(*e)
+
+
+def _stream_of(stream, index: int) -> int:
+    """The given stream, or the device's current one."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(index)
+    return _stream(stream)
+
+
+def _empty(shape, dtype, device, stream, raw: int):
     """torch.empty whose memory belongs to `stream`, the one that will use it."""
     import torch
-    if stream == torch.cuda.current_stream(device).cuda_stream:
+    if stream is None or raw == torch._C._cuda_getCurrentRawStream(device.index):
         return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
+    with torch.cuda.stream(torch.cuda.ExternalStream(raw, device=device)):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _need(t, what: str, dtype, shape, device):
-    if t.dtype != dtype or t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+
+
+def _i64(x) -> np.ndarray:
+    a = x if type(x) is np.ndarray else np.asarray(x)
+    if a.dtype != np.int64 or a.ndim != 1 or not a.flags.c_contiguous:
+        if a.ndim != 1 or a.size and (a.dtype.kind not in "iu" or a.dtype == np.uint64):
+            raise ValueError("lengths and starts must be one integer per segment")
+        a = np.ascontiguousarray(a, dtype=np.int64)
+    return a
 
 
 def rope_table(rot_dim: int, theta: float = 10000.0, inv_freq=None, device="cuda"):
@@ -316,41 +345,36 @@ def qk_norm_rope(q, k, positions, table, q_weight=None, k_weight=None, eps: floa
     kvpool_qk_norm_rope in include/kvpool.h."""
     import torch
     x = q if q is not None else k
-    if x is None:
-        raise ValueError("qk_norm_rope: neither q nor k")
-    if not x.is_cuda:
-        raise ValueError("qk_norm_rope: the tensors must be on a CUDA device")
-    T, D = x.shape[0], x.shape[-1]
-    with torch.cuda.device(x.device):
-        s = _stream(stream)
-    hs, outs = [], []
-    for t, o, what in ((q, out_q, "q"), (k, out_k, "k")):
-        if t is None:
-            hs += [None, None]
-            outs.append(None)
-            continue
-        a = _heads(t, what, x)
-        if t.shape[0] != T:
-            raise ValueError("qk_norm_rope: q and k must have the same tokens")
-        if o is None:
-            o = _empty(t.shape, t.dtype, t.device, s)
-        elif o.shape != t.shape:
-            raise ValueError(f"qk_norm_rope: out_{what} must have the shape of {what}")
-        hs += [a, _out_heads(o, "out_" + what, x)]
-        outs.append(o)
-    rot = 0
-    if table is not None:
-        rot = 2 * table.numel()
-        _need(table, "table", torch.int64, (rot // 2,), x.device)
-        _need(positions, "positions", torch.int64, (T,), x.device)
-    for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _need(w, what, torch.float32, (D,), x.device)
-    ref = [C.byref(h) if h is not None else None for h in hs]
-    with torch.cuda.device(x.device):
-        rc = lib().kvpool_qk_norm_rope(_dtype(x), D, T, ref[0], ref[2], ref[1], ref[3], _ptr(q_weight), _ptr(k_weight),
-                                       eps, rot, int(bool(interleaved)), _ptr(table) if rot else None,
-                                       _ptr(positions) if rot else None, s)
+    if x is None or not x.is_cuda:
+        raise ValueError("qk_norm_rope: q or k must be a CUDA tensor")
+    dev, kind = x.device, _dtype(x)
+    with _on(dev.index):
+        raw = _stream_of(stream, dev.index)
+        heads, outs = [None] * 4, [None, None]
+        for i, (t, o) in enumerate(((q, out_q), (k, out_k))):
+            if t is None:
+                continue
+            heads[i] = _HEADS.pack(*_rows(t, "qk"[i], x))
+            if t.shape[0] != x.shape[0]:
+                raise ValueError("qk_norm_rope: q and k must have the same tokens")
+            if o is None:
+                o = _empty(t.shape, t.dtype, dev, stream, raw)
+            elif o.shape != t.shape:
+                raise ValueError(f"qk_norm_rope: out_{'qk'[i]} must have the shape of {'qk'[i]}")
+            heads[2 + i] = _HEADS.pack(*_rows(o, "out_" + "qk"[i], x, True))
+            outs[i] = o
+        T, _, D = x.shape
+        rot = 0
+        if table is not None:
+            rot = 2 * table.numel()
+            _need(table, "table", torch.int64, (rot // 2,), dev)
+            _need(positions, "positions", torch.int64, (T,), dev)
+        for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+            if w is not None:
+                _need(w, what, torch.float32, (D,), dev)
+        rc = lib().kvpool_qk_norm_rope(kind, D, T, *heads, _ptr(q_weight), _ptr(k_weight), eps, rot,
+                                       1 if interleaved else 0, _ptr(table) if rot else None,
+                                       _ptr(positions) if rot else None, raw)
     if rc != OK:
         raise KvpoolError(rc, "qk_norm_rope refused its arguments" if rc == ERR_INVALID_ARG else "qk_norm_rope: CUDA error")
     return outs[0], outs[1]
@@ -366,21 +390,25 @@ def window_attend(q, k, v, q_len, k_start, k_len, window: int, n_sink: int = 0, 
     kvpool_window_attend in include/kvpool.h."""
     import torch
     if not q.is_cuda:
-        raise ValueError("window_attend: the tensors must be on a CUDA device")
-    with torch.cuda.device(q.device):
-        s = _stream(stream)
+        raise ValueError("window_attend: the tensors must be CUDA tensors")
+    dev = q.device
+    with _on(dev.index):
+        raw = _stream_of(stream, dev.index)
         if out is None:
-            out = _empty(q.shape, q.dtype, q.device, s)
-        a, ql, ks, kl = _window_args(q, k, v, q_len, k_start, k_len, window, n_sink, scale, out, lse)
-        call = (C.byref(a), ql.size, ql.ctypes.data, ks.ctypes.data, kl.ctypes.data)
-        rc = int(lib().kvpool_window_workspace(*call))
+            out = _empty(q.shape, q.dtype, dev, stream, raw)
+        call, keep = _window_call(q, k, v, q_len, k_start, k_len, window, n_sink, scale, out, lse)
+        L = lib()
+        rc = L.kvpool_window_workspace(*call)
         if rc >= 0:
-            if workspace is None and rc > 0:
-                workspace = _empty((rc,), torch.uint8, q.device, s)
-            if workspace is not None and (workspace.device != q.device or not workspace.is_contiguous()):
-                raise ValueError("window_attend: workspace must be a contiguous tensor on the queries' device")
-            nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-            rc = lib().kvpool_window_attend(*call, _ptr(workspace), nbytes, s)
+            nbytes = 0
+            if workspace is not None:
+                if workspace.device != dev or not workspace.is_contiguous():
+                    raise ValueError("window_attend: workspace must be a contiguous tensor on the queries' device")
+                nbytes = workspace.numel() * workspace.element_size()
+            elif rc > 0:
+                nbytes = rc
+                workspace = _empty((rc,), torch.uint8, dev, stream, raw)
+            rc = L.kvpool_window_attend(*call, workspace.data_ptr() if nbytes else None, nbytes, raw)
     if rc != OK:
         raise KvpoolError(rc, "window_attend refused its arguments" if rc == ERR_INVALID_ARG else "window_attend: CUDA error")
     return out
@@ -388,40 +416,40 @@ def window_attend(q, k, v, q_len, k_start, k_len, window: int, n_sink: int = 0, 
 
 def window_workspace(q, k, v, q_len, k_start, k_len, window: int, n_sink: int = 0) -> int:
     """Workspace bytes of window_attend with these arguments."""
-    import torch
-    a, ql, ks, kl = _window_args(q, k, v, q_len, k_start, k_len, window, n_sink, None, q, None)
-    with torch.cuda.device(q.device):
-        rc = int(lib().kvpool_window_workspace(C.byref(a), ql.size, ql.ctypes.data, ks.ctypes.data, kl.ctypes.data))
+    with _on(q.device.index):
+        call, keep = _window_call(q, k, v, q_len, k_start, k_len, window, n_sink, None, q, None)
+        rc = int(lib().kvpool_window_workspace(*call))
     if rc < 0:
         raise KvpoolError(rc, "window_workspace refused its arguments")
     return rc
 
 
-def _window_args(q, k, v, q_len, k_start, k_len, window, n_sink, scale, out, lse):
-    import torch
-    qh, kh, vh = _heads(q, "q"), _heads(k, "k", q), _heads(v, "v", q)
-    if k.shape != v.shape:
-        raise ValueError("window_attend: k and v must have the same shape")
-    if out.shape != q.shape:
-        raise ValueError("window_attend: out must have the shape of q")
-    oh = _out_heads(out, "out", q)
+def window_check(stream=None) -> tuple:
+    """(return code, device error flags) of the window_attend calls on the
+    current device since the last check; synchronizes the stream."""
+    w = C.c_uint32(0)
+    rc = lib().kvpool_window_check(_stream(stream), C.byref(w))
+    return int(rc), int(w.value)
+
+
+def _window_call(q, k, v, q_len, k_start, k_len, window, n_sink, scale, out, lse):
+    """(args, n, lengths) as kvpool_window_attend takes them, and what must outlive the call."""
+    if k.shape != v.shape or out.shape != q.shape:
+        raise ValueError("window_attend: k and v, and q and out, must have the same shape")
     if lse is not None:
+        import torch
         _need(lse, "lse", torch.float32, q.shape[:2], q.device)
-    ql, ks, kl = (_ints(x, t) for x, t in ((q_len, np.int32), (k_start, np.int64), (k_len, np.int32)))
-    if not ql.shape == ks.shape == kl.shape or ql.ndim != 1:
+    ql, ks, kl = _i64(q_len), _i64(k_start), _i64(k_len)
+    if not ql.size == ks.size == kl.size:
         raise ValueError("window_attend: q_len, k_start and k_len must have one value per segment")
-    a = _WindowArgs(_dtype(q), q.shape[2], qh, kh, vh, oh, q.shape[0], k.shape[0], _ptr(lse), window, n_sink,
-                    1.0 / float(np.sqrt(q.shape[2])) if scale is None else scale, 0)
-    return a, ql, ks, kl
-
-
-def _ints(x, dtype) -> np.ndarray:
-    a = np.asarray(x)
-    if a.size and a.dtype.kind not in "iu":
-        raise ValueError("lengths and starts must be integers")
-    if a.size and (a.min() < np.iinfo(dtype).min or a.max() > np.iinfo(dtype).max):
-        raise ValueError("a length or start is out of range")
-    return np.ascontiguousarray(a, dtype=dtype)
+    rows, _, D = q.shape
+    try:
+        a = _WINDOW_ARGS.pack(_dtype(q), D, *_rows(q, "q"), *_rows(k, "k", q), *_rows(v, "v", q),
+                              *_rows(out, "out", q, out is not q), rows, k.shape[0], 0 if lse is None else lse.data_ptr(), window,
+                              n_sink, D ** -0.5 if scale is None else scale, 0)
+    except (struct.error, OverflowError) as e:
+        raise ValueError(f"window_attend: {e}") from None
+    return (a, ql.size, ql.ctypes.data, ks.ctypes.data, kl.ctypes.data), (ql, ks, kl)
 
 
 class Pool:

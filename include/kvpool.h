@@ -448,10 +448,17 @@ typedef struct kvpool_window_args {
 
 /* Workspace bytes of that call on the current device (a negative error code
  * if its arguments are refused). */
-int64_t kvpool_window_workspace(const kvpool_window_args* args, int32_t n, const int32_t* h_q_len,
-                                const int64_t* h_k_start, const int32_t* h_k_len);
-int kvpool_window_attend(const kvpool_window_args* args, int32_t n, const int32_t* h_q_len, const int64_t* h_k_start,
-                         const int32_t* h_k_len, void* d_workspace, int64_t workspace_bytes, void* stream);
+int64_t kvpool_window_workspace(const kvpool_window_args* args, int32_t n, const int64_t* h_q_len,
+                                const int64_t* h_k_start, const int64_t* h_k_len);
+int kvpool_window_attend(const kvpool_window_args* args, int32_t n, const int64_t* h_q_len, const int64_t* h_k_start,
+                         const int64_t* h_k_len, void* d_workspace, int64_t workspace_bytes, void* stream);
+
+/* Device-side error flags of the kvpool_window_attend calls on the current
+ * device since the last check (the kvpool_check_device bits: 1 = a wait passed
+ * its limit; that call's output is not valid).  Synchronizes `stream`, copies
+ * the word to *h_flags (may be NULL) and clears it.  Returns OK when it is
+ * zero, DEVICE_CHECK when a flag is set, CUDA on a CUDA error. */
+int kvpool_window_check(void* stream, uint32_t* h_flags);
 
 /* ---- host-side queries (no device access) ---- */
 typedef struct kvpool_info {

@@ -1,6 +1,4 @@
 """Refusals and host parts of the entry points without a pool (no GPU)."""
-import ctypes as C
-
 import numpy as np
 import pytest
 
@@ -10,7 +8,7 @@ P16 = 1 << 20  # a plausible, aligned address that nothing reads
 
 
 def heads(n=4, d=64, data=P16, ts=None, hs=None):
-    return K._Heads(data, n * d if ts is None else ts, d if hs is None else hs, n, 0)
+    return (data or 0, n * d if ts is None else ts, d if hs is None else hs, n, 0)
 
 
 def table(rot, f):
@@ -52,8 +50,8 @@ def test_rope_table_refuses_frequencies(bad):
 def rope(dtype=K.BF16, d=64, T=2, q=None, k=None, qo=None, ko=None, eps=1e-6, rot=64, inter=0, tab=P16, pos=P16):
     q, k = q or heads(), k or heads()
     qo, ko = qo or q, ko or k
-    r = C.byref
-    return K.lib().kvpool_qk_norm_rope(dtype, d, T, r(q), r(k), r(qo), r(ko), None, None, eps, rot, inter, tab, pos, None)
+    q, k, qo, ko = (K._HEADS.pack(*x) for x in (q, k, qo, ko))
+    return K.lib().kvpool_qk_norm_rope(dtype, d, T, q, k, qo, ko, None, None, eps, rot, inter, tab, pos, None)
 
 
 @pytest.mark.parametrize("bad", [
@@ -72,11 +70,11 @@ def test_rope_without_work():
 
 
 def window(q_len, k_start, k_len, n=None, ws=None, ws_bytes=0, **kw):
-    a = K._WindowArgs(kw.get("dtype", K.BF16), kw.get("d", 64), kw.get("q", heads(8)), kw.get("k", heads(4)),
-                      kw.get("v", heads(4)), kw.get("out", heads(8)), kw.get("q_rows", 100), kw.get("kv_rows", 1000), None,
-                      kw.get("window", 16), kw.get("sink", 0), kw.get("scale", 0.125), 0)
-    ql, ks, kl = (np.array(x, t) for x, t in ((q_len, np.int32), (k_start, np.int64), (k_len, np.int32)))
-    call = (C.byref(a), ql.size if n is None else n, ql.ctypes.data, ks.ctypes.data, kl.ctypes.data)
+    a = K._WINDOW_ARGS.pack(kw.get("dtype", K.BF16), kw.get("d", 64), *kw.get("q", heads(8)), *kw.get("k", heads(4)),
+                            *kw.get("v", heads(4)), *kw.get("out", heads(8)), kw.get("q_rows", 100), kw.get("kv_rows", 1000), 0,
+                            kw.get("window", 16), kw.get("sink", 0), kw.get("scale", 0.125), 0)
+    ql, ks, kl = (np.array(x, np.int64) for x in (q_len, k_start, k_len))
+    call = (a, ql.size if n is None else n, ql.ctypes.data, ks.ctypes.data, kl.ctypes.data)
     got = K.lib().kvpool_window_attend(*call, ws, ws_bytes, None)
     assert K.lib().kvpool_window_workspace(*call) == (got if got else 0)
     return got
