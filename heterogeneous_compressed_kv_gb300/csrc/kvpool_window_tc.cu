@@ -3,9 +3,10 @@
 //
 // A work item is 256 query rows (token, query head of the group) of one key
 // head: two tiles of 128 rows that share every K and V tile of 128 keys.
-// Persistent CTAs, one per SM, of ten warps: one issues the tensor copies
-// (Q tiles, and a ring of K and V tiles), one the matrix products, and a group
-// of four per query tile does its softmax, a thread per row.  Scores S = Q K^T
+// Persistent CTAs, one per SM, of eleven warps: one issues the tensor copies
+// (Q tiles, and a ring of K and V tiles), one the matrix products, one zeroes V
+// rows that nobody sees, and a group of four per query tile does its softmax, a
+// thread per row.  Scores S = Q K^T
 // go to tensor memory; the softmax reads a row, keeps the running maximum and
 // sum in fp32, and writes the weights back as bf16 over the scores; O += P V
 // accumulates in tensor memory.  While one tile's rows go through the softmax
@@ -31,7 +32,7 @@ namespace kvp {
 namespace {
 
 constexpr int kTcKeys = 128;
-constexpr int kTcThreads = 320;
+constexpr int kTcThreads = 352;
 constexpr float kRescale = 8.0f;  // log2 growth of the maximum that rescales O
 
 template <int D>
@@ -39,7 +40,7 @@ struct TcShape {
   static constexpr int kTileBytes = 128 * D * 2;  // a Q, K or V tile: D / 64 runs of 128 rows x 128 bytes
   static constexpr int kStages = D == 128 ? 5 : 8;
   static constexpr int kBarOff = (2 + kStages) * kTileBytes;
-  static constexpr int kSmem = kBarOff + 256 + 1024;  // + slack to align the tiles to 1,024 bytes
+  static constexpr int kSmem = kBarOff + 512 + 1024;  // + slack to align the tiles to 1,024 bytes
 };
 
 struct TcMaps {
@@ -77,10 +78,25 @@ __device__ __forceinline__ TcTile tc_tile(const WinParams& P, const WinItem& w, 
   q.p1 = q.p0 + q.n - 1;
   return q;
 }
-// does some row of the tile see some key of the step?
-__device__ __forceinline__ bool tc_need(const WinParams& P, const TcTile& q, const TcStep& s) {
-  if (q.n <= 0) return false;
-  return s.sink || (s.t0 <= q.p1 && (s.t0 + kTcKeys - 1 > q.p0 - P.window || s.t0 < P.n_sink));
+// The steps of [a, b) that some row of a query tile needs: those before `sink`
+// (first tokens) and those in [lo, hi).
+struct TcNeed {
+  int sink, lo, hi;
+  __device__ __forceinline__ bool operator()(int st) const { return st < sink || (st >= lo && st < hi); }
+  __device__ __forceinline__ int last(int a) const { return hi > lo ? hi - 1 : sink > a ? sink - 1 : -1; }
+};
+__device__ __forceinline__ TcNeed tc_need(const WinParams& P, const WinItem& w, const TcTile& q, int a, int b) {
+  TcNeed n{a, a, a};
+  if (q.n <= 0) return n;
+  const int st_s = (w.n_s + kTcKeys - 1) / kTcKeys;
+  // window steps: step st holds tokens w.lo + (st - st_s) * 128 ..
+  const int first = max(0, q.p0 - P.window + 1 - w.lo) / kTcKeys;  // of the first token in the window
+  const int past = q.p1 < w.lo ? 0 : (q.p1 - w.lo) / kTcKeys + 1;
+  const int sinks = P.n_sink > w.lo ? (P.n_sink - w.lo + kTcKeys - 1) / kTcKeys : 0;  // first tokens behind w.lo
+  n.sink = min(b, max(a, st_s + min(sinks, past)));
+  n.lo = max(n.sink, st_s + first);
+  n.hi = max(n.lo, min(b, st_s + past));
+  return n;
 }
 
 // k-th item of a CTA: back and forth over the CTAs, the last (longest) tiles first
@@ -102,7 +118,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
   uint8_t* ring = smem + 2 * Sh::kTileBytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Sh::kBarOff);
   uint64_t *kv_full = bars, *kv_free = kv_full + NS, *q_full = kv_free + NS, *q_free = q_full + 2, *s_full = q_free + 2,
-           *p_ready = s_full + 2, *o_full = p_ready + 2, *o_free = o_full + 2, *drain = o_free + 2;
+           *p_ready = s_full + 2, *o_full = p_ready + 2, *o_free = o_full + 2, *v_ask = o_free + 2, *v_ok = v_ask + 1, *drain = v_ok + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -118,6 +134,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
       mbar_init(&o_full[t], 1);
       mbar_init(&o_free[t], 4);
     }
+    mbar_init(v_ask, 1);
+    mbar_init(v_ok, 1);
     mbar_init(drain, 1);
     mbar_fence_init();
   }
@@ -128,182 +146,199 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
   const uint32_t tmem = *tmem_slot;  // columns: S0, S1 (128 each), O0, O1 (128 each)
 
   if (warp == 8) {
-    // ---- tensor copies ----
-    int stage = 0, n_q[2] = {0, 0};
-    uint32_t round = 0;  // of the ring
-    int issued = 0;
-    bool ok = true;
-    auto load = [&](const CUtensorMap* map, int hk, int row) {
-      if (round > 0) ok = ok && warp_wait(&kv_free[stage], (round - 1) & 1, P.err);
-      if (!ok) return;
-      if (lane == 0) {
+    // ---- tensor copies (one thread) ----
+    if (elect_one()) {
+      int stage = 0, n_q[2] = {0, 0}, issued = 0;
+      uint32_t round = 0;  // of the ring
+      bool ok = true;
+      auto load = [&](const CUtensorMap* map, int hk, int row) {
+        if (round > 0 && !mbar_wait_word(&kv_free[stage], (round - 1) & 1, P.err)) ok = false;
+        if (!ok) return;
         mbar_arrive_expect_tx(&kv_full[stage], Sh::kTileBytes);
 #pragma unroll
         for (int c = 0; c < D / 64; ++c)
           tma_load_3d(ring + stage * Sh::kTileBytes + c * 16384, map, 64 * c, hk, row, &kv_full[stage]);
-      }
-      __syncwarp();
-      ++issued;
-      if (++stage == NS) {
-        stage = 0;
-        ++round;
-      }
-    };
-    for (int k = 0; ok; ++k) {
-      const int item = tc_nth(P, k);
-      if (item < 0) break;
-      const WinItem w = win_item(P, item);
-      const WinSeg& S = P.segs[w.seg];
-      int a, b;
-      tc_range(w, a, b);
-      if (a >= b) continue;
-      const int tt = P.tile_tokens / 2;
-      for (int t = 0; t < 2; ++t) {
-        if (w.n_tok <= t * tt) break;
-        if (n_q[t] > 0) ok = ok && warp_wait(&q_free[t], (n_q[t] - 1) & 1, P.err);
-        if (!ok) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&q_full[t], tt * P.group * D * 2);
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c)
-            tma_load_4d(q_tile + t * Sh::kTileBytes + c * 16384, &M.q, 64 * c, 0, w.hk, (int)S.q_row0 + w.tok0 + t * tt,
-                        &q_full[t]);
+        ++issued;
+        if (++stage == NS) {
+          stage = 0;
+          ++round;
         }
-        __syncwarp();
-        ++n_q[t];
-        if (t == 0 && ok) load(&M.k, w.hk, (int)S.k_start + tc_step(w, a).t0);  // the first K between the Q tiles
-      }
-      for (int st = a; st < b && ok; ++st) {
-        const int row = (int)S.k_start + tc_step(w, st).t0;
-        if (st > a) load(&M.k, w.hk, row);
-        if (ok) load(&M.v, w.hk, row);
-      }
-    }
-    // the CTA does not end while copies land in its shared memory
-    for (int i = issued > NS ? issued - NS : 0; i < issued; ++i) warp_wait(&kv_full[i % NS], (i / NS) & 1, P.err);
-    for (int t = 0; t < 2; ++t)
-      if (n_q[t] > 0) warp_wait(&q_full[t], (n_q[t] - 1) & 1, P.err);
-  } else if (warp == 9) {
-    // ---- matrix products (lane 0 issues) ----
-    constexpr uint32_t kIdQK = bf16_idesc(128, kTcKeys, false), kIdPV = bf16_idesc(128, D, true);
-    const uint32_t q_addr = smem_addr(q_tile), ring_addr = smem_addr(ring);
-    int stage = 0;
-    uint32_t round = 0;
-    int n_q[2] = {0, 0}, n_p[2] = {0, 0}, n_o[2] = {0, 0};
-    bool ok = true;
-    auto next = [&]() {
-      if (++stage == NS) {
-        stage = 0;
-        ++round;
-      }
-    };
-    auto qk = [&](int t, int s) {
-      if (lane == 0) {
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-          const uint32_t off = (c / 4) * 16384 + (c % 4) * 32;
-          mma_ss(tmem + 128 * t, smem_desc(q_addr + t * Sh::kTileBytes + off, 16),
-                 smem_desc(ring_addr + s * Sh::kTileBytes + off, 16), kIdQK, c > 0);
-        }
-        mma_commit(&s_full[t]);
-      }
-    };
-    for (int k = 0; ok; ++k) {
-      const int item = tc_nth(P, k);
-      if (item < 0) break;
-      const WinItem w = win_item(P, item);
-      int a, b;
-      tc_range(w, a, b);
-      if (a >= b) continue;
-      const TcTile q[2] = {tc_tile(P, w, 0), tc_tile(P, w, 1)};
-      int last[2] = {-1, -1};  // the last step that the tile needs
-      for (int t = 0; t < 2; ++t)
-        for (int st = b - 1; st >= a && last[t] < 0; --st)
-          if (tc_need(P, q[t], tc_step(w, st))) last[t] = st;
-      bool first_qk[2] = {true, true}, first_pv[2] = {true, true};
-      // scores of step st against the K tile in ring stage s
-      auto scores = [&](int t, int st, int s) {
-        if (!tc_need(P, q[t], tc_step(w, st))) return;
-        if (first_qk[t]) {
-          ok = ok && warp_wait(&q_full[t], n_q[t] & 1, P.err);
-          if (!ok) return;
-          tc_fence_after();
-          ++n_q[t];
-          first_qk[t] = false;
-        }
-        qk(t, s);
-        if (lane == 0 && st == last[t]) mma_commit(&q_free[t]);
       };
-      ok = ok && warp_wait(&kv_full[stage], round & 1, P.err);
-      if (!ok) break;
-      tc_fence_after();
-      for (int t = 0; t < 2 && ok; ++t) scores(t, a, stage);
-      if (!ok) break;
-      if (lane == 0) mma_commit(&kv_free[stage]);
-      next();
-      for (int st = a; st < b && ok; ++st) {
-        const TcStep cur = tc_step(w, st);
-        const int vs = stage;
-        ok = warp_wait(&kv_full[vs], round & 1, P.err);
-        if (!ok) break;
-        tc_fence_after();
-        next();
-        if (cur.t0 + kTcKeys > cur.end) {  // rows that nobody sees: zeros
-          const int r0 = cur.end - cur.t0;
-          for (int c = 0; c < D / 64; ++c) {
-            uint4* base = reinterpret_cast<uint4*>(ring + vs * Sh::kTileBytes + c * 16384);
-            for (int i = r0 * 8 + lane; i < 128 * 8; i += 32) base[i] = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+      for (int k = 0; ok; ++k) {
+        const int item = tc_nth(P, k);
+        if (item < 0) break;
+        const WinItem w = win_item(P, item);
+        const WinSeg& S = P.segs[w.seg];
+        int a, b;
+        tc_range(w, a, b);
+        if (a >= b) continue;
+        const int tt = P.tile_tokens / 2;
+#pragma unroll 1
+        for (int st = a; st < b && ok; ++st) {
+          // the first K tile goes out between the Q tiles
+#pragma unroll 1
+          for (int t = 0; st == a && t < 2 && ok; ++t) {
+            if (w.n_tok > t * tt) {
+              if (n_q[t] > 0 && !mbar_wait_word(&q_free[t], (n_q[t] - 1) & 1, P.err)) ok = false;
+              if (!ok) break;
+              mbar_arrive_expect_tx(&q_full[t], tt * P.group * D * 2);
+#pragma unroll
+              for (int c = 0; c < D / 64; ++c)
+                tma_load_4d(q_tile + t * Sh::kTileBytes + c * 16384, &M.q, 64 * c, 0, w.hk,
+                            (int)S.q_row0 + w.tok0 + t * tt, &q_full[t]);
+              ++n_q[t];
+            }
+            if (t == 0) load(&M.k, w.hk, (int)S.k_start + tc_step(w, a).t0);
           }
-          fence_proxy_async();
-          __syncwarp();
+          const int row = (int)S.k_start + tc_step(w, st).t0;
+          if (st > a && ok) load(&M.k, w.hk, row);
+          if (ok) load(&M.v, w.hk, row);
         }
-        const int ks = stage;
-        if (st + 1 < b) {
-          ok = warp_wait(&kv_full[ks], round & 1, P.err);
+      }
+      // the CTA does not end while copies land in its shared memory
+      for (int i = issued > NS ? issued - NS : 0; i < issued; ++i)
+        mbar_wait_word(&kv_full[i % NS], (i / NS) & 1, P.err);
+      for (int t = 0; t < 2; ++t)
+        if (n_q[t] > 0) mbar_wait_word(&q_full[t], (n_q[t] - 1) & 1, P.err);
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // ---- matrix products (one thread) ----
+    if (elect_one()) {
+      constexpr uint32_t kIdQK = bf16_idesc(128, kTcKeys, false), kIdPV = bf16_idesc(128, D, true);
+      const uint64_t q_desc = smem_desc(smem_addr(q_tile), 16), k_desc = smem_desc(smem_addr(ring), 16),
+                     v_desc = smem_desc(smem_addr(ring), 16384);
+      int stage = 0;
+      uint32_t round = 0;
+      int n_q[2] = {0, 0}, n_p[2] = {0, 0}, n_o[2] = {0, 0};
+      int n_v = 0;
+      bool ok = true;
+#pragma unroll 1
+      for (int k = 0; ok; ++k) {
+        const int item = tc_nth(P, k);
+        if (item < 0) break;
+        const WinItem w = win_item(P, item);
+        int a, b;
+        tc_range(w, a, b);
+        if (a >= b) continue;
+        const TcTile q[2] = {tc_tile(P, w, 0), tc_tile(P, w, 1)};
+        const TcNeed need[2] = {tc_need(P, w, q[0], a, b), tc_need(P, w, q[1], a, b)};
+        const int last[2] = {need[0].last(a), need[1].last(a)};
+        uint32_t seen_q = 0, seen_pv = 0;  // tiles whose Q has been waited for, whose outputs have begun
+        int vs = 0;
+        bool zeroing = false;  // the V tile in stage vs is with the zeroing warp
+        // round st: outputs of step st - 1, then scores of step st
+#pragma unroll 1
+        for (int st = a; st <= b && ok; ++st) {
+          const int ks = stage;
+          if (st < b) {
+            if (!mbar_wait_word(&kv_full[ks], round & 1, P.err)) ok = false;
+            if (++stage == NS) {
+              stage = 0;
+              ++round;
+            }
+          }
+          if (ok && zeroing) {
+            ok = mbar_wait_word(v_ok, n_v++ & 1, P.err);
+            zeroing = false;
+          }
           if (!ok) break;
-          tc_fence_after();
-        }
-        for (int t = 0; t < 2; ++t) {
-          if (tc_need(P, q[t], cur)) {
-            ok = ok && warp_wait(&p_ready[t], n_p[t] & 1, P.err);
-            ++n_p[t];
-            if (ok && first_pv[t] && n_o[t] > 0) ok = warp_wait(&o_free[t], (n_o[t] - 1) & 1, P.err);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
             if (!ok) break;
-            tc_fence_after();
-            if (lane == 0) {
+            if (st > a && need[t](st - 1)) {
+              ok = mbar_wait_word(&p_ready[t], n_p[t] & 1, P.err);
+              ++n_p[t];
+              const bool begun = (seen_pv >> t) & 1;
+              if (ok && !begun && n_o[t] > 0) ok = mbar_wait_word(&o_free[t], (n_o[t] - 1) & 1, P.err);
+              if (!ok) break;
+              tc_fence_after();
+              const uint64_t vd = v_desc + vs * (Sh::kTileBytes >> 4);
 #pragma unroll
               for (int c = 0; c < kTcKeys / 16; ++c)
-                mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * c,
-                       smem_desc(ring_addr + vs * Sh::kTileBytes + c * 2048, 16384), kIdPV, !first_pv[t] || c > 0);
-              if (st == last[t]) mma_commit(&o_full[t]);
+                mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * c, vd + c * (2048 >> 4), kIdPV, begun || c > 0);
+              seen_pv |= 1u << t;
+              if (st - 1 == last[t]) {
+                mma_commit(&o_full[t]);
+                ++n_o[t];
+              }
             }
-            first_pv[t] = false;
-            if (st == last[t]) ++n_o[t];
+            if (st < b && need[t](st)) {
+              if (!((seen_q >> t) & 1)) {
+                ok = mbar_wait_word(&q_full[t], n_q[t] & 1, P.err);
+                if (!ok) break;
+                ++n_q[t];
+                seen_q |= 1u << t;
+              }
+              tc_fence_after();
+              const uint64_t qd = q_desc + t * (Sh::kTileBytes >> 4), kd = k_desc + ks * (Sh::kTileBytes >> 4);
+#pragma unroll
+              for (int c = 0; c < D / 16; ++c) {
+                const uint32_t off = ((c / 4) * 16384 + (c % 4) * 32) >> 4;
+                mma_ss(tmem + 128 * t, qd + off, kd + off, kIdQK, c > 0);
+              }
+              mma_commit(&s_full[t]);
+              if (st == last[t]) mma_commit(&q_free[t]);
+            }
           }
-          if (st + 1 < b) scores(t, st + 1, ks);
           if (!ok) break;
+          if (st > a) mma_commit(&kv_free[vs]);
+          if (st == b) break;
+          mma_commit(&kv_free[ks]);
+          // V of this step
+          vs = stage;
+          ok = mbar_wait_word(&kv_full[vs], round & 1, P.err);
+          const TcStep cur = tc_step(w, st);
+          zeroing = ok && cur.t0 + kTcKeys > cur.end;
+          if (zeroing) mbar_arrive(v_ask);  // while the step's scores go through the softmax
+          if (++stage == NS) {
+            stage = 0;
+            ++round;
+          }
         }
-        if (!ok) break;
-        if (lane == 0) {
-          mma_commit(&kv_free[vs]);
-          if (st + 1 < b) mma_commit(&kv_free[ks]);
-        }
-        if (st + 1 < b) next();
+        // a tile whose rows need no step was loaded all the same: take its Q
+        for (int t = 0; t < 2 && ok; ++t)
+          if (q[t].n > 0 && !((seen_q >> t) & 1)) {
+            ok = mbar_wait_word(&q_full[t], n_q[t] & 1, P.err);
+            ++n_q[t];
+            mma_commit(&q_free[t]);
+          }
       }
-      // a tile whose rows need no step was loaded all the same: take its Q
-      for (int t = 0; t < 2 && ok; ++t)
-        if (q[t].n > 0 && first_qk[t]) {
-          ok = warp_wait(&q_full[t], n_q[t] & 1, P.err);
-          ++n_q[t];
-          if (lane == 0) mma_commit(&q_free[t]);
-        }
-      __syncwarp();
-    }
-    if (lane == 0) {  // every product and its arrivals are done before the CTA ends
+      // every product and its arrivals are done before the CTA ends
       mma_commit(drain);
       mbar_wait_word(drain, 0, P.err);
     }
     __syncwarp();
+  } else if (warp == 10) {
+    // ---- V rows that nobody sees: zeros, when the products' thread asks ----
+    int seq = 0, n_v = 0;  // ring tiles before this item
+    bool ok = true;
+#pragma unroll 1
+    for (int k = 0; ok; ++k) {
+      const int item = tc_nth(P, k);
+      if (item < 0) break;
+      const WinItem w = win_item(P, item);
+      int a, b;
+      tc_range(w, a, b);
+      if (a >= b) continue;
+#pragma unroll 1
+      for (int st = a; st < b && ok; ++st) {
+        const TcStep c = tc_step(w, st);
+        if (c.t0 + kTcKeys <= c.end) continue;
+        ok = warp_wait(v_ask, n_v++ & 1, P.err);
+        if (!ok) break;
+        uint8_t* tile = ring + (seq + 2 * (st - a) + 1) % NS * Sh::kTileBytes;
+        for (int h = 0; h < D / 64; ++h) {
+          uint4* base = reinterpret_cast<uint4*>(tile + h * 16384);
+          for (int j = (c.end - c.t0) * 8 + lane; j < 128 * 8; j += 32) base[j] = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(v_ok);
+      }
+      seq += 2 * (b - a);
+    }
   } else {
     // ---- softmax of query tile t: a thread per row ----
     const int t = warp >> 2, row = (warp & 3) * 32 + lane;
@@ -314,6 +349,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
     const float scale = P.scale_log2;
     int n_s = 0, n_o = 0;
     bool ok = true;
+#pragma unroll 1
     for (int k = 0; ok; ++k) {
       const int item = tc_nth(P, k);
       if (item < 0) break;
@@ -322,49 +358,63 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
       int a, b;
       tc_range(w, a, b);
       const TcTile q = tc_tile(P, w, t);
+      const TcNeed need = tc_need(P, w, q, a, b);
       const int pos = q.p0 + r_tok;
       float m = -INFINITY, l = 0.0f;  // m: of the scaled scores (log2)
       bool first = true;
+#pragma unroll 1
       for (int st = a; st < b; ++st) {
+        if (!need(st)) continue;
         const TcStep c = tc_step(w, st);
-        if (!tc_need(P, q, c)) continue;
         if (!warp_wait(&s_full[t], n_s & 1, P.err)) {
           ok = false;
           break;
         }
         ++n_s;
         tc_fence_after();
-        uint32_t s[128];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, s + 32 * i);
-        tmem_wait_ld();
         // columns that the row does not see (none in a tile in the middle)
         const bool whole = c.t0 + kTcKeys <= c.end &&
                            (c.sink || (c.t0 + kTcKeys - 1 <= q.p0 &&
                                        (c.t0 > q.p1 - P.window || c.t0 + kTcKeys <= P.n_sink)));
+        uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
         if (!whole) {
-          const int hi = min(c.sink ? c.end - 1 : pos, c.end - 1) - c.t0;         // last column
-          const int lo = c.sink ? 0 : pos - P.window + 1 - c.t0;                   // first of the window
-          const int sk = c.sink ? 0 : P.n_sink - c.t0;                            // columns before it: first tokens
+          const int hi = min(c.sink ? c.end - 1 : pos, c.end - 1) - c.t0;  // last column
+          const int lo = c.sink ? 0 : pos - P.window + 1 - c.t0;            // first of the window
+          const int sk = c.sink ? 0 : P.n_sink - c.t0;                     // columns before it: first tokens
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int h = hi - 32 * i, g = lo - 32 * i, f = sk - 32 * i;
             const uint32_t le = h < 0 ? 0u : h >= 31 ? ~0u : (2u << h) - 1u;
             const uint32_t ge = g <= 0 ? ~0u : g >= 32 ? 0u : ~((1u << g) - 1u);
             const uint32_t lt = f <= 0 ? 0u : f >= 32 ? ~0u : (1u << f) - 1u;
-            const uint32_t see = le & (ge | lt);
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (!((see >> j) & 1u)) s[32 * i + j] = 0xFF800000u;  // -inf
+            see[i] = le & (ge | lt);
           }
         }
-        float mx[4];
+        // the row's 128 scores pass through registers 32 at a time, twice: for
+        // the maximum, and for the weights; a quarter that none of the warp's
+        // rows sees is skipped
+        uint32_t all = 0, some = 0;  // bit i: every row sees all of quarter i; some row sees some of it
 #pragma unroll
-        for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(s[i]);
+        for (int i = 0; i < 4; ++i) {
+          all |= (uint32_t)__all_sync(0xffffffffu, see[i] == ~0u) << i;
+          some |= (uint32_t)__any_sync(0xffffffffu, see[i] != 0u) << i;
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        uint32_t x[32];
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+          if (!((some >> i) & 1)) continue;
+          tmem_ld32(ts + 32 * i, x);
+          tmem_wait_ld();
+          if (!((all >> i) & 1)) {
+            const uint32_t se = i < 2 ? (i ? see[1] : see[0]) : (i == 2 ? see[2] : see[3]);
 #pragma unroll
-        for (int i = 4; i < 128; i += 4)
+            for (int j = 0; j < 32; ++j)
+              if (!((se >> j) & 1u)) x[j] = 0xFF800000u;  // -inf
+          }
 #pragma unroll
-          for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], __uint_as_float(s[i + j]));
+          for (int j = 0; j < 32; j += 2) mx[(j >> 1) & 3] = max3(mx[(j >> 1) & 3], __uint_as_float(x[j]), __uint_as_float(x[j + 1]));
+        }
         const float mn = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
         if (first) {
           m = mn;
@@ -374,33 +424,49 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
           const float f = m2 == -INFINITY ? 1.0f : ex2f(m - m2);
           m = m2;
           l *= f;
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            uint32_t o[32];
-            tmem_ld32(to + 32 * i, o);
+#pragma unroll 1
+          for (int i = 0; i < D / 16; ++i) {
+            uint32_t o[16];
+            tmem_ld16(to + 16 * i, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-            tmem_st32(to + 32 * i, o);
+            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+            tmem_st16(to + 16 * i, o);
           }
         }
         const float base = m == -INFINITY ? 0.0f : m;
-        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        uint64_t sum[2] = {0, 0};  // packed pairs of fp32
+        const uint64_t scale2 = pack2(scale, scale), base2 = pack2(-base, -base);
+        // weights of columns 32 i .. 32 i + 31 go to words 16 i .. 16 i + 15: over scores that are in registers by then
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+          uint32_t pk[16];
+          if (!((some >> i) & 1)) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float p0 = ex2f(fmaf(__uint_as_float(s[64 * i + 2 * j]), scale, -base));
-            const float p1 = ex2f(fmaf(__uint_as_float(s[64 * i + 2 * j + 1]), scale, -base));
-            sum[(2 * j) & 3] += p0;
-            sum[(2 * j + 1) & 3] += p1;
-            const __nv_bfloat162 x = __floats2bfloat162_rn(p0, p1);
-            pk[j] = *reinterpret_cast<const uint32_t*>(&x);
+            for (int j = 0; j < 16; ++j) pk[j] = 0u;
+            tmem_st16(ts + 16 * i, pk);
+            continue;
           }
-          tmem_st32(ts + 32 * i, pk);
+          tmem_ld32(ts + 32 * i, x);
+          tmem_wait_ld();
+          if (!((all >> i) & 1)) {
+            const uint32_t se = i < 2 ? (i ? see[1] : see[0]) : (i == 2 ? see[2] : see[3]);
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (!((se >> j) & 1u)) x[j] = 0xFF800000u;
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float2 y = unpack2(fma2(pack2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), scale2, base2));
+            const float p0 = ex2f(y.x), p1 = ex2f(y.y);
+            sum[j & 1] = add2(sum[j & 1], pack2(p0, p1));
+            const __nv_bfloat162 z = __floats2bfloat162_rn(p0, p1);
+            pk[j] = *reinterpret_cast<const uint32_t*>(&z);
+          }
+          tmem_st16(ts + 16 * i, pk);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        const float2 sa = unpack2(sum[0]), sb = unpack2(sum[1]);
+        l += (sa.x + sa.y) + (sb.x + sb.y);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -418,7 +484,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
         tc_fence_after();
       }
       const int64_t pr = (int64_t)w.slot * P.tile_rows + t * tt * P.group + row;
-#pragma unroll
+#pragma unroll 1
       for (int i = 0; i < D / 32; ++i) {
         uint32_t o[32];
         __syncwarp();

@@ -12,6 +12,12 @@ pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
 
 
+@pytest.fixture(autouse=True)
+def no_wait_runs_out():
+    yield
+    assert K.window_check() == (K.OK, 0)
+
+
 def formula(q, k, v, ql, ks, kl, window, sink, scale):
     """(out, lse, mass) in 64 bits: mass = sum of p |v|, which the tolerances count in."""
     q, k, v = q.double(), k.double(), v.double()
@@ -109,6 +115,13 @@ def test_many_segments(dtype):
     kl = r.randint(0, 90, 600).tolist()
     ql = [int(min(m, x)) for m, x in zip(kl, r.randint(0, 4, 600))]
     run(ql, kl, 2, 1, 64, dtype, 20, 2, gap=1)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_tiles_per_cta(d):
+    """Prompts of more tiles than the GPU has multiprocessors: every CTA takes several, of different lengths."""
+    run([1664, 1500, 700], [1664, 1800, 700], 16, 16, d, BF, 128, 4)
+    run([4096], [4300], 16, 8, d, BF, 1000, 4)
 
 
 def test_long_single_tokens_split_and_merge():
