@@ -106,6 +106,60 @@ __device__ __forceinline__ int tc_nth(const WinParams& P, int k) {
   return i < P.n_items ? P.n_items - 1 - i : -1;
 }
 
+// ---- softmax of one row -----------------------------------------------------------
+__device__ __forceinline__ float tc_max32(const uint32_t* x, float mx) {
+  float a[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int j = 0; j < 32; j += 2)
+    a[(j >> 1) & 3] = max3(a[(j >> 1) & 3], __uint_as_float(x[j]), __uint_as_float(x[j + 1]));
+  return fmaxf(max3(a[0], a[1], a[2]), a[3]);
+}
+__device__ __forceinline__ float tc_max64(const uint32_t* x, float mx) { return tc_max32(x + 32, tc_max32(x, mx)); }
+
+// weights 2^(x scale - base) of 32 scores as bf16 to 16 words of tensor
+// memory, and their fp32 sums (packed pairs)
+__device__ __forceinline__ void tc_weights32(const uint32_t* x, float scale, float base, uint64_t* sum, uint32_t addr) {
+  const uint64_t scale2 = pack2(scale, scale), base2 = pack2(-base, -base);
+  uint32_t pk[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const float2 y = unpack2(fma2(pack2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), scale2, base2));
+    const float p0 = ex2f(y.x), p1 = ex2f(y.y);
+    sum[j & 1] = add2(sum[j & 1], pack2(p0, p1));
+    const __nv_bfloat162 z = __floats2bfloat162_rn(p0, p1);
+    pk[j] = *reinterpret_cast<const uint32_t*>(&z);
+  }
+  tmem_st16(addr, pk);
+}
+__device__ __forceinline__ void tc_weights64(const uint32_t* x, float scale, float base, uint64_t* sum, uint32_t addr) {
+  tc_weights32(x, scale, base, sum, addr);
+  tc_weights32(x + 32, scale, base, sum, addr + 16);
+}
+
+// Take a step's maximum into the row's; the whole warp rescales its sums and
+// outputs (in tensor memory from `to` on) when some row's grew by too much.
+template <int D>
+__device__ __forceinline__ void tc_maximum(float mn, bool& first, float& m, float& l, uint32_t to) {
+  if (first) {
+    m = mn;
+    first = false;
+  } else if (__any_sync(0xffffffffu, mn > m + kRescale)) {
+    const float m2 = fmaxf(m, mn);
+    const float f = m2 == -INFINITY ? 1.0f : ex2f(m - m2);
+    m = m2;
+    l *= f;
+#pragma unroll 1
+    for (int i = 0; i < D / 16; ++i) {
+      uint32_t o[16];
+      tmem_ld16(to + 16 * i, o);
+      tmem_wait_ld();
+#pragma unroll
+      for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+      tmem_st16(to + 16 * i, o);
+    }
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_constant__ WinParams P,
                                                                   const __grid_constant__ TcMaps M) {
@@ -372,15 +426,40 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
         }
         ++n_s;
         tc_fence_after();
-        // columns that the row does not see (none in a tile in the middle)
+        // a tile in the middle: every row of the query tile sees all of it
         const bool whole = c.t0 + kTcKeys <= c.end &&
                            (c.sink || (c.t0 + kTcKeys - 1 <= q.p0 &&
                                        (c.t0 > q.p1 - P.window || c.t0 + kTcKeys <= P.n_sink)));
-        uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
-        if (!whole) {
+        if (whole) {
+          // Scores in registers, 64 at a time: the second half first, for its
+          // maximum; the first half, whose registers then serve for the
+          // weights too; and the second again, on its way while the first
+          // half's weights are worked out (the weights of columns 0 .. 63 are
+          // written over columns 0 .. 31).
+          uint32_t x[64], y[64];
+          tmem_ld32(ts + 64, y);
+          tmem_ld32(ts + 96, y + 32);
+          tmem_wait_ld();
+          tmem_ld32(ts, x);
+          tmem_ld32(ts + 32, x + 32);
+          float mx = tc_max64(y, -INFINITY);
+          tmem_wait_ld();
+          mx = tc_max64(x, mx);
+          tmem_ld32(ts + 64, y);
+          tmem_ld32(ts + 96, y + 32);
+          tc_maximum<D>(mx * scale, first, m, l, to);
+          const float base = m == -INFINITY ? 0.0f : m;
+          uint64_t sum[2] = {0, 0};
+          tc_weights64(x, scale, base, sum, ts);
+          tmem_wait_ld();
+          tc_weights64(y, scale, base, sum, ts + 32);
+          const float2 sa = unpack2(sum[0]), sb = unpack2(sum[1]);
+          l += (sa.x + sa.y) + (sb.x + sb.y);
+        } else {
           const int hi = min(c.sink ? c.end - 1 : pos, c.end - 1) - c.t0;  // last column
           const int lo = c.sink ? 0 : pos - P.window + 1 - c.t0;            // first of the window
           const int sk = c.sink ? 0 : P.n_sink - c.t0;                     // columns before it: first tokens
+          uint32_t see[4], all = 0, some = 0;  // bit i: every row of the warp sees all of quarter i; some row some of it
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int h = hi - 32 * i, g = lo - 32 * i, f = sk - 32 * i;
@@ -388,85 +467,45 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
             const uint32_t ge = g <= 0 ? ~0u : g >= 32 ? 0u : ~((1u << g) - 1u);
             const uint32_t lt = f <= 0 ? 0u : f >= 32 ? ~0u : (1u << f) - 1u;
             see[i] = le & (ge | lt);
+            all |= (uint32_t)__all_sync(0xffffffffu, see[i] == ~0u) << i;
+            some |= (uint32_t)__any_sync(0xffffffffu, see[i] != 0u) << i;
           }
-        }
-        // the row's 128 scores pass through registers 32 at a time, twice: for
-        // the maximum, and for the weights; a quarter that none of the warp's
-        // rows sees is skipped
-        uint32_t all = 0, some = 0;  // bit i: every row sees all of quarter i; some row sees some of it
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          all |= (uint32_t)__all_sync(0xffffffffu, see[i] == ~0u) << i;
-          some |= (uint32_t)__any_sync(0xffffffffu, see[i] != 0u) << i;
-        }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        uint32_t x[32];
-#pragma unroll 1
-        for (int i = 0; i < 4; ++i) {
-          if (!((some >> i) & 1)) continue;
-          tmem_ld32(ts + 32 * i, x);
-          tmem_wait_ld();
-          if (!((all >> i) & 1)) {
+          // 32 scores at a time, twice; a quarter that none of the warp's rows sees is skipped
+          auto quarter = [&](uint32_t* x, int i) {
+            tmem_ld32(ts + 32 * i, x);
+            tmem_wait_ld();
+            if ((all >> i) & 1) return;
             const uint32_t se = i < 2 ? (i ? see[1] : see[0]) : (i == 2 ? see[2] : see[3]);
 #pragma unroll
             for (int j = 0; j < 32; ++j)
               if (!((se >> j) & 1u)) x[j] = 0xFF800000u;  // -inf
-          }
-#pragma unroll
-          for (int j = 0; j < 32; j += 2) mx[(j >> 1) & 3] = max3(mx[(j >> 1) & 3], __uint_as_float(x[j]), __uint_as_float(x[j + 1]));
-        }
-        const float mn = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
-        if (first) {
-          m = mn;
-          first = false;
-        } else if (__any_sync(0xffffffffu, mn > m + kRescale)) {
-          const float m2 = fmaxf(m, mn);
-          const float f = m2 == -INFINITY ? 1.0f : ex2f(m - m2);
-          m = m2;
-          l *= f;
+          };
+          float mx = -INFINITY;
+          uint32_t x[32];
 #pragma unroll 1
-          for (int i = 0; i < D / 16; ++i) {
-            uint32_t o[16];
-            tmem_ld16(to + 16 * i, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-            tmem_st16(to + 16 * i, o);
+          for (int i = 0; i < 4; ++i) {
+            if (!((some >> i) & 1)) continue;
+            quarter(x, i);
+            mx = tc_max32(x, mx);
           }
-        }
-        const float base = m == -INFINITY ? 0.0f : m;
-        uint64_t sum[2] = {0, 0};  // packed pairs of fp32
-        const uint64_t scale2 = pack2(scale, scale), base2 = pack2(-base, -base);
-        // weights of columns 32 i .. 32 i + 31 go to words 16 i .. 16 i + 15: over scores that are in registers by then
+          tc_maximum<D>(mx * scale, first, m, l, to);
+          const float base = m == -INFINITY ? 0.0f : m;
+          uint64_t sum[2] = {0, 0};
+          // weights of columns 32 i .. 32 i + 31 go to words 16 i .. 16 i + 15: over scores that are in registers by then
 #pragma unroll 1
-        for (int i = 0; i < 4; ++i) {
-          uint32_t pk[16];
-          if (!((some >> i) & 1)) {
+          for (int i = 0; i < 4; ++i) {
+            if ((some >> i) & 1) {
+              quarter(x, i);
+              tc_weights32(x, scale, base, sum, ts + 16 * i);
+            } else {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) pk[j] = 0u;
-            tmem_st16(ts + 16 * i, pk);
-            continue;
+              for (int j = 0; j < 16; ++j) x[j] = 0u;
+              tmem_st16(ts + 16 * i, x);
+            }
           }
-          tmem_ld32(ts + 32 * i, x);
-          tmem_wait_ld();
-          if (!((all >> i) & 1)) {
-            const uint32_t se = i < 2 ? (i ? see[1] : see[0]) : (i == 2 ? see[2] : see[3]);
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (!((se >> j) & 1u)) x[j] = 0xFF800000u;
-          }
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float2 y = unpack2(fma2(pack2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), scale2, base2));
-            const float p0 = ex2f(y.x), p1 = ex2f(y.y);
-            sum[j & 1] = add2(sum[j & 1], pack2(p0, p1));
-            const __nv_bfloat162 z = __floats2bfloat162_rn(p0, p1);
-            pk[j] = *reinterpret_cast<const uint32_t*>(&z);
-          }
-          tmem_st16(ts + 16 * i, pk);
+          const float2 sa = unpack2(sum[0]), sb = unpack2(sum[1]);
+          l += (sa.x + sa.y) + (sb.x + sb.y);
         }
-        const float2 sa = unpack2(sum[0]), sb = unpack2(sum[1]);
-        l += (sa.x + sa.y) + (sb.x + sb.y);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
