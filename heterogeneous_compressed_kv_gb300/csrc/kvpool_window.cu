@@ -204,7 +204,7 @@ int check_args(const kvpool_window_args* a, int32_t n, const int64_t* q_len, con
 }
 
 // ---- which kernel takes a segment ------------------------------------------------
-enum Form { kFormTc, kFormFma, kForms };
+enum Form { kFormTok, kFormTc, kFormFma, kForms };
 
 // The tensor copies' limits: strides of used axes positive and below 2^40
 // bytes; the softmax takes the maximum before the scale, so that is positive.
@@ -218,7 +218,7 @@ bool tc_able(const kvpool_window_args* a) {
 
 Form form_of(const kvpool_window_args* a, bool tc, int64_t q_len, int64_t k_len) {
   const int64_t rows = q_len * (a->q.heads / a->k.heads);
-  return tc && k_len > 0 && rows > 16 ? kFormTc : kFormFma;
+  return rows <= kTokRows ? kFormTok : tc && k_len > 0 ? kFormTc : kFormFma;
 }
 
 // the most keys that a tile of the segment sees
@@ -234,7 +234,13 @@ int plan_launch(const kvpool_window_args* a, Form form, bool tc, int32_t i0, int
                 const int64_t* k_start, const int64_t* k_len, int64_t q_row0, int n_sms, WinParams* P, int64_t* next_row,
                 int64_t* slots) {
   const int Hk = a->k.heads;
-  P->tile_tokens = form == kFormTc ? 2 * (kTcTileRows / P->group) : kFmaRows / P->group;
+  int64_t most = 1;  // queries of a single-token segment
+  if (form == kFormTok)
+    for (int j = i0; j < n; ++j)
+      if (form_of(a, tc, q_len[j], k_len[j]) == form) most = std::max(most, q_len[j]);
+  P->tile_tokens = form == kFormTok  ? (int32_t)most
+                   : form == kFormTc ? 2 * (kTcTileRows / P->group)
+                                     : kFmaRows / P->group;
   P->tile_rows = P->tile_tokens * P->group;
   int i = i0;
   P->n_segs = 0;
@@ -252,8 +258,8 @@ int plan_launch(const kvpool_window_args* a, Form form, bool tc, int32_t i0, int
     q_row0 += q_len[i];
   }
   *next_row = q_row0;
-  constexpr int kMinSplitKeys = 128;
-  const int64_t want = form == kFormTc ? n_sms : 2LL * n_sms;  // work items
+  const int64_t min_keys = form == kFormTok ? 256 : 128;
+  const int64_t want = form == kFormTok ? 3LL * n_sms : form == kFormTc ? n_sms : 2LL * n_sms;  // work items
   int64_t items = 0, slot = 0;
   for (int s = 0; s < P->n_segs; ++s) {
     WinSeg& S = P->segs[s];
@@ -262,7 +268,7 @@ int plan_launch(const kvpool_window_args* a, Form form, bool tc, int32_t i0, int
     if (tiles < want)
       split = std::max<int64_t>(
           1, std::min<int64_t>((want + tiles - 1) / tiles,
-                               (tile_keys(a, S.q_len, S.k_len, P->tile_tokens) + kMinSplitKeys - 1) / kMinSplitKeys));
+                               (tile_keys(a, S.q_len, S.k_len, P->tile_tokens) + min_keys - 1) / min_keys));
     S.n_split = (int32_t)split;
     S.item_base = (int32_t)items;
     S.part_base = (int32_t)(slot);
@@ -372,7 +378,8 @@ extern "C" int kvpool_window_attend(const kvpool_window_args* a, int32_t n, cons
       P->part_o = static_cast<float*>(d_workspace);
       P->part_ml = reinterpret_cast<float2*>(P->part_o + slots * P->tile_rows * a->head_dim);
       cudaError_t e = cudaSuccess;
-      if (f == kFormTc) e = (cudaError_t)launch_window_tc(*P, a->head_dim, a->q_rows, a->kv_rows, sms, stream);
+      if (f == kFormTok) e = (cudaError_t)launch_window_tok(*P, a->dtype, a->head_dim, stream);
+      else if (f == kFormTc) e = (cudaError_t)launch_window_tc(*P, a->head_dim, a->q_rows, a->kv_rows, sms, stream);
       else if (a->dtype == KVPOOL_F32)
         e = a->head_dim == 128 ? launch_fma<KVPOOL_F32, 128>(*P, s) : launch_fma<KVPOOL_F32, 64>(*P, s);
       else

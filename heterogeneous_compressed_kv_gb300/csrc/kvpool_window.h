@@ -84,6 +84,11 @@ __device__ __forceinline__ bool win_sees(const WinParams& P, int p, int t) {
   return t <= p && (t > p - P.window || t < P.n_sink);
 }
 
+// Single-token form: at most 16 query rows per key head, the whole segment in
+// one tile.  Returns a cudaError_t.
+constexpr int kTokRows = 16;
+int launch_window_tok(const WinParams& P, int dtype, int head_dim, void* stream);
+
 // Tensor-core form of a launch of prompts (bf16); tiles of two times
 // tile_tokens / 2 tokens.  Returns a cudaError_t.
 constexpr int kTcTileRows = 128;
