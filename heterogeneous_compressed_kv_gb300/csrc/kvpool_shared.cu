@@ -15,6 +15,7 @@
 #include "device_util.cuh"
 #include "kvpool_fma.cuh"
 #include "kvpool_internal.h"
+#include "kvpool_mma.cuh"
 
 namespace kvp {
 namespace {
@@ -115,6 +116,237 @@ __global__ void __launch_bounds__(kFmaThreads) shared_fma_kernel(const __grid_co
   }
 }
 
+// ---- bf16 queries and cache: tensor cores -----------------------------------------
+// Eight warps share stages of 64 entries (K and V of the head, asynchronous
+// copies through a ring of four): RG groups of 16 requests times 8 / RG groups
+// of keys.  Fragments as in the single-token window attention: S^T = K Q^T, 16
+// keys x 8 requests per product, lane (g, t) holding dims 8t .. 8t + 7 of a
+// 32-dim piece; O^T = V^T P^T with V's pairs along the keys from byte permutes.
+//
+// The outputs are fp32 and the cache is bf16, so a bf16 weight would be the one
+// rounding that shows (2^-9): each weight is taken apart into three bf16 numbers
+// whose sum holds its 24 bits, and O^T takes three products.  Scores are exact
+// products summed in fp32.
+constexpr int kMmaWarps = 8, kMmaKeys = 64, kMmaStages = 4;
+
+template <int D>
+struct MmaShared {
+  static constexpr int kTile = kMmaKeys * D * 2;  // K or V of a stage
+  static constexpr int kSmem = kMmaStages * 2 * kTile;
+  static_assert(kSmem >= kMmaWarps * 16 * D * 4, "the warps' outputs reuse the stages");
+};
+
+// 16-byte piece u of row r: swizzled so that both fragments' loads (two rows x
+// four pieces, four rows two apart x two pieces) meet eight different banks
+__device__ __forceinline__ int shared_piece(int r, int u) { return u ^ (r & 6) ^ ((r & 1) << 2); }
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+
+template <int D, int RG>
+__global__ void __launch_bounds__(kMmaWarps * 32, 1) shared_mma_kernel(const __grid_constant__ AttendParams P,
+                                                                       const __grid_constant__ SharedShape H) {
+  pdl_start();
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  __shared__ float2 sml[kMmaWarps][16];
+  constexpr int kTile = MmaShared<D>::kTile, C = D / 32, U = D / 8, KG = kMmaWarps / RG;
+  const PoolDesc& pd = P.pool;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int rg = warp % RG, kg = warp / RG;
+  const int h = blockIdx.x, split = blockIdx.y, i0 = blockIdx.z * kSharedRows;
+  const int rows = min(kSharedRows, P.n - i0);
+  const int a = (int)((int64_t)H.n_entries * split / H.n_split);
+  const int b = (int)((int64_t)H.n_entries * (split + 1) / H.n_split);
+  const float qscale = 1.4426950408889634f * rsqrtf((float)D);
+  const uint32_t base = smem_addr(smem_raw);
+
+  // query fragments: request 16 rg + 8n + g, dims 32c + 8t .. + 7
+  uint4 q[2][C];
+#pragma unroll
+  for (int n = 0; n < 2; ++n)
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int r = 16 * rg + 8 * n + g;
+      q[n][c] = make_uint4(0, 0, 0, 0);
+      if (r < rows)
+        q[n][c] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(P.q) +
+                                                  2 * ((int64_t)(P.row0 + i0 + r) * pd.HD + h * D + 32 * c + 8 * t));
+    }
+  // four threads copy an entry: pieces tid % 4, + 4, ... of its K and V
+  const int n_st = (b - a + kMmaKeys - 1) / kMmaKeys;
+  const int ce = tid >> 2, cu = tid & 3;
+  auto copy = [&](int st) {
+    const int e = a + st * kMmaKeys + ce;
+    if (st < n_st) {
+      // entries behind the end repeat the last one (masked below)
+      const uint8_t* src = shared_entry(P, H, min(e, b - 1)) + h * D * 2;
+      const uint32_t dst = base + (st % kMmaStages) * 2 * kTile + ce * D * 2;
+#pragma unroll
+      for (int u = 0; u < U; u += 4) {
+        const uint32_t at = shared_piece(ce, u + cu) * 16;
+        cp_async16(dst + at, src + (u + cu) * 16);
+        cp_async16(dst + kTile + at, src + pd.HD * 2 + (u + cu) * 16);
+      }
+    }
+    cp_async_commit();
+  };
+  for (int st = 0; st < kMmaStages - 1; ++st) copy(st);
+
+  float m[2][2], l[2][2], o[2][D / 16][4];
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    m[n][0] = m[n][1] = -INFINITY;
+    l[n][0] = l[n][1] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[n][i][j] = 0.0f;
+  }
+  for (int st = 0; st < n_st; ++st) {
+    cp_async_wait<kMmaStages - 2>();
+    __syncthreads();  // the stage has landed for all; the one copied next has been read by all
+    copy(st + kMmaStages - 1);
+    const uint32_t sk = base + (st % kMmaStages) * 2 * kTile, sv = sk + kTile;
+    const int n_key = min(kMmaKeys, b - a - st * kMmaKeys);
+    for (int k0 = 16 * kg; k0 < n_key; k0 += 16 * KG) {
+      float s[2][4] = {};
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const uint4 ka = lds16(sk + (k0 + g) * D * 2 + shared_piece(g, 4 * c + t) * 16);
+        const uint4 kb = lds16(sk + (k0 + 8 + g) * D * 2 + shared_piece(g, 4 * c + t) * 16);
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          mma_bf16(s[n], ka.x, kb.x, ka.y, kb.y, q[n][c].x, q[n][c].y);
+          mma_bf16(s[n], ka.z, kb.z, ka.w, kb.w, q[n][c].z, q[n][c].w);
+        }
+      }
+      uint32_t pt[2][3][2];  // [requests][piece of the weights][keys 0 - 7, 8 - 15]
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        float corr[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          s[n][e] = k0 + g < n_key ? s[n][e] * qscale : -INFINITY;
+          s[n][2 + e] = k0 + 8 + g < n_key ? s[n][2 + e] * qscale : -INFINITY;
+          float mx = fmaxf(s[n][e], s[n][2 + e]);
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+          mx = fmaxf(mx, m[n][e]);  // finite: some key of the group counts
+          corr[e] = ex2f(m[n][e] - mx);
+          m[n][e] = mx;
+          s[n][e] = ex2f(s[n][e] - mx);
+          s[n][2 + e] = ex2f(s[n][2 + e] - mx);
+          l[n][e] = fmaf(l[n][e], corr[e], s[n][e] + s[n][2 + e]);  // this lane's keys only
+        }
+        if (__any_sync(0xffffffffu, corr[0] != 1.0f || corr[1] != 1.0f)) {
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[n][i][j] *= corr[j & 1];
+        }
+#pragma unroll
+        for (int x = 0; x < 3; ++x)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t pk = pack_bf16(s[n][2 * i], s[n][2 * i + 1]);
+            s[n][2 * i] -= __uint_as_float(pk << 16);
+            s[n][2 * i + 1] -= __uint_as_float(pk & 0xFFFF0000u);
+            pt[n][x][i] = transpose8x8(pk);
+          }
+      }
+#pragma unroll
+      for (int hh = 0; hh < D / 64; ++hh) {
+        uint4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = k0 + 2 * t + (i & 1) + 8 * (i >> 1);
+          v[i] = lds16(sv + r * D * 2 + shared_piece(r & 7, 8 * hh + g) * 16);
+        }
+        const uint32_t v0[4] = {v[0].x, v[0].y, v[0].z, v[0].w}, v1[4] = {v[1].x, v[1].y, v[1].z, v[1].w};
+        const uint32_t v2[4] = {v[2].x, v[2].y, v[2].z, v[2].w}, v3[4] = {v[3].x, v[3].y, v[3].z, v[3].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t a0 = __byte_perm(v0[j], v1[j], 0x5410), a1 = __byte_perm(v0[j], v1[j], 0x7632);
+          const uint32_t a2 = __byte_perm(v2[j], v3[j], 0x5410), a3 = __byte_perm(v2[j], v3[j], 0x7632);
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int x = 2; x >= 0; --x) mma_bf16(o[n][4 * hh + j], a0, a1, a2, a3, pt[n][x][0], pt[n][x][1]);
+        }
+      }
+    }
+  }
+  cp_async_wait<0>();
+  __syncthreads();
+  // the key groups' states of a request into one
+  float* so = reinterpret_cast<float*>(smem_raw);  // [warp][16][D]
+#pragma unroll
+  for (int n = 0; n < 2; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], off);
+      const int r = 8 * n + 2 * t + e;
+      if (g == 0) sml[warp][r] = make_float2(m[n][e], l[n][e]);
+#pragma unroll
+      for (int hh = 0; hh < D / 64; ++hh)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<float2*>(so + (warp * 16 + r) * D + 64 * hh + 8 * g + 2 * j) =
+              make_float2(o[n][4 * hh + j][e], o[n][4 * hh + j][2 + e]);
+    }
+  __syncthreads();
+  for (int i = tid; i < min(rows, 16 * RG) * (D / 4); i += kMmaWarps * 32) {
+    const int r = i / (D / 4), c = 4 * (i % (D / 4));
+    float mx = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < KG; ++k) mx = fmaxf(mx, sml[k * RG + r / 16][r % 16].x);
+    float ls = 0.0f;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < KG; ++k) {
+      const int wp = k * RG + r / 16;
+      const float2 ml = sml[wp][r % 16];
+      const float f = ex2f(ml.x - mx);
+      const float4 y = *reinterpret_cast<const float4*>(so + (wp * 16 + r % 16) * D + c);
+      ls = fmaf(ml.y, f, ls);
+      x.x = fmaf(y.x, f, x.x);
+      x.y = fmaf(y.y, f, x.y);
+      x.z = fmaf(y.z, f, x.z);
+      x.w = fmaf(y.w, f, x.w);
+    }
+    const int64_t slot = shared_slot(P, i0 + r, split);
+    *reinterpret_cast<float4*>(P.part_o + slot * pd.HD + h * D + c) = x;
+    if (c == 0) *reinterpret_cast<float2*>(P.part_ml + (slot * pd.heads + h) * 2) = make_float2(mx, ls);
+  }
+}
+
+template <int D, int RG>
+cudaError_t launch_mma_t(const AttendParams& p, const SharedShape& h, cudaStream_t s) {
+  auto* kern = shared_mma_kernel<D, RG>;
+  constexpr int smem = MmaShared<D>::kSmem;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(true, kern, dim3(p.pool.heads, h.n_split, (p.n + kSharedRows - 1) / kSharedRows),
+                       dim3(kMmaWarps * 32), smem, s, p, h);
+}
+// the fewest groups of 16 requests that hold a CTA's
+template <int D>
+cudaError_t launch_mma(const AttendParams& p, const SharedShape& h, cudaStream_t s) {
+  return p.n <= 16 ? launch_mma_t<D, 1>(p, h, s) : p.n <= 32 ? launch_mma_t<D, 2>(p, h, s) : launch_mma_t<D, 4>(p, h, s);
+}
+
 template <int IN, int CACHE, int D>
 cudaError_t launch_shared_t(const AttendParams& p, const SharedShape& h, cudaStream_t s) {
   auto* kern = shared_fma_kernel<IN, CACHE, D>;
@@ -133,10 +365,12 @@ cudaError_t launch_shared_d(const AttendParams& p, const SharedShape& h, cudaStr
 }  // namespace
 
 // Splits of the shared entries for n requests: CTAs (head, split, 64
-// requests) that fill the GPU twice over, of at least 64 entries each.
+// requests) that fill the GPU (the FMA form: twice over), of at least 64
+// entries each.
 int shared_splits(const PoolDesc& pd, int n, int n_entries, int n_sms) {
   const int per = pd.heads * ((n + kSharedRows - 1) / kSharedRows);
-  return std::max(1, std::min((2 * n_sms + per - 1) / per, (n_entries + 63) / 64));
+  const bool mma = pd.in_dtype == KVPOOL_BF16 && pd.cache_dtype == KVPOOL_BF16;
+  return std::max(1, std::min(mma ? n_sms / per : (2 * n_sms + per - 1) / per, (n_entries + 63) / 64));
 }
 
 int launch_shared(const AttendParams& p, int n_entries, int n_split, void* stream, int* n_kernels) {
@@ -148,7 +382,8 @@ int launch_shared(const AttendParams& p, int n_entries, int n_split, void* strea
     case KVPOOL_F32 * 3 + KVPOOL_BF16: return (int)launch_shared_d<KVPOOL_F32, KVPOOL_BF16>(p, h, s);
     case KVPOOL_F32 * 3 + KVPOOL_FP8_E4M3: return (int)launch_shared_d<KVPOOL_F32, KVPOOL_FP8_E4M3>(p, h, s);
     case KVPOOL_BF16 * 3 + KVPOOL_F32: return (int)launch_shared_d<KVPOOL_BF16, KVPOOL_F32>(p, h, s);
-    case KVPOOL_BF16 * 3 + KVPOOL_BF16: return (int)launch_shared_d<KVPOOL_BF16, KVPOOL_BF16>(p, h, s);
+    case KVPOOL_BF16 * 3 + KVPOOL_BF16:
+      return (int)(p.pool.head_dim == 128 ? launch_mma<128>(p, h, s) : launch_mma<64>(p, h, s));
     case KVPOOL_BF16 * 3 + KVPOOL_FP8_E4M3: return (int)launch_shared_d<KVPOOL_BF16, KVPOOL_FP8_E4M3>(p, h, s);
     default: return (int)cudaErrorInvalidValue;
   }
