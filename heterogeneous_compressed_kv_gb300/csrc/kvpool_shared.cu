@@ -161,6 +161,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 1) shared_mma_kernel(const __g
   extern __shared__ __align__(128) uint8_t smem_raw[];
   __shared__ float2 sml[kMmaWarps][16];
   constexpr int kTile = MmaShared<D>::kTile, C = D / 32, U = D / 8, KG = kMmaWarps / RG;
+  constexpr int KB = KG <= 2 ? 2 : 1;  // blocks of 16 keys that a warp takes at once
   const PoolDesc& pd = P.pool;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int rg = warp % RG, kg = warp / RG;
@@ -219,35 +220,49 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 1) shared_mma_kernel(const __g
     copy(st + kMmaStages - 1);
     const uint32_t sk = base + (st % kMmaStages) * 2 * kTile, sv = sk + kTile;
     const int n_key = min(kMmaKeys, b - a - st * kMmaKeys);
-    for (int k0 = 16 * kg; k0 < n_key; k0 += 16 * KG) {
-      float s[2][4] = {};
+    for (int k0 = 16 * KB * kg; k0 < n_key; k0 += 16 * KB * KG) {
+      float s[KB][2][4] = {};
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const uint4 ka = lds16(sk + (k0 + g) * D * 2 + shared_piece(g, 4 * c + t) * 16);
-        const uint4 kb = lds16(sk + (k0 + 8 + g) * D * 2 + shared_piece(g, 4 * c + t) * 16);
+      for (int c = 0; c < C; ++c)
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          mma_bf16(s[n], ka.x, kb.x, ka.y, kb.y, q[n][c].x, q[n][c].y);
-          mma_bf16(s[n], ka.z, kb.z, ka.w, kb.w, q[n][c].z, q[n][c].w);
+        for (int k = 0; k < KB; ++k) {
+          const uint4 ka = lds16(sk + (k0 + 16 * k + g) * D * 2 + shared_piece(g, 4 * c + t) * 16);
+          const uint4 kb = lds16(sk + (k0 + 16 * k + 8 + g) * D * 2 + shared_piece(g, 4 * c + t) * 16);
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            mma_bf16(s[k][n], ka.x, kb.x, ka.y, kb.y, q[n][c].x, q[n][c].y);
+            mma_bf16(s[k][n], ka.z, kb.z, ka.w, kb.w, q[n][c].z, q[n][c].w);
+          }
         }
-      }
-      uint32_t pt[2][3][2];  // [requests][piece of the weights][keys 0 - 7, 8 - 15]
+      uint32_t pt[KB][2][3][2];  // [16 keys][requests][piece of the weights][keys 0 - 7, 8 - 15]
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
         float corr[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          s[n][e] = k0 + g < n_key ? s[n][e] * qscale : -INFINITY;
-          s[n][2 + e] = k0 + 8 + g < n_key ? s[n][2 + e] * qscale : -INFINITY;
-          float mx = fmaxf(s[n][e], s[n][2 + e]);
+          float mx = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < KB; ++k)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float& x = s[k][n][2 * i + e];
+              x = k0 + 16 * k + 8 * i + g < n_key ? x * qscale : -INFINITY;
+              mx = fmaxf(mx, x);
+            }
 #pragma unroll
           for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
           mx = fmaxf(mx, m[n][e]);  // finite: some key of the group counts
           corr[e] = ex2f(m[n][e] - mx);
           m[n][e] = mx;
-          s[n][e] = ex2f(s[n][e] - mx);
-          s[n][2 + e] = ex2f(s[n][2 + e] - mx);
-          l[n][e] = fmaf(l[n][e], corr[e], s[n][e] + s[n][2 + e]);  // this lane's keys only
+          l[n][e] *= corr[e];
+#pragma unroll
+          for (int k = 0; k < KB; ++k)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float& x = s[k][n][2 * i + e];
+              x = ex2f(x - mx);
+              l[n][e] += x;  // this lane's keys only
+            }
         }
         if (__any_sync(0xffffffffu, corr[0] != 1.0f || corr[1] != 1.0f)) {
 #pragma unroll
@@ -256,35 +271,46 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 1) shared_mma_kernel(const __g
             for (int j = 0; j < 4; ++j) o[n][i][j] *= corr[j & 1];
         }
 #pragma unroll
-        for (int x = 0; x < 3; ++x)
+        for (int k = 0; k < KB; ++k)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t pk = pack_bf16(s[n][2 * i], s[n][2 * i + 1]);
-            s[n][2 * i] -= __uint_as_float(pk << 16);
-            s[n][2 * i + 1] -= __uint_as_float(pk & 0xFFFF0000u);
-            pt[n][x][i] = transpose8x8(pk);
+          for (int x = 0; x < 3; ++x)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t pk = pack_bf16(s[k][n][2 * i], s[k][n][2 * i + 1]);
+              s[k][n][2 * i] -= __uint_as_float(pk << 16);
+              s[k][n][2 * i + 1] -= __uint_as_float(pk & 0xFFFF0000u);
+              pt[k][n][x][i] = transpose8x8(pk);
+            }
+      }
+#pragma unroll
+      for (int k = 0; k < KB; ++k)
+#pragma unroll
+        for (int hh = 0; hh < D / 64; ++hh) {
+          uint4 v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = k0 + 16 * k + 2 * t + (i & 1) + 8 * (i >> 1);
+            v[i] = lds16(sv + r * D * 2 + shared_piece(r & 7, 8 * hh + g) * 16);
           }
-      }
+          const uint32_t v0[4] = {v[0].x, v[0].y, v[0].z, v[0].w}, v1[4] = {v[1].x, v[1].y, v[1].z, v[1].w};
+          const uint32_t v2[4] = {v[2].x, v[2].y, v[2].z, v[2].w}, v3[4] = {v[3].x, v[3].y, v[3].z, v[3].w};
+          uint32_t f[4][4];
 #pragma unroll
-      for (int hh = 0; hh < D / 64; ++hh) {
-        uint4 v[4];
+          for (int j = 0; j < 4; ++j) {
+            f[j][0] = __byte_perm(v0[j], v1[j], 0x5410);
+            f[j][1] = __byte_perm(v0[j], v1[j], 0x7632);
+            f[j][2] = __byte_perm(v2[j], v3[j], 0x5410);
+            f[j][3] = __byte_perm(v2[j], v3[j], 0x7632);
+          }
+          // eight independent sums in a row
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = k0 + 2 * t + (i & 1) + 8 * (i >> 1);
-          v[i] = lds16(sv + r * D * 2 + shared_piece(r & 7, 8 * hh + g) * 16);
+          for (int x = 2; x >= 0; --x)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int n = 0; n < 2; ++n)
+                mma_bf16(o[n][4 * hh + j], f[j][0], f[j][1], f[j][2], f[j][3], pt[k][n][x][0], pt[k][n][x][1]);
         }
-        const uint32_t v0[4] = {v[0].x, v[0].y, v[0].z, v[0].w}, v1[4] = {v[1].x, v[1].y, v[1].z, v[1].w};
-        const uint32_t v2[4] = {v[2].x, v[2].y, v[2].z, v[2].w}, v3[4] = {v[3].x, v[3].y, v[3].z, v[3].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t a0 = __byte_perm(v0[j], v1[j], 0x5410), a1 = __byte_perm(v0[j], v1[j], 0x7632);
-          const uint32_t a2 = __byte_perm(v2[j], v3[j], 0x5410), a3 = __byte_perm(v2[j], v3[j], 0x7632);
-#pragma unroll
-          for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int x = 2; x >= 0; --x) mma_bf16(o[n][4 * hh + j], a0, a1, a2, a3, pt[n][x][0], pt[n][x][1]);
-        }
-      }
     }
   }
   cp_async_wait<0>();
