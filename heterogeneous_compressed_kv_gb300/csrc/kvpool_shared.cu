@@ -117,8 +117,8 @@ __global__ void __launch_bounds__(kFmaThreads) shared_fma_kernel(const __grid_co
 }
 
 // ---- bf16 queries and cache: tensor cores -----------------------------------------
-// Eight warps share stages of 64 entries (K and V of the head, asynchronous
-// copies through a ring of four): RG groups of 16 requests times 8 / RG groups
+// Eight warps share stages of 128 entries (K and V of the head, asynchronous
+// copies through a ring of three): RG groups of 16 requests times 8 / RG groups
 // of keys.  Fragments as in the single-token window attention: S^T = K Q^T, 16
 // keys x 8 requests per product, lane (g, t) holding dims 8t .. 8t + 7 of a
 // 32-dim piece; O^T = V^T P^T with V's pairs along the keys from byte permutes.
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kFmaThreads) shared_fma_kernel(const __grid_co
 // rounding that shows (2^-9): each weight is taken apart into three bf16 numbers
 // whose sum holds its 24 bits, and O^T takes three products.  Scores are exact
 // products summed in fp32.
-constexpr int kMmaWarps = 8, kMmaKeys = 64, kMmaStages = 4;
+constexpr int kMmaWarps = 8, kMmaKeys = 128, kMmaStages = 3;
 
 template <int D>
 struct MmaShared {
@@ -188,18 +188,20 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 1) shared_mma_kernel(const __g
   const int n_st = (b - a + kMmaKeys - 1) / kMmaKeys;
   const int ce = tid >> 2, cu = tid & 3;
   auto copy = [&](int st) {
-    const int e = a + st * kMmaKeys + ce;
-    if (st < n_st) {
-      // entries behind the end repeat the last one (masked below)
-      const uint8_t* src = shared_entry(P, H, min(e, b - 1)) + h * D * 2;
-      const uint32_t dst = base + (st % kMmaStages) * 2 * kTile + ce * D * 2;
+    if (st < n_st)
 #pragma unroll
-      for (int u = 0; u < U; u += 4) {
-        const uint32_t at = shared_piece(ce, u + cu) * 16;
-        cp_async16(dst + at, src + (u + cu) * 16);
-        cp_async16(dst + kTile + at, src + pd.HD * 2 + (u + cu) * 16);
+      for (int x = 0; x < kMmaKeys; x += 64) {
+        const int e = a + st * kMmaKeys + x + ce;
+        // entries behind the end repeat the last one (masked below)
+        const uint8_t* src = shared_entry(P, H, min(e, b - 1)) + h * D * 2;
+        const uint32_t dst = base + (st % kMmaStages) * 2 * kTile + (x + ce) * D * 2;
+#pragma unroll
+        for (int u = 0; u < U; u += 4) {
+          const uint32_t at = shared_piece(ce, u + cu) * 16;
+          cp_async16(dst + at, src + (u + cu) * 16);
+          cp_async16(dst + kTile + at, src + pd.HD * 2 + (u + cu) * 16);
+        }
       }
-    }
     cp_async_commit();
   };
   for (int st = 0; st < kMmaStages - 1; ++st) copy(st);
