@@ -19,18 +19,27 @@
 // cosines once (two per lane at 128 dims), pass them through shared memory,
 // and then stream heads, 8 values (16 bytes of bf16) per lane and four loads
 // ahead.  Norms are held in fp32; one rounding at the store.
+//
+// What the first form lost was instructions (214 a step of two 128-dim heads,
+// 66% of the issue slots at 3.7 TB/s): the weights are now multiplied into the
+// sines and cosines once per token and tensor, so that with r = 1 / sqrt(...)
+//   y = r * (x * (w cos) + z * (w_z sin)),  z the pair's other value,
+// z travels between lanes as it was loaded (two bf16 to a word), and fp32 pairs
+// share instructions.
 #include <cmath>
+#include <type_traits>
 
 #include <cuda_runtime.h>
 
 #include "device_util.cuh"
 #include "kvpool_internal.h"
+#include "kvpool_pair.cuh"
 
 namespace kvp {
 namespace {
 
 constexpr int kRopeWarps = 4;    // warps per CTA
-constexpr int kRopeAhead = 4;    // heads per lane group in flight
+constexpr int kRopeAhead = 4;    // steps (heads per lane group) in flight
 constexpr int kRopeMaxDim = 256;
 
 struct RopeTensor {
@@ -46,67 +55,97 @@ struct RopeParams {
   const int64_t* pos;
   const uint64_t* table;
   int64_t n_tokens;
-  int32_t head_dim, rot_dim, lanes, group;  // lanes with values per head, lanes per head (a power of two)
-  int32_t interleaved, runs, run_steps;     // runs: warps per token, steps of each
+  int32_t rot_dim, lanes;   // lanes with values per head
+  int32_t runs, run_steps;  // runs: warps per token, steps of each
   float eps, inv_dim;
 };
 
-// 8 values from memory in fp32
+// 8 values as loaded: W words, V = 8 / W of them to a word
 template <int T>
 struct Vec8;
 template <>
 struct Vec8<KVPOOL_BF16> {
-  uint4 r;
-  __device__ __forceinline__ void load(const uint8_t* p) { r = *reinterpret_cast<const uint4*>(p); }
-  __device__ __forceinline__ void get(float* x) const {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
+  static constexpr int W = 4;
+  uint32_t w[4];
+  __device__ __forceinline__ void load(const uint8_t* p) {
+    const uint4 r = *reinterpret_cast<const uint4*>(p);
+    w[0] = r.x, w[1] = r.y, w[2] = r.z, w[3] = r.w;
   }
-  static __device__ __forceinline__ void put(uint8_t* p, const float* x) {
-    uint32_t w[4];
+  // values 2i and 2i + 1 in fp32
+  __device__ __forceinline__ uint64_t pair(int i) const {
+    return pack2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+  }
+  static __device__ __forceinline__ void put(uint8_t* p, const uint64_t* y) {
+    uint32_t o[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&b);
+      const float2 f = unpack2(y[i]);
+      const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
+      o[i] = *reinterpret_cast<const uint32_t*>(&b);
     }
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(p) = make_uint4(o[0], o[1], o[2], o[3]);
   }
 };
 template <>
 struct Vec8<KVPOOL_F32> {
-  float4 a, b;
+  static constexpr int W = 8;
+  uint32_t w[8];
   __device__ __forceinline__ void load(const uint8_t* p) {
-    a = reinterpret_cast<const float4*>(p)[0];
-    b = reinterpret_cast<const float4*>(p)[1];
+    const uint4 a = reinterpret_cast<const uint4*>(p)[0], b = reinterpret_cast<const uint4*>(p)[1];
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+    w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
   }
-  __device__ __forceinline__ void get(float* x) const {
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  __device__ __forceinline__ uint64_t pair(int i) const {
+    return pack2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
   }
-  static __device__ __forceinline__ void put(uint8_t* p, const float* x) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+  static __device__ __forceinline__ void put(uint8_t* p, const uint64_t* y) {
+    const float2 a = unpack2(y[0]), b = unpack2(y[1]), c = unpack2(y[2]), d = unpack2(y[3]);
+    reinterpret_cast<float4*>(p)[0] = make_float4(a.x, a.y, b.x, b.y);
+    reinterpret_cast<float4*>(p)[1] = make_float4(c.x, c.y, d.x, d.y);
   }
 };
 
-template <int T, bool INTER>
-__global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const __grid_constant__ RopeParams P) {
+// G: lanes of a head (of which head_dim / 8 have values)
+template <int T, bool INTER, int G>
+__global__ void __launch_bounds__(kRopeWarps * 32, T == KVPOOL_BF16 ? 8 : 5) rope_kernel(const __grid_constant__ RopeParams P) {
   pdl_start();
-  __shared__ float2 turn[kRopeWarps][kRopeMaxDim / 2];  // (cos, sin) of the warp's token
-  constexpr int kValBytes = T == KVPOOL_BF16 ? 2 : 4;
+  // cosines and sines of the warps' tokens, in two rows: a lane takes 4 or 8
+  // neighbours of each in 16-byte loads (as pairs, 8 bytes each, their bank
+  // conflicts cost more than the heads' shuffles)
+  __shared__ __align__(16) float turn[kRopeWarps][2][G * 4];
+  constexpr int kVecBytes = T == KVPOOL_BF16 ? 16 : 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t task = (int64_t)blockIdx.x * kRopeWarps + warp;
-  const int64_t tok = task / P.runs;
+  const int64_t tok = P.runs == 1 ? task : task / P.runs;
   if (tok >= P.n_tokens) return;
   const int s0 = (int)(task - tok * P.runs) * P.run_steps;
   const int s1 = min(s0 + P.run_steps, P.t[0].steps + P.t[1].steps);
-  const int sub = lane / P.group, l = lane % P.group;  // head within a step, lane within the head
-  const int per_step = 32 / P.group;
+  const int sub = lane / G, l = lane % G;  // head within a step, lane within the head
+  constexpr int per_step = 32 / G;
   const bool on = l < P.lanes;
+
+  // The batch of steps st .. st + 3 of tensor X, of which those below b and of
+  // a head that there is: pointers are of step st.
+  Vec8<T> v[kRopeAhead];
+  auto load = [&](const RopeTensor& X, const uint8_t* in, int st, int b, int left) {
+    const int64_t in_step = per_step * X.in_head;
+#pragma unroll
+    for (int u = 0; u < kRopeAhead; ++u) {
+#pragma unroll
+      for (int i = 0; i < Vec8<T>::W; ++i) v[u].w[i] = 0u;
+      if (st + u < b && u * per_step < left) v[u].load(in + u * in_step);
+    }
+  };
+  auto in_ptr = [&](const RopeTensor& X, int st) {
+    return X.in + tok * X.in_tok + (int64_t)(st * per_step + sub) * X.in_head + l * kVecBytes;
+  };
+  // the first batch is on its way while the angles are worked out
+  {
+    const int which = s0 >= P.t[0].steps, a = s0 - (which ? P.t[0].steps : 0);
+    const RopeTensor& X = P.t[which];
+    load(X, in_ptr(X, a), a, min(s1 - s0 + a, X.steps), on ? X.heads - (a * per_step + sub) : 0);
+  }
+  bool loaded = true;
 
   const int half = P.rot_dim / 2;
   if (half > 0) {
@@ -115,72 +154,98 @@ __global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const __grid_cons
       const int32_t t = (int32_t)((p * P.table[i]) >> 32);
       float s, c;
       sincospif((float)t * 0x1p-31f, &s, &c);
-      turn[warp][i] = make_float2(c, s);
+      turn[warp][0][i] = c;
+      turn[warp][1][i] = s;
     }
     __syncwarp();
   }
-  // this lane's angles: of its 8 values (pairs half a rotation apart) or of its 4 pairs
   const bool rot = on && 8 * l < P.rot_dim;
-  constexpr int kAng = INTER ? 4 : 8;
-  float2 cs[kAng];
   const bool low = 8 * l < half;  // pairs half a rotation apart: the first of its pairs?
-#pragma unroll
-  for (int j = 0; j < kAng; ++j)
-    cs[j] = rot ? turn[warp][INTER ? 4 * l + j : (low ? 8 * l : 8 * l - half) + j] : make_float2(1.0f, 0.0f);
   const int partner = (lane - l) + (rot ? (low ? l + half / 8 : l - half / 8) : l);
+  const int other = partner - (lane - l);  // the partner's lane within the head
 
-  float w[8];
-  int have = -1;  // tensor whose weights w holds
-  for (int s = s0; s < s1; s += kRopeAhead) {
-    Vec8<T> v[kRopeAhead];
+#pragma unroll 1
+  for (int which = 0; which < 2; ++which) {
+    const RopeTensor& X = P.t[which];
+    const int from = which ? P.t[0].steps : 0;
+    const int a = max(s0 - from, 0), b = min(s1 - from, X.steps);  // steps of this tensor
+    if (a >= b) continue;
+    const uint8_t* in = in_ptr(X, a);
+    uint8_t* out = X.out + tok * X.out_tok + (int64_t)(a * per_step + sub) * X.out_head + l * kVecBytes;
+    const int64_t in_step = per_step * X.in_head, out_step = per_step * X.out_head;
+    int left = on ? X.heads - (a * per_step + sub) : 0;  // heads from this lane's first one on
+    // weight times cosine of the value's own, weight times signed sine of the pair's other value
+    uint64_t wc[4], ws[4];
+    float c[8], sn[8], w[8], wz[8];
 #pragma unroll
-    for (int u = 0; u < kRopeAhead; ++u) {
-      const int st = s + u;
-      if (st < s1) {
-        const int which = st >= P.t[0].steps;
-        const RopeTensor& X = P.t[which];
-        const int h = (st - (which ? P.t[0].steps : 0)) * per_step + sub;
-        if (on && h < X.heads) v[u].load(X.in + tok * X.in_tok + h * X.in_head + l * 8 * kValBytes);
+    for (int j = 0; j < 8; ++j) c[j] = w[j] = wz[j] = 1.0f, sn[j] = 0.0f;
+    if (rot) {
+      constexpr int kAng = INTER ? 4 : 8;
+      const int at = INTER ? 4 * l : low ? 8 * l : 8 * l - half;
+      float x[kAng], y[kAng];
+#pragma unroll
+      for (int j = 0; j < kAng; j += 4) {
+        *reinterpret_cast<float4*>(x + j) = *reinterpret_cast<const float4*>(&turn[warp][0][at + j]);
+        *reinterpret_cast<float4*>(y + j) = *reinterpret_cast<const float4*>(&turn[warp][1][at + j]);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        c[j] = x[INTER ? j / 2 : j];
+        sn[j] = (INTER ? j % 2 == 0 : low) ? -y[INTER ? j / 2 : j] : y[INTER ? j / 2 : j];
+      }
+    }
+    if (X.w && on) {
+#pragma unroll
+      for (int j = 0; j < 8; j += 4) {
+        *reinterpret_cast<float4*>(w + j) = *reinterpret_cast<const float4*>(X.w + 8 * l + j);
+        if (!INTER) *reinterpret_cast<float4*>(wz + j) = *reinterpret_cast<const float4*>(X.w + 8 * other + j);
       }
     }
 #pragma unroll
-    for (int u = 0; u < kRopeAhead; ++u) {
-      const int st = s + u;
-      if (st >= s1) break;
-      const int which = st >= P.t[0].steps;
-      const RopeTensor& X = P.t[which];
-      if (have != which) {
-        have = which;
+    for (int i = 0; i < 4; ++i) {
+      wc[i] = pack2(c[2 * i] * w[2 * i], c[2 * i + 1] * w[2 * i + 1]);
+      ws[i] = INTER ? pack2(sn[2 * i] * w[2 * i + 1], sn[2 * i + 1] * w[2 * i])
+                    : pack2(sn[2 * i] * wz[2 * i], sn[2 * i + 1] * wz[2 * i + 1]);
+    }
+#pragma unroll 1
+    for (int st = a; st < b; st += kRopeAhead) {
+      if (!loaded) load(X, in, st, b, left);
+      loaded = false;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = X.w && on ? X.w[8 * l + j] : 1.0f;
-      }
-      const int h = (st - (which ? P.t[0].steps : 0)) * per_step + sub;
-      const bool mine = on && h < X.heads;
-      float x[8], y[8];
+      for (int u = 0; u < kRopeAhead; ++u) {
+        if (st + u >= b) break;
+        uint64_t sq = 0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = 0.0f;
-      if (mine) v[u].get(x);
-      float ss = 0.0f;
+        for (int i = 0; i < 4; ++i) sq = fma2(v[u].pair(i), v[u].pair(i), sq);
+        const float2 f = unpack2(sq);
+        float ss = f.x + f.y;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
-      for (int o = P.group / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      const float r = rsqrtf(fmaf(ss, P.inv_dim, P.eps));
+        for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        const float r = rsqrtf(fmaf(ss, P.inv_dim, P.eps));
+        Vec8<T> z;
+        if constexpr (!INTER) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = x[j] * r * w[j];
-      if constexpr (INTER) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          y[2 * j] = fmaf(x[2 * j], cs[j].x, -x[2 * j + 1] * cs[j].y);
-          y[2 * j + 1] = fmaf(x[2 * j + 1], cs[j].x, x[2 * j] * cs[j].y);
+          for (int i = 0; i < Vec8<T>::W; ++i) z.w[i] = __shfl_sync(0xffffffffu, v[u].w[i], partner);
         }
-      } else {
+        const uint64_t r2 = pack2(r, r);
+        uint64_t y[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float z = __shfl_sync(0xffffffffu, x[j], partner);
-          y[j] = fmaf(x[j], cs[j].x, low ? -z * cs[j].y : z * cs[j].y);
+        for (int i = 0; i < 4; ++i) {
+          const uint64_t x = v[u].pair(i);
+          uint64_t zz;
+          if constexpr (INTER) {
+            const float2 q = unpack2(x);
+            zz = pack2(q.y, q.x);
+          } else {
+            zz = z.pair(i);
+          }
+          y[i] = mul2(fma2(zz, ws[i], mul2(x, wc[i])), r2);
         }
+        if (u * per_step < left) Vec8<T>::put(out + u * out_step, y);
       }
-      if (mine) Vec8<T>::put(X.out + tok * X.out_tok + h * X.out_head + l * 8 * kValBytes, y);
+      in += kRopeAhead * in_step;
+      out += kRopeAhead * out_step;
+      left -= kRopeAhead * per_step;
     }
   }
 }
@@ -222,8 +287,7 @@ extern "C" int kvpool_qk_norm_rope(int32_t dtype, int32_t head_dim, int64_t n_to
   const kvpool_heads* out[2] = {q_out, k_out};
   const float* wt[2] = {d_q_weight, d_k_weight};
   RopeParams P{};
-  int group = 1;
-  while (group * 8 < head_dim) group *= 2;
+  const int group = head_dim <= 64 ? 8 : head_dim <= 128 ? 16 : 32;  // lanes of a head
   const int per_step = 32 / group;
   const int64_t vb = dtype == KVPOOL_BF16 ? 2 : 4;
   for (int i = 0; i < 2; ++i) {
@@ -231,6 +295,7 @@ extern "C" int kvpool_qk_norm_rope(int32_t dtype, int32_t head_dim, int64_t n_to
     if (in[i]->heads < 0 || in[i]->heads > 65536 || !out[i] || out[i]->heads != in[i]->heads)
       return KVPOOL_ERR_INVALID_ARG;
     if (n_tokens > 0 && (!in[i]->data || !out[i]->data)) return KVPOOL_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(wt[i]) % 16 != 0) return KVPOOL_ERR_INVALID_ARG;
     if (!heads_ok(in[i], dtype) || !heads_ok(out[i], dtype)) return KVPOOL_ERR_INVALID_ARG;
     RopeTensor& X = P.t[i];
     X.in = static_cast<const uint8_t*>(in[i]->data);
@@ -249,11 +314,8 @@ extern "C" int kvpool_qk_norm_rope(int32_t dtype, int32_t head_dim, int64_t n_to
   P.pos = d_positions;
   P.table = d_table;
   P.n_tokens = n_tokens;
-  P.head_dim = head_dim;
   P.rot_dim = rot_dim;
   P.lanes = head_dim / 8;
-  P.group = group;
-  P.interleaved = interleaved;
   P.eps = eps;
   P.inv_dim = 1.0f / (float)head_dim;
   // warps per token: one takes all its heads (its angles are worked out once)
@@ -267,12 +329,17 @@ extern "C" int kvpool_qk_norm_rope(int32_t dtype, int32_t head_dim, int64_t n_to
   if (ctas > 0x7FFFFFFF) return KVPOOL_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const dim3 grid((unsigned)ctas), block(kRopeWarps * 32);
-  cudaError_t e;
-  if (dtype == KVPOOL_BF16)
-    e = interleaved ? launch_kernel(true, rope_kernel<KVPOOL_BF16, true>, grid, block, 0, s, P)
-                    : launch_kernel(true, rope_kernel<KVPOOL_BF16, false>, grid, block, 0, s, P);
-  else
-    e = interleaved ? launch_kernel(true, rope_kernel<KVPOOL_F32, true>, grid, block, 0, s, P)
-                    : launch_kernel(true, rope_kernel<KVPOOL_F32, false>, grid, block, 0, s, P);
+  auto go = [&](auto t, auto inter) {
+    constexpr int T = decltype(t)::value;
+    constexpr bool I = decltype(inter)::value;
+    return group == 8    ? launch_kernel(true, rope_kernel<T, I, 8>, grid, block, 0, s, P)
+           : group == 16 ? launch_kernel(true, rope_kernel<T, I, 16>, grid, block, 0, s, P)
+                         : launch_kernel(true, rope_kernel<T, I, 32>, grid, block, 0, s, P);
+  };
+  auto types = [&](auto inter) {
+    return dtype == KVPOOL_BF16 ? go(std::integral_constant<int, KVPOOL_BF16>(), inter)
+                                : go(std::integral_constant<int, KVPOOL_F32>(), inter);
+  };
+  const cudaError_t e = interleaved ? types(std::true_type()) : types(std::false_type());
   return e == cudaSuccess ? KVPOOL_OK : KVPOOL_ERR_CUDA;
 }

@@ -11,6 +11,7 @@
 #include <cmath>
 #include <cstddef>
 #include <memory>
+#include <mutex>
 #include <new>
 
 #include <cuda_runtime.h>
@@ -304,11 +305,30 @@ void fill_params(const kvpool_window_args* a, WinParams* P) {
 
 int64_t slot_bytes(const WinParams& P, int head_dim) { return (int64_t)P.tile_rows * (head_dim + 2) * 4; }
 
-int device_sms() {
-  int dev = 0, v = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 0;
-  return v;
+// What a call needs to know of the current device, looked up once for each:
+// its multiprocessors and the address of the error word.
+constexpr int kMaxDevices = 64;
+struct DeviceInfo {
+  int sms;
+  uint32_t* err;
+};
+const DeviceInfo* device_info() {
+  static std::mutex mu;
+  static DeviceInfo info[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
+  std::lock_guard<std::mutex> lock(mu);
+  DeviceInfo& d = info[dev];
+  if (!d.err) {
+    void* p = nullptr;
+    int sms = 0;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1 ||
+        cudaGetSymbolAddress(&p, g_ops_error) != cudaSuccess || !p)
+      return nullptr;
+    d.sms = sms;
+    d.err = static_cast<uint32_t*>(p);
+  }
+  return &d;
 }
 
 template <int T, int D>
@@ -334,8 +354,9 @@ extern "C" int64_t kvpool_window_workspace(const kvpool_window_args* a, int32_t 
   const int rc = check_args(a, n, h_q_len, h_k_start, h_k_len, &total);
   if (rc != KVPOOL_OK) return rc;
   if (total == 0) return 0;
-  const int sms = device_sms();
-  if (sms <= 0) return KVPOOL_ERR_CUDA;
+  const DeviceInfo* dev = device_info();
+  if (!dev) return KVPOOL_ERR_CUDA;
+  const int sms = dev->sms;
   std::unique_ptr<WinParams> P(new (std::nothrow) WinParams);
   if (!P) return KVPOOL_ERR_INVALID_ARG;
   fill_params(a, P.get());
@@ -362,13 +383,13 @@ extern "C" int kvpool_window_attend(const kvpool_window_args* a, int32_t n, cons
   if (need < 0) return (int)need;
   if (need > 0 && (!d_workspace || workspace_bytes < need || reinterpret_cast<uintptr_t>(d_workspace) % 16 != 0))
     return KVPOOL_ERR_INVALID_ARG;
-  const int sms = device_sms();
+  const DeviceInfo* dev = device_info();
+  if (!dev) return KVPOOL_ERR_CUDA;
+  const int sms = dev->sms;
   std::unique_ptr<WinParams> P(new (std::nothrow) WinParams);
   if (!P) return KVPOOL_ERR_INVALID_ARG;
   fill_params(a, P.get());
-  uint32_t* err = nullptr;
-  if (cudaGetSymbolAddress(reinterpret_cast<void**>(&err), g_ops_error) != cudaSuccess) return KVPOOL_ERR_CUDA;
-  P->err = err;
+  P->err = dev->err;
   const bool tc = tc_able(a);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   for (int f = 0; f < kForms; ++f)
@@ -398,8 +419,9 @@ extern "C" int kvpool_window_attend(const kvpool_window_args* a, int32_t n, cons
 extern "C" int kvpool_window_check(void* stream, uint32_t* h_flags) {
   using namespace kvp;
   uint32_t word = 0;
-  void* err = nullptr;
-  if (cudaGetSymbolAddress(&err, g_ops_error) != cudaSuccess) return KVPOOL_ERR_CUDA;
+  const DeviceInfo* dev = device_info();
+  if (!dev) return KVPOOL_ERR_CUDA;
+  uint32_t* err = dev->err;
   const uint32_t zero = 0;
   if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess ||
       cudaMemcpy(&word, err, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess ||

@@ -408,7 +408,7 @@ int kvpool_rope_table(int32_t rot_dim, const double* h_inv_freq, uint64_t* h_tab
  * 256; rot_dim: a multiple of 16 up to head_dim (0: norms only, no table or
  * positions needed).  q or k may be NULL or have no heads.  An output may be
  * its own input (same data and strides); otherwise they must not overlap.
- * Weights: [head_dim] fp32 or NULL (ones).  d_positions: [n_tokens], any sign
+ * Weights: [head_dim] fp32, 16-byte aligned, or NULL (ones).  d_positions: [n_tokens], any sign
  * and size.  Errors: INVALID_ARG, CUDA. */
 int kvpool_qk_norm_rope(int32_t dtype, int32_t head_dim, int64_t n_tokens, const kvpool_heads* q,
                         const kvpool_heads* k, const kvpool_heads* q_out, const kvpool_heads* k_out,
