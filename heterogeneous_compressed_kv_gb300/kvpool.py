@@ -218,9 +218,9 @@ def _ptr(t) -> Optional[int]:
 
 
 def _stream(stream) -> Optional[int]:
-    if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:  # the current device's current stream
+        from torch import _C
+        return _C._cuda_getCurrentRawStream(_C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -259,28 +259,43 @@ def _rows(t, what: str, like=None, out: bool = False) -> tuple:
     shape = t.shape
     if len(shape) != 3 or not t.is_cuda:
         raise ValueError(f"{what} must be a [tokens][heads][dim] CUDA tensor")
-    if like is not None and (t.dtype is not like.dtype or shape[2] != like.shape[2] or t.device != like.device):
-        raise ValueError(f"{what} must have the type, device and head dim of the other tensors")
+    n, heads, dim = shape
+    size = 2
+    if like is not None:
+        if t.dtype is not like[0] or dim != like[1] or t.get_device() != like[2]:
+            raise ValueError(f"{what} must have the type, head dim and device of the other tensors")
+        size = like[3]
     ts, hs, vs = t.stride()
     # the stride of an axis of length 1 is never used
-    ts, hs = ts if shape[0] > 1 else 0, hs if shape[1] > 1 else 0
+    if n <= 1:
+        ts = 0
+    if heads <= 1:
+        hs = 0
     ptr = t.data_ptr()
-    if (ptr | ts * t.element_size() | hs * t.element_size()) & 15 and t.numel() or vs != 1 and shape[2] > 1:
+    if (ptr | ts * size | hs * size) & 15 and n * heads * dim or vs != 1 and dim > 1:
         raise ValueError(f"{what}: a head's values must be adjacent, data and strides whole multiples of 16 bytes")
-    if out and (shape[0] > 1 and ts < shape[2] or shape[1] > 1 and hs < shape[2]):
+    if out and (n > 1 and ts < dim or heads > 1 and hs < dim):
         raise ValueError(f"{what}: two values share a place")
-    return ptr, ts, hs, shape[1], 0
+    return ptr, ts, hs, heads, 0
+
+
+def _like(t) -> tuple:
+    """What _rows compares the other tensors of a call with."""
+    return t.dtype, t.shape[-1], t.get_device(), t.element_size()
 
 
 class _on:
-    """The tensors' device as the current one, entered only where it is not."""
+    """A device as the current one."""
 
     def __init__(self, index: int):
-        import torch
-        self.ctx = None if torch.cuda.current_device() == index else torch.cuda.device(index)
+        self.index = index
 
     def __enter__(self):
-        if self.ctx is not None:
+        from torch import _C
+        self.ctx = None
+        if _C._cuda_getDevice() != self.index:
+            import torch
+            self.ctx = torch.cuda.device(self.index)
             self.ctx.__enter__()
 
     def __exit__(self, *e):
@@ -291,8 +306,8 @@ class _on:
 def _stream_of(stream, index: int) -> int:
     """The given stream, or the device's current one."""
     if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(index)
+        from torch import _C
+        return _C._cuda_getCurrentRawStream(index)
     return _stream(stream)
 
 
@@ -305,9 +320,11 @@ def _empty(shape, dtype, device, stream, raw: int):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _need(t, what: str, dtype, shape, device):
-    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+def _need(t, what: str, dtype, shape, index: int) -> int:
+    """The address of a contiguous tensor of that type and shape on that device."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{index}")
+    return t.data_ptr()
 
 
 def _i64(x) -> np.ndarray:
@@ -347,34 +364,33 @@ def qk_norm_rope(q, k, positions, table, q_weight=None, k_weight=None, eps: floa
     x = q if q is not None else k
     if x is None or not x.is_cuda:
         raise ValueError("qk_norm_rope: q or k must be a CUDA tensor")
-    dev, kind = x.device, _dtype(x)
-    with _on(dev.index):
-        raw = _stream_of(stream, dev.index)
+    kind, like, dev = _dtype(x), _like(x), x.device
+    index = like[2]
+    with _on(index):
+        raw = _stream_of(stream, index)
         heads, outs = [None] * 4, [None, None]
         for i, (t, o) in enumerate(((q, out_q), (k, out_k))):
             if t is None:
                 continue
-            heads[i] = _HEADS.pack(*_rows(t, "qk"[i], x))
+            heads[i] = _HEADS.pack(*_rows(t, "qk"[i], like))
             if t.shape[0] != x.shape[0]:
                 raise ValueError("qk_norm_rope: q and k must have the same tokens")
             if o is None:
                 o = _empty(t.shape, t.dtype, dev, stream, raw)
             elif o.shape != t.shape:
                 raise ValueError(f"qk_norm_rope: out_{'qk'[i]} must have the shape of {'qk'[i]}")
-            heads[2 + i] = _HEADS.pack(*_rows(o, "out_" + "qk"[i], x, True))
+            heads[2 + i] = _HEADS.pack(*_rows(o, "out_" + "qk"[i], like, True))
             outs[i] = o
         T, _, D = x.shape
-        rot = 0
+        rot = tab = pos = 0
         if table is not None:
             rot = 2 * table.numel()
-            _need(table, "table", torch.int64, (rot // 2,), dev)
-            _need(positions, "positions", torch.int64, (T,), dev)
-        for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-            if w is not None:
-                _need(w, what, torch.float32, (D,), dev)
-        rc = lib().kvpool_qk_norm_rope(kind, D, T, *heads, _ptr(q_weight), _ptr(k_weight), eps, rot,
-                                       1 if interleaved else 0, _ptr(table) if rot else None,
-                                       _ptr(positions) if rot else None, raw)
+            tab = _need(table, "table", torch.int64, (rot // 2,), index)
+            pos = _need(positions, "positions", torch.int64, (T,), index)
+        qw = None if q_weight is None else _need(q_weight, "q_weight", torch.float32, (D,), index)
+        kw = None if k_weight is None else _need(k_weight, "k_weight", torch.float32, (D,), index)
+        rc = lib().kvpool_qk_norm_rope(kind, D, T, *heads, qw, kw, eps, rot, 1 if interleaved else 0, tab or None,
+                                       pos or None, raw)
     if rc != OK:
         raise KvpoolError(rc, "qk_norm_rope refused its arguments" if rc == ERR_INVALID_ARG else "qk_norm_rope: CUDA error")
     return outs[0], outs[1]
@@ -436,17 +452,18 @@ def _window_call(q, k, v, q_len, k_start, k_len, window, n_sink, scale, out, lse
     """(args, n, lengths) as kvpool_window_attend takes them, and what must outlive the call."""
     if k.shape != v.shape or out.shape != q.shape:
         raise ValueError("window_attend: k and v, and q and out, must have the same shape")
+    z = 0
     if lse is not None:
         import torch
-        _need(lse, "lse", torch.float32, q.shape[:2], q.device)
+        z = _need(lse, "lse", torch.float32, q.shape[:2], q.get_device())
     ql, ks, kl = _i64(q_len), _i64(k_start), _i64(k_len)
     if not ql.size == ks.size == kl.size:
         raise ValueError("window_attend: q_len, k_start and k_len must have one value per segment")
-    rows, _, D = q.shape
+    rows, D, like = q.shape[0], q.shape[-1], _like(q)
     try:
-        a = _WINDOW_ARGS.pack(_dtype(q), D, *_rows(q, "q"), *_rows(k, "k", q), *_rows(v, "v", q),
-                              *_rows(out, "out", q, out is not q), rows, k.shape[0], 0 if lse is None else lse.data_ptr(), window,
-                              n_sink, D ** -0.5 if scale is None else scale, 0)
+        a = _WINDOW_ARGS.pack(_dtype(q), D, *_rows(q, "q", like), *_rows(k, "k", like), *_rows(v, "v", like),
+                              *_rows(out, "out", like, out is not q), rows, k.shape[0], z, window, n_sink,
+                              D ** -0.5 if scale is None else scale, 0)
     except (struct.error, OverflowError) as e:
         raise ValueError(f"window_attend: {e}") from None
     return (a, ql.size, ql.ctypes.data, ks.ctypes.data, kl.ctypes.data), (ql, ks, kl)
