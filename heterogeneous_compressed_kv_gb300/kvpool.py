@@ -412,7 +412,7 @@ def window_attend(q, k, v, q_len, k_start, k_len, window: int, n_sink: int = 0, 
         raw = _stream_of(stream, dev.index)
         if out is None:
             out = _empty(q.shape, q.dtype, dev, stream, raw)
-        call, keep = _window_call(q, k, v, q_len, k_start, k_len, window, n_sink, scale, out, lse)
+        call = _window_call(q, k, v, q_len, k_start, k_len, window, n_sink, scale, out, lse)
         L = lib()
         rc = L.kvpool_window_workspace(*call)
         if rc >= 0:
@@ -433,7 +433,7 @@ def window_attend(q, k, v, q_len, k_start, k_len, window: int, n_sink: int = 0, 
 def window_workspace(q, k, v, q_len, k_start, k_len, window: int, n_sink: int = 0) -> int:
     """Workspace bytes of window_attend with these arguments."""
     with _on(q.device.index):
-        call, keep = _window_call(q, k, v, q_len, k_start, k_len, window, n_sink, None, q, None)
+        call = _window_call(q, k, v, q_len, k_start, k_len, window, n_sink, None, q, None)
         rc = int(lib().kvpool_window_workspace(*call))
     if rc < 0:
         raise KvpoolError(rc, "window_workspace refused its arguments")
@@ -449,7 +449,7 @@ def window_check(stream=None) -> tuple:
 
 
 def _window_call(q, k, v, q_len, k_start, k_len, window, n_sink, scale, out, lse):
-    """(args, n, lengths) as kvpool_window_attend takes them, and what must outlive the call."""
+    """(args, n, lengths) as kvpool_window_attend takes them (copies in bytes objects: quicker than array addresses)."""
     if k.shape != v.shape or out.shape != q.shape:
         raise ValueError("window_attend: k and v, and q and out, must have the same shape")
     z = 0
@@ -466,7 +466,7 @@ def _window_call(q, k, v, q_len, k_start, k_len, window, n_sink, scale, out, lse
                               D ** -0.5 if scale is None else scale, 0)
     except (struct.error, OverflowError) as e:
         raise ValueError(f"window_attend: {e}") from None
-    return (a, ql.size, ql.ctypes.data, ks.ctypes.data, kl.ctypes.data), (ql, ks, kl)
+    return a, ql.size, ql.tobytes(), ks.tobytes(), kl.tobytes()
 
 
 class Pool:
