@@ -38,7 +38,7 @@ constexpr float kRescale = 8.0f;  // log2 growth of the maximum that rescales O
 template <int D>
 struct TcShape {
   static constexpr int kTileBytes = 128 * D * 2;  // a Q, K or V tile: D / 64 runs of 128 rows x 128 bytes
-  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kStages = D == 128 ? 4 : 8;
   static constexpr int kBarOff = (2 + kStages) * kTileBytes;
   static constexpr int kSmem = kBarOff + 512 + 1024;  // + slack to align the tiles to 1,024 bytes
 };
