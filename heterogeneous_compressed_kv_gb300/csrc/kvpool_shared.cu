@@ -16,30 +16,12 @@
 #include "kvpool_fma.cuh"
 #include "kvpool_internal.h"
 #include "kvpool_mma.cuh"
+#include "kvpool_shared.h"
 
 namespace kvp {
 namespace {
 
 constexpr int kSharedRows = 64;  // requests of a CTA
-
-struct SharedShape {
-  int32_t n_entries, n_split, slot;  // slot: the request whose table holds the shared ids
-};
-
-__device__ __forceinline__ const uint8_t* shared_entry(const AttendParams& P, const SharedShape& H, int e) {
-  const PoolDesc& pd = P.pool;
-  int32_t b = reinterpret_cast<const int32_t*>(pd.arena + pd.table)[(int64_t)H.slot * pd.max_bpr + e];
-  if (b < 0 || b >= pd.max_blocks) {
-    flag_error(pd, kErrBadBlock);
-    b = 0;
-  }
-  return pd.arena + P.layer.hca_pool + (int64_t)b * P.layer.hca_stride;
-}
-
-__device__ __forceinline__ int64_t shared_slot(const AttendParams& P, int i, int split) {
-  const AttendReq& R = P.reqs[i];
-  return R.part_base + R.n_split0 + R.n_split1 + split;
-}
 
 // 4 values of a row of codes in fp32 (fp8: without the scale)
 template <int T>
@@ -87,7 +69,7 @@ __global__ void __launch_bounds__(kFmaThreads) shared_fma_kernel(const __grid_co
       const int r = i / (D / 4), c = 4 * (i % (D / 4));
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
       if (e0 + r < b) {
-        const uint8_t* ent = shared_entry(P, H, e0 + r);
+        const uint8_t* ent = shared_entry(P, shared_id(P, H, e0 + r));
         x = codes4<CACHE>(ent + h * D * pd.vs, c);
         y = codes4<CACHE>(ent + (pd.HD + h * D) * pd.vs, c);
         if (CACHE == KVPOOL_FP8_E4M3 && c == 0) {
@@ -187,14 +169,22 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 1) shared_mma_kernel(const __g
   // four threads copy an entry: pieces tid % 4, + 4, ... of its K and V
   const int n_st = (b - a + kMmaKeys - 1) / kMmaKeys;
   const int ce = tid >> 2, cu = tid & 3;
-  auto copy = [&](int st) {
-    if (st < n_st)
+  // their block ids are asked for a stage ahead; entries behind the end repeat
+  // the last one (masked below)
+  int32_t next[2];
+  auto look_up = [&](int st) {
 #pragma unroll
-      for (int x = 0; x < kMmaKeys; x += 64) {
-        const int e = a + st * kMmaKeys + x + ce;
-        // entries behind the end repeat the last one (masked below)
-        const uint8_t* src = shared_entry(P, H, min(e, b - 1)) + h * D * 2;
-        const uint32_t dst = base + (st % kMmaStages) * 2 * kTile + (x + ce) * D * 2;
+    for (int x = 0; x < 2; ++x) next[x] = shared_id(P, H, min(a + st * kMmaKeys + 64 * x + ce, b - 1));
+  };
+  look_up(0);
+  auto copy = [&](int st) {
+    if (st < n_st) {
+      const int32_t id[2] = {next[0], next[1]};
+      if (st + 1 < n_st) look_up(st + 1);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const uint8_t* src = shared_entry(P, id[x]) + h * D * 2;
+        const uint32_t dst = base + (st % kMmaStages) * 2 * kTile + (64 * x + ce) * D * 2;
 #pragma unroll
         for (int u = 0; u < U; u += 4) {
           const uint32_t at = shared_piece(ce, u + cu) * 16;
@@ -202,6 +192,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 1) shared_mma_kernel(const __g
           cp_async16(dst + kTile + at, src + pd.HD * 2 + (u + cu) * 16);
         }
       }
+    }
     cp_async_commit();
   };
   for (int st = 0; st < kMmaStages - 1; ++st) copy(st);
@@ -392,12 +383,23 @@ cudaError_t launch_shared_d(const AttendParams& p, const SharedShape& h, cudaStr
 
 }  // namespace
 
+// bf16 on the 5th-generation tensor cores or on the small products?  The
+// former read an entry once for up to 128 requests and need a tile of 128
+// entries to get going; measured as whole steps of 16 heads x 128 (small
+// products / 5th generation, us):
+//   entries     32 requests    64 requests    128 requests
+//   1,024       18.2 / 21.7    26.9 / 28.6    40.4 / 43.4
+//   4,096       26.0 / 27.5    37.8 / 33.4    64.8 / 48.9
+//   8,192       36.2 / 35.4    52.9 / 41.6    96.7 / 58.4
+bool shared_tc(int n, int n_entries) { return n > 32 && n_entries >= 2048; }
+
 // Splits of the shared entries for n requests: CTAs (head, split, 64
 // requests) that fill the GPU (the FMA form: twice over), of at least 64
 // entries each.
 int shared_splits(const PoolDesc& pd, int n, int n_entries, int n_sms) {
-  const int per = pd.heads * ((n + kSharedRows - 1) / kSharedRows);
   const bool mma = pd.in_dtype == KVPOOL_BF16 && pd.cache_dtype == KVPOOL_BF16;
+  const int rows = mma && shared_tc(n, n_entries) ? kSharedTcRows : kSharedRows;
+  const int per = pd.heads * ((n + rows - 1) / rows);
   return std::max(1, std::min(mma ? n_sms / per : (2 * n_sms + per - 1) / per, (n_entries + 63) / 64));
 }
 
@@ -411,7 +413,9 @@ int launch_shared(const AttendParams& p, int n_entries, int n_split, void* strea
     case KVPOOL_F32 * 3 + KVPOOL_FP8_E4M3: return (int)launch_shared_d<KVPOOL_F32, KVPOOL_FP8_E4M3>(p, h, s);
     case KVPOOL_BF16 * 3 + KVPOOL_F32: return (int)launch_shared_d<KVPOOL_BF16, KVPOOL_F32>(p, h, s);
     case KVPOOL_BF16 * 3 + KVPOOL_BF16:
-      return (int)(p.pool.head_dim == 128 ? launch_mma<128>(p, h, s) : launch_mma<64>(p, h, s));
+      return (int)(shared_tc(p.n, n_entries) ? launch_shared_tc(p, h, s)
+                   : p.pool.head_dim == 128 ? launch_mma<128>(p, h, s)
+                                            : launch_mma<64>(p, h, s));
     case KVPOOL_BF16 * 3 + KVPOOL_FP8_E4M3: return (int)launch_shared_d<KVPOOL_BF16, KVPOOL_FP8_E4M3>(p, h, s);
     default: return (int)cudaErrorInvalidValue;
   }

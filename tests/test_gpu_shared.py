@@ -98,6 +98,40 @@ def test_sizes_of_batch_and_prefix(n, prefix, types):
     close(out, ref, *types[::-1])
 
 
+@pytest.mark.parametrize("n,entries,heads,dim", [(33, 2048, 4, 64), (64, 2049, 2, 128), (129, 2300, 4, 64), (40, 2175, 16, 128)])
+def test_many_entries_and_requests(n, entries, heads, dim):
+    """Enough of both for the products of 128 rows: whole and ragged tiles, one and two of them, few and many splits."""
+    w = dict(BASE, heads=heads, head_dim=dim)
+    g, _, slots = build(w, n, 128 * entries, [(i * 37) % 200 for i in range(n)], oracle=False)
+    out, ref = attend(g, 0, slots, list(range(n)), 0, 128 * entries)
+    close(out, ref, K.BF16, K.BF16)
+    assert torch.equal(out, attend(g, 0, slots, list(range(n)), 0, 128 * entries)[0])
+
+
+def test_growing_scores_rescale_the_outputs():
+    """Entries whose scores grow along the prefix, so that every row's maximum grows by more than a rescaling's step
+    again and again."""
+    w = dict(BASE, heads=4, head_dim=64)
+    n, entries = 40, 2048
+    blocks = entries + 8
+    g = GpuCase(w, n, blocks, entries + 2, n, 4)
+    slots = [g.pool.alloc_request() for _ in range(n)]
+    q = torch.ones((n, g.HD), device="cuda", dtype=torch.bfloat16)
+    for p0 in range(0, 128 * entries, 2048):
+        t = torch.arange(p0, p0 + 2048, device="cuda", dtype=torch.float32)
+        k = (t / 40000)[:, None].expand(2048, g.HD).to(torch.bfloat16).contiguous()  # scores up to 64 * 6.5 / 8 = 52
+        v = torch.randn((2048, g.HD), device="cuda").to(torch.bfloat16)
+        g.pool.append([slots[0]], [2048], k, v, None)
+    for s in slots[1:]:
+        g.pool.share_prefix(s, slots[0], 128 * entries, k[-128:].contiguous(), v[-128:].contiguous())
+    out, ref = torch.empty((n, g.HD), device="cuda"), torch.empty((n, g.HD), device="cuda")
+    g.pool.decode_attend_shared(0, slots, 128 * entries, q, None, 0, out)
+    g.pool.decode_attend(0, slots, q, None, 0, ref)
+    assert g.pool.check_device() == 0
+    # scores of 52 are off by at most 2 * 68 * 2^-24 * 64 * 6.5 / 8: 2^-11 in the worst weight, far less in their sum
+    assert float((out - ref).norm() / ref.norm()) <= 2.0 ** -13
+
+
 def test_more_requests_than_one_launch():
     w = dict(BASE, heads=4, head_dim=64)
     g, _, slots = build(w, 300, 256, [i % 3 for i in range(300)], oracle=False)
