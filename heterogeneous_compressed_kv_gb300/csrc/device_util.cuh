@@ -227,6 +227,18 @@ __device__ __forceinline__ void bulk_g2s_stream(void* dst, const void* src, uint
 }
 
 // ---------------------------------------------------------------------------
+// asynchronous copies by thread (16 bytes each; zeros where `bytes` is 0)
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes = 16) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// ---------------------------------------------------------------------------
 // streaming loads
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ uint4 ld_stream16(const void* p) {

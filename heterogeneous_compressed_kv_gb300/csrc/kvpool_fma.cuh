@@ -17,8 +17,8 @@ constexpr int kFmaRows = 64, kFmaKeys = 32, kFmaThreads = 256;
 template <int D>
 struct FmaSmem {
   float q[kFmaRows][D + 4];
-  float k[kFmaKeys][D + 4];
-  float v[kFmaKeys][D];
+  float k[2][kFmaKeys][D + 4];  // two buffers
+  float v[2][kFmaKeys][D];
   float p[kFmaRows][kFmaKeys + 4];
 };
 
@@ -43,14 +43,14 @@ struct FmaTile {
   // scores of the staged keys times ks(key), masked by see(row of the thread,
   // key of the step); weights times vs(key) for the values
   template <class See, class KScale, class VScale>
-  __device__ __forceinline__ void step(FmaSmem<D>& sm, int ty, int tx, See see, KScale ks, VScale vs) {
+  __device__ __forceinline__ void step(FmaSmem<D>& sm, int buf, int ty, int tx, See see, KScale ks, VScale vs) {
     float s[4][2];
 #pragma unroll
     for (int r = 0; r < 4; ++r) s[r][0] = s[r][1] = 0.0f;
 #pragma unroll 4
     for (int c = 0; c < D; c += 4) {
-      const float4 k0 = *reinterpret_cast<const float4*>(&sm.k[tx][c]);
-      const float4 k1 = *reinterpret_cast<const float4*>(&sm.k[tx + 16][c]);
+      const float4 k0 = *reinterpret_cast<const float4*>(&sm.k[buf][tx][c]);
+      const float4 k1 = *reinterpret_cast<const float4*>(&sm.k[buf][tx + 16][c]);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const float4 x = *reinterpret_cast<const float4*>(&sm.q[4 * ty + r][c]);
@@ -93,7 +93,7 @@ struct FmaTile {
       for (int jj = 0; jj < 4; ++jj)
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
-          const float4 y = *reinterpret_cast<const float4*>(&sm.v[j + jj][64 * c + 4 * tx]);
+          const float4 y = *reinterpret_cast<const float4*>(&sm.v[buf][j + jj][64 * c + 4 * tx]);
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             o[r][4 * c] = fmaf(p[r][jj], y.x, o[r][4 * c]);

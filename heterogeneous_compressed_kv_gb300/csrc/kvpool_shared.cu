@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(kFmaThreads) shared_fma_kernel(const __grid_co
   pdl_start();
   extern __shared__ __align__(16) uint8_t smem_raw[];
   FmaSmem<D>& sm = *reinterpret_cast<FmaSmem<D>*>(smem_raw);
-  __shared__ float scales[2][kFmaKeys];
+  __shared__ float scales[2][2][kFmaKeys];
   const PoolDesc& pd = P.pool;
   const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
   const int h = blockIdx.x, split = blockIdx.y, i0 = blockIdx.z * kSharedRows;
@@ -63,30 +63,49 @@ __global__ void __launch_bounds__(kFmaThreads) shared_fma_kernel(const __grid_co
   }
   FmaTile<D> t;
   t.init();
-  for (int e0 = a; e0 < b; e0 += kFmaKeys) {
-    __syncthreads();
+  // a step's entries go to one buffer while the other is worked on; fp32 rows
+  // by asynchronous copies
+  auto load = [&](int e0, int buf) {
     for (int i = tid; i < kFmaKeys * (D / 4); i += kFmaThreads) {
       const int r = i / (D / 4), c = 4 * (i % (D / 4));
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-      if (e0 + r < b) {
-        const uint8_t* ent = shared_entry(P, shared_id(P, H, e0 + r));
-        x = codes4<CACHE>(ent + h * D * pd.vs, c);
-        y = codes4<CACHE>(ent + (pd.HD + h * D) * pd.vs, c);
-        if (CACHE == KVPOOL_FP8_E4M3 && c == 0) {
-          const uint32_t s2 = *reinterpret_cast<const uint32_t*>(ent + 2 * pd.HD);
-          scales[0][r] = qscale * __uint_as_float(s2 << 16);
-          scales[1][r] = __uint_as_float(s2 & 0xFFFF0000u);
+      const bool in = e0 + r < b;
+      const uint8_t* ent = in ? shared_entry(P, shared_id(P, H, e0 + r)) : pd.arena;
+      const uint8_t* kr = ent + h * D * pd.vs;
+      if constexpr (CACHE == KVPOOL_F32) {
+        cp_async16(smem_addr(&sm.k[buf][r][c]), in ? kr + 4 * c : ent, in ? 16 : 0);
+        cp_async16(smem_addr(&sm.v[buf][r][c]), in ? kr + 4 * (pd.HD + c) : ent, in ? 16 : 0);
+      } else {
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+        if (in) {
+          x = codes4<CACHE>(kr, c);
+          y = codes4<CACHE>(kr + pd.HD * pd.vs, c);
+          if (CACHE == KVPOOL_FP8_E4M3 && c == 0) {
+            const uint32_t s2 = *reinterpret_cast<const uint32_t*>(ent + 2 * pd.HD);
+            scales[buf][0][r] = qscale * __uint_as_float(s2 << 16);
+            scales[buf][1][r] = __uint_as_float(s2 & 0xFFFF0000u);
+          }
         }
+        *reinterpret_cast<float4*>(&sm.k[buf][r][c]) = x;
+        *reinterpret_cast<float4*>(&sm.v[buf][r][c]) = y;
       }
-      *reinterpret_cast<float4*>(&sm.k[r][c]) = x;
-      *reinterpret_cast<float4*>(&sm.v[r][c]) = y;
+    }
+    cp_async_commit();
+  };
+  load(a, 0);
+  for (int e0 = a, buf = 0; e0 < b; e0 += kFmaKeys, buf ^= 1) {
+    if (e0 + kFmaKeys < b) {
+      load(e0 + kFmaKeys, buf ^ 1);
+      cp_async_wait<1>();
+    } else {
+      cp_async_wait<0>();
     }
     __syncthreads();
     const int n = b - e0;
     t.step(
-        sm, ty, tx, [&](int, int j) { return j < n; },
-        [&](int j) { return CACHE != KVPOOL_FP8_E4M3 ? qscale : j < n ? scales[0][j] : 0.0f; },
-        [&](int j) { return CACHE != KVPOOL_FP8_E4M3 ? 1.0f : j < n ? scales[1][j] : 0.0f; });
+        sm, buf, ty, tx, [&](int, int j) { return j < n; },
+        [&](int j) { return CACHE != KVPOOL_FP8_E4M3 ? qscale : j < n ? scales[buf][0][j] : 0.0f; },
+        [&](int j) { return CACHE != KVPOOL_FP8_E4M3 ? 1.0f : j < n ? scales[buf][1][j] : 0.0f; });
+    __syncthreads();
   }
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
@@ -122,14 +141,6 @@ struct MmaShared {
 // four pieces, four rows two apart x two pieces) meet eight different banks
 __device__ __forceinline__ int shared_piece(int r, int u) { return u ^ (r & 6) ^ ((r & 1) << 2); }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ uint4 lds16(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));

@@ -40,15 +40,6 @@ struct Shape {
   static_assert(kLag < kStages, "a tile is announced before the ring needs its stage");
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // tiles go out as K0 K1 V0 K2 V1 ... K(n-1) V(n-2) V(n-1): the order of their use
 __device__ __forceinline__ bool tile_is_k(int i, int n, int& j) {
   if (i == 0 || n == 1) {

@@ -72,28 +72,51 @@ __global__ void __launch_bounds__(kFmaThreads) window_fma_kernel(const __grid_co
   const int st_s = (w.n_s + kFmaKeys - 1) / kFmaKeys, st_w = (w.n_w + kFmaKeys - 1) / kFmaKeys;
   const int n_st = st_s + st_w;
   const int a = (int)((int64_t)n_st * w.split / w.n_split), b = (int)((int64_t)n_st * (w.split + 1) / w.n_split);
-  for (int st = a; st < b; ++st) {
+  struct Step {
+    int t0, end;  // tokens from `end` on are nobody's: read as zeros
+    bool sink;
+  };
+  auto step_of = [&](int st) {
     const bool sink = st < st_s;
-    const int t0 = sink ? st * kFmaKeys : w.lo + (st - st_s) * kFmaKeys;
-    const int end = sink ? w.n_s : w.lo + w.n_w;  // tokens from here on are nobody's: read as zeros
-    __syncthreads();
+    return Step{sink ? st * kFmaKeys : w.lo + (st - st_s) * kFmaKeys, sink ? w.n_s : w.lo + w.n_w, sink};
+  };
+  // a step's rows go to one buffer while the other is worked on; fp32 rows by
+  // asynchronous copies
+  auto load = [&](int st, int buf) {
+    const Step c = step_of(st);
     for (int i = tid; i < kFmaKeys * (D / 4); i += kFmaThreads) {
-      const int r = i / (D / 4), c = 4 * (i % (D / 4));
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-      if (t0 + r < end) {
-        x = load4<T>(P.k, (S.k_start + t0 + r) * P.k_tok + w.hk * P.k_head + c);
-        y = load4<T>(P.v, (S.k_start + t0 + r) * P.v_tok + w.hk * P.v_head + c);
+      const int r = i / (D / 4), x = 4 * (i % (D / 4));
+      const bool in = c.t0 + r < c.end;
+      const int64_t ka = in ? (S.k_start + c.t0 + r) * P.k_tok + w.hk * P.k_head + x : 0;
+      const int64_t va = in ? (S.k_start + c.t0 + r) * P.v_tok + w.hk * P.v_head + x : 0;
+      if constexpr (T == KVPOOL_F32) {
+        cp_async16(smem_addr(&sm.k[buf][r][x]), P.k + 4 * ka, in ? 16 : 0);
+        cp_async16(smem_addr(&sm.v[buf][r][x]), P.v + 4 * va, in ? 16 : 0);
+      } else {
+        const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+        *reinterpret_cast<float4*>(&sm.k[buf][r][x]) = in ? load4<T>(P.k, ka) : zero;
+        *reinterpret_cast<float4*>(&sm.v[buf][r][x]) = in ? load4<T>(P.v, va) : zero;
       }
-      *reinterpret_cast<float4*>(&sm.k[r][c]) = x;
-      *reinterpret_cast<float4*>(&sm.v[r][c]) = y;
+    }
+    cp_async_commit();
+  };
+  if (a < b) load(a, 0);
+  for (int st = a, buf = 0; st < b; ++st, buf ^= 1) {
+    if (st + 1 < b) {
+      load(st + 1, buf ^ 1);
+      cp_async_wait<1>();
+    } else {
+      cp_async_wait<0>();
     }
     __syncthreads();
+    const Step c = step_of(st);
     f.step(
-        sm, ty, tx,
+        sm, buf, ty, tx,
         [&](int r, int j) {
-          return t0 + j < end && (sink ? pos[r] >= 0 : win_sees(P, pos[r], t0 + j));
+          return c.t0 + j < c.end && (c.sink ? pos[r] >= 0 : win_sees(P, pos[r], c.t0 + j));
         },
         [&](int) { return P.scale_log2; }, [](int) { return 1.0f; });
+    __syncthreads();
   }
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
@@ -121,15 +144,28 @@ __global__ void __launch_bounds__(kFmaThreads) window_fma_kernel(const __grid_co
 // ---- merge of the splits ------------------------------------------------------
 // One warp per row of a tile whose keys were split: out = sum_s 2^(m_s - M)
 // o_s / sum_s 2^(m_s - M) l_s, splits in order (the same sum on every run).
+constexpr int kMergeWarps = 8;
 template <int T, int D>
-__global__ void __launch_bounds__(128) window_merge_kernel(const __grid_constant__ WinParams P) {
+__global__ void __launch_bounds__(kMergeWarps * 32) window_merge_kernel(const __grid_constant__ WinParams P) {
   pdl_start();
   const int lane = threadIdx.x & 31;
-  const int row = blockIdx.y * 4 + (threadIdx.x >> 5);
-  // items of a split tile come in runs of n_split * kv_heads; the tile's
-  // first run (split 0) stands for it
-  const WinItem w = win_item(P, blockIdx.x);
-  if (w.n_split == 1 || w.split != 0 || row >= w.n_tok * P.group) return;
+  // blockIdx.x counts the (tile, key head)s of split segments
+  int seg = 0;
+  for (int lo = 0, hi = P.n_segs - 1; lo <= hi;) {  // the last segment whose first one is not behind it
+    const int mid = (lo + hi) >> 1;
+    if (P.segs[mid].merge_base <= (int)blockIdx.x) {
+      seg = mid;
+      lo = mid + 1;
+    } else {
+      hi = mid - 1;
+    }
+  }
+  const int tile_head = blockIdx.x - P.segs[seg].merge_base;
+  const int item = P.segs[seg].item_base + (tile_head / P.kv_heads) * P.segs[seg].n_split * P.kv_heads +
+                   tile_head % P.kv_heads;  // its first split
+  const WinItem w = win_item(P, item);
+  const int row = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
+  if (row >= w.n_tok * P.group) return;
   const WinSeg& S = P.segs[w.seg];
   constexpr int V = D / 32;
   float m = -INFINITY, l = 0.0f, acc[V];
@@ -261,7 +297,7 @@ int plan_launch(const kvpool_window_args* a, Form form, bool tc, int32_t i0, int
   *next_row = q_row0;
   const int64_t min_keys = form == kFormTok ? 256 : 128;
   const int64_t want = form == kFormTok ? 3LL * n_sms : form == kFormTc ? n_sms : 2LL * n_sms;  // work items
-  int64_t items = 0, slot = 0;
+  int64_t items = 0, slot = 0, merge = 0, rows = 0;
   for (int s = 0; s < P->n_segs; ++s) {
     WinSeg& S = P->segs[s];
     const int64_t st = (int64_t)((S.q_len + P->tile_tokens - 1) / P->tile_tokens) * Hk;
@@ -272,11 +308,18 @@ int plan_launch(const kvpool_window_args* a, Form form, bool tc, int32_t i0, int
                                (tile_keys(a, S.q_len, S.k_len, P->tile_tokens) + min_keys - 1) / min_keys));
     S.n_split = (int32_t)split;
     S.item_base = (int32_t)items;
-    S.part_base = (int32_t)(slot);
+    S.part_base = (int32_t)slot;
+    S.merge_base = (int32_t)merge;
     items += st * split;
-    if (split > 1) slot += st * split;
+    if (split > 1) {
+      slot += st * split;
+      merge += st;
+      rows = std::max<int64_t>(rows, std::min<int64_t>(S.q_len, P->tile_tokens) * P->group);
+    }
   }
   P->n_items = items <= (1 << 30) ? (int32_t)items : -1;
+  P->n_merge = (int32_t)merge;
+  P->merge_rows = (int32_t)rows;
   *slots = slot;
   return i;
 }
@@ -341,7 +384,8 @@ cudaError_t launch_fma(const WinParams& P, cudaStream_t s) {
 
 template <int T, int D>
 cudaError_t launch_merge(const WinParams& P, cudaStream_t s) {
-  return launch_kernel(true, window_merge_kernel<T, D>, dim3(P.n_items, (P.tile_rows + 3) / 4), dim3(128), 0, s, P);
+  return launch_kernel(true, window_merge_kernel<T, D>, dim3(P.n_merge, (P.merge_rows + kMergeWarps - 1) / kMergeWarps),
+                       dim3(kMergeWarps * 32), 0, s, P);
 }
 
 }  // namespace

@@ -19,7 +19,7 @@ struct WinSeg {
   int32_t item_base;  // first work item: ((tile * n_split + split) * kv_heads + head)
   int32_t n_split;    // parts that each tile's keys are cut into
   int32_t part_base;  // first partial slot (n_split > 1)
-  int32_t pad;
+  int32_t merge_base; // (tile, key head)s of the split segments before this one
 };
 
 struct WinParams {
@@ -34,6 +34,7 @@ struct WinParams {
   float scale_log2;  // softmax scale times log2(e)
   int32_t tile_tokens, tile_rows;
   int32_t n_segs, n_items;
+  int32_t n_merge, merge_rows;  // (tile, key head)s to merge, the most rows that one has
   float* part_o;    // [slots][tile_rows][head_dim]
   float2* part_ml;  // [slots][tile_rows]: (max in the log2 domain, sum)
   uint32_t* err;
