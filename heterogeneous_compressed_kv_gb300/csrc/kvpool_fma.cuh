@@ -1,5 +1,11 @@
-// kvpool_fma.cuh -- attention of a tile of 64 query rows over steps of 32 keys
+// kvpool_fma.cuh -- attention of a tile of 32 query rows over steps of 64 keys
 // in fp32 FMAs: the step that the fp32 forms of the attention kernels share.
+//
+// Bound by shared-memory loads beside the FMAs: a thread's 4 rows x 4 keys take
+// 8 16-byte loads per 64 FMAs.  Tiles are small (128 threads) so that several
+// CTAs share an SM: while one waits for its keys the others compute, which
+// takes less shared memory than a second buffer, and few rows still make many
+// tiles.
 #pragma once
 
 #include "device_util.cuh"
@@ -12,18 +18,18 @@ __device__ __forceinline__ float ex2f(float x) {
   return y;
 }
 
-constexpr int kFmaRows = 64, kFmaKeys = 32, kFmaThreads = 256;
+constexpr int kFmaRows = 32, kFmaKeys = 64, kFmaThreads = 128;
 
 template <int D>
 struct FmaSmem {
   float q[kFmaRows][D + 4];
-  float k[2][kFmaKeys][D + 4];  // two buffers
-  float v[2][kFmaKeys][D];
+  float k[kFmaKeys][D + 4];
+  float v[kFmaKeys][D];
   float p[kFmaRows][kFmaKeys + 4];
 };
 
 // The state of thread (ty, tx) = (tid / 16, tid % 16): rows 4 ty .. 4 ty + 3,
-// keys tx and tx + 16 of a step's scores, dims 4 tx .. 4 tx + 3 (and 64 more)
+// keys tx, tx + 16, tx + 32 and tx + 48 of a step's scores, dims 4 tx .. 4 tx + 3 (and 64 more)
 // of the outputs.  The running maximum (log2 domain) and sum are the same in
 // the 16 threads of a row.
 template <int D>
@@ -43,40 +49,49 @@ struct FmaTile {
   // scores of the staged keys times ks(key), masked by see(row of the thread,
   // key of the step); weights times vs(key) for the values
   template <class See, class KScale, class VScale>
-  __device__ __forceinline__ void step(FmaSmem<D>& sm, int buf, int ty, int tx, See see, KScale ks, VScale vs) {
-    float s[4][2];
+  __device__ __forceinline__ void step(FmaSmem<D>& sm, int ty, int tx, See see, KScale ks, VScale vs) {
+    float s[4][4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) s[r][0] = s[r][1] = 0.0f;
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[r][j] = 0.0f;
 #pragma unroll 4
     for (int c = 0; c < D; c += 4) {
-      const float4 k0 = *reinterpret_cast<const float4*>(&sm.k[buf][tx][c]);
-      const float4 k1 = *reinterpret_cast<const float4*>(&sm.k[buf][tx + 16][c]);
+      float4 x[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float4 x = *reinterpret_cast<const float4*>(&sm.q[4 * ty + r][c]);
-        s[r][0] = fmaf(x.x, k0.x, fmaf(x.y, k0.y, fmaf(x.z, k0.z, fmaf(x.w, k0.w, s[r][0]))));
-        s[r][1] = fmaf(x.x, k1.x, fmaf(x.y, k1.y, fmaf(x.z, k1.z, fmaf(x.w, k1.w, s[r][1]))));
+      for (int r = 0; r < 4; ++r) x[r] = *reinterpret_cast<const float4*>(&sm.q[4 * ty + r][c]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float4 k = *reinterpret_cast<const float4*>(&sm.k[tx + 16 * j][c]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          s[r][j] = fmaf(x[r].x, k.x, fmaf(x[r].y, k.y, fmaf(x[r].z, k.z, fmaf(x[r].w, k.w, s[r][j]))));
       }
     }
-    const float ks0 = ks(tx), ks1 = ks(tx + 16), vs0 = vs(tx), vs1 = vs(tx + 16);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      s[r][0] = see(r, tx) ? s[r][0] * ks0 : -INFINITY;
-      s[r][1] = see(r, tx + 16) ? s[r][1] * ks1 : -INFINITY;
-      float mx = fmaxf(s[r][0], s[r][1]);
+      float mx = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[r][j] = see(r, tx + 16 * j) ? s[r][j] * ks(tx + 16 * j) : -INFINITY;
+        mx = fmaxf(mx, s[r][j]);
+      }
 #pragma unroll
       for (int off = 8; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
       mx = fmaxf(mx, m[r]);
       const float base = mx == -INFINITY ? 0.0f : mx;
       const float corr = ex2f(m[r] - base);
-      const float p0 = ex2f(s[r][0] - base), p1 = ex2f(s[r][1] - base);
-      float ps = p0 + p1;
+      float ps = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float p = ex2f(s[r][j] - base);
+        ps += p;
+        sm.p[4 * ty + r][tx + 16 * j] = p * vs(tx + 16 * j);
+      }
 #pragma unroll
       for (int off = 8; off > 0; off >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, off);
       l[r] = l[r] * corr + ps;
       m[r] = mx;
-      sm.p[4 * ty + r][tx] = p0 * vs0;
-      sm.p[4 * ty + r][tx + 16] = p1 * vs1;
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) o[r][c] *= corr;
     }
@@ -93,7 +108,7 @@ struct FmaTile {
       for (int jj = 0; jj < 4; ++jj)
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
-          const float4 y = *reinterpret_cast<const float4*>(&sm.v[buf][j + jj][64 * c + 4 * tx]);
+          const float4 y = *reinterpret_cast<const float4*>(&sm.v[j + jj][64 * c + 4 * tx]);
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             o[r][4 * c] = fmaf(p[r][jj], y.x, o[r][4 * c]);

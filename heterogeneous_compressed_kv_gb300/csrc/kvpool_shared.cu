@@ -21,7 +21,7 @@
 namespace kvp {
 namespace {
 
-constexpr int kSharedRows = 64;  // requests of a CTA
+constexpr int kSharedRows = 64;  // requests of a CTA of the small products
 
 // 4 values of a row of codes in fp32 (fp8: without the scale)
 template <int T>
@@ -46,15 +46,15 @@ __global__ void __launch_bounds__(kFmaThreads) shared_fma_kernel(const __grid_co
   pdl_start();
   extern __shared__ __align__(16) uint8_t smem_raw[];
   FmaSmem<D>& sm = *reinterpret_cast<FmaSmem<D>*>(smem_raw);
-  __shared__ float scales[2][2][kFmaKeys];
+  __shared__ float scales[2][kFmaKeys];
   const PoolDesc& pd = P.pool;
   const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
-  const int h = blockIdx.x, split = blockIdx.y, i0 = blockIdx.z * kSharedRows;
-  const int rows = min(kSharedRows, P.n - i0);
+  const int h = blockIdx.x, split = blockIdx.y, i0 = blockIdx.z * kFmaRows;
+  const int rows = min(kFmaRows, P.n - i0);
   const int a = (int)((int64_t)H.n_entries * split / H.n_split);
   const int b = (int)((int64_t)H.n_entries * (split + 1) / H.n_split);
   const float qscale = 1.4426950408889634f * rsqrtf((float)D);
-  for (int i = tid; i < kSharedRows * (D / 4); i += kFmaThreads) {
+  for (int i = tid; i < kFmaRows * (D / 4); i += kFmaThreads) {
     const int r = i / (D / 4), c = 4 * (i % (D / 4));
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r < rows)
@@ -63,17 +63,15 @@ __global__ void __launch_bounds__(kFmaThreads) shared_fma_kernel(const __grid_co
   }
   FmaTile<D> t;
   t.init();
-  // a step's entries go to one buffer while the other is worked on; fp32 rows
-  // by asynchronous copies
-  auto load = [&](int e0, int buf) {
+  auto load = [&](int e0) {  // fp32 rows by asynchronous copies
     for (int i = tid; i < kFmaKeys * (D / 4); i += kFmaThreads) {
       const int r = i / (D / 4), c = 4 * (i % (D / 4));
       const bool in = e0 + r < b;
       const uint8_t* ent = in ? shared_entry(P, shared_id(P, H, e0 + r)) : pd.arena;
       const uint8_t* kr = ent + h * D * pd.vs;
       if constexpr (CACHE == KVPOOL_F32) {
-        cp_async16(smem_addr(&sm.k[buf][r][c]), in ? kr + 4 * c : ent, in ? 16 : 0);
-        cp_async16(smem_addr(&sm.v[buf][r][c]), in ? kr + 4 * (pd.HD + c) : ent, in ? 16 : 0);
+        cp_async16(smem_addr(&sm.k[r][c]), in ? kr + 4 * c : ent, in ? 16 : 0);
+        cp_async16(smem_addr(&sm.v[r][c]), in ? kr + 4 * (pd.HD + c) : ent, in ? 16 : 0);
       } else {
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
         if (in) {
@@ -81,30 +79,25 @@ __global__ void __launch_bounds__(kFmaThreads) shared_fma_kernel(const __grid_co
           y = codes4<CACHE>(kr + pd.HD * pd.vs, c);
           if (CACHE == KVPOOL_FP8_E4M3 && c == 0) {
             const uint32_t s2 = *reinterpret_cast<const uint32_t*>(ent + 2 * pd.HD);
-            scales[buf][0][r] = qscale * __uint_as_float(s2 << 16);
-            scales[buf][1][r] = __uint_as_float(s2 & 0xFFFF0000u);
+            scales[0][r] = qscale * __uint_as_float(s2 << 16);
+            scales[1][r] = __uint_as_float(s2 & 0xFFFF0000u);
           }
         }
-        *reinterpret_cast<float4*>(&sm.k[buf][r][c]) = x;
-        *reinterpret_cast<float4*>(&sm.v[buf][r][c]) = y;
+        *reinterpret_cast<float4*>(&sm.k[r][c]) = x;
+        *reinterpret_cast<float4*>(&sm.v[r][c]) = y;
       }
     }
     cp_async_commit();
   };
-  load(a, 0);
-  for (int e0 = a, buf = 0; e0 < b; e0 += kFmaKeys, buf ^= 1) {
-    if (e0 + kFmaKeys < b) {
-      load(e0 + kFmaKeys, buf ^ 1);
-      cp_async_wait<1>();
-    } else {
-      cp_async_wait<0>();
-    }
+  for (int e0 = a; e0 < b; e0 += kFmaKeys) {
+    load(e0);
+    cp_async_wait<0>();
     __syncthreads();
     const int n = b - e0;
     t.step(
-        sm, buf, ty, tx, [&](int, int j) { return j < n; },
-        [&](int j) { return CACHE != KVPOOL_FP8_E4M3 ? qscale : j < n ? scales[buf][0][j] : 0.0f; },
-        [&](int j) { return CACHE != KVPOOL_FP8_E4M3 ? 1.0f : j < n ? scales[buf][1][j] : 0.0f; });
+        sm, ty, tx, [&](int, int j) { return j < n; },
+        [&](int j) { return CACHE != KVPOOL_FP8_E4M3 ? qscale : j < n ? scales[0][j] : 0.0f; },
+        [&](int j) { return CACHE != KVPOOL_FP8_E4M3 ? 1.0f : j < n ? scales[1][j] : 0.0f; });
     __syncthreads();
   }
 #pragma unroll
@@ -383,7 +376,7 @@ cudaError_t launch_shared_t(const AttendParams& p, const SharedShape& h, cudaStr
   constexpr int smem = (int)sizeof(FmaSmem<D>);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return launch_kernel(true, kern, dim3(p.pool.heads, h.n_split, (p.n + kSharedRows - 1) / kSharedRows),
+  return launch_kernel(true, kern, dim3(p.pool.heads, h.n_split, (p.n + kFmaRows - 1) / kFmaRows),
                        dim3(kFmaThreads), smem, s, p, h);
 }
 
@@ -404,14 +397,14 @@ cudaError_t launch_shared_d(const AttendParams& p, const SharedShape& h, cudaStr
 //   8,192       36.2 / 35.4    52.9 / 41.6    96.7 / 58.4
 bool shared_tc(int n, int n_entries) { return n > 32 && n_entries >= 2048; }
 
-// Splits of the shared entries for n requests: CTAs (head, split, 64
-// requests) that fill the GPU (the FMA form: twice over), of at least 64
-// entries each.
+// Splits of the shared entries for n requests: CTAs (head, split, block of
+// requests) that fill the GPU (the FMA form: with three to an SM), of at least
+// 64 entries each.
 int shared_splits(const PoolDesc& pd, int n, int n_entries, int n_sms) {
   const bool mma = pd.in_dtype == KVPOOL_BF16 && pd.cache_dtype == KVPOOL_BF16;
-  const int rows = mma && shared_tc(n, n_entries) ? kSharedTcRows : kSharedRows;
+  const int rows = !mma ? kFmaRows : shared_tc(n, n_entries) ? kSharedTcRows : kSharedRows;
   const int per = pd.heads * ((n + rows - 1) / rows);
-  return std::max(1, std::min(mma ? n_sms / per : (2 * n_sms + per - 1) / per, (n_entries + 63) / 64));
+  return std::max(1, std::min(mma ? n_sms / per : 3 * n_sms / per, (n_entries + 63) / 64));
 }
 
 int launch_shared(const AttendParams& p, int n_entries, int n_split, void* stream, int* n_kernels) {

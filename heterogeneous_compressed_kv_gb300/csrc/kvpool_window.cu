@@ -45,7 +45,7 @@ __device__ __forceinline__ void store4(uint8_t* base, int64_t i, float4 x) {
   }
 }
 
-// ---- fp32 FMA tiles: 64 rows, 32 keys per step ----------------------------------
+// ---- fp32 FMA tiles: 32 rows, 64 keys per step ----------------------------------
 template <int T, int D>
 __global__ void __launch_bounds__(kFmaThreads) window_fma_kernel(const __grid_constant__ WinParams P) {
   pdl_start();
@@ -80,9 +80,7 @@ __global__ void __launch_bounds__(kFmaThreads) window_fma_kernel(const __grid_co
     const bool sink = st < st_s;
     return Step{sink ? st * kFmaKeys : w.lo + (st - st_s) * kFmaKeys, sink ? w.n_s : w.lo + w.n_w, sink};
   };
-  // a step's rows go to one buffer while the other is worked on; fp32 rows by
-  // asynchronous copies
-  auto load = [&](int st, int buf) {
+  auto load = [&](int st) {  // fp32 rows by asynchronous copies
     const Step c = step_of(st);
     for (int i = tid; i < kFmaKeys * (D / 4); i += kFmaThreads) {
       const int r = i / (D / 4), x = 4 * (i % (D / 4));
@@ -90,28 +88,23 @@ __global__ void __launch_bounds__(kFmaThreads) window_fma_kernel(const __grid_co
       const int64_t ka = in ? (S.k_start + c.t0 + r) * P.k_tok + w.hk * P.k_head + x : 0;
       const int64_t va = in ? (S.k_start + c.t0 + r) * P.v_tok + w.hk * P.v_head + x : 0;
       if constexpr (T == KVPOOL_F32) {
-        cp_async16(smem_addr(&sm.k[buf][r][x]), P.k + 4 * ka, in ? 16 : 0);
-        cp_async16(smem_addr(&sm.v[buf][r][x]), P.v + 4 * va, in ? 16 : 0);
+        cp_async16(smem_addr(&sm.k[r][x]), P.k + 4 * ka, in ? 16 : 0);
+        cp_async16(smem_addr(&sm.v[r][x]), P.v + 4 * va, in ? 16 : 0);
       } else {
         const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-        *reinterpret_cast<float4*>(&sm.k[buf][r][x]) = in ? load4<T>(P.k, ka) : zero;
-        *reinterpret_cast<float4*>(&sm.v[buf][r][x]) = in ? load4<T>(P.v, va) : zero;
+        *reinterpret_cast<float4*>(&sm.k[r][x]) = in ? load4<T>(P.k, ka) : zero;
+        *reinterpret_cast<float4*>(&sm.v[r][x]) = in ? load4<T>(P.v, va) : zero;
       }
     }
     cp_async_commit();
   };
-  if (a < b) load(a, 0);
-  for (int st = a, buf = 0; st < b; ++st, buf ^= 1) {
-    if (st + 1 < b) {
-      load(st + 1, buf ^ 1);
-      cp_async_wait<1>();
-    } else {
-      cp_async_wait<0>();
-    }
+  for (int st = a; st < b; ++st) {
+    load(st);
+    cp_async_wait<0>();
     __syncthreads();
     const Step c = step_of(st);
     f.step(
-        sm, buf, ty, tx,
+        sm, ty, tx,
         [&](int r, int j) {
           return c.t0 + j < c.end && (c.sink ? pos[r] >= 0 : win_sees(P, pos[r], c.t0 + j));
         },
@@ -295,8 +288,10 @@ int plan_launch(const kvpool_window_args* a, Form form, bool tc, int32_t i0, int
     q_row0 += q_len[i];
   }
   *next_row = q_row0;
-  const int64_t min_keys = form == kFormTok ? 256 : 128;
-  const int64_t want = form == kFormTok ? 3LL * n_sms : form == kFormTc ? n_sms : 2LL * n_sms;  // work items
+  // work items that fill the GPU, and the fewest keys of one (fp32 prompts of
+  // 1,021 tokens: 53, 41, 44, 46 us at 2, 4, 6, 8 items per multiprocessor)
+  const int64_t min_keys = form == kFormTok ? 256 : form == kFormTc ? 128 : kFmaKeys;
+  const int64_t want = n_sms * (form == kFormTok ? 3LL : form == kFormTc ? 1LL : 4LL);
   int64_t items = 0, slot = 0, merge = 0, rows = 0;
   for (int s = 0; s < P->n_segs; ++s) {
     WinSeg& S = P->segs[s];

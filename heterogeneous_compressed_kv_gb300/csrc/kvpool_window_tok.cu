@@ -84,7 +84,7 @@ __device__ void tok_finish(const WinParams& P, const WinItem& w, const float* so
 
 // ---- bf16: NT tiles of 8 rows ------------------------------------------------------
 template <int D, int NT>
-__global__ void __launch_bounds__(kTokWarps * 32, NT == 1 ? 3 : 2) window_tok_kernel(const __grid_constant__ WinParams P) {
+__global__ void __launch_bounds__(kTokWarps * 32, NT == 1 ? 4 : 2) window_tok_kernel(const __grid_constant__ WinParams P) {
   pdl_start();
   __shared__ float so[kTokWarps][NT * 8][D];
   __shared__ float2 sml[kTokWarps][NT * 8];
