@@ -288,19 +288,19 @@ int plan_launch(const kvpool_window_args* a, Form form, bool tc, int32_t i0, int
     q_row0 += q_len[i];
   }
   *next_row = q_row0;
-  // work items that fill the GPU, and the fewest keys of one (fp32 prompts of
-  // 1,021 tokens: 53, 41, 44, 46 us at 2, 4, 6, 8 items per multiprocessor)
+  // Work items that fill the GPU, and the fewest keys of one.  Tensor-core and
+  // single-token items are counted down to one wave (one and four CTAs to a
+  // multiprocessor; a few past it would double the time); fp32 ones up (prompts
+  // of 1,021 tokens: 53, 41, 44, 46 us at 2, 4, 6, 8 to a multiprocessor).
   const int64_t min_keys = form == kFormTok ? 256 : form == kFormTc ? 128 : kFmaKeys;
-  const int64_t want = n_sms * (form == kFormTok ? 3LL : form == kFormTc ? 1LL : 4LL);
+  const int64_t want = n_sms * (form == kFormTc ? 1LL : 4LL);
+  const int64_t fill = tiles == 0 ? 1 : form == kFormFma ? (want + tiles - 1) / tiles : std::max<int64_t>(1, want / tiles);
   int64_t items = 0, slot = 0, merge = 0, rows = 0;
   for (int s = 0; s < P->n_segs; ++s) {
     WinSeg& S = P->segs[s];
     const int64_t st = (int64_t)((S.q_len + P->tile_tokens - 1) / P->tile_tokens) * Hk;
-    int64_t split = 1;
-    if (tiles < want)
-      split = std::max<int64_t>(
-          1, std::min<int64_t>((want + tiles - 1) / tiles,
-                               (tile_keys(a, S.q_len, S.k_len, P->tile_tokens) + min_keys - 1) / min_keys));
+    const int64_t keys = tile_keys(a, S.q_len, S.k_len, P->tile_tokens);
+    const int64_t split = std::max<int64_t>(1, std::min(fill, (keys + min_keys - 1) / min_keys));
     S.n_split = (int32_t)split;
     S.item_base = (int32_t)items;
     S.part_base = (int32_t)slot;

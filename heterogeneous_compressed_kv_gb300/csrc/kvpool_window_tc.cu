@@ -131,11 +131,6 @@ __device__ __forceinline__ void tc_weights32(const uint32_t* x, float scale, flo
   }
   tmem_st16(addr, pk);
 }
-__device__ __forceinline__ void tc_weights64(const uint32_t* x, float scale, float base, uint64_t* sum, uint32_t addr) {
-  tc_weights32(x, scale, base, sum, addr);
-  tc_weights32(x + 32, scale, base, sum, addr + 16);
-}
-
 // Take a step's maximum into the row's; the whole warp rescales its sums and
 // outputs (in tensor memory from `to` on) when some row's grew by too much.
 template <int D>
@@ -430,82 +425,34 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
         const bool whole = c.t0 + kTcKeys <= c.end &&
                            (c.sink || (c.t0 + kTcKeys - 1 <= q.p0 &&
                                        (c.t0 > q.p1 - P.window || c.t0 + kTcKeys <= P.n_sink)));
-        if (whole) {
-          // Scores in registers, 64 at a time: the second half first, for its
-          // maximum; the first half, whose registers then serve for the
-          // weights too; and the second again, on its way while the first
-          // half's weights are worked out (the weights of columns 0 .. 63 are
-          // written over columns 0 .. 31).
-          uint32_t x[64], y[64];
-          tmem_ld32(ts + 64, y);
-          tmem_ld32(ts + 96, y + 32);
-          tmem_wait_ld();
-          tmem_ld32(ts, x);
-          tmem_ld32(ts + 32, x + 32);
-          float mx = tc_max64(y, -INFINITY);
-          tmem_wait_ld();
-          mx = tc_max64(x, mx);
-          tmem_ld32(ts + 64, y);
-          tmem_ld32(ts + 96, y + 32);
-          tc_maximum<D>(mx * scale, first, m, l, to);
-          const float base = m == -INFINITY ? 0.0f : m;
-          uint64_t sum[2] = {0, 0};
-          tc_weights64(x, scale, base, sum, ts);
-          tmem_wait_ld();
-          tc_weights64(y, scale, base, sum, ts + 32);
-          const float2 sa = unpack2(sum[0]), sb = unpack2(sum[1]);
-          l += (sa.x + sa.y) + (sb.x + sb.y);
-        } else {
-          const int hi = min(c.sink ? c.end - 1 : pos, c.end - 1) - c.t0;  // last column
+        // the row's 128 scores in registers: mask, maximum, weights
+        uint32_t x[128];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, x + 32 * i);
+        tmem_wait_ld();
+        if (!whole) {
+          const int hi = min(c.sink ? c.end - 1 : pos, c.end - 1) - c.t0;  // last column that the row sees
           const int lo = c.sink ? 0 : pos - P.window + 1 - c.t0;            // first of the window
           const int sk = c.sink ? 0 : P.n_sink - c.t0;                     // columns before it: first tokens
-          uint32_t see[4], all = 0, some = 0;  // bit i: every row of the warp sees all of quarter i; some row some of it
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int h = hi - 32 * i, g = lo - 32 * i, f = sk - 32 * i;
             const uint32_t le = h < 0 ? 0u : h >= 31 ? ~0u : (2u << h) - 1u;
             const uint32_t ge = g <= 0 ? ~0u : g >= 32 ? 0u : ~((1u << g) - 1u);
             const uint32_t lt = f <= 0 ? 0u : f >= 32 ? ~0u : (1u << f) - 1u;
-            see[i] = le & (ge | lt);
-            all |= (uint32_t)__all_sync(0xffffffffu, see[i] == ~0u) << i;
-            some |= (uint32_t)__any_sync(0xffffffffu, see[i] != 0u) << i;
-          }
-          // 32 scores at a time, twice; a quarter that none of the warp's rows sees is skipped
-          auto quarter = [&](uint32_t* x, int i) {
-            tmem_ld32(ts + 32 * i, x);
-            tmem_wait_ld();
-            if ((all >> i) & 1) return;
-            const uint32_t se = i < 2 ? (i ? see[1] : see[0]) : (i == 2 ? see[2] : see[3]);
+            const uint32_t see = le & (ge | lt);
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if (!((se >> j) & 1u)) x[j] = 0xFF800000u;  // -inf
-          };
-          float mx = -INFINITY;
-          uint32_t x[32];
-#pragma unroll 1
-          for (int i = 0; i < 4; ++i) {
-            if (!((some >> i) & 1)) continue;
-            quarter(x, i);
-            mx = tc_max32(x, mx);
+              if (!((see >> j) & 1u)) x[32 * i + j] = 0xFF800000u;  // -inf
           }
-          tc_maximum<D>(mx * scale, first, m, l, to);
-          const float base = m == -INFINITY ? 0.0f : m;
-          uint64_t sum[2] = {0, 0};
-          // weights of columns 32 i .. 32 i + 31 go to words 16 i .. 16 i + 15: over scores that are in registers by then
-#pragma unroll 1
-          for (int i = 0; i < 4; ++i) {
-            if ((some >> i) & 1) {
-              quarter(x, i);
-              tc_weights32(x, scale, base, sum, ts + 16 * i);
-            } else {
-#pragma unroll
-              for (int j = 0; j < 16; ++j) x[j] = 0u;
-              tmem_st16(ts + 16 * i, x);
-            }
-          }
-          const float2 sa = unpack2(sum[0]), sb = unpack2(sum[1]);
-          l += (sa.x + sa.y) + (sb.x + sb.y);
         }
+        tc_maximum<D>(tc_max64(x + 64, tc_max64(x, -INFINITY)) * scale, first, m, l, to);
+        const float base = m == -INFINITY ? 0.0f : m;
+        uint64_t sum[2] = {0, 0};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tc_weights32(x + 32 * i, scale, base, sum, ts + 16 * i);
+        const float2 sa = unpack2(sum[0]), sb = unpack2(sum[1]);
+        l += (sa.x + sa.y) + (sb.x + sb.y);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
