@@ -3,10 +3,9 @@
 //
 // A work item is 256 query rows (token, query head of the group) of one key
 // head: two tiles of 128 rows that share every K and V tile of 128 keys.
-// Persistent CTAs, one per SM, of eleven warps: one issues the tensor copies
-// (Q tiles, and a ring of K and V tiles), one the matrix products, one zeroes V
-// rows that nobody sees, and a group of four per query tile does its softmax, a
-// thread per row.  Scores S = Q K^T
+// Persistent CTAs, one per SM, of ten warps: one issues the tensor copies
+// (Q tiles, and a ring of K and V tiles), one the matrix products, and a group
+// of four per query tile does its softmax, a thread per row.  Scores S = Q K^T
 // go to tensor memory; the softmax reads a row, keeps the running maximum and
 // sum in fp32, and writes the weights back as bf16 over the scores; O += P V
 // accumulates in tensor memory.  While one tile's rows go through the softmax
@@ -18,9 +17,9 @@
 // relative precision up to 2^8, the sums are fp32), so the read-modify-write
 // of O leaves the critical path.
 //
-// Rows of K and V behind what any row of the item sees never count: scores are
-// masked, and such V rows are zeroed in shared memory before the product (0
-// times a NaN there would reach every row).
+// Rows of K and V behind a segment never count: scores are masked, and such V
+// rows are zeroed in shared memory before the product (0 times a NaN there
+// would reach every row).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -32,7 +31,8 @@ namespace kvp {
 namespace {
 
 constexpr int kTcKeys = 128;
-constexpr int kTcThreads = 352;
+constexpr int kTcThreads = 320;
+constexpr int kTcTable = 96;  // items of a CTA that are worked out at its start
 constexpr float kRescale = 8.0f;  // log2 growth of the maximum that rescales O
 
 template <int D>
@@ -40,37 +40,41 @@ struct TcShape {
   static constexpr int kTileBytes = 128 * D * 2;  // a Q, K or V tile: D / 64 runs of 128 rows x 128 bytes
   static constexpr int kStages = D == 128 ? 4 : 8;
   static constexpr int kBarOff = (2 + kStages) * kTileBytes;
-  static constexpr int kSmem = kBarOff + 512 + 1024;  // + slack to align the tiles to 1,024 bytes
+  static constexpr int kTableOff = kBarOff + 512;
+  static constexpr int kSmem = kTableOff + kTcTable * 64 + 1024;  // + slack to align the tiles to 1,024 bytes
 };
 
 struct TcMaps {
   CUtensorMap q, k, v;
 };
 
-// Step st of an item: 128 keys from token t0 on, of which those before `end` count.
+// A work item as the roles take it: its keys are the first n_s tokens and n_w
+// from lo on, in steps [a, b) of 128.
+struct TcItem {
+  int hk, q_row, k_row, n_tok, pos0, n_split, slot, k_len;
+  int n_s, lo, n_w, a, b;
+  int pad[3];
+};
+static_assert(sizeof(TcItem) == 64, "the item table's stride");
+
+// Step st of a key list: 128 keys from token t0 on, of which those before `end` count.
 struct TcStep {
   int t0, end;
   bool sink;
 };
-__device__ __forceinline__ TcStep tc_step(const WinItem& w, int st) {
+__device__ __forceinline__ TcStep tc_step(const TcItem& w, int st) {
   const int st_s = (w.n_s + kTcKeys - 1) / kTcKeys;
-  TcStep s;
-  s.sink = st < st_s;
-  s.t0 = s.sink ? st * kTcKeys : w.lo + (st - st_s) * kTcKeys;
-  s.end = s.sink ? w.n_s : w.lo + w.n_w;
-  return s;
+  TcStep c;
+  c.sink = st < st_s;
+  c.t0 = c.sink ? st * kTcKeys : w.lo + (st - st_s) * kTcKeys;
+  c.end = c.sink ? w.n_s : w.lo + w.n_w;
+  return c;
 }
-// this split's steps [a, b) of an item
-__device__ __forceinline__ void tc_range(const WinItem& w, int& a, int& b) {
-  const int n = (w.n_s + kTcKeys - 1) / kTcKeys + (w.n_w + kTcKeys - 1) / kTcKeys;
-  a = (int)((int64_t)n * w.split / w.n_split);
-  b = (int)((int64_t)n * (w.split + 1) / w.n_split);
-}
-// A query tile of an item: tokens at positions p0 .. p1 (n of them)
+// A query tile of an item: n tokens at positions p0 .. p1
 struct TcTile {
   int n, p0, p1;
 };
-__device__ __forceinline__ TcTile tc_tile(const WinParams& P, const WinItem& w, int t) {
+__device__ __forceinline__ TcTile tc_tile(const WinParams& P, const TcItem& w, int t) {
   const int tt = P.tile_tokens / 2;
   TcTile q;
   q.n = max(0, min(tt, w.n_tok - t * tt));
@@ -78,6 +82,7 @@ __device__ __forceinline__ TcTile tc_tile(const WinParams& P, const WinItem& w, 
   q.p1 = q.p0 + q.n - 1;
   return q;
 }
+
 // The steps of [a, b) that some row of a query tile needs: those before `sink`
 // (first tokens) and those in [lo, hi).
 struct TcNeed {
@@ -85,17 +90,17 @@ struct TcNeed {
   __device__ __forceinline__ bool operator()(int st) const { return st < sink || (st >= lo && st < hi); }
   __device__ __forceinline__ int last(int a) const { return hi > lo ? hi - 1 : sink > a ? sink - 1 : -1; }
 };
-__device__ __forceinline__ TcNeed tc_need(const WinParams& P, const WinItem& w, const TcTile& q, int a, int b) {
-  TcNeed n{a, a, a};
+__device__ __forceinline__ TcNeed tc_need(const WinParams& P, const TcItem& w, const TcTile& q) {
+  TcNeed n{w.a, w.a, w.a};
   if (q.n <= 0) return n;
   const int st_s = (w.n_s + kTcKeys - 1) / kTcKeys;
-  // window steps: step st holds tokens w.lo + (st - st_s) * 128 ..
+  // window steps: step st holds tokens lo + (st - st_s) * 128 ..
   const int first = max(0, q.p0 - P.window + 1 - w.lo) / kTcKeys;  // of the first token in the window
   const int past = q.p1 < w.lo ? 0 : (q.p1 - w.lo) / kTcKeys + 1;
-  const int sinks = P.n_sink > w.lo ? (P.n_sink - w.lo + kTcKeys - 1) / kTcKeys : 0;  // first tokens behind w.lo
-  n.sink = min(b, max(a, st_s + min(sinks, past)));
+  const int sinks = P.n_sink > w.lo ? (P.n_sink - w.lo + kTcKeys - 1) / kTcKeys : 0;  // first tokens behind lo
+  n.sink = min(w.b, max(w.a, st_s + min(sinks, past)));
   n.lo = max(n.sink, st_s + first);
-  n.hi = max(n.lo, min(b, st_s + past));
+  n.hi = max(n.lo, min(w.b, st_s + past));
   return n;
 }
 
@@ -104,6 +109,28 @@ __device__ __forceinline__ int tc_nth(const WinParams& P, int k) {
   const int g = gridDim.x, c = blockIdx.x;
   const int i = k * g + ((k & 1) ? g - 1 - c : c);
   return i < P.n_items ? P.n_items - 1 - i : -1;
+}
+
+__device__ __forceinline__ TcItem tc_make(const WinParams& P, int item) {
+  const WinItem w = win_item(P, item);
+  const WinSeg& S = P.segs[w.seg];
+  const int n = (w.n_s + kTcKeys - 1) / kTcKeys + (w.n_w + kTcKeys - 1) / kTcKeys;
+  TcItem x;
+  x.hk = w.hk;
+  x.q_row = (int)S.q_row0 + w.tok0;
+  x.k_row = (int)S.k_start;
+  x.n_tok = w.n_tok;
+  x.pos0 = w.pos0;
+  x.n_split = w.n_split;
+  x.slot = w.slot;
+  x.k_len = S.k_len;
+  x.n_s = w.n_s;
+  x.lo = w.lo;
+  x.n_w = w.n_w;
+  x.a = (int)((int64_t)n * w.split / w.n_split);
+  x.b = (int)((int64_t)n * (w.split + 1) / w.n_split);
+  x.pad[0] = x.pad[1] = x.pad[2] = 0;
+  return x;
 }
 
 // ---- softmax of one row -----------------------------------------------------------
@@ -158,7 +185,6 @@ __device__ __forceinline__ void tc_maximum(float mn, bool& first, float& m, floa
 template <int D>
 __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_constant__ WinParams P,
                                                                   const __grid_constant__ TcMaps M) {
-  pdl_start();
   using Sh = TcShape<D>;
   constexpr int NS = Sh::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -167,13 +193,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
   uint8_t* ring = smem + 2 * Sh::kTileBytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Sh::kBarOff);
   uint64_t *kv_full = bars, *kv_free = kv_full + NS, *q_full = kv_free + NS, *q_free = q_full + 2, *s_full = q_free + 2,
-           *p_ready = s_full + 2, *o_full = p_ready + 2, *o_free = o_full + 2, *v_ask = o_free + 2, *v_ok = v_ask + 1, *drain = v_ok + 1;
+           *p_ready = s_full + 2, *o_full = p_ready + 2, *o_free = o_full + 2, *v_ok = o_free + 2, *drain = v_ok + NS;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  TcItem* table = reinterpret_cast<TcItem*>(smem + Sh::kTableOff);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(&kv_full[i], 1);
       mbar_init(&kv_free[i], 1);
+      mbar_init(&v_ok[i], 1);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&q_full[t], 1);
@@ -183,75 +211,95 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
       mbar_init(&o_full[t], 1);
       mbar_init(&o_free[t], 4);
     }
-    mbar_init(v_ask, 1);
-    mbar_init(v_ok, 1);
     mbar_init(drain, 1);
     mbar_fence_init();
+  }
+  // The CTA's first items, a thread each (the divisions and the search for the
+  // segment cost ~2,000 cycles, once instead of per item and role)
+  if (threadIdx.x >= 32 && threadIdx.x < 32 + kTcTable) {
+    const int item = tc_nth(P, threadIdx.x - 32);
+    if (item >= 0) table[threadIdx.x - 32] = tc_make(P, item);
   }
   if (warp == 9) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;  // columns: S0, S1 (128 each), O0, O1 (128 each)
+  pdl_start();  // nothing before touches what an earlier kernel writes
+  auto item_of = [&](int k, int item) -> TcItem {
+    if (k < kTcTable) return table[k];
+    return tc_make(P, item);
+  };
 
   if (warp == 8) {
-    // ---- tensor copies (one thread) ----
-    if (elect_one()) {
-      int stage = 0, n_q[2] = {0, 0}, issued = 0;
-      uint32_t round = 0;  // of the ring
-      bool ok = true;
-      auto load = [&](const CUtensorMap* map, int hk, int row) {
-        if (round > 0 && !mbar_wait_word(&kv_free[stage], (round - 1) & 1, P.err)) ok = false;
-        if (!ok) return;
+    // ---- tensor copies (one lane issues them) ----
+    const bool leader = elect_one();
+    int stage = 0, n_q[2] = {0, 0}, issued = 0;
+    uint32_t round = 0;  // of the ring
+    bool ok = true;
+    auto load = [&](const CUtensorMap* map, int hk, int row) {
+      if (round > 0) ok = ok && warp_wait(&kv_free[stage], (round - 1) & 1, P.err);
+      if (!ok) return;
+      if (leader) {
         mbar_arrive_expect_tx(&kv_full[stage], Sh::kTileBytes);
 #pragma unroll
         for (int c = 0; c < D / 64; ++c)
           tma_load_3d(ring + stage * Sh::kTileBytes + c * 16384, map, 64 * c, hk, row, &kv_full[stage]);
-        ++issued;
-        if (++stage == NS) {
-          stage = 0;
-          ++round;
+      }
+      __syncwarp();
+      ++issued;
+      if (++stage == NS) {
+        stage = 0;
+        ++round;
+      }
+    };
+#pragma unroll 1
+    for (int k = 0; ok; ++k) {
+      const int item = tc_nth(P, k);
+      if (item < 0) break;
+      const TcItem w = item_of(k, item);
+      const int tt = P.tile_tokens / 2;
+      auto load_q = [&](int t) {
+        if (w.n_tok <= t * tt) return;
+        if (n_q[t] > 0) ok = ok && warp_wait(&q_free[t], (n_q[t] - 1) & 1, P.err);
+        if (!ok) return;
+        if (leader) {
+          mbar_arrive_expect_tx(&q_full[t], tt * P.group * D * 2);
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_4d(q_tile + t * Sh::kTileBytes + c * 16384, &M.q, 64 * c, 0, w.hk, w.q_row + t * tt, &q_full[t]);
         }
+        __syncwarp();
+        ++n_q[t];
       };
 #pragma unroll 1
-      for (int k = 0; ok; ++k) {
-        const int item = tc_nth(P, k);
-        if (item < 0) break;
-        const WinItem w = win_item(P, item);
-        const WinSeg& S = P.segs[w.seg];
-        int a, b;
-        tc_range(w, a, b);
-        if (a >= b) continue;
-        const int tt = P.tile_tokens / 2;
-#pragma unroll 1
-        for (int st = a; st < b && ok; ++st) {
-          // the first K tile goes out between the Q tiles
-#pragma unroll 1
-          for (int t = 0; st == a && t < 2 && ok; ++t) {
-            if (w.n_tok > t * tt) {
-              if (n_q[t] > 0 && !mbar_wait_word(&q_free[t], (n_q[t] - 1) & 1, P.err)) ok = false;
-              if (!ok) break;
-              mbar_arrive_expect_tx(&q_full[t], tt * P.group * D * 2);
-#pragma unroll
-              for (int c = 0; c < D / 64; ++c)
-                tma_load_4d(q_tile + t * Sh::kTileBytes + c * 16384, &M.q, 64 * c, 0, w.hk,
-                            (int)S.q_row0 + w.tok0 + t * tt, &q_full[t]);
-              ++n_q[t];
-            }
-            if (t == 0) load(&M.k, w.hk, (int)S.k_start + tc_step(w, a).t0);
+      for (int st = w.a; st < w.b && ok; ++st) {
+        const int t0 = tc_step(w, st).t0;
+        if (st == w.a) load_q(0);
+        if (ok) load(&M.k, w.hk, w.k_row + t0);
+        if (st == w.a && ok) load_q(1);
+        const int vs = stage;
+        const uint32_t vr = round;
+        if (ok) load(&M.v, w.hk, w.k_row + t0);
+        if (ok && w.k_len - t0 < kTcKeys) {
+          // V rows behind the segment: zeros, once the tile is there (only the
+          // segment's last tile; the copies after it wait that long)
+          ok = warp_wait(&kv_full[vs], vr & 1, P.err);
+          if (!ok) break;
+          for (int h = 0; h < D / 64; ++h) {
+            uint4* base = reinterpret_cast<uint4*>(ring + vs * Sh::kTileBytes + h * 16384);
+            for (int j = (w.k_len - t0) * 8 + lane; j < 128 * 8; j += 32) base[j] = make_uint4(0, 0, 0, 0);
           }
-          const int row = (int)S.k_start + tc_step(w, st).t0;
-          if (st > a && ok) load(&M.k, w.hk, row);
-          if (ok) load(&M.v, w.hk, row);
+          fence_proxy_async();
+          __syncwarp();
+          if (leader) mbar_arrive(&v_ok[vs]);
         }
       }
-      // the CTA does not end while copies land in its shared memory
-      for (int i = issued > NS ? issued - NS : 0; i < issued; ++i)
-        mbar_wait_word(&kv_full[i % NS], (i / NS) & 1, P.err);
-      for (int t = 0; t < 2; ++t)
-        if (n_q[t] > 0) mbar_wait_word(&q_full[t], (n_q[t] - 1) & 1, P.err);
     }
-    __syncwarp();
+    // the CTA does not end while copies land in its shared memory
+    for (int i = issued > NS ? issued - NS : 0; i < issued; ++i) warp_wait(&kv_full[i % NS], (i / NS) & 1, P.err);
+    for (int t = 0; t < 2; ++t)
+      if (n_q[t] > 0) warp_wait(&q_full[t], (n_q[t] - 1) & 1, P.err);
   } else if (warp == 9) {
     // ---- matrix products (one thread) ----
     if (elect_one()) {
@@ -261,94 +309,97 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
       int stage = 0;
       uint32_t round = 0;
       int n_q[2] = {0, 0}, n_p[2] = {0, 0}, n_o[2] = {0, 0};
-      int n_v = 0;
+      uint32_t v_par = 0;  // per stage: parity of its next v_ok phase
       bool ok = true;
+      auto next = [&]() {
+        if (++stage == NS) {
+          stage = 0;
+          ++round;
+        }
+      };
+      // the ring's next tile is there; returns its stage
+      auto take = [&]() {
+        const int s = stage;
+        if (!mbar_wait_word(&kv_full[s], round & 1, P.err)) ok = false;
+        next();
+        return s;
+      };
+      // O_t += P_t V, V in ring stage vs
+      auto outputs = [&](int t, int vs, bool begun, bool last) {
+        ok = ok && mbar_wait_word(&p_ready[t], n_p[t] & 1, P.err);
+        ++n_p[t];
+        if (ok && !begun && n_o[t] > 0) ok = mbar_wait_word(&o_free[t], (n_o[t] - 1) & 1, P.err);
+        if (!ok) return;
+        tc_fence_after();
+        const uint64_t vd = v_desc + vs * (Sh::kTileBytes >> 4);
+#pragma unroll
+        for (int c = 0; c < kTcKeys / 16; ++c)
+          mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * c, vd + c * (2048 >> 4), kIdPV, begun || c > 0);
+        if (last) {
+          mma_commit(&o_full[t]);
+          ++n_o[t];
+        }
+      };
+      // S_t = Q_t K^T, K in ring stage ks
+      auto scores = [&](int t, int ks, bool begun, bool last) {
+        if (!begun) {
+          ok = ok && mbar_wait_word(&q_full[t], n_q[t] & 1, P.err);
+          ++n_q[t];
+        }
+        if (!ok) return;
+        tc_fence_after();
+        const uint64_t qd = q_desc + t * (Sh::kTileBytes >> 4), kd = k_desc + ks * (Sh::kTileBytes >> 4);
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          const uint32_t off = ((c / 4) * 16384 + (c % 4) * 32) >> 4;
+          mma_ss(tmem + 128 * t, qd + off, kd + off, kIdQK, c > 0);
+        }
+        mma_commit(&s_full[t]);
+        if (last) mma_commit(&q_free[t]);
+      };
 #pragma unroll 1
       for (int k = 0; ok; ++k) {
         const int item = tc_nth(P, k);
         if (item < 0) break;
-        const WinItem w = win_item(P, item);
-        int a, b;
-        tc_range(w, a, b);
+        const TcItem w = item_of(k, item);
+        const int a = w.a, b = w.b;
         if (a >= b) continue;
         const TcTile q[2] = {tc_tile(P, w, 0), tc_tile(P, w, 1)};
-        const TcNeed need[2] = {tc_need(P, w, q[0], a, b), tc_need(P, w, q[1], a, b)};
+        const TcNeed need[2] = {tc_need(P, w, q[0]), tc_need(P, w, q[1])};
         const int last[2] = {need[0].last(a), need[1].last(a)};
-        uint32_t seen_q = 0, seen_pv = 0;  // tiles whose Q has been waited for, whose outputs have begun
+        bool seen_q[2] = {false, false}, seen_pv[2] = {false, false};
         int vs = 0;
-        bool zeroing = false;  // the V tile in stage vs is with the zeroing warp
         // round st: outputs of step st - 1, then scores of step st
 #pragma unroll 1
         for (int st = a; st <= b && ok; ++st) {
-          const int ks = stage;
-          if (st < b) {
-            if (!mbar_wait_word(&kv_full[ks], round & 1, P.err)) ok = false;
-            if (++stage == NS) {
-              stage = 0;
-              ++round;
-            }
-          }
-          if (ok && zeroing) {
-            ok = mbar_wait_word(v_ok, n_v++ & 1, P.err);
-            zeroing = false;
-          }
+          int ks = 0;
+          if (st < b) ks = take();
           if (!ok) break;
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            if (!ok) break;
-            if (st > a && need[t](st - 1)) {
-              ok = mbar_wait_word(&p_ready[t], n_p[t] & 1, P.err);
-              ++n_p[t];
-              const bool begun = (seen_pv >> t) & 1;
-              if (ok && !begun && n_o[t] > 0) ok = mbar_wait_word(&o_free[t], (n_o[t] - 1) & 1, P.err);
-              if (!ok) break;
-              tc_fence_after();
-              const uint64_t vd = v_desc + vs * (Sh::kTileBytes >> 4);
-#pragma unroll
-              for (int c = 0; c < kTcKeys / 16; ++c)
-                mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * c, vd + c * (2048 >> 4), kIdPV, begun || c > 0);
-              seen_pv |= 1u << t;
-              if (st - 1 == last[t]) {
-                mma_commit(&o_full[t]);
-                ++n_o[t];
-              }
+            if (ok && st > a && need[t](st - 1)) {
+              outputs(t, vs, seen_pv[t], st - 1 == last[t]);
+              seen_pv[t] = true;
             }
-            if (st < b && need[t](st)) {
-              if (!((seen_q >> t) & 1)) {
-                ok = mbar_wait_word(&q_full[t], n_q[t] & 1, P.err);
-                if (!ok) break;
-                ++n_q[t];
-                seen_q |= 1u << t;
-              }
-              tc_fence_after();
-              const uint64_t qd = q_desc + t * (Sh::kTileBytes >> 4), kd = k_desc + ks * (Sh::kTileBytes >> 4);
-#pragma unroll
-              for (int c = 0; c < D / 16; ++c) {
-                const uint32_t off = ((c / 4) * 16384 + (c % 4) * 32) >> 4;
-                mma_ss(tmem + 128 * t, qd + off, kd + off, kIdQK, c > 0);
-              }
-              mma_commit(&s_full[t]);
-              if (st == last[t]) mma_commit(&q_free[t]);
+            if (ok && st < b && need[t](st)) {
+              scores(t, ks, seen_q[t], st == last[t]);
+              seen_q[t] = true;
             }
           }
           if (!ok) break;
           if (st > a) mma_commit(&kv_free[vs]);
           if (st == b) break;
           mma_commit(&kv_free[ks]);
-          // V of this step
-          vs = stage;
-          ok = mbar_wait_word(&kv_full[vs], round & 1, P.err);
-          const TcStep cur = tc_step(w, st);
-          zeroing = ok && cur.t0 + kTcKeys > cur.end;
-          if (zeroing) mbar_arrive(v_ask);  // while the step's scores go through the softmax
-          if (++stage == NS) {
-            stage = 0;
-            ++round;
+          vs = take();
+          if (ok && w.k_len - tc_step(w, st).t0 < kTcKeys) {  // its rows behind the segment have been zeroed
+            ok = mbar_wait_word(&v_ok[vs], (v_par >> vs) & 1, P.err);
+            v_par ^= 1u << vs;
           }
         }
         // a tile whose rows need no step was loaded all the same: take its Q
-        for (int t = 0; t < 2 && ok; ++t)
-          if (q[t].n > 0 && !((seen_q >> t) & 1)) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if (ok && q[t].n > 0 && !seen_q[t]) {
             ok = mbar_wait_word(&q_full[t], n_q[t] & 1, P.err);
             ++n_q[t];
             mma_commit(&q_free[t]);
@@ -359,35 +410,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
       mbar_wait_word(drain, 0, P.err);
     }
     __syncwarp();
-  } else if (warp == 10) {
-    // ---- V rows that nobody sees: zeros, when the products' thread asks ----
-    int seq = 0, n_v = 0;  // ring tiles before this item
-    bool ok = true;
-#pragma unroll 1
-    for (int k = 0; ok; ++k) {
-      const int item = tc_nth(P, k);
-      if (item < 0) break;
-      const WinItem w = win_item(P, item);
-      int a, b;
-      tc_range(w, a, b);
-      if (a >= b) continue;
-#pragma unroll 1
-      for (int st = a; st < b && ok; ++st) {
-        const TcStep c = tc_step(w, st);
-        if (c.t0 + kTcKeys <= c.end) continue;
-        ok = warp_wait(v_ask, n_v++ & 1, P.err);
-        if (!ok) break;
-        uint8_t* tile = ring + (seq + 2 * (st - a) + 1) % NS * Sh::kTileBytes;
-        for (int h = 0; h < D / 64; ++h) {
-          uint4* base = reinterpret_cast<uint4*>(tile + h * 16384);
-          for (int j = (c.end - c.t0) * 8 + lane; j < 128 * 8; j += 32) base[j] = make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(v_ok);
-      }
-      seq += 2 * (b - a);
-    }
   } else {
     // ---- softmax of query tile t: a thread per row ----
     const int t = warp >> 2, row = (warp & 3) * 32 + lane;
@@ -402,17 +424,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
     for (int k = 0; ok; ++k) {
       const int item = tc_nth(P, k);
       if (item < 0) break;
-      const WinItem w = win_item(P, item);
-      const WinSeg& S = P.segs[w.seg];
-      int a, b;
-      tc_range(w, a, b);
+      const TcItem w = item_of(k, item);
       const TcTile q = tc_tile(P, w, t);
-      const TcNeed need = tc_need(P, w, q, a, b);
+      const TcNeed need = tc_need(P, w, q);
       const int pos = q.p0 + r_tok;
       float m = -INFINITY, l = 0.0f;  // m: of the scaled scores (log2)
       bool first = true;
 #pragma unroll 1
-      for (int st = a; st < b; ++st) {
+      for (int st = w.a; st < w.b; ++st) {
         if (!need(st)) continue;
         const TcStep c = tc_step(w, st);
         if (!warp_wait(&s_full[t], n_s & 1, P.err)) {
@@ -425,32 +444,58 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
         const bool whole = c.t0 + kTcKeys <= c.end &&
                            (c.sink || (c.t0 + kTcKeys - 1 <= q.p0 &&
                                        (c.t0 > q.p1 - P.window || c.t0 + kTcKeys <= P.n_sink)));
-        // the row's 128 scores in registers: mask, maximum, weights
-        uint32_t x[128];
+        const int hi = min(c.sink ? c.end - 1 : pos, c.end - 1) - c.t0;  // last column that the row sees
+        const int lo = c.sink ? 0 : pos - P.window + 1 - c.t0;            // first of the window
+        const int sk = c.sink ? 0 : P.n_sink - c.t0;                     // columns before it: first tokens
+        uint64_t sum[2] = {0, 0};
+        if (whole) {
+          // the row's 128 scores in registers: maximum, weights
+          uint32_t x[128];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, x + 32 * i);
-        tmem_wait_ld();
-        if (!whole) {
-          const int hi = min(c.sink ? c.end - 1 : pos, c.end - 1) - c.t0;  // last column that the row sees
-          const int lo = c.sink ? 0 : pos - P.window + 1 - c.t0;            // first of the window
-          const int sk = c.sink ? 0 : P.n_sink - c.t0;                     // columns before it: first tokens
+          for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, x + 32 * i);
+          tmem_wait_ld();
+          tc_maximum<D>(tc_max64(x + 64, tc_max64(x, -INFINITY)) * scale, first, m, l, to);
+          const float base = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < 4; ++i) tc_weights32(x + 32 * i, scale, base, sum, ts + 16 * i);
+        } else {
+          // 32 scores at a time, twice (little code: it is run through cold);
+          // a quarter that none of the warp's rows sees is skipped
+          uint32_t x[32];
+          auto quarter = [&](int i) {  // false: nobody sees it
             const int h = hi - 32 * i, g = lo - 32 * i, f = sk - 32 * i;
             const uint32_t le = h < 0 ? 0u : h >= 31 ? ~0u : (2u << h) - 1u;
             const uint32_t ge = g <= 0 ? ~0u : g >= 32 ? 0u : ~((1u << g) - 1u);
             const uint32_t lt = f <= 0 ? 0u : f >= 32 ? ~0u : (1u << f) - 1u;
             const uint32_t see = le & (ge | lt);
+            if (!__any_sync(0xffffffffu, see != 0u)) return false;
+            tmem_ld32(ts + 32 * i, x);
+            tmem_wait_ld();
+            if (!__all_sync(0xffffffffu, see == ~0u)) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (!((see >> j) & 1u)) x[32 * i + j] = 0xFF800000u;  // -inf
+              for (int j = 0; j < 32; ++j)
+                if (!((see >> j) & 1u)) x[j] = 0xFF800000u;  // -inf
+            }
+            return true;
+          };
+          float mx = -INFINITY;
+#pragma unroll 1
+          for (int i = 0; i < 4; ++i)
+            if (quarter(i)) mx = tc_max32(x, mx);
+          tc_maximum<D>(mx * scale, first, m, l, to);
+          const float base = m == -INFINITY ? 0.0f : m;
+          // weights of columns 32 i .. 32 i + 31 go to words 16 i .. 16 i + 15: over scores that have been read by then
+#pragma unroll 1
+          for (int i = 0; i < 4; ++i) {
+            if (quarter(i)) {
+              tc_weights32(x, scale, base, sum, ts + 16 * i);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) x[j] = 0u;
+              tmem_st16(ts + 16 * i, x);
+            }
           }
         }
-        tc_maximum<D>(tc_max64(x + 64, tc_max64(x, -INFINITY)) * scale, first, m, l, to);
-        const float base = m == -INFINITY ? 0.0f : m;
-        uint64_t sum[2] = {0, 0};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tc_weights32(x + 32 * i, scale, base, sum, ts + 16 * i);
         const float2 sa = unpack2(sum[0]), sb = unpack2(sum[1]);
         l += (sa.x + sa.y) + (sb.x + sb.y);
         tmem_wait_st();
@@ -461,7 +506,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
       if (!ok) break;
       // ---- outputs of the tile ----
       const bool mine = r_tok < q.n && row < tt * P.group;
-      const int64_t tok = S.q_row0 + w.tok0 + t * tt + r_tok;
+      const int64_t tok = w.q_row + t * tt + r_tok;
       const int head = w.hk * P.group + r_head;
       const float inv = l > 0.0f ? 1.0f / l : 0.0f;
       if (!first) {
