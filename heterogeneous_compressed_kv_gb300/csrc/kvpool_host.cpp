@@ -1351,7 +1351,7 @@ static int decode_attend(kvpool_t* p, int32_t layer, int32_t n, const int32_t* h
     len1 = fit_one_wave(src_1, len1, max_split_len, attend_target);
     int split2 = n_sh > 0 ? shared_splits(pd, gn, n_sh, p->n_sms) : 0;
     int splits0 = 0, splits1 = 0, parts = 0;
-    for (int pass = 0; pass < 2; ++pass) {
+    for (int pass = 0; pass < 3; ++pass) {
       splits0 = splits1 = parts = 0;
       for (int i = 0; i < gn; ++i) {
         AttendReq& R = P.reqs[i];
@@ -1368,7 +1368,7 @@ static int decode_attend(kvpool_t* p, int32_t layer, int32_t n, const int32_t* h
       }
       if (parts <= kMaxSplits) break;
       len0 = len1 = max_split_len;
-      split2 = std::min(split2, 4);  // of at most 256 requests
+      split2 = std::min(split2, pass == 0 ? 4 : 1);
     }
     if (parts > kMaxSplits) {
       rc = -1;
@@ -1397,7 +1397,7 @@ static int decode_attend(kvpool_t* p, int32_t layer, int32_t n, const int32_t* h
       if (e != cudaSuccess) rc = (int)e;
     }
     if (rc == 0 && n_sh > 0)
-      rc = p->launch(KVPOOL_KERNEL_ATTEND, bytes2, s0, [&](int* nk) { return launch_shared(P, n_sh, split2, s0, nk); });
+      rc = p->launch(KVPOOL_KERNEL_ATTEND, bytes2, s0, [&](int* nk) { return launch_shared(P, n_sh, split2, !fork, s0, nk); });
     P.pool.table = pd.table + 4LL * n_sh;  // part 0 sees the tables from each request's own blocks on
     if (rc == 0)
       rc = p->launch(KVPOOL_KERNEL_ATTEND, bytes0, s0, [&](int* nk) { return launch_attend(P, 0, ctas0, s0, nk); });

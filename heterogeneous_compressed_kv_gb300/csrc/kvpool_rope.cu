@@ -252,7 +252,8 @@ __global__ void __launch_bounds__(kRopeWarps * 32, T == KVPOOL_BF16 ? 8 : 5) rop
 
 bool heads_ok(const kvpool_heads* h, int32_t dtype) {
   const int64_t unit = dtype == KVPOOL_BF16 ? 8 : 4;  // values in 16 bytes
-  return reinterpret_cast<uintptr_t>(h->data) % 16 == 0 && h->token_stride % unit == 0 && h->head_stride % unit == 0;
+  return reinterpret_cast<uintptr_t>(h->data) % 16 == 0 && h->token_stride % unit == 0 && h->head_stride % unit == 0 &&
+         h->token_stride >= 0 && h->head_stride >= 0;
 }
 
 }  // namespace

@@ -361,7 +361,7 @@ cudaError_t launch_mma_t(const AttendParams& p, const SharedShape& h, cudaStream
   constexpr int smem = MmaShared<D>::kSmem;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return launch_kernel(true, kern, dim3(p.pool.heads, h.n_split, (p.n + kSharedRows - 1) / kSharedRows),
+  return launch_kernel(h.pdl != 0, kern, dim3(p.pool.heads, h.n_split, (p.n + kSharedRows - 1) / kSharedRows),
                        dim3(kMmaWarps * 32), smem, s, p, h);
 }
 // the fewest groups of 16 requests that hold a CTA's
@@ -376,7 +376,7 @@ cudaError_t launch_shared_t(const AttendParams& p, const SharedShape& h, cudaStr
   constexpr int smem = (int)sizeof(FmaSmem<D>);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return launch_kernel(true, kern, dim3(p.pool.heads, h.n_split, (p.n + kFmaRows - 1) / kFmaRows),
+  return launch_kernel(h.pdl != 0, kern, dim3(p.pool.heads, h.n_split, (p.n + kFmaRows - 1) / kFmaRows),
                        dim3(kFmaThreads), smem, s, p, h);
 }
 
@@ -407,8 +407,8 @@ int shared_splits(const PoolDesc& pd, int n, int n_entries, int n_sms) {
   return std::max(1, std::min(mma ? n_sms / per : 3 * n_sms / per, (n_entries + 63) / 64));
 }
 
-int launch_shared(const AttendParams& p, int n_entries, int n_split, void* stream, int* n_kernels) {
-  const SharedShape h{n_entries, n_split, p.reqs[0].slot};
+int launch_shared(const AttendParams& p, int n_entries, int n_split, bool pdl, void* stream, int* n_kernels) {
+  const SharedShape h{n_entries, n_split, p.reqs[0].slot, pdl};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   *n_kernels += 1;
   switch (p.pool.in_dtype * 3 + p.pool.cache_dtype) {

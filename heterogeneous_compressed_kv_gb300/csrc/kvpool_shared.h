@@ -9,6 +9,7 @@ namespace kvp {
 
 struct SharedShape {
   int32_t n_entries, n_split, slot;  // slot: the request whose table holds the shared ids
+  int32_t pdl;                       // programmatic dependent launch
 };
 
 // the block id of shared entry e as it stands in the table, and the entry's

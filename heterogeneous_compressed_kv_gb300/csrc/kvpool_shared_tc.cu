@@ -355,7 +355,7 @@ cudaError_t launch_t(const AttendParams& p, const SharedShape& h, cudaStream_t s
   auto* kern = shared_tc_kernel<D>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D>::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_kernel(true, kern, dim3(p.pool.heads, h.n_split, (p.n + kSharedTcRows - 1) / kSharedTcRows),
+  return launch_kernel(h.pdl != 0, kern, dim3(p.pool.heads, h.n_split, (p.n + kSharedTcRows - 1) / kSharedTcRows),
                        dim3(kThreads), Shape<D>::kSmem, s, p, h);
 }
 

@@ -266,8 +266,8 @@ int plan_launch(const kvpool_window_args* a, Form form, bool tc, int32_t i0, int
   const int Hk = a->k.heads;
   int64_t most = 1;  // queries of a single-token segment
   if (form == kFormTok)
-    for (int j = i0; j < n; ++j)
-      if (form_of(a, tc, q_len[j], k_len[j]) == form) most = std::max(most, q_len[j]);
+    for (int j = i0, m = 0; j < n && m < kMaxWinSegs; ++j)
+      if (q_len[j] > 0 && form_of(a, tc, q_len[j], k_len[j]) == form) most = std::max(most, q_len[j]), ++m;
   P->tile_tokens = form == kFormTok  ? (int32_t)most
                    : form == kFormTc ? 2 * (kTcTileRows / P->group)
                                      : kFmaRows / P->group;

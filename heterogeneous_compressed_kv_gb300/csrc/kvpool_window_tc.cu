@@ -17,9 +17,8 @@
 // relative precision up to 2^8, the sums are fp32), so the read-modify-write
 // of O leaves the critical path.
 //
-// Rows of K and V behind a segment never count: scores are masked, and such V
-// rows are zeroed in shared memory before the product (0 times a NaN there
-// would reach every row).
+// Rows of K and V behind a segment, or between the first tokens and the window,
+// never count: scores are masked, and such V rows are not copied.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -45,7 +44,7 @@ struct TcShape {
 };
 
 struct TcMaps {
-  CUtensorMap q, k, v;
+  CUtensorMap q, k, v, v16, v1;  // v16, v1: boxes of 16 rows and of one
 };
 
 // A work item as the roles take it: its keys are the first n_s tokens and n_w
@@ -69,6 +68,12 @@ __device__ __forceinline__ TcStep tc_step(const TcItem& w, int st) {
   c.t0 = c.sink ? st * kTcKeys : w.lo + (st - st_s) * kTcKeys;
   c.end = c.sink ? w.n_s : w.lo + w.n_w;
   return c;
+}
+// Rows of the step's tile that hold values; the others, behind the first tokens
+// or behind the segment, may hold anything
+__device__ __forceinline__ int tc_valid(const TcItem& w, int st) {
+  const TcStep c = tc_step(w, st);
+  return min(kTcKeys, (c.sink ? c.end : w.k_len) - c.t0);
 }
 // A query tile of an item: n tokens at positions p0 .. p1
 struct TcTile {
@@ -193,7 +198,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
   uint8_t* ring = smem + 2 * Sh::kTileBytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Sh::kBarOff);
   uint64_t *kv_full = bars, *kv_free = kv_full + NS, *q_full = kv_free + NS, *q_free = q_full + 2, *s_full = q_free + 2,
-           *p_ready = s_full + 2, *o_full = p_ready + 2, *o_free = o_full + 2, *v_ok = o_free + 2, *drain = v_ok + NS;
+           *p_ready = s_full + 2, *o_full = p_ready + 2, *o_free = o_full + 2, *drain = o_free + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   TcItem* table = reinterpret_cast<TcItem*>(smem + Sh::kTableOff);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -201,7 +206,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
     for (int i = 0; i < NS; ++i) {
       mbar_init(&kv_full[i], 1);
       mbar_init(&kv_free[i], 1);
-      mbar_init(&v_ok[i], 1);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&q_full[t], 1);
@@ -237,14 +241,37 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
     int stage = 0, n_q[2] = {0, 0}, issued = 0;
     uint32_t round = 0;  // of the ring
     bool ok = true;
-    auto load = [&](const CUtensorMap* map, int hk, int row) {
+    // the tile's first `valid` rows
+    auto load = [&](const CUtensorMap* map, int hk, int row, int valid) {
       if (round > 0) ok = ok && warp_wait(&kv_free[stage], (round - 1) & 1, P.err);
       if (!ok) return;
-      if (leader) {
-        mbar_arrive_expect_tx(&kv_full[stage], Sh::kTileBytes);
+      uint8_t* tile = ring + stage * Sh::kTileBytes;
+      if (valid == kTcKeys) {
+        if (leader) {
+          mbar_arrive_expect_tx(&kv_full[stage], Sh::kTileBytes);
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c)
-          tma_load_3d(ring + stage * Sh::kTileBytes + c * 16384, map, 64 * c, hk, row, &kv_full[stage]);
+          for (int c = 0; c < D / 64; ++c) tma_load_3d(tile + c * 16384, map, 64 * c, hk, row, &kv_full[stage]);
+        }
+      } else {
+        // A V tile that ends early: its rows in boxes of 16 and of 1, and zeros
+        // in the rest of the last 16 (the product takes whole groups of 16; 0
+        // times a NaN there would reach every row)
+        const int n16 = (valid + 15) / 16;
+        for (int h = 0; h < D / 64; ++h) {
+          uint4* base = reinterpret_cast<uint4*>(tile + h * 16384);
+          for (int j = valid * 8 + lane; j < n16 * 128; j += 32) base[j] = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (leader) {
+          mbar_arrive_expect_tx(&kv_full[stage], valid * D * 2);
+          for (int r = 0; r < valid;) {
+            const bool many = valid - r >= 16;
+            for (int c = 0; c < D / 64; ++c)
+              tma_load_3d(tile + c * 16384 + r * 128, many ? &M.v16 : &M.v1, 64 * c, hk, row + r, &kv_full[stage]);
+            r += many ? 16 : 1;
+          }
+        }
       }
       __syncwarp();
       ++issued;
@@ -276,24 +303,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
       for (int st = w.a; st < w.b && ok; ++st) {
         const int t0 = tc_step(w, st).t0;
         if (st == w.a) load_q(0);
-        if (ok) load(&M.k, w.hk, w.k_row + t0);
+        if (ok) load(&M.k, w.hk, w.k_row + t0, kTcKeys);
         if (st == w.a && ok) load_q(1);
-        const int vs = stage;
-        const uint32_t vr = round;
-        if (ok) load(&M.v, w.hk, w.k_row + t0);
-        if (ok && w.k_len - t0 < kTcKeys) {
-          // V rows behind the segment: zeros, once the tile is there (only the
-          // segment's last tile; the copies after it wait that long)
-          ok = warp_wait(&kv_full[vs], vr & 1, P.err);
-          if (!ok) break;
-          for (int h = 0; h < D / 64; ++h) {
-            uint4* base = reinterpret_cast<uint4*>(ring + vs * Sh::kTileBytes + h * 16384);
-            for (int j = (w.k_len - t0) * 8 + lane; j < 128 * 8; j += 32) base[j] = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async();
-          __syncwarp();
-          if (leader) mbar_arrive(&v_ok[vs]);
-        }
+        if (ok) load(&M.v, w.hk, w.k_row + t0, tc_valid(w, st));
       }
     }
     // the CTA does not end while copies land in its shared memory
@@ -309,7 +321,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
       int stage = 0;
       uint32_t round = 0;
       int n_q[2] = {0, 0}, n_p[2] = {0, 0}, n_o[2] = {0, 0};
-      uint32_t v_par = 0;  // per stage: parity of its next v_ok phase
       bool ok = true;
       auto next = [&]() {
         if (++stage == NS) {
@@ -324,17 +335,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
         next();
         return s;
       };
-      // O_t += P_t V, V in ring stage vs
-      auto outputs = [&](int t, int vs, bool begun, bool last) {
+      // O_t += P_t V, V in ring stage vs, over n16 groups of 16 keys
+      auto outputs = [&](int t, int vs, int n16, bool begun, bool last) {
         ok = ok && mbar_wait_word(&p_ready[t], n_p[t] & 1, P.err);
         ++n_p[t];
         if (ok && !begun && n_o[t] > 0) ok = mbar_wait_word(&o_free[t], (n_o[t] - 1) & 1, P.err);
         if (!ok) return;
         tc_fence_after();
         const uint64_t vd = v_desc + vs * (Sh::kTileBytes >> 4);
+        if (n16 == kTcKeys / 16) {
 #pragma unroll
-        for (int c = 0; c < kTcKeys / 16; ++c)
-          mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * c, vd + c * (2048 >> 4), kIdPV, begun || c > 0);
+          for (int c = 0; c < kTcKeys / 16; ++c)
+            mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * c, vd + c * (2048 >> 4), kIdPV, begun || c > 0);
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < n16; ++c)
+            mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * c, vd + c * (2048 >> 4), kIdPV, begun || c > 0);
+        }
         if (last) {
           mma_commit(&o_full[t]);
           ++n_o[t];
@@ -368,7 +385,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
         const TcNeed need[2] = {tc_need(P, w, q[0]), tc_need(P, w, q[1])};
         const int last[2] = {need[0].last(a), need[1].last(a)};
         bool seen_q[2] = {false, false}, seen_pv[2] = {false, false};
-        int vs = 0;
+        int vs = 0, v16 = 0;  // of the step before: V's stage and its groups of 16 keys
         // round st: outputs of step st - 1, then scores of step st
 #pragma unroll 1
         for (int st = a; st <= b && ok; ++st) {
@@ -378,7 +395,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             if (ok && st > a && need[t](st - 1)) {
-              outputs(t, vs, seen_pv[t], st - 1 == last[t]);
+              outputs(t, vs, v16, seen_pv[t], st - 1 == last[t]);
               seen_pv[t] = true;
             }
             if (ok && st < b && need[t](st)) {
@@ -391,10 +408,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
           if (st == b) break;
           mma_commit(&kv_free[ks]);
           vs = take();
-          if (ok && w.k_len - tc_step(w, st).t0 < kTcKeys) {  // its rows behind the segment have been zeroed
-            ok = mbar_wait_word(&v_ok[vs], (v_par >> vs) & 1, P.err);
-            v_par ^= 1u << vs;
-          }
+          v16 = (tc_valid(w, st) + 15) / 16;
         }
         // a tile whose rows need no step was loaded all the same: take its Q
 #pragma unroll
@@ -612,8 +626,9 @@ int launch_window_tc(const WinParams& P, int head_dim, int64_t q_rows, int64_t k
   const cuuint64_t kd[3] = {d, hk, (cuuint64_t)kv_rows};
   const cuuint64_t ks[2] = {stride_bytes(P.k_head, hk), stride_bytes(P.k_tok, kv_rows)};
   const cuuint64_t vs[2] = {stride_bytes(P.v_head, hk), stride_bytes(P.v_tok, kv_rows)};
-  const cuuint32_t kb[3] = {64, 1, kTcKeys};
-  if (!encode(&M.q, P.q, 4, qd, qs, qb) || !encode(&M.k, P.k, 3, kd, ks, kb) || !encode(&M.v, P.v, 3, kd, vs, kb))
+  const cuuint32_t kb[3] = {64, 1, kTcKeys}, b16[3] = {64, 1, 16}, b1[3] = {64, 1, 1};
+  if (!encode(&M.q, P.q, 4, qd, qs, qb) || !encode(&M.k, P.k, 3, kd, ks, kb) || !encode(&M.v, P.v, 3, kd, vs, kb) ||
+      !encode(&M.v16, P.v, 3, kd, vs, b16) || !encode(&M.v1, P.v, 3, kd, vs, b1))
     return (int)cudaErrorInvalidValue;
   const int ctas = P.n_items < n_sms ? P.n_items : n_sms;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

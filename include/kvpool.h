@@ -427,9 +427,9 @@ int kvpool_qk_norm_rope(int32_t dtype, int32_t head_dim, int64_t n_tokens, const
  * 16) of k.heads: query head h reads key head h / (q.heads / k.heads).
  * out: like q, in dtype; d_lse: [q_rows][q.heads] fp32 natural-log sums of
  * the exponentials, or NULL.  Query rows behind the last segment are left as
- * they were.  K/V rows outside the segments are never let into a result; the
- * values of a segment's own rows should be finite (a NaN or infinity in a
- * value row may reach queries of the same tile that do not see it).
+ * they were.  K/V rows that no query of a segment sees (outside it, between
+ * the first tokens and the window) may hold anything; a NaN or infinity in a
+ * value row that some queries see may also reach queries nearby that do not.
  * dtype: KVPOOL_F32 (fp32 throughout) or KVPOOL_BF16 (softmax statistics and
  * sums in fp32); head_dim 64 or 128; window and n_sink >= 0.
  * d_workspace: kvpool_window_workspace bytes (16-byte aligned, may be NULL

@@ -130,6 +130,53 @@ def test_long_single_tokens_split_and_merge():
     run([2], [9000], 4, 4, 128, BF, 4096, 500)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("ql,kl,window,sink", [([200], [1000], 100, 4), ([1, 300], [900, 2000], 130, 140), ([17], [600], 64, 1),
+                                               ([700], [5000], 256, 16)])
+def test_rows_that_nobody_sees_may_hold_anything(ql, kl, window, sink, dtype):
+    """NaN between the first tokens and the first query's window (tokens that were dropped there) changes nothing."""
+    q, k, v, ks = inputs(ql, kl, 4, 2, 128, dtype, gap=1)
+    want = K.window_attend(q, k, v, ql, ks, kl, window, sink)
+    for n, k0, m in zip(ql, ks, kl):
+        k[k0 + sink:k0 + m - n - window + 1] = math.nan
+        v[k0 + sink:k0 + m - n - window + 1] = math.nan
+    got = K.window_attend(q, k, v, ql, ks, kl, window, sink)
+    assert bool(torch.isfinite(got).all()) and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.2, 1e-30])
+@pytest.mark.parametrize("ql", [[1], [40]])
+def test_any_scale(ql, scale):
+    q, k, v, ks = inputs(ql, [300], 4, 2, 64, BF)
+    lse = torch.empty(q.shape[:2], device="cuda")
+    out = K.window_attend(q, k, v, ql, ks, [300], 100, 3, scale=scale, lse=lse)
+    check(out, lse, formula(q, k, v, ql, ks, [300], 100, 3, scale), q, k, abs(scale), BF, 300)
+
+
+@pytest.mark.parametrize("ql", [[1], [40]])
+def test_broadcast_key_heads(ql):
+    """One key head's rows seen as four by a stride of zero."""
+    q, k, v, ks = inputs(ql, [300], 4, 1, 64, BF)
+    want = K.window_attend(q, k, v, ql, ks, [300], 100, 3)
+    got = K.window_attend(q, k.expand(-1, 4, -1), v.expand(-1, 4, -1), ql, ks, [300], 100, 3)
+    # the same scores; weights are rounded to bf16 (half a step each) in either or both, and the outputs
+    assert float((got.float() - want.float()).norm() / want.float().norm()) <= 2.0 ** -7
+
+
+def test_two_streams_at_once():
+    q, k, v, ks = inputs([300, 1], [900, 4000], 8, 2, 128, BF, gap=0)
+    args = (q, k, v, [300, 1], ks, [900, 4000], 500, 4)
+    want = K.window_attend(*args)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    outs = []
+    for _ in range(10):
+        for s in streams:
+            outs.append(K.window_attend(*args, stream=s))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+
+
 def test_large_scores_keep_the_softmax_finite():
     q, k, v, ks = inputs([40], [40], 2, 2, 64, BF)
     q, k = q * 40, k * 40  # scores in the thousands: one key has all the weight
