@@ -284,25 +284,6 @@ def _like(t) -> tuple:
     return t.dtype, t.shape[-1], t.get_device(), t.element_size()
 
 
-class _on:
-    """A device as the current one."""
-
-    def __init__(self, index: int):
-        self.index = index
-
-    def __enter__(self):
-        from torch import _C
-        self.ctx = None
-        if _C._cuda_getDevice() != self.index:
-            import torch
-            self.ctx = torch.cuda.device(self.index)
-            self.ctx.__enter__()
-
-    def __exit__(self, *e):
-        if self.ctx is not None:
-            self.ctx.__exit__(*e)
-
-
 def _stream_of(stream, index: int) -> int:
     """The given stream, or the device's current one."""
     if stream is None:
@@ -311,13 +292,25 @@ def _stream_of(stream, index: int) -> int:
     return _stream(stream)
 
 
-def _empty(shape, dtype, device, stream, raw: int):
-    """torch.empty whose memory belongs to `stream`, the one that will use it."""
+def _fresh(t, stream, raw: int):
+    """An uninitialized contiguous tensor like t whose memory belongs to
+    `stream`, the one that will write it, and its kvpool_heads fields."""
+    import torch
+    n, heads, dim = t.shape
+    if stream is None or raw == torch._C._cuda_getCurrentRawStream(t.get_device()):
+        o = torch.empty((n, heads, dim), dtype=t.dtype, device=t.device)
+    else:
+        with torch.cuda.stream(torch.cuda.ExternalStream(raw, device=t.device)):
+            o = torch.empty((n, heads, dim), dtype=t.dtype, device=t.device)
+    return o, (o.data_ptr(), heads * dim if n > 1 else 0, dim if heads > 1 else 0, heads, 0)
+
+
+def _fresh_bytes(n: int, device, stream, raw: int):
     import torch
     if stream is None or raw == torch._C._cuda_getCurrentRawStream(device.index):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(n, dtype=torch.uint8, device=device)
     with torch.cuda.stream(torch.cuda.ExternalStream(raw, device=device)):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(n, dtype=torch.uint8, device=device)
 
 
 def _need(t, what: str, dtype, shape, index: int) -> int:
@@ -364,36 +357,47 @@ def qk_norm_rope(q, k, positions, table, q_weight=None, k_weight=None, eps: floa
     x = q if q is not None else k
     if x is None or not x.is_cuda:
         raise ValueError("qk_norm_rope: q or k must be a CUDA tensor")
-    kind, like, dev = _dtype(x), _like(x), x.device
+    like = _like(x)
     index = like[2]
-    with _on(index):
-        raw = _stream_of(stream, index)
-        heads, outs = [None] * 4, [None, None]
-        for i, (t, o) in enumerate(((q, out_q), (k, out_k))):
-            if t is None:
-                continue
-            heads[i] = _HEADS.pack(*_rows(t, "qk"[i], like))
-            if t.shape[0] != x.shape[0]:
-                raise ValueError("qk_norm_rope: q and k must have the same tokens")
-            if o is None:
-                o = _empty(t.shape, t.dtype, dev, stream, raw)
-            elif o.shape != t.shape:
-                raise ValueError(f"qk_norm_rope: out_{'qk'[i]} must have the shape of {'qk'[i]}")
-            heads[2 + i] = _HEADS.pack(*_rows(o, "out_" + "qk"[i], like, True))
-            outs[i] = o
-        T, _, D = x.shape
-        rot = tab = pos = 0
-        if table is not None:
-            rot = 2 * table.numel()
-            tab = _need(table, "table", torch.int64, (rot // 2,), index)
-            pos = _need(positions, "positions", torch.int64, (T,), index)
-        qw = None if q_weight is None else _need(q_weight, "q_weight", torch.float32, (D,), index)
-        kw = None if k_weight is None else _need(k_weight, "k_weight", torch.float32, (D,), index)
-        rc = lib().kvpool_qk_norm_rope(kind, D, T, *heads, qw, kw, eps, rot, 1 if interleaved else 0, tab or None,
-                                       pos or None, raw)
+    if torch._C._cuda_getDevice() != index:
+        with torch.cuda.device(index):
+            return qk_norm_rope(q, k, positions, table, q_weight, k_weight, eps, interleaved, out_q, out_k, stream)
+    kind = _dtype(x)
+    raw = _stream_of(stream, index)
+    T = x.shape[0]
+    qi = ki = qo = ko = None
+    if q is not None:
+        qi = _HEADS.pack(*_rows(q, "q", like))
+        if out_q is None:
+            out_q, r = _fresh(q, stream, raw)
+        else:
+            r = _rows(out_q, "out_q", like, True)
+            if out_q.shape != q.shape:
+                raise ValueError("qk_norm_rope: out_q must have the shape of q")
+        qo = _HEADS.pack(*r)
+    if k is not None:
+        ki = _HEADS.pack(*_rows(k, "k", like))
+        if k.shape[0] != T:
+            raise ValueError("qk_norm_rope: q and k must have the same tokens")
+        if out_k is None:
+            out_k, r = _fresh(k, stream, raw)
+        else:
+            r = _rows(out_k, "out_k", like, True)
+            if out_k.shape != k.shape:
+                raise ValueError("qk_norm_rope: out_k must have the shape of k")
+        ko = _HEADS.pack(*r)
+    D = like[1]
+    rot, tab, pos = 0, None, None
+    if table is not None:
+        rot = 2 * table.numel()
+        tab = _need(table, "table", torch.int64, (rot // 2,), index) or None
+        pos = _need(positions, "positions", torch.int64, (T,), index) or None
+    qw = None if q_weight is None else _need(q_weight, "q_weight", torch.float32, (D,), index)
+    kw = None if k_weight is None else _need(k_weight, "k_weight", torch.float32, (D,), index)
+    rc = lib().kvpool_qk_norm_rope(kind, D, T, qi, ki, qo, ko, qw, kw, eps, rot, 1 if interleaved else 0, tab, pos, raw)
     if rc != OK:
         raise KvpoolError(rc, "qk_norm_rope refused its arguments" if rc == ERR_INVALID_ARG else "qk_norm_rope: CUDA error")
-    return outs[0], outs[1]
+    return out_q if q is not None else None, out_k if k is not None else None
 
 
 def window_attend(q, k, v, q_len, k_start, k_len, window: int, n_sink: int = 0, scale=None, out=None, lse=None,
@@ -407,24 +411,30 @@ def window_attend(q, k, v, q_len, k_start, k_len, window: int, n_sink: int = 0, 
     import torch
     if not q.is_cuda:
         raise ValueError("window_attend: the tensors must be CUDA tensors")
-    dev = q.device
-    with _on(dev.index):
-        raw = _stream_of(stream, dev.index)
-        if out is None:
-            out = _empty(q.shape, q.dtype, dev, stream, raw)
-        call = _window_call(q, k, v, q_len, k_start, k_len, window, n_sink, scale, out, lse)
-        L = lib()
-        rc = L.kvpool_window_workspace(*call)
-        if rc >= 0:
-            nbytes = 0
-            if workspace is not None:
-                if workspace.device != dev or not workspace.is_contiguous():
-                    raise ValueError("window_attend: workspace must be a contiguous tensor on the queries' device")
-                nbytes = workspace.numel() * workspace.element_size()
-            elif rc > 0:
-                nbytes = rc
-                workspace = _empty((rc,), torch.uint8, dev, stream, raw)
-            rc = L.kvpool_window_attend(*call, workspace.data_ptr() if nbytes else None, nbytes, raw)
+    like = _like(q)
+    index = like[2]
+    if torch._C._cuda_getDevice() != index:
+        with torch.cuda.device(index):
+            return window_attend(q, k, v, q_len, k_start, k_len, window, n_sink, scale, out, lse, workspace, stream)
+    raw = _stream_of(stream, index)
+    rows = _rows(q, "q", like)
+    if out is None:
+        out, o = _fresh(q, stream, raw)
+    else:
+        o = _rows(out, "out", like, True)
+    call = _window_call(q, like, rows, k, v, q_len, k_start, k_len, window, n_sink, scale, out, o, lse)
+    L = lib()
+    rc = L.kvpool_window_workspace(*call)
+    if rc >= 0:
+        nbytes = 0
+        if workspace is not None:
+            if workspace.get_device() != index or not workspace.is_contiguous():
+                raise ValueError("window_attend: workspace must be a contiguous tensor on the queries' device")
+            nbytes = workspace.numel() * workspace.element_size()
+        elif rc > 0:
+            nbytes = rc
+            workspace = _fresh_bytes(rc, q.device, stream, raw)
+        rc = L.kvpool_window_attend(*call, workspace.data_ptr() if nbytes else None, nbytes, raw)
     if rc != OK:
         raise KvpoolError(rc, "window_attend refused its arguments" if rc == ERR_INVALID_ARG else "window_attend: CUDA error")
     return out
@@ -432,8 +442,11 @@ def window_attend(q, k, v, q_len, k_start, k_len, window: int, n_sink: int = 0, 
 
 def window_workspace(q, k, v, q_len, k_start, k_len, window: int, n_sink: int = 0) -> int:
     """Workspace bytes of window_attend with these arguments."""
-    with _on(q.device.index):
-        call = _window_call(q, k, v, q_len, k_start, k_len, window, n_sink, None, q, None)
+    import torch
+    like = _like(q)
+    with torch.cuda.device(like[2]):
+        rows = _rows(q, "q", like)
+        call = _window_call(q, like, rows, k, v, q_len, k_start, k_len, window, n_sink, None, q, rows, None)
         rc = int(lib().kvpool_window_workspace(*call))
     if rc < 0:
         raise KvpoolError(rc, "window_workspace refused its arguments")
@@ -448,22 +461,21 @@ def window_check(stream=None) -> tuple:
     return int(rc), int(w.value)
 
 
-def _window_call(q, k, v, q_len, k_start, k_len, window, n_sink, scale, out, lse):
+def _window_call(q, like, q_rows, k, v, q_len, k_start, k_len, window, n_sink, scale, out, out_rows, lse):
     """(args, n, lengths) as kvpool_window_attend takes them (copies in bytes objects: quicker than array addresses)."""
     if k.shape != v.shape or out.shape != q.shape:
         raise ValueError("window_attend: k and v, and q and out, must have the same shape")
     z = 0
     if lse is not None:
         import torch
-        z = _need(lse, "lse", torch.float32, q.shape[:2], q.get_device())
+        z = _need(lse, "lse", torch.float32, q.shape[:2], like[2])
     ql, ks, kl = _i64(q_len), _i64(k_start), _i64(k_len)
     if not ql.size == ks.size == kl.size:
         raise ValueError("window_attend: q_len, k_start and k_len must have one value per segment")
-    rows, D, like = q.shape[0], q.shape[-1], _like(q)
+    D = like[1]
     try:
-        a = _WINDOW_ARGS.pack(_dtype(q), D, *_rows(q, "q", like), *_rows(k, "k", like), *_rows(v, "v", like),
-                              *_rows(out, "out", like, out is not q), rows, k.shape[0], z, window, n_sink,
-                              D ** -0.5 if scale is None else scale, 0)
+        a = _WINDOW_ARGS.pack(_dtype(q), D, *q_rows, *_rows(k, "k", like), *_rows(v, "v", like), *out_rows, q.shape[0],
+                              k.shape[0], z, window, n_sink, D ** -0.5 if scale is None else scale, 0)
     except (struct.error, OverflowError) as e:
         raise ValueError(f"window_attend: {e}") from None
     return a, ql.size, ql.tobytes(), ks.tobytes(), kl.tobytes()
@@ -615,7 +627,7 @@ class Pool:
         """decode_attend of requests whose first n_shared tokens are the same
         blocks, whose HCA entries are read once for all of them."""
         req = _i32(req_ids)
-        rc = self.L.kvpool_decode_attend_shared(self.h, layer, req.size, req.ctypes.data, n_shared, _ptr(q), _ptr(q_idx),
+        rc = self.L.kvpool_decode_attend_shared(self.h, layer, req.size, req.tobytes(), n_shared, _ptr(q), _ptr(q_idx),
                                                 top_k, _ptr(out), _ptr(topk_out), _stream(stream))
         return self._check(rc, "decode_attend_shared") if check else rc
 
