@@ -320,6 +320,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_ready[j & 1]);
     }
+    // the outputs of the tile before the last one may be on their way too: its
+    // phase first (the barrier tells two phases apart, not three)
+    if (ok && n_tile > 1) ok = warp_wait(pv_done, (n_tile - 2) & 1, err);
     if (ok && n_tile > 0) ok = warp_wait(pv_done, (n_tile - 1) & 1, err);
     tc_fence_after();
     float theirs = 0.0f;
