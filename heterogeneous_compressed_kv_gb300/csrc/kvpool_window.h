@@ -75,7 +75,8 @@ __device__ __forceinline__ WinItem win_item(const WinParams& P, int item) {
   w.pos0 = S.k_len - S.q_len + w.tok0;
   const int hi = w.pos0 + w.n_tok - 1;  // the last query's own position
   w.lo = max(0, w.pos0 - P.window + 1);
-  w.n_w = max(0, hi - w.lo + 1);
+  // a window of 0: of these, only the first tokens are anybody's
+  w.n_w = max(0, (P.window > 0 ? hi : min(hi, P.n_sink - 1)) - w.lo + 1);
   w.n_s = max(0, min(P.n_sink, min(w.lo, hi + 1)));
   return w;
 }

@@ -71,9 +71,9 @@ __device__ __forceinline__ TcStep tc_step(const TcItem& w, int st) {
 }
 // Rows of the step's tile that hold values; the others, behind the first tokens
 // or behind the segment, may hold anything
-__device__ __forceinline__ int tc_valid(const TcItem& w, int st) {
+__device__ __forceinline__ int tc_valid(const WinParams& P, const TcItem& w, int st) {
   const TcStep c = tc_step(w, st);
-  return min(kTcKeys, (c.sink ? c.end : w.k_len) - c.t0);
+  return min(kTcKeys, (c.sink || P.window == 0 ? c.end : w.k_len) - c.t0);
 }
 // A query tile of an item: n tokens at positions p0 .. p1
 struct TcTile {
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
         if (st == w.a) load_q(0);
         if (ok) load(&M.k, w.hk, w.k_row + t0, kTcKeys);
         if (st == w.a && ok) load_q(1);
-        if (ok) load(&M.v, w.hk, w.k_row + t0, tc_valid(w, st));
+        if (ok) load(&M.v, w.hk, w.k_row + t0, tc_valid(P, w, st));
       }
     }
     // the CTA does not end while copies land in its shared memory
@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
           if (st == b) break;
           mma_commit(&kv_free[ks]);
           vs = take();
-          v16 = (tc_valid(w, st) + 15) / 16;
+          v16 = (tc_valid(P, w, st) + 15) / 16;
         }
         // a tile whose rows need no step was loaded all the same: take its Q
 #pragma unroll

@@ -254,3 +254,24 @@ def test_refusals():
     if K.window_workspace(**call):
         with pytest.raises(K.KvpoolError):
             K.window_attend(**call, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("ql,kl,sink", [([150], [400], 7), ([150], [160], 40), ([200, 3], [200, 300], 0), ([20], [20], 9)])
+def test_a_window_of_nothing_reads_the_first_tokens_alone(ql, kl, sink, dtype):
+    """With window 0 no query sees a row behind the first tokens: NaN there changes nothing."""
+    q, k, v, ks = inputs(ql, kl, 4, 2, 64, dtype, gap=1)
+    want = formula(q, k, v, ql, ks, kl, 0, sink, 0.125)
+    for k0, m in zip(ks, kl):
+        k[k0 + sink:k0 + m] = math.nan
+        v[k0 + sink:k0 + m] = math.nan
+    lse = torch.empty(q.shape[:2], device="cuda")
+    check(K.window_attend(q, k, v, ql, ks, kl, 0, sink, lse=lse), lse, want, q, k, 0.125, dtype, max(sink, 1))
+
+
+def test_more_items_than_a_cta_works_out_at_its_start():
+    """16,384 work items: over 96 for each of 152 persistent CTAs."""
+    r = np.random.RandomState(2)
+    ql = [int(x) for x in r.randint(17, 21, 256)]
+    kl = [n + int(x) for n, x in zip(ql, r.randint(0, 30, 256))]
+    run(ql, kl, 64, 64, 64, BF, 24, 2, gap=0)
