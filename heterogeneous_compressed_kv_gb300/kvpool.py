@@ -440,13 +440,15 @@ def window_attend(q, k, v, q_len, k_start, k_len, window: int, n_sink: int = 0, 
     return out
 
 
-def window_workspace(q, k, v, q_len, k_start, k_len, window: int, n_sink: int = 0) -> int:
+def window_workspace(q, k, v, q_len, k_start, k_len, window: int, n_sink: int = 0, scale=None) -> int:
     """Workspace bytes of window_attend with these arguments."""
     import torch
     like = _like(q)
     with torch.cuda.device(like[2]):
         rows = _rows(q, "q", like)
-        call = _window_call(q, like, rows, k, v, q_len, k_start, k_len, window, n_sink, None, q, rows, None)
+        # an output like q, which may be a view that no output could have
+        o = (rows[0], q.shape[1] * q.shape[2], q.shape[2], q.shape[1], 0)
+        call = _window_call(q, like, rows, k, v, q_len, k_start, k_len, window, n_sink, scale, q, o, None)
         rc = int(lib().kvpool_window_workspace(*call))
     if rc < 0:
         raise KvpoolError(rc, "window_workspace refused its arguments")

@@ -275,3 +275,23 @@ def test_more_items_than_a_cta_works_out_at_its_start():
     ql = [int(x) for x in r.randint(17, 21, 256)]
     kl = [n + int(x) for n, x in zip(ql, r.randint(0, 30, 256))]
     run(ql, kl, 64, 64, 64, BF, 24, 2, gap=0)
+
+
+@pytest.mark.parametrize("scale", [None, -0.3])
+def test_workspace_of_the_same_arguments_is_enough(scale):
+    """Scales that are not positive go to another form of the kernel, which may want another workspace."""
+    q, k, v, ks = inputs([40], [5000], 2, 1, 64, BF)
+    args = (q, k, v, [40], ks, [5000], 4096, 3)
+    space = torch.empty(max(K.window_workspace(*args, scale=scale), 1), dtype=torch.uint8, device="cuda")
+    assert space.numel() > 1
+    got = K.window_attend(*args, scale=scale, workspace=space)
+    s = 0.125 if scale is None else scale
+    check(got, None, formula(q, k, v, [40], ks, [5000], 4096, 3, s), q, k, abs(s), BF, 5000)
+
+
+def test_window_workspace_of_broadcast_queries():
+    q = torch.zeros((1, 2, 64), device="cuda", dtype=BF).expand(40, -1, -1)
+    k = torch.zeros((5000, 1, 64), device="cuda", dtype=BF)
+    args = (q, k, k, [40], [0], [5000], 4096)
+    assert K.window_workspace(*args) > 0
+    assert K.window_attend(*args).shape == (40, 2, 64)
