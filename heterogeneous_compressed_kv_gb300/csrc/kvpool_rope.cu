@@ -298,6 +298,9 @@ extern "C" int kvpool_qk_norm_rope(int32_t dtype, int32_t head_dim, int64_t n_to
     if (n_tokens > 0 && (!in[i]->data || !out[i]->data)) return KVPOOL_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(wt[i]) % 16 != 0) return KVPOOL_ERR_INVALID_ARG;
     if (!heads_ok(in[i], dtype) || !heads_ok(out[i], dtype)) return KVPOOL_ERR_INVALID_ARG;
+    // no two heads of an output start in the same values (axes of length 1: any stride)
+    if ((n_tokens > 1 && out[i]->token_stride < head_dim) || (out[i]->heads > 1 && out[i]->head_stride < head_dim))
+      return KVPOOL_ERR_INVALID_ARG;
     RopeTensor& X = P.t[i];
     X.in = static_cast<const uint8_t*>(in[i]->data);
     X.out = static_cast<uint8_t*>(const_cast<void*>(out[i]->data));

@@ -203,6 +203,11 @@ bool strides_ok(const kvpool_heads& h, int32_t dtype) {
          h.token_stride >= 0 && h.head_stride >= 0;
 }
 
+// no two heads of an output start in the same values (axes of length 1: any stride)
+bool rows_apart(const kvpool_heads& h, int64_t tokens, int32_t dim) {
+  return (tokens <= 1 || h.token_stride >= dim) && (h.heads <= 1 || h.head_stride >= dim);
+}
+
 int check_args(const kvpool_window_args* a, int32_t n, const int64_t* q_len, const int64_t* k_start,
                const int64_t* k_len, int64_t* total_q) {
   if (!a || n < 0) return KVPOOL_ERR_INVALID_ARG;
@@ -215,7 +220,7 @@ int check_args(const kvpool_window_args* a, int32_t n, const int64_t* q_len, con
     return KVPOOL_ERR_INVALID_ARG;
   if (a->q_rows > 0x7FFFFFFF || a->kv_rows > 0x7FFFFFFF) return KVPOOL_ERR_INVALID_ARG;
   if (!strides_ok(a->q, a->dtype) || !strides_ok(a->k, a->dtype) || !strides_ok(a->v, a->dtype) ||
-      !strides_ok(a->out, a->dtype))
+      !strides_ok(a->out, a->dtype) || !rows_apart(a->out, a->q_rows, a->head_dim))
     return KVPOOL_ERR_INVALID_ARG;
   if (n > 0 && (!q_len || !k_start || !k_len)) return KVPOOL_ERR_INVALID_ARG;
   int64_t q = 0;

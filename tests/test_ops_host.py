@@ -101,6 +101,13 @@ def test_window_without_work():
     assert window([1], [0], [5], n=-1) == K.ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("bad", [dict(ts=0), dict(hs=0), dict(ts=32), dict(hs=56)])
+def test_outputs_that_share_values_are_refused(bad):
+    assert rope(qo=heads(**bad)) == K.ERR_INVALID_ARG
+    assert rope(ko=heads(**bad)) == K.ERR_INVALID_ARG
+    assert window([2], [0], [5], out=heads(8, **bad)) == K.ERR_INVALID_ARG
+
+
 def test_shared_decode_refuses_what_is_not_shared():
     from tests.test_abi_host import base_workload, cfg_of
     p = K.Pool(cfg_of(base_workload(layer_kinds=[K.HCA])))
