@@ -43,7 +43,7 @@ __device__ __forceinline__ float4 codes4(const uint8_t* row, int i) {
 template <int IN, int CACHE, int D>
 __global__ void __launch_bounds__(kFmaThreads) shared_fma_kernel(const __grid_constant__ AttendParams P,
                                                                  const __grid_constant__ SharedShape H) {
-  pdl_start();
+  shared_start(H);
   extern __shared__ __align__(16) uint8_t smem_raw[];
   FmaSmem<D>& sm = *reinterpret_cast<FmaSmem<D>*>(smem_raw);
   __shared__ float scales[2][kFmaKeys];
@@ -108,6 +108,7 @@ __global__ void __launch_bounds__(kFmaThreads) shared_fma_kernel(const __grid_co
     t.put(P.part_o + slot * pd.HD + h * D, r, tx);
     if (tx == 0) *reinterpret_cast<float2*>(P.part_ml + (slot * pd.heads + h) * 2) = make_float2(t.m[r], t.l[r]);
   }
+  shared_end();
 }
 
 // ---- bf16 queries and cache: tensor cores -----------------------------------------
@@ -143,7 +144,7 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
 template <int D, int RG>
 __global__ void __launch_bounds__(kMmaWarps * 32, 1) shared_mma_kernel(const __grid_constant__ AttendParams P,
                                                                        const __grid_constant__ SharedShape H) {
-  pdl_start();
+  shared_start(H);
   extern __shared__ __align__(128) uint8_t smem_raw[];
   __shared__ float2 sml[kMmaWarps][16];
   constexpr int kTile = MmaShared<D>::kTile, C = D / 32, U = D / 8, KG = kMmaWarps / RG;
@@ -353,6 +354,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 1) shared_mma_kernel(const __g
     *reinterpret_cast<float4*>(P.part_o + slot * pd.HD + h * D + c) = x;
     if (c == 0) *reinterpret_cast<float2*>(P.part_ml + (slot * pd.heads + h) * 2) = make_float2(mx, ls);
   }
+  shared_end();
 }
 
 template <int D, int RG>
@@ -407,8 +409,8 @@ int shared_splits(const PoolDesc& pd, int n, int n_entries, int n_sms) {
   return std::max(1, std::min(mma ? n_sms / per : 3 * n_sms / per, (n_entries + 63) / 64));
 }
 
-int launch_shared(const AttendParams& p, int n_entries, int n_split, bool pdl, void* stream, int* n_kernels) {
-  const SharedShape h{n_entries, n_split, p.reqs[0].slot, pdl};
+int launch_shared(const AttendParams& p, int n_entries, int n_split, bool behind, bool pdl, void* stream, int* n_kernels) {
+  const SharedShape h{n_entries, n_split, p.reqs[0].slot, behind, pdl};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   *n_kernels += 1;
   switch (p.pool.in_dtype * 3 + p.pool.cache_dtype) {

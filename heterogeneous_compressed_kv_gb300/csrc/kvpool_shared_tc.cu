@@ -57,7 +57,7 @@ __device__ __forceinline__ bool tile_is_k(int i, int n, int& j) {
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_constant__ AttendParams P,
                                                                 const __grid_constant__ SharedShape H) {
-  pdl_start();
+  shared_start(H);
   using Sh = Shape<D>;
   constexpr int NS = Sh::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -351,6 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
   __syncthreads();
   tc_fence_after();
   if (warp == kSoftmaxWarps) tmem_free(tmem, 512);
+  shared_end();
 }
 
 template <int D>
