@@ -5,9 +5,15 @@
 // decode_attend at one query per head streams every request's entries past one
 // vector each.  Behind a shared prefix the same entries meet the queries of n
 // requests: per head a dense product, scores [n x entries] and outputs [n x
-// dim].  A CTA takes one head, a run of the shared entries and up to 64
-// requests, and leaves a partial (max, sum, output) per request and head in
-// the slots behind the request's other splits; the ordinary merge joins them.
+// dim].  A CTA takes one head, a run of the shared entries and a block of
+// requests (32 in the FMA form, 64 in the bf16 one), and leaves a partial (max,
+// sum, output) per request and head in the slots behind the request's other
+// splits; the ordinary merge joins them.
+//
+// Measured as whole steps of 16 heads x 128 in bf16: 4 requests behind 128
+// entries 9.4 us (three launches that wait for one another), 32 behind 1,024
+// entries 20.7 us (decode_attend: 44), 64 behind 8,192 (kvpool_shared_tc.cu)
+// 46 us.
 #include <algorithm>
 
 #include <cuda_runtime.h>
@@ -400,13 +406,15 @@ cudaError_t launch_shared_d(const AttendParams& p, const SharedShape& h, cudaStr
 bool shared_tc(int n, int n_entries) { return n > 32 && n_entries >= 2048; }
 
 // Splits of the shared entries for n requests: CTAs (head, split, block of
-// requests) that fill the GPU (the FMA form: with three to an SM), of at least
-// 64 entries each.
+// requests) that fill the GPU (the FMA form: with three to an SM; the
+// 5th-generation form: each takes two), of at least 64 entries each.
 int shared_splits(const PoolDesc& pd, int n, int n_entries, int n_sms) {
   const bool mma = pd.in_dtype == KVPOOL_BF16 && pd.cache_dtype == KVPOOL_BF16;
-  const int rows = !mma ? kFmaRows : shared_tc(n, n_entries) ? kSharedTcRows : kSharedRows;
+  const bool tc = mma && shared_tc(n, n_entries);
+  const int rows = !mma ? kFmaRows : tc ? kSharedTcRows : kSharedRows;
   const int per = pd.heads * ((n + rows - 1) / rows);
-  return std::max(1, std::min(mma ? n_sms / per : 3 * n_sms / per, (n_entries + 63) / 64));
+  const int most = !mma ? 3 * n_sms / per : tc ? 2 * std::max(1, n_sms / per) : n_sms / per;
+  return std::max(1, std::min(most, (n_entries + 63) / 64));
 }
 
 int launch_shared(const AttendParams& p, int n_entries, int n_split, bool behind, bool pdl, void* stream, int* n_kernels) {

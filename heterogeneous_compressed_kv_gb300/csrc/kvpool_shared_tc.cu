@@ -3,7 +3,7 @@
 //
 // A CTA takes one head, a run of the shared entries and up to 128 requests:
 // the requests' queries are the 128 rows of S = Q K^T and O += P V over tiles
-// of 128 entries.  Thirteen warps: four gather the entries (through the block
+// of 128 entries, in two runs with a partial result each.  Thirteen warps: four gather the entries (through the block
 // table: a tensor copy would want them adjacent) into a ring of K and V tiles
 // with asynchronous copies, one thread issues the products, and eight do the
 // softmax, two threads per row.  The scores of the next tile are computed while
@@ -13,6 +13,14 @@
 // rounding that shows (2^-9): each weight is taken apart into three bf16 numbers
 // whose sum holds its 24 bits, and O += P V takes three products.  Two of the
 // weights' pieces lie over the scores, the third beside them.
+// Measured: 64 requests behind 8,192 entries of 16 heads x 128 27 us (5 tiles
+// of 32 KB in flight; DRAM 31%, issue slots 21% busy: a CTA has 8 tiles, and
+// each waits for its gather and for the softmax of the tile before).  Four rows
+// to a gathering tensor copy in place of the threads' 16-byte ones: the step
+// takes 68 us instead of 46.
+// Two runs: the tensor core cuts each sum's last bit off instead of rounding it,
+// 24 times per tile; over one run of 8 tiles that made the outputs' error 1.0e-6
+// (relative, 64 requests behind 8,192 entries), over two 0.5e-6.
 // Outputs are rescaled when a row's maximum grows by more than 2^8 (see
 // kvpool_window_tc.cu).
 #include <cuda_runtime.h>
@@ -64,19 +72,25 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
   uint8_t* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
   uint8_t* ring = smem + Sh::kTileBytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Sh::kBarOff);
-  // scores and weights: a barrier per buffer (with one, a phase could pass
-  // while a slow waiter still looks for the one before)
+  // scores, weights, outputs: two barriers in turn (with one, a phase could pass
+  // while a slow waiter still looks for the one before, or a wait be taken for
+  // the phase before the one before it)
   uint64_t *kv_full = bars, *kv_free = kv_full + NS, *s_full = kv_free + NS, *p_ready = s_full + 2, *pv_done = p_ready + 2,
-           *swap = pv_done + 1, *drain = swap + 4;
+           *swap = pv_done + 2, *drain = swap + 4;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   const PoolDesc& pd = P.pool;
   uint32_t* err = reinterpret_cast<uint32_t*>(pd.arena + pd.err);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = blockIdx.x, split = blockIdx.y, i0 = blockIdx.z * kSharedTcRows;
+  const int h = blockIdx.x, split = 2 * blockIdx.y, i0 = blockIdx.z * kSharedTcRows;
   const int rows = min(kSharedTcRows, P.n - i0);
+  // the two runs: entries [a, mid) in n0 tiles, [mid, b) in the others
   const int a = (int)((int64_t)H.n_entries * split / H.n_split);
-  const int b = (int)((int64_t)H.n_entries * (split + 1) / H.n_split);
-  const int n_tile = (b - a + kKeys - 1) / kKeys;
+  const int mid = (int)((int64_t)H.n_entries * (split + 1) / H.n_split);
+  const int b = split + 2 > H.n_split ? mid : (int)((int64_t)H.n_entries * (split + 2) / H.n_split);
+  const int n0 = (mid - a + kKeys - 1) / kKeys, n_tile = n0 + (b - mid + kKeys - 1) / kKeys;
+  // first entry of tile j, and the end of its run
+  auto tile_at = [&](int j) { return j < n0 ? a + j * kKeys : mid + (j - n0) * kKeys; };
+  auto run_end = [&](int j) { return j < n0 ? mid : b; };
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(&kv_full[i], kCopyWarps);
@@ -85,28 +99,45 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_ready[i], kSoftmaxWarps);
+      mbar_init(&pv_done[i], 1);
     }
     mbar_init(drain, 1);
-    mbar_init(pv_done, 1);
     for (int i = 0; i < 4; ++i) mbar_init(&swap[i], 2);
     mbar_fence_init();
   }
-  if (warp == kSoftmaxWarps) tmem_alloc(tmem_slot, 512);
-  // the queries' tile: row r, 16-byte piece u of each run of 64 dims at u ^ (r % 8)
-  for (int i = threadIdx.x; i < 128 * (D / 8); i += kThreads) {
-    const int r = i / (D / 8), u = i % (D / 8);
-    uint4 x = make_uint4(0, 0, 0, 0);
-    if (r < rows)
-      x = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(P.q) +
-                                          2 * ((int64_t)(P.row0 + i0 + r) * pd.HD + h * D + 8 * u));
-    *reinterpret_cast<uint4*>(smem + (u / 8) * 16384 + r * 128 + (((u % 8) ^ (r & 7)) << 4)) = x;
-  }
-  fence_proxy_async();
-  tc_fence_before();
   __syncthreads();
-  tc_fence_after();
   // columns: scores 0 - 127 and 128 - 255, outputs 256 - 383, third pieces 384 - 447 and 448 - 511
-  const uint32_t tmem = *tmem_slot;
+  uint32_t tmem = 0;
+  // The copy warps start at once; the others stage the queries first (in one
+  // go, the loads in flight together: started one by one, and with the copies
+  // behind them, the first product waited 3 us longer)
+  if (warp <= kSoftmaxWarps) {
+    if (warp == kSoftmaxWarps) {
+      tmem_alloc(tmem_slot, 512);
+    } else {
+      // row r, 16-byte piece u of each run of 64 dims at u ^ (r % 8)
+      constexpr int kEach = 128 * (D / 8) / (32 * kSoftmaxWarps);
+      uint4 x[kEach];
+#pragma unroll
+      for (int y = 0; y < kEach; ++y) {
+        const int i = threadIdx.x + y * 32 * kSoftmaxWarps, r = i / (D / 8), u = i % (D / 8);
+        x[y] = make_uint4(0, 0, 0, 0);
+        if (r < rows)
+          x[y] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(P.q) +
+                                                 2 * ((int64_t)(P.row0 + i0 + r) * pd.HD + h * D + 8 * u));
+      }
+#pragma unroll
+      for (int y = 0; y < kEach; ++y) {
+        const int i = threadIdx.x + y * 32 * kSoftmaxWarps, r = i / (D / 8), u = i % (D / 8);
+        *reinterpret_cast<uint4*>(smem + (u / 8) * 16384 + r * 128 + (((u % 8) ^ (r & 7)) << 4)) = x[y];
+      }
+      fence_proxy_async();
+    }
+    tc_fence_before();
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * (kSoftmaxWarps + 1)) : "memory");
+    tc_fence_after();
+    tmem = *tmem_slot;
+  }
 
   if (warp > kSoftmaxWarps) {
     // ---- copies: four threads per entry ----
@@ -115,8 +146,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     auto look_up = [&](int j, int32_t* id) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int e = a + j * kKeys + r0 + 32 * i;
-        id[i] = e < b ? shared_id(P, H, e) : INT32_MIN;
+        const int e = tile_at(j) + r0 + 32 * i;
+        id[i] = e < run_end(j) ? shared_id(P, H, e) : INT32_MIN;
       }
     };
     int32_t next[4];                  // ids of the K tile to come, asked for a tile ahead
@@ -207,8 +238,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
           for (int x = 0; x < 3; ++x)
 #pragma unroll
             for (int c = 0; c < kKeys / 16; ++c)
-              mma_ts(tmem + 256, piece[x] + 8 * c, vd + c * (2048 >> 4), kIdPV, j > 1 || x > 0 || c > 0);
-          mma_commit(pv_done);
+              mma_ts(tmem + 256, piece[x] + 8 * c, vd + c * (2048 >> 4), kIdPV, (j > 1 && j - 1 != n0) || x > 0 || c > 0);
+          mma_commit(&pv_done[e]);
           mma_commit(&kv_free[stage]);
           ++i;
         }
@@ -241,6 +272,33 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     };
     float m = -INFINITY, l = 0.0f;
     bool ok = true;
+    // (looked up before the first scores are there: an index of its own for each
+    // lane makes 32 reads of the parameters, 2 us when they are cold)
+    const int64_t slot0 = shared_slot(P, min(i0 + row, P.n - 1), split);
+    // A run's maximum, sum and outputs, the last of them those of tile j
+    auto put = [&](int run, int j, float m, float l) {
+      float theirs;
+      if (!warp_wait(&pv_done[j & 1], (j >> 1) & 1, err) || !exchange(l, theirs)) return false;
+      tc_fence_after();
+      const int64_t slot = slot0 + run;
+      float4* dst = reinterpret_cast<float4*>(P.part_o + slot * pd.HD + h * D + (D / 2) * half);
+#pragma unroll 1
+      for (int c = 0; c < D / 2; c += 16) {
+        uint32_t o[16];
+        __syncwarp();
+        tmem_ld16(base_lane + 256 + (D / 2) * half + c, o);
+        tmem_wait_ld();
+        if (row < rows) {
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            dst[c / 4 + y] = make_float4(__uint_as_float(o[4 * y]), __uint_as_float(o[4 * y + 1]),
+                                         __uint_as_float(o[4 * y + 2]), __uint_as_float(o[4 * y + 3]));
+        }
+      }
+      if (row < rows && half == 0)
+        *reinterpret_cast<float2*>(P.part_ml + (slot * pd.heads + h) * 2) = make_float2(m, l + theirs);
+      return true;
+    };
 #pragma unroll 1
     for (int j = 0; j < n_tile; ++j) {
       if (!warp_wait(&s_full[j & 1], (j >> 1) & 1, err)) {
@@ -254,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
         tmem_ld32(ts + 64 * half, x);
         tmem_ld32(ts + 64 * half + 32, x + 32);
         tmem_wait_ld();
-        const int n_key = b - a - j * kKeys - 64 * half;  // columns of this half that count
+        const int n_key = run_end(j) - tile_at(j) - 64 * half;  // columns of this half that count
         if (n_key < 64) {
 #pragma unroll
           for (int c = 0; c < 64; ++c)
@@ -269,10 +327,12 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
           break;
         }
         const float mn = fmaxf(mx, theirs) * scale;  // finite: some key of the tile counts
-        if (j == 0) {
+        const float m0 = m, l0 = l;
+        if (j == 0 || j == n0) {
           m = mn;
+          l = 0.0f;
         } else if (__any_sync(0xffffffffu, mn > m + kGrow)) {
-          if (!warp_wait(pv_done, (j - 1) & 1, err)) {
+          if (!warp_wait(&pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, err)) {
             ok = false;
             break;
           }
@@ -315,37 +375,17 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
         }
         l += sum[0] + sum[1];
         tmem_wait_st();
+        // the first run's outputs leave before the second one's first product replaces them
+        if (j == n0 && !put(0, j - 1, m0, l0)) {
+          ok = false;
+          break;
+        }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_ready[j & 1]);
     }
-    // the outputs of the tile before the last one may be on their way too: its
-    // phase first (the barrier tells two phases apart, not three)
-    if (ok && n_tile > 1) ok = warp_wait(pv_done, (n_tile - 2) & 1, err);
-    if (ok && n_tile > 0) ok = warp_wait(pv_done, (n_tile - 1) & 1, err);
-    tc_fence_after();
-    float theirs = 0.0f;
-    if (ok && live) ok = exchange(l, theirs);
-    if (ok && live) {
-      const int64_t slot = shared_slot(P, min(i0 + row, P.n - 1), split);
-      float4* dst = reinterpret_cast<float4*>(P.part_o + slot * pd.HD + h * D + (D / 2) * half);
-#pragma unroll 1
-      for (int c = 0; c < D / 2; c += 16) {
-        uint32_t o[16];
-        __syncwarp();
-        tmem_ld16(base_lane + 256 + (D / 2) * half + c, o);
-        tmem_wait_ld();
-        if (row < rows) {
-#pragma unroll
-          for (int y = 0; y < 4; ++y)
-            dst[c / 4 + y] = make_float4(__uint_as_float(o[4 * y]), __uint_as_float(o[4 * y + 1]),
-                                         __uint_as_float(o[4 * y + 2]), __uint_as_float(o[4 * y + 3]));
-        }
-      }
-      if (row < rows && half == 0)
-        *reinterpret_cast<float2*>(P.part_ml + (slot * pd.heads + h) * 2) = make_float2(m, l + theirs);
-    }
+    if (ok && live) put(n_tile > n0, n_tile - 1, m, l);
   }
   tc_fence_before();
   __syncthreads();
@@ -359,7 +399,7 @@ cudaError_t launch_t(const AttendParams& p, const SharedShape& h, cudaStream_t s
   auto* kern = shared_tc_kernel<D>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D>::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_kernel(h.pdl != 0, kern, dim3(p.pool.heads, h.n_split, (p.n + kSharedTcRows - 1) / kSharedTcRows),
+  return launch_kernel(h.pdl != 0, kern, dim3(p.pool.heads, (h.n_split + 1) / 2, (p.n + kSharedTcRows - 1) / kSharedTcRows),
                        dim3(kThreads), Shape<D>::kSmem, s, p, h);
 }
 
