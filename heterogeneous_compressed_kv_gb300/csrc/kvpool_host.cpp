@@ -1239,7 +1239,21 @@ static int decode_attend(kvpool_t* p, int32_t layer, int32_t n, const int32_t* h
     if ((int64_t)t.size() < sh_blocks || t[sh_blocks - 1] != p->reqs[h_req_ids[0]].table[sh_blocks - 1])
       return p->fail(KVPOOL_ERR_NOT_SHAREABLE, "decode_attend: the requests do not share that prefix");
   }
-  const int n_sh = p->lay.layers[layer].has_hca ? (int)sh_blocks : 0;  // shared HCA entries
+  // Shared HCA entries.  Where few bytes are read once instead of n times, the
+  // shared entries' kernel costs more than it saves, and every request reads
+  // its own.  Steps of 16 heads x 128 in bf16 (shared / each its own, us):
+  //   requests  128 entries  256        512        1,024
+  //   64        19.0 / 16.9  19.9/21.3  20.9/30.1  23.0/48.0
+  //   32        15.6 / 12.5  16.0/14.6  16.8/19.2  17.7/28.4
+  //   16        12.6 / 10.8  13.4/11.8  14.3/14.2  15.3/19.0
+  //   8          9.6 /  9.3   9.8/10.2  13.6/11.1  13.8/13.3
+  //   8         2,400 entries 17.7 / 19.6, 4,800 entries 21.0 / 29.6
+  // 64 MB saved is at 64 x 127, 32 x 258, 16 x 533 and 8 x 1,143 of them; with 16
+  // heads x 64 the two meet at 64 x 256, 32 x 512 and 16 x 256, with 4 x 64 in
+  // fp32 at 64 x 300 and 32 x 1,024 (20 to 66 MB).
+  constexpr int64_t kShareBytes = 64LL << 20;
+  const bool share = (n - 1) * sh_blocks * p->lay.pd.entry_bytes >= kShareBytes;
+  const int n_sh = share && p->lay.layers[layer].has_hca ? (int)sh_blocks : 0;
   if (!p->device()) return p->fail(KVPOOL_ERR_INVALID_ARG, "decode_attend: pool has no device");
   if (n == 0) return KVPOOL_OK;
   if (reinterpret_cast<uintptr_t>(d_q) % 16 != 0) return p->fail(KVPOOL_ERR_INVALID_ARG, "decode_attend: q not 16-byte aligned");
@@ -1396,21 +1410,12 @@ static int decode_attend(kvpool_t* p, int32_t layer, int32_t n, const int32_t* h
       if (e == cudaSuccess) e = cudaStreamWaitEvent(p->side, p->ev_fork, 0);
       if (e != cudaSuccess) rc = (int)e;
     }
-    // The shared entries' kernel wants whole SMs.  Where part 0 leaves some free
-    // it starts beside it (4 requests, 32 part-0 CTAs: 12.8 -> 9.4 us a step);
-    // where part 0 fills them all it goes first (64 requests, 456 CTAs, 8,192
-    // entries: 45.9 us, 48.1 behind it).
-    const bool behind = ctas0 <= p->n_sms;
-    auto shared = [&]() {
-      return p->launch(KVPOOL_KERNEL_ATTEND, bytes2, s0,
-                       [&](int* nk) { return launch_shared(P, n_sh, split2, behind, behind || !fork, s0, nk); });
-    };
-    if (rc == 0 && n_sh > 0 && !behind) rc = shared();
+    if (rc == 0 && n_sh > 0)
+      rc = p->launch(KVPOOL_KERNEL_ATTEND, bytes2, s0, [&](int* nk) { return launch_shared(P, n_sh, split2, !fork, s0, nk); });
     P.pool.table = pd.table + 4LL * n_sh;  // part 0 sees the tables from each request's own blocks on
     if (rc == 0)
       rc = p->launch(KVPOOL_KERNEL_ATTEND, bytes0, s0, [&](int* nk) { return launch_attend(P, 0, ctas0, s0, nk); });
     P.pool.table = pd.table;
-    if (rc == 0 && n_sh > 0 && behind) rc = shared();
     if (rc == 0 && key_ctas > 0)
       rc = p->launch(KVPOOL_KERNEL_SELECT, 0, stream, [&](int* nk) { return launch_select(P, stream, nk, !fork); });
     if (rc == 0)

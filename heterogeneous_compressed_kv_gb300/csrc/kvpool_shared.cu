@@ -10,10 +10,10 @@
 // sum, output) per request and head in the slots behind the request's other
 // splits; the ordinary merge joins them.
 //
-// Measured as whole steps of 16 heads x 128 in bf16: 4 requests behind 128
-// entries 9.4 us (three launches that wait for one another), 32 behind 1,024
-// entries 20.7 us (decode_attend: 44), 64 behind 8,192 (kvpool_shared_tc.cu)
-// 46 us.
+// Measured as whole steps of 16 heads x 128 in bf16: 8 requests behind 2,400
+// entries 17.7 us (decode_attend 19.6), 32 behind 1,024 18 us (28; the shared
+// entries' kernel by itself 6.9), 64 behind 8,192 (kvpool_shared_tc.cu) 44 us
+// (442).  Below about 64 MB saved the caller does not come here.
 #include <algorithm>
 
 #include <cuda_runtime.h>
@@ -49,7 +49,7 @@ __device__ __forceinline__ float4 codes4(const uint8_t* row, int i) {
 template <int IN, int CACHE, int D>
 __global__ void __launch_bounds__(kFmaThreads) shared_fma_kernel(const __grid_constant__ AttendParams P,
                                                                  const __grid_constant__ SharedShape H) {
-  shared_start(H);
+  pdl_start();
   extern __shared__ __align__(16) uint8_t smem_raw[];
   FmaSmem<D>& sm = *reinterpret_cast<FmaSmem<D>*>(smem_raw);
   __shared__ float scales[2][kFmaKeys];
@@ -114,7 +114,6 @@ __global__ void __launch_bounds__(kFmaThreads) shared_fma_kernel(const __grid_co
     t.put(P.part_o + slot * pd.HD + h * D, r, tx);
     if (tx == 0) *reinterpret_cast<float2*>(P.part_ml + (slot * pd.heads + h) * 2) = make_float2(t.m[r], t.l[r]);
   }
-  shared_end();
 }
 
 // ---- bf16 queries and cache: tensor cores -----------------------------------------
@@ -150,7 +149,7 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
 template <int D, int RG>
 __global__ void __launch_bounds__(kMmaWarps * 32, 1) shared_mma_kernel(const __grid_constant__ AttendParams P,
                                                                        const __grid_constant__ SharedShape H) {
-  shared_start(H);
+  pdl_start();
   extern __shared__ __align__(128) uint8_t smem_raw[];
   __shared__ float2 sml[kMmaWarps][16];
   constexpr int kTile = MmaShared<D>::kTile, C = D / 32, U = D / 8, KG = kMmaWarps / RG;
@@ -360,7 +359,6 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 1) shared_mma_kernel(const __g
     *reinterpret_cast<float4*>(P.part_o + slot * pd.HD + h * D + c) = x;
     if (c == 0) *reinterpret_cast<float2*>(P.part_ml + (slot * pd.heads + h) * 2) = make_float2(mx, ls);
   }
-  shared_end();
 }
 
 template <int D, int RG>
@@ -417,8 +415,8 @@ int shared_splits(const PoolDesc& pd, int n, int n_entries, int n_sms) {
   return std::max(1, std::min(most, (n_entries + 63) / 64));
 }
 
-int launch_shared(const AttendParams& p, int n_entries, int n_split, bool behind, bool pdl, void* stream, int* n_kernels) {
-  const SharedShape h{n_entries, n_split, p.reqs[0].slot, behind, pdl};
+int launch_shared(const AttendParams& p, int n_entries, int n_split, bool pdl, void* stream, int* n_kernels) {
+  const SharedShape h{n_entries, n_split, p.reqs[0].slot, pdl};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   *n_kernels += 1;
   switch (p.pool.in_dtype * 3 + p.pool.cache_dtype) {

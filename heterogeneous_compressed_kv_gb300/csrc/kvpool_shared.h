@@ -9,19 +9,8 @@ namespace kvp {
 
 struct SharedShape {
   int32_t n_entries, n_split, slot;  // slot: the request whose table holds the shared ids
-  int32_t behind;                    // launched behind the [HCA | window] part (else before it)
   int32_t pdl;                       // programmatic dependent launch
 };
-
-// The kernels and the [HCA | window] part do not depend on one another.  Behind
-// it (which itself starts only when all before it has finished: no early
-// launch) they start while it runs, touch memory at once and wait for it at
-// their end: what follows them follows both.
-__device__ __forceinline__ void shared_start(const SharedShape& H) {
-  if (H.behind) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  else pdl_start();
-}
-__device__ __forceinline__ void shared_end() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // the block id of shared entry e as it stands in the table, and the entry's
 // address (the id is looked at there: a load that is early enough costs nothing)

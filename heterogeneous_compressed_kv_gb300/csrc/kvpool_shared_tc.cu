@@ -13,11 +13,13 @@
 // rounding that shows (2^-9): each weight is taken apart into three bf16 numbers
 // whose sum holds its 24 bits, and O += P V takes three products.  Two of the
 // weights' pieces lie over the scores, the third beside them.
-// Measured: 64 requests behind 8,192 entries of 16 heads x 128 27 us (5 tiles
-// of 32 KB in flight; DRAM 31%, issue slots 21% busy: a CTA has 8 tiles, and
-// each waits for its gather and for the softmax of the tile before).  Four rows
-// to a gathering tensor copy in place of the threads' 16-byte ones: the step
-// takes 68 us instead of 46.
+// Measured: 64 requests behind 8,192 entries of 16 heads x 128 24 us.  The first
+// tile is there after 5.4 us (parameters, block ids, entries: three reads in a
+// row), a tile's K and V take 1.9 us (4.9 TB/s over the CTAs; four tiles of 32 KB
+// in flight), a run's outputs 1.7 us.  Without its softmax the step would take
+// 4.5 us less, with one product of three 2.4 us, with its entries in the L2 cache
+// 3 us.  Four rows to a gathering tensor copy in place of the threads' 16-byte
+// ones: 68 us a step instead of 46.
 // Two runs: the tensor core cuts each sum's last bit off instead of rounding it,
 // 24 times per tile; over one run of 8 tiles that made the outputs' error 1.0e-6
 // (relative, 64 requests behind 8,192 entries), over two 0.5e-6.
@@ -65,7 +67,7 @@ __device__ __forceinline__ bool tile_is_k(int i, int n, int& j) {
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_constant__ AttendParams P,
                                                                 const __grid_constant__ SharedShape H) {
-  shared_start(H);
+  pdl_start();
   using Sh = Shape<D>;
   constexpr int NS = Sh::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -391,7 +393,6 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
   __syncthreads();
   tc_fence_after();
   if (warp == kSoftmaxWarps) tmem_free(tmem, 512);
-  shared_end();
 }
 
 template <int D>

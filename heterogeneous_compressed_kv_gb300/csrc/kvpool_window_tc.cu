@@ -18,7 +18,19 @@
 // of O leaves the critical path.
 //
 // Rows of K and V behind a segment, or between the first tokens and the window,
-// never count: scores are masked, and such V rows are not copied.
+// never count: scores are masked, and such V rows are not copied (boxes of 16
+// and of 1 row up to the last one that holds values, zeros behind it).
+//
+// Bound: the tensor core for long windows -- 32,768 tokens x 16 heads of 128
+// under a window of 4,096 take 757 us, 1,360 TFLOP/s of visible products (0.70
+// of the library product's rate, under the same power limit; partial tiles
+// compute up to 6% more than is visible).  Short windows are bound by their partial
+// tiles and by instruction fetch (2.2 stalled cycles per instruction): 4 x 2,048
+// queries x 16 heads under a window of 128 38 us, of which the tiles' 128-key
+// steps compute 3 keys for 1 that is seen.
+// Measured and not kept: K and V tiles of its own for each query tile (38.8 us
+// against 36.6 there), two threads per row (174 against 164 us for 8,192 tokens
+// under 4,096), outputs staged for whole-line stores (slower).
 #include <cuda.h>
 #include <cuda_runtime.h>
 

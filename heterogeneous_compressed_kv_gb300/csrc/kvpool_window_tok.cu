@@ -16,6 +16,11 @@
 // 8 x 8 transposition of bf16 pairs (movmatrix).  The 5th-generation products
 // (128 rows) would do the same with 8 to 128 times the padding.
 // fp32: FMAs; four lanes per key, each lane its own running softmax per row.
+//
+// Measured: 64 requests under a window of 4,096 (16 query heads on 4 key heads
+// of 128) 82 us, 6.6 TB/s (0.98 of the copy rate); 32 requests under 128 (16
+// heads) 8.5 - 10.3 us against 5.2 us of reading: launch and one round of
+// loads' latency.  Four CTAs to an SM: three took 98 and 14.5 us.
 #include <cuda_runtime.h>
 
 #include "kvpool_fma.cuh"

@@ -326,7 +326,8 @@ int kvpool_decode_attend(kvpool_t* pool, int32_t layer, int32_t n, const int32_t
 /* kvpool_decode_attend of requests whose first n_shared tokens are the same
  * sealed blocks ([P3] s2.2; kvpool_share_prefix): the HCA entries of those
  * blocks are read once for the whole batch instead of once per request, as a
- * dense product of all requests' queries per head.  Same arguments, outputs
+ * dense product of all requests' queries per head (where that saves 64 MB of
+ * reading or more: below, the call is kvpool_decode_attend).  Same arguments, outputs
  * and selected entries as kvpool_decode_attend; outputs differ from its by
  * the order of the fp32 sums (and, with an fp8 cache, by being closer to the
  * decoded values).  The indexer scan, the selected CSA entries and the window

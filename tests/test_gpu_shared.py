@@ -240,3 +240,89 @@ def test_a_layer_as_a_model_runs_it():
     g.pool.decode_attend(1, [a, b], new, None, 0, plain)
     assert g.pool.check_device() == 0
     close(shared, plain, K.BF16, K.BF16)
+
+
+def size_of(w, n, prefix):
+    size = {K.F32: 4, K.BF16: 2, K.FP8_E4M3: 1}[w["cache_dtype"]]
+    return (n - 1) * (prefix // 128) * 2 * w["heads"] * w["head_dim"] * size
+
+
+@pytest.mark.parametrize("types,heads,dim,n,entries", [
+    # bf16 on the small products: 16, 32 and 64 requests to a CTA, whole and ragged stages, one CTA's requests and more
+    ((K.BF16, K.BF16), 16, 128, 2, 8200), ((K.BF16, K.BF16), 16, 128, 9, 1101), ((K.BF16, K.BF16), 16, 128, 17, 600),
+    ((K.BF16, K.BF16), 16, 64, 31, 577), ((K.BF16, K.BF16), 16, 128, 33, 257), ((K.BF16, K.BF16), 16, 128, 65, 129),
+    ((K.BF16, K.BF16), 16, 64, 150, 113),
+    # the products of 128 rows
+    ((K.BF16, K.BF16), 16, 128, 34, 2050), ((K.BF16, K.BF16), 4, 128, 130, 2100), ((K.BF16, K.BF16), 16, 64, 40, 2309),
+    # FMAs
+    ((K.F32, K.F32), 16, 128, 5, 1025), ((K.F32, K.F32), 4, 64, 33, 1101), ((K.BF16, K.FP8_E4M3), 16, 128, 33, 515),
+    ((K.F32, K.BF16), 16, 64, 64, 300), ((K.BF16, K.F32), 4, 128, 50, 400), ((K.F32, K.FP8_E4M3), 16, 64, 70, 500)])
+def test_sizes_that_share(types, heads, dim, n, entries):
+    w = dict(BASE, in_dtype=types[0], cache_dtype=types[1], heads=heads, head_dim=dim)
+    assert size_of(w, n, 128 * entries) >= 64 << 20
+    g, _, slots = build(w, n, 128 * entries, [(i * 37) % 300 for i in range(n)], oracle=False)
+    out, ref = attend(g, 0, slots, list(range(n)), 0, 128 * entries)
+    close(out, ref, *types[::-1])
+    assert torch.equal(out, attend(g, 0, slots, list(range(n)), 0, 128 * entries)[0])  # the same bits again
+    # a shorter prefix of the same requests (some of it then each request's own), and one too short to share
+    for blocks in (entries - 1, 3):
+        out, ref = attend(g, 0, slots, list(range(n)), 0, 128 * blocks)
+        close(out, ref, *types[::-1])
+
+
+@pytest.mark.parametrize("dim,n,entries", [(128, 9, 1200), (64, 40, 2100)])
+def test_layers_with_csa_share_beside_the_select(dim, n, entries):
+    """The shared entries' kernel on the stream beside the indexer's select, before and behind the [HCA | window] part."""
+    w = dict(BASE, layer_kinds=[K.CSA_HCA], heads=16, head_dim=dim, idx_heads=1, idx_dim=32)
+    assert size_of(w, n, 128 * entries) >= 64 << 20
+    g, _, slots = build(w, n, 128 * entries, [i * 9 for i in range(n)], oracle=False)
+    for top_k in (16, 0):
+        out, ref = attend(g, 0, slots, list(range(n)), top_k, 128 * entries)
+        close(out, ref, K.BF16, K.BF16)
+
+
+def test_more_requests_than_one_launch_share():
+    w = dict(BASE, heads=4, head_dim=64)
+    g, _, slots = build(w, 300, 128 * 300, [i % 3 for i in range(300)], oracle=False)
+    assert size_of(w, 300, 128 * 300) >= 64 << 20
+    out, ref = attend(g, 0, slots, list(range(300)), 0, 128 * 300)
+    close(out, ref, K.BF16, K.BF16)
+
+
+@pytest.mark.parametrize("n,entries", [(9, 1200), (40, 2100)])
+def test_graph_and_other_stream_where_entries_are_shared(n, entries):
+    w = dict(BASE, heads=16, head_dim=128)
+    g, _, slots = build(w, n, 128 * entries, [i * 20 for i in range(n)], oracle=False)
+    q, qi = g.queries(0, list(range(n)), 0)
+    want = torch.empty((n, g.HD), device="cuda")
+    g.pool.decode_attend_shared(0, slots, 128 * entries, q, qi, 0, want)
+    torch.cuda.synchronize()
+    side, out = torch.cuda.Stream(), torch.zeros_like(want)
+    g.pool.decode_attend_shared(0, slots, 128 * entries, q, qi, 0, out, stream=side)
+    side.synchronize()
+    assert torch.equal(out, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(3):  # each behind the one before, in the same partials
+            g.pool.decode_attend_shared(0, slots, 128 * entries, q, qi, 0, out)
+    out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and g.pool.check_device() == 0
+
+
+def test_large_scores_where_entries_are_shared():
+    """Queries so large that one entry has all the weight, and queries of zeros."""
+    for types, heads, dim, n, entries in (((K.BF16, K.BF16), 16, 128, 9, 1100), ((K.BF16, K.BF16), 16, 64, 40, 2048),
+                                          ((K.F32, K.F32), 4, 64, 33, 1100)):
+        w = dict(BASE, in_dtype=types[0], cache_dtype=types[1], heads=heads, head_dim=dim)
+        g, _, slots = build(w, n, 128 * entries, [i * 3 for i in range(n)], oracle=False)
+        q, _ = g.queries(0, list(range(n)), 0)
+        for scale in (300.0, 0.0):
+            x = q * scale
+            out, ref = torch.empty((n, g.HD), device="cuda"), torch.empty((n, g.HD), device="cuda")
+            g.pool.decode_attend_shared(0, slots, 128 * entries, x, None, 0, out)
+            g.pool.decode_attend(0, slots, x, None, 0, ref)
+            assert bool(torch.isfinite(out).all())
+            # scores of up to a few thousand are off by 2^-24 of themselves: 2^-10 in the weights
+            assert float((out - ref).norm() / ref.norm()) <= 2.0 ** -8
