@@ -10,7 +10,8 @@
 // Measured: 3 prompts of 1,021 fp32 tokens x 4 heads of 64 under a window of 256
 // 41 us (issue slots 47% busy at 14 warps to an SM).  Not kept, no faster there:
 // fp32 pairs in one instruction (40.8), the next step's keys and values on
-// their way during a step (42.4).
+// their way during a step (42.4), five CTAs to an SM with the weights in the
+// keys' place (42.9).
 #pragma once
 
 #include "device_util.cuh"
