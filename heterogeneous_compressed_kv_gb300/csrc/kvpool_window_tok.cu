@@ -15,6 +15,9 @@
 // the pairs along the keys that the fragment wants; P^T comes from S^T by an
 // 8 x 8 transposition of bf16 pairs (movmatrix).  The 5th-generation products
 // (128 rows) would do the same with 8 to 128 times the padding.
+// A weight goes into the product as two bf16 numbers whose sum holds 16 of its
+// bits (off by 2^-18 of it at most): one alone would be off by 2^-9, as much as
+// the output's own rounding.  The second product is hidden behind the loads.
 // fp32: FMAs; four lanes per key, each lane its own running softmax per row.
 //
 // Measured: 64 requests under a window of 4,096 (16 query heads on 4 key heads
@@ -151,7 +154,7 @@ __global__ void __launch_bounds__(kTokWarps * 32, NT == 1 ? 4 : 2) window_tok_ke
 #pragma unroll
       for (int h = 0; h < D / 64; ++h) vf[i][h] = ld_stream16(p + 128 * h);
     }
-    uint32_t pt[NT][2];
+    uint32_t pt[NT][2][2];  // [piece of the weights][keys 0 - 7, 8 - 15]
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       float s[4] = {0.f, 0.f, 0.f, 0.f};
@@ -186,8 +189,16 @@ __global__ void __launch_bounds__(kTokWarps * 32, NT == 1 ? 4 : 2) window_tok_ke
 #pragma unroll
           for (int j = 0; j < 4; ++j) o[n][i][j] *= corr[j & 1];
       }
-      pt[n][0] = transpose8x8(pack_bf16(s[0], s[1]));  // row g, keys 2t, 2t + 1
-      pt[n][1] = transpose8x8(pack_bf16(s[2], s[3]));  // ... + 8
+      // the weights' first 8 bits, then the next 8
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t pk = pack_bf16(s[2 * i], s[2 * i + 1]);
+          s[2 * i] -= __uint_as_float(pk << 16);
+          s[2 * i + 1] -= __uint_as_float(pk & 0xFFFF0000u);
+          pt[n][x][i] = transpose8x8(pk);  // row g, keys 2t, 2t + 1 (+ 8)
+        }
     }
     // O^T tiles: lane's dims 64h + 8g + 2j (rows g) and + 1 (rows g + 8)
 #pragma unroll
@@ -201,7 +212,9 @@ __global__ void __launch_bounds__(kTokWarps * 32, NT == 1 ? 4 : 2) window_tok_ke
         const uint32_t a0 = __byte_perm(v0[j], v1[j], 0x5410), a1 = __byte_perm(v0[j], v1[j], 0x7632);
         const uint32_t a2 = __byte_perm(v2[j], v3[j], 0x5410), a3 = __byte_perm(v2[j], v3[j], 0x7632);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) mma_bf16(o[n][4 * h + j], a0, a1, a2, a3, pt[n][0], pt[n][1]);
+        for (int x = 1; x >= 0; --x)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma_bf16(o[n][4 * h + j], a0, a1, a2, a3, pt[n][x][0], pt[n][x][1]);
       }
     }
   }

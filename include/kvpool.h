@@ -432,8 +432,12 @@ int kvpool_qk_norm_rope(int32_t dtype, int32_t head_dim, int64_t n_tokens, const
  * they were.  K/V rows that no query of a segment sees (outside it, between
  * the first tokens and the window) may hold anything; a NaN or infinity in a
  * value row that some queries see may also reach queries nearby that do not.
- * dtype: KVPOOL_F32 (fp32 throughout) or KVPOOL_BF16 (softmax statistics and
- * sums in fp32); head_dim 64 or 128; window and n_sink >= 0.
+ * dtype: KVPOOL_F32 (fp32 throughout) or KVPOOL_BF16: scores, softmax
+ * statistics, sums and d_lse in fp32, one rounding of the outputs, and one of
+ * the softmax weights before their product with the values -- to 16 bits where
+ * a segment has at most 16 query rows per key head (h_q_len * group), to bf16
+ * (2^-9 of each weight) in longer ones.  Callers that need a prompt's weights
+ * unrounded pass fp32 tensors.  head_dim 64 or 128; window and n_sink >= 0.
  * d_workspace: kvpool_window_workspace bytes (16-byte aligned, may be NULL
  * when that is 0); calls that overlap on the GPU need one each.  The lengths
  * are read during the call: a captured call replays with the same ones.

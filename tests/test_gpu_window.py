@@ -295,3 +295,24 @@ def test_window_workspace_of_broadcast_queries():
     args = (q, k, k, [40], [0], [5000], 4096)
     assert K.window_workspace(*args) > 0
     assert K.window_attend(*args).shape == (40, 2, 64)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hk", [(4, 4), (16, 2), (16, 1)])
+@pytest.mark.parametrize("ql,kl,window,sink", [([1] * 6, [1, 40, 129, 1000, 4000, 9000], 4096, 4), ([1, 1], [8, 700], 128, 0),
+                                               ([1], [70001], 1 << 20, 1)])
+def test_single_tokens_hold_their_weights_in_16_bits(ql, kl, window, sink, hq, hk, d):
+    """The output's own rounding is the one that shows: no half step of bf16 for the weights, whose two pieces leave
+    2^-18 of each (half a step of half a step)."""
+    q, k, v, ks = inputs(ql, kl, hq, hk, d, BF, seed=len(kl))
+    q = q / 8  # many keys count, and the scores' own error stays small
+    out = K.window_attend(q, k, v, ql, ks, kl, window, sink)
+    scale = 1 / math.sqrt(d)
+    ref, _, mass = formula(q, k, v, ql, ks, kl, window, sink, scale)
+    qk = scale * float(q.double().norm(dim=-1).max() * k.double().nan_to_num(0, 0, 0).norm(dim=-1).max())
+    n_keys = min(window + sink, max(kl))
+    # as in check(), but a weight's rounding is 2^-18 (twice: in a sum of two products)
+    rel = 4 * (d + 4) * 2.0 ** -24 * qk + 2.0 ** -20 + n_keys * 2.0 ** -24 + 2.0 ** -17
+    tol = torch.finfo(BF).eps / 2 * ref.abs() + rel * mass * 1.01 + 1e-30
+    err = (out.double() - ref).abs()
+    assert bool((err <= tol).all()), float((err / tol).max())
