@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kFmaThreads) window_fma_kernel(const __grid_co
                 make_float4(f.o[r][4 * c] * inv, f.o[r][4 * c + 1] * inv, f.o[r][4 * c + 2] * inv,
                             f.o[r][4 * c + 3] * inv));
     if (P.lse && tx == 0)
-      P.lse[tok * P.q_heads + h] = f.l[r] > 0.0f ? (f.m[r] + log2f(f.l[r])) * 0.69314718055994531f : -INFINITY;
+      P.lse[tok * P.q_heads + h] = win_lse(f.m[r], f.l[r]);
   }
 }
 
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) window_merge_kernel(const __
     for (int i = 0; i < V; i += 2)
       *reinterpret_cast<__nv_bfloat162*>(P.out + 2 * (at + i)) = __floats2bfloat162_rn(acc[i] * inv, acc[i + 1] * inv);
   }
-  if (P.lse && lane == 0) P.lse[tok * P.q_heads + h] = l > 0.0f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+  if (P.lse && lane == 0) P.lse[tok * P.q_heads + h] = win_lse(m, l);
 }
 
 // ---- host plan ------------------------------------------------------------------

@@ -86,6 +86,12 @@ __device__ __forceinline__ bool win_sees(const WinParams& P, int p, int t) {
   return t <= p && (t > p - P.window || t < P.n_sink);
 }
 
+// A row's log-sum-exp from its maximum (log2 domain) and sum: -inf where it saw
+// nothing, NaN where its sum is one (a NaN or an infinity among its scores)
+__device__ __forceinline__ float win_lse(float m, float l) {
+  return l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+}
+
 // Single-token form: at most 16 query rows per key head, the whole segment in
 // one tile.  Returns a cudaError_t.
 constexpr int kTokRows = 16;

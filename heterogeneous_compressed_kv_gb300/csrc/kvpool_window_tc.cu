@@ -586,7 +586,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
       }
       if (mine) {
         if (w.n_split > 1) P.part_ml[pr] = make_float2(l > 0.0f ? m : -INFINITY, l);
-        else if (P.lse) P.lse[tok * P.q_heads + head] = l > 0.0f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        else if (P.lse) P.lse[tok * P.q_heads + head] = win_lse(m, l);
       }
     }
   }

@@ -86,7 +86,7 @@ __device__ void tok_finish(const WinParams& P, const WinItem& w, const float* so
     else
       *reinterpret_cast<uint2*>(P.out + 2 * at) =
           make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-    if (P.lse && c == 0) P.lse[tok * P.q_heads + h] = l > 0.0f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    if (P.lse && c == 0) P.lse[tok * P.q_heads + h] = win_lse(m, l);
   }
 }
 

@@ -425,7 +425,8 @@ int kvpool_qk_norm_rope(int32_t dtype, int32_t head_dim, int64_t n_tokens, const
  * h_k_len[i] - 1, its tokens at positions 0 .. h_k_len[i] - 1; its queries are
  * the last ones: query j is at position p = h_k_len[i] - h_q_len[i] + j and
  * sees the token at t when t <= p and (t > p - window or t < n_sink).  A query
- * that sees nothing gives zeros and -inf.  q.heads must be a multiple (up to
+ * that sees nothing, or scores of -inf alone, gives zeros and -inf; one that
+ * sees a score that is NaN or +inf gives NaN in out and d_lse.  q.heads must be a multiple (up to
  * 16) of k.heads: query head h reads key head h / (q.heads / k.heads).
  * out: like q, in dtype; d_lse: [q_rows][q.heads] fp32 natural-log sums of
  * the exponentials, or NULL.  Query rows behind the last segment are left as

@@ -316,3 +316,47 @@ def test_single_tokens_hold_their_weights_in_16_bits(ql, kl, window, sink, hq, h
     tol = torch.finfo(BF).eps / 2 * ref.abs() + rel * mass * 1.01 + 1e-30
     err = (out.double() - ref).abs()
     assert bool((err <= tol).all()), float((err / tol).max())
+
+
+FORMS = [  # q_len, k_len, window, dtype, scale: single tokens, prompts (tensor cores, FMAs), keys split over CTAs
+    ([1, 1], [40, 300], 64, BF, None), ([1, 1], [40, 300], 64, F32, None), ([1], [9000], 8000, BF, None),
+    ([2], [9000], 8000, F32, None), ([60, 200], [60, 500], 128, BF, None), ([150], [5000], 4096, BF, None),
+    ([60, 200], [60, 500], 128, F32, None), ([60, 200], [60, 500], 128, BF, -0.125), ([40], [5000], 4096, F32, None)]
+
+
+@pytest.mark.parametrize("ql,kl,window,dtype,scale", FORMS)
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_a_score_that_is_not_finite_reaches_what_sees_it_and_nothing_else(ql, kl, window, dtype, scale, bad):
+    """A NaN or an overflow among a query's own scores is no row that sees nothing: its outputs and its log-sum-exp are
+    NaN.  A NaN among the values leaves the log-sum-exp alone."""
+    q, k, v, ks = inputs(ql, kl, 4, 2, 64, dtype)
+    s = 0.125 if scale is None else scale
+    t = kl[-1] - ql[-1]  # the last segment's first query's own token, under key head 1
+    want = formula(q, k, v, ql, ks, kl, window, 0, s)
+    hit = torch.zeros(q.shape[:2], dtype=torch.bool, device="cuda")
+    at = sum(ql[:-1])
+    hit[at:at + min(window, ql[-1]), 2:] = True
+    bad_k = k.clone()
+    bad_k[ks[-1] + t, 1] = bad
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    out = K.window_attend(q, bad_k, v, ql, ks, kl, window, scale=scale, lse=lse)
+    # (products of an infinity with queries of both signs sum to NaN)
+    assert bool(torch.isnan(out[hit]).all()) and bool(torch.isnan(lse[hit]).all())
+    other = [torch.where(hit[..., None] if x.dim() == 3 else hit, y, x) for x, y in
+             ((out, want[0].to(dtype)), (lse, want[1].float()))]
+    check(*other, want, q, k, abs(s), dtype, max(kl))
+    bad_v = v.clone()
+    bad_v[ks[-1] + t, 1, 5] = bad
+    lse2 = torch.full(q.shape[:2], 7.0, device="cuda")
+    out = K.window_attend(q, k, bad_v, ql, ks, kl, window, scale=scale, lse=lse2)
+    check(out.nan_to_num(0, 0, 0) * 0, lse2, (want[0] * 0, want[1], want[2]), q, k, abs(s), dtype, max(kl))
+    assert not bool(torch.isfinite(out[hit][:, 5]).any())
+
+
+def test_scores_of_minus_infinity_alone():
+    for ql, dtype in (([1], BF), ([1], F32), ([40], BF), ([40], F32)):
+        q, k, v, ks = inputs(ql, [200], 2, 1, 64, dtype)
+        q, k = q.abs() + 1, -torch.full_like(k, math.inf)
+        lse = torch.full(q.shape[:2], 7.0, device="cuda")
+        out = K.window_attend(q, k, v, ql, ks, [200], 64, 1, lse=lse)
+        assert bool((out == 0).all()) and bool((lse == -math.inf).all())
