@@ -39,6 +39,7 @@
 #include "device_util.cuh"
 #include "kvpool_internal.h"
 #include "kvpool_pair.cuh"
+#include "kvpool_rows.h"
 
 namespace kvp {
 namespace {
@@ -255,12 +256,6 @@ __global__ void __launch_bounds__(kRopeWarps * 32, T == KVPOOL_BF16 ? 8 : 5) rop
   }
 }
 
-bool heads_ok(const kvpool_heads* h, int32_t dtype) {
-  const int64_t unit = dtype == KVPOOL_BF16 ? 8 : 4;  // values in 16 bytes
-  return reinterpret_cast<uintptr_t>(h->data) % 16 == 0 && h->token_stride % unit == 0 && h->head_stride % unit == 0 &&
-         h->token_stride >= 0 && h->head_stride >= 0;
-}
-
 }  // namespace
 }  // namespace kvp
 
@@ -302,10 +297,8 @@ extern "C" int kvpool_qk_norm_rope(int32_t dtype, int32_t head_dim, int64_t n_to
       return KVPOOL_ERR_INVALID_ARG;
     if (n_tokens > 0 && (!in[i]->data || !out[i]->data)) return KVPOOL_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(wt[i]) % 16 != 0) return KVPOOL_ERR_INVALID_ARG;
-    if (!heads_ok(in[i], dtype) || !heads_ok(out[i], dtype)) return KVPOOL_ERR_INVALID_ARG;
-    // no two heads of an output start in the same values (axes of length 1: any stride)
-    if ((n_tokens > 1 && out[i]->token_stride < head_dim) || (out[i]->heads > 1 && out[i]->head_stride < head_dim))
-      return KVPOOL_ERR_INVALID_ARG;
+    if (!rows_aligned(*in[i], dtype) || !rows_aligned(*out[i], dtype)) return KVPOOL_ERR_INVALID_ARG;
+    if (!rows_apart(*out[i], n_tokens, head_dim)) return KVPOOL_ERR_INVALID_ARG;
     RopeTensor& X = P.t[i];
     X.in = static_cast<const uint8_t*>(in[i]->data);
     X.out = static_cast<uint8_t*>(const_cast<void*>(out[i]->data));

@@ -17,6 +17,7 @@
 #include <cuda_runtime.h>
 
 #include "kvpool_fma.cuh"
+#include "kvpool_rows.h"
 #include "kvpool_window.h"
 
 namespace kvp {
@@ -197,17 +198,6 @@ __global__ void __launch_bounds__(kMergeWarps * 32) window_merge_kernel(const __
 // ---- host plan ------------------------------------------------------------------
 constexpr int32_t kMaxLen = 1 << 30;
 
-bool strides_ok(const kvpool_heads& h, int32_t dtype) {
-  const int64_t unit = dtype == KVPOOL_BF16 ? 8 : 4;  // values in 16 bytes
-  return reinterpret_cast<uintptr_t>(h.data) % 16 == 0 && h.token_stride % unit == 0 && h.head_stride % unit == 0 &&
-         h.token_stride >= 0 && h.head_stride >= 0;
-}
-
-// no two heads of an output start in the same values (axes of length 1: any stride)
-bool rows_apart(const kvpool_heads& h, int64_t tokens, int32_t dim) {
-  return (tokens <= 1 || h.token_stride >= dim) && (h.heads <= 1 || h.head_stride >= dim);
-}
-
 int check_args(const kvpool_window_args* a, int32_t n, const int64_t* q_len, const int64_t* k_start,
                const int64_t* k_len, int64_t* total_q) {
   if (!a || n < 0) return KVPOOL_ERR_INVALID_ARG;
@@ -219,8 +209,8 @@ int check_args(const kvpool_window_args* a, int32_t n, const int64_t* q_len, con
   if (a->window < 0 || a->n_sink < 0 || !std::isfinite(a->scale) || a->q_rows < 0 || a->kv_rows < 0)
     return KVPOOL_ERR_INVALID_ARG;
   if (a->q_rows > 0x7FFFFFFF || a->kv_rows > 0x7FFFFFFF) return KVPOOL_ERR_INVALID_ARG;
-  if (!strides_ok(a->q, a->dtype) || !strides_ok(a->k, a->dtype) || !strides_ok(a->v, a->dtype) ||
-      !strides_ok(a->out, a->dtype) || !rows_apart(a->out, a->q_rows, a->head_dim))
+  if (!rows_aligned(a->q, a->dtype) || !rows_aligned(a->k, a->dtype) || !rows_aligned(a->v, a->dtype) ||
+      !rows_aligned(a->out, a->dtype) || !rows_apart(a->out, a->q_rows, a->head_dim))
     return KVPOOL_ERR_INVALID_ARG;
   if (n > 0 && (!q_len || !k_start || !k_len)) return KVPOOL_ERR_INVALID_ARG;
   int64_t q = 0;

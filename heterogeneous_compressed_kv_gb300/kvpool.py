@@ -274,7 +274,8 @@ def _rows(t, what: str, like=None, out: bool = False) -> tuple:
     ptr = t.data_ptr()
     if (ptr | ts * size | hs * size) & 15 and n * heads * dim or vs != 1 and dim > 1:
         raise ValueError(f"{what}: a head's values must be adjacent, data and strides whole multiples of 16 bytes")
-    if out and (n > 1 and ts < dim or heads > 1 and hs < dim):
+    if out and (n > 1 and ts < dim or heads > 1 and hs < dim or
+                n > 1 and heads > 1 and (hs < ts * (n - 1) + dim if ts < hs else ts < hs * (heads - 1) + dim)):
         raise ValueError(f"{what}: two values share a place")
     return ptr, ts, hs, heads, 0
 

@@ -384,8 +384,10 @@ int kvpool_topk_static_check(void* stream, uint32_t* h_flags);
 /* The heads of a run of tokens: value j of head h of token t is at element
  * t * token_stride + h * head_stride + j of data (a head's values are
  * adjacent).  data and both strides are whole multiples of 16 bytes; strides
- * are in elements and not negative.  An input's may be 0 (one row for many);
- * an output's are head_dim or more where the axis is longer than 1. */
+ * are in elements and not negative.  An input's may be 0 (one row for many).
+ * No value of an output has two places in it: where an axis is longer than 1
+ * its stride is head_dim or more, and where both are, the larger stride steps
+ * over the whole of the other axis (e.g. a token's over all of its heads). */
 typedef struct kvpool_heads {
   const void* data;
   int64_t token_stride, head_stride;

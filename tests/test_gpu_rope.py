@@ -137,3 +137,20 @@ def test_stream_and_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, K.qk_norm_rope(q, None, pos, tab)[0])
+
+
+def test_outputs_whose_heads_lie_on_each_other_are_refused():
+    q = torch.randn((4, 2, 64), device="cuda")
+    pos, tab = torch.arange(4, device="cuda"), K.rope_table(64)
+    space = torch.zeros(64 * 16, device="cuda")
+    on_each_other = torch.as_strided(space, (4, 2, 64), (64, 64, 1))  # head 1 of a token on head 0 of the next
+    with pytest.raises(ValueError):
+        K.qk_norm_rope(q, None, pos, tab, out_q=on_each_other)
+    with pytest.raises(ValueError):
+        K.window_attend(q, q, q, [4], [0], [4], 4, out=on_each_other)
+    assert bool((space == 0).all())
+    want, _ = K.qk_norm_rope(q, None, pos, tab)
+    for strides in ((192, 72, 1), (72, 288, 1)):  # heads within a token, tokens within a head, with room in between
+        o = torch.as_strided(space, (4, 2, 64), strides)
+        got, _ = K.qk_norm_rope(q, None, pos, tab, out_q=o)
+        assert got.data_ptr() == o.data_ptr() and torch.equal(got, want)

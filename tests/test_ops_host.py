@@ -130,3 +130,18 @@ def test_shared_decode_refuses_what_is_not_shared():
     assert call([a, 7], 128) == K.ERR_BAD_REQUEST
     assert call([a], 0, layer=1) == K.ERR_INVALID_ARG
     assert p.L.kvpool_decode_attend_shared(None, 0, 0, None, 0, None, None, 0, None, None, None) == K.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("ts,hs,good", [
+    (64, 64, False), (128, 64, False), (448, 64, False), (512, 64, True), (520, 64, True), (512, 72, False), (568, 72, True),
+    (64, 64 * 99, False), (64, 64 * 100, True), (72, 72 * 99, False), (72, 72 * 99 + 64, True), (1 << 62, 64, True),
+    (1 << 62, 1 << 62, False), (64, 1 << 62, True)])
+def test_the_outer_axis_of_an_output_steps_over_the_inner_one(ts, hs, good):
+    """8 heads of 100 tokens: a head of one token on a head of another is refused, however large both strides are."""
+    o = heads(8, ts=ts, hs=hs)
+    if not good:
+        assert rope(T=100, q=heads(8), qo=o) == K.ERR_INVALID_ARG
+        assert rope(T=100, k=heads(8), ko=o) == K.ERR_INVALID_ARG
+    assert window([0], [0], [0], out=o, q_rows=100) == (K.OK if good else K.ERR_INVALID_ARG)
+    assert window([0], [0], [0], out=o, q_rows=1) == K.OK
+    assert window([0], [0], [0], out=heads(1, ts=ts, hs=0), q=heads(1), k=heads(1), v=heads(1)) == K.OK
