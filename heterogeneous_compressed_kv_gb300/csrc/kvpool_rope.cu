@@ -310,6 +310,15 @@ extern "C" int kvpool_qk_norm_rope(int32_t dtype, int32_t head_dim, int64_t n_to
     X.heads = in[i]->heads;
     X.steps = (X.heads + per_step - 1) / per_step;
   }
+  for (int i = 0; i < 2; ++i) {  // an output is its own input or lies apart from everything
+    if (P.t[i].steps == 0) continue;
+    for (int j = 0; j < 2; ++j) {
+      if (P.t[j].steps == 0) continue;
+      if (!(i == j && rows_same(*out[i], *in[i], n_tokens)) && rows_meet(*out[i], n_tokens, *in[j], n_tokens, head_dim, vb))
+        return KVPOOL_ERR_INVALID_ARG;
+      if (i < j && rows_meet(*out[i], n_tokens, *out[j], n_tokens, head_dim, vb)) return KVPOOL_ERR_INVALID_ARG;
+    }
+  }
   const int steps = P.t[0].steps + P.t[1].steps;
   if (n_tokens == 0 || steps == 0) return KVPOOL_OK;
   if (rot_dim > 0 && (!d_table || !d_positions)) return KVPOOL_ERR_INVALID_ARG;

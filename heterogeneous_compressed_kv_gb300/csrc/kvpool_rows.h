@@ -23,4 +23,40 @@ inline bool rows_apart(const kvpool_heads& h, int64_t tokens, int32_t dim) {
   return lo >= dim && (hi - dim) / (n - 1) >= lo;  // hi >= lo * (n - 1) + dim
 }
 
+// The same places in the same order?
+inline bool rows_same(const kvpool_heads& a, const kvpool_heads& b, int64_t tokens) {
+  return a.data == b.data && a.heads == b.heads && (tokens <= 1 || a.token_stride == b.token_stride) &&
+         (a.heads <= 1 || a.head_stride == b.head_stride);
+}
+
+// Do na tokens of a and nb of b share a value (of vb bytes)?  Tensors in one
+// piece of memory share their strides, as the parts of a fused projection do:
+// head h of token t of a and head g of token u of b then meet where (t - u)
+// token strides and (h - g) head strides are less than dim from the distance of
+// the two tensors.  With strides that differ they are taken to meet.
+inline bool rows_meet(const kvpool_heads& a, int64_t na, const kvpool_heads& b, int64_t nb, int32_t dim, int64_t vb) {
+  if (na <= 0 || nb <= 0 || a.heads <= 0 || b.heads <= 0) return false;
+  using Wide = __int128;
+  auto bytes = [&](const kvpool_heads& h, int64_t n) {
+    return (Wide)vb * ((Wide)(n - 1) * h.token_stride + (Wide)(h.heads - 1) * h.head_stride + dim);
+  };
+  const Wide a0 = (Wide) reinterpret_cast<uintptr_t>(a.data), b0 = (Wide) reinterpret_cast<uintptr_t>(b.data);
+  if (a0 + bytes(a, na) <= b0 || b0 + bytes(b, nb) <= a0) return false;
+  if ((na > 1 && nb > 1 && a.token_stride != b.token_stride) || (a.heads > 1 && b.heads > 1 && a.head_stride != b.head_stride))
+    return true;
+  const Wide ts = (Wide)vb * (na > 1 ? a.token_stride : nb > 1 ? b.token_stride : 0);
+  const Wide hs = (Wide)vb * (a.heads > 1 ? a.head_stride : b.heads > 1 ? b.head_stride : 0);
+  const Wide row = (Wide)vb * dim;
+  for (int64_t j = 1 - (int64_t)b.heads; j < a.heads; ++j) {  // heads between the two
+    const Wide r = b0 - a0 - j * hs;                          // i token strides are nearest to r
+    for (int up = 0; up < 2; ++up) {
+      Wide i = ts > 0 ? r / ts + (r < 0 ? -up : up) : 0;
+      i = i > na - 1 ? na - 1 : i < 1 - nb ? 1 - nb : i;
+      const Wide d = r - i * ts;
+      if (d < row && -d < row) return true;
+    }
+  }
+  return false;
+}
+
 }  // namespace kvp

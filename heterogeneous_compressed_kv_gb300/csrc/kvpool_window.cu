@@ -228,6 +228,27 @@ int check_args(const kvpool_window_args* a, int32_t n, const int64_t* q_len, con
   return KVPOOL_OK;
 }
 
+// Does the output lie on rows that the call reads, other than as its queries
+// themselves?  (A tile's queries are read by the CTAs that write its outputs,
+// or by a kernel before the one that does.)
+bool out_meets_inputs(const kvpool_window_args* a, int32_t n, const int64_t* q_len, const int64_t* k_start,
+                      const int64_t* k_len, int64_t total_q) {
+  const int64_t vb = a->dtype == KVPOOL_BF16 ? 2 : 4;
+  if (!rows_same(a->out, a->q, total_q) && rows_meet(a->out, total_q, a->q, total_q, a->head_dim, vb)) return true;
+  int64_t first = INT64_MAX, end = 0;  // K and V rows of the segments
+  for (int i = 0; i < n; ++i)
+    if (q_len[i] > 0 && k_len[i] > 0) {
+      first = std::min(first, k_start[i]);
+      end = std::max(end, k_start[i] + k_len[i]);
+    }
+  if (first >= end) return false;
+  for (kvpool_heads h : {a->k, a->v}) {
+    h.data = static_cast<const uint8_t*>(h.data) + vb * first * h.token_stride;
+    if (rows_meet(a->out, total_q, h, end - first, a->head_dim, vb)) return true;
+  }
+  return false;
+}
+
 // ---- which kernel takes a segment ------------------------------------------------
 enum Form { kFormTok, kFormTc, kFormFma, kForms };
 
@@ -413,6 +434,7 @@ extern "C" int kvpool_window_attend(const kvpool_window_args* a, int32_t n, cons
   const int rc = check_args(a, n, h_q_len, h_k_start, h_k_len, &total);
   if (rc != KVPOOL_OK) return rc;
   if (total == 0) return KVPOOL_OK;
+  if (out_meets_inputs(a, n, h_q_len, h_k_start, h_k_len, total)) return KVPOOL_ERR_INVALID_ARG;
   const int64_t need = kvpool_window_workspace(a, n, h_q_len, h_k_start, h_k_len);
   if (need < 0) return (int)need;
   if (need > 0 && (!d_workspace || workspace_bytes < need || reinterpret_cast<uintptr_t>(d_workspace) % 16 != 0))

@@ -411,7 +411,8 @@ int kvpool_rope_table(int32_t rot_dim, const double* h_inv_freq, uint64_t* h_tab
  * queries.  dtype: KVPOOL_F32 or KVPOOL_BF16.  head_dim: a multiple of 8 up to
  * 256; rot_dim: a multiple of 16 up to head_dim (0: norms only, no table or
  * positions needed).  q or k may be NULL or have no heads.  An output may be
- * its own input (same data and strides); otherwise they must not overlap.
+ * its own input (same data and strides); otherwise it lies apart from q, k and
+ * the other output (between their rows in memory only with their strides).
  * Weights: [head_dim] fp32, 16-byte aligned, or NULL (ones).  d_positions: [n_tokens], any sign
  * and size.  Errors: INVALID_ARG, CUDA. */
 int kvpool_qk_norm_rope(int32_t dtype, int32_t head_dim, int64_t n_tokens, const kvpool_heads* q,
@@ -430,7 +431,9 @@ int kvpool_qk_norm_rope(int32_t dtype, int32_t head_dim, int64_t n_tokens, const
  * that sees nothing, or scores of -inf alone, gives zeros and -inf; one that
  * sees a score that is NaN or +inf gives NaN in out and d_lse.  q.heads must be a multiple (up to
  * 16) of k.heads: query head h reads key head h / (q.heads / k.heads).
- * out: like q, in dtype; d_lse: [q_rows][q.heads] fp32 natural-log sums of
+ * out: like q, in dtype; it may be q itself (same data and strides), otherwise
+ * it lies apart from q, k and v (between their rows in memory only with their
+ * strides; this is looked at by the call, not for its workspace's size).  d_lse: [q_rows][q.heads] fp32 natural-log sums of
  * the exponentials, or NULL.  Query rows behind the last segment are left as
  * they were.  K/V rows that no query of a segment sees (outside it, between
  * the first tokens and the window) may hold anything; a NaN or infinity in a

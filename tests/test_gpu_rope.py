@@ -154,3 +154,45 @@ def test_outputs_whose_heads_lie_on_each_other_are_refused():
         o = torch.as_strided(space, (4, 2, 64), strides)
         got, _ = K.qk_norm_rope(q, None, pos, tab, out_q=o)
         assert got.data_ptr() == o.data_ptr() and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("T", [1, 2, 5])
+def test_outputs_among_the_inputs_rows(T):
+    """The layouts of one buffer that lie apart, or in place, give what an output of its own gives; all others are refused
+    and write nothing."""
+    from tests.test_ops_host import FUSED, P16, meets
+    g = torch.Generator(device="cuda").manual_seed(4)
+    pos, tab = torch.arange(T, device="cuda") + 3, K.rope_table(64)
+    for layout in FUSED:
+        space = torch.randn((4096,), device="cuda", generator=g).bfloat16()
+        keep = space.clone()
+        q, k, o = (torch.as_strided(space, (T, n, 64), (ts, hs, 1), (p - P16) // 2) for p, ts, hs, n, _ in layout)
+        wq, wk = K.qk_norm_rope(q.clone(), k.clone(), pos, tab)
+        ww = K.window_attend(q.clone(), k.clone(), k.clone(), [T], [0], [T], 16)
+        if meets(*layout, T):
+            with pytest.raises(K.KvpoolError):
+                K.qk_norm_rope(q, k, pos, tab, out_q=o)
+            with pytest.raises(K.KvpoolError):
+                K.window_attend(q, k, k, [T], [0], [T], 16, out=o)
+            assert torch.equal(space, keep)
+            continue
+        lk = k.clone()
+        oq, ok = K.qk_norm_rope(q, k, pos, tab, out_q=o)
+        assert torch.equal(oq, wq) and torch.equal(ok, wk) and torch.equal(k, lk)
+        space.copy_(keep)
+        assert torch.equal(K.window_attend(q, k, k, [T], [0], [T], 16, out=o), ww) and torch.equal(k, lk)
+
+
+@pytest.mark.parametrize("ql,kl,window,dtype,scale", [
+    ([1, 3], [40, 300], 64, torch.bfloat16, None), ([1], [9000], 8000, torch.bfloat16, None), ([2], [9000], 8000, torch.float32, None),
+    ([70, 300, 1], [100, 500, 90], 128, torch.bfloat16, None), ([40], [5000], 4096, torch.bfloat16, None),
+    ([70, 300], [100, 500], 128, torch.float32, None), ([70, 300], [100, 500], 128, torch.bfloat16, -0.1)])
+def test_window_outputs_in_the_queries_place(ql, kl, window, dtype, scale):
+    g = torch.Generator(device="cuda").manual_seed(sum(kl))
+    rows = torch.randn((sum(ql), 6 + 2, 64), device="cuda", generator=g).to(dtype)
+    k, v = (torch.randn((sum(kl), 2, 64), device="cuda", generator=g).to(dtype) for _ in range(2))
+    ks = [0] + list(np.cumsum(kl)[:-1])
+    keep, q = rows.clone(), rows[:, :6]
+    want = K.window_attend(q, k, v, ql, ks, kl, window, 2, scale=scale)
+    got = K.window_attend(q, k, v, ql, ks, kl, window, 2, scale=scale, out=q)
+    assert got.data_ptr() == rows.data_ptr() and torch.equal(got, want) and torch.equal(rows[:, 6:], keep[:, 6:])

@@ -145,3 +145,61 @@ def test_the_outer_axis_of_an_output_steps_over_the_inner_one(ts, hs, good):
     assert window([0], [0], [0], out=o, q_rows=100) == (K.OK if good else K.ERR_INVALID_ARG)
     assert window([0], [0], [0], out=o, q_rows=1) == K.OK
     assert window([0], [0], [0], out=heads(1, ts=ts, hs=0), q=heads(1), k=heads(1), v=heads(1)) == K.OK
+
+
+def row(n, at, ts, hs, heads=None):
+    """n heads of 64 bf16 values from value `at` of one buffer on."""
+    return (P16 + 2 * at, ts, hs, n, 0)
+
+
+def brute(a, na, b, nb, dim=64):
+    pos = lambda x, n: {(x[0] - P16) // 2 + t * x[1] + h * x[2] + j for t in range(n) for h in range(x[3])  # noqa: E731
+                        for j in range(dim)}
+    return not pos(a, na).isdisjoint(pos(b, nb))
+
+
+FUSED = [  # q, k (2 heads each unless said), output; the strides of each in one buffer
+    (row(2, 0, 256, 64), row(2, 128, 256, 64), row(2, 0, 256, 64)),           # the queries' own place
+    (row(2, 0, 256, 64), row(2, 128, 256, 64), row(2, 128, 256, 64)),         # the keys' place
+    (row(2, 0, 256, 64), row(2, 128, 256, 64), row(2, 64, 256, 64)),          # a head behind the queries
+    (row(2, 0, 256, 64), row(2, 128, 256, 64), row(2, 256, 256, 64)),         # a token behind them
+    (row(2, 0, 384, 64), row(2, 128, 384, 64), row(2, 256, 384, 64)),         # a third part of the rows
+    (row(2, 0, 384, 192), row(2, 64, 384, 192), row(2, 128, 384, 192)),       # parts of each head
+    (row(2, 0, 384, 192), row(2, 64, 384, 192), row(2, 72, 384, 192)),
+    (row(2, 0, 64, 64 * 20), row(2, 64 * 5, 64, 64 * 20), row(2, 64 * 10, 64, 64 * 20)),  # tokens inside heads
+    (row(2, 0, 64, 64 * 20), row(2, 64 * 5, 64, 64 * 20), row(2, 64 * 8, 64, 64 * 20)),
+    (row(2, 0, 0, 64), row(2, 128, 0, 64), row(2, 256, 128, 64)),             # one row for many
+    (row(2, 0, 0, 64), row(2, 128, 0, 64), row(2, 128, 128, 64)),
+    (row(2, 0, 384, 64), row(1, 128, 384, 0), row(2, 192, 384, 64)),          # one key head
+    (row(2, 0, 384, 64), row(1, 128, 384, 0), row(2, 128, 384, 64)),
+]
+
+
+def meets(q, k, o, T):
+    """Is that output neither the queries themselves nor apart from queries and keys?"""
+    own = o[0] == q[0] and o[2] == q[2] and (T == 1 or o[1] == q[1])
+    return not own and brute(o, T, q, T) or brute(o, T, k, T)
+
+
+MET = [(i, T) for i in range(len(FUSED)) for T in (1, 2, 5) if meets(*FUSED[i], T)]
+
+
+@pytest.mark.parametrize("case,T", MET)
+def test_outputs_on_rows_that_are_read_are_refused(case, T):
+    """(Those that are accepted are run in tests/test_gpu_rope.py.)"""
+    q, k, o = FUSED[case]
+    assert rope(T=T, q=q, k=k, qo=o, ko=row(k[3], 10 ** 6, 256, 64)) == K.ERR_INVALID_ARG
+    if k[3] == q[3]:
+        assert rope(T=T, q=k, k=q, qo=row(k[3], 10 ** 6, 256, 64), ko=o) == K.ERR_INVALID_ARG
+    seg = ([T], [0], [T])
+    a = K._WINDOW_ARGS.pack(K.BF16, 64, *q, *k, *k, *o, T, T, 0, 16, 0, 0.125, 0)
+    seg = [np.array(x, np.int64) for x in seg]
+    assert K.lib().kvpool_window_attend(a, 1, *(x.ctypes.data for x in seg), P16, 1 << 30, None) == K.ERR_INVALID_ARG
+
+
+def test_outputs_on_each_other_are_refused():
+    for at in (0, 64, 128 * 3 + 64):
+        assert rope(T=4, q=row(2, 0, 128, 64), k=row(2, 4096, 128, 64), qo=row(2, 9000 * 8, 128, 64),
+                    ko=row(2, 9000 * 8 + at, 128, 64)) == K.ERR_INVALID_ARG
+    # strides that differ in one piece of memory
+    assert rope(T=4, q=row(2, 0, 256, 64), qo=row(2, 128, 512, 64)) == K.ERR_INVALID_ARG
