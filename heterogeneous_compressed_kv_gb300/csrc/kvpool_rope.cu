@@ -7,12 +7,14 @@
 //   (y_a, y_b) -> (y_a cos t - y_b sin t, y_b cos t + y_a sin t)
 // over the pairs (a, b) of the first rot_dim dims, t = p * freq_i.
 //
-// The table holds freq_i / (2 pi) as a 64-bit fraction of a turn, so p *
-// table[i] modulo 2^64 is the angle's place in its turn: the integer product
-// loses nothing at any position (p * freq_i in fp32 is off by 0.06 rad at p =
-// 2^20), and three integer multiplies replace a 64-bit float product and its
-// range reduction.  Its top 32 bits as a signed number, times 2^-31, are the
-// angle in units of pi in [-1, 1): off by 2^-25 turns at most.
+// The table holds freq_i / (2 pi) modulo 1 as a 64-bit fraction of a turn, so p
+// * table[i] modulo 2^64 is the angle's place in its turn: the integer product
+// loses nothing of the table (p * freq_i in fp32 is off by 0.06 rad at p = 2^20),
+// and three integer multiplies replace a 64-bit float product and its range
+// reduction.  Its top 32 bits as a signed number, times 2^-31, are the angle in
+// units of pi in [-1, 1): off by 2^-25 turns at most.  The table itself is a
+// quotient in doubles (two roundings) cut off at 2^-64: an angle of N turns at
+// position p is off by N 2^-52 + p 2^-64 more, 2^-25 turns at 2^27 of them.
 //
 // Bound: HBM (one read and one write of every value).  A warp takes one token
 // and a run of its heads: the lanes work out the token's rot_dim / 2 sines and

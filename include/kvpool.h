@@ -397,7 +397,8 @@ typedef struct kvpool_heads {
 
 /* Rotation table of kvpool_qk_norm_rope, on the host: h_table[i] =
  * h_inv_freq[i] / (2 pi) modulo 1 as a 64-bit fraction of a turn, i <
- * rot_dim / 2.  Copy it to the device once.  Errors: INVALID_ARG (rot_dim
+ * rot_dim / 2, the quotient taken in doubles (so the double nearest to pi / 2 is
+ * a quarter turn).  Copy it to the device once.  Errors: INVALID_ARG (rot_dim
  * negative, above 256 or not a multiple of 16; a frequency that is not
  * finite). */
 int kvpool_rope_table(int32_t rot_dim, const double* h_inv_freq, uint64_t* h_table);
@@ -413,8 +414,9 @@ int kvpool_rope_table(int32_t rot_dim, const double* h_inv_freq, uint64_t* h_tab
  * positions needed).  q or k may be NULL or have no heads.  An output may be
  * its own input (same data and strides); otherwise it lies apart from q, k and
  * the other output (between their rows in memory only with their strides).
- * Weights: [head_dim] fp32, 16-byte aligned, or NULL (ones).  d_positions: [n_tokens], any sign
- * and size.  Errors: INVALID_ARG, CUDA. */
+ * Weights: [head_dim] fp32, 16-byte aligned, or NULL (ones).  d_positions: [n_tokens], of any sign
+ * and size; the angle of position p, |p * inv_freq[i]| = 2 pi N, is off by
+ * 2^-25 + 2^-52 N + 2^-64 |p| turns at most (2^-24 at N = 2^27).  Errors: INVALID_ARG, CUDA. */
 int kvpool_qk_norm_rope(int32_t dtype, int32_t head_dim, int64_t n_tokens, const kvpool_heads* q,
                         const kvpool_heads* k, const kvpool_heads* q_out, const kvpool_heads* k_out,
                         const float* d_q_weight, const float* d_k_weight, float eps, int32_t rot_dim,

@@ -196,3 +196,40 @@ def test_window_outputs_in_the_queries_place(ql, kl, window, dtype, scale):
     want = K.window_attend(q, k, v, ql, ks, kl, window, 2, scale=scale)
     got = K.window_attend(q, k, v, ql, ks, kl, window, 2, scale=scale, out=q)
     assert got.data_ptr() == rows.data_ptr() and torch.equal(got, want) and torch.equal(rows[:, 6:], keep[:, 6:])
+
+
+def exact_turns(p, f):
+    """The fraction of a turn of angle p f, from integers: pi to 400 bits by Machin's formula."""
+    from fractions import Fraction
+    one = 1 << 400
+
+    def arctan_inv(n):
+        total, term, k = 0, one // n, 1
+        while term:
+            total += term // k if k % 4 == 1 else -(term // k)
+            term //= n * n
+            k += 2
+        return total
+    two_pi = Fraction(2 * 4 * (4 * arctan_inv(5) - arctan_inv(239)), one)
+    t = Fraction(int(p)) * Fraction(float(f)) / two_pi
+    return float(t - (t.numerator // t.denominator)), abs(float(t))
+
+
+@pytest.mark.parametrize("p", [1 << 20, 1 << 31, 1 << 40, -(1 << 40) - 12345, 1 << 50])
+def test_angles_of_far_positions_hold_what_is_said_of_them(p):
+    """Frequencies of no particular relation to a turn: 2^-25 turns, 2^-52 of the turns and p 2^-64 (cosine and sine move
+    by 2 pi times that at most), and fp32 arithmetic as in check().  The last of the three: a table entry is cut off at
+    2^-64, so it is short of the quotient by less than that, and p of them by less than p 2^-64."""
+    f = np.array([1.0, 0.7316, 10000 ** -0.25, 0.1, 3.3, 2.0 ** -9 * 1.37, 1e-4, 17.77])
+    x = torch.randn((1, 3, 16), device="cuda")
+    y, _ = K.qk_norm_rope(x, None, torch.tensor([p], device="cuda"), K.rope_table(16, inv_freq=f))
+    turns, count = (torch.tensor(z, dtype=torch.float64) for z in zip(*(exact_turns(p, v) for v in f)))
+    n = x.double().cpu()
+    n = n / torch.sqrt((n * n).mean(-1, keepdim=True) + 1e-6)
+    a, b = n[..., :8], n[..., 8:]
+    c, s = torch.cos(2 * np.pi * turns), torch.sin(2 * np.pi * turns)
+    mag = torch.cat([torch.sqrt(a * a + b * b)] * 2, -1)
+    want = torch.cat([a * c - b * s, b * c + a * s], -1)
+    tol = (2.0 ** -20 + 2 * np.pi * (2.0 ** -25 + count * 2.0 ** -52 + abs(p) * 2.0 ** -64)).repeat(2) * mag
+    err = (y.double().cpu() - want).abs()
+    assert bool((err <= tol).all()), float((err / tol).max())
