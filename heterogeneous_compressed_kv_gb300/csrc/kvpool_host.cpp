@@ -348,6 +348,7 @@ struct kvpool {
   std::vector<int32_t> loc;
   std::set<int32_t> hot_free, host_free;
   uint32_t epoch = 0;
+  int64_t share_bytes = -1;  // kvpool_set_share_bytes
   uint8_t* host_pool = nullptr;  // device alias of the caller's host slots
   int64_t host_pool_bytes = 0;
   std::string err;
@@ -1252,7 +1253,7 @@ static int decode_attend(kvpool_t* p, int32_t layer, int32_t n, const int32_t* h
   // heads x 64 the two meet at 64 x 256, 32 x 512 and 16 x 256, with 4 x 64 in
   // fp32 at 64 x 300 and 32 x 1,024 (20 to 66 MB).
   constexpr int64_t kShareBytes = 64LL << 20;
-  const bool share = (n - 1) * sh_blocks * p->lay.pd.entry_bytes >= kShareBytes;
+  const bool share = (n - 1) * sh_blocks * p->lay.pd.entry_bytes >= (p->share_bytes < 0 ? kShareBytes : p->share_bytes);
   const int n_sh = share && p->lay.layers[layer].has_hca ? (int)sh_blocks : 0;
   if (!p->device()) return p->fail(KVPOOL_ERR_INVALID_ARG, "decode_attend: pool has no device");
   if (n == 0) return KVPOOL_OK;
@@ -1445,6 +1446,12 @@ int kvpool_decode_attend_shared(kvpool_t* p, int32_t layer, int32_t n, const int
                                 void* stream) {
   if (!p) return KVPOOL_ERR_INVALID_ARG;
   return decode_attend(p, layer, n, h_req_ids, n_shared, d_q, d_q_idx, top_k, d_out, d_topk_out, stream);
+}
+
+int kvpool_set_share_bytes(kvpool_t* p, int64_t bytes) {
+  if (!p) return KVPOOL_ERR_INVALID_ARG;
+  p->share_bytes = bytes;
+  return KVPOOL_OK;
 }
 
 int kvpool_request_info(const kvpool_t* p, int32_t r, kvpool_info* info, int32_t* ids, int32_t cap) {

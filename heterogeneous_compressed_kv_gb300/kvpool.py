@@ -35,7 +35,7 @@ EXPORTS = ["kvpool_required_bytes", "kvpool_create", "kvpool_destroy", "kvpool_a
            "kvpool_offload", "kvpool_fetch", "kvpool_block_location", "kvpool_epoch", "kvpool_block_activity",
            "kvpool_inactive_blocks", "kvpool_wait_selftest", "kvpool_topk_static_check", "kvpool_rope_table",
            "kvpool_qk_norm_rope", "kvpool_window_workspace", "kvpool_window_attend",
-           "kvpool_decode_attend_shared", "kvpool_window_check"]
+           "kvpool_decode_attend_shared", "kvpool_window_check", "kvpool_set_share_bytes"]
 
 
 class KvpoolError(RuntimeError):
@@ -96,6 +96,7 @@ def lib():
         L.kvpool_append.argtypes = [vp, i32, vp, vp, vp, vp, vp, vp]
         L.kvpool_decode_attend.argtypes = [vp, i32, i32, vp, vp, vp, i32, vp, vp, vp]
         L.kvpool_decode_attend_shared.argtypes = [vp, i32, i32, vp, i64, vp, vp, i32, vp, vp, vp]
+        L.kvpool_set_share_bytes.argtypes = [vp, i64]
         L.kvpool_request_info.argtypes = [vp, i32, C.POINTER(_Info), vp, i32]
         L.kvpool_block_refcount.argtypes = [vp, i32]
         L.kvpool_free_block_count.argtypes = [vp]
@@ -633,6 +634,10 @@ class Pool:
         rc = self.L.kvpool_decode_attend_shared(self.h, layer, req.size, req.tobytes(), n_shared, _ptr(q), _ptr(q_idx),
                                                 top_k, _ptr(out), _ptr(topk_out), _stream(stream))
         return self._check(rc, "decode_attend_shared") if check else rc
+
+    def set_share_bytes(self, nbytes: int) -> None:
+        """The reading that decode_attend_shared has to save to share entries (negative: the measured rule)."""
+        self._check(self.L.kvpool_set_share_bytes(self.h, nbytes), "set_share_bytes")
 
     # ---- queries ----
     def request_info(self, req: int, cap: int = 1 << 16):

@@ -327,8 +327,9 @@ int kvpool_decode_attend(kvpool_t* pool, int32_t layer, int32_t n, const int32_t
  * sealed blocks ([P3] s2.2; kvpool_share_prefix): the HCA entries of those
  * blocks are read once for the whole batch instead of once per request, as a
  * dense product of all requests' queries per head (where that saves 64 MB of
- * reading or more: below, the call is kvpool_decode_attend).  Same arguments, outputs
- * and selected entries as kvpool_decode_attend; outputs differ from its by
+ * reading or more: below, the call is kvpool_decode_attend; see
+ * kvpool_set_share_bytes).  Same arguments, outputs and selected entries as
+ * kvpool_decode_attend; outputs differ from its by
  * the order of the fp32 sums (and, with an fp8 cache, by being closer to the
  * decoded values).  The indexer scan, the selected CSA entries and the window
  * stay per request.  n_shared: a multiple of m' (0: nothing is shared).
@@ -338,6 +339,11 @@ int kvpool_decode_attend(kvpool_t* pool, int32_t layer, int32_t n, const int32_t
 int kvpool_decode_attend_shared(kvpool_t* pool, int32_t layer, int32_t n, const int32_t* h_req_ids, int64_t n_shared,
                                 const void* d_q, const void* d_q_idx, int32_t top_k, float* d_out, int32_t* d_topk_out,
                                 void* stream);
+
+/* How much reading kvpool_decode_attend_shared has to save to share entries:
+ * bytes (0: every shared entry is read once for the batch, however few), or
+ * negative for the measured rule, which a new pool has.  Errors: INVALID_ARG. */
+int kvpool_set_share_bytes(kvpool_t* pool, int64_t bytes);
 
 /* Top-k selection over a caller's score matrix that allocates nothing.  The
  * design pages have no counterpart of this entry point: it is the indexer's

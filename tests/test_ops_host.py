@@ -203,3 +203,11 @@ def test_outputs_on_each_other_are_refused():
                     ko=row(2, 9000 * 8 + at, 128, 64)) == K.ERR_INVALID_ARG
     # strides that differ in one piece of memory
     assert rope(T=4, q=row(2, 0, 256, 64), qo=row(2, 128, 512, 64)) == K.ERR_INVALID_ARG
+
+
+def test_share_bytes():
+    from tests.test_abi_host import base_workload, cfg_of
+    p = K.Pool(cfg_of(base_workload(layer_kinds=[K.HCA])))
+    for n in (0, 1 << 50, -1):
+        p.set_share_bytes(n)
+    assert p.L.kvpool_set_share_bytes(None, 0) == K.ERR_INVALID_ARG
