@@ -1254,7 +1254,7 @@ static int decode_attend(kvpool_t* p, int32_t layer, int32_t n, const int32_t* h
   // fp32 at 64 x 300 and 32 x 1,024 (20 to 66 MB).
   constexpr int64_t kShareBytes = 64LL << 20;
   const bool share = (n - 1) * sh_blocks * p->lay.pd.entry_bytes >= (p->share_bytes < 0 ? kShareBytes : p->share_bytes);
-  const int n_sh = share && p->lay.layers[layer].has_hca ? (int)sh_blocks : 0;
+  const int n_share = share && p->lay.layers[layer].has_hca ? (int)sh_blocks : 0;
   if (!p->device()) return p->fail(KVPOOL_ERR_INVALID_ARG, "decode_attend: pool has no device");
   if (n == 0) return KVPOOL_OK;
   if (reinterpret_cast<uintptr_t>(d_q) % 16 != 0) return p->fail(KVPOOL_ERR_INVALID_ARG, "decode_attend: q not 16-byte aligned");
@@ -1301,15 +1301,19 @@ static int decode_attend(kvpool_t* p, int32_t layer, int32_t n, const int32_t* h
     int score_ctas = 0, key_ctas = 0;
     int64_t score_bytes = 0, attend_bytes = 0, out_bytes = 0;
     std::vector<int64_t> req_segs;  // segments each request has scored
+    int64_t least = 0;              // partials with shared entries, of the longest splits
     for (int i = 0; i < gn; ++i) {
       const Request& q = p->reqs[h_req_ids[g0 + i]];
       const int32_t n_cand = Ld.has_csa ? (int32_t)(q.length / p->cfg.m) : 0;
       const int32_t k = std::min(top_k, n_cand);
+      const int64_t own = q.length / p->cfg.m_prime - n_share + std::min<int64_t>(q.length, p->cfg.n_win);
+      least += (own + max_split_len - 1) / max_split_len + (k + max_split_len - 1) / max_split_len + 1;
       if (k != n_cand && k > 0) {
         total_segs += (n_cand + EPS - 1) / EPS;
         req_segs.push_back((n_cand + EPS - 1) / EPS);
       }
     }
+    const int n_sh = least <= kMaxSplits ? n_share : 0;
     // a score CTA takes a run of one request's segments; every request rounds
     // its CTA count up, so lengthen the runs until the CTAs fit one wave
     const int64_t score_target = (int64_t)kScoreCtasPerSm * p->n_sms;
@@ -1364,10 +1368,14 @@ static int decode_attend(kvpool_t* p, int32_t layer, int32_t n, const int32_t* h
     }
     len0 = fit_one_wave(src_0, len0, max_split_len, target0);
     len1 = fit_one_wave(src_1, len1, max_split_len, attend_target);
-    int split2 = n_sh > 0 ? shared_splits(pd, gn, n_sh, p->n_sms) : 0;
-    int splits0 = 0, splits1 = 0, parts = 0;
-    for (int pass = 0; pass < 3; ++pass) {
-      splits0 = splits1 = parts = 0;
+    // The partials of a launch have kMaxSplits places.  The shared entries' runs
+    // take what the other parts leave of them (4 heads x 64 requests behind
+    // 8,192 entries want 76 runs and get 62; with 4 the step took 84 us instead
+    // of 26); the other parts' splits are lengthened where they alone are too
+    // many.
+    int split2 = 0, splits0 = 0, splits1 = 0, parts = 0;
+    for (int pass = 0; pass < 2; ++pass) {
+      splits0 = splits1 = 0;
       for (int i = 0; i < gn; ++i) {
         AttendReq& R = P.reqs[i];
         R.split_len0 = (int32_t)len0;
@@ -1376,19 +1384,24 @@ static int decode_attend(kvpool_t* p, int32_t layer, int32_t n, const int32_t* h
         R.n_split1 = (int32_t)(((int64_t)R.k + len1 - 1) / len1);
         R.cta_base0 = splits0;
         R.cta_base1 = splits1;
-        R.part_base = parts;
         splits0 += R.n_split0;
         splits1 += R.n_split1;
-        parts += R.n_split0 + R.n_split1 + split2;
       }
+      if (n_sh > 0)
+        split2 = std::max(1, std::min(shared_splits(pd, gn, n_sh, p->n_sms), (kMaxSplits - splits0 - splits1) / gn));
+      parts = splits0 + splits1 + gn * split2;
       if (parts <= kMaxSplits) break;
       len0 = len1 = max_split_len;
-      split2 = std::min(split2, pass == 0 ? 4 : 1);
     }
     if (parts > kMaxSplits) {
       rc = -1;
       p->fail(KVPOOL_ERR_INVALID_ARG, "decode_attend: too many attention splits");
       break;
+    }
+    for (int i = 0, base = 0; i < gn; ++i) {
+      AttendReq& R = P.reqs[i];
+      R.part_base = base;
+      base += R.n_split0 + R.n_split1 + split2;
     }
     const int ctas0 = splits0, ctas1 = splits1;
     P.total_score_ctas = score_ctas;

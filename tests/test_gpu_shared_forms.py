@@ -199,3 +199,72 @@ def test_large_scores():
             assert bool(torch.isfinite(out).all())
             # scores of up to a few thousand are off by 2^-24 of themselves: 2^-10 in the weights
             assert float((out - ref).norm() / ref.norm()) <= 2.0 ** -8
+
+
+def filled(w, n, entries, seed=1):
+    """n requests behind a prefix whose HCA entries are random numbers (written into the pool as its layout says; the
+    window's tokens are zeros), the entries and queries."""
+    g = GpuCase(w, n, entries + 4, entries + 2, n, 4)
+    slots = [g.pool.alloc_request() for _ in range(n)]
+    step = 1 << 15
+    z = torch.zeros((1, step, g.HD), dtype=g.tdtype, device="cuda")
+    for p in range(0, 128 * entries, step):
+        m = min(step, 128 * entries - p)
+        zs = z[:, :m].contiguous()
+        g.pool.append([slots[0]], [m], zs, zs, None)
+    for s in slots[1:]:
+        g.pool.share_prefix(s, slots[0], 128 * entries, z[:, :128].contiguous(), z[:, :128].contiguous())
+    assert [int(x) for x in g.pool.request_info(slots[0])[2]] == list(range(entries))
+    d = g.pool.layout(0)
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    kv = torch.randn((entries, 2, w["heads"], w["head_dim"]), device="cuda", generator=gen)
+    kv = kv.to({K.F32: torch.float32, K.BF16: torch.bfloat16}[w["cache_dtype"]])
+    pool = g.arena[d["hca_offset"]:d["hca_offset"] + entries * d["hca_block_bytes"]].view(entries, -1)
+    pool[:, :2 * g.HD * g.vs] = kv.view(entries, -1).view(torch.uint8)
+    return g, slots, kv, torch.randn((n, w["heads"], w["head_dim"]), device="cuda", generator=gen).to(g.tdtype)
+
+
+def exact(kv, q):
+    """In 64 bits, over the entries and a window of 128 zeros."""
+    out = torch.empty(q.shape, dtype=torch.float64, device="cuda")
+    for h in range(q.shape[1]):
+        s = q[:, h].double() @ kv[:, 0, h].double().T / math.sqrt(q.shape[2])
+        m = s.amax(1, keepdim=True).clamp(min=0)
+        p = torch.exp(s - m)
+        out[:, h] = p @ kv[:, 1, h].double() / (p.sum(1, keepdim=True) + 128 * torch.exp(-m))
+    return out
+
+
+def off(w, n, entries):
+    """The outputs' distance from 64 bits, of their norm."""
+    g, slots, kv, q = filled(w, n, entries)
+    g.pool.set_share_bytes(0)
+    out = torch.empty(q.shape, device="cuda")
+    assert launches(g.pool, lambda: g.pool.decode_attend_shared(0, slots, 128 * entries, q, None, 0, out)) == 2
+    assert g.pool.check_device() == 0
+    want = exact(kv, q)
+    return float((out.double() - want).norm() / want.norm())
+
+
+@pytest.mark.parametrize("heads,dim,n,entries", [(4, 64, 64, 8192), (4, 128, 64, 8192), (8, 128, 128, 8192)])
+def test_more_runs_than_partials_have_places(heads, dim, n, entries):
+    """Batches whose runs do not all get a place for their partials get as many as there are: runs stay short, and their
+    sums (which the tensor core cuts off, tile after tile) within what close() allows."""
+    assert off(dict(BASE, heads=heads, head_dim=dim), n, entries) <= 2.0 ** -18
+
+
+def test_entries_are_not_shared_where_their_partials_would_be_too_many():
+    """256 requests with 16 partials each of their windows and entries fill all places: the call is the ordinary one,
+    which takes them, and not refused."""
+    n, blocks = 256, 127
+    w = dict(BASE, heads=4, head_dim=64, n_win=128 * blocks)
+    g = GpuCase(w, n, blocks + 2, blocks + 2, n, 4)
+    slots = [g.pool.alloc_request() for _ in range(n)]
+    k, v, _ = g.tokens([0], [0], [128 * blocks])
+    g.pool.append([slots[0]], [128 * blocks], k, v, None)
+    for s in slots[1:]:
+        g.pool.share_prefix(s, slots[0], 128 * blocks, k, v)
+    out, ref = shared(g, 0, slots, list(range(n)), 0, 128 * blocks, more=0)
+    assert torch.equal(out, ref)
+    few, _ = shared(g, 0, slots[:9], list(range(9)), 0, 128 * blocks)  # fewer requests share
+    close(few, ref[:9], *BF)
