@@ -268,3 +268,9 @@ def test_entries_are_not_shared_where_their_partials_would_be_too_many():
     assert torch.equal(out, ref)
     few, _ = shared(g, 0, slots[:9], list(range(9)), 0, 128 * blocks)  # fewer requests share
     close(few, ref[:9], *BF)
+
+
+@pytest.mark.parametrize("heads,dim,n,entries", [(64, 64, 30, 16384), (64, 64, 16, 32768)])
+def test_long_runs_of_the_small_products(heads, dim, n, entries):
+    """8,192 and 16,384 entries to a CTA, whose sums the tensor core would cut off 1,536 times: still within close()."""
+    assert off(dict(BASE, m=32, heads=heads, head_dim=dim), n, entries) <= 2.0 ** -18
