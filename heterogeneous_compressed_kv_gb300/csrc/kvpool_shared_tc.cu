@@ -20,9 +20,13 @@
 // 4.5 us less, with one product of three 2.4 us, with its entries in the L2 cache
 // 3 us.  Four rows to a gathering tensor copy in place of the threads' 16-byte
 // ones: 68 us a step instead of 46.
-// Two runs: the tensor core cuts each sum's last bit off instead of rounding it,
-// 24 times per tile; over one run of 8 tiles that made the outputs' error 1.0e-6
-// (relative, 64 requests behind 8,192 entries), over two 0.5e-6.
+// The tensor core cuts each sum's last bit off instead of rounding it, 24 times
+// per tile, so that a running sum loses the more the longer it is: of the outputs'
+// norm 1.4e-6 over 4 tiles of random entries and 2.9e-6 over 8 (each other fp32
+// step together 0.3e-6; decode_attend 0.6e-6).  Hence two runs to a CTA, and a sum
+// of 8 tiles at most, after which it is added to its run's partial in global
+// memory (by the threads that wrote it).  Behind 16,384 entries (64 requests of 16
+// heads x 128, runs of 8 tiles) sums of 4 took 69.5 us a step and sums of 8 58.6.
 // Outputs are rescaled when a row's maximum grows by more than 2^8 (see
 // kvpool_window_tc.cu).
 #include <cuda_runtime.h>
@@ -39,6 +43,7 @@ constexpr int kSoftmaxWarps = 8, kCopyWarps = 4;
 constexpr int kThreads = 32 * (kSoftmaxWarps + 1 + kCopyWarps);
 constexpr int kLag = 3;  // tiles on their way behind the one being started
 constexpr float kGrow = 8.0f;
+constexpr int kRunTiles = 8;  // tiles that are summed in tensor memory
 
 template <int D>
 struct Shape {
@@ -64,7 +69,8 @@ __device__ __forceinline__ bool tile_is_k(int i, int n, int& j) {
   return i % 2 == 1;
 }
 
-template <int D>
+// LONG: runs of more than kRunTiles tiles
+template <int D, bool LONG>
 __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_constant__ AttendParams P,
                                                                 const __grid_constant__ SharedShape H) {
   pdl_start();
@@ -93,6 +99,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
   // first entry of tile j, and the end of its run
   auto tile_at = [&](int j) { return j < n0 ? a + j * kKeys : mid + (j - n0) * kKeys; };
   auto run_end = [&](int j) { return j < n0 ? mid : b; };
+  // is tile j the first of its sum in tensor memory?
+  auto fresh = [&](int j) { return LONG ? (j < n0 ? j : j - n0) % kRunTiles == 0 : j == 0 || j == n0; };
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(&kv_full[i], kCopyWarps);
@@ -240,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
           for (int x = 0; x < 3; ++x)
 #pragma unroll
             for (int c = 0; c < kKeys / 16; ++c)
-              mma_ts(tmem + 256, piece[x] + 8 * c, vd + c * (2048 >> 4), kIdPV, (j > 1 && j - 1 != n0) || x > 0 || c > 0);
+              mma_ts(tmem + 256, piece[x] + 8 * c, vd + c * (2048 >> 4), kIdPV, !fresh(j - 1) || x > 0 || c > 0);
           mma_commit(&pv_done[e]);
           mma_commit(&kv_free[stage]);
           ++i;
@@ -272,33 +280,62 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       ++n_swap;
       return done;
     };
-    float m = -INFINITY, l = 0.0f;
+    float m = -INFINITY, l = 0.0f;    // of the sum in tensor memory
+    float run_m = -INFINITY, run_l = 0.0f;  // of the run's sums before it
     bool ok = true;
     // (looked up before the first scores are there: an index of its own for each
     // lane makes 32 reads of the parameters, 2 us when they are cold)
     const int64_t slot0 = shared_slot(P, min(i0 + row, P.n - 1), split);
-    // A run's maximum, sum and outputs, the last of them those of tile j
-    auto put = [&](int run, int j, float m, float l) {
+    // The sum in tensor memory, whose last tile is j, goes to its run's partial:
+    // as it is where it is the run's first one, else added to what is there
+    auto put = [&](int j, float m, float l) {
+      const int run = j >= n0;
+      const bool first = !LONG || j - (run ? n0 : 0) < kRunTiles;
+      const int64_t slot = slot0 + run;
+      float4* dst = reinterpret_cast<float4*>(P.part_o + slot * pd.HD + h * D + (D / 2) * half);
       float theirs;
       if (!warp_wait(&pv_done[j & 1], (j >> 1) & 1, err) || !exchange(l, theirs)) return false;
       tc_fence_after();
-      const int64_t slot = slot0 + run;
-      float4* dst = reinterpret_cast<float4*>(P.part_o + slot * pd.HD + h * D + (D / 2) * half);
+      l += theirs;
+      float fo = 0.0f, fn = 1.0f;
+      if (!first) {
+        const float m2 = fmaxf(run_m, m);
+        fo = ex2f(run_m - m2);
+        fn = ex2f(m - m2);
+        m = m2;
+        l = fmaf(run_l, fo, l * fn);
+      }
+      run_m = m;
+      run_l = l;
 #pragma unroll 1
       for (int c = 0; c < D / 2; c += 16) {
         uint32_t o[16];
+        float4 old[4];
+        if (!first && row < rows) {
+#pragma unroll
+          for (int y = 0; y < 4; ++y) old[y] = dst[c / 4 + y];
+        }
         __syncwarp();
         tmem_ld16(base_lane + 256 + (D / 2) * half + c, o);
         tmem_wait_ld();
         if (row < rows) {
 #pragma unroll
-          for (int y = 0; y < 4; ++y)
-            dst[c / 4 + y] = make_float4(__uint_as_float(o[4 * y]), __uint_as_float(o[4 * y + 1]),
-                                         __uint_as_float(o[4 * y + 2]), __uint_as_float(o[4 * y + 3]));
+          for (int y = 0; y < 4; ++y) {
+            float4 x = make_float4(__uint_as_float(o[4 * y]), __uint_as_float(o[4 * y + 1]),
+                                   __uint_as_float(o[4 * y + 2]), __uint_as_float(o[4 * y + 3]));
+            if (!first) {
+              const float4 w = old[y];
+              x.x = fmaf(w.x, fo, x.x * fn);
+              x.y = fmaf(w.y, fo, x.y * fn);
+              x.z = fmaf(w.z, fo, x.z * fn);
+              x.w = fmaf(w.w, fo, x.w * fn);
+            }
+            dst[c / 4 + y] = x;
+          }
         }
       }
       if (row < rows && half == 0)
-        *reinterpret_cast<float2*>(P.part_ml + (slot * pd.heads + h) * 2) = make_float2(m, l + theirs);
+        *reinterpret_cast<float2*>(P.part_ml + (slot * pd.heads + h) * 2) = make_float2(m, l);
       return true;
     };
 #pragma unroll 1
@@ -330,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
         }
         const float mn = fmaxf(mx, theirs) * scale;  // finite: some key of the tile counts
         const float m0 = m, l0 = l;
-        if (j == 0 || j == n0) {
+        if (fresh(j)) {
           m = mn;
           l = 0.0f;
         } else if (__any_sync(0xffffffffu, mn > m + kGrow)) {
@@ -377,8 +414,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
         }
         l += sum[0] + sum[1];
         tmem_wait_st();
-        // the first run's outputs leave before the second one's first product replaces them
-        if (j == n0 && !put(0, j - 1, m0, l0)) {
+        // a sum leaves before the next one's first product replaces it
+        if (j > 0 && fresh(j) && !put(j - 1, m0, l0)) {
           ok = false;
           break;
         }
@@ -387,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_ready[j & 1]);
     }
-    if (ok && live) put(n_tile > n0, n_tile - 1, m, l);
+    if (ok && live) put(n_tile - 1, m, l);
   }
   tc_fence_before();
   __syncthreads();
@@ -395,13 +432,18 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
   if (warp == kSoftmaxWarps) tmem_free(tmem, 512);
 }
 
-template <int D>
-cudaError_t launch_t(const AttendParams& p, const SharedShape& h, cudaStream_t s) {
-  auto* kern = shared_tc_kernel<D>;
+template <int D, bool LONG>
+cudaError_t launch_l(const AttendParams& p, const SharedShape& h, cudaStream_t s) {
+  auto* kern = shared_tc_kernel<D, LONG>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D>::kSmem);
   if (e != cudaSuccess) return e;
   return launch_kernel(h.pdl != 0, kern, dim3(p.pool.heads, (h.n_split + 1) / 2, (p.n + kSharedTcRows - 1) / kSharedTcRows),
                        dim3(kThreads), Shape<D>::kSmem, s, p, h);
+}
+
+template <int D>
+cudaError_t launch_t(const AttendParams& p, const SharedShape& h, cudaStream_t s) {
+  return h.n_entries > (int64_t)h.n_split * kRunTiles * kKeys ? launch_l<D, true>(p, h, s) : launch_l<D, false>(p, h, s);
 }
 
 }  // namespace

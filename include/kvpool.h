@@ -329,9 +329,10 @@ int kvpool_decode_attend(kvpool_t* pool, int32_t layer, int32_t n, const int32_t
  * dense product of all requests' queries per head (where that saves 64 MB of
  * reading or more: below, the call is kvpool_decode_attend; see
  * kvpool_set_share_bytes).  Same arguments, outputs and selected entries as
- * kvpool_decode_attend; outputs differ from its by
- * the order of the fp32 sums (and, with an fp8 cache, by being closer to the
- * decoded values).  The indexer scan, the selected CSA entries and the window
+ * kvpool_decode_attend; outputs differ from its by the order of the fp32 sums;
+ * with bf16 queries and cache, by sums that the tensor core cuts off instead of
+ * rounding (under 2^-18 of the outputs' norm, however long the prefix); with an
+ * fp8 cache, by being closer to the decoded values.  The indexer scan, the selected CSA entries and the window
  * stay per request.  n_shared: a multiple of m' (0: nothing is shared).
  * Errors: as kvpool_decode_attend; INVALID_ARG (n_shared negative),
  * NOT_SHAREABLE (n_shared not a multiple of m', or requests whose first

@@ -274,3 +274,30 @@ def test_entries_are_not_shared_where_their_partials_would_be_too_many():
 def test_long_runs_of_the_small_products(heads, dim, n, entries):
     """8,192 and 16,384 entries to a CTA, whose sums the tensor core would cut off 1,536 times: still within close()."""
     assert off(dict(BASE, m=32, heads=heads, head_dim=dim), n, entries) <= 2.0 ** -18
+
+
+@pytest.mark.parametrize("heads,dim,n,entries", [(64, 64, 256, 8192), (16, 128, 64, 16500), (8, 128, 128, 32768), (32, 128, 34, 9000),
+                                                 (64, 64, 40, 16001)])
+def test_long_runs_of_the_products_of_128_rows(heads, dim, n, entries):
+    """Runs of 8 to 63 tiles, in sums of 8 that join: within close(), however long the run."""
+    assert off(dict(BASE, m=32, heads=heads, head_dim=dim), n, entries) <= 2.0 ** -18
+
+
+def test_growing_scores_in_long_runs():
+    """Scores that grow along a run of 32 tiles, so that each of its sums outweighs those before it, and that fall, so that
+    the last ones hardly count."""
+    heads, dim, n, entries = 64, 64, 40, 8192
+    g, slots, kv, q = filled(dict(BASE, heads=heads, head_dim=dim), n, entries)
+    g.pool.set_share_bytes(0)
+    d = g.pool.layout(0)
+    pool = g.arena[d["hca_offset"]:d["hca_offset"] + entries * d["hca_block_bytes"]].view(entries, -1)
+    q.fill_(1.0)
+    for sign in (1, -1):
+        kv[:, 0] = (sign * torch.arange(entries, device="cuda") / 1000)[:, None, None].bfloat16()  # scores up to 65
+        pool[:, :2 * g.HD * 2] = kv.view(entries, -1).view(torch.uint8)
+        out = torch.empty(q.shape, device="cuda")
+        g.pool.decode_attend_shared(0, slots, 128 * entries, q, None, 0, out)
+        assert g.pool.check_device() == 0
+        want = exact(kv, q)
+        # scores of 65 are off by at most 2 * 68 * 2^-24 * 65: 2^-10.9 in the worst weight, far less in their sum
+        assert float((out.double() - want).norm() / want.norm()) <= 2.0 ** -13
