@@ -24,10 +24,6 @@
 #include "kvpool.h"
 #include "kvpool_internal.h"
 
-namespace kvp {
-int attend_max_split_len();
-}  // namespace kvp
-
 using namespace kvp;
 
 namespace {
@@ -1240,21 +1236,7 @@ static int decode_attend(kvpool_t* p, int32_t layer, int32_t n, const int32_t* h
     if ((int64_t)t.size() < sh_blocks || t[sh_blocks - 1] != p->reqs[h_req_ids[0]].table[sh_blocks - 1])
       return p->fail(KVPOOL_ERR_NOT_SHAREABLE, "decode_attend: the requests do not share that prefix");
   }
-  // Shared HCA entries.  Where few bytes are read once instead of n times, the
-  // shared entries' kernel costs more than it saves, and every request reads
-  // its own.  Steps of 16 heads x 128 in bf16 (shared / each its own, us):
-  //   requests  128 entries  256        512        1,024
-  //   64        19.0 / 16.9  19.9/21.3  20.9/30.1  23.0/48.0
-  //   32        15.6 / 12.5  16.0/14.6  16.8/19.2  17.7/28.4
-  //   16        12.6 / 10.8  13.4/11.8  14.3/14.2  15.3/19.0
-  //   8          9.6 /  9.3   9.8/10.2  13.6/11.1  13.8/13.3
-  //   8         2,400 entries 17.7 / 19.6, 4,800 entries 21.0 / 29.6
-  // 64 MB saved is at 64 x 127, 32 x 258, 16 x 533 and 8 x 1,143 of them; with 16
-  // heads x 64 the two meet at 64 x 256, 32 x 512 and 16 x 256, with 4 x 64 in
-  // fp32 at 64 x 300 and 32 x 1,024 (20 to 66 MB).
-  constexpr int64_t kShareBytes = 64LL << 20;
-  const bool share = (n - 1) * sh_blocks * p->lay.pd.entry_bytes >= (p->share_bytes < 0 ? kShareBytes : p->share_bytes);
-  const int n_share = share && p->lay.layers[layer].has_hca ? (int)sh_blocks : 0;
+  const int n_share = p->lay.layers[layer].has_hca ? (int)sh_blocks : 0;
   if (!p->device()) return p->fail(KVPOOL_ERR_INVALID_ARG, "decode_attend: pool has no device");
   if (n == 0) return KVPOOL_OK;
   if (reinterpret_cast<uintptr_t>(d_q) % 16 != 0) return p->fail(KVPOOL_ERR_INVALID_ARG, "decode_attend: q not 16-byte aligned");
@@ -1301,19 +1283,25 @@ static int decode_attend(kvpool_t* p, int32_t layer, int32_t n, const int32_t* h
     int score_ctas = 0, key_ctas = 0;
     int64_t score_bytes = 0, attend_bytes = 0, out_bytes = 0;
     std::vector<int64_t> req_segs;  // segments each request has scored
-    int64_t least = 0;              // partials with shared entries, of the longest splits
+    int64_t least = 0, least_own = 0;  // partials of the longest splits, with shared entries and without
     for (int i = 0; i < gn; ++i) {
       const Request& q = p->reqs[h_req_ids[g0 + i]];
       const int32_t n_cand = Ld.has_csa ? (int32_t)(q.length / p->cfg.m) : 0;
       const int32_t k = std::min(top_k, n_cand);
-      const int64_t own = q.length / p->cfg.m_prime - n_share + std::min<int64_t>(q.length, p->cfg.n_win);
-      least += (own + max_split_len - 1) / max_split_len + (k + max_split_len - 1) / max_split_len + 1;
+      const int64_t all = q.length / p->cfg.m_prime + std::min<int64_t>(q.length, p->cfg.n_win);
+      const int64_t sel = (k + max_split_len - 1) / max_split_len;
+      least += (all - n_share + max_split_len - 1) / max_split_len + sel + 1;
+      least_own += (all + max_split_len - 1) / max_split_len + sel;
       if (k != n_cand && k > 0) {
         total_segs += (n_cand + EPS - 1) / EPS;
         req_segs.push_back((n_cand + EPS - 1) / EPS);
       }
     }
-    const int n_sh = least <= kMaxSplits ? n_share : 0;
+    // where that costs more than it saves, every request reads its own (if the
+    // partials of that have places)
+    const bool pays = p->share_bytes >= 0 ? (gn - 1) * (int64_t)n_share * pd.entry_bytes >= p->share_bytes
+                                          : shared_pays(pd, gn, n_share, p->n_sms);
+    const int n_sh = (pays || least_own > kMaxSplits) && least <= kMaxSplits ? n_share : 0;
     // a score CTA takes a run of one request's segments; every request rounds
     // its CTA count up, so lengthen the runs until the CTAs fit one wave
     const int64_t score_target = (int64_t)kScoreCtasPerSm * p->n_sms;

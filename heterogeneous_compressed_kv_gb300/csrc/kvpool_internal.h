@@ -220,11 +220,14 @@ size_t attend_smem_bytes(const PoolDesc& pd);
 int launch_select(const AttendParams& p, void* stream, int* n_kernels, bool alone);
 int launch_attend(const AttendParams& p, int part, int ctas, void* stream, int* n_kernels);
 int launch_combine(const AttendParams& p, void* stream, int* n_kernels);
+int attend_max_split_len();  // the longest split of a request's sources
 // the first n_entries HCA entries of every request of the launch (the same
 // blocks in all of them), cut into n_split runs: partials in the slots behind
 // each request's n_split0 + n_split1 others.  pdl: the launch may start early
 // (its stream's last operation is a kernel, not another stream's event)
 int shared_splits(const PoolDesc& pd, int n, int n_entries, int n_sms);
+// is that quicker than n requests reading n_entries each?
+bool shared_pays(const PoolDesc& pd, int n, int n_entries, int n_sms);
 int launch_shared(const AttendParams& p, int n_entries, int n_split, bool pdl, void* stream, int* n_kernels);
 
 }  // namespace kvp

@@ -13,7 +13,7 @@
 // Measured as whole steps of 16 heads x 128 in bf16: 8 requests behind 2,400
 // entries 17.7 us (decode_attend 19.6), 32 behind 1,024 18 us (28; the shared
 // entries' kernel by itself 6.9), 64 behind 8,192 (kvpool_shared_tc.cu) 44 us
-// (442).  Below about 64 MB saved the caller does not come here.
+// (442).  Where it does not pay (shared_pays) the caller does not come here.
 #include <algorithm>
 
 #include <cuda_runtime.h>
@@ -427,6 +427,59 @@ int shared_splits(const PoolDesc& pd, int n, int n_entries, int n_sms) {
   const int per = pd.heads * ((n + rows - 1) / rows);
   const int most = !mma ? 3 * n_sms / per : tc ? 2 * std::max(1, n_sms / per) : n_sms / per;
   return std::max(1, std::min(most, (n_entries + 63) / 64));
+}
+
+// Does it pay?  What the call saves is n requests' reading of the entries: a time
+// per entry and request that depends on the entry's values (heads x head_dim) and
+// type, half as much again where there is more to read than one wave of
+// decode_attend's longest splits takes.  What it costs is another launch and
+// partial results (start, and kShareRequest for each request), and the tiles that
+// a multiprocessor works through one after another: 128 entries by up to 64
+// requests (small products) or 128 (5th generation, in two runs), 64 entries by 32
+// requests in the FMA form, which takes as long for 2 requests as for 32.
+//
+// Times in ns, fitted to steps of 4 and 16 heads x 64 and 8, 16 and 32 x 128, 2 to
+// 128 requests, 128 to 8,192 entries, every type.  Some of them, shared / each its
+// own in us, at 16 x 128:
+//                   8 requests,  32 requests,  64 requests,  64 requests,
+//                   2,048 entries  1,024         512          8,192
+//   bf16            16.6 / 18.8  20.1 / 29.2   26.0 / 30.6   44.0 / 442
+//   bf16 on fp8     59.6 / 17.4  28.4 / 26.3   31.7 / 26.7    276 / 328
+//   fp32 on bf16    57.0 / 19.8  29.3 / 31.4   35.0 / 33.5    284 / 474
+//   fp32            54.8 / 42.7  33.4 / 79.4   42.9 / 86.3    259 / 1,717
+// Of all 2,520 steps the slower side is taken in 89, by more than 3% in 59; of 336
+// of layers with CSA (fp8 and bf16), in 61 and 23.  With 64 MB of reading saved as
+// the rule for every type, steps that shared an fp8 cache's entries took up to 8
+// times as long as those that did not.
+constexpr double kShareRequest = 25.0;
+bool shared_pays(const PoolDesc& pd, int n, int n_entries, int n_sms) {
+  if (n < 2 || n_entries < 1) return false;
+  // an entry read by one request, at these values per entry
+  constexpr double kValues[4] = {256, 1024, 2048, 4096};
+  constexpr double kRead[3][4] = {{0.34, 1.04, 1.87, 4.05}, {0.25, 0.34, 0.56, 1.75}, {0.25, 0.29, 0.45, 1.2}};
+  const double* t = kRead[pd.cache_dtype];
+  int k = 0;
+  while (k < 2 && pd.HD > kValues[k + 1]) ++k;
+  const double per_entry = t[k] + (t[k + 1] - t[k]) * (pd.HD - kValues[k]) / (kValues[k + 1] - kValues[k]);
+  const double entries = (double)n * n_entries;
+  const double read = entries * per_entry * (entries > 3.0 * n_sms * attend_max_split_len() ? 1.5 : 1.0);
+
+  struct Cost {
+    double tile64, tile128, start;  // a tile of heads of 64 and of 128
+  };
+  const bool mma = pd.in_dtype == KVPOOL_BF16 && pd.cache_dtype == KVPOOL_BF16;
+  const bool tc = mma && shared_tc(n, n_entries);
+  const Cost c = tc                                  ? Cost{400, 650, 7000}
+                 : mma                               ? Cost{400, 2500, 2800}
+                 : pd.cache_dtype == KVPOOL_FP8_E4M3 ? Cost{3200, 8200, 5000}
+                 : pd.cache_dtype == KVPOOL_BF16     ? Cost{2600, 7500, 4000}
+                                                     : Cost{1950, 4800, 6500};
+  const int rows = !mma ? kFmaRows : tc ? kSharedTcRows : kSharedRows, keys = mma ? kMmaKeys : kFmaKeys;
+  const int runs = shared_splits(pd, n, n_entries, n_sms), per_cta = tc ? 2 : 1;
+  const int64_t ctas = (int64_t)pd.heads * ((n + rows - 1) / rows) * ((runs + per_cta - 1) / per_cta);
+  const int64_t run = (n_entries + runs - 1) / runs;
+  const double tiles = (double)((run + keys - 1) / keys * per_cta) * (double)((ctas + n_sms - 1) / n_sms);
+  return read > tiles * (pd.head_dim == 64 ? c.tile64 : c.tile128) + c.start + kShareRequest * n;
 }
 
 int launch_shared(const AttendParams& p, int n_entries, int n_split, bool pdl, void* stream, int* n_kernels) {

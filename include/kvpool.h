@@ -326,9 +326,9 @@ int kvpool_decode_attend(kvpool_t* pool, int32_t layer, int32_t n, const int32_t
 /* kvpool_decode_attend of requests whose first n_shared tokens are the same
  * sealed blocks ([P3] s2.2; kvpool_share_prefix): the HCA entries of those
  * blocks are read once for the whole batch instead of once per request, as a
- * dense product of all requests' queries per head (where that saves 64 MB of
- * reading or more: below, the call is kvpool_decode_attend; see
- * kvpool_set_share_bytes).  Same arguments, outputs and selected entries as
+ * dense product of all requests' queries per head (where that is the quicker
+ * way by a rule measured for sizes and types; else the call is
+ * kvpool_decode_attend; see kvpool_set_share_bytes).  Same arguments, outputs and selected entries as
  * kvpool_decode_attend; outputs differ from its by the order of the fp32 sums;
  * with bf16 queries and cache, by sums that the tensor core cuts off instead of
  * rounding (under 2^-18 of the outputs' norm, however long the prefix); with an
@@ -343,7 +343,8 @@ int kvpool_decode_attend_shared(kvpool_t* pool, int32_t layer, int32_t n, const 
 
 /* How much reading kvpool_decode_attend_shared has to save to share entries:
  * bytes (0: every shared entry is read once for the batch, however few), or
- * negative for the measured rule, which a new pool has.  Errors: INVALID_ARG. */
+ * negative for the measured rule, which a new pool has.  (A batch too large for
+ * kvpool_decode_attend shares in any case.)  Errors: INVALID_ARG. */
 int kvpool_set_share_bytes(kvpool_t* pool, int64_t bytes);
 
 /* Top-k selection over a caller's score matrix that allocates nothing.  The

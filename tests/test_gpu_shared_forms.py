@@ -36,9 +36,9 @@ def shared(g, layer, slots, wids, top_k, n_shared, more=1):
 
 
 def test_the_rule_decides_what_is_shared():
-    g, _, slots = build(dict(BASE), 9, 128 * 1200, [i for i in range(9)], oracle=False)
-    q, qi = g.queries(0, list(range(9)), 0)
-    out = torch.empty((9, g.HD), device="cuda")
+    g, _, slots = build(dict(BASE), 16, 128 * 1200, [i for i in range(16)], oracle=False)
+    q, qi = g.queries(0, list(range(16)), 0)
+    out = torch.empty((16, g.HD), device="cuda")
     call = lambda n: launches(g.pool, lambda: g.pool.decode_attend_shared(0, slots, n, q, qi, 0, out))  # noqa: E731
     assert (call(128 * 1200), call(128), call(0)) == (2, 1, 1)
     g.pool.set_share_bytes(0)
@@ -301,3 +301,38 @@ def test_growing_scores_in_long_runs():
         want = exact(kv, q)
         # scores of 65 are off by at most 2 * 68 * 2^-24 * 65: 2^-10.9 in the worst weight, far less in their sum
         assert float((out.double() - want).norm() / want.norm()) <= 2.0 ** -13
+
+
+@pytest.mark.parametrize("types,heads,dim,n,entries,pays", [
+    # (steps as shared / each its own: the slower of the two takes 1.2 to 8 times as long)
+    (BF, 16, 128, 64, 1024, True), (BF, 16, 128, 16, 128, False), (BF, 4, 64, 16, 4096, True),
+    ((K.BF16, K.FP8_E4M3), 16, 128, 8, 8192, False), ((K.F32, K.FP8_E4M3), 16, 128, 4, 8192, False),
+    ((K.BF16, K.FP8_E4M3), 16, 128, 32, 2048, False), ((K.BF16, K.FP8_E4M3), 4, 64, 64, 8192, True),
+    ((K.F32, K.BF16), 16, 128, 8, 8192, False), ((K.F32, K.BF16), 16, 64, 64, 8192, True),
+    ((K.F32, K.F32), 16, 128, 2, 4096, False), ((K.F32, K.F32), 16, 128, 64, 2048, True),
+    ((K.BF16, K.F32), 16, 128, 32, 2048, True)])
+def test_the_rule_takes_the_quicker_side(types, heads, dim, n, entries, pays):
+    w = dict(BASE, m=32, in_dtype=types[0], cache_dtype=types[1], heads=heads, head_dim=dim)
+    g = GpuCase(w, n, entries + 4, entries + 2, n, 4)
+    slots = [g.pool.alloc_request() for _ in range(n)]
+    z = torch.zeros((1, 128 * 128, g.HD), dtype=g.tdtype, device="cuda")
+    for _ in range(entries // 128):
+        g.pool.append([slots[0]], [128 * 128], z, z, None)
+    for s in slots[1:]:
+        g.pool.share_prefix(s, slots[0], 128 * entries, z[:, :128].contiguous(), z[:, :128].contiguous())
+    q = torch.zeros((n, g.HD), dtype=g.tdtype, device="cuda")
+    out = torch.empty((n, g.HD), device="cuda")
+    assert launches(g.pool, lambda: g.pool.decode_attend_shared(0, slots, 128 * entries, q, None, 0, out)) == 1 + pays
+
+
+def test_a_batch_too_large_for_the_ordinary_call_shares():
+    n, entries = 256, 16400
+    g, slots, kv, q = filled(dict(BASE, m=32, heads=4, head_dim=64), n, entries)
+    out = torch.empty(q.shape, device="cuda")
+    assert g.pool.decode_attend(0, slots, q, None, 0, out, check=False) == K.ERR_INVALID_ARG
+    want = exact(kv, q)
+    for nbytes in (-1, 1 << 50):
+        g.pool.set_share_bytes(nbytes)
+        out.zero_()
+        g.pool.decode_attend_shared(0, slots, 128 * entries, q, None, 0, out)
+        assert float((out.double() - want).norm() / want.norm()) <= 2.0 ** -18
