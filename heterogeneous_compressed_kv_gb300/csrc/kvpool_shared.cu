@@ -50,7 +50,7 @@ template <int IN, int CACHE, int D>
 __global__ void __launch_bounds__(kFmaThreads) shared_fma_kernel(const __grid_constant__ AttendParams P,
                                                                  const __grid_constant__ SharedShape H) {
   pdl_start();
-  extern __shared__ __align__(16) uint8_t smem_raw[];
+  extern __shared__ __align__(128) uint8_t smem_raw[];
   FmaSmem<D>& sm = *reinterpret_cast<FmaSmem<D>*>(smem_raw);
   __shared__ float scales[2][kFmaKeys];
   const PoolDesc& pd = P.pool;
