@@ -220,6 +220,8 @@ size_t attend_smem_bytes(const PoolDesc& pd);
 int launch_select(const AttendParams& p, void* stream, int* n_kernels, bool alone);
 int launch_attend(const AttendParams& p, int part, int ctas, void* stream, int* n_kernels);
 int launch_combine(const AttendParams& p, void* stream, int* n_kernels);
+// multiprocessors of the current device (0: it cannot be told)
+int device_sms();
 int attend_max_split_len();  // the longest split of a request's sources
 // the first n_entries HCA entries of every request of the launch (the same
 // blocks in all of them), cut into n_split runs: partials in the slots behind

@@ -333,10 +333,12 @@ extern "C" int kvpool_qk_norm_rope(int32_t dtype, int32_t head_dim, int64_t n_to
   P.inv_dim = 1.0f / (float)head_dim;
   // warps per token: one takes all its heads (its angles are worked out once)
   // unless there are too few tokens to fill the GPU
-  constexpr int64_t kFill = 152 * 32;  // warps that keep every SM's loads in flight
+  const int sms = device_sms();
+  if (sms < 1) return KVPOOL_ERR_CUDA;
+  const int64_t fill = 32LL * sms;  // warps that keep every SM's loads in flight
   P.run_steps = kRopeAhead;
-  while (P.run_steps < steps && n_tokens * ((steps + 2 * P.run_steps - 1) / (2 * P.run_steps)) >= kFill) P.run_steps *= 2;
-  while (P.run_steps > 1 && n_tokens * ((steps + P.run_steps - 1) / P.run_steps) < kFill) P.run_steps /= 2;
+  while (P.run_steps < steps && n_tokens * ((steps + 2 * P.run_steps - 1) / (2 * P.run_steps)) >= fill) P.run_steps *= 2;
+  while (P.run_steps > 1 && n_tokens * ((steps + P.run_steps - 1) / P.run_steps) < fill) P.run_steps /= 2;
   P.runs = (steps + P.run_steps - 1) / P.run_steps;
   const int64_t ctas = (n_tokens * P.runs + kRopeWarps - 1) / kRopeWarps;
   if (ctas > 0x7FFFFFFF) return KVPOOL_ERR_INVALID_ARG;

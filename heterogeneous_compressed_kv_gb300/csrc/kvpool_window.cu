@@ -8,6 +8,7 @@
 //   or t < n_sink;  lse = log sum_t exp(scale <q, k_t>);  a query that sees
 //   nothing gives zeros and -inf.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstddef>
 #include <memory>
@@ -23,6 +24,7 @@
 namespace kvp {
 namespace {
 
+constexpr int kMaxDevices = 64;
 __device__ uint32_t g_ops_error;  // device error word of the calls that have no pool
 
 template <int T>
@@ -361,7 +363,6 @@ int64_t slot_bytes(const WinParams& P, int head_dim) { return (int64_t)P.tile_ro
 
 // What a call needs to know of the current device, looked up once for each:
 // its multiprocessors and the address of the error word.
-constexpr int kMaxDevices = 64;
 struct DeviceInfo {
   int sms;
   uint32_t* err;
@@ -375,10 +376,8 @@ const DeviceInfo* device_info() {
   DeviceInfo& d = info[dev];
   if (!d.err) {
     void* p = nullptr;
-    int sms = 0;
-    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1 ||
-        cudaGetSymbolAddress(&p, g_ops_error) != cudaSuccess || !p)
-      return nullptr;
+    const int sms = device_sms();
+    if (sms < 1 || cudaGetSymbolAddress(&p, g_ops_error) != cudaSuccess || !p) return nullptr;
     d.sms = sms;
     d.err = static_cast<uint32_t*>(p);
   }
@@ -400,6 +399,17 @@ cudaError_t launch_merge(const WinParams& P, cudaStream_t s) {
 }
 
 }  // namespace
+
+int device_sms() {
+  static std::atomic<int> known[kMaxDevices];
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+  if ((sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) return 0;
+  known[dev].store(sms, std::memory_order_relaxed);
+  return sms;
+}
+
 }  // namespace kvp
 
 extern "C" int64_t kvpool_window_workspace(const kvpool_window_args* a, int32_t n, const int64_t* h_q_len,
