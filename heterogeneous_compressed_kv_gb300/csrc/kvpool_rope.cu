@@ -31,8 +31,11 @@
 //
 // Measured (bf16, heads of 128): 65,537 tokens x 20 heads 116 us, 5.8 TB/s (0.86
 // of the copy rate; DRAM 68% busy and the issue slots 60%, 64 registers);
-// 8,192 tokens x 32 heads 23.5 us (0.85); 32 tokens x 32 heads 2.5 us, a
-// launch's latency.
+// 8,192 tokens x 32 heads 23.5 us (0.85); 32 tokens x 32 heads 2.7 us, a
+// launch's latency.  Few heads: 4,099 tokens x 8 heads of 64 in fp32 6.3 us for 2.5
+// us of traffic -- a token is two steps, a warp takes one token at most and here
+// one step of it, so that 1 KB is in flight for a position, a table row and a
+// sine read and worked out before it.
 #include <cmath>
 #include <type_traits>
 

@@ -10,10 +10,10 @@
 // sum, output) per request and head in the slots behind the request's other
 // splits; the ordinary merge joins them.
 //
-// Measured as whole steps of 16 heads x 128 in bf16: 8 requests behind 2,400
-// entries 17.7 us (decode_attend 19.6), 32 behind 1,024 18 us (28; the shared
-// entries' kernel by itself 6.9), 64 behind 8,192 (kvpool_shared_tc.cu) 44 us
-// (442).  Where it does not pay (shared_pays) the caller does not come here.
+// Measured as whole steps of 16 heads x 128 in bf16, no tokens of the requests'
+// own (decode_attend in brackets): 32 requests behind 1,024 entries 17.9 us (28.4;
+// the shared entries' kernel by itself 6.9), 64 behind 8,192 (kvpool_shared_tc.cu)
+// 43.7 us (440).  Where it does not pay (shared_pays) the caller does not come here.
 #include <algorithm>
 
 #include <cuda_runtime.h>
@@ -412,9 +412,10 @@ cudaError_t launch_shared_d(const AttendParams& p, const SharedShape& h, cudaStr
 // entries to get going; measured as whole steps of 16 heads x 128 (small
 // products / 5th generation, us):
 //   entries     32 requests    64 requests    128 requests
-//   1,024       18.2 / 21.7    26.9 / 28.6    40.4 / 43.4
-//   4,096       26.0 / 27.5    37.8 / 33.4    64.8 / 48.9
-//   8,192       36.2 / 35.4    52.9 / 41.6    96.7 / 58.4
+//   1,024       17.9 / 23.3    26.2 / 30.3    39.9 / 48.5
+//   2,048       22.1 / 25.5    31.7 / 31.5    50.0 / 48.1
+//   4,096       26.7 / 28.1    39.4 / 35.1    67.6 / 51.0
+//   8,192       36.7 / 35.9    55.7 / 43.7     102 / 59.9
 bool shared_tc(int n, int n_entries) { return n > 32 && n_entries >= 2048; }
 
 // Splits of the shared entries for n requests: CTAs (head, split, block of

@@ -13,10 +13,11 @@
 // (both about 1,024 cycles per 128 x 128 x 128 tile pair and side) overlap.
 //
 // The bf16 weights are the one rounding besides the output's own (2^-9 of a
-// weight, against sums of the unrounded ones): a second piece of them would
-// double the products with V, half of what bounds long windows.  Measured
-// against 64 bits, the outputs are off by 1.2 to 1.4 times what their own
-// rounding leaves (2.0e-3 to 2.3e-3 against 1.66e-3 of their norm).
+// weight, against sums of the unrounded ones).  A second piece of each, and a
+// second product with V, was measured: 32,768 tokens under a window of 4,096
+// 1,075 us against 770, 4 x 2,048 under 128 44.3 against 38.6.  Against 64 bits the
+// outputs are off by 2.0e-3 to 2.3e-3 of their norm, where their own rounding
+// alone leaves 1.5e-3 to 1.7e-3.
 //
 // The outputs are rescaled only when a row's maximum grows by more than 2^8:
 // until then its weights are taken against the older maximum (bf16 keeps its
@@ -27,13 +28,18 @@
 // never count: scores are masked, and such V rows are not copied (boxes of 16
 // and of 1 row up to the last one that holds values, zeros behind it).
 //
-// Bound: the tensor core for long windows -- 32,768 tokens x 16 heads of 128
-// under a window of 4,096 take 757 us, 1,360 TFLOP/s of visible products (0.70
-// of the library product's rate, under the same power limit; partial tiles
-// compute up to 6% more than is visible).  Short windows are bound by their partial
-// tiles and by instruction fetch (2.2 stalled cycles per instruction): 4 x 2,048
-// queries x 16 heads under a window of 128 38 us, of which the tiles' 128-key
-// steps compute 3 keys for 1 that is seen.
+// Bound: the chain scores -> softmax -> outputs -> next scores of a query tile,
+// which one other tile covers.  32,768 tokens x 16 heads of 128 under a window of
+// 4,096 take 770 us, 1,335 TFLOP/s of visible products (0.69 of the library
+// product's rate; partial tiles compute up to 6% more than is visible).  At 8,192
+// tokens the tensor pipe is busy 52% of the time and 56% of an active SM's, the
+// exponentials' 27%, issue slots 33%; warps wait on loads and barriers (3.5 of 7.5
+// cycles per instruction).  The power limit takes 6% (1,940 of 2,070 MHz in a loop
+// of calls, where the library product falls to 1,450).
+// Short windows: 4 x 2,048 queries x 16 heads under a window of 128 38.6 us, of which
+// the tiles' 128-key steps compute 3 keys for 1 that is seen; tensor pipe 16% busy,
+// issue slots 22%, loads and barriers 6.2 of 11.7 cycles per instruction,
+// instruction fetch 1.0.
 // Measured and not kept: K and V tiles of its own for each query tile (38.8 us
 // against 36.6 there), two threads per row (174 against 164 us for 8,192 tokens
 // under 4,096), outputs staged for whole-line stores (slower).

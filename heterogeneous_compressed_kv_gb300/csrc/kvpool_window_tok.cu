@@ -21,9 +21,12 @@
 // fp32: FMAs; four lanes per key, each lane its own running softmax per row.
 //
 // Measured: 64 requests under a window of 4,096 (16 query heads on 4 key heads
-// of 128) 82 us, 6.6 TB/s (0.98 of the copy rate); 32 requests under 128 (16
-// heads) 8.5 - 10.3 us against 5.2 us of reading: launch and one round of
+// of 128) 81 - 82 us, 6.6 TB/s (0.97 of the copy rate); 32 requests under 128 (16
+// heads) 8.5 - 10.4 us against 5.1 us of reading: launch and one round of
 // loads' latency.  Four CTAs to an SM: three took 98 and 14.5 us.
+// fp32: the same 64 requests 229 us for 142 us of reading, with 4 heads of 64 100
+// for 71; 32 under 128 14.7 for 10.2 (16 heads of 128) and 5.2 for 1.3 (4 of 64).
+// Four rows of 128 take 255 registers, which leaves two CTAs to an SM.
 #include <cuda_runtime.h>
 
 #include "kvpool_fma.cuh"

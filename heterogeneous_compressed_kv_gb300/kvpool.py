@@ -353,8 +353,8 @@ def qk_norm_rope(q, k, positions, table, q_weight=None, k_weight=None, eps: floa
     """Norm every head of q and k ([tokens][heads][dim], float32 or bfloat16,
     either may be None) and rotate it by its token's position (int64
     [tokens]) with the table of rope_table (None: norms only); returns (out_q,
-    out_k), which may be given and may be q and k themselves.  See
-    kvpool_qk_norm_rope in include/kvpool.h."""
+    out_k), which may be given and may be q and k themselves.  No gradients
+    flow through.  See kvpool_qk_norm_rope in include/kvpool.h."""
     import torch
     x = q if q is not None else k
     if x is None or not x.is_cuda:
@@ -406,7 +406,9 @@ def window_attend(q, k, v, q_len, k_start, k_len, window: int, n_sink: int = 0, 
                   workspace=None, stream=None):
     """Attention of a ragged batch over raw K/V rows with a sliding window and
     n_sink first tokens that stay visible; returns out ([rows][q heads][dim],
-    like q).  q_len, k_start, k_len: host integers per segment; lse: a float32
+    like q, and q itself if given as out).  bf16 prompts round each softmax
+    weight to bf16 once; fp32 tensors are fp32 throughout.  No gradients flow
+    through.  q_len, k_start, k_len: host integers per segment; lse: a float32
     [rows][q heads] tensor to fill, or None; workspace: a uint8 CUDA tensor of
     window_workspace bytes (one is allocated when None).  See
     kvpool_window_attend in include/kvpool.h."""
@@ -629,7 +631,8 @@ class Pool:
     def decode_attend_shared(self, layer, req_ids, n_shared, q, q_idx, top_k, out, topk_out=None, stream=None,
                              check=True) -> int:
         """decode_attend of requests whose first n_shared tokens are the same
-        blocks, whose HCA entries are read once for all of them."""
+        blocks, whose HCA entries are read once for all of them where that is
+        the quicker way (set_share_bytes)."""
         req = _i32(req_ids)
         rc = self.L.kvpool_decode_attend_shared(self.h, layer, req.size, req.tobytes(), n_shared, _ptr(q), _ptr(q_idx),
                                                 top_k, _ptr(out), _ptr(topk_out), _stream(stream))
