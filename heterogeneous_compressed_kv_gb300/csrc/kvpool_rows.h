@@ -37,22 +37,27 @@ inline bool rows_same(const kvpool_heads& a, const kvpool_heads& b, int64_t toke
 inline bool rows_meet(const kvpool_heads& a, int64_t na, const kvpool_heads& b, int64_t nb, int32_t dim, int64_t vb) {
   if (na <= 0 || nb <= 0 || a.heads <= 0 || b.heads <= 0) return false;
   using Wide = __int128;
+  constexpr int64_t kMost = (int64_t)1 << 60;  // more bytes than any memory: strides that no tensor has
   auto bytes = [&](const kvpool_heads& h, int64_t n) {
-    return (Wide)vb * ((Wide)(n - 1) * h.token_stride + (Wide)(h.heads - 1) * h.head_stride + dim);
+    const Wide x = (Wide)vb * ((Wide)(n - 1) * h.token_stride + (Wide)(h.heads - 1) * h.head_stride + dim);
+    return x < kMost ? (int64_t)x : kMost;
   };
-  const Wide a0 = (Wide) reinterpret_cast<uintptr_t>(a.data), b0 = (Wide) reinterpret_cast<uintptr_t>(b.data);
-  if (a0 + bytes(a, na) <= b0 || b0 + bytes(b, nb) <= a0) return false;
+  const int64_t an = bytes(a, na), bn = bytes(b, nb);
+  if (an == kMost || bn == kMost) return true;
+  const int64_t d0 = (int64_t)(reinterpret_cast<uintptr_t>(b.data) - reinterpret_cast<uintptr_t>(a.data));
+  if (d0 >= an || -d0 >= bn) return false;
   if ((na > 1 && nb > 1 && a.token_stride != b.token_stride) || (a.heads > 1 && b.heads > 1 && a.head_stride != b.head_stride))
     return true;
-  const Wide ts = (Wide)vb * (na > 1 ? a.token_stride : nb > 1 ? b.token_stride : 0);
-  const Wide hs = (Wide)vb * (a.heads > 1 ? a.head_stride : b.heads > 1 ? b.head_stride : 0);
-  const Wide row = (Wide)vb * dim;
+  const int64_t ts = vb * (na > 1 ? a.token_stride : nb > 1 ? b.token_stride : 0);
+  const int64_t hs = vb * (a.heads > 1 ? a.head_stride : b.heads > 1 ? b.head_stride : 0);
+  const int64_t row = vb * dim;
   for (int64_t j = 1 - (int64_t)b.heads; j < a.heads; ++j) {  // heads between the two
-    const Wide r = b0 - a0 - j * hs;                          // i token strides are nearest to r
+    const int64_t r = d0 - j * hs;                            // i token strides are nearest to r
+    const int64_t at = ts > 0 ? r / ts : 0;
     for (int up = 0; up < 2; ++up) {
-      Wide i = ts > 0 ? r / ts + (r < 0 ? -up : up) : 0;
+      int64_t i = at + (r < 0 ? -up : up);
       i = i > na - 1 ? na - 1 : i < 1 - nb ? 1 - nb : i;
-      const Wide d = r - i * ts;
+      const int64_t d = r - i * ts;
       if (d < row && -d < row) return true;
     }
   }

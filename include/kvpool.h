@@ -422,7 +422,8 @@ int kvpool_rope_table(int32_t rot_dim, const double* h_inv_freq, uint64_t* h_tab
  * positions needed).  q or k may be NULL or have no heads.  An output may be
  * its own input (same data and strides); otherwise it lies apart from q, k and
  * the other output (between their rows in memory only with their strides).
- * Weights: [head_dim] fp32, 16-byte aligned, or NULL (ones).  d_positions: [n_tokens], of any sign
+ * Weights: [head_dim] fp32, 16-byte aligned, or NULL (ones); they, the table
+ * and the positions lie apart from the outputs.  d_positions: [n_tokens], of any sign
  * and size; the angle of position p, |p * inv_freq[i]| = 2 pi N, is off by
  * 2^-25 + 2^-52 N + 2^-64 |p| turns at most (2^-24 at N = 2^27).  Errors: INVALID_ARG, CUDA. */
 int kvpool_qk_norm_rope(int32_t dtype, int32_t head_dim, int64_t n_tokens, const kvpool_heads* q,
@@ -455,7 +456,8 @@ int kvpool_qk_norm_rope(int32_t dtype, int32_t head_dim, int64_t n_tokens, const
  * (2^-9 of each weight) in longer ones.  Callers that need a prompt's weights
  * unrounded pass fp32 tensors.  head_dim 64 or 128; window and n_sink >= 0.
  * d_workspace: kvpool_window_workspace bytes (16-byte aligned, may be NULL
- * when that is 0); calls that overlap on the GPU need one each.  The lengths
+ * when that is 0); calls that overlap on the GPU need one each.  It and d_lse
+ * lie apart from everything else.  The lengths
  * are read during the call: a captured call replays with the same ones.
  * Errors: INVALID_ARG, CUDA. */
 typedef struct kvpool_window_args {
