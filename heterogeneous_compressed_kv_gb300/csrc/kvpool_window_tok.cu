@@ -17,7 +17,8 @@
 // (128 rows) would do the same with 8 to 128 times the padding.
 // A weight goes into the product as two bf16 numbers whose sum holds 16 of its
 // bits (off by 2^-18 of it at most): one alone would be off by 2^-9, as much as
-// the output's own rounding.  The second product is hidden behind the loads.
+// the output's own rounding.  The second product takes 0 to 4% of the time
+// (most with 16 rows to a key head).
 // fp32: FMAs; four lanes per key, each lane its own running softmax per row.
 //
 // Measured: 64 requests under a window of 4,096 (16 query heads on 4 key heads
