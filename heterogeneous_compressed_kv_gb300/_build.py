@@ -40,8 +40,9 @@ LIBS = {
         "sources": ["csrc/kvpool_host.cpp", "csrc/kvpool_append.cu", "csrc/kvpool_score.cu", "csrc/kvpool_select.cu",
                     "csrc/kvpool_attend.cu", "csrc/kvpool_image.cu", "csrc/kvpool_rope.cu", "csrc/kvpool_window.cu",
                     "csrc/kvpool_shared.cu", "csrc/kvpool_window_tc.cu",
-                    "csrc/kvpool_window_tok.cu", "csrc/kvpool_shared_tc.cu"],
-        "headers": ["csrc/kvpool_internal.h", "csrc/kvpool_rows.h", "csrc/kvpool_window.h", "csrc/kvpool_fma.cuh", "csrc/kvpool_mma.cuh", "csrc/kvpool_shared.h", "csrc/kvpool_pair.cuh", "csrc/kvpool_tcgen05.cuh", "csrc/device_util.cuh", "../include/kvpool.h"],
+                    "csrc/kvpool_window_tok.cu", "csrc/kvpool_shared_tc.cu", "csrc/kvpool_kv4.cu",
+                    "csrc/kvpool_kv4_attend.cu", "csrc/kvpool_kv4_evict.cu"],
+        "headers": ["csrc/kvpool_internal.h", "csrc/kvpool_rows.h", "csrc/kvpool_window.h", "csrc/kvpool_kv4.h", "csrc/kvpool_fma.cuh", "csrc/kvpool_mma.cuh", "csrc/kvpool_shared.h", "csrc/kvpool_pair.cuh", "csrc/kvpool_tcgen05.cuh", "csrc/device_util.cuh", "../include/kvpool.h"],
     },
     "kvgen": {
         "out": os.path.join(PKG, "gen", "libkvgen.so"),

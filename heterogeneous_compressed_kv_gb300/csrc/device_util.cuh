@@ -209,6 +209,25 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const 
   }
 }
 
+// The same for kernels that have no pool:
+__device__ __forceinline__ bool mbar_wait_word(uint64_t* bar, uint32_t parity, uint32_t* err) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+  while (true) {
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (global_ns() - t0 > kWaitLimitNs) {
+      atomicOr(err, (uint32_t)kErrWaitTimeout);
+      return false;
+    }
+  }
+}
+
+// The whole warp waits; every lane gets the same answer.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t* err) {
+  return __all_sync(0xffffffffu, mbar_wait_word(bar, parity, err));
+}
+
 // L2 policy for data read once (a stream through the cache): its lines are
 // the first evicted, so it does not push out what later kernels read again
 __device__ __forceinline__ uint64_t l2_evict_first_policy() {

@@ -222,6 +222,13 @@ int launch_attend(const AttendParams& p, int part, int ctas, void* stream, int* 
 int launch_combine(const AttendParams& p, void* stream, int* n_kernels);
 // multiprocessors of the current device (0: it cannot be told)
 int device_sms();
+// What a call without a pool needs to know of the current device, looked up
+// once for each (null: it cannot be told).
+struct OpsDevice {
+  int sms;
+  uint32_t* err;  // the device error word of such calls
+};
+const OpsDevice* ops_device();
 int attend_max_split_len();  // the longest split of a request's sources
 // the first n_entries HCA entries of every request of the launch (the same
 // blocks in all of them), cut into n_split runs: partials in the slots behind

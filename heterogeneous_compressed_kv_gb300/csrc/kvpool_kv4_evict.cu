@@ -1,0 +1,381 @@
+// kvpool_kv4_evict.cu -- the heaviest tokens of a 4-bit paged cache into other
+// pages: of a segment's tokens every key head keeps the first n_sink, the last
+// n_recent and of the others the ones of largest weight (ties to the lowest
+// place), in their order.
+//
+// Two kernels.  The first finds what stays: a cluster of CTAs takes the weights of
+// one segment and key head, a slice each; four passes over 8 bits of an order-
+// keeping integer of the weight narrow the last weight that stays (histograms in
+// shared memory, added up over the cluster), a count by warp slices gives every
+// slice its first place, and the places go out in order.  The second moves the
+// tokens, a warp to a tile of 16 of them.
+#include <algorithm>
+#include <memory>
+#include <new>
+
+#include <cooperative_groups.h>
+#include <cuda_runtime.h>
+
+#include "kvpool_kv4.h"
+#include "kvpool_rows.h"
+
+namespace kvp {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
+constexpr int kMaxCluster = 8;
+constexpr int kMoveWarps = 4;
+
+struct EvictSeg {
+  int32_t k_len;
+  int32_t task_base;  // first task of the moving kernel: tile * kv_heads + head
+  int32_t table_row;  // of the first launch's tables, weights and outputs
+};
+
+struct EvictParams {
+  Kv4Cache c;  // table: the tokens' places
+  const int32_t* out_table;
+  int64_t out_stride;
+  const float* w;
+  float* out_w;   // or null
+  int32_t* index; // [segments][kv_heads][keep]
+  int64_t w_seg, w_head, ow_seg, ow_head;
+  int32_t keep, sink, recent, ow_width;
+  int32_t cluster;
+  int32_t n_segs, n_tasks;
+  EvictSeg segs[kKv4MaxSegs];
+};
+
+// A larger weight has a larger key; -0 and +0 are alike and a NaN is the largest.
+__device__ __forceinline__ uint32_t weight_key(float w) { return w != w ? 0xFFFFFFFFu : score_key(w); }
+
+__global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const __grid_constant__ EvictParams P) {
+  pdl_start();
+  __shared__ uint32_t hist[4][256];
+  __shared__ uint2 counts[kSelWarps];  // (above the last weight that stays, equal to it) of a warp's slice
+  __shared__ uint32_t sh_digit, sh_left;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int C = P.cluster, rank = blockIdx.x % C, id = blockIdx.x / C;
+  const int head = id % P.c.kv_heads;
+  const EvictSeg& S = P.segs[id / P.c.kv_heads];
+  const int n = S.k_len, keep = P.keep;
+  const float* w = P.w + S.table_row * P.w_seg + head * P.w_head;
+  float* ow = P.out_w ? P.out_w + S.table_row * P.ow_seg + head * P.ow_head : nullptr;
+  int32_t* index = P.index + ((int64_t)S.table_row * P.c.kv_heads + head) * keep;
+  const int all = C * kSelThreads, at = rank * kSelThreads + tid;
+  // behind what stays: no token, no weight
+  const int kept = min(n, keep);
+  for (int i = kept + at; i < keep; i += all) index[i] = -1;
+  if (ow)
+    for (int i = kept + at; i < P.ow_width; i += all) ow[i] = 0.0f;
+  if (n <= keep) {
+    for (int i = at; i < n; i += all) {
+      index[i] = i;
+      if (ow) ow[i] = w[i];
+    }
+    return;  // (the whole cluster)
+  }
+  // the first and the last tokens stay
+  for (int i = at; i < P.sink + P.recent; i += all) {
+    const int t = i < P.sink ? i : n - P.recent + (i - P.sink), to = i < P.sink ? i : keep - P.recent + (i - P.sink);
+    index[to] = t;
+    if (ow) ow[to] = w[t];
+  }
+  const int lo = P.sink, hi = n - P.recent, want = keep - P.sink - P.recent;  // want < hi - lo
+  if (want == 0) return;
+  const int warps = C * kSelWarps, per = ((hi - lo + warps - 1) / warps + 31) & ~31;  // a warp's slice
+  const int a = min(hi, lo + (rank * kSelWarps + warp) * per), b = min(hi, a + per);
+  for (int i = tid; i < 4 * 256; i += kSelThreads) (&hist[0][0])[i] = 0;
+  __syncthreads();
+  uint32_t prefix = 0, left = want;
+#pragma unroll 1
+  for (int pass = 0; pass < 4; ++pass) {
+    const int shift = 24 - 8 * pass;
+#pragma unroll 4
+    for (int i = a + lane; i < b; i += 32) {
+      const uint32_t key = weight_key(w[i]);
+      if (pass == 0 || key >> (shift + 8) == prefix) atomicAdd(&hist[pass][key >> shift & 255], 1u);
+    }
+    cluster.sync();
+    // counts from the largest digit down: thread i holds digit 255 - i
+    if (tid < 256) {
+      uint32_t x = 0;
+      for (int r = 0; r < C; ++r) x += cluster.map_shared_rank(&hist[pass][0], r)[255 - tid];
+      uint32_t up = x;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, up, off);
+        if (lane >= off) up += y;
+      }
+      if (lane == 31) counts[warp].x = up;
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      for (int k = 0; k < warp; ++k) up += counts[k].x;
+      if (up >= left && up - x < left) {  // one thread
+        sh_digit = 255 - tid;
+        sh_left = left - (up - x);
+      }
+    }
+    __syncthreads();
+    prefix = prefix << 8 | sh_digit;
+    left = sh_left;
+    __syncthreads();
+  }
+  // `prefix` is the key of the last weight that stays, `left` how many of those equal to it do
+  uint2 mine = make_uint2(0, 0);
+  for (int i = a + lane; i < b; i += 32) {
+    const uint32_t key = weight_key(w[i]);
+    mine.x += key > prefix;
+    mine.y += key == prefix;
+  }
+  mine.x = __reduce_add_sync(0xffffffffu, mine.x);
+  mine.y = __reduce_add_sync(0xffffffffu, mine.y);
+  if (lane == 0) counts[warp] = mine;
+  cluster.sync();
+  uint32_t above = 0, equal = 0;  // before this warp's slice
+  for (int i = lane; i < rank * kSelWarps + warp; i += 32) {
+    const uint2 x = cluster.map_shared_rank(&counts[0], i / kSelWarps)[i % kSelWarps];
+    above += x.x;
+    equal += x.y;
+  }
+  above = __reduce_add_sync(0xffffffffu, above);
+  equal = __reduce_add_sync(0xffffffffu, equal);
+  for (int i0 = a; i0 < b; i0 += 32) {
+    const int i = i0 + lane;
+    const float x = i < b ? w[i] : 0.0f;
+    const uint32_t key = weight_key(x);
+    const uint32_t gt = __ballot_sync(0xffffffffu, i < b && key > prefix), eq = __ballot_sync(0xffffffffu, i < b && key == prefix);
+    const uint32_t below = (1u << lane) - 1;
+    const uint32_t e = equal + __popc(eq & below);
+    if ((gt >> lane & 1) || ((eq >> lane & 1) && e < left)) {
+      const int to = P.sink + above + __popc(gt & below) + min(e, left);
+      index[to] = i;
+      if (ow) ow[to] = x;
+    }
+    above += __popc(gt);
+    equal += __popc(eq);
+  }
+  cluster.sync();  // no CTA ends while another one reads its counts
+}
+
+// A warp moves a tile of 16 tokens of one head.
+template <int D>
+__global__ void __launch_bounds__(kMoveWarps * 32) kv4_move_kernel(const __grid_constant__ EvictParams P) {
+  pdl_start();
+  using L = Kv4Tile<D>;
+  const int task = blockIdx.x * kMoveWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (task >= P.n_tasks) return;
+  int lo = 0, hi = P.n_segs - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (P.segs[mid].task_base <= task) lo = mid;
+    else hi = mid - 1;
+  }
+  const EvictSeg& S = P.segs[lo];
+  const int head = (task - S.task_base) % P.c.kv_heads, tile = (task - S.task_base) / P.c.kv_heads;
+  const int n = min(kKv4Tile, min(S.k_len, P.keep) - tile * kKv4Tile);
+  Kv4Cache to = P.c;
+  to.table = P.out_table;
+  to.table_stride = P.out_stride;
+  const int to_id = kv4_page(to, S.table_row, tile);
+  if (to_id < 0) return;
+  uint8_t* dst = P.c.pages + kv4_tile_offset<D>(P.c, to_id, head, tile);
+  // lane r (of 16): the place of token r of the tile; a bad page id reads as zeros
+  int64_t off = -1;
+  int slot = 0;
+  if (lane < n) {
+    const int t = P.index[((int64_t)S.table_row * P.c.kv_heads + head) * P.keep + tile * kKv4Tile + lane];
+    slot = t % kKv4Tile;
+    const int id = kv4_page(P.c, S.table_row, t / kKv4Tile);
+    if (id >= 0) off = kv4_tile_offset<D>(P.c, id, head, t / kKv4Tile);
+  }
+  auto off_of = [&](int r) { return __shfl_sync(0xffffffffu, off, r); };
+  auto slot_of = [&](int r) { return __shfl_sync(0xffffffffu, slot, r); };
+  const uint8_t* pages = P.c.pages;
+  // all loads first (nothing that is written is read)
+  constexpr int KI = D / 64;  // 16-byte pieces of keys to a lane
+  uint4 k[KI];
+#pragma unroll
+  for (int i = 0; i < KI; ++i) {
+    const int x = i * 32 + lane, r = x / (D / 32), c = x % (D / 32);
+    const int64_t o = off_of(r);
+    const int sl = slot_of(r);
+    k[i] = o >= 0 ? *reinterpret_cast<const uint4*>(pages + o + sl * (D / 2) + 16 * c) : make_uint4(0, 0, 0, 0);
+  }
+  constexpr int G = D / kKv4Group, SI = kKv4Tile * G / 32;  // scales to a lane
+  uint8_t ks[SI], vs[SI];
+#pragma unroll
+  for (int i = 0; i < SI; ++i) {
+    const int x = i * 32 + lane, r = x / G, e = x % G;
+    const int64_t o = off_of(r);
+    const int sl = slot_of(r);
+    ks[i] = o >= 0 ? pages[o + L::kKs + sl * G + e] : 0;
+    vs[i] = o >= 0 ? pages[o + L::kVs + (sl >> 1) * 2 * G + 2 * e + (sl & 1)] : 0;
+  }
+  constexpr int VW = D / 64;  // 8-byte words of a V chunk
+  uint2 v[2][VW];             // pairs lane / 8 and + 4, chunk lane % 8
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int j = lane / 8 + 4 * i, c = lane % 8;
+#pragma unroll
+    for (int y = 0; y < VW; ++y) v[i][y] = make_uint2(0, 0);
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      const int64_t o = off_of(2 * j + y);
+      const int sl = slot_of(2 * j + y), p = sl >> 1;
+      if (o < 0) continue;
+      const uint8_t* src = pages + o + L::kV + p * D + (c ^ kv4_swizzle<D>(p)) * L::kChunk;
+#pragma unroll
+      for (int z = 0; z < VW; ++z) {
+        const uint2 x = *reinterpret_cast<const uint2*>(src + 8 * z);
+        v[i][z].x |= (x.x >> 4 * (sl & 1) & 0x0F0F0F0Fu) << 4 * y;
+        v[i][z].y |= (x.y >> 4 * (sl & 1) & 0x0F0F0F0Fu) << 4 * y;
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < KI; ++i) {
+    const int x = i * 32 + lane, r = x / (D / 32), c = x % (D / 32);
+    if (r < n) *reinterpret_cast<uint4*>(dst + r * (D / 2) + 16 * c) = k[i];
+  }
+#pragma unroll
+  for (int i = 0; i < SI; ++i) {
+    const int x = i * 32 + lane, r = x / G, e = x % G;
+    if (r >= n) continue;
+    dst[L::kKs + r * G + e] = ks[i];
+    dst[L::kVs + (r >> 1) * 2 * G + 2 * e + (r & 1)] = vs[i];
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int j = lane / 8 + 4 * i, c = lane % 8;
+    if (2 * j >= n) continue;
+    uint2* p = reinterpret_cast<uint2*>(dst + L::kV + j * D + (c ^ kv4_swizzle<D>(j)) * L::kChunk);
+#pragma unroll
+    for (int z = 0; z < VW; ++z) {
+      uint2 x = v[i][z];
+      if (2 * j + 1 >= n) {  // the place of the pair's second token stays
+        const uint2 old = p[z];
+        x = make_uint2((x.x & 0x0F0F0F0Fu) | (old.x & 0xF0F0F0F0u), (x.y & 0x0F0F0F0Fu) | (old.y & 0xF0F0F0F0u));
+      }
+      p[z] = x;
+    }
+  }
+}
+
+int check_args(const kvpool_kv4_evict_args* a, int32_t n, const int64_t* k_len, int64_t* most) {
+  if (!a || n < 0) return KVPOOL_ERR_INVALID_ARG;
+  const int rc = kv4_check(&a->cache, n);
+  if (rc != KVPOOL_OK) return rc;
+  const kvpool_kv4& c = a->cache;
+  if (a->keep < 1 || a->keep > (1 << 30) || a->n_sink < 0 || a->n_recent < 0 || a->n_sink > a->keep ||
+      a->n_recent > a->keep - a->n_sink)
+    return KVPOOL_ERR_INVALID_ARG;
+  if (n > 0 && !k_len) return KVPOOL_ERR_INVALID_ARG;
+  int64_t len = 0;
+  for (int32_t i = 0; i < n; ++i) {
+    if (k_len[i] < 0 || k_len[i] > kv4_tokens(&c)) return KVPOOL_ERR_INVALID_ARG;
+    len = std::max(len, k_len[i]);
+  }
+  *most = len;
+  if (n == 0) return KVPOOL_OK;
+  if (!a->d_index || reinterpret_cast<uintptr_t>(a->d_index) % 4 != 0) return KVPOOL_ERR_INVALID_ARG;
+  if (a->out_table_rows < n || a->out_table_stride < 0 || reinterpret_cast<uintptr_t>(a->d_out_table) % 4 != 0 ||
+      a->out_table_width < 0 || (int64_t)a->out_table_width * c.page_tokens < std::min<int64_t>(len, a->keep))
+    return KVPOOL_ERR_INVALID_ARG;
+  if (len > 0 && (!c.d_pages || !c.d_table || c.n_pages < 1 || !a->d_out_table || !a->d_weights)) return KVPOOL_ERR_INVALID_ARG;
+  auto strides = [&](const float* p, int64_t seg, int64_t head, int64_t width, bool out) {
+    if (reinterpret_cast<uintptr_t>(p) % 4 != 0 || seg < 0 || head < 0 || seg > (1ll << 40) || head > (1ll << 40)) return false;
+    if (!out) return true;
+    return (c.kv_heads == 1 || head >= width) && (n == 1 || seg >= (c.kv_heads - 1) * head + width);
+  };
+  if (!strides(a->d_weights, a->weight_stride, a->weight_head_stride, len, false)) return KVPOOL_ERR_INVALID_ARG;
+  if (a->d_out_weights) {
+    if (a->out_weight_width < a->keep ||
+        !strides(a->d_out_weights, a->out_weight_stride, a->out_weight_head_stride, a->out_weight_width, true))
+      return KVPOOL_ERR_INVALID_ARG;
+    auto end = [&](const float* p, int64_t seg, int64_t head, int64_t width) {
+      return reinterpret_cast<uintptr_t>(p + (n - 1) * seg + (c.kv_heads - 1) * head + width);
+    };
+    if (len > 0 && reinterpret_cast<uintptr_t>(a->d_weights) < end(a->d_out_weights, a->out_weight_stride, a->out_weight_head_stride, a->out_weight_width) &&
+        reinterpret_cast<uintptr_t>(a->d_out_weights) < end(a->d_weights, a->weight_stride, a->weight_head_stride, len))
+      return KVPOOL_ERR_INVALID_ARG;
+  }
+  return KVPOOL_OK;
+}
+
+cudaError_t launch_select(const EvictParams& P, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(P.n_segs * P.c.kv_heads * P.cluster);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = P.cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kv4_select_kernel, P);
+}
+
+}  // namespace
+}  // namespace kvp
+
+extern "C" int kvpool_kv4_evict(const kvpool_kv4_evict_args* a, int32_t n, const int64_t* h_k_len, void* stream) {
+  using namespace kvp;
+  int64_t most = 0;
+  const int rc = check_args(a, n, h_k_len, &most);
+  if (rc != KVPOOL_OK || n == 0) return rc;
+  const OpsDevice* dev = ops_device();
+  if (!dev) return KVPOOL_ERR_CUDA;
+  std::unique_ptr<EvictParams> P(new (std::nothrow) EvictParams);
+  if (!P) return KVPOOL_ERR_INVALID_ARG;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int hk = a->cache.kv_heads;
+  P->w_seg = a->weight_stride;
+  P->w_head = a->weight_head_stride;
+  P->ow_seg = a->out_weight_stride;
+  P->ow_head = a->out_weight_head_stride;
+  P->out_stride = a->out_table_stride;
+  P->keep = a->keep;
+  P->sink = a->n_sink;
+  P->recent = a->n_recent;
+  P->ow_width = a->out_weight_width;
+  // CTAs to a segment and head: as many as fill the GPU together, of 2,048 weights at least
+  P->cluster = 1;
+  while (P->cluster < kMaxCluster && (int64_t)std::min(n, kKv4MaxSegs) * hk * P->cluster * 2 <= 2 * dev->sms &&
+         most >= 4096 * P->cluster)
+    P->cluster *= 2;
+  for (int32_t i = 0; i < n;) {
+    const int32_t first = i;
+    P->n_segs = 0;
+    int64_t tasks = 0;
+    for (; i < n && P->n_segs < kKv4MaxSegs; ++i) {
+      const int64_t tiles = (std::min<int64_t>(h_k_len[i], a->keep) + kKv4Tile - 1) / kKv4Tile;
+      if (tiles * hk > (1 << 30)) return KVPOOL_ERR_INVALID_ARG;
+      if (tasks > 0 && tasks + tiles * hk > (1 << 30)) break;
+      EvictSeg& S = P->segs[P->n_segs++];
+      S.k_len = (int32_t)h_k_len[i];
+      S.task_base = (int32_t)tasks;
+      S.table_row = i - first;
+      tasks += tiles * hk;
+    }
+    P->n_tasks = (int32_t)tasks;
+    P->c = kv4_cache(&a->cache, first, dev->err);
+    P->out_table = a->d_out_table + first * a->out_table_stride;
+    P->w = a->d_weights + first * a->weight_stride;
+    P->out_w = a->d_out_weights ? a->d_out_weights + first * a->out_weight_stride : nullptr;
+    P->index = a->d_index + (int64_t)first * hk * a->keep;
+    cudaError_t e = launch_select(*P, s);
+    if (e == cudaSuccess && P->n_tasks > 0) {
+      const dim3 grid((unsigned)((P->n_tasks + kMoveWarps - 1) / kMoveWarps)), block(kMoveWarps * 32);
+      e = a->cache.head_dim == 128 ? launch_kernel(true, kv4_move_kernel<128>, grid, block, 0, s, *P)
+                                   : launch_kernel(true, kv4_move_kernel<64>, grid, block, 0, s, *P);
+    }
+    if (e != cudaSuccess) return KVPOOL_ERR_CUDA;
+  }
+  return KVPOOL_OK;
+}

@@ -5,7 +5,9 @@
 // For one head x of a token at position p:
 //   y = x / sqrt(mean(x^2) + eps) * w
 //   (y_a, y_b) -> (y_a cos t - y_b sin t, y_b cos t + y_a sin t)
-// over the pairs (a, b) of the first rot_dim dims, t = p * freq_i.
+// over the pairs (a, b) of the first rot_dim dims, t = p * freq_i.  With several
+// axes (time, height, width of a token of an image or a video) a token has a
+// position on each and pair i turns by the one on axis[i].
 //
 // The table holds freq_i / (2 pi) modulo 1 as a 64-bit fraction of a turn, so p
 // * table[i] modulo 2^64 is the angle's place in its turn: the integer product
@@ -52,6 +54,7 @@ namespace {
 constexpr int kRopeWarps = 4;    // warps per CTA
 constexpr int kRopeAhead = 4;    // steps (heads per lane group) in flight
 constexpr int kRopeMaxDim = 256;
+constexpr int kRopeMaxAxes = 8;
 
 struct RopeTensor {
   const uint8_t* in;
@@ -69,6 +72,8 @@ struct RopeParams {
   int32_t rot_dim, lanes;   // lanes with values per head
   int32_t runs, run_steps;  // runs: warps per token, steps of each
   float eps, inv_dim;
+  int32_t n_axes;                    // positions of a token
+  uint8_t axis[kRopeMaxDim / 2];     // the axis of each pair (n_axes > 1)
 };
 
 // 8 values as loaded: W words, V = 8 / W of them to a word
@@ -160,8 +165,10 @@ __global__ void __launch_bounds__(kRopeWarps * 32, T == KVPOOL_BF16 ? 8 : 5) rop
 
   const int half = P.rot_dim / 2;
   if (half > 0) {
-    const uint64_t p = (uint64_t)P.pos[tok];
+    const int64_t* pos = P.pos + tok * P.n_axes;
+    const uint64_t p0 = (uint64_t)pos[0];
     for (int i = lane; i < half; i += 32) {
+      const uint64_t p = P.n_axes > 1 ? (uint64_t)pos[P.axis[i]] : p0;
       const int32_t t = (int32_t)((p * P.table[i]) >> 32);
       float s, c;
       sincospif((float)t * 0x1p-31f, &s, &c);
@@ -283,12 +290,24 @@ extern "C" int kvpool_qk_norm_rope(int32_t dtype, int32_t head_dim, int64_t n_to
                                    const float* d_q_weight, const float* d_k_weight, float eps, int32_t rot_dim,
                                    int32_t interleaved, const uint64_t* d_table, const int64_t* d_positions,
                                    void* stream) {
+  return kvpool_qk_norm_rope_axes(dtype, head_dim, n_tokens, q, k, q_out, k_out, d_q_weight, d_k_weight, eps, rot_dim,
+                                  interleaved, d_table, d_positions, 1, nullptr, stream);
+}
+
+extern "C" int kvpool_qk_norm_rope_axes(int32_t dtype, int32_t head_dim, int64_t n_tokens, const kvpool_heads* q,
+                                        const kvpool_heads* k, const kvpool_heads* q_out, const kvpool_heads* k_out,
+                                        const float* d_q_weight, const float* d_k_weight, float eps, int32_t rot_dim,
+                                        int32_t interleaved, const uint64_t* d_table, const int64_t* d_positions,
+                                        int32_t n_axes, const uint8_t* h_axes, void* stream) {
   using namespace kvp;
   if (dtype != KVPOOL_F32 && dtype != KVPOOL_BF16) return KVPOOL_ERR_INVALID_ARG;
   if (head_dim < 8 || head_dim > kRopeMaxDim || head_dim % 8 != 0) return KVPOOL_ERR_INVALID_ARG;
   if (rot_dim < 0 || rot_dim > head_dim || rot_dim % 16 != 0 || (interleaved != 0 && interleaved != 1))
     return KVPOOL_ERR_INVALID_ARG;
   if (n_tokens < 0 || !(eps >= 0.0f) || !std::isfinite(eps)) return KVPOOL_ERR_INVALID_ARG;
+  if (n_axes < 1 || n_axes > kRopeMaxAxes || (n_axes > 1 && rot_dim > 0 && !h_axes)) return KVPOOL_ERR_INVALID_ARG;
+  for (int i = 0; h_axes && i < rot_dim / 2; ++i)
+    if (h_axes[i] >= n_axes) return KVPOOL_ERR_INVALID_ARG;
   const kvpool_heads* in[2] = {q, k};
   const kvpool_heads* out[2] = {q_out, k_out};
   const float* wt[2] = {d_q_weight, d_k_weight};
@@ -333,6 +352,8 @@ extern "C" int kvpool_qk_norm_rope(int32_t dtype, int32_t head_dim, int64_t n_to
   P.rot_dim = rot_dim;
   P.lanes = head_dim / 8;
   P.eps = eps;
+  P.n_axes = n_axes;
+  for (int i = 0; n_axes > 1 && i < rot_dim / 2; ++i) P.axis[i] = h_axes[i];
   P.inv_dim = 1.0f / (float)head_dim;
   // warps per token: one takes all its heads (its angles are worked out once)
   // unless there are too few tokens to fill the GPU

@@ -1,32 +1,11 @@
 // kvpool_tcgen05.cuh -- the 5th-generation tensor core's instructions (matrix
-// products into tensor memory), tensor copies, and waits of kernels that have
-// no pool.
+// products into tensor memory) and tensor copies.
 #pragma once
 
 #include "device_util.cuh"
 #include "kvpool_pair.cuh"
 
 namespace kvp {
-
-// Wait for the phase with the given parity; false, and the flag set in *err,
-// if it has not completed within kWaitLimitNs.
-__device__ __forceinline__ bool mbar_wait_word(uint64_t* bar, uint32_t parity, uint32_t* err) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = global_ns();
-  while (true) {
-    for (int i = 0; i < 64; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
-    if (global_ns() - t0 > kWaitLimitNs) {
-      atomicOr(err, (uint32_t)kErrWaitTimeout);
-      return false;
-    }
-  }
-}
-
-// The whole warp waits; every lane gets the same answer.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t* err) {
-  return __all_sync(0xffffffffu, mbar_wait_word(bar, parity, err));
-}
 
 // One lane of the whole warp, the same one every time.  The compiler knows that
 // what it guards runs in a single thread, so the products' descriptors go

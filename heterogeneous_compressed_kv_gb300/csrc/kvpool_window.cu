@@ -361,29 +361,6 @@ void fill_params(const kvpool_window_args* a, WinParams* P) {
 
 int64_t slot_bytes(const WinParams& P, int head_dim) { return (int64_t)P.tile_rows * (head_dim + 2) * 4; }
 
-// What a call needs to know of the current device, looked up once for each:
-// its multiprocessors and the address of the error word.
-struct DeviceInfo {
-  int sms;
-  uint32_t* err;
-};
-const DeviceInfo* device_info() {
-  static std::mutex mu;
-  static DeviceInfo info[kMaxDevices];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
-  std::lock_guard<std::mutex> lock(mu);
-  DeviceInfo& d = info[dev];
-  if (!d.err) {
-    void* p = nullptr;
-    const int sms = device_sms();
-    if (sms < 1 || cudaGetSymbolAddress(&p, g_ops_error) != cudaSuccess || !p) return nullptr;
-    d.sms = sms;
-    d.err = static_cast<uint32_t*>(p);
-  }
-  return &d;
-}
-
 template <int T, int D>
 cudaError_t launch_fma(const WinParams& P, cudaStream_t s) {
   constexpr int smem = (int)sizeof(FmaSmem<D>);
@@ -410,6 +387,23 @@ int device_sms() {
   return sms;
 }
 
+const OpsDevice* ops_device() {
+  static std::mutex mu;
+  static OpsDevice info[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
+  std::lock_guard<std::mutex> lock(mu);
+  OpsDevice& d = info[dev];
+  if (!d.err) {
+    void* p = nullptr;
+    const int sms = device_sms();
+    if (sms < 1 || cudaGetSymbolAddress(&p, g_ops_error) != cudaSuccess || !p) return nullptr;
+    d.sms = sms;
+    d.err = static_cast<uint32_t*>(p);
+  }
+  return &d;
+}
+
 }  // namespace kvp
 
 extern "C" int64_t kvpool_window_workspace(const kvpool_window_args* a, int32_t n, const int64_t* h_q_len,
@@ -419,7 +413,7 @@ extern "C" int64_t kvpool_window_workspace(const kvpool_window_args* a, int32_t 
   const int rc = check_args(a, n, h_q_len, h_k_start, h_k_len, &total);
   if (rc != KVPOOL_OK) return rc;
   if (total == 0) return 0;
-  const DeviceInfo* dev = device_info();
+  const OpsDevice* dev = ops_device();
   if (!dev) return KVPOOL_ERR_CUDA;
   const int sms = dev->sms;
   std::unique_ptr<WinParams> P(new (std::nothrow) WinParams);
@@ -449,7 +443,7 @@ extern "C" int kvpool_window_attend(const kvpool_window_args* a, int32_t n, cons
   if (need < 0) return (int)need;
   if (need > 0 && (!d_workspace || workspace_bytes < need || reinterpret_cast<uintptr_t>(d_workspace) % 16 != 0))
     return KVPOOL_ERR_INVALID_ARG;
-  const DeviceInfo* dev = device_info();
+  const OpsDevice* dev = ops_device();
   if (!dev) return KVPOOL_ERR_CUDA;
   const int sms = dev->sms;
   std::unique_ptr<WinParams> P(new (std::nothrow) WinParams);
@@ -485,7 +479,7 @@ extern "C" int kvpool_window_attend(const kvpool_window_args* a, int32_t n, cons
 extern "C" int kvpool_window_check(void* stream, uint32_t* h_flags) {
   using namespace kvp;
   uint32_t word = 0;
-  const DeviceInfo* dev = device_info();
+  const OpsDevice* dev = ops_device();
   if (!dev) return KVPOOL_ERR_CUDA;
   uint32_t* err = dev->err;
   const uint32_t zero = 0;

@@ -35,7 +35,9 @@ EXPORTS = ["kvpool_required_bytes", "kvpool_create", "kvpool_destroy", "kvpool_a
            "kvpool_offload", "kvpool_fetch", "kvpool_block_location", "kvpool_epoch", "kvpool_block_activity",
            "kvpool_inactive_blocks", "kvpool_wait_selftest", "kvpool_topk_static_check", "kvpool_rope_table",
            "kvpool_qk_norm_rope", "kvpool_window_workspace", "kvpool_window_attend",
-           "kvpool_decode_attend_shared", "kvpool_window_check", "kvpool_set_share_bytes"]
+           "kvpool_decode_attend_shared", "kvpool_window_check", "kvpool_set_share_bytes", "kvpool_qk_norm_rope_axes",
+           "kvpool_kv4_page_bytes", "kvpool_kv4_store", "kvpool_kv4_load", "kvpool_kv4_workspace", "kvpool_kv4_attend",
+           "kvpool_kv4_evict"]
 
 
 class KvpoolError(RuntimeError):
@@ -128,10 +130,18 @@ def lib():
         L.kvpool_rope_table.argtypes = [i32, vp, vp]
         cp = C.c_char_p  # a packed structure
         L.kvpool_qk_norm_rope.argtypes = [i32, i32, i64, cp, cp, cp, cp, vp, vp, C.c_float, i32, i32, vp, vp, vp]
+        L.kvpool_qk_norm_rope_axes.argtypes = L.kvpool_qk_norm_rope.argtypes[:-1] + [i32, cp, vp]
         L.kvpool_window_workspace.restype = i64
         L.kvpool_window_workspace.argtypes = [cp, i32, vp, vp, vp]
         L.kvpool_window_attend.argtypes = [cp, i32, vp, vp, vp, vp, i64, vp]
         L.kvpool_window_check.argtypes = [vp, C.POINTER(C.c_uint32)]
+        L.kvpool_kv4_page_bytes.restype = i64
+        L.kvpool_kv4_page_bytes.argtypes = [i32, i32, i32]
+        L.kvpool_kv4_store.argtypes = L.kvpool_kv4_load.argtypes = [cp, i32, cp, cp, i64, i32, vp, vp, vp]
+        L.kvpool_kv4_workspace.restype = i64
+        L.kvpool_kv4_workspace.argtypes = [cp, i32, vp, vp]
+        L.kvpool_kv4_attend.argtypes = [cp, i32, vp, vp, vp, i64, vp]
+        L.kvpool_kv4_evict.argtypes = [cp, i32, vp, vp]
         L.kvpool_last_error.restype = C.c_char_p
         L.kvpool_last_error.argtypes = [vp]
         _lib = L
@@ -253,6 +263,9 @@ def _dtype(t) -> int:
 # (filling ctypes structures field by field takes longer than a small launch)
 _HEADS = struct.Struct("@Pqqii")
 _WINDOW_ARGS = struct.Struct("@ii" + 4 * "Pqqii" + "qqPiifi")
+_KV4 = struct.Struct("@PqPqiiiiiffi")  # kvpool_kv4
+_KV4_ARGS = struct.Struct("@if" + 2 * "Pqqii" + "qPPqqfi")  # kvpool_kv4_args behind its cache
+_KV4_EVICT = struct.Struct("@PqiiPqqPqqPiiii")  # kvpool_kv4_evict_args behind its cache
 
 
 def _rows(t, what: str, like=None, out: bool = False) -> tuple:
@@ -349,12 +362,14 @@ def rope_table(rot_dim: int, theta: float = 10000.0, inv_freq=None, device="cuda
 
 
 def qk_norm_rope(q, k, positions, table, q_weight=None, k_weight=None, eps: float = 1e-6, interleaved: bool = False,
-                 out_q=None, out_k=None, stream=None):
+                 out_q=None, out_k=None, stream=None, axes=None):
     """Norm every head of q and k ([tokens][heads][dim], float32 or bfloat16,
     either may be None) and rotate it by its token's position (int64
     [tokens]) with the table of rope_table (None: norms only); returns (out_q,
-    out_k), which may be given and may be q and k themselves.  No gradients
-    flow through.  See kvpool_qk_norm_rope in include/kvpool.h."""
+    out_k), which may be given and may be q and k themselves.  axes: rot_dim / 2
+    axis numbers (host integers); positions are then [tokens][n_axes] and pair i
+    turns by the one on axis axes[i].  No gradients flow through.  See
+    kvpool_qk_norm_rope and kvpool_qk_norm_rope_axes in include/kvpool.h."""
     import torch
     x = q if q is not None else k
     if x is None or not x.is_cuda:
@@ -363,7 +378,7 @@ def qk_norm_rope(q, k, positions, table, q_weight=None, k_weight=None, eps: floa
     index = like[2]
     if torch._C._cuda_getDevice() != index:
         with torch.cuda.device(index):
-            return qk_norm_rope(q, k, positions, table, q_weight, k_weight, eps, interleaved, out_q, out_k, stream)
+            return qk_norm_rope(q, k, positions, table, q_weight, k_weight, eps, interleaved, out_q, out_k, stream, axes)
     kind = _dtype(x)
     raw = _stream_of(stream, index)
     T = x.shape[0]
@@ -393,10 +408,28 @@ def qk_norm_rope(q, k, positions, table, q_weight=None, k_weight=None, eps: floa
     if table is not None:
         rot = 2 * table.numel()
         tab = _need(table, "table", torch.int64, (rot // 2,), index) or None
-        pos = _need(positions, "positions", torch.int64, (T,), index) or None
+        if axes is None:
+            pos = _need(positions, "positions", torch.int64, (T,), index) or None
+        else:
+            if positions.dim() != 2:
+                raise ValueError("qk_norm_rope: with axes, positions must be [tokens][n_axes]")
+            n_axes = positions.shape[1]
+            pos = _need(positions, "positions", torch.int64, (T, n_axes), index) or None
+            try:
+                axes = bytes(axes.tolist() if hasattr(axes, "tolist") else list(axes))
+            except (TypeError, ValueError):
+                raise ValueError("qk_norm_rope: axes must be small host integers") from None
+            if len(axes) != rot // 2:
+                raise ValueError("qk_norm_rope: axes must have one axis per pair (rot_dim / 2)")
+    elif axes is not None:
+        raise ValueError("qk_norm_rope: axes need a table")
     qw = None if q_weight is None else _need(q_weight, "q_weight", torch.float32, (D,), index)
     kw = None if k_weight is None else _need(k_weight, "k_weight", torch.float32, (D,), index)
-    rc = lib().kvpool_qk_norm_rope(kind, D, T, qi, ki, qo, ko, qw, kw, eps, rot, 1 if interleaved else 0, tab, pos, raw)
+    call = (kind, D, T, qi, ki, qo, ko, qw, kw, eps, rot, 1 if interleaved else 0, tab, pos)
+    if axes is None:
+        rc = lib().kvpool_qk_norm_rope(*call, raw)
+    else:
+        rc = lib().kvpool_qk_norm_rope_axes(*call, n_axes, axes, raw)
     if rc != OK:
         raise KvpoolError(rc, "qk_norm_rope refused its arguments" if rc == ERR_INVALID_ARG else "qk_norm_rope: CUDA error")
     return out_q if q is not None else None, out_k if k is not None else None
@@ -460,8 +493,8 @@ def window_workspace(q, k, v, q_len, k_start, k_len, window: int, n_sink: int = 
 
 
 def window_check(stream=None) -> tuple:
-    """(return code, device error flags) of the window_attend calls on the
-    current device since the last check; synchronizes the stream."""
+    """(return code, device error flags) of the window_attend and Kv4Cache calls
+    on the current device since the last check; synchronizes the stream."""
     w = C.c_uint32(0)
     rc = lib().kvpool_window_check(_stream(stream), C.byref(w))
     return int(rc), int(w.value)
@@ -485,6 +518,213 @@ def _window_call(q, like, q_rows, k, v, q_len, k_start, k_len, window, n_sink, s
     except (struct.error, OverflowError) as e:
         raise ValueError(f"window_attend: {e}") from None
     return a, ql.size, ql.tobytes(), ks.tobytes(), kl.tobytes()
+
+
+def kv4_page_bytes(kv_heads: int, head_dim: int, page_tokens: int) -> int:
+    """Bytes of a page of a Kv4Cache."""
+    n = int(lib().kvpool_kv4_page_bytes(kv_heads, head_dim, page_tokens))
+    if n < 0:
+        raise KvpoolError(n, "kv4_page_bytes: 1 to 1024 heads of 64 or 128, pages of 16 to 1024 tokens (a power of two)")
+    return n
+
+
+def _table(t, what: str, index: int) -> tuple:
+    """(address, row stride, rows, ids per row) of a table of page ids."""
+    import torch
+    if t.dim() != 2 or t.dtype is not torch.int32 or t.get_device() != index or t.stride(1) != 1 and t.shape[1] > 1:
+        raise ValueError(f"{what} must be a 2-D int32 tensor on cuda:{index} whose rows are contiguous")
+    return t.data_ptr(), t.stride(0), t.shape[0], t.shape[1]
+
+
+def _weights(w, what: str, n: int, heads: int, width: int, index: int) -> tuple:
+    """(address, segment stride, head stride) of fp32 weights [segments][key heads][>= width]."""
+    import torch
+    if (w.dim() != 3 or w.dtype is not torch.float32 or w.get_device() != index or w.stride(2) != 1 and w.shape[2] > 1
+            or w.shape[0] < n or w.shape[1] != heads or w.shape[2] < width):
+        raise ValueError(f"{what} must be float32 [segments][key heads][at least {width} places] on cuda:{index}, places adjacent")
+    return w.data_ptr(), w.stride(0), w.stride(1)
+
+
+class Kv4Cache:
+    """A paged cache of raw tokens held in 4 bits, in the caller's pages: a
+    contiguous uint8 CUDA tensor [n_pages][kv4_page_bytes].  Segment i of a call
+    is row i of the int32 CUDA table of page ids that the call is given; lengths
+    and starts are host integers.  Nothing but the pages is kept between calls.
+    See kvpool_kv4 in include/kvpool.h."""
+
+    def __init__(self, pages, kv_heads: int, head_dim: int, page_tokens: int, k_scale: float = 1.0, v_scale: float = 1.0):
+        import torch
+        size = kv4_page_bytes(kv_heads, head_dim, page_tokens)
+        if not pages.is_cuda or pages.dtype is not torch.uint8 or pages.dim() != 2 or pages.shape[1] != size or \
+                not pages.is_contiguous() or pages.data_ptr() % 16:
+            raise ValueError(f"Kv4Cache: pages must be a contiguous uint8 CUDA tensor [n_pages][{size}]")
+        self.pages, self.kv_heads, self.head_dim, self.page_tokens = pages, kv_heads, head_dim, page_tokens
+        self.k_scale, self.v_scale = k_scale, v_scale
+        self.index = pages.get_device()
+
+    def _pack(self, table, n: int) -> bytes:
+        ptr, stride, rows, width = _table(table, "table", self.index)
+        if rows < n:
+            raise ValueError("the table must have a row per segment")
+        return _KV4.pack(self.pages.data_ptr(), self.pages.shape[0], ptr, stride, rows, width, self.kv_heads, self.head_dim,
+                         self.page_tokens, self.k_scale, self.v_scale, 0)
+
+    def _done(self, rc: int, what: str) -> None:
+        if rc != OK:
+            raise KvpoolError(rc, f"{what} refused its arguments" if rc == ERR_INVALID_ARG else f"{what}: CUDA error")
+
+    def _two(self, start, length, what: str):
+        a, b = _i64(start), _i64(length)
+        if a.size != b.size:
+            raise ValueError(f"{what}: one value of each kind per segment")
+        return a, b
+
+    def store(self, k, v, table, start, n_new, stream=None) -> None:
+        """Store the next n_new[i] rows of k and v ([rows][key heads][dim],
+        float32 or bfloat16) as the tokens of segment i from place start[i] on.
+        See kvpool_kv4_store in include/kvpool.h."""
+        import torch
+        if torch._C._cuda_getDevice() != self.index:
+            with torch.cuda.device(self.index):
+                return self.store(k, v, table, start, n_new, stream)
+        start, n_new = self._two(start, n_new, "store")
+        self._move("kvpool_kv4_store", k, v, table, start, n_new, False, stream)
+
+    def load(self, table, start, length, dtype=None, out_k=None, out_v=None, stream=None) -> tuple:
+        """(k, v): segment i's length[i] tokens from place start[i] on, as the
+        values that they stand for (bfloat16 unless dtype or out_k says float32).
+        See kvpool_kv4_load in include/kvpool.h."""
+        import torch
+        if torch._C._cuda_getDevice() != self.index:
+            with torch.cuda.device(self.index):
+                return self.load(table, start, length, dtype, out_k, out_v, stream)
+        start, length = self._two(start, length, "load")
+        shape = (int(length.sum()) if length.size else 0, self.kv_heads, self.head_dim)
+        if out_k is None or out_v is None:
+            if dtype is None:
+                o = out_k if out_k is not None else out_v
+                dtype = torch.bfloat16 if o is None else o.dtype
+            fresh = [None if o is not None else self._empty(shape, dtype, stream) for o in (out_k, out_v)]
+            out_k, out_v = out_k if out_k is not None else fresh[0], out_v if out_v is not None else fresh[1]
+        self._move("kvpool_kv4_load", out_k, out_v, table, start, length, True, stream)
+        return out_k, out_v
+
+    def _empty(self, shape, dtype, stream):
+        """A tensor whose memory belongs to the stream that will write it."""
+        import torch
+        raw = _stream_of(stream, self.index)
+        if stream is None or raw == torch._C._cuda_getCurrentRawStream(self.index):
+            return torch.empty(shape, dtype=dtype, device=self.pages.device)
+        with torch.cuda.stream(torch.cuda.ExternalStream(raw, device=self.pages.device)):
+            return torch.empty(shape, dtype=dtype, device=self.pages.device)
+
+    def _move(self, name, k, v, table, start, length, out, stream) -> None:
+        if not k.is_cuda:
+            raise ValueError("k and v must be CUDA tensors")
+        like = _like(k)
+        if like[2] != self.index or like[1] != self.head_dim or k.shape != v.shape:
+            raise ValueError("k and v must be alike, of the cache's head dim and on its device")
+        rc = getattr(lib(), name)(self._pack(table, start.size), _dtype(k), _HEADS.pack(*_rows(k, "k", like, out)),
+                                  _HEADS.pack(*_rows(v, "v", like, out)), k.shape[0], start.size, start.tobytes(),
+                                  length.tobytes(), _stream_of(stream, self.index))
+        self._done(rc, name[7:])
+
+    def attend(self, q, table, q_len, k_len, scale=None, out=None, lse=None, weights=None, decay: float = 1.0, workspace=None,
+               stream=None):
+        """Attention of a ragged batch of queries, each segment's last ones, over
+        its k_len[i] tokens; returns out ([rows][q heads][dim], like q, and q
+        itself if given as out).  lse: a float32 [rows][q heads] tensor to fill, or
+        None.  weights: None, or float32 accumulators [segments][key heads][places]
+        that become decay times what they were plus the softmax weights that each
+        token got from its head's queries.  workspace: a uint8 CUDA tensor of
+        workspace() bytes (one is allocated when None).  No gradients flow through.
+        See kvpool_kv4_attend in include/kvpool.h."""
+        import torch
+        if torch._C._cuda_getDevice() != self.index:
+            with torch.cuda.device(self.index):
+                return self.attend(q, table, q_len, k_len, scale, out, lse, weights, decay, workspace, stream)
+        raw = _stream_of(stream, self.index)
+        if not q.is_cuda:
+            raise ValueError("attend: q must be a CUDA tensor")
+        like = _like(q)
+        rows = _rows(q, "q", like)
+        if out is None:
+            out, o = _fresh(q, stream, raw)
+        else:
+            o = _rows(out, "out", like, True)
+        call = self._call(q, like, rows, table, q_len, k_len, scale, out, o, lse, weights, decay)
+        L = lib()
+        rc = L.kvpool_kv4_workspace(*call)
+        if rc >= 0:
+            nbytes = 0
+            if workspace is not None:
+                if workspace.get_device() != self.index or not workspace.is_contiguous():
+                    raise ValueError("attend: workspace must be a contiguous tensor on the cache's device")
+                nbytes = workspace.numel() * workspace.element_size()
+            elif rc > 0:
+                nbytes = rc
+                workspace = self._empty((rc,), torch.uint8, stream)
+            rc = L.kvpool_kv4_attend(*call, workspace.data_ptr() if nbytes else None, nbytes, raw)
+        self._done(rc, "attend")
+        return out
+
+    def workspace(self, q, table, q_len, k_len, scale=None, weights=None) -> int:
+        """Workspace bytes of attend with these arguments."""
+        import torch
+        like = _like(q)
+        with torch.cuda.device(self.index):
+            rows = _rows(q, "q", like)
+            # an output like q, which may be a view that no output could have
+            o = (rows[0], q.shape[1] * q.shape[2], q.shape[2], q.shape[1], 0)
+            rc = int(lib().kvpool_kv4_workspace(*self._call(q, like, rows, table, q_len, k_len, scale, q, o, None, weights, 1.0)))
+        if rc < 0:
+            raise KvpoolError(rc, "workspace refused its arguments")
+        return rc
+
+    def _call(self, q, like, q_rows, table, q_len, k_len, scale, out, out_rows, lse, weights, decay):
+        import torch
+        if like[1] != self.head_dim or like[2] != self.index or out.shape != q.shape:
+            raise ValueError("attend: q and out must be alike, of the cache's head dim and on its device")
+        ql, kl = self._two(q_len, k_len, "attend")
+        z = 0 if lse is None else _need(lse, "lse", torch.float32, q.shape[:2], self.index)
+        w = (0, 0, 0)
+        if weights is not None:
+            w = _weights(weights, "weights", ql.size, self.kv_heads, int(kl.max()) if kl.size else 0, self.index)
+        try:
+            a = _KV4_ARGS.pack(_dtype(q), self.head_dim ** -0.5 if scale is None else scale, *q_rows, *out_rows, q.shape[0], z,
+                               *w, decay, 0)
+        except (struct.error, OverflowError) as e:
+            raise ValueError(f"attend: {e}") from None
+        return self._pack(table, ql.size) + a, ql.size, ql.tobytes(), kl.tobytes()
+
+    def evict(self, table, k_len, weights, keep: int, out_table, n_sink: int = 0, n_recent: int = 0, index=None,
+              out_weights=None, stream=None) -> tuple:
+        """Keep, of each segment's k_len[i] tokens and for every key head, the
+        first n_sink, the last n_recent and the heaviest others, keep in all, in
+        the pages of out_table (none of which is in table); returns (index,
+        out_weights): the places they had ([segments][key heads][keep] int32, -1
+        behind the last) and their weights (zeros behind).  See kvpool_kv4_evict in
+        include/kvpool.h."""
+        import torch
+        if torch._C._cuda_getDevice() != self.index:
+            with torch.cuda.device(self.index):
+                return self.evict(table, k_len, weights, keep, out_table, n_sink, n_recent, index, out_weights, stream)
+        kl = _i64(k_len)
+        n, H = kl.size, self.kv_heads
+        w = _weights(weights, "weights", n, H, int(kl.max()) if n else 0, self.index)
+        ot = _table(out_table, "out_table", self.index)
+        if index is None:
+            index = self._empty((n, H, max(keep, 0)), torch.int32, stream)
+        if out_weights is None:
+            out_weights = self._empty((n, H, max(keep, 0)), torch.float32, stream)
+        at = _need(index, "index", torch.int32, torch.Size((n, H, keep)), self.index)
+        ow = _weights(out_weights, "out_weights", n, H, keep, self.index)
+        try:
+            a = _KV4_EVICT.pack(*ot, *w, *ow, at, out_weights.shape[2], keep, n_sink, n_recent)
+        except (struct.error, OverflowError) as e:
+            raise ValueError(f"evict: {e}") from None
+        self._done(lib().kvpool_kv4_evict(self._pack(table, n) + a, n, kl.tobytes(), _stream_of(stream, self.index)), "evict")
+        return index, out_weights
 
 
 class Pool:

@@ -431,6 +431,16 @@ int kvpool_qk_norm_rope(int32_t dtype, int32_t head_dim, int64_t n_tokens, const
                         const float* d_q_weight, const float* d_k_weight, float eps, int32_t rot_dim,
                         int32_t interleaved, const uint64_t* d_table, const int64_t* d_positions, void* stream);
 
+/* The same with positions on several axes (time, height and width of a token of
+ * an image or a video): d_positions is [n_tokens][n_axes], and pair i turns by
+ * the position on axis h_axes[i] < n_axes (rot_dim / 2 host bytes, read during
+ * the call; NULL with one axis).  n_axes: 1 to 8.  Errors: INVALID_ARG, CUDA. */
+int kvpool_qk_norm_rope_axes(int32_t dtype, int32_t head_dim, int64_t n_tokens, const kvpool_heads* q,
+                             const kvpool_heads* k, const kvpool_heads* q_out, const kvpool_heads* k_out,
+                             const float* d_q_weight, const float* d_k_weight, float eps, int32_t rot_dim,
+                             int32_t interleaved, const uint64_t* d_table, const int64_t* d_positions, int32_t n_axes,
+                             const uint8_t* h_axes, void* stream);
+
 /* Attention of a ragged batch over raw K/V tokens with a sliding window and a
  * few first tokens that stay visible: a prompt's own outputs in a window
  * layer (kvpool_append takes the same tokens into the cache), or single
@@ -477,9 +487,131 @@ int64_t kvpool_window_workspace(const kvpool_window_args* args, int32_t n, const
 int kvpool_window_attend(const kvpool_window_args* args, int32_t n, const int64_t* h_q_len, const int64_t* h_k_start,
                          const int64_t* h_k_len, void* d_workspace, int64_t workspace_bytes, void* stream);
 
-/* Device-side error flags of the kvpool_window_attend calls on the current
- * device since the last check (the kvpool_check_device bits: 1 = a wait passed
- * its limit; that call's output is not valid).  Synchronizes `stream`, copies
+/* ---- a paged cache of raw tokens held in 4 bits ----
+ * For layers that attend to every token.  Tokens lie in pages of page_tokens
+ * tokens of all key heads (a power of two, 16 to 1024; kvpool_kv4_page_bytes bytes
+ * each, one after the other at d_pages, 16-byte aligned); row i of the table
+ * (int32 on the device, table_stride apart) lists the pages of segment i of a
+ * call: its token at place t is token t % page_tokens of page
+ * table[i][t / page_tokens].  Pages may be in any order and shared by rows that
+ * are only read; entries behind a segment's tokens are not looked at.  A page id
+ * outside [0, n_pages) sets flag 2 of kvpool_window_check: its tokens are not
+ * stored, read back as zeros, and attention over them is not valid.
+ * Format: 16 neighbouring values x of a head, divided by k_scale (v_scale), share
+ * s = e4m3(amax / 6), amax their largest magnitude (the fp32 quotient, to the
+ * nearest, at most 448); a value is held as the nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6
+ * to x / s (ties to the even code) with its sign, and stands for s times that
+ * times k_scale, which fp16 and bf16 hold exactly.  Values whose group has s = 0
+ * (amax <= 6 * 2^-10) are zeros, larger ones than 2688 are 2688; a group that holds
+ * a NaN or an infinity stands for NaNs.  k_scale, v_scale: powers of two, 2^-16 to 2^16.
+ * head_dim 64 or 128; up to 1024 key heads; a segment has at most 2^30 tokens.
+ * Nothing is kept between calls but the pages.  Inputs and the table lie apart
+ * from what a call writes. */
+typedef struct kvpool_kv4 {
+  void* d_pages;
+  int64_t n_pages;
+  const int32_t* d_table; /* [table_rows][table_stride], table_width ids each */
+  int64_t table_stride;
+  int32_t table_rows, table_width;
+  int32_t kv_heads, head_dim, page_tokens;
+  float k_scale, v_scale;
+  int32_t pad;
+} kvpool_kv4;
+
+/* Bytes of a page, or INVALID_ARG. */
+int64_t kvpool_kv4_page_bytes(int32_t kv_heads, int32_t head_dim, int32_t page_tokens);
+
+/* Store a ragged batch of tokens: segment i (table row i) has the next
+ * h_n_new[i] rows of k and v (of kv_heads heads, in dtype F32 or BF16), which
+ * become its tokens at places h_start[i] and on, whatever was there before; its
+ * other tokens stay as they were.  Two segments of a call must not store into
+ * one page.  rows: rows of k and v.  Errors: INVALID_ARG, CUDA. */
+int kvpool_kv4_store(const kvpool_kv4* cache, int32_t dtype, const kvpool_heads* k, const kvpool_heads* v, int64_t rows,
+                     int32_t n, const int64_t* h_start, const int64_t* h_n_new, void* stream);
+
+/* Read tokens back as the values that they stand for: segment i's h_len[i]
+ * tokens from place h_start[i] on become the next rows of k and v (outputs that
+ * lie apart from each other; rows behind the last segment stay).  Errors:
+ * INVALID_ARG, CUDA. */
+int kvpool_kv4_load(const kvpool_kv4* cache, int32_t dtype, const kvpool_heads* k, const kvpool_heads* v, int64_t rows,
+                    int32_t n, const int64_t* h_start, const int64_t* h_len, void* stream);
+
+/* Attention of a ragged batch over the cache: segment i (table row i) has the
+ * next h_q_len[i] query rows and h_k_len[i] tokens; its queries are the last ones
+ * (query j is at place p = h_k_len[i] - h_q_len[i] + j) and see the tokens at
+ * places t <= p.  A query at a place below 0 sees nothing and gives zeros and -inf.
+ * q.heads: a multiple (up to 16) of kv_heads, query head h reads key head
+ * h / (q.heads / kv_heads).  out: like q, in dtype; it may be q itself (same data
+ * and strides), otherwise it lies apart from q.  d_lse: [q_rows][q.heads] fp32
+ * natural-log sums of the exponentials, or NULL.  Query rows behind the last
+ * segment are left as they were.  A query that is NaN or infinite, or that sees a
+ * key that is NaN, gives NaN; a NaN among the values that some queries of a
+ * segment see may also reach others of it that do not.
+ * d_weights: NULL, or fp32 accumulators of segment i, key head h and the token at
+ * place t at [i * weight_stride + h * weight_head_stride + t]: the call makes them
+ * decay * what they were (which is not read when decay is 0) plus the sum of the
+ * softmax weights that the query rows of the head give the token; rows of NaN make
+ * NaNs of them.  Places from h_k_len[i] on and segments without queries stay as
+ * they were.  With d_weights a segment has at most 64 query rows per key head.
+ * dtype: KVPOOL_F32 or KVPOOL_BF16 (of q and out).  Scores, softmax statistics and
+ * sums are fp32.  Where a segment has at most 64 query rows per key head (h_q_len *
+ * group), products are of fp16 numbers: keys and values exactly, bf16 queries
+ * exactly and fp32 ones to 2^-22 of each, softmax weights to 2^-11 of each for bf16
+ * outputs and to 2^-22 for fp32 ones, all of them to 2^-39 of their row's largest
+ * where that is more.  Longer segments
+ * are read back to rows in the workspace and go through window attention with
+ * everything visible, as kvpool_window_attend says.
+ * d_workspace: kvpool_kv4_workspace bytes (16-byte aligned, may be NULL when that is
+ * 0); calls that overlap on the GPU need one each.  It, d_lse and d_weights lie
+ * apart from everything else.  The lengths are read during the call: a captured
+ * call replays with the same ones.  Errors: INVALID_ARG, CUDA. */
+typedef struct kvpool_kv4_args {
+  kvpool_kv4 cache;
+  int32_t dtype;
+  float scale; /* of the scores, e.g. 1 / sqrt(head_dim) */
+  kvpool_heads q, out;
+  int64_t q_rows; /* rows of q and out */
+  float* d_lse;
+  float* d_weights;
+  int64_t weight_stride, weight_head_stride;
+  float decay;
+  int32_t pad;
+} kvpool_kv4_args;
+
+/* Workspace bytes of that call on the current device (a negative error code
+ * if its arguments are refused). */
+int64_t kvpool_kv4_workspace(const kvpool_kv4_args* args, int32_t n, const int64_t* h_q_len, const int64_t* h_k_len);
+int kvpool_kv4_attend(const kvpool_kv4_args* args, int32_t n, const int64_t* h_q_len, const int64_t* h_k_len,
+                      void* d_workspace, int64_t workspace_bytes, void* stream);
+
+/* Evict the lightest tokens: of segment i's h_k_len[i] tokens every key head
+ * keeps the first n_sink, the last n_recent and, of the others, the ones of the
+ * largest weight (ties to the lowest place, a NaN before every number), keep in
+ * all -- every one where there are no more than that.  What stays goes, in its
+ * order, to places 0 .. min(h_k_len[i], keep) - 1 of row i of d_out_table, in
+ * pages that are no row's of d_table (those stay as they were, so they may be
+ * shared): its codes and scales are copied.  d_index: [n][kv_heads][keep], the
+ * places the tokens had, -1 behind the last.  d_out_weights: NULL, or the weights of
+ * what stays, zeros behind up to out_weight_width (at least keep); it lies apart
+ * from d_weights.  Errors: INVALID_ARG, CUDA. */
+typedef struct kvpool_kv4_evict_args {
+  kvpool_kv4 cache;
+  const int32_t* d_out_table;
+  int64_t out_table_stride;
+  int32_t out_table_rows, out_table_width;
+  const float* d_weights; /* as for kvpool_kv4_attend */
+  int64_t weight_stride, weight_head_stride;
+  float* d_out_weights;
+  int64_t out_weight_stride, out_weight_head_stride;
+  int32_t* d_index;
+  int32_t out_weight_width, keep, n_sink, n_recent;
+} kvpool_kv4_evict_args;
+int kvpool_kv4_evict(const kvpool_kv4_evict_args* args, int32_t n, const int64_t* h_k_len, void* stream);
+
+/* Device-side error flags of the kvpool_window_attend and kvpool_kv4_ calls on
+ * the current device since the last check (the kvpool_check_device bits: 1 = a
+ * wait passed its limit, 2 = a page id out of range; that call's output is not
+ * valid).  Synchronizes `stream`, copies
  * the word to *h_flags (may be NULL) and clears it.  Returns OK when it is
  * zero, DEVICE_CHECK when a flag is set, CUDA on a CUDA error. */
 int kvpool_window_check(void* stream, uint32_t* h_flags);
