@@ -13,17 +13,19 @@
 // Bound: reading the cache, 1.125 bytes for a key's and a value's number.  The
 // keys of a segment and head are cut into parts of equal length, so that all
 // parts of the launch are one wave of CTAs.  A CTA of four warps takes a part;
-// each warp has a ring of tiles (16 tokens, one bulk copy each), so that some
-// 100 KB are in flight on a multiprocessor without a register held for them.
+// each warp has a ring of pairs of tiles (32 tokens, one bulk copy), so that up to
+// 220 KB are in flight on a multiprocessor without a register held for them.
 //
 // A tile's products are mma m16n8k16 in fp16: S^T = K Q^T over 16 keys x 8 rows,
 // O^T = V^T P^T.  Codes times their scale are exact in fp16.  Queries are
 // multiplied by a power of two that brings their row's largest value to 2^14 ..
-// 2^15: a bf16 one is exact then, or off by 2^-39 of the largest (fp16's
+// 2^15: a bf16 one is exact then, or off by 2^-39 of the largest (half of fp16's
 // smallest step); an fp32 one goes in as two halves that hold 22 bits.  Softmax
-// weights (at most 1, times 2^14) go in as one half for bf16 outputs (off by
-// 2^-11 of it, the outputs' own rounding is 2^-8) and as two for fp32 ones (2^-22);
-// a weight below 2^-28 of the largest (2^-16 with two halves) by 2^-39 of that.
+// weights go in as one half for bf16 outputs (off by 2^-11 of it, the outputs'
+// own rounding is 2^-8) and as two for fp32 ones (2^-22), between 2^6 and 2^14 for
+// the largest so far, so that small ones are off by 2^-31 of that at most.  The
+// unit changes only when a weight passes 2^14 (a running maximum kept exactly
+// takes three shuffles and a rescaling test of every tile).
 #include <algorithm>
 #include <cmath>
 #include <memory>
@@ -43,7 +45,7 @@ constexpr int kWarps = 4;
 constexpr int kMaxGroup = 16;   // query heads per key head
 constexpr int kMaxRows = 64;    // query rows per key head of this file's kernel
 constexpr int kMergeWarps = 4;
-constexpr float kWeightUp = 16384.0f;  // softmax weights go into their product times this
+constexpr float kUp = 6.0f, kMost = 14.0f;  // see the kernel's c
 
 struct Kv4Seg {
   int64_t q_row0;      // first query row
@@ -67,12 +69,12 @@ struct Kv4Params {
   int64_t w_seg, w_head;
   int32_t group;
   int32_t tile_rows;       // rows of a row tile
-  int32_t part_tiles;      // tiles of a part
+  int32_t part_pairs;      // pairs of tiles of a part
   float scale_log2;        // softmax scale times log2(e) and the keys' scale
   float decay;
   int32_t n_segs, n_items, n_rows, n_blocks;
   float* part_o;    // [partials][tile_rows][head_dim]
-  float2* part_ml;  // [partials][tile_rows]: (max in the log2 domain, sum)
+  float2* part_ml;  // [partials][tile_rows]: (exponent of the weights' unit, sum)
   float* lse2;      // [n_rows], log2 domain (weights wanted)
   float* scores;    // log2 domain (weights wanted)
   Kv4Seg segs[kKv4MaxSegs];
@@ -113,16 +115,48 @@ __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t by
                : "memory");
 }
 
-constexpr int kStages = 4;
+constexpr int kStages = 3;
+constexpr int kPair = 2;  // tiles of a stage
 
 template <int D, int NT>
 struct Kv4Smem {
   union {
-    uint8_t ring[kWarps][kStages][Kv4Tile<D>::kBytes];
+    uint8_t ring[kWarps][kStages][kPair * Kv4Tile<D>::kBytes];
     float o[kWarps][NT * 8][D];  // once the ring is done with
   };
   float2 ml[kWarps][NT * 8];
   uint64_t bar[kWarps][kStages];
+};
+
+// The keys of a tile as the lane's share of fragments: keys g and g + 8, dims
+// D / 4 * t and on, eight dims to a word; sc: [key][half of the lane's dims]
+template <int D>
+struct Kv4Keys {
+  uint32_t k0[D / 32], k1[D / 32], sc[2][2];
+  __device__ __forceinline__ void load(const uint8_t* tile, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    if constexpr (D == 128) {
+      const uint4 x = *reinterpret_cast<const uint4*>(tile + lane * 16), y = *reinterpret_cast<const uint4*>(tile + 512 + lane * 16);
+      k0[0] = x.x, k0[1] = x.y, k0[2] = x.z, k0[3] = x.w;
+      k1[0] = y.x, k1[1] = y.y, k1[2] = y.z, k1[3] = y.w;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t h =
+            e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(tile + Kv4Tile<D>::kKs + (g + 8 * i) * 8 + 2 * t));
+        sc[i][0] = __byte_perm(h, h, 0x1010);
+        sc[i][1] = __byte_perm(h, h, 0x3232);
+      }
+    } else {
+      const uint2 x = *reinterpret_cast<const uint2*>(tile + lane * 8), y = *reinterpret_cast<const uint2*>(tile + 256 + lane * 8);
+      k0[0] = x.x, k0[1] = x.y;
+      k1[0] = y.x, k1[1] = y.y;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t h = tile[Kv4Tile<D>::kKs + (g + 8 * i) * 4 + t];
+        sc[i][0] = sc[i][1] = e4m3x2_to_f16x2((uint16_t)(h | h << 8));
+      }
+    }
+  }
 };
 
 // NT: tiles of 8 query rows; F32: fp32 queries and outputs
@@ -146,39 +180,54 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && !F32 ? 4 : 2) kv4_atte
   r /= P.c.kv_heads;
   const int row0 = r % row_tiles * P.tile_rows, part = r / row_tiles;
   const int rows = min(P.tile_rows, n_rows - row0);
-  const int pos0 = S.k_len - S.q_len + row0 / P.group;                // the first row's place
+  const int pos0 = S.k_len - S.q_len + row0 / P.group;  // the first row's place
   // keys that some row sees (may be < 1); where scores are kept, every key has one
   const int seen = P.scores ? S.k_len : S.k_len - S.q_len + (row0 + rows - 1) / P.group + 1;
-  const int a = part * P.part_tiles;
-  const int b = min((max(seen, 0) + kKv4Tile - 1) / kKv4Tile, a + P.part_tiles);
-  const int n_my = b > a + warp ? (b - a - warp + kWarps - 1) / kWarps : 0;  // tiles a + warp, + kWarps, ...
+  // pairs of tiles a + warp, + kWarps, ... below b
+  const int a = part * P.part_pairs;
+  const int b = min((max(seen, 0) + kPair * kKv4Tile - 1) / (kPair * kKv4Tile), a + P.part_pairs);
+  const int n_my = b > a + warp ? (b - a - warp + kWarps - 1) / kWarps : 0;
 
   // ---- the ring ----
   uint64_t* bar = sm.bar[warp];
   if (lane < kStages) mbar_init(&bar[lane], 1);
   mbar_fence_init();
   __syncwarp();
-  // page ids of 32 of the warp's tiles, and of the next 32
+  // Page ids of 16 of the warp's pairs, and of the next 16: lane 2i + j has the
+  // one of tile j of pair i (a pair in one page has two equal ones).  A tile
+  // behind the segment's last one is never looked up: its pair is in one page,
+  // or it is not copied.
+  const int last = (S.k_len - 1) / kKv4Tile;
   auto ids_from = [&](int i) {
-    const int tile = a + warp + kWarps * (i + lane);
-    return i + lane < n_my ? kv4_page(P.c, S.table_row, tile) : 0;
+    const int tile = kPair * (a + warp + kWarps * (i + (lane >> 1))) + (lane & 1);
+    return i + (lane >> 1) < n_my ? kv4_page(P.c, S.table_row, min(tile, last)) : 0;
   };
-  int ids = ids_from(0), ids_next = ids_from(32);
-  auto issue = [&](int i) {
-    if (i > 0 && (i & 31) == 0) {
+  int ids = ids_from(0), ids_next = ids_from(16);
+  auto issue = [&](int i, int stage) {
+    if (i > 0 && (i & 15) == 0) {
       ids = ids_next;
-      ids_next = ids_from(i + 32);
+      ids_next = ids_from(i + 16);
     }
-    const int id = __shfl_sync(0xffffffffu, ids, i & 31);
-    const int64_t off = kv4_tile_offset<D>(P.c, max(id, 0), head, a + warp + kWarps * i);  // a bad page: page 0 (flagged)
+    // (a bad page: page 0, flagged)
+    const int id0 = max(__shfl_sync(0xffffffffu, ids, 2 * (i & 15)), 0);
+    const int id1 = max(__shfl_sync(0xffffffffu, ids, 2 * (i & 15) + 1), 0);
+    const int tile = kPair * (a + warp + kWarps * i);
     if (lane == 0) {
-      uint64_t* mb = &bar[i % kStages];
-      mbar_arrive_expect_tx(mb, L::kBytes);
-      bulk_g2s(sm.ring[warp][i % kStages], P.c.pages + off, L::kBytes, mb);
+      uint64_t* mb = &bar[stage];
+      uint8_t* dst = sm.ring[warp][stage];
+      const uint8_t* src = P.c.pages + kv4_tile_offset<D>(P.c, id0, head, tile);
+      if (P.c.page_shift > 0) {  // both tiles in one page
+        mbar_arrive_expect_tx(mb, kPair * L::kBytes);
+        bulk_g2s(dst, src, kPair * L::kBytes, mb);
+      } else {
+        mbar_arrive_expect_tx(mb, (tile < last ? kPair : 1) * L::kBytes);
+        bulk_g2s(dst, src, L::kBytes, mb);
+        if (tile < last) bulk_g2s(dst + L::kBytes, P.c.pages + kv4_tile_offset<D>(P.c, id1, head, tile + 1), L::kBytes, mb);
+      }
     }
   };
   int issued = 0;
-  for (; issued < min(kStages, n_my); ++issued) issue(issued);
+  for (; issued < min(kStages, n_my); ++issued) issue(issued, issued);
 
   // ---- queries: row 8n + g, dims D / 4 * t .. as fp16 pieces ----
   constexpr int vb = F32 ? 4 : 2;
@@ -230,10 +279,14 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && !F32 ? 4 : 2) kv4_atte
     }
   }
 
-  float m[NT][2], l[NT][2], o[NT][D / 16][4];
+  // A row's weights are 2^(score + c): c is such that the largest score seen when
+  // it was last set gave 2^kUp, and is set anew when one passes 2^kMost (`most`;
+  // -inf before the row's first score).
+  float c[NT][2], most[NT][2], l[NT][2], o[NT][D / 16][4];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    m[n][0] = m[n][1] = -INFINITY;
+    c[n][0] = c[n][1] = 0.0f;
+    most[n][0] = most[n][1] = -INFINITY;
     l[n][0] = l[n][1] = 0.0f;
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
@@ -244,153 +297,157 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && !F32 ? 4 : 2) kv4_atte
   const int pitch = score_pitch(S.k_len);
   if (P.scores) scores = P.scores + S.score_base + ((int64_t)head * n_rows + row0) * pitch;
 
-  // ---- tiles ----
+  // ---- pairs of tiles ----
+  int stage = 0, phase = 0;
 #pragma unroll 1
   for (int i = 0; i < n_my; ++i) {
-    const int stage = i % kStages;
-    if (!warp_wait(&bar[stage], (i / kStages) & 1, P.c.err)) {  // (flagged) the copies on their way, then the end
-      for (int j = i + 1; j < issued; ++j) warp_wait(&bar[j % kStages], (j / kStages) & 1, P.c.err);
+    if (!warp_wait(&bar[stage], phase, P.c.err)) {  // (flagged) the copies on their way, then the end
+      for (int j = i + 1; j < issued; ++j) warp_wait(&bar[j % kStages], j / kStages & 1, P.c.err);
       break;
     }
-    const uint8_t* tile = sm.ring[warp][stage];
-    const int u0 = (a + warp + kWarps * i) * kKv4Tile;
-    float s[NT][4];
-    {
+    const uint8_t* ring = sm.ring[warp][stage];
+    const int u0 = (a + warp + kWarps * i) * kPair * kKv4Tile;
+    float s[kPair][NT][4];  // [2i + c]: key g + 8i of the tile, row 8n + 2t + c
+#pragma unroll
+    for (int y = 0; y < kPair; ++y) {
+      Kv4Keys<D> K;
+      K.load(ring + y * L::kBytes, lane);
       float s2[NT][4];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[n][j] = s2[n][j] = 0.0f;
-      // keys g and g + 8, dims D / 4 * t and on
-      constexpr int W = D / 32;  // words of 8 dims
-      uint32_t k0[W], k1[W], sc[2][2];
-      if constexpr (D == 128) {
-        const uint4 x = *reinterpret_cast<const uint4*>(tile + lane * 16), y = *reinterpret_cast<const uint4*>(tile + 512 + lane * 16);
-        k0[0] = x.x, k0[1] = x.y, k0[2] = x.z, k0[3] = x.w;
-        k1[0] = y.x, k1[1] = y.y, k1[2] = y.z, k1[3] = y.w;
+        for (int j = 0; j < 4; ++j) s[y][n][j] = s2[n][j] = 0.0f;
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const uint32_t h = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(tile + L::kKs + (g + 8 * y) * 8 + 2 * t));
-          sc[y][0] = __byte_perm(h, h, 0x1010);
-          sc[y][1] = __byte_perm(h, h, 0x3232);
-        }
-      } else {
-        const uint2 x = *reinterpret_cast<const uint2*>(tile + lane * 8), y = *reinterpret_cast<const uint2*>(tile + 256 + lane * 8);
-        k0[0] = x.x, k0[1] = x.y;
-        k1[0] = y.x, k1[1] = y.y;
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const uint32_t h = tile[L::kKs + (g + 8 * y) * 4 + t];
-          sc[y][0] = sc[y][1] = e4m3x2_to_f16x2((uint16_t)(h | h << 8));
-        }
-      }
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
-        uint32_t x[4], y[4];
-        e2m1x8_to_f16x2x4(k0[w], x);
-        e2m1x8_to_f16x2x4(k1[w], y);
+      for (int w = 0; w < D / 32; ++w) {
+        uint32_t k0[4], k1[4];
+        e2m1x8_to_f16x2x4(K.k0[w], k0);
+        e2m1x8_to_f16x2x4(K.k1[w], k1);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          x[j] = mul_f16x2(x[j], sc[0][w / 2]);
-          y[j] = mul_f16x2(y[j], sc[1][w / 2]);
+          k0[j] = mul_f16x2(k0[j], K.sc[0][w / 2]);
+          k1[j] = mul_f16x2(k1[j], K.sc[1][w / 2]);
         }
 #pragma unroll
-        for (int c = kPieces - 1; c >= 0; --c)
+        for (int x = kPieces - 1; x >= 0; --x)
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            mma_f16(s[n], x[0], y[0], x[1], y[1], q[c][n][4 * w], q[c][n][4 * w + 1]);
-            mma_f16(s2[n], x[2], y[2], x[3], y[3], q[c][n][4 * w + 2], q[c][n][4 * w + 3]);
+            mma_f16(s[y][n], k0[0], k1[0], k0[1], k1[1], q[x][n][4 * w], q[x][n][4 * w + 1]);
+            mma_f16(s2[n], k0[2], k1[2], k0[3], k1[3], q[x][n][4 * w + 2], q[x][n][4 * w + 3]);
           }
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[n][j] = (s[n][j] + s2[n][j]) * mul[n][j & 1];
-    }
-    // s[n][2i + c]: key g + 8i, row 8n + 2t + c
-    const bool whole = u0 + kKv4Tile - 1 <= pos0;  // every row sees every key of the tile
-    if (!whole) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (u0 + g + 8 * (j >> 1) > pos[n][j & 1]) s[n][j] = -INFINITY;
+        for (int j = 0; j < 4; ++j) s[y][n][j] += s2[n][j];
     }
     if (scores) {
 #pragma unroll
+      for (int y = 0; y < kPair; ++y)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int row = 8 * n + 2 * t + (j & 1), u = u0 + kKv4Tile * y + g + 8 * (j >> 1);
+            if (row < rows && u < S.k_len)
+              scores[(int64_t)row * pitch + u] = u <= pos[n][j & 1] ? s[y][n][j] * mul[n][j & 1] : -INFINITY;
+          }
+    }
+    bool high = false;
+#pragma unroll
+    for (int y = 0; y < kPair; ++y)
+#pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int row = 8 * n + 2 * t + (j & 1), u = u0 + g + 8 * (j >> 1);
-          if (row < rows && u < S.k_len) scores[(int64_t)row * pitch + u] = s[n][j];
-        }
-    }
-    uint32_t pt[kPieces][NT][2];  // [keys 0 - 7, 8 - 15]
+        for (int j = 0; j < 4; ++j) s[y][n][j] = fmaf(s[y][n][j], mul[n][j & 1], c[n][j & 1]);
+    if (u0 + kPair * kKv4Tile - 1 > pos0) {  // some row does not see some key
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      float mx[2], corr[2];
+      for (int y = 0; y < kPair; ++y)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (u0 + kKv4Tile * y + g + 8 * (j >> 1) > pos[n][j & 1]) s[y][n][j] = -INFINITY;
+    }
+    float mx[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        mx[e] = fmaxf(s[n][e], s[n][2 + e]);
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], off));
-        mx[e] = fmaxf(mx[e], m[n][e]);
-        const float base = mx[e] == -INFINITY ? 0.0f : mx[e];
-        corr[e] = ex2f(m[n][e] - base);
-        m[n][e] = mx[e];
-        s[n][e] = ex2f(s[n][e] - base);
-        s[n][2 + e] = ex2f(s[n][2 + e] - base);
-        l[n][e] = fmaf(l[n][e], corr[e], s[n][e] + s[n][2 + e]);  // this lane's keys only
+        mx[n][e] = fmaxf(fmaxf(s[0][n][e], s[0][n][2 + e]), fmaxf(s[1][n][e], s[1][n][2 + e]));
+        high |= mx[n][e] > most[n][e];
       }
-      if (__any_sync(0xffffffffu, corr[0] != 1.0f || corr[1] != 1.0f)) {
+    if (__any_sync(0xffffffffu, high)) {
 #pragma unroll
-        for (int x = 0; x < D / 16; ++x)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) o[n][x][j] *= corr[j & 1];
-      }
+        for (int e = 0; e < 2; ++e) {
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const float p0 = s[n][2 * y] * kWeightUp, p1 = s[n][2 * y + 1] * kWeightUp;
-        const uint32_t pk = pack_f16(p0, p1);
-        if constexpr (F32) {
-          const float2 h = unpack_f16(pk);
-          pt[1][n][y] = transpose8x8(pack_f16(p0 - h.x, p1 - h.y));
+          for (int off = 4; off < 32; off <<= 1) mx[n][e] = fmaxf(mx[n][e], __shfl_xor_sync(0xffffffffu, mx[n][e], off));
+          if (!(mx[n][e] > most[n][e])) continue;
+          const float d = kUp - mx[n][e], f = ex2f(d);  // (the first time, l and o are zeros or NaN)
+          c[n][e] += d;
+          most[n][e] = kMost;
+          l[n][e] = l[n][e] == 0.0f ? 0.0f : l[n][e] * f;
+#pragma unroll
+          for (int y = 0; y < kPair; ++y) s[y][n][e] += d, s[y][n][2 + e] += d;
+#pragma unroll
+          for (int x = 0; x < D / 16; ++x) {
+            o[n][x][e] = o[n][x][e] == 0.0f ? 0.0f : o[n][x][e] * f;
+            o[n][x][2 + e] = o[n][x][2 + e] == 0.0f ? 0.0f : o[n][x][2 + e] * f;
+          }
         }
-        pt[0][n][y] = transpose8x8(pk);  // row g, keys 2t, 2t + 1 (+ 8)
-      }
     }
-    // values: lane's dims D / 8 * g and on of the token pairs t and t + 4
-    {
+#pragma unroll
+    for (int y = 0; y < kPair; ++y) {
+      uint32_t pt[kPieces][NT][2];  // [keys 0 - 7, 8 - 15]
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[y][n][j] = ex2f(s[y][n][j]);
+        l[n][0] += s[y][n][0] + s[y][n][2];  // this lane's keys only
+        l[n][1] += s[y][n][1] + s[y][n][3];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t pk = pack_f16(s[y][n][2 * j], s[y][n][2 * j + 1]);
+          if constexpr (F32) {
+            const float2 h = unpack_f16(pk);
+            pt[1][n][j] = transpose8x8(pack_f16(s[y][n][2 * j] - h.x, s[y][n][2 * j + 1] - h.y));
+          }
+          pt[0][n][j] = transpose8x8(pk);  // row g, keys 2t, 2t + 1 (+ 8)
+        }
+      }
+      // values: lane's dims D / 8 * g and on of the token pairs t and t + 4
       constexpr int W = D / 32;  // words of 4 dims
       uint32_t v0[W], v1[W];
+      const uint8_t* tile = ring + y * L::kBytes;
       const uint8_t* p = tile + L::kV + t * D + (g ^ kv4_swizzle<D>(t)) * L::kChunk;  // (t and t + 4 swizzle alike)
       if constexpr (D == 128) {
-        const uint4 x = *reinterpret_cast<const uint4*>(p), y = *reinterpret_cast<const uint4*>(p + 4 * D);
+        const uint4 x = *reinterpret_cast<const uint4*>(p), z = *reinterpret_cast<const uint4*>(p + 4 * D);
         v0[0] = x.x, v0[1] = x.y, v0[2] = x.z, v0[3] = x.w;
-        v1[0] = y.x, v1[1] = y.y, v1[2] = y.z, v1[3] = y.w;
+        v1[0] = z.x, v1[1] = z.y, v1[2] = z.z, v1[3] = z.w;
       } else {
-        const uint2 x = *reinterpret_cast<const uint2*>(p), y = *reinterpret_cast<const uint2*>(p + 4 * D);
+        const uint2 x = *reinterpret_cast<const uint2*>(p), z = *reinterpret_cast<const uint2*>(p + 4 * D);
         v0[0] = x.x, v0[1] = x.y;
-        v1[0] = y.x, v1[1] = y.y;
+        v1[0] = z.x, v1[1] = z.y;
       }
       const int grp = g * L::kChunk / kKv4Group;
       uint32_t e0 = *reinterpret_cast<const uint16_t*>(tile + L::kVs + t * (D / 8) + 2 * grp);
       uint32_t e1 = *reinterpret_cast<const uint16_t*>(tile + L::kVs + (t + 4) * (D / 8) + 2 * grp);
-      if (u0 + kKv4Tile > S.k_len) {  // places behind the last token may hold anything
-        const int left = S.k_len - u0 - 2 * t;
+      if (u0 + kKv4Tile * (y + 1) > S.k_len) {  // places behind the last token may hold anything
+        const int left = S.k_len - u0 - kKv4Tile * y - 2 * t;
         e0 &= left >= 2 ? 0xFFFFu : left == 1 ? 0xFFu : 0u;
         e1 &= left >= 10 ? 0xFFFFu : left == 9 ? 0xFFu : 0u;
       }
       const uint32_t f0 = e4m3x2_to_f16x2((uint16_t)e0), f1 = e4m3x2_to_f16x2((uint16_t)e1);
 #pragma unroll
       for (int w = 0; w < W; ++w) {
-        uint32_t x[4], y[4];
+        uint32_t x[4], z[4];
         e2m1x8_to_f16x2x4(v0[w], x);
-        e2m1x8_to_f16x2x4(v1[w], y);
+        e2m1x8_to_f16x2x4(v1[w], z);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           x[j] = mul_f16x2(x[j], f0);
-          y[j] = mul_f16x2(y[j], f1);
+          z[j] = mul_f16x2(z[j], f1);
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j)
@@ -398,18 +455,19 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && !F32 ? 4 : 2) kv4_atte
           for (int n = 0; n < NT; ++n) {
             if constexpr (F32) {  // a tile's own sum, added with rounding (the tensor core cuts a running sum off)
               float d[4] = {0.f, 0.f, 0.f, 0.f};
-              mma_f16(d, x[2 * j], x[2 * j + 1], y[2 * j], y[2 * j + 1], pt[1][n][0], pt[1][n][1]);
-              mma_f16(d, x[2 * j], x[2 * j + 1], y[2 * j], y[2 * j + 1], pt[0][n][0], pt[0][n][1]);
+              mma_f16(d, x[2 * j], x[2 * j + 1], z[2 * j], z[2 * j + 1], pt[1][n][0], pt[1][n][1]);
+              mma_f16(d, x[2 * j], x[2 * j + 1], z[2 * j], z[2 * j + 1], pt[0][n][0], pt[0][n][1]);
 #pragma unroll
-              for (int z = 0; z < 4; ++z) o[n][2 * w + j][z] += d[z];
+              for (int k = 0; k < 4; ++k) o[n][2 * w + j][k] += d[k];
             } else {
-              mma_f16(o[n][2 * w + j], x[2 * j], x[2 * j + 1], y[2 * j], y[2 * j + 1], pt[0][n][0], pt[0][n][1]);
+              mma_f16(o[n][2 * w + j], x[2 * j], x[2 * j + 1], z[2 * j], z[2 * j + 1], pt[0][n][0], pt[0][n][1]);
             }
           }
       }
     }
-    __syncwarp();  // the tile is read
-    if (issued < n_my) issue(issued++);
+    __syncwarp();  // the pair is read
+    if (issued < n_my) issue(issued++, stage);
+    if (++stage == kStages) stage = 0, phase ^= 1;
   }
 
   // ---- the warps' states into one ----
@@ -421,7 +479,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && !F32 ? 4 : 2) kv4_atte
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], off);
       const int row = 8 * n + 2 * t + e;
-      if (g == 0) sm.ml[warp][row] = make_float2(m[n][e], l[n][e]);
+      // the exponent of the weights' unit (-inf: the row saw nothing)
+      if (g == 0) sm.ml[warp][row] = make_float2(l[n][e] == 0.0f ? -INFINITY : -c[n][e], l[n][e]);
 #pragma unroll
       for (int x = 0; x < D / 16; ++x)  // dims D / 8 * g + 2x, + 1
         *reinterpret_cast<float2*>(&sm.o[warp][row][L::kChunk * g + 2 * x]) = make_float2(o[n][x][e], o[n][x][2 + e]);
@@ -452,7 +511,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && !F32 ? 4 : 2) kv4_atte
       if (c == 0) P.part_ml[pr] = make_float2(mx, sum);
       continue;
     }
-    const float inv = sum > 0.0f ? P.c.v_scale / kWeightUp / sum : sum == 0.0f ? 0.0f : sum;  // (a NaN stays one)
+    const float inv = sum > 0.0f ? P.c.v_scale / sum : sum == 0.0f ? 0.0f : sum;  // (a NaN stays one)
     const int gr = row0 + row;
     const int64_t tok = S.q_row0 + gr / P.group;
     const int h = head * P.group + gr % P.group;
@@ -502,7 +561,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) kv4_merge_kernel(const __gri
     for (int i = 0; i < V; ++i) acc[i] = acc[i] * fa + x[i] * fb;
     m = mx;
   }
-  const float inv = l > 0.0f ? P.c.v_scale / kWeightUp / l : l == 0.0f ? 0.0f : l;
+  const float inv = l > 0.0f ? P.c.v_scale / l : l == 0.0f ? 0.0f : l;
   const int64_t tok = S.q_row0 + gr / P.group;
   const int h = head * P.group + gr % P.group;
   const int64_t at = tok * P.o_tok + h * P.o_head + lane * V;
@@ -588,7 +647,7 @@ int check_args(const kvpool_kv4_args* a, int32_t n, const int64_t* q_len, const 
   return KVPOOL_OK;
 }
 
-constexpr int64_t kMinTiles = 16;  // tiles of a part, at least
+constexpr int64_t kMinPairs = 8;  // pairs of tiles of a part, at least
 
 // Where a launch's workspace lies, in bytes from its start.
 struct Space {
@@ -618,30 +677,32 @@ int32_t plan(const kvpool_kv4_args* a, int32_t i0, int32_t n, const int64_t* q_l
   *q_row = row;
   P->tile_rows = most_rows <= 8 ? 8 : 16;
   auto row_tiles = [&](const Kv4Seg& S) { return ((int64_t)S.q_len * group + P->tile_rows - 1) / P->tile_rows; };
-  auto tiles = [&](const Kv4Seg& S) { return std::max<int64_t>(1, ((int64_t)S.k_len + kKv4Tile - 1) / kKv4Tile); };
+  auto pairs = [&](const Kv4Seg& S) {
+    return std::max<int64_t>(1, ((int64_t)S.k_len + kPair * kKv4Tile - 1) / (kPair * kKv4Tile));
+  };
   auto items = [&](int64_t part) {
     int64_t x = 0;
     for (int s = 0; s < P->n_segs; ++s) {
       const Kv4Seg& S = P->segs[s];
-      x += (tiles(S) + part - 1) / part * row_tiles(S) * hk;
+      x += (pairs(S) + part - 1) / part * row_tiles(S) * hk;
     }
     return x;
   };
   // the shortest parts that are one wave of CTAs together
   const int64_t want = (int64_t)n_sms * (P->tile_rows == 8 && a->dtype == KVPOOL_BF16 ? 4 : 2);
-  int64_t lo = kMinTiles, hi = kMinTiles;
+  int64_t lo = kMinPairs, hi = kMinPairs;
   while (hi < (1 << 26) && items(hi) > want) hi *= 2;
   while (lo < hi) {
     const int64_t mid = (lo + hi) / 2;
     if (items(mid) <= want) hi = mid;
     else lo = mid + 1;
   }
-  P->part_tiles = (int32_t)lo;
+  P->part_pairs = (int32_t)lo;
   int64_t item = 0, partials = 0, rows = 0, blocks = 0, scores = 0;
   bool cut = false;
   for (int s = 0; s < P->n_segs; ++s) {
     Kv4Seg& S = P->segs[s];
-    const int64_t parts = (tiles(S) + lo - 1) / lo, its = parts * row_tiles(S) * hk;
+    const int64_t parts = (pairs(S) + lo - 1) / lo, its = parts * row_tiles(S) * hk;
     S.n_parts = (int32_t)parts;
     S.item_base = (int32_t)item;
     S.part_base = (int32_t)partials;

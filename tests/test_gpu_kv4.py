@@ -141,8 +141,8 @@ def check(q, k, v, q_len, k_len, scale, dtype, out, lse, w=None, w0=None, decay=
     products are exact (fp32 queries to 2^-22 of each), sums of up to 128 of them in the tensor core, cut off at a few
     2^-24 of their size for each of at most 16 steps, and two roundings of the scale: 2^-19 A at most.  A weight is then off by
     d = 2^-19 A + 2^-20 of itself (exp2 and its argument), the sum of them by as much, and goes into the product rounded (r:
-    half an fp16 step 2^-11, of two halves 2^-21; prompts of bf16 2^-8) or to fp16's smallest step, 2^-24 of weights times 2^14: half of it is 2^-39 of
-    the row's largest weight, which is 1 at most, so that an output is off by 2^-39 sum |v| more.  The product's running sum loses 2^-23 of its size per step, 2^-17 over the 64 steps that a warp takes here.  Prompts of fp32
+    half an fp16 step 2^-11, of two halves 2^-21; prompts of bf16 2^-8) or to fp16's smallest step, 2^-24 of weights times 2^6 to 2^14: half of it is 2^-31
+    of the row's largest weight, which is 1 at most, so that an output is off by 2^-31 sum |v| more.  The product's running sum loses 2^-23 of its size per step, 2^-17 over the 64 steps that a warp takes here.  Prompts of fp32
     go through chains of 64 fused multiply-adds for a score (2^-17 A with the rest) and of up to 400 for an output (2^-15)."""
     at, rows = 0, 0
     f32 = dtype == F32
@@ -151,7 +151,7 @@ def check(q, k, v, q_len, k_len, scale, dtype, out, lse, w=None, w0=None, decay=
         o, z, wt, A, mag, flat = F.attend(q[rows:rows + n], k[at:at + kl], v[at:at + kl], n, kl, scale)
         d = 2.0 ** (-17 if prompt else -19) * A + 2.0 ** -20
         got, gz = out[rows:rows + n].double().cpu(), lse[rows:rows + n].double().cpu()
-        tol = torch.finfo(dtype).eps / 2 * o.abs() + (2 * d[..., None] + r + 2.0 ** (-15 if prompt else -17)) * mag + 2.0 ** -39 * flat + 1e-30
+        tol = torch.finfo(dtype).eps / 2 * o.abs() + (2 * d[..., None] + r + 2.0 ** (-15 if prompt else -17)) * mag + 2.0 ** -31 * flat + 1e-30
         assert bool(((got - o).abs() <= tol).all()), (i, float(((got - o).abs() / tol).max()))
         fin = z > -math.inf
         assert torch.equal(gz == -math.inf, ~fin)
