@@ -96,9 +96,11 @@ __device__ __forceinline__ uint32_t score_key(float s) {
 // without it: their early-started CTAs held SM resources that the work
 // beside them needed (measured slower).
 // ---------------------------------------------------------------------------
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_start() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  pdl_launch();
+  pdl_wait();
 }
 
 template <typename... KArgs, typename... Args>

@@ -11,9 +11,8 @@
 // (exact) or fp32 rows and go through window attention.
 //
 // Bound: reading the cache, 1.125 bytes for a key's and a value's number.  The
-// keys of a segment and head are cut into parts of equal length, so that all
-// parts of the launch are one wave of CTAs.  A CTA of four warps takes a part;
-// each warp has a ring of pairs of tiles (32 tokens, one bulk copy), so that up to
+// whole list of keys, across segments and heads, is cut into equal shares, one to
+// each warp that the GPU holds (16 to a multiprocessor).  A warp has a ring of pairs of tiles (32 tokens, one bulk copy), so that up to
 // 220 KB are in flight on a multiprocessor without a register held for them.
 //
 // A tile's products are mma m16n8k16 in fp16: S^T = K Q^T over 16 keys x 8 rows,
@@ -27,6 +26,7 @@
 // unit changes only when a weight passes 2^14 (a running maximum kept exactly
 // takes three shuffles and a rescaling test of every tile).
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <memory>
 #include <new>
@@ -41,22 +41,23 @@
 namespace kvp {
 namespace {
 
-constexpr int kWarps = 4;
 constexpr int kMaxGroup = 16;   // query heads per key head
 constexpr int kMaxRows = 64;    // query rows per key head of this file's kernel
-constexpr int kMergeWarps = 4;
+constexpr int kPair = 2;        // tiles of a stage
 constexpr float kUp = 6.0f, kMost = 14.0f;  // see the kernel's c
 
+// A launch is one list of pairs of tiles: segments in order, of each its units
+// (row tile, key head; heads fastest) in order, of each its keys.  The list is cut
+// into equal shares, one to a warp: the end of a unit, whole units, the start of one.
 struct Kv4Seg {
-  int64_t q_row0;      // first query row
-  int64_t score_base;  // first score (weights wanted)
+  int64_t q_row0;     // first query row
+  int64_t score_base; // first score (weights wanted)
+  int64_t pair_base;  // first pair of the list
   int32_t q_len, k_len;
-  int32_t n_parts;     // parts that each head's keys are cut into
-  int32_t item_base;   // first work item: (part * row tiles + row tile) * kv_heads + head
-  int32_t part_base;   // first partial (partials wanted)
-  int32_t row_base;    // first of the rows (head, row) that have partials
-  int32_t key_base;    // first block of keys whose weights are summed
+  int32_t row_base;   // first of its rows (head, row)
+  int32_t key_base;   // first block of keys whose weights are summed
   int32_t table_row;
+  int32_t unit_base;  // first unit
 };
 
 struct Kv4Params {
@@ -67,21 +68,52 @@ struct Kv4Params {
   float* weights;  // or null
   int64_t q_tok, q_head, o_tok, o_head;  // strides in values
   int64_t w_seg, w_head;
+  int64_t n_pairs, share;  // pairs of the list, of a share (of the first `longer` shares one more)
+  int32_t longer, n_shares;
+  int32_t n_units, unit_warps;  // unit_warps > 0: a CTA of so many warps takes a whole unit
   int32_t group;
-  int32_t tile_rows;       // rows of a row tile
-  int32_t part_pairs;      // pairs of tiles of a part
-  float scale_log2;        // softmax scale times log2(e) and the keys' scale
+  int32_t tile_rows;  // rows of a row tile
+  float scale_log2;   // softmax scale times log2(e) and the keys' scale
   float decay;
-  int32_t n_segs, n_items, n_rows, n_blocks;
-  float* part_o;    // [partials][tile_rows][head_dim]
-  float2* part_ml;  // [partials][tile_rows]: (exponent of the weights' unit, sum)
-  float* lse2;      // [n_rows], log2 domain (weights wanted)
+  int32_t n_segs, n_rows, n_blocks;  // rows (head, row), blocks of keys to sum
+  float* part_o;    // [share][its first unit, its last][tile_rows][head_dim]
+  float2* part_ml;  // [share][2][tile_rows]: (exponent of the weights' unit, sum)
+  float* lse2;      // [rows] of whole units, log2 domain (weights wanted)
   float* scores;    // log2 domain (weights wanted)
   Kv4Seg segs[kKv4MaxSegs];
 };
 
+// a share's first pair, and the share that has pair x of the list
+__device__ __forceinline__ int64_t share_start(const Kv4Params& P, int share) { return share * P.share + min(share, P.longer); }
+__device__ __forceinline__ int share_of(const Kv4Params& P, int64_t x) {
+  const int64_t y = P.longer * (P.share + 1);
+  if (P.n_pairs >> 32) return (int)(x < y ? x / (P.share + 1) : P.longer + (x - y) / P.share);
+  const uint32_t d = (uint32_t)P.share + (x < y ? 1 : 0);
+  return x < y ? (uint32_t)x / d : P.longer + (uint32_t)(x - y) / d;
+}
+
+__device__ __forceinline__ int seg_pairs(const Kv4Seg& S) {
+  return max(1, (S.k_len + kPair * kKv4Tile - 1) / (kPair * kKv4Tile));
+}
+
+// The shares first .. last that have a part of a unit whose pairs start at x0, and
+// where the rows of a share's part lie.
+struct Kv4Parts {
+  int64_t x0;
+  int first, last;
+};
+__device__ __forceinline__ Kv4Parts parts_of(const Kv4Params& P, const Kv4Seg& S, int unit) {
+  if (P.unit_warps > 0) return Kv4Parts{0, 0, 0};  // whole units
+  const int pairs = seg_pairs(S);
+  const int64_t x0 = S.pair_base + (int64_t)unit * pairs;
+  return Kv4Parts{x0, share_of(P, x0), share_of(P, x0 + pairs - 1)};
+}
+__device__ __forceinline__ int64_t part_row(const Kv4Params& P, const Kv4Parts& u, int share) {
+  return (2 * (int64_t)share + (share_start(P, share) < u.x0 ? 1 : 0)) * P.tile_rows;
+}
+
 template <typename F>
-__device__ __forceinline__ int find_seg(const Kv4Params& P, int x, F base) {
+__device__ __forceinline__ int find_seg(const Kv4Params& P, int64_t x, F base) {
   int lo = 0, hi = P.n_segs - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -90,6 +122,9 @@ __device__ __forceinline__ int find_seg(const Kv4Params& P, int x, F base) {
   }
   return lo;
 }
+
+// a row's log-sum-exp in the log2 domain: -inf where it saw nothing
+__device__ __forceinline__ float lse2_of(float unit, float sum) { return sum == 0.0f ? -INFINITY : unit + log2f(sum); }
 
 __device__ __forceinline__ int score_pitch(int k_len) { return (k_len + 3) & ~3; }
 
@@ -116,16 +151,19 @@ __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t by
 }
 
 constexpr int kStages = 3;
-constexpr int kPair = 2;  // tiles of a stage
 
-template <int D, int NT>
-struct Kv4Smem {
+// One CTA fills a multiprocessor's registers: 16 warps, or 8 where a warp holds
+// more rows or pieces.
+__host__ __device__ constexpr int kv4_warps(int NT, bool F32) { return NT == 1 && !F32 ? 16 : 8; }
+
+template <int D>
+struct alignas(128) Kv4Smem {  // a warp's
   union {
-    uint8_t ring[kWarps][kStages][kPair * Kv4Tile<D>::kBytes];
-    float o[kWarps][NT * 8][D];  // once the ring is done with
+    uint8_t ring[kStages][kPair * Kv4Tile<D>::kBytes];
+    float o[16][D];  // its rows, for the CTA's other warps (once the ring is done with)
   };
-  float2 ml[kWarps][NT * 8];
-  uint64_t bar[kWarps][kStages];
+  uint64_t bar[kStages];
+  float2 ml[16];
 };
 
 // The keys of a tile as the lane's share of fragments: keys g and g + 8, dims
@@ -159,75 +197,99 @@ struct Kv4Keys {
   }
 };
 
-// NT: tiles of 8 query rows; F32: fp32 queries and outputs
-template <int D, int NT, bool F32>
-__global__ void __launch_bounds__(kWarps * 32, NT == 1 && !F32 ? 4 : 2) kv4_attend_kernel(const __grid_constant__ Kv4Params P) {
-  pdl_start();
+// NT: tiles of 8 query rows; F32: fp32 queries and outputs; UNIT: a CTA's warps
+// share one unit and join their states in shared memory
+template <int D, int NT, bool F32, bool UNIT>
+__global__ void __launch_bounds__(kv4_warps(NT, F32) * 32, 1) kv4_attend_kernel(const __grid_constant__ Kv4Params P) {
+  pdl_launch();
   using L = Kv4Tile<D>;
   extern __shared__ __align__(128) uint8_t smem_raw[];
-  Kv4Smem<D, NT>& sm = *reinterpret_cast<Kv4Smem<D, NT>*>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  Kv4Smem<D>& sm = reinterpret_cast<Kv4Smem<D>*>(smem_raw)[warp];
   constexpr int kPieces = F32 ? 2 : 1;
   constexpr int KS = D / 16;  // steps of 16 dims
-
-  // ---- the work item ----
-  const int seg = find_seg(P, blockIdx.x, [](const Kv4Seg& s) { return s.item_base; });
-  const Kv4Seg& S = P.segs[seg];
-  const int n_rows = S.q_len * P.group, row_tiles = (n_rows + P.tile_rows - 1) / P.tile_rows;
-  int r = blockIdx.x - S.item_base;
-  const int slot = S.part_base + r;
-  const int head = r % P.c.kv_heads;
-  r /= P.c.kv_heads;
-  const int row0 = r % row_tiles * P.tile_rows, part = r / row_tiles;
-  const int rows = min(P.tile_rows, n_rows - row0);
-  const int pos0 = S.k_len - S.q_len + row0 / P.group;  // the first row's place
-  // keys that some row sees (may be < 1); where scores are kept, every key has one
-  const int seen = P.scores ? S.k_len : S.k_len - S.q_len + (row0 + rows - 1) / P.group + 1;
-  // pairs of tiles a + warp, + kWarps, ... below b
-  const int a = part * P.part_pairs;
-  const int b = min((max(seen, 0) + kPair * kKv4Tile - 1) / (kPair * kKv4Tile), a + P.part_pairs);
-  const int n_my = b > a + warp ? (b - a - warp + kWarps - 1) / kWarps : 0;
-
-  // ---- the ring ----
-  uint64_t* bar = sm.bar[warp];
-  if (lane < kStages) mbar_init(&bar[lane], 1);
+  const int share = warp * gridDim.x + blockIdx.x;
+  if (!UNIT && share >= P.n_shares) return pdl_wait();
+  if (lane < kStages) mbar_init(&sm.bar[lane], 1);
   mbar_fence_init();
   __syncwarp();
-  // Page ids of 16 of the warp's pairs, and of the next 16: lane 2i + j has the
-  // one of tile j of pair i (a pair in one page has two equal ones).  A tile
-  // behind the segment's last one is never looked up: its pair is in one page,
-  // or it is not copied.
-  const int last = (S.k_len - 1) / kKv4Tile;
-  auto ids_from = [&](int i) {
-    const int tile = kPair * (a + warp + kWarps * (i + (lane >> 1))) + (lane & 1);
-    return i + (lane >> 1) < n_my ? kv4_page(P.c, S.table_row, min(tile, last)) : 0;
+
+  // ---- the ring ----
+  int seg, n_my;  // the first pair's segment, pairs
+  int64_t x_first;
+  if constexpr (UNIT) {
+    seg = find_seg(P, blockIdx.x, [](const Kv4Seg& s) { return s.unit_base; });
+    const int pairs = seg_pairs(P.segs[seg]), warps = blockDim.x >> 5;
+    const int first = (int)((int64_t)pairs * warp / warps);
+    n_my = (int)((int64_t)pairs * (warp + 1) / warps) - first;
+    x_first = P.segs[seg].pair_base + (int64_t)(blockIdx.x - P.segs[seg].unit_base) * pairs + first;
+  } else {
+    x_first = share_start(P, share);
+    n_my = (int)(share_start(P, share + 1) - x_first);
+    seg = find_seg(P, x_first, [](const Kv4Seg& s) { return s.pair_base; });
+  }
+  auto unit_of = [&](const Kv4Seg& S, int pairs, int64_t x) {
+    const int64_t off = x - S.pair_base;
+    return off >> 32 ? (int)(off / pairs) : (int)((uint32_t)off / (uint32_t)pairs);
   };
-  int ids = ids_from(0), ids_next = ids_from(16);
-  auto issue = [&](int i, int stage) {
-    if (i > 0 && (i & 15) == 0) {
-      ids = ids_next;
-      ids_next = ids_from(i + 16);
-    }
-    // (a bad page: page 0, flagged)
-    const int id0 = max(__shfl_sync(0xffffffffu, ids, 2 * (i & 15)), 0);
-    const int id1 = max(__shfl_sync(0xffffffffu, ids, 2 * (i & 15) + 1), 0);
-    const int tile = kPair * (a + warp + kWarps * i);
-    if (lane == 0) {
-      uint64_t* mb = &bar[stage];
-      uint8_t* dst = sm.ring[warp][stage];
-      const uint8_t* src = P.c.pages + kv4_tile_offset<D>(P.c, id0, head, tile);
-      if (P.c.page_shift > 0) {  // both tiles in one page
-        mbar_arrive_expect_tx(mb, kPair * L::kBytes);
-        bulk_g2s(dst, src, kPair * L::kBytes, mb);
-      } else {
-        mbar_arrive_expect_tx(mb, (tile < last ? kPair : 1) * L::kBytes);
-        bulk_g2s(dst, src, L::kBytes, mb);
-        if (tile < last) bulk_g2s(dst + L::kBytes, P.c.pages + kv4_tile_offset<D>(P.c, id1, head, tile + 1), L::kBytes, mb);
-      }
-    }
+  // Places of 16 of the share's pairs, and of the next 16: lane 2i + j has the one
+  // of tile j of pair i.  (-1: no such tile; a bad page, which is flagged: page 0)
+  int ahead = seg;
+  auto places_from = [&](int i) -> int64_t {
+    i += lane >> 1;
+    if (i >= n_my) return -1;
+    const int64_t x = x_first + i;
+    while (ahead + 1 < P.n_segs && P.segs[ahead + 1].pair_base <= x) ++ahead;
+    const Kv4Seg& S = P.segs[ahead];
+    const int pairs = seg_pairs(S), unit = unit_of(S, pairs, x);
+    const int tile = kPair * (int)(x - S.pair_base - (int64_t)unit * pairs) + (lane & 1);
+    if (tile * kKv4Tile >= S.k_len) return -1;
+    return kv4_tile_offset<D>(P.c, max(kv4_page(P.c, S.table_row, tile), 0), unit % P.c.kv_heads, tile);
   };
+  pdl_wait();
+  int64_t places = places_from(0), places_next = places_from(16);
   int issued = 0;
-  for (; issued < min(kStages, n_my); ++issued) issue(issued, issued);
+  auto issue = [&](int to) {
+    if (issued > 0 && (issued & 15) == 0) {
+      places = places_next;
+      places_next = places_from(issued + 16);
+    }
+    const int64_t p0 = __shfl_sync(0xffffffffu, places, 2 * (issued & 15));
+    const int64_t p1 = __shfl_sync(0xffffffffu, places, 2 * (issued & 15) + 1);
+    ++issued;
+    if (lane != 0) return;
+    uint64_t* mb = &sm.bar[to];
+    uint8_t* dst = sm.ring[to];
+    if (p0 < 0) {  // (a segment without tokens)
+      mbar_arrive(mb);
+    } else if (P.c.page_shift > 0) {  // both tiles in one page
+      mbar_arrive_expect_tx(mb, kPair * L::kBytes);
+      bulk_g2s(dst, P.c.pages + p0, kPair * L::kBytes, mb);
+    } else {
+      mbar_arrive_expect_tx(mb, (p1 < 0 ? 1 : kPair) * L::kBytes);
+      bulk_g2s(dst, P.c.pages + p0, L::kBytes, mb);
+      if (p1 >= 0) bulk_g2s(dst + L::kBytes, P.c.pages + p1, L::kBytes, mb);
+    }
+  };
+  while (issued < min(kStages, n_my)) issue(issued);
+
+  int stage = 0, phase = 0;  // of the pair that is read next
+  int done = 0;
+#pragma unroll 1
+  do {  // (a share has a pair at least; a CTA's warp may have none of its unit)
+  // ---- a part: the share's keys of a unit ----
+  if (!UNIT)
+    while (seg + 1 < P.n_segs && P.segs[seg + 1].pair_base <= x_first + done) ++seg;
+  const Kv4Seg& S = P.segs[seg];
+  const int pairs = seg_pairs(S), unit = UNIT ? blockIdx.x - S.unit_base : unit_of(S, pairs, x_first + done);
+  const int a = (int)(x_first + done - S.pair_base - (int64_t)unit * pairs);  // the part's pairs of the unit: a .. b - 1
+  const int b = min(pairs, a + (n_my - done));
+  const bool first_unit = done == 0, whole_unit = b - a == pairs;
+  done += b - a;
+  const int n_rows = S.q_len * P.group;
+  const int head = unit % P.c.kv_heads, row0 = unit / P.c.kv_heads * P.tile_rows;
+  const int rows = min(P.tile_rows, n_rows - row0);
+  const int pos0 = S.k_len - S.q_len + row0 / P.group;  // the first row's place
 
   // ---- queries: row 8n + g, dims D / 4 * t .. as fp16 pieces ----
   constexpr int vb = F32 ? 4 : 2;
@@ -298,15 +360,18 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && !F32 ? 4 : 2) kv4_atte
   if (P.scores) scores = P.scores + S.score_base + ((int64_t)head * n_rows + row0) * pitch;
 
   // ---- pairs of tiles ----
-  int stage = 0, phase = 0;
 #pragma unroll 1
-  for (int i = 0; i < n_my; ++i) {
-    if (!warp_wait(&bar[stage], phase, P.c.err)) {  // (flagged) the copies on their way, then the end
-      for (int j = i + 1; j < issued; ++j) warp_wait(&bar[j % kStages], j / kStages & 1, P.c.err);
+  for (int i = a; i < b; ++i) {
+    if (!warp_wait(&sm.bar[stage], phase, P.c.err)) {  // (flagged) the copies on their way, then the end
+      for (int j = done - b + i + 1; j < issued; ++j) {
+        if (++stage == kStages) stage = 0, phase ^= 1;
+        warp_wait(&sm.bar[stage], phase, P.c.err);
+      }
+      if (!UNIT) return;
       break;
     }
-    const uint8_t* ring = sm.ring[warp][stage];
-    const int u0 = (a + warp + kWarps * i) * kPair * kKv4Tile;
+    const uint8_t* ring = sm.ring[stage];
+    const int u0 = i * kPair * kKv4Tile;
     float s[kPair][NT][4];  // [2i + c]: key g + 8i of the tile, row 8n + 2t + c
 #pragma unroll
     for (int y = 0; y < kPair; ++y) {
@@ -466,147 +531,249 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && !F32 ? 4 : 2) kv4_atte
       }
     }
     __syncwarp();  // the pair is read
-    if (issued < n_my) issue(issued++, stage);
+    if (issued < n_my) issue(stage);
     if (++stage == kStages) stage = 0, phase ^= 1;
   }
 
-  // ---- the warps' states into one ----
-  __syncthreads();  // every warp's ring is done with (and no copy on its way)
+  // ---- the part's rows: dims D / 8 * g and on of rows 8n + 2t, + 1 ----
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
+      float sum = l[n][e];
 #pragma unroll
-      for (int off = 4; off < 32; off <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], off);
-      const int row = 8 * n + 2 * t + e;
-      // the exponent of the weights' unit (-inf: the row saw nothing)
-      if (g == 0) sm.ml[warp][row] = make_float2(l[n][e] == 0.0f ? -INFINITY : -c[n][e], l[n][e]);
+      for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+      const float m = sum == 0.0f ? -INFINITY : -c[n][e];  // the exponent of the weights' unit
+      const int row = 8 * n + 2 * t + e, gr = row0 + row;
+      float y[D / 8];
 #pragma unroll
-      for (int x = 0; x < D / 16; ++x)  // dims D / 8 * g + 2x, + 1
-        *reinterpret_cast<float2*>(&sm.o[warp][row][L::kChunk * g + 2 * x]) = make_float2(o[n][x][e], o[n][x][2 + e]);
+      for (int x = 0; x < D / 16; ++x) y[2 * x] = o[n][x][e], y[2 * x + 1] = o[n][x][2 + e];
+      if constexpr (UNIT) {
+#pragma unroll
+        for (int x = 0; x < D / 8; x += 4)
+          *reinterpret_cast<float4*>(&sm.o[row][L::kChunk * g + x]) = make_float4(y[x], y[x + 1], y[x + 2], y[x + 3]);
+        if (g == 0) sm.ml[row] = make_float2(m, sum);
+        continue;
+      }
+      if (row >= rows) continue;
+      if (!whole_unit) {
+        const int64_t pr = (2 * (int64_t)share + (first_unit ? 0 : 1)) * P.tile_rows + row;
+#pragma unroll
+        for (int x = 0; x < D / 8; x += 4)
+          *reinterpret_cast<float4*>(P.part_o + pr * D + L::kChunk * g + x) = make_float4(y[x], y[x + 1], y[x + 2], y[x + 3]);
+        if (g == 0) P.part_ml[pr] = make_float2(m, sum);
+        continue;
+      }
+      const float inv = sum > 0.0f ? P.c.v_scale / sum : sum == 0.0f ? 0.0f : sum;  // (a NaN stays one)
+      const int64_t tok = S.q_row0 + gr / P.group;
+      const int h = head * P.group + gr % P.group;
+      const int64_t at = tok * P.o_tok + h * P.o_head + L::kChunk * g;
+#pragma unroll
+      for (int x = 0; x < D / 8; x += 8) {
+        if constexpr (F32) {
+          *reinterpret_cast<float4*>(P.out + 4 * (at + x)) = make_float4(y[x] * inv, y[x + 1] * inv, y[x + 2] * inv, y[x + 3] * inv);
+          *reinterpret_cast<float4*>(P.out + 4 * (at + x + 4)) =
+              make_float4(y[x + 4] * inv, y[x + 5] * inv, y[x + 6] * inv, y[x + 7] * inv);
+        } else {
+          *reinterpret_cast<uint4*>(P.out + 2 * (at + x)) =
+              make_uint4(pack_bf16(y[x] * inv, y[x + 1] * inv), pack_bf16(y[x + 2] * inv, y[x + 3] * inv),
+                         pack_bf16(y[x + 4] * inv, y[x + 5] * inv), pack_bf16(y[x + 6] * inv, y[x + 7] * inv));
+        }
+      }
+      if (g == 0) {
+        const float z = lse2_of(m, sum);
+        if (P.lse) P.lse[tok * (P.c.kv_heads * P.group) + h] = z * 0.69314718055994531f;
+        if (P.lse2) P.lse2[S.row_base + head * n_rows + gr] = z;
+      }
     }
-  __syncthreads();
-  for (int i = threadIdx.x; i < rows * (D / 4); i += kWarps * 32) {
-    const int row = i / (D / 4), c = 4 * (i % (D / 4));
-    float mx = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < kWarps; ++k) mx = fmaxf(mx, sm.ml[k][row].x);
-    const float base = mx == -INFINITY ? 0.0f : mx;
-    float sum = 0.0f;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int k = 0; k < kWarps; ++k) {
-      const float2 ml = sm.ml[k][row];
-      const float f = ex2f(ml.x - base);
-      const float4 y = *reinterpret_cast<const float4*>(&sm.o[k][row][c]);
-      sum = fmaf(ml.y, f, sum);
-      x.x = fmaf(y.x, f, x.x);
-      x.y = fmaf(y.y, f, x.y);
-      x.z = fmaf(y.z, f, x.z);
-      x.w = fmaf(y.w, f, x.w);
-    }
-    if (S.n_parts > 1) {
-      const int64_t pr = (int64_t)slot * P.tile_rows + row;
-      *reinterpret_cast<float4*>(P.part_o + pr * D + c) = x;
-      if (c == 0) P.part_ml[pr] = make_float2(mx, sum);
-      continue;
-    }
-    const float inv = sum > 0.0f ? P.c.v_scale / sum : sum == 0.0f ? 0.0f : sum;  // (a NaN stays one)
-    const int gr = row0 + row;
-    const int64_t tok = S.q_row0 + gr / P.group;
-    const int h = head * P.group + gr % P.group;
-    const int64_t at = tok * P.o_tok + h * P.o_head + c;
-    if constexpr (F32)
-      *reinterpret_cast<float4*>(P.out + 4 * at) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
-    else
-      *reinterpret_cast<uint2*>(P.out + 2 * at) = make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
-    if (c == 0) {
-      const float z = sum == 0.0f ? -INFINITY : mx + log2f(sum);
-      if (P.lse) P.lse[tok * (P.c.kv_heads * P.group) + h] = z * 0.69314718055994531f;
-      if (P.lse2) P.lse2[S.row_base + head * n_rows + gr] = z;
+  if constexpr (UNIT) {
+    __syncthreads();
+    const Kv4Smem<D>* all = reinterpret_cast<const Kv4Smem<D>*>(smem_raw);
+    const int warps = blockDim.x >> 5;
+    for (int i = threadIdx.x; i < rows * (D / 4); i += blockDim.x) {
+      const int row = i / (D / 4), x = 4 * (i % (D / 4)), gr = row0 + row;
+      float mx = -INFINITY;
+      for (int k = 0; k < warps; ++k) mx = fmaxf(mx, all[k].ml[row].x);
+      const float base = mx == -INFINITY ? 0.0f : mx;
+      float sum = 0.0f;
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int k = 0; k < warps; ++k) {
+        const float2 ml = all[k].ml[row];
+        const float f = ex2f(ml.x - base);
+        const float4 z = *reinterpret_cast<const float4*>(&all[k].o[row][x]);
+        sum = fmaf(ml.y, f, sum);
+        y.x = fmaf(z.x, f, y.x), y.y = fmaf(z.y, f, y.y), y.z = fmaf(z.z, f, y.z), y.w = fmaf(z.w, f, y.w);
+      }
+      const float inv = sum > 0.0f ? P.c.v_scale / sum : sum == 0.0f ? 0.0f : sum;  // (a NaN stays one)
+      const int64_t tok = S.q_row0 + gr / P.group;
+      const int h = head * P.group + gr % P.group;
+      const int64_t at = tok * P.o_tok + h * P.o_head + x;
+      if constexpr (F32)
+        *reinterpret_cast<float4*>(P.out + 4 * at) = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+      else
+        *reinterpret_cast<uint2*>(P.out + 2 * at) = make_uint2(pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv));
+      if (x == 0) {
+        const float z = lse2_of(mx, sum);
+        if (P.lse) P.lse[tok * (P.c.kv_heads * P.group) + h] = z * 0.69314718055994531f;
+        if (P.lse2) P.lse2[S.row_base + head * n_rows + gr] = z;
+      }
     }
   }
+  } while (!UNIT && done < n_my);
 }
 
-// One warp per row (head, row) of a segment whose keys were cut: out = sum_s
-// 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s, parts in order.
+// What is left once every part is done, in one launch.  The first CTAs merge the
+// rows (head, row) of segments whose keys were cut: out = sum_s
+// 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s.  The others sum the
+// weights of kWeightKeys keys of a segment and head, rows in order (the same sums
+// on every run), from the rows' log-sum-exps, which each works out of the parts'
+// (unit, sum)s; a row that saw nothing gives none.
+constexpr int kFinishThreads = 512;  // at most (of a merging CTA)
+constexpr int kWeightThreads = 128, kWeightKeys = 4 * kWeightThreads;
+
+// the state (unit, sum, outputs) of `from` joins the one of `to`
+__device__ __forceinline__ void join_state(float& m, float& l, float4& o, float fm, float fl, float4 fo) {
+  const float mx = fmaxf(m, fm), base = mx == -INFINITY ? 0.0f : mx;
+  const float a = ex2f(m - base), b = ex2f(fm - base);
+  m = mx;
+  l = l * a + fl * b;
+  o = make_float4(o.x * a + fo.x * b, o.y * a + fo.y * b, o.z * a + fo.z * b, o.w * a + fo.w * b);
+}
+
+// `slices` groups of D / 4 threads merge row `id`, each every slices-th part: one
+// group of a CTA's several, or the whole CTA.
 template <int D, bool F32>
-__global__ void __launch_bounds__(kMergeWarps * 32) kv4_merge_kernel(const __grid_constant__ Kv4Params P) {
-  pdl_start();
-  const int lane = threadIdx.x & 31, id = blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
-  if (id >= P.n_rows) return;
+__device__ void kv4_merge_row(const Kv4Params& P, int id, int slices) {
+  constexpr int kLanes = D / 4, kMost = kFinishThreads / kLanes, kAtOnce = 8;
+  __shared__ float4 so[kMost][kLanes];
+  __shared__ float2 sml[kMost];
+  const int slice = slices > 1 ? threadIdx.x / kLanes : 0, lane = threadIdx.x % kLanes;
   const int seg = find_seg(P, id, [](const Kv4Seg& s) { return s.row_base; });
   const Kv4Seg& S = P.segs[seg];
-  if (S.n_parts <= 1) return;
-  const int n_rows = S.q_len * P.group, row_tiles = (n_rows + P.tile_rows - 1) / P.tile_rows;
+  const int n_rows = S.q_len * P.group;
   const int head = (id - S.row_base) / n_rows, gr = (id - S.row_base) % n_rows;
-  const int64_t step = (int64_t)row_tiles * P.c.kv_heads;  // partials of a part
-  const int64_t slot0 = S.part_base + (int64_t)(gr / P.tile_rows) * P.c.kv_heads + head;
-  constexpr int V = D / 32;
-  float m = -INFINITY, l = 0.0f, acc[V];
+  const Kv4Parts u = parts_of(P, S, gr / P.tile_rows * P.c.kv_heads + head);
+  pdl_wait();
+  if (u.first == u.last) return;  // the unit's warp wrote the outputs
+  float m = -INFINITY, l = 0.0f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c0 = u.first + slice; c0 <= u.last; c0 += kAtOnce * slices) {
+    float2 ml[kAtOnce];
+    float4 o[kAtOnce];
 #pragma unroll
-  for (int i = 0; i < V; ++i) acc[i] = 0.0f;
-#pragma unroll 4
-  for (int s = 0; s < S.n_parts; ++s) {
-    const int64_t pr = (slot0 + s * step) * P.tile_rows + gr % P.tile_rows;
-    const float2 ml = P.part_ml[pr];
-    float x[V];
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int c = c0 + i * slices;
+      ml[i] = make_float2(-INFINITY, 0.0f);
+      o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (c > u.last) continue;
+      const int64_t r = part_row(P, u, c) + gr % P.tile_rows;
+      ml[i] = P.part_ml[r];
+      o[i] = *reinterpret_cast<const float4*>(P.part_o + r * D + 4 * lane);
+    }
+    float mx = m;
 #pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = P.part_o[pr * D + lane * V + i];
-    const float mx = fmaxf(m, ml.x);
-    const float base = mx == -INFINITY ? 0.0f : mx;
-    const float fa = ex2f(m - base), fb = ex2f(ml.x - base);
-    l = l * fa + ml.y * fb;
-#pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = acc[i] * fa + x[i] * fb;
+    for (int i = 0; i < kAtOnce; ++i) mx = fmaxf(mx, ml[i].x);
+    const float base = mx == -INFINITY ? 0.0f : mx, f = ex2f(m - base);
     m = mx;
+    l *= f;
+    acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const float g = ex2f(ml[i].x - base);
+      l = fmaf(ml[i].y, g, l);
+      acc = make_float4(fmaf(o[i].x, g, acc.x), fmaf(o[i].y, g, acc.y), fmaf(o[i].z, g, acc.z), fmaf(o[i].w, g, acc.w));
+    }
+  }
+  if (slices > 1) {
+    so[slice][lane] = acc;
+    if (lane == 0) sml[slice] = make_float2(m, l);
+    __syncthreads();
+    if (slice != 0) return;
+    for (int i = 1; i < slices; ++i) join_state(m, l, acc, sml[i].x, sml[i].y, so[i][lane]);
   }
   const float inv = l > 0.0f ? P.c.v_scale / l : l == 0.0f ? 0.0f : l;
   const int64_t tok = S.q_row0 + gr / P.group;
   const int h = head * P.group + gr % P.group;
-  const int64_t at = tok * P.o_tok + h * P.o_head + lane * V;
-#pragma unroll
-  for (int i = 0; i < V; i += 2) {
-    if constexpr (F32)
-      *reinterpret_cast<float2*>(P.out + 4 * (at + i)) = make_float2(acc[i] * inv, acc[i + 1] * inv);
-    else
-      *reinterpret_cast<uint32_t*>(P.out + 2 * (at + i)) = pack_bf16(acc[i] * inv, acc[i + 1] * inv);
-  }
-  if (lane == 0) {
-    const float z = l == 0.0f ? -INFINITY : m + log2f(l);
-    if (P.lse) P.lse[tok * (P.c.kv_heads * P.group) + h] = z * 0.69314718055994531f;
-    if (P.lse2) P.lse2[id] = z;
-  }
+  const int64_t at = tok * P.o_tok + h * P.o_head + 4 * lane;
+  if constexpr (F32)
+    *reinterpret_cast<float4*>(P.out + 4 * at) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+  else
+    *reinterpret_cast<uint2*>(P.out + 2 * at) = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  if (lane == 0 && P.lse) P.lse[tok * (P.c.kv_heads * P.group) + h] = lse2_of(m, l) * 0.69314718055994531f;
 }
 
-// A CTA sums the weights of kWeightKeys keys of a segment and head, rows in
-// order (the same sum on every run); a row that saw nothing gives none.
-constexpr int kWeightThreads = 128, kWeightKeys = 4 * kWeightThreads;
-__global__ void __launch_bounds__(kWeightThreads) kv4_weights_kernel(const __grid_constant__ Kv4Params P) {
-  pdl_start();
-  const int seg = find_seg(P, blockIdx.x, [](const Kv4Seg& s) { return s.key_base; });
+// The weights of kWeightKeys keys, by kWeightThreads threads.
+__device__ void kv4_weights_block(const Kv4Params& P, int block) {
+  __shared__ float z[kMaxRows];  // the rows' log-sum-exps, log2 domain
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int seg = find_seg(P, block, [](const Kv4Seg& s) { return s.key_base; });
   const Kv4Seg& S = P.segs[seg];
-  const int r = blockIdx.x - S.key_base, head = r % P.c.kv_heads;
+  const int r = block - S.key_base, head = r % P.c.kv_heads;
   const int t0 = r / P.c.kv_heads * kWeightKeys + 4 * threadIdx.x;
   const int n_rows = S.q_len * P.group, pitch = score_pitch(S.k_len);
-  if (t0 >= S.k_len) return;
   const float* s = P.scores + S.score_base + (int64_t)head * n_rows * pitch + t0;
-  const float* z = P.lse2 + S.row_base + head * n_rows;
+  const bool in = t0 < S.k_len;
+  pdl_wait();
+  float4 x[4];  // the first rows' scores are on their way while the sums are worked out
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (in && i < n_rows) x[i] = *reinterpret_cast<const float4*>(s + (int64_t)i * pitch);
+  for (int row = warp; row < n_rows; row += kWeightThreads / 32) {
+    const Kv4Parts u = parts_of(P, S, row / P.tile_rows * P.c.kv_heads + head);
+    if (u.first == u.last) {
+      if (lane == 0) z[row] = P.lse2[S.row_base + head * n_rows + row];
+      continue;
+    }
+    float m = -INFINITY, l = 0.0f;
+    for (int c = u.first + lane; c <= u.last; c += 32) {
+      const float2 y = P.part_ml[part_row(P, u, c) + row % P.tile_rows];
+      const float mx = fmaxf(m, y.x), base = mx == -INFINITY ? 0.0f : mx;
+      l = l * ex2f(m - base) + y.y * ex2f(y.x - base);
+      m = mx;
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+      const float fm = __shfl_xor_sync(0xffffffffu, m, off), fl = __shfl_xor_sync(0xffffffffu, l, off);
+      const float mx = fmaxf(m, fm), base = mx == -INFINITY ? 0.0f : mx;
+      // (both lanes of a pair add the same two terms: in the same order)
+      const float a = l * ex2f(m - base), b = fl * ex2f(fm - base);
+      l = a + b;
+      m = mx;
+    }
+    if (lane == 0) z[row] = lse2_of(m, l);
+  }
+  __syncthreads();
+  if (!in) return;
   float w[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-  for (int i = 0; i < n_rows; ++i) {
-    const float4 x = *reinterpret_cast<const float4*>(s + (int64_t)i * pitch);
-    const float y = z[i];
-    if (y == -INFINITY) continue;
-    w[0] += ex2f(x.x - y);
-    w[1] += ex2f(x.y - y);
-    w[2] += ex2f(x.z - y);
-    w[3] += ex2f(x.w - y);
+  for (int i0 = 0; i0 < n_rows; i0 += 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i0 > 0 && i0 + i < n_rows) x[i] = *reinterpret_cast<const float4*>(s + (int64_t)(i0 + i) * pitch);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i0 + i >= n_rows || z[i0 + i] == -INFINITY) continue;
+      const float y = z[i0 + i];
+      w[0] += ex2f(x[i].x - y);
+      w[1] += ex2f(x[i].y - y);
+      w[2] += ex2f(x[i].z - y);
+      w[3] += ex2f(x[i].w - y);
+    }
   }
   float* out = P.weights + S.table_row * P.w_seg + head * P.w_head + t0;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     if (t0 + i < S.k_len) out[i] = P.decay == 0.0f ? w[i] : fmaf(P.decay, out[i], w[i]);
+}
+
+template <int D, bool F32>
+__global__ void __launch_bounds__(kFinishThreads) kv4_finish_kernel(const __grid_constant__ Kv4Params P, int n_merge, int slices) {
+  pdl_launch();  // (the wait follows in both parts)
+  if ((int)blockIdx.x >= n_merge) return kv4_weights_block(P, blockIdx.x - n_merge);
+  if (slices > 1) return kv4_merge_row<D, F32>(P, blockIdx.x, slices);  // (the whole CTA)
+  const int id = blockIdx.x * (kWeightThreads / (D / 4)) + threadIdx.x / (D / 4);
+  if (id < P.n_rows) kv4_merge_row<D, F32>(P, id, 1);
+  else pdl_wait();
 }
 
 // ---- host -------------------------------------------------------------------
@@ -647,12 +814,36 @@ int check_args(const kvpool_kv4_args* a, int32_t n, const int64_t* q_len, const 
   return KVPOOL_OK;
 }
 
-constexpr int64_t kMinPairs = 8;  // pairs of tiles of a part, at least
+constexpr int64_t kMinPairs = 2;  // of a share
 
 // Where a launch's workspace lies, in bytes from its start.
 struct Space {
   int64_t part_ml, lse2, scores, total;
 };
+
+// Which form is the quicker one: a CTA of 4, 8 or 16 warps for every unit (no
+// merging launch; the answer), or equal shares (0).  Times in us, fitted to 34
+// batches of equal and of ragged lengths, of 16 to 524,288 tokens: a round (one
+// pair to each warp of a multiprocessor) takes 0.55 us and 1/16 more for each
+// warp, a wave of unit CTAs 3.5 beside its rounds, shares 8.5 and up to 0.004 for
+// every row to merge.  (152 requests of 256 tokens, 4 key heads: 8.9 us as units,
+// 13.9 as shares; 32 of 4,096 18.7 and 22.2; 256 of 1 to 2,048 43.6 and 51; 32 of
+// 1 to 8,192 30.4 and 23.2; one of 16,384 55 and 12.4.)
+int unit_warps(int64_t units, int64_t most_pairs, int64_t pairs, int64_t rows, int64_t shares, int n_sms, int64_t warps_per_sm) {
+  auto round_us = [](double warps) { return 0.55 + 0.0625 * warps; };
+  const double rounds = (double)pairs / (double)shares;
+  double best = 8.5 + rounds * round_us(std::min((double)warps_per_sm, (double)shares / n_sms) + 3.0) +
+                0.004 * (double)rows * std::min(1.0, rounds / 8);
+  int answer = 0;
+  for (int w = 4; w <= warps_per_sm; w *= 2) {
+    const double waves = (double)units * w / (double)(n_sms * warps_per_sm);
+    const double round = round_us((double)std::min<int64_t>(warps_per_sm, (units + n_sms - 1) / n_sms * w));
+    const double longest = (double)((most_pairs + w - 1) / w) * round + 3.5, mean = (double)pairs / (double)units / w * round + 3.5;
+    const double t = 0.5 + (waves > 1.0 ? waves * mean + 0.5 * longest : longest);
+    if (t < best) best = t, answer = w;
+  }
+  return answer;
+}
 
 // Segments [i0, n) of one launch (at most kKv4MaxSegs that are no prompts);
 // returns the next segment, or -1 (too large for one launch).
@@ -660,72 +851,58 @@ int32_t plan(const kvpool_kv4_args* a, int32_t i0, int32_t n, const int64_t* q_l
              int n_sms, Kv4Params* P, Space* w) {
   const int hk = a->cache.kv_heads, group = a->q.heads / hk;
   int32_t i = i0;
-  int64_t row = *q_row, most_rows = 0;
+  int64_t row = *q_row, most_rows = 0, rows = 0, blocks = 0, scores = 0;
   P->n_segs = 0;
   for (; i < n && P->n_segs < kKv4MaxSegs; ++i) {
     if (q_len[i] > 0 && !is_prompt(a, q_len[i])) {
       Kv4Seg& S = P->segs[P->n_segs++];
-      S = Kv4Seg{};
       S.q_row0 = row;
       S.q_len = (int32_t)q_len[i];
       S.k_len = (int32_t)k_len[i];
       S.table_row = i - i0;
+      S.row_base = (int32_t)rows;
+      S.key_base = (int32_t)blocks;
+      S.score_base = scores;
       most_rows = std::max(most_rows, q_len[i] * group);
+      rows += q_len[i] * group * hk;
+      if (a->d_weights) {
+        blocks += (k_len[i] + kWeightKeys - 1) / kWeightKeys * hk;
+        scores += q_len[i] * group * hk * ((k_len[i] + 3) & ~3);
+      }
     }
     row += q_len[i];
   }
+  if (rows + blocks > (1 << 30)) return -1;
   *q_row = row;
   P->tile_rows = most_rows <= 8 ? 8 : 16;
-  auto row_tiles = [&](const Kv4Seg& S) { return ((int64_t)S.q_len * group + P->tile_rows - 1) / P->tile_rows; };
-  auto pairs = [&](const Kv4Seg& S) {
-    return std::max<int64_t>(1, ((int64_t)S.k_len + kPair * kKv4Tile - 1) / (kPair * kKv4Tile));
-  };
-  auto items = [&](int64_t part) {
-    int64_t x = 0;
-    for (int s = 0; s < P->n_segs; ++s) {
-      const Kv4Seg& S = P->segs[s];
-      x += (pairs(S) + part - 1) / part * row_tiles(S) * hk;
-    }
-    return x;
-  };
-  // the shortest parts that are one wave of CTAs together
-  const int64_t want = (int64_t)n_sms * (P->tile_rows == 8 && a->dtype == KVPOOL_BF16 ? 4 : 2);
-  int64_t lo = kMinPairs, hi = kMinPairs;
-  while (hi < (1 << 26) && items(hi) > want) hi *= 2;
-  while (lo < hi) {
-    const int64_t mid = (lo + hi) / 2;
-    if (items(mid) <= want) hi = mid;
-    else lo = mid + 1;
-  }
-  P->part_pairs = (int32_t)lo;
-  int64_t item = 0, partials = 0, rows = 0, blocks = 0, scores = 0;
-  bool cut = false;
+  P->n_pairs = 0;
+  int64_t n_units = 0;
+  int most = 1;
   for (int s = 0; s < P->n_segs; ++s) {
     Kv4Seg& S = P->segs[s];
-    const int64_t parts = (pairs(S) + lo - 1) / lo, its = parts * row_tiles(S) * hk;
-    S.n_parts = (int32_t)parts;
-    S.item_base = (int32_t)item;
-    S.part_base = (int32_t)partials;
-    S.row_base = (int32_t)rows;
-    S.key_base = (int32_t)blocks;
-    S.score_base = scores;
-    item += its;
-    if (parts > 1) partials += its, cut = true;
-    rows += (int64_t)S.q_len * group * hk;
-    if (a->d_weights) {
-      blocks += ((int64_t)S.k_len + kWeightKeys - 1) / kWeightKeys * hk;
-      scores += (int64_t)S.q_len * group * hk * ((S.k_len + 3) & ~3);
-    }
+    S.pair_base = P->n_pairs;
+    S.unit_base = (int32_t)n_units;
+    const int units = (S.q_len * group + P->tile_rows - 1) / P->tile_rows * hk;
+    const int pairs = std::max(1, (S.k_len + kPair * kKv4Tile - 1) / (kPair * kKv4Tile));
+    n_units += units;
+    most = std::max(most, pairs);
+    P->n_pairs += (int64_t)units * pairs;
   }
-  if (item > (1 << 30) || partials > (1 << 30) || rows > (1 << 30) || blocks > (1 << 30)) return -1;
-  P->n_items = (int32_t)item;
+  P->n_units = (int32_t)n_units;
+  // a share to each warp that the GPU holds, of kMinPairs pairs at least
+  const int64_t warps = (int64_t)n_sms * kv4_warps(P->tile_rows / 8, a->dtype == KVPOOL_F32);
+  P->n_shares = (int32_t)std::max<int64_t>(1, std::min(warps, P->n_pairs / kMinPairs));
+  P->share = P->n_pairs / P->n_shares;
+  if (P->share > (1 << 30)) return -1;
+  P->longer = (int32_t)(P->n_pairs % P->n_shares);
+  P->unit_warps = unit_warps(P->n_units, most, P->n_pairs, rows, P->n_shares, n_sms, warps / n_sms);
   P->n_rows = (int32_t)rows;
   P->n_blocks = (int32_t)blocks;
-  w->part_ml = partials * P->tile_rows * a->cache.head_dim * 4;
-  w->lse2 = w->part_ml + partials * P->tile_rows * 8;
+  const int64_t parts = P->unit_warps == 0 && P->n_shares > 1 ? 2 * (int64_t)P->n_shares * P->tile_rows : 0;
+  w->part_ml = parts * a->cache.head_dim * 4;
+  w->lse2 = w->part_ml + parts * 8;
   w->scores = w->lse2 + (a->d_weights ? (rows * 4 + 15) / 16 * 16 : 0);
   w->total = w->scores + 4 * scores;
-  if (!cut) w->part_ml = -1;
   return i;
 }
 
@@ -788,23 +965,78 @@ bool window_call(const kvpool_kv4_args* a, const Run& run, const int64_t* q_len,
   return true;
 }
 
+template <int D, int NT, bool F32, bool UNIT>
+cudaError_t launch_attend(const Kv4Params& P, int n_sms, cudaStream_t s) {
+  constexpr int smem = (int)sizeof(Kv4Smem<D>);  // of a warp
+  auto* kern = kv4_attend_kernel<D, NT, F32, UNIT>;
+  static std::atomic<uint64_t> told;  // the devices (of 64) that know of the kernel's shared memory
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && !(told.load(std::memory_order_relaxed) >> dev & 1)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem * kv4_warps(NT, F32));
+    if (e == cudaSuccess) told.fetch_or(1ull << dev, std::memory_order_relaxed);
+  }
+  if (e != cudaSuccess) return e;
+  // neighbouring shares go to different multiprocessors: few of them still use all
+  const int ctas = UNIT ? P.n_units : std::min(n_sms, P.n_shares);
+  const int warps = UNIT ? P.unit_warps : (P.n_shares + ctas - 1) / ctas;
+  return launch_kernel(true, kern, dim3(ctas), dim3(warps * 32), smem * warps, s, P);
+}
 template <int D, int NT, bool F32>
-cudaError_t launch_attend(const Kv4Params& P, cudaStream_t s) {
-  constexpr int smem = (int)sizeof(Kv4Smem<D, NT>);
-  auto* kern = kv4_attend_kernel<D, NT, F32>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  return e == cudaSuccess ? launch_kernel(true, kern, dim3(P.n_items), dim3(kWarps * 32), smem, s, P) : e;
+cudaError_t launch_form(const Kv4Params& P, int n_sms, cudaStream_t s) {
+  return P.unit_warps > 0 ? launch_attend<D, NT, F32, true>(P, n_sms, s) : launch_attend<D, NT, F32, false>(P, n_sms, s);
 }
 
 template <int D, bool F32>
-cudaError_t launch_all(const Kv4Params& P, bool cut, cudaStream_t s) {
-  cudaError_t e = P.tile_rows == 8 ? launch_attend<D, 1, F32>(P, s) : launch_attend<D, 2, F32>(P, s);
-  if (e == cudaSuccess && cut)
-    e = launch_kernel(true, kv4_merge_kernel<D, F32>, dim3((P.n_rows + kMergeWarps - 1) / kMergeWarps), dim3(kMergeWarps * 32),
-                      0, s, P);
-  if (e == cudaSuccess && P.n_blocks > 0)
-    e = launch_kernel(true, kv4_weights_kernel, dim3(P.n_blocks), dim3(kWeightThreads), 0, s, P);
+cudaError_t launch_all(const Kv4Params& P, int n_sms, cudaStream_t s) {
+  cudaError_t e = P.tile_rows == 8 ? launch_form<D, 1, F32>(P, n_sms, s) : launch_form<D, 2, F32>(P, n_sms, s);
+  const bool parts = P.unit_warps == 0 && P.n_shares > 1;
+  auto* kern = kv4_finish_kernel<D, F32>;
+  int n_merge = 0;
+  // A row of a unit in n parts takes n / slices / 8 loads' latencies: rows of few parts, or too many rows for one
+  // wave of CTAs, go four or eight to a CTA, others take a CTA of 128 or 512 threads each (512 rows of 19 parts: 28.5
+  // us a call with 512 threads, 23.5 with 128)
+  constexpr int kRows = kWeightThreads / (D / 4);  // or slices of 128 threads
+  int slices = 1;
+  if (parts && P.n_shares / 16 >= P.n_units && P.n_rows <= n_sms) {
+    if (e == cudaSuccess)
+      e = launch_kernel(true, kern, dim3(P.n_rows), dim3(kFinishThreads), 0, s, P, P.n_rows, kFinishThreads / (D / 4));
+  } else if (parts) {
+    slices = P.n_shares / 6 >= P.n_units && P.n_rows <= 8 * n_sms ? kRows : 1;
+    n_merge = slices > 1 ? P.n_rows : (P.n_rows + kRows - 1) / kRows;
+  }
+  if (e == cudaSuccess && n_merge + P.n_blocks > 0)
+    e = launch_kernel(true, kern, dim3(n_merge + P.n_blocks), dim3(kWeightThreads), 0, s, P, n_merge, slices);
   return e;
+}
+
+}  // namespace
+}  // namespace kvp
+
+namespace kvp {
+namespace {
+
+// Bytes that the call's launches take, one after the other (a negative error code).
+int64_t space_of(const kvpool_kv4_args* a, int32_t n, const int64_t* q_len, const int64_t* k_len, int n_sms, Kv4Params* P) {
+  Space w;
+  int64_t row = 0, most = 0;
+  for (int32_t i = 0; i < n;) {
+    i = plan(a, i, n, q_len, k_len, &row, n_sms, P, &w);
+    if (i < 0) return KVPOOL_ERR_INVALID_ARG;
+    most = std::max(most, w.total);
+  }
+  Run run;
+  row = 0;
+  for (int32_t i = 0; next_run(a, &i, &row, n, q_len, k_len, &run);) {
+    WindowCall call;
+    if (!window_call(a, run, q_len, k_len, nullptr, &call)) return KVPOOL_ERR_INVALID_ARG;
+    call.args.k.data = call.args.v.data = reinterpret_cast<const void*>((uintptr_t)16);  // (sizes only)
+    const int64_t x = kvpool_window_workspace(&call.args, run.end - run.first, q_len + run.first, call.start.get(),
+                                              call.len.get());
+    if (x < 0) return x;
+    most = std::max(most, 2 * run.bytes + x);
+  }
+  return most;
 }
 
 }  // namespace
@@ -812,33 +1044,14 @@ cudaError_t launch_all(const Kv4Params& P, bool cut, cudaStream_t s) {
 
 extern "C" int64_t kvpool_kv4_workspace(const kvpool_kv4_args* a, int32_t n, const int64_t* h_q_len, const int64_t* h_k_len) {
   using namespace kvp;
-  int64_t total = 0, most = 0;
+  int64_t total = 0;
   const int rc = check_args(a, n, h_q_len, h_k_len, &total);
   if (rc != KVPOOL_OK) return rc;
   if (total == 0) return 0;
   const OpsDevice* dev = ops_device();
   if (!dev) return KVPOOL_ERR_CUDA;
   std::unique_ptr<Kv4Params> P(new (std::nothrow) Kv4Params);
-  if (!P) return KVPOOL_ERR_INVALID_ARG;
-  Space w;
-  int64_t row = 0;
-  for (int32_t i = 0; i < n;) {
-    i = plan(a, i, n, h_q_len, h_k_len, &row, dev->sms, P.get(), &w);
-    if (i < 0) return KVPOOL_ERR_INVALID_ARG;
-    most = std::max(most, w.total);
-  }
-  Run run;
-  row = 0;
-  for (int32_t i = 0; next_run(a, &i, &row, n, h_q_len, h_k_len, &run);) {
-    WindowCall call;
-    if (!window_call(a, run, h_q_len, h_k_len, nullptr, &call)) return KVPOOL_ERR_INVALID_ARG;
-    call.args.k.data = call.args.v.data = reinterpret_cast<const void*>((uintptr_t)16);  // (sizes only)
-    const int64_t x = kvpool_window_workspace(&call.args, run.end - run.first, h_q_len + run.first, call.start.get(),
-                                              call.len.get());
-    if (x < 0) return x;
-    most = std::max(most, 2 * run.bytes + x);
-  }
-  return most;
+  return P ? space_of(a, n, h_q_len, h_k_len, dev->sms, P.get()) : KVPOOL_ERR_INVALID_ARG;
 }
 
 extern "C" int kvpool_kv4_attend(const kvpool_kv4_args* a, int32_t n, const int64_t* h_q_len, const int64_t* h_k_len,
@@ -850,14 +1063,19 @@ extern "C" int kvpool_kv4_attend(const kvpool_kv4_args* a, int32_t n, const int6
   if (!rows_same(a->out, a->q, total) &&
       rows_meet(a->out, total, a->q, total, a->cache.head_dim, a->dtype == KVPOOL_BF16 ? 2 : 4))
     return KVPOOL_ERR_INVALID_ARG;
-  const int64_t need = kvpool_kv4_workspace(a, n, h_q_len, h_k_len);
-  if (need < 0) return (int)need;
-  if (need > 0 && (!d_workspace || workspace_bytes < need || reinterpret_cast<uintptr_t>(d_workspace) % 16 != 0))
-    return KVPOOL_ERR_INVALID_ARG;
   const OpsDevice* dev = ops_device();
   if (!dev) return KVPOOL_ERR_CUDA;
   std::unique_ptr<Kv4Params> P(new (std::nothrow) Kv4Params);
   if (!P) return KVPOOL_ERR_INVALID_ARG;
+  Space w;
+  int64_t row = 0;
+  int32_t next = plan(a, 0, n, h_q_len, h_k_len, &row, dev->sms, P.get(), &w);
+  bool whole = next == n;  // one launch is the whole call
+  for (int32_t i = 0; whole && i < n; ++i) whole = !is_prompt(a, h_q_len[i]);
+  const int64_t need = whole ? w.total : space_of(a, n, h_q_len, h_k_len, dev->sms, P.get());
+  if (need < 0) return (int)need;
+  if (need > 0 && (!d_workspace || workspace_bytes < need || reinterpret_cast<uintptr_t>(d_workspace) % 16 != 0))
+    return KVPOOL_ERR_INVALID_ARG;
   uint8_t* space = static_cast<uint8_t*>(d_workspace);
   P->q = static_cast<const uint8_t*>(a->q.data);
   P->out = static_cast<uint8_t*>(const_cast<void*>(a->out.data));
@@ -872,26 +1090,25 @@ extern "C" int kvpool_kv4_attend(const kvpool_kv4_args* a, int32_t n, const int6
   P->scale_log2 = a->scale * 1.4426950408889634f * a->cache.k_scale;
   P->decay = a->decay;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  Space w;
-  int64_t row = 0;
+  row = 0;
   for (int32_t i = 0; i < n;) {
     const int32_t first = i;
-    i = plan(a, i, n, h_q_len, h_k_len, &row, dev->sms, P.get(), &w);
+    i = whole ? n : plan(a, i, n, h_q_len, h_k_len, &row, dev->sms, P.get(), &w);
     if (P->n_segs == 0) continue;
     P->c = kv4_cache(&a->cache, first, dev->err);
     P->weights = a->d_weights ? a->d_weights + first * a->weight_stride : nullptr;
     P->part_o = reinterpret_cast<float*>(space);
-    P->part_ml = reinterpret_cast<float2*>(space + std::max<int64_t>(w.part_ml, 0));
+    P->part_ml = reinterpret_cast<float2*>(space + w.part_ml);
     P->lse2 = a->d_weights ? reinterpret_cast<float*>(space + w.lse2) : nullptr;
     P->scores = a->d_weights ? reinterpret_cast<float*>(space + w.scores) : nullptr;
-    const bool cut = w.part_ml >= 0, f32 = a->dtype == KVPOOL_F32;
-    const cudaError_t e = a->cache.head_dim == 128 ? (f32 ? launch_all<128, true>(*P, cut, s) : launch_all<128, false>(*P, cut, s))
-                                                   : (f32 ? launch_all<64, true>(*P, cut, s) : launch_all<64, false>(*P, cut, s));
+    const bool f32 = a->dtype == KVPOOL_F32;
+    const cudaError_t e = a->cache.head_dim == 128 ? (f32 ? launch_all<128, true>(*P, dev->sms, s) : launch_all<128, false>(*P, dev->sms, s))
+                                                   : (f32 ? launch_all<64, true>(*P, dev->sms, s) : launch_all<64, false>(*P, dev->sms, s));
     if (e != cudaSuccess) return KVPOOL_ERR_CUDA;
   }
   Run run;
   row = 0;
-  for (int32_t i = 0; next_run(a, &i, &row, n, h_q_len, h_k_len, &run);) {
+  for (int32_t i = 0; !whole && next_run(a, &i, &row, n, h_q_len, h_k_len, &run);) {
     WindowCall call;
     if (!window_call(a, run, h_q_len, h_k_len, space, &call)) return KVPOOL_ERR_INVALID_ARG;
     const int32_t m = run.end - run.first;
