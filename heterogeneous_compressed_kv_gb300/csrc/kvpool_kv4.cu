@@ -64,14 +64,16 @@ __device__ __forceinline__ MoveTask move_task(const MoveParams& P, int task) {
   return t;
 }
 
-// 8 values of a row, in fp32
+// 8 values of a row as loaded
 template <int T>
-__device__ __forceinline__ void load8(const uint8_t* p, float* x) {
-  if constexpr (T == KVPOOL_F32) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-  } else {
-    const uint4 r = *reinterpret_cast<const uint4*>(p);
+struct Raw8;
+template <>
+struct Raw8<KVPOOL_BF16> {
+  uint4 r;
+  __device__ __forceinline__ void load(const uint8_t* p, bool in) {
+    r = in ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void get(float* x) const {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -79,7 +81,18 @@ __device__ __forceinline__ void load8(const uint8_t* p, float* x) {
       x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     }
   }
-}
+};
+template <>
+struct Raw8<KVPOOL_F32> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const uint8_t* p, bool in) {
+    a = b = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (in) a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void get(float* x) const {
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  }
+};
 template <int T>
 __device__ __forceinline__ void store8(uint8_t* p, const float* x) {
   if constexpr (T == KVPOOL_F32) {
@@ -99,28 +112,44 @@ __device__ __forceinline__ void store8(uint8_t* p, const float* x) {
 // Eight codes (nibble i of the result: value i) of half a group, and the group's
 // scale; the other half is with the neighbouring lane.  A NaN or an infinity
 // makes the scale NaN: the whole group reads back as NaN.
-__device__ __forceinline__ uint32_t quantize8(float* x, float inv_scale, uint32_t& s) {
+template <int T>
+__device__ __forceinline__ uint32_t quantize8(const Raw8<T>& raw, float inv_scale, uint32_t& s) {
+  float x[8];
+  raw.get(x);
   uint32_t amax = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    x[i] *= inv_scale;  // a power of two
-    amax = max(amax, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-  }
+  for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(x[i]) & 0x7FFFFFFFu);
   amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-  if (amax >= 0x7F800000u) {
+  const float top = __uint_as_float(amax) * inv_scale;  // (a power of two)
+  if (!(top < INFINITY)) {
     s = 0x7F;
     return 0;
   }
-  s = f32x2_to_e4m3x2(__fdiv_rn(__uint_as_float(amax), 6.0f), 0.0f) & 0xFFu;
+  s = f32x2_to_e4m3x2(__fdiv_rn(top, 6.0f), 0.0f) & 0xFFu;
   if (s == 0) return 0;
   const float f = e4m3x2_to_f32x2((uint16_t)s).x;
-  // The fp32 quotient stands for x / s here: it lies on a border between two
-  // codes only where x / s does (x and border * s are fp32 numbers, so unequal
-  // ones differ by more than the quotient's rounding).
   uint32_t c = 0;
+  if constexpr (T == KVPOOL_F32) {
+    // The fp32 quotient stands for x / s: it lies on a border between two codes
+    // only where x / s does (x and border * s are fp32 numbers, so unequal ones
+    // differ by more than the quotient's rounding).
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    c |= (uint32_t)f32x2_to_e2m1x2(__fdiv_rn(x[2 * i], f), __fdiv_rn(x[2 * i + 1], f)) << (8 * i);
+    for (int i = 0; i < 4; ++i)
+      c |= (uint32_t)f32x2_to_e2m1x2(__fdiv_rn(x[2 * i] * inv_scale, f), __fdiv_rn(x[2 * i + 1] * inv_scale, f)) << (8 * i);
+  } else {
+    // A bf16 number is border * s (7 bits) or at least 2^-8 of it away, so a
+    // product with the reciprocal (off by 2^-24 of it) rounded to a multiple of
+    // 2^-11 (borders are multiples of 0.25 up to 5) is the border where x / s is, and
+    // on x / s's side of it elsewhere; what is beyond 6 stays there.  (With quotients
+    // 6,144 tokens of 16 heads x 128 took 30.9 us instead of SPEED.)
+    const float r = __frcp_rn(f) * inv_scale;
+    constexpr float kGrid = 6144.0f;  // 1.5 * 2^12: a sum with it is a multiple of 2^-11
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float q0 = __fadd_rn(__fmaf_rn(x[2 * i], r, kGrid), -kGrid), q1 = __fadd_rn(__fmaf_rn(x[2 * i + 1], r, kGrid), -kGrid);
+      c |= (uint32_t)f32x2_to_e2m1x2(q0, q1) << (8 * i);
+    }
+  }
   return c;
 }
 
@@ -131,7 +160,8 @@ __device__ __forceinline__ uint32_t nibbles_to_bytes(uint32_t x) {
   return (x | (x << 4)) & 0x0F0F0F0Fu;
 }
 
-// A warp takes a tile of one head: the lanes of a row hold 8 dims each.
+// A warp takes a tile of one head: the lanes of a row hold 8 dims each.  All of
+// its loads are on their way before the first is needed.
 template <int T, int D>
 __global__ void __launch_bounds__(kWarps * 32) kv4_store_kernel(const __grid_constant__ MoveParams P) {
   pdl_start();
@@ -142,49 +172,59 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_store_kernel(const __grid_con
   if (t.off < 0) return;
   uint8_t* tile = P.c.pages + t.off;
   constexpr int kLanes = D / 8, kPer = 32 / kLanes;  // lanes of a row, rows at a time
+  constexpr int kK = kKv4Tile / kPer, kV = kKv4Tile / 2 / kPer;  // steps over the keys, the pairs of values
   constexpr int vb = T == KVPOOL_F32 ? 4 : 2;
   const int sub = lane / kLanes, l = lane % kLanes;
   const uint8_t* k = P.k + t.row * P.k_tok + t.head * P.k_head + 8 * vb * l;
   const uint8_t* v = P.v + t.row * P.v_tok + t.head * P.v_head + 8 * vb * l;
   const float k_inv = 1.0f / P.c.k_scale, v_inv = 1.0f / P.c.v_scale;
+  Raw8<T> rk[kK], rv[kV][2];
 #pragma unroll
-  for (int it = 0; it < kKv4Tile / kPer; ++it) {
+  for (int it = 0; it < kK; ++it) {
+    const int r = it * kPer + sub;
+    rk[it].load(k + r * P.k_tok, r >= t.lo && r < t.hi);
+  }
+#pragma unroll
+  for (int it = 0; it < kV; ++it)
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      const int r = 2 * (it * kPer + sub) + y;
+      rv[it][y].load(v + r * P.v_tok, r >= t.lo && r < t.hi);
+    }
+#pragma unroll
+  for (int it = 0; it < kK; ++it) {
     const int r = it * kPer + sub;
     const bool in = r >= t.lo && r < t.hi;
     if (!__any_sync(0xffffffffu, in)) continue;
-    float x[8] = {};
-    if (in) load8<T>(k + r * P.k_tok, x);
     uint32_t s;
-    const uint32_t c = quantize8(x, k_inv, s);
+    const uint32_t c = quantize8<T>(rk[it], k_inv, s);
     if (in) {
       *reinterpret_cast<uint32_t*>(tile + r * (D / 2) + 4 * l) = c;
       if (l % 2 == 0) tile[L::kKs + r * (D / kKv4Group) + l / 2] = (uint8_t)s;
     }
   }
 #pragma unroll
-  for (int it = 0; it < kKv4Tile / 2 / kPer; ++it) {
+  for (int it = 0; it < kV; ++it) {
     const int j = it * kPer + sub, r = 2 * j;
     const bool in0 = r >= t.lo && r < t.hi, in1 = r + 1 >= t.lo && r + 1 < t.hi;
     if (!__any_sync(0xffffffffu, in0 || in1)) continue;
-    float x0[8] = {}, x1[8] = {};
-    if (in0) load8<T>(v + r * P.v_tok, x0);
-    if (in1) load8<T>(v + (r + 1) * P.v_tok, x1);
     uint32_t s0, s1;
-    const uint32_t c0 = quantize8(x0, v_inv, s0), c1 = quantize8(x1, v_inv, s1);
+    const uint32_t c0 = quantize8<T>(rv[it][0], v_inv, s0), c1 = quantize8<T>(rv[it][1], v_inv, s1);
     if (!in0 && !in1) continue;
     const int chunk = 8 * l / L::kChunk, at = 8 * l % L::kChunk;
     uint2* p = reinterpret_cast<uint2*>(tile + L::kV + j * D + (chunk ^ kv4_swizzle<D>(j)) * L::kChunk + at);
     uint2 w = make_uint2(nibbles_to_bytes(c0) | nibbles_to_bytes(c1) << 4,
                          nibbles_to_bytes(c0 >> 16) | nibbles_to_bytes(c1 >> 16) << 4);
-    if (!in0 || !in1) {  // the pair's other token stays
+    uint8_t* sc = tile + L::kVs + j * (D / 8) + l / 2 * 2;
+    if (in0 && in1) {
+      *p = w;
+      if (l % 2 == 0) *reinterpret_cast<uint16_t*>(sc) = (uint16_t)(s0 | s1 << 8);
+    } else {  // the pair's other token stays
       const uint32_t mine = in0 ? 0x0F0F0F0Fu : 0xF0F0F0F0u;
       const uint2 old = *p;
-      w = make_uint2((w.x & mine) | (old.x & ~mine), (w.y & mine) | (old.y & ~mine));
+      *p = make_uint2((w.x & mine) | (old.x & ~mine), (w.y & mine) | (old.y & ~mine));
+      if (l % 2 == 0) sc[in0 ? 0 : 1] = (uint8_t)(in0 ? s0 : s1);
     }
-    *p = w;
-    uint8_t* sc = tile + L::kVs + j * (D / 8) + l / 2 * 2;
-    if (l % 2 == 0 && in0) sc[0] = (uint8_t)s0;
-    if (l % 2 == 0 && in1) sc[1] = (uint8_t)s1;
   }
 }
 
@@ -204,21 +244,35 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_load_kernel(const __grid_cons
   const bool bad = t.off < 0;  // reads as zeros
   const uint8_t* tile = P.c.pages + (bad ? 0 : t.off);
   constexpr int kLanes = D / 8, kPer = 32 / kLanes;
+  constexpr int kK = kKv4Tile / kPer, kV = kKv4Tile / 2 / kPer;
   constexpr int vb = T == KVPOOL_F32 ? 4 : 2;
   const int sub = lane / kLanes, l = lane % kLanes;
   uint8_t* k = const_cast<uint8_t*>(P.k) + t.row * P.k_tok + t.head * P.k_head + 8 * vb * l;
   uint8_t* v = const_cast<uint8_t*>(P.v) + t.row * P.v_tok + t.head * P.v_head + 8 * vb * l;
+  uint32_t kc[kK], ks[kK], vs[kV];
+  uint2 vc[kV];
 #pragma unroll
-  for (int it = 0; it < kKv4Tile / kPer; ++it) {
+  for (int it = 0; it < kK; ++it) {
+    const int r = it * kPer + sub;
+    kc[it] = bad ? 0 : *reinterpret_cast<const uint32_t*>(tile + r * (D / 2) + 4 * l);
+    ks[it] = bad ? 0 : tile[L::kKs + r * (D / kKv4Group) + l / 2];
+  }
+#pragma unroll
+  for (int it = 0; it < kV; ++it) {
+    const int j = it * kPer + sub, chunk = 8 * l / L::kChunk, at = 8 * l % L::kChunk;
+    vc[it] = make_uint2(0, 0);
+    vs[it] = 0;
+    if (bad) continue;
+    vc[it] = *reinterpret_cast<const uint2*>(tile + L::kV + j * D + (chunk ^ kv4_swizzle<D>(j)) * L::kChunk + at);
+    vs[it] = *reinterpret_cast<const uint16_t*>(tile + L::kVs + j * (D / 8) + l / 2 * 2);
+  }
+#pragma unroll
+  for (int it = 0; it < kK; ++it) {
     const int r = it * kPer + sub;
     if (r < t.lo || r >= t.hi) continue;
-    uint32_t c = 0, s = 0, h[4];
-    if (!bad) {
-      c = *reinterpret_cast<const uint32_t*>(tile + r * (D / 2) + 4 * l);
-      s = tile[L::kKs + r * (D / kKv4Group) + l / 2];
-    }
-    const uint32_t s2 = e4m3x2_to_f16x2((uint16_t)(s | s << 8));
-    e2m1x8_to_f16x2x4(c, h);
+    uint32_t h[4];
+    const uint32_t s2 = e4m3x2_to_f16x2((uint16_t)(ks[it] | ks[it] << 8));
+    e2m1x8_to_f16x2x4(kc[it], h);
     float x[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -229,21 +283,12 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_load_kernel(const __grid_cons
     store8<T>(k + r * P.k_tok, x);
   }
 #pragma unroll
-  for (int it = 0; it < kKv4Tile / 2 / kPer; ++it) {
-    const int j = it * kPer + sub, r = 2 * j;
-    const bool in0 = r >= t.lo && r < t.hi, in1 = r + 1 >= t.lo && r + 1 < t.hi;
-    if (!in0 && !in1) continue;
-    uint2 w = make_uint2(0, 0);
-    uint32_t s = 0;
-    if (!bad) {
-      const int chunk = 8 * l / L::kChunk, at = 8 * l % L::kChunk;
-      w = *reinterpret_cast<const uint2*>(tile + L::kV + j * D + (chunk ^ kv4_swizzle<D>(j)) * L::kChunk + at);
-      s = *reinterpret_cast<const uint16_t*>(tile + L::kVs + j * (D / 8) + l / 2 * 2);
-    }
-    const uint32_t s2 = e4m3x2_to_f16x2((uint16_t)s);
+  for (int it = 0; it < kV; ++it) {
+    const int r = 2 * (it * kPer + sub);
+    const uint32_t s2 = e4m3x2_to_f16x2((uint16_t)vs[it]);
     uint32_t h[8];
-    e2m1x8_to_f16x2x4(w.x, h);
-    e2m1x8_to_f16x2x4(w.y, h + 4);
+    e2m1x8_to_f16x2x4(vc[it].x, h);
+    e2m1x8_to_f16x2x4(vc[it].y, h + 4);
     float x0[8], x1[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -251,8 +296,8 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_load_kernel(const __grid_cons
       x0[i] = f.x * P.c.v_scale;
       x1[i] = f.y * P.c.v_scale;
     }
-    if (in0) store8<T>(v + r * P.v_tok, x0);
-    if (in1) store8<T>(v + (r + 1) * P.v_tok, x1);
+    if (r >= t.lo && r < t.hi) store8<T>(v + r * P.v_tok, x0);
+    if (r + 1 >= t.lo && r + 1 < t.hi) store8<T>(v + (r + 1) * P.v_tok, x1);
   }
 }
 

@@ -560,14 +560,15 @@ class Kv4Cache:
             raise ValueError(f"Kv4Cache: pages must be a contiguous uint8 CUDA tensor [n_pages][{size}]")
         self.pages, self.kv_heads, self.head_dim, self.page_tokens = pages, kv_heads, head_dim, page_tokens
         self.k_scale, self.v_scale = k_scale, v_scale
-        self.index = pages.get_device()
+        self.index, self.device = pages.get_device(), pages.device
+        self._at = pages.data_ptr(), pages.shape[0]
+        self._kind = kv_heads, head_dim, page_tokens, k_scale, v_scale, 0
 
     def _pack(self, table, n: int) -> bytes:
         ptr, stride, rows, width = _table(table, "table", self.index)
         if rows < n:
             raise ValueError("the table must have a row per segment")
-        return _KV4.pack(self.pages.data_ptr(), self.pages.shape[0], ptr, stride, rows, width, self.kv_heads, self.head_dim,
-                         self.page_tokens, self.k_scale, self.v_scale, 0)
+        return _KV4.pack(*self._at, ptr, stride, rows, width, *self._kind)
 
     def _done(self, rc: int, what: str) -> None:
         if rc != OK:
@@ -588,7 +589,7 @@ class Kv4Cache:
             with torch.cuda.device(self.index):
                 return self.store(k, v, table, start, n_new, stream)
         start, n_new = self._two(start, n_new, "store")
-        self._move("kvpool_kv4_store", k, v, table, start, n_new, False, stream)
+        self._move(lib().kvpool_kv4_store, "store", k, v, table, start, n_new, False, stream)
 
     def load(self, table, start, length, dtype=None, out_k=None, out_v=None, stream=None) -> tuple:
         """(k, v): segment i's length[i] tokens from place start[i] on, as the
@@ -599,35 +600,37 @@ class Kv4Cache:
             with torch.cuda.device(self.index):
                 return self.load(table, start, length, dtype, out_k, out_v, stream)
         start, length = self._two(start, length, "load")
-        shape = (int(length.sum()) if length.size else 0, self.kv_heads, self.head_dim)
         if out_k is None or out_v is None:
-            if dtype is None:
-                o = out_k if out_k is not None else out_v
-                dtype = torch.bfloat16 if o is None else o.dtype
-            fresh = [None if o is not None else self._empty(shape, dtype, stream) for o in (out_k, out_v)]
-            out_k, out_v = out_k if out_k is not None else fresh[0], out_v if out_v is not None else fresh[1]
-        self._move("kvpool_kv4_load", out_k, out_v, table, start, length, True, stream)
+            given = out_k if out_k is not None else out_v
+            dtype = dtype if dtype is not None else torch.bfloat16 if given is None else given.dtype
+            shape = (sum(length.tolist()), self.kv_heads, self.head_dim)
+            if out_k is None:
+                out_k = self._empty(shape, dtype, stream)
+            if out_v is None:
+                out_v = self._empty(shape, dtype, stream)
+        self._move(lib().kvpool_kv4_load, "load", out_k, out_v, table, start, length, True, stream)
         return out_k, out_v
 
     def _empty(self, shape, dtype, stream):
         """A tensor whose memory belongs to the stream that will write it."""
         import torch
-        raw = _stream_of(stream, self.index)
-        if stream is None or raw == torch._C._cuda_getCurrentRawStream(self.index):
-            return torch.empty(shape, dtype=dtype, device=self.pages.device)
-        with torch.cuda.stream(torch.cuda.ExternalStream(raw, device=self.pages.device)):
-            return torch.empty(shape, dtype=dtype, device=self.pages.device)
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        raw = _stream(stream)
+        if raw == torch._C._cuda_getCurrentRawStream(self.index):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(torch.cuda.ExternalStream(raw, device=self.device)):
+            return torch.empty(shape, dtype=dtype, device=self.device)
 
-    def _move(self, name, k, v, table, start, length, out, stream) -> None:
-        if not k.is_cuda:
-            raise ValueError("k and v must be CUDA tensors")
+    def _move(self, call, what, k, v, table, start, length, out, stream) -> None:
         like = _like(k)
         if like[2] != self.index or like[1] != self.head_dim or k.shape != v.shape:
-            raise ValueError("k and v must be alike, of the cache's head dim and on its device")
-        rc = getattr(lib(), name)(self._pack(table, start.size), _dtype(k), _HEADS.pack(*_rows(k, "k", like, out)),
-                                  _HEADS.pack(*_rows(v, "v", like, out)), k.shape[0], start.size, start.tobytes(),
-                                  length.tobytes(), _stream_of(stream, self.index))
-        self._done(rc, name[7:])
+            raise ValueError("k and v must be CUDA tensors alike, of the cache's head dim and on its device")
+        rc = call(self._pack(table, start.size), _dtype(k), _HEADS.pack(*_rows(k, "k", like, out)),
+                  _HEADS.pack(*_rows(v, "v", like, out)), k.shape[0], start.size, start.tobytes(), length.tobytes(),
+                  _stream_of(stream, self.index))
+        if rc != OK:
+            self._done(rc, what)
 
     def attend(self, q, table, q_len, k_len, scale=None, out=None, lse=None, weights=None, decay: float = 1.0, workspace=None,
                stream=None):
@@ -643,13 +646,15 @@ class Kv4Cache:
         if torch._C._cuda_getDevice() != self.index:
             with torch.cuda.device(self.index):
                 return self.attend(q, table, q_len, k_len, scale, out, lse, weights, decay, workspace, stream)
-        raw = _stream_of(stream, self.index)
         if not q.is_cuda:
             raise ValueError("attend: q must be a CUDA tensor")
+        raw = _stream_of(stream, self.index)
         like = _like(q)
         rows = _rows(q, "q", like)
         if out is None:
-            out, o = _fresh(q, stream, raw)
+            n, heads, dim = q.shape
+            out = self._empty((n, heads, dim), like[0], stream)
+            o = (out.data_ptr(), heads * dim if n > 1 else 0, dim if heads > 1 else 0, heads, 0)
         else:
             o = _rows(out, "out", like, True)
         call = self._call(q, like, rows, table, q_len, k_len, scale, out, o, lse, weights, decay)
@@ -665,7 +670,8 @@ class Kv4Cache:
                 nbytes = rc
                 workspace = self._empty((rc,), torch.uint8, stream)
             rc = L.kvpool_kv4_attend(*call, workspace.data_ptr() if nbytes else None, nbytes, raw)
-        self._done(rc, "attend")
+        if rc != OK:
+            self._done(rc, "attend")
         return out
 
     def workspace(self, q, table, q_len, k_len, scale=None, weights=None) -> int:
@@ -689,7 +695,7 @@ class Kv4Cache:
         z = 0 if lse is None else _need(lse, "lse", torch.float32, q.shape[:2], self.index)
         w = (0, 0, 0)
         if weights is not None:
-            w = _weights(weights, "weights", ql.size, self.kv_heads, int(kl.max()) if kl.size else 0, self.index)
+            w = _weights(weights, "weights", ql.size, self.kv_heads, max(kl.tolist(), default=0), self.index)
         try:
             a = _KV4_ARGS.pack(_dtype(q), self.head_dim ** -0.5 if scale is None else scale, *q_rows, *out_rows, q.shape[0], z,
                                *w, decay, 0)
@@ -711,7 +717,7 @@ class Kv4Cache:
                 return self.evict(table, k_len, weights, keep, out_table, n_sink, n_recent, index, out_weights, stream)
         kl = _i64(k_len)
         n, H = kl.size, self.kv_heads
-        w = _weights(weights, "weights", n, H, int(kl.max()) if n else 0, self.index)
+        w = _weights(weights, "weights", n, H, max(kl.tolist(), default=0), self.index)
         ot = _table(out_table, "out_table", self.index)
         if index is None:
             index = self._empty((n, H, max(keep, 0)), torch.int32, stream)
