@@ -229,6 +229,12 @@ struct OpsDevice {
   uint32_t* err;  // the device error word of such calls
 };
 const OpsDevice* ops_device();
+// kvpool_window_workspace and kvpool_window_attend.  even: key lists are cut into
+// parts that fill the multiprocessors evenly (no window, long lists).
+int64_t window_space(const kvpool_window_args* a, int32_t n, const int64_t* h_q_len, const int64_t* h_k_start,
+                     const int64_t* h_k_len, bool even);
+int window_run(const kvpool_window_args* a, int32_t n, const int64_t* h_q_len, const int64_t* h_k_start,
+               const int64_t* h_k_len, bool even, void* d_workspace, int64_t workspace_bytes, void* stream);
 int attend_max_split_len();  // the longest split of a request's sources
 // the first n_entries HCA entries of every request of the launch (the same
 // blocks in all of them), cut into n_split runs: partials in the slots behind

@@ -75,7 +75,8 @@ struct Kv4Params {
   int32_t tile_rows;  // rows of a row tile
   float scale_log2;   // softmax scale times log2(e) and the keys' scale
   float decay;
-  int32_t n_segs, n_rows, n_blocks;  // rows (head, row), blocks of keys to sum
+  int32_t n_segs, n_rows, n_blocks;  // rows (head, row), blocks of keys whose weights are summed
+  int32_t turns;
   float* part_o;    // [share][its first unit, its last][tile_rows][head_dim]
   float2* part_ml;  // [share][2][tile_rows]: (exponent of the weights' unit, sum)
   float* lse2;      // [rows] of whole units, log2 domain (weights wanted)
@@ -703,22 +704,29 @@ __device__ void kv4_merge_row(const Kv4Params& P, int id, int slices) {
   if (lane == 0 && P.lse) P.lse[tok * (P.c.kv_heads * P.group) + h] = lse2_of(m, l) * 0.69314718055994531f;
 }
 
-// The weights of kWeightKeys keys, by kWeightThreads threads.
+// The weights of P.turns * kWeightKeys keys, by kWeightThreads threads.
 __device__ void kv4_weights_block(const Kv4Params& P, int block) {
   __shared__ float z[kMaxRows];  // the rows' log-sum-exps, log2 domain
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int seg = find_seg(P, block, [](const Kv4Seg& s) { return s.key_base; });
   const Kv4Seg& S = P.segs[seg];
   const int r = block - S.key_base, head = r % P.c.kv_heads;
-  const int t0 = r / P.c.kv_heads * kWeightKeys + 4 * threadIdx.x;
+  const int t0 = r / P.c.kv_heads * (P.turns * kWeightKeys) + 4 * threadIdx.x;  // and kWeightKeys on, `turns` times
   const int n_rows = S.q_len * P.group, pitch = score_pitch(S.k_len);
   const float* s = P.scores + S.score_base + (int64_t)head * n_rows * pitch + t0;
-  const bool in = t0 < S.k_len;
   pdl_wait();
-  float4 x[4];  // the first rows' scores are on their way while the sums are worked out
+  // the first rows' scores of two turns are on their way while the sums are worked out
+  float4 x[2][4];
+  auto load = [&](int turn, int i0) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (in && i < n_rows) x[i] = *reinterpret_cast<const float4*>(s + (int64_t)i * pitch);
+    for (int y = 0; y < 2; ++y)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int at = kWeightKeys * (turn + y);
+        if (turn + y < P.turns && t0 + at < S.k_len && i0 + i < n_rows) x[y][i] = *reinterpret_cast<const float4*>(s + at + (int64_t)(i0 + i) * pitch);
+      }
+  };
+  load(0, 0);
   for (int row = warp; row < n_rows; row += kWeightThreads / 32) {
     const Kv4Parts u = parts_of(P, S, row / P.tile_rows * P.c.kv_heads + head);
     if (u.first == u.last) {
@@ -744,26 +752,34 @@ __device__ void kv4_weights_block(const Kv4Params& P, int block) {
     if (lane == 0) z[row] = lse2_of(m, l);
   }
   __syncthreads();
-  if (!in) return;
-  float w[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int i0 = 0; i0 < n_rows; i0 += 4) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i0 > 0 && i0 + i < n_rows) x[i] = *reinterpret_cast<const float4*>(s + (int64_t)(i0 + i) * pitch);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (i0 + i >= n_rows || z[i0 + i] == -INFINITY) continue;
-      const float y = z[i0 + i];
-      w[0] += ex2f(x[i].x - y);
-      w[1] += ex2f(x[i].y - y);
-      w[2] += ex2f(x[i].z - y);
-      w[3] += ex2f(x[i].w - y);
-    }
-  }
   float* out = P.weights + S.table_row * P.w_seg + head * P.w_head + t0;
+#pragma unroll 1
+  for (int turn = 0; turn < P.turns && t0 + kWeightKeys * turn < S.k_len; turn += 2) {
+    float w[2][4] = {};
+#pragma unroll 1
+    for (int i0 = 0; i0 < n_rows; i0 += 4) {
+      if (turn > 0 || i0 > 0) load(turn, i0);
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (t0 + i < S.k_len) out[i] = P.decay == 0.0f ? w[i] : fmaf(P.decay, out[i], w[i]);
+      for (int i = 0; i < 4; ++i) {
+        if (i0 + i >= n_rows || z[i0 + i] == -INFINITY) continue;
+        const float lse = z[i0 + i];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          w[y][0] += ex2f(x[y][i].x - lse);
+          w[y][1] += ex2f(x[y][i].y - lse);
+          w[y][2] += ex2f(x[y][i].z - lse);
+          w[y][3] += ex2f(x[y][i].w - lse);
+        }
+      }
+    }
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int at = kWeightKeys * (turn + y) + i;
+        if (turn + y < P.turns && t0 + at < S.k_len) out[at] = P.decay == 0.0f ? w[y][i] : fmaf(P.decay, out[at], w[y][i]);
+      }
+  }
 }
 
 template <int D, bool F32>
@@ -861,12 +877,11 @@ int32_t plan(const kvpool_kv4_args* a, int32_t i0, int32_t n, const int64_t* q_l
       S.k_len = (int32_t)k_len[i];
       S.table_row = i - i0;
       S.row_base = (int32_t)rows;
-      S.key_base = (int32_t)blocks;
       S.score_base = scores;
       most_rows = std::max(most_rows, q_len[i] * group);
       rows += q_len[i] * group * hk;
       if (a->d_weights) {
-        blocks += (k_len[i] + kWeightKeys - 1) / kWeightKeys * hk;
+        blocks += (k_len[i] + kWeightKeys - 1) / kWeightKeys * hk;  // of one turn
         scores += q_len[i] * group * hk * ((k_len[i] + 3) & ~3);
       }
     }
@@ -874,6 +889,13 @@ int32_t plan(const kvpool_kv4_args* a, int32_t i0, int32_t n, const int64_t* q_l
   }
   if (rows + blocks > (1 << 30)) return -1;
   *q_row = row;
+  // a block's row sums are worth several turns where there are many keys (64 requests 19.5 us -> TURNS with four)
+  P->turns = blocks >= 16LL * n_sms ? 4 : blocks >= 8LL * n_sms ? 2 : 1;
+  blocks = 0;
+  for (int s = 0; a->d_weights && s < P->n_segs; ++s) {
+    P->segs[s].key_base = (int32_t)blocks;
+    blocks += (P->segs[s].k_len + (int64_t)P->turns * kWeightKeys - 1) / (P->turns * kWeightKeys) * hk;
+  }
   P->tile_rows = most_rows <= 8 ? 8 : 16;
   P->n_pairs = 0;
   int64_t n_units = 0;
@@ -1031,8 +1053,7 @@ int64_t space_of(const kvpool_kv4_args* a, int32_t n, const int64_t* q_len, cons
     WindowCall call;
     if (!window_call(a, run, q_len, k_len, nullptr, &call)) return KVPOOL_ERR_INVALID_ARG;
     call.args.k.data = call.args.v.data = reinterpret_cast<const void*>((uintptr_t)16);  // (sizes only)
-    const int64_t x = kvpool_window_workspace(&call.args, run.end - run.first, q_len + run.first, call.start.get(),
-                                              call.len.get());
+    const int64_t x = window_space(&call.args, run.end - run.first, q_len + run.first, call.start.get(), call.len.get(), true);
     if (x < 0) return x;
     most = std::max(most, 2 * run.bytes + x);
   }
@@ -1117,8 +1138,8 @@ extern "C" int kvpool_kv4_attend(const kvpool_kv4_args* a, int32_t n, const int6
     int rc = kv4_load_rows(&a->cache, a->dtype, call.args.k, call.args.v, m, run.first, zero.get(), call.len.get(), dev->err,
                            stream);
     if (rc != KVPOOL_OK) return rc;
-    rc = kvpool_window_attend(&call.args, m, h_q_len + run.first, call.start.get(), call.len.get(), space + 2 * run.bytes,
-                              workspace_bytes - 2 * run.bytes, stream);
+    rc = window_run(&call.args, m, h_q_len + run.first, call.start.get(), call.len.get(), true, space + 2 * run.bytes,
+                    workspace_bytes - 2 * run.bytes, stream);
     if (rc != KVPOOL_OK) return rc;
   }
   return KVPOOL_OK;

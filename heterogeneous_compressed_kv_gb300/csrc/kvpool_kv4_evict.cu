@@ -4,11 +4,11 @@
 // place), in their order.
 //
 // Two kernels.  The first finds what stays: a cluster of CTAs takes the weights of
-// one segment and key head, a slice each; four passes over 8 bits of an order-
-// keeping integer of the weight narrow the last weight that stays (histograms in
-// shared memory, added up over the cluster), a count by warp slices gives every
-// slice its first place, and the places go out in order.  The second moves the
-// tokens, a warp to a tile of 16 of them.
+// one segment and key head, a slice each, which stays in shared memory; four
+// passes over 8 bits of an order-keeping integer of the weight narrow the last
+// weight that stays (histograms in shared memory, added up over the cluster), a
+// count by warp slices gives every slice its first place, and the places go out in
+// order.  The second moves the tokens, a warp to a tile of 16 of them.
 #include <algorithm>
 #include <memory>
 #include <new>
@@ -26,6 +26,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
 constexpr int kMaxCluster = 8;
+constexpr int64_t kMaxShared = 49152;  // keys of a CTA's slice in shared memory
 constexpr int kMoveWarps = 4;
 
 struct EvictSeg {
@@ -51,8 +52,12 @@ struct EvictParams {
 // A larger weight has a larger key; -0 and +0 are alike and a NaN is the largest.
 __device__ __forceinline__ uint32_t weight_key(float w) { return w != w ? 0xFFFFFFFFu : score_key(w); }
 
+// SHARED: a CTA's slice of the weights stays in shared memory as keys (up to
+// kMaxShared of them), otherwise every pass reads it again.
+template <bool SHARED>
 __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const __grid_constant__ EvictParams P) {
   pdl_start();
+  extern __shared__ uint32_t keys[];
   __shared__ uint32_t hist[4][256];
   __shared__ uint2 counts[kSelWarps];  // (above the last weight that stays, equal to it) of a warp's slice
   __shared__ uint32_t sh_digit, sh_left;
@@ -90,20 +95,36 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const __grid_co
   const int a = min(hi, lo + (rank * kSelWarps + warp) * per), b = min(hi, a + per);
   for (int i = tid; i < 4 * 256; i += kSelThreads) (&hist[0][0])[i] = 0;
   __syncthreads();
+  uint32_t* mine_keys = keys + warp * per;  // key of weight i: [i - a]
+  auto key_at = [&](int i) { return SHARED ? mine_keys[i - a] : weight_key(w[i]); };
   uint32_t prefix = 0, left = want;
 #pragma unroll 1
   for (int pass = 0; pass < 4; ++pass) {
     const int shift = 24 - 8 * pass;
-#pragma unroll 4
-    for (int i = a + lane; i < b; i += 32) {
-      const uint32_t key = weight_key(w[i]);
-      if (pass == 0 || key >> (shift + 8) == prefix) atomicAdd(&hist[pass][key >> shift & 255], 1u);
+    // eight weights to a lane at a time
+#pragma unroll 1
+    for (int i0 = a; i0 < b; i0 += 256) {
+      uint32_t key[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int i = i0 + 32 * u + lane;
+        key[u] = i < b ? (SHARED && pass == 0 ? __float_as_uint(w[i]) : key_at(i)) : 0u;
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int i = i0 + 32 * u + lane;
+        if (i >= b) continue;
+        if (SHARED && pass == 0) mine_keys[i - a] = key[u] = weight_key(__uint_as_float(key[u]));
+        if (pass == 0 || key[u] >> (shift + 8) == prefix) atomicAdd(&hist[pass][key[u] >> shift & 255], 1u);
+      }
     }
     cluster.sync();
     // counts from the largest digit down: thread i holds digit 255 - i
     if (tid < 256) {
       uint32_t x = 0;
-      for (int r = 0; r < C; ++r) x += cluster.map_shared_rank(&hist[pass][0], r)[255 - tid];
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r)
+        if (r < C) x += cluster.map_shared_rank(&hist[pass][0], r)[255 - tid];
       uint32_t up = x;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -125,8 +146,9 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const __grid_co
   }
   // `prefix` is the key of the last weight that stays, `left` how many of those equal to it do
   uint2 mine = make_uint2(0, 0);
+#pragma unroll 8
   for (int i = a + lane; i < b; i += 32) {
-    const uint32_t key = weight_key(w[i]);
+    const uint32_t key = key_at(i);
     mine.x += key > prefix;
     mine.y += key == prefix;
   }
@@ -142,17 +164,17 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const __grid_co
   }
   above = __reduce_add_sync(0xffffffffu, above);
   equal = __reduce_add_sync(0xffffffffu, equal);
+#pragma unroll 4
   for (int i0 = a; i0 < b; i0 += 32) {
     const int i = i0 + lane;
-    const float x = i < b ? w[i] : 0.0f;
-    const uint32_t key = weight_key(x);
+    const uint32_t key = i < b ? key_at(i) : 0u;
     const uint32_t gt = __ballot_sync(0xffffffffu, i < b && key > prefix), eq = __ballot_sync(0xffffffffu, i < b && key == prefix);
     const uint32_t below = (1u << lane) - 1;
     const uint32_t e = equal + __popc(eq & below);
     if ((gt >> lane & 1) || ((eq >> lane & 1) && e < left)) {
       const int to = P.sink + above + __popc(gt & below) + min(e, left);
       index[to] = i;
-      if (ow) ow[to] = x;
+      if (ow) ow[to] = w[i];
     }
     above += __popc(gt);
     equal += __popc(eq);
@@ -204,15 +226,21 @@ __global__ void __launch_bounds__(kMoveWarps * 32) kv4_move_kernel(const __grid_
     const int sl = slot_of(r);
     k[i] = o >= 0 ? *reinterpret_cast<const uint4*>(pages + o + sl * (D / 2) + 16 * c) : make_uint4(0, 0, 0, 0);
   }
-  constexpr int G = D / kKv4Group, SI = kKv4Tile * G / 32;  // scales to a lane
-  uint8_t ks[SI], vs[SI];
+  // scales: of token `lane`'s keys (8 or 4 bytes), of pair `lane`'s values (16 or 8: two tokens' bytes alternate)
+  constexpr int G = D / kKv4Group, SW = G / 4;
+  uint32_t ks[SW], vs[2 * SW];
 #pragma unroll
-  for (int i = 0; i < SI; ++i) {
-    const int x = i * 32 + lane, r = x / G, e = x % G;
-    const int64_t o = off_of(r);
-    const int sl = slot_of(r);
-    ks[i] = o >= 0 ? pages[o + L::kKs + sl * G + e] : 0;
-    vs[i] = o >= 0 ? pages[o + L::kVs + (sl >> 1) * 2 * G + 2 * e + (sl & 1)] : 0;
+  for (int i = 0; i < SW; ++i) ks[i] = off >= 0 ? reinterpret_cast<const uint32_t*>(pages + off + L::kKs + slot * G)[i] : 0;
+  {
+    const int j = lane % 8;
+    const int64_t o0 = off_of(2 * j), o1 = off_of(2 * j + 1);
+    const int s0 = slot_of(2 * j), s1 = slot_of(2 * j + 1);
+#pragma unroll
+    for (int i = 0; i < 2 * SW; ++i) {
+      const uint32_t x = o0 >= 0 ? reinterpret_cast<const uint32_t*>(pages + o0 + L::kVs + (s0 >> 1) * 2 * G)[i] : 0;
+      const uint32_t y = o1 >= 0 ? reinterpret_cast<const uint32_t*>(pages + o1 + L::kVs + (s1 >> 1) * 2 * G)[i] : 0;
+      vs[i] = (x >> 8 * (s0 & 1) & 0x00FF00FFu) | (y >> 8 * (s1 & 1) & 0x00FF00FFu) << 8;
+    }
   }
   constexpr int VW = D / 64;  // 8-byte words of a V chunk
   uint2 v[2][VW];             // pairs lane / 8 and + 4, chunk lane % 8
@@ -240,12 +268,14 @@ __global__ void __launch_bounds__(kMoveWarps * 32) kv4_move_kernel(const __grid_
     const int x = i * 32 + lane, r = x / (D / 32), c = x % (D / 32);
     if (r < n) *reinterpret_cast<uint4*>(dst + r * (D / 2) + 16 * c) = k[i];
   }
+  if (lane < n) {
 #pragma unroll
-  for (int i = 0; i < SI; ++i) {
-    const int x = i * 32 + lane, r = x / G, e = x % G;
-    if (r >= n) continue;
-    dst[L::kKs + r * G + e] = ks[i];
-    dst[L::kVs + (r >> 1) * 2 * G + 2 * e + (r & 1)] = vs[i];
+    for (int i = 0; i < SW; ++i) reinterpret_cast<uint32_t*>(dst + L::kKs + lane * G)[i] = ks[i];
+  }
+  if (lane < 8 && 2 * lane < n) {
+    uint32_t* p = reinterpret_cast<uint32_t*>(dst + L::kVs + lane * 2 * G);
+#pragma unroll
+    for (int i = 0; i < 2 * SW; ++i) p[i] = 2 * lane + 1 < n ? vs[i] : (vs[i] & 0x00FF00FFu) | (p[i] & 0xFF00FF00u);
   }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -305,11 +335,18 @@ int check_args(const kvpool_kv4_evict_args* a, int32_t n, const int64_t* k_len, 
   return KVPOOL_OK;
 }
 
-cudaError_t launch_select(const EvictParams& P, cudaStream_t s) {
+template <bool SHARED>
+cudaError_t launch_select(const EvictParams& P, int64_t slice, cudaStream_t s) {
+  auto* kern = kv4_select_kernel<SHARED>;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(P.n_segs * P.c.kv_heads * P.cluster);
   cfg.blockDim = dim3(kSelThreads);
   cfg.stream = s;
+  if (SHARED) {
+    cfg.dynamicSmemBytes = 4 * slice;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * (int)kMaxShared);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -318,7 +355,7 @@ cudaError_t launch_select(const EvictParams& P, cudaStream_t s) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kv4_select_kernel, P);
+  return cudaLaunchKernelEx(&cfg, kern, P);
 }
 
 }  // namespace
@@ -349,6 +386,9 @@ extern "C" int kvpool_kv4_evict(const kvpool_kv4_evict_args* a, int32_t n, const
   while (P->cluster < kMaxCluster && (int64_t)std::min(n, kKv4MaxSegs) * hk * P->cluster * 2 <= 2 * dev->sms &&
          most >= 4096 * P->cluster)
     P->cluster *= 2;
+  // keys of the longest segment's slice, as the kernel cuts it
+  const int64_t warps = (int64_t)P->cluster * kSelWarps, between = std::max<int64_t>(0, most - a->n_sink - a->n_recent);
+  const int64_t slice = (((between + warps - 1) / warps + 31) & ~(int64_t)31) * kSelWarps;
   for (int32_t i = 0; i < n;) {
     const int32_t first = i;
     P->n_segs = 0;
@@ -369,7 +409,7 @@ extern "C" int kvpool_kv4_evict(const kvpool_kv4_evict_args* a, int32_t n, const
     P->w = a->d_weights + first * a->weight_stride;
     P->out_w = a->d_out_weights ? a->d_out_weights + first * a->out_weight_stride : nullptr;
     P->index = a->d_index + (int64_t)first * hk * a->keep;
-    cudaError_t e = launch_select(*P, s);
+    cudaError_t e = slice <= kMaxShared ? launch_select<true>(*P, slice, s) : launch_select<false>(*P, slice, s);
     if (e == cudaSuccess && P->n_tasks > 0) {
       const dim3 grid((unsigned)((P->n_tasks + kMoveWarps - 1) / kMoveWarps)), block(kMoveWarps * 32);
       e = a->cache.head_dim == 128 ? launch_kernel(true, kv4_move_kernel<128>, grid, block, 0, s, *P)

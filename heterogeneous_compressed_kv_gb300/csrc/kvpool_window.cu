@@ -275,10 +275,40 @@ int64_t tile_keys(const kvpool_window_args* a, int64_t q_len, int64_t k_len, int
   return std::min<int64_t>(k_len, w);
 }
 
+// Long key lists under few query tiles (no window): the length of parts, each a
+// work item, that makes k rounds of one item to every multiprocessor shortest, an
+// item taking as long as 256 keys beside its own (two prompts of 1,024 and 512
+// queries, 16 heads on 4, behind 16,000 to 33,000 tokens: 96 query tiles on 152
+// multiprocessors took 330 us whole, WINDOW in parts).
+int64_t even_part(const kvpool_window_args* a, const WinParams& P, int n_sms) {
+  auto items = [&](int64_t part) {
+    int64_t x = 0;
+    for (int s = 0; s < P.n_segs; ++s) {
+      const WinSeg& S = P.segs[s];
+      const int64_t keys = std::max<int64_t>(1, tile_keys(a, S.q_len, S.k_len, P.tile_tokens));
+      x += (int64_t)((S.q_len + P.tile_tokens - 1) / P.tile_tokens) * a->k.heads * ((keys + part - 1) / part);
+    }
+    return x;
+  };
+  const int64_t whole = items(kMaxLen);
+  int64_t best = kMaxLen, cost = INT64_MAX;
+  for (int64_t k = 1; k <= 6; ++k) {
+    if (k * n_sms < whole) continue;
+    int64_t lo = 1, hi = kMaxLen / 128;  // in steps of 128 keys
+    while (lo < hi) {
+      const int64_t mid = (lo + hi) / 2;
+      if (items(128 * mid) <= k * n_sms) hi = mid;
+      else lo = mid + 1;
+    }
+    if (k * (128 * lo + 256) < cost) cost = k * (128 * lo + 256), best = 128 * lo;
+  }
+  return best;
+}
+
 // Fill segments [i0, n) of one launch (at most kMaxWinSegs with queries);
 // returns the next segment.  A launch with few tiles cuts each tile's keys
 // into parts (merged by a second kernel) so that the GPU is filled.
-int plan_launch(const kvpool_window_args* a, Form form, bool tc, int32_t i0, int32_t n, const int64_t* q_len,
+int plan_launch(const kvpool_window_args* a, Form form, bool tc, bool even, int32_t i0, int32_t n, const int64_t* q_len,
                 const int64_t* k_start, const int64_t* k_len, int64_t q_row0, int n_sms, WinParams* P, int64_t* next_row,
                 int64_t* slots) {
   const int Hk = a->k.heads;
@@ -313,12 +343,13 @@ int plan_launch(const kvpool_window_args* a, Form form, bool tc, int32_t i0, int
   const int64_t min_keys = form == kFormTok ? 256 : form == kFormTc ? 128 : kFmaKeys;
   const int64_t want = n_sms * (form == kFormTc ? 1LL : 4LL);
   const int64_t fill = tiles == 0 ? 1 : form == kFormFma ? (want + tiles - 1) / tiles : std::max<int64_t>(1, want / tiles);
+  const int64_t part = even && form == kFormTc && tiles > 0 ? even_part(a, *P, n_sms) : 0;
   int64_t items = 0, slot = 0, merge = 0, rows = 0;
   for (int s = 0; s < P->n_segs; ++s) {
     WinSeg& S = P->segs[s];
     const int64_t st = (int64_t)((S.q_len + P->tile_tokens - 1) / P->tile_tokens) * Hk;
     const int64_t keys = tile_keys(a, S.q_len, S.k_len, P->tile_tokens);
-    const int64_t split = std::max<int64_t>(1, std::min(fill, (keys + min_keys - 1) / min_keys));
+    const int64_t split = std::max<int64_t>(1, part > 0 ? (keys + part - 1) / part : std::min(fill, (keys + min_keys - 1) / min_keys));
     S.n_split = (int32_t)split;
     S.item_base = (int32_t)items;
     S.part_base = (int32_t)slot;
@@ -406,9 +437,10 @@ const OpsDevice* ops_device() {
 
 }  // namespace kvp
 
-extern "C" int64_t kvpool_window_workspace(const kvpool_window_args* a, int32_t n, const int64_t* h_q_len,
-                                           const int64_t* h_k_start, const int64_t* h_k_len) {
-  using namespace kvp;
+namespace kvp {
+
+int64_t window_space(const kvpool_window_args* a, int32_t n, const int64_t* h_q_len, const int64_t* h_k_start,
+                     const int64_t* h_k_len, bool even) {
   int64_t total = 0;
   const int rc = check_args(a, n, h_q_len, h_k_start, h_k_len, &total);
   if (rc != KVPOOL_OK) return rc;
@@ -423,23 +455,21 @@ extern "C" int64_t kvpool_window_workspace(const kvpool_window_args* a, int32_t 
   int64_t most = 0;
   for (int f = 0; f < kForms; ++f)
     for (int64_t i = 0, row = 0, slots = 0; i < n;) {
-      i = plan_launch(a, (Form)f, tc, (int32_t)i, n, h_q_len, h_k_start, h_k_len, row, sms, P.get(), &row, &slots);
+      i = plan_launch(a, (Form)f, tc, even, (int32_t)i, n, h_q_len, h_k_start, h_k_len, row, sms, P.get(), &row, &slots);
       if (P->n_items < 0) return KVPOOL_ERR_INVALID_ARG;
       most = std::max(most, slots * slot_bytes(*P, a->head_dim));
     }
   return most;
 }
 
-extern "C" int kvpool_window_attend(const kvpool_window_args* a, int32_t n, const int64_t* h_q_len,
-                                    const int64_t* h_k_start, const int64_t* h_k_len, void* d_workspace,
-                                    int64_t workspace_bytes, void* stream) {
-  using namespace kvp;
+int window_run(const kvpool_window_args* a, int32_t n, const int64_t* h_q_len, const int64_t* h_k_start,
+               const int64_t* h_k_len, bool even, void* d_workspace, int64_t workspace_bytes, void* stream) {
   int64_t total = 0;
   const int rc = check_args(a, n, h_q_len, h_k_start, h_k_len, &total);
   if (rc != KVPOOL_OK) return rc;
   if (total == 0) return KVPOOL_OK;
   if (out_meets_inputs(a, n, h_q_len, h_k_start, h_k_len, total)) return KVPOOL_ERR_INVALID_ARG;
-  const int64_t need = kvpool_window_workspace(a, n, h_q_len, h_k_start, h_k_len);
+  const int64_t need = window_space(a, n, h_q_len, h_k_start, h_k_len, even);
   if (need < 0) return (int)need;
   if (need > 0 && (!d_workspace || workspace_bytes < need || reinterpret_cast<uintptr_t>(d_workspace) % 16 != 0))
     return KVPOOL_ERR_INVALID_ARG;
@@ -454,7 +484,7 @@ extern "C" int kvpool_window_attend(const kvpool_window_args* a, int32_t n, cons
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   for (int f = 0; f < kForms; ++f)
     for (int64_t i = 0, row = 0, slots = 0; i < n;) {
-      i = plan_launch(a, (Form)f, tc, (int32_t)i, n, h_q_len, h_k_start, h_k_len, row, sms, P.get(), &row, &slots);
+      i = plan_launch(a, (Form)f, tc, even, (int32_t)i, n, h_q_len, h_k_start, h_k_len, row, sms, P.get(), &row, &slots);
       if (P->n_segs == 0) continue;
       P->part_o = static_cast<float*>(d_workspace);
       P->part_ml = reinterpret_cast<float2*>(P->part_o + slots * P->tile_rows * a->head_dim);
@@ -474,6 +504,19 @@ extern "C" int kvpool_window_attend(const kvpool_window_args* a, int32_t n, cons
       if (e != cudaSuccess) return KVPOOL_ERR_CUDA;
     }
   return KVPOOL_OK;
+}
+
+}  // namespace kvp
+
+extern "C" int64_t kvpool_window_workspace(const kvpool_window_args* a, int32_t n, const int64_t* h_q_len,
+                                           const int64_t* h_k_start, const int64_t* h_k_len) {
+  return kvp::window_space(a, n, h_q_len, h_k_start, h_k_len, false);
+}
+
+extern "C" int kvpool_window_attend(const kvpool_window_args* a, int32_t n, const int64_t* h_q_len,
+                                    const int64_t* h_k_start, const int64_t* h_k_len, void* d_workspace,
+                                    int64_t workspace_bytes, void* stream) {
+  return kvp::window_run(a, n, h_q_len, h_k_start, h_k_len, false, d_workspace, workspace_bytes, stream);
 }
 
 extern "C" int kvpool_window_check(void* stream, uint32_t* h_flags) {

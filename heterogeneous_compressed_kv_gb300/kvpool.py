@@ -531,18 +531,20 @@ def kv4_page_bytes(kv_heads: int, head_dim: int, page_tokens: int) -> int:
 def _table(t, what: str, index: int) -> tuple:
     """(address, row stride, rows, ids per row) of a table of page ids."""
     import torch
-    if t.dim() != 2 or t.dtype is not torch.int32 or t.get_device() != index or t.stride(1) != 1 and t.shape[1] > 1:
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or t.dtype is not torch.int32 or t.get_device() != index or stride[1] != 1 and shape[1] > 1:
         raise ValueError(f"{what} must be a 2-D int32 tensor on cuda:{index} whose rows are contiguous")
-    return t.data_ptr(), t.stride(0), t.shape[0], t.shape[1]
+    return t.data_ptr(), stride[0], shape[0], shape[1]
 
 
 def _weights(w, what: str, n: int, heads: int, width: int, index: int) -> tuple:
     """(address, segment stride, head stride) of fp32 weights [segments][key heads][>= width]."""
     import torch
-    if (w.dim() != 3 or w.dtype is not torch.float32 or w.get_device() != index or w.stride(2) != 1 and w.shape[2] > 1
-            or w.shape[0] < n or w.shape[1] != heads or w.shape[2] < width):
+    shape, stride = w.shape, w.stride()
+    if (len(shape) != 3 or w.dtype is not torch.float32 or w.get_device() != index or stride[2] != 1 and shape[2] > 1
+            or shape[0] < n or shape[1] != heads or shape[2] < width):
         raise ValueError(f"{what} must be float32 [segments][key heads][at least {width} places] on cuda:{index}, places adjacent")
-    return w.data_ptr(), w.stride(0), w.stride(1)
+    return w.data_ptr(), stride[0], stride[1]
 
 
 class Kv4Cache:
