@@ -72,8 +72,9 @@ struct RopeParams {
   int32_t rot_dim, lanes;   // lanes with values per head
   int32_t runs, run_steps;  // runs: warps per token, steps of each
   float eps, inv_dim;
-  int32_t n_axes;                    // positions of a token
-  uint8_t axis[kRopeMaxDim / 2];     // the axis of each pair (n_axes > 1)
+  int32_t n_axes, ascend;         // positions of a token; do the pairs' axes ascend?
+  int32_t bound[kRopeMaxAxes];    // the first pair of axis k + 1 or a higher one
+  uint8_t axis[kRopeMaxDim / 2];  // the axis of each pair (n_axes > 1)
 };
 
 // 8 values as loaded: W words, V = 8 / W of them to a word
@@ -165,15 +166,31 @@ __global__ void __launch_bounds__(kRopeWarps * 32, T == KVPOOL_BF16 ? 8 : 5) rop
 
   const int half = P.rot_dim / 2;
   if (half > 0) {
-    const int64_t* pos = P.pos + tok * P.n_axes;
-    const uint64_t p0 = (uint64_t)pos[0];
-    for (int i = lane; i < half; i += 32) {
-      const uint64_t p = P.n_axes > 1 ? (uint64_t)pos[P.axis[i]] : p0;
+    auto put = [&](int i, uint64_t p) {
       const int32_t t = (int32_t)((p * P.table[i]) >> 32);
       float s, c;
       sincospif((float)t * 0x1p-31f, &s, &c);
       turn[warp][0][i] = c;
       turn[warp][1][i] = s;
+    };
+    if (P.n_axes == 1) {
+      const uint64_t p = (uint64_t)P.pos[tok];
+      for (int i = lane; i < half; i += 32) put(i, p);
+    } else {
+      // the token's positions, one to a lane; a pair's axis is how many bounds lie
+      // at or below it, where axes ascend (a lookup by lane costs 7% of a long call)
+      const uint64_t mine = lane < P.n_axes ? (uint64_t)P.pos[tok * P.n_axes + lane] : 0u;
+      for (int i0 = 0; i0 < half; i0 += 32) {
+        const int i = i0 + lane;
+        int axis = 0;
+        if (P.ascend) {
+          for (int k = 0; k < P.n_axes - 1; ++k) axis += i >= P.bound[k];
+        } else if (i < half) {
+          axis = P.axis[i];
+        }
+        const uint64_t p = __shfl_sync(0xffffffffu, mine, axis);
+        if (i < half) put(i, p);
+      }
     }
     __syncwarp();
   }
@@ -353,7 +370,12 @@ extern "C" int kvpool_qk_norm_rope_axes(int32_t dtype, int32_t head_dim, int64_t
   P.lanes = head_dim / 8;
   P.eps = eps;
   P.n_axes = n_axes;
-  for (int i = 0; n_axes > 1 && i < rot_dim / 2; ++i) P.axis[i] = h_axes[i];
+  P.ascend = 1;
+  for (int i = 0; n_axes > 1 && i < rot_dim / 2; ++i) {
+    P.axis[i] = h_axes[i];
+    if (i > 0 && h_axes[i] < h_axes[i - 1]) P.ascend = 0;
+    for (int k = 0; k < n_axes - 1; ++k) P.bound[k] += h_axes[i] <= k;
+  }
   P.inv_dim = 1.0f / (float)head_dim;
   // warps per token: one takes all its heads (its angles are worked out once)
   // unless there are too few tokens to fill the GPU
