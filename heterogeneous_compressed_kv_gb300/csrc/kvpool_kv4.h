@@ -66,6 +66,9 @@ __device__ __forceinline__ int64_t kv4_tile_offset(const Kv4Cache& C, int id, in
 // of it for table rows row0 and on.  Returns KVPOOL_OK or an error.
 int kv4_check(const kvpool_kv4* c, int64_t rows);
 Kv4Cache kv4_cache(const kvpool_kv4* c, int64_t row0, uint32_t* err);
+// Do n tokens' rows of h lie on the cache's pages or its table?
+bool kv4_meets(const kvpool_kv4* c, const kvpool_heads& h, int64_t n, int64_t vb);
+bool kv4_meets(const kvpool_kv4* c, const void* p, __int128 bytes);
 inline int64_t kv4_tokens(const kvpool_kv4* c) { return (int64_t)c->table_width * c->page_tokens; }
 
 // Read the tokens [0, len[i]) of table rows row0 + i into rows of k and v

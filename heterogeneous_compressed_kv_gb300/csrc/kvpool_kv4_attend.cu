@@ -822,9 +822,8 @@ int check_args(const kvpool_kv4_args* a, int32_t n, const int64_t* q_len, const 
   if (q > a->q_rows) return KVPOOL_ERR_INVALID_ARG;
   if (q > 0 && (!a->q.data || !a->out.data)) return KVPOOL_ERR_INVALID_ARG;
   if (keys && (!a->cache.d_pages || !a->cache.d_table || a->cache.n_pages < 1)) return KVPOOL_ERR_INVALID_ARG;
-  if (a->d_weights && (reinterpret_cast<uintptr_t>(a->d_weights) % 4 != 0 ||
-                       (hk > 1 && a->weight_head_stride < most) ||
-                       (n > 1 && a->weight_stride < (int64_t)(hk - 1) * a->weight_head_stride + most)))
+  if (a->d_weights && (reinterpret_cast<uintptr_t>(a->d_weights) % 4 != 0 || a->weight_stride < 0 || a->weight_head_stride < 0 ||
+                       !runs_apart(n, a->weight_stride, hk, a->weight_head_stride, most)))
     return KVPOOL_ERR_INVALID_ARG;
   *total_q = q;
   return KVPOOL_OK;
@@ -889,7 +888,7 @@ int32_t plan(const kvpool_kv4_args* a, int32_t i0, int32_t n, const int64_t* q_l
   }
   if (rows + blocks > (1 << 30)) return -1;
   *q_row = row;
-  // a block's row sums are worth several turns where there are many keys (64 requests 19.5 us -> TURNS with four)
+  // a block's row sums are worth several turns where there are many keys (64 requests 19.5 us -> 16 with four)
   P->turns = blocks >= 16LL * n_sms ? 4 : blocks >= 8LL * n_sms ? 2 : 1;
   blocks = 0;
   for (int s = 0; a->d_weights && s < P->n_segs; ++s) {
@@ -1081,8 +1080,10 @@ extern "C" int kvpool_kv4_attend(const kvpool_kv4_args* a, int32_t n, const int6
   int64_t total = 0;
   const int bad = check_args(a, n, h_q_len, h_k_len, &total);
   if (bad != KVPOOL_OK || total == 0) return bad;
-  if (!rows_same(a->out, a->q, total) &&
-      rows_meet(a->out, total, a->q, total, a->cache.head_dim, a->dtype == KVPOOL_BF16 ? 2 : 4))
+  const int64_t vb = a->dtype == KVPOOL_BF16 ? 2 : 4;
+  if (!rows_same(a->out, a->q, total) && rows_meet(a->out, total, a->q, total, a->cache.head_dim, vb)) return KVPOOL_ERR_INVALID_ARG;
+  if (kv4_meets(&a->cache, a->out, total, vb) || kv4_meets(&a->cache, a->d_lse, (__int128)4 * total * a->q.heads) ||
+      kv4_meets(&a->cache, d_workspace, workspace_bytes))
     return KVPOOL_ERR_INVALID_ARG;
   const OpsDevice* dev = ops_device();
   if (!dev) return KVPOOL_ERR_CUDA;

@@ -318,8 +318,10 @@ int check_args(const kvpool_kv4_evict_args* a, int32_t n, const int64_t* k_len, 
   auto strides = [&](const float* p, int64_t seg, int64_t head, int64_t width, bool out) {
     if (reinterpret_cast<uintptr_t>(p) % 4 != 0 || seg < 0 || head < 0 || seg > (1ll << 40) || head > (1ll << 40)) return false;
     if (!out) return true;
-    return (c.kv_heads == 1 || head >= width) && (n == 1 || seg >= (c.kv_heads - 1) * head + width);
+    return runs_apart(n, seg, c.kv_heads, head, width);
   };
+  const __int128 index_bytes = (__int128)4 * n * c.kv_heads * a->keep;
+  if (kv4_meets(&c, a->d_index, index_bytes)) return KVPOOL_ERR_INVALID_ARG;
   if (!strides(a->d_weights, a->weight_stride, a->weight_head_stride, len, false)) return KVPOOL_ERR_INVALID_ARG;
   if (a->d_out_weights) {
     if (a->out_weight_width < a->keep ||

@@ -64,4 +64,21 @@ inline bool rows_meet(const kvpool_heads& a, int64_t na, const kvpool_heads& b, 
   return false;
 }
 
+// Does the memory from the first value of n tokens' rows to the last one share a
+// byte with [p, p + bytes)?
+inline bool rows_touch(const kvpool_heads& h, int64_t n, int32_t dim, int64_t vb, const void* p, __int128 bytes) {
+  if (n <= 0 || h.heads <= 0 || bytes <= 0 || !p) return false;
+  const __int128 a = reinterpret_cast<uintptr_t>(h.data), b = reinterpret_cast<uintptr_t>(p);
+  const __int128 an = (__int128)vb * ((__int128)(n - 1) * h.token_stride + (__int128)(h.heads - 1) * h.head_stride + dim);
+  return a < b + bytes && b < a + an;
+}
+
+// Are n1 x n2 runs of `len` values, s1 and s2 values apart, in places of their own?
+inline bool runs_apart(int64_t n1, int64_t s1, int64_t n2, int64_t s2, int64_t len) {
+  if (len <= 0 || n1 <= 0 || n2 <= 0) return true;
+  if (n1 == 1 || n2 == 1) return (n1 == 1 || s1 >= len) && (n2 == 1 || s2 >= len);
+  const int64_t lo = s1 < s2 ? s1 : s2, hi = s1 < s2 ? s2 : s1, n = s1 < s2 ? n1 : n2;
+  return lo >= len && (hi - len) / (n - 1) >= lo;
+}
+
 }  // namespace kvp

@@ -277,9 +277,9 @@ int64_t tile_keys(const kvpool_window_args* a, int64_t q_len, int64_t k_len, int
 
 // Long key lists under few query tiles (no window): the length of parts, each a
 // work item, that makes k rounds of one item to every multiprocessor shortest, an
-// item taking as long as 256 keys beside its own (two prompts of 1,024 and 512
-// queries, 16 heads on 4, behind 16,000 to 33,000 tokens: 96 query tiles on 152
-// multiprocessors took 330 us whole, WINDOW in parts).
+// item taking as long as 256 keys beside its own (two prompts of 1,024 and 768
+// queries, 16 heads on 4, behind up to 32,768 tokens read back from a 4-bit cache:
+// 360 us a call whole, 263 in parts).
 int64_t even_part(const kvpool_window_args* a, const WinParams& P, int n_sms) {
   auto items = [&](int64_t part) {
     int64_t x = 0;

@@ -529,3 +529,195 @@ def test_refusals():
     with pytest.raises(ValueError):
         cache.evict(table, [64, 64], w, 40, table, index=torch.zeros(2, hk, 39, dtype=torch.int32, device="cuda"))
     ok()
+
+
+@pytest.mark.parametrize("q_len,k_len,hq,hk", [([1, 3], [500, 40], 8, 2), ([1], [9000], 4, 1), ([1] * 40, [3000] * 40, 16, 4),
+                                               ([70, 1], [200, 100], 2, 1)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_outputs_over_the_queries(q_len, k_len, hq, hk, dtype):
+    g = gen(81)
+    cache, table = make(k_len, 64, hk, 64)
+    fill(cache, table, k_len, dtype, g)
+    rows = randn((sum(q_len), hq + 2, 64), dtype, g)
+    q = rows[:, 1:-1]
+    want = cache.attend(q, table, q_len, k_len)
+    assert cache.attend(q, table, q_len, k_len, out=q) is q and torch.equal(q, want)
+    ok()
+
+
+def test_weights_in_either_order():
+    """Accumulators [key heads][segments][places] seen as [segments][key heads][places]."""
+    g, lens = gen(83), [100, 333, 2]
+    cache, table = make(lens, 16, 4, 64)
+    fill(cache, table, lens, BF, g)
+    q = randn((3, 8, 64), BF, g)
+    a, b = torch.zeros((3, 4, 333), device="cuda"), torch.zeros((4, 3, 340), device="cuda")
+    cache.attend(q, table, [1] * 3, lens, weights=a)
+    cache.attend(q, table, [1] * 3, lens, weights=b.transpose(0, 1))
+    assert torch.equal(a, b.transpose(0, 1)[..., :333]) and bool((b[..., 333:] == 0).all())
+    with pytest.raises(K.KvpoolError):
+        cache.attend(q, table, [1] * 3, lens, weights=b[:, :1].expand(4, 3, 340).transpose(0, 1))
+    ok()
+
+
+def test_shared_pages_are_read():
+    """Two requests behind one prefix: their tables name the same pages; eviction leaves them to both."""
+    g, hk, d, page = gen(85), 2, 128, 16
+    cache, table = make([160, 32, 0, 0], page, hk, d, spare=12)
+    used = set(table.flatten().tolist())
+    free = [i for i in range(cache.pages.shape[0]) if i not in used]
+    rows = torch.zeros((2, 12), dtype=torch.int32, device="cuda")
+    rows[0, :10] = rows[1, :10] = table[0, :10]
+    rows[1, 10:] = table[1, :2]
+    k, v = randn((192, hk, d), BF, g), randn((192, hk, d), BF, g)
+    cache.store(k[:160], v[:160], rows[:1], [0], [160])
+    cache.store(k[160:], v[160:], rows[1:], [160], [32])
+    hk_, hv_ = F.held(k), F.held(v)
+    q, lse, w = randn((2, 4, d), BF, g), torch.empty((2, 4), device="cuda"), torch.zeros((2, hk, 192), device="cuda")
+    out = cache.attend(q, rows, [1, 1], [160, 192], lse=lse, weights=w, decay=0.0)
+    both = [torch.cat([x[:160], x]) for x in (hk_, hv_)]
+    check(q, *both, [1, 1], [160, 192], d ** -0.5, BF, out, lse, w, torch.zeros_like(w))
+    before = cache.pages.clone()
+    outs = torch.tensor(free[:8], dtype=torch.int32, device="cuda").view(2, 4)
+    cache.evict(rows, [160, 192], w, 64, outs)
+    for p in used:
+        assert torch.equal(cache.pages[p], before[p])
+    assert torch.equal(cache.attend(q, rows, [1, 1], [160, 192]), out)
+    ok()
+
+
+def test_pages_past_32_bits():
+    g, hk, d, page = gen(87), 2, 64, 1024
+    size = K.kv4_page_bytes(hk, d, page)
+    n = (1 << 32) // size + 4
+    pages = torch.empty((n, size), dtype=torch.uint8, device="cuda")
+    cache = K.Kv4Cache(pages, hk, d, page)
+    table = torch.tensor([[n - 1, 0, n - 2]], dtype=torch.int32, device="cuda")
+    outs = torch.tensor([[n - 3]], dtype=torch.int32, device="cuda")
+    k, v = fill(cache, table, [3000], BF, g)
+    q, lse, w = randn((1, 4, d), BF, g), torch.empty((1, 4), device="cuda"), torch.zeros((1, hk, 3000), device="cuda")
+    out = cache.attend(q, table, [1], [3000], lse=lse, weights=w)
+    check(q, k, v, [1], [3000], 0.125, BF, out, lse, w, torch.zeros_like(w))
+    index, _ = cache.evict(table, [3000], w, 1000, outs)
+    k2, v2 = cache.load(outs, [0], [1000], dtype=F32)
+    for h in range(hk):
+        assert same(k2[:, h], k[index[0, h].cpu().long(), h]) and same(v2[:, h], v[index[0, h].cpu().long(), h])
+    ok()
+
+
+def test_evict_from_more_tokens_than_shared_memory_holds():
+    g, n, keep = gen(89), 450_000, 700
+    cache, table = make([n], 1024, 1, 64, spare=1)
+    used = set(table.flatten().tolist())
+    outs = torch.tensor([[i for i in range(cache.pages.shape[0]) if i not in used]], dtype=torch.int32, device="cuda")
+    k, _ = fill(cache, table, [n], BF, g)
+    w = torch.rand((1, 1, n), device="cuda", generator=g).bfloat16().float()
+    index, left = cache.evict(table, [n], w, keep, outs, 4, 50)
+    idx = kept(w[0, 0].cpu().numpy(), n, keep, 4, 50)
+    assert index[0, 0].tolist() == idx.tolist() and torch.equal(left[0, 0], w[0, 0, idx])
+    assert same(cache.load(outs, [0], [keep], dtype=F32)[0][:, 0], k[idx, 0])
+    ok()
+
+
+def test_evict_many_segments():
+    g, n, keep = gen(91), 300, 20
+    lens = np.random.RandomState(1).randint(0, 60, n).tolist()
+    cache, table = make(lens, 16, 1, 64, spare=2 * n)
+    used = set(int(x) for i, m in enumerate(lens) for x in table[i, :max(1, -(-m // 16))].tolist())
+    free = [i for i in range(cache.pages.shape[0]) if i not in used]
+    outs = torch.tensor(free[:2 * n], dtype=torch.int32, device="cuda").view(n, 2)
+    k, _ = fill(cache, table, lens, BF, g)
+    w = torch.rand((n, 1, 60), device="cuda", generator=g)
+    index, left = cache.evict(table, lens, w, keep, outs, 2, 5)
+    got = cache.load(outs, [0] * n, [min(m, keep) for m in lens], dtype=F32)[0]
+    at = to = 0
+    for i, m in enumerate(lens):
+        idx = kept(w[i, 0].cpu().numpy(), m, keep, 2, 5)
+        assert index[i, 0].tolist() == idx.tolist() + [-1] * (keep - len(idx))
+        assert same(got[to:to + len(idx), 0], k[at + idx, 0])
+        at, to = at + m, to + len(idx)
+    ok()
+
+
+FIRST = """
+import sys; sys.path.insert(0, {root!r})
+import torch
+from heterogeneous_compressed_kv_gb300 import kvpool as K
+n = 2000
+cache = K.Kv4Cache(torch.zeros((40, K.kv4_page_bytes(2, 64, 64)), dtype=torch.uint8, device="cuda"), 2, 64, 64)
+table = torch.arange(32, dtype=torch.int32, device="cuda")[None]
+outs = torch.arange(32, 40, dtype=torch.int32, device="cuda")[None]
+k = torch.randn((n, 2, 64), device="cuda").bfloat16()
+q = torch.randn(({rows}, 8, 64), device="cuda").bfloat16()
+w = torch.zeros((1, 2, n), device="cuda") if {rows} < 16 else None
+index = torch.zeros((1, 2, 500), dtype=torch.int32, device="cuda")
+left = torch.zeros((1, 2, 500), device="cuda")
+out = torch.zeros_like(q)
+def call():
+    cache.store(k, k, table, [0], [n])
+    cache.attend(q, table, [{rows}], [n], out=out, weights=w, decay=0.0)
+    if w is not None:
+        cache.evict(table, [n], w, 500, outs, index=index, out_weights=left)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    call()
+graph.replay()
+torch.cuda.synchronize()
+first = [x.clone() for x in (out, index, left)]
+assert float(first[0].float().abs().sum()) > 0
+call()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(first, (out, index, left)))
+assert K.window_check() == (K.OK, 0)
+"""
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+def test_the_first_calls_of_a_process_inside_a_capture(rows):
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST.format(root=root, rows=rows)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_two_threads_at_once():
+    import threading
+    g, hk, d, lens = gen(93), 2, 64, [3000, 50, 700]
+    cache, table = make(lens, 64, hk, d)
+    fill(cache, table, lens, BF, g)
+    q = randn((5, 8, d), BF, g)
+    args = (q, table, [1, 3, 1], lens)
+    w0 = torch.zeros((3, hk, 3000), device="cuda")
+    want, back = cache.attend(*args, weights=w0, decay=0.0), cache.load(table, [0] * 3, lens)[0]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work():
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            got = []
+            for _ in range(20):
+                w = torch.zeros_like(w0)
+                got.append((cache.attend(*args, weights=w, decay=0.0), w, cache.load(table, [0] * 3, lens)[0]))
+            s.synchronize()
+            bad.extend(1 for a, b, c in got if not (torch.equal(a, want) and torch.equal(b, w0) and torch.equal(c, back)))
+            s.synchronize()
+
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+    ok()
+
+
+@pytest.mark.parametrize("q_len,lens,hq,hk,dtype", [([1], [20000], 16, 1, BF), ([1] * 8, [7000] * 8, 16, 4, BF), ([2], [9000], 8, 1, BF),
+                                                    ([1] * 60, [130] * 60, 8, 2, BF), ([5], [6000], 4, 2, F32), ([1] * 3, [9000, 20, 400], 8, 8, F32)])
+def test_both_forms_in_many_parts(q_len, lens, hq, hk, dtype):
+    """Long units in hundreds of shares, short ones in a CTA each."""
+    run(q_len, lens, hq, hk, 128, 64, dtype, True)
+    run(q_len, lens, hq, hk, 128, 16, dtype, False)

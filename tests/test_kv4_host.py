@@ -83,9 +83,19 @@ def attend(q_len=(1, 2), k_len=(100, 200), dtype=K.BF16, scale=0.125, q=None, ou
     dict(q=heads(3)), dict(q=heads(1)), dict(q=heads(34), out=heads(34, data=FAR * 2)), dict(out=heads(2, data=FAR * 2)),
     dict(q=heads(4, data=P16 + 2)), dict(q=heads(4, ts=4)), dict(out=heads(4, data=FAR * 2, hs=0)), dict(q=heads(4, data=None)),
     dict(out=heads(4, data=None)), dict(pages=None), dict(table=None), dict(n_pages=0),
-    dict(w=P16 + 2), dict(w=P16, wh=199), dict(w=P16, ws=1 << 10), dict(w=P16, q_len=(1, 33))])
+    dict(w=P16 + 2), dict(w=P16, wh=199), dict(w=P16, ws=199), dict(w=P16, ws=1 << 9, wh=500), dict(w=P16, ws=-1),
+    dict(w=P16, q_len=(1, 33))])
 def test_attend_refuses(bad):
     assert attend(**bad) == K.ERR_INVALID_ARG
+
+
+def test_outputs_on_the_cache_are_refused():
+    on = heads(4, data=FAR + 4096)
+    assert attend(out=on, work_too=False) == K.ERR_INVALID_ARG and attend(lse=FAR - 16, work_too=False) == K.ERR_INVALID_ARG
+    assert attend(out=heads(4, data=FAR + (1 << 24) + 32), work_too=False) == K.ERR_INVALID_ARG  # the table
+    assert attend(w=P16, space=FAR + 256, space_bytes=1 << 20, work_too=False) == K.ERR_INVALID_ARG
+    assert move("store", k=heads(data=FAR + 64)) == K.ERR_INVALID_ARG and move("load", v=heads(data=FAR - 128)) == K.ERR_INVALID_ARG
+    assert evict(index=FAR + 64) == K.ERR_INVALID_ARG
 
 
 def test_attend_refuses_an_output_on_its_queries():
@@ -110,7 +120,7 @@ def evict(k_len=(100, 200), keep=50, sink=4, recent=8, out=FAR * 4, ostride=4, o
     dict(k_len=(1, -1)), dict(k_len=(1, 257)), dict(k_len=(1, 1 << 62)), dict(keep=0), dict(keep=-1), dict(sink=-1), dict(recent=-1),
     dict(sink=51), dict(sink=40, recent=11), dict(sink=2147483647, recent=2147483647), dict(out=None), dict(out=FAR + 2), dict(ostride=-1),
     dict(orows=1), dict(owidth=0), dict(owidth=-1), dict(w=None), dict(w=P16 + 2), dict(ws=-1), dict(wh=-1), dict(ow=P16),
-    dict(ow=P16 + 4 * 5000), dict(ow=FAR * 3 + 1), dict(ows=100), dict(owh=59), dict(wide=49), dict(index=None), dict(index=FAR + 1),
+    dict(ow=P16 + 4 * 5000), dict(ow=FAR * 3 + 1), dict(ows=59), dict(ows=1 << 9, owh=500), dict(owh=59), dict(ows=-1), dict(owh=-1), dict(wide=49), dict(index=None), dict(index=FAR + 1),
     dict(segs=-1), dict(n_pages=0), dict(pages=None), dict(table=None)])
 def test_evict_refuses(bad):
     assert evict(**bad) == K.ERR_INVALID_ARG
