@@ -12,6 +12,7 @@
 #include <cuda_runtime.h>
 
 #include "kvpool_kv4.h"
+#include "kvpool_pair.cuh"
 #include "kvpool_rows.h"
 
 namespace kvp {
@@ -109,11 +110,22 @@ __device__ __forceinline__ void store8(uint8_t* p, const float* x) {
   }
 }
 
-// Eight codes (nibble i of the result: value i) of half a group, and the group's
-// scale; the other half is with the neighbouring lane.  A NaN or an infinity
-// makes the scale NaN: the whole group reads back as NaN.
+// The scale of a group, of which a lane has one half and its neighbour the other,
+// and what quotients by it are made with: a code, and its value or a multiple of
+// its reciprocal.  A NaN or an infinity makes the scale NaN: the whole group reads
+// back as NaN.
 template <int T>
-__device__ __forceinline__ uint32_t quantize8(const Raw8<T>& raw, float inv_scale, uint32_t& s) {
+struct Scale {
+  uint32_t code;
+  float by;
+};
+
+__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+__device__ __forceinline__ Scale<KVPOOL_F32> scale_of(const Raw8<KVPOOL_F32>& raw, float inv_scale) {
   float x[8];
   raw.get(x);
   uint32_t amax = 0;
@@ -121,43 +133,62 @@ __device__ __forceinline__ uint32_t quantize8(const Raw8<T>& raw, float inv_scal
   for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(x[i]) & 0x7FFFFFFFu);
   amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
   const float top = __uint_as_float(amax) * inv_scale;  // (a power of two)
-  if (!(top < INFINITY)) {
-    s = 0x7F;
-    return 0;
-  }
-  s = f32x2_to_e4m3x2(__fdiv_rn(top, 6.0f), 0.0f) & 0xFFu;
-  if (s == 0) return 0;
-  const float f = e4m3x2_to_f32x2((uint16_t)s).x;
-  uint32_t c = 0;
-  if constexpr (T == KVPOOL_F32) {
-    // The fp32 quotient stands for x / s: it lies on a border between two codes
-    // only where x / s does (x and border * s are fp32 numbers, so unequal ones
-    // differ by more than the quotient's rounding).
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      c |= (uint32_t)f32x2_to_e2m1x2(__fdiv_rn(x[2 * i] * inv_scale, f), __fdiv_rn(x[2 * i + 1] * inv_scale, f)) << (8 * i);
-  } else {
-    // A bf16 number is border * s (7 bits) or at least 2^-8 of it away, so a
-    // product with the reciprocal (off by 2^-24 of it) rounded to a multiple of
-    // 2^-11 (borders are multiples of 0.25 up to 5) is the border where x / s is, and
-    // on x / s's side of it elsewhere; what is beyond 6 stays there.  (With quotients
-    // 6,144 tokens of 16 heads x 128 took 30.9 us instead of 18.9.)
-    const float r = __frcp_rn(f) * inv_scale;
-    constexpr float kGrid = 6144.0f;  // 1.5 * 2^12: a sum with it is a multiple of 2^-11
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float q0 = __fadd_rn(__fmaf_rn(x[2 * i], r, kGrid), -kGrid), q1 = __fadd_rn(__fmaf_rn(x[2 * i + 1], r, kGrid), -kGrid);
-      c |= (uint32_t)f32x2_to_e2m1x2(q0, q1) << (8 * i);
-    }
-  }
-  return c;
+  if (!(top < INFINITY)) return {0x7F, 0.0f};
+  const uint32_t s = f32x2_to_e4m3x2(__fdiv_rn(top, 6.0f), 0.0f) & 0xFFu;
+  return {s, e4m3x2_to_f32x2((uint16_t)s).x};
 }
 
-// the low four nibbles of x to four bytes
-__device__ __forceinline__ uint32_t nibbles_to_bytes(uint32_t x) {
-  x &= 0xFFFFu;
-  x = (x | (x << 8)) & 0x00FF00FFu;
-  return (x | (x << 4)) & 0x0F0F0F0Fu;
+// For bf16 a product with a reciprocal stands for the quotient.  With a rounding
+// that brings a quotient that is a border between two codes back to it: a bf16
+// number (8 bits) is 6 times a border between two scales (5 bits), or a border
+// between two codes times a scale (7 bits), or at least 2^-8 of it away, where the
+// product is off by 2^-22 of it and the rounding (to fp16's 11 bits; to multiples of
+// 2^-11 beside borders from 0.25 to 5) by less than 2^-10.  (With quotients 6,144
+// tokens of 16 heads x 128 took 30.9 us.)
+__device__ __forceinline__ Scale<KVPOOL_BF16> scale_of(const Raw8<KVPOOL_BF16>& raw, float inv_scale) {
+  constexpr uint32_t kAbs = 0x7FFF7FFFu;
+  uint32_t m = max_abs_bf16x2(max_abs_bf16x2(raw.r.x & kAbs, raw.r.y & kAbs), max_abs_bf16x2(raw.r.z & kAbs, raw.r.w & kAbs));
+  m = max_abs_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  const float top = __uint_as_float(max(m << 16, m & 0xFFFF0000u)) * inv_scale;  // (a power of two; NaN is the largest)
+  if (!(top < INFINITY)) return {0x7F, 0.0f};
+  uint16_t s;
+  asm("{.reg .b32 h;\n\tcvt.rn.f16x2.f32 h, %1, %1;\n\tcvt.rn.satfinite.e4m3x2.f16x2 %0, h;}" : "=h"(s) : "f"(top * (1.0f / 6.0f)));
+  const float f = e4m3x2_to_f32x2(s).x;
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(f));
+  return {s & 0xFFu, f > 0.0f ? r * inv_scale : 0.0f};
+}
+
+// eight values' quotients, as the codes' rounding takes them
+__device__ __forceinline__ void quotients(const Raw8<KVPOOL_F32>& raw, float inv_scale, const Scale<KVPOOL_F32>& s, float* q) {
+  raw.get(q);
+  // The fp32 quotient stands for x / s: it lies on a border between two codes only
+  // where x / s does (x and border * s are fp32 numbers, so unequal ones differ by
+  // more than the quotient's rounding).
+#pragma unroll
+  for (int i = 0; i < 8; ++i) q[i] = s.by > 0.0f ? __fdiv_rn(q[i] * inv_scale, s.by) : 0.0f;
+}
+__device__ __forceinline__ void quotients(const Raw8<KVPOOL_BF16>& raw, float, const Scale<KVPOOL_BF16>& s, float* q) {
+  raw.get(q);
+  constexpr float kGrid = 6144.0f;  // 1.5 * 2^12: a sum with it is a multiple of 2^-11 (what is beyond 6 stays there)
+  const uint64_t by = pack2(s.by, s.by), up = pack2(kGrid, kGrid), down = pack2(-kGrid, -kGrid);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 y = unpack2(add2(fma2(pack2(q[2 * i], q[2 * i + 1]), by, up), down));
+    q[2 * i] = y.x, q[2 * i + 1] = y.y;
+  }
+}
+
+// byte i: the codes of a[i] (low nibble) and b[i]
+__device__ __forceinline__ uint32_t codes4(float a0, float b0, float a1, float b1, float a2, float b2, float a3, float b3) {
+  uint32_t r;
+  asm("{.reg .b8 t0, t1, t2, t3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 t0, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 t1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 t2, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 t3, %8, %7;\n\t"
+      "mov.b32 %0, {t0, t1, t2, t3};}"
+      : "=r"(r)
+      : "f"(a0), "f"(b0), "f"(a1), "f"(b1), "f"(a2), "f"(b2), "f"(a3), "f"(b3));
+  return r;
 }
 
 // A warp takes a tile of one head: the lanes of a row hold 8 dims each.  All of
@@ -196,11 +227,12 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_store_kernel(const __grid_con
     const int r = it * kPer + sub;
     const bool in = r >= t.lo && r < t.hi;
     if (!__any_sync(0xffffffffu, in)) continue;
-    uint32_t s;
-    const uint32_t c = quantize8<T>(rk[it], k_inv, s);
+    const auto s = scale_of(rk[it], k_inv);
+    float q[8];
+    quotients(rk[it], k_inv, s, q);
     if (in) {
-      *reinterpret_cast<uint32_t*>(tile + r * (D / 2) + 4 * l) = c;
-      if (l % 2 == 0) tile[L::kKs + r * (D / kKv4Group) + l / 2] = (uint8_t)s;
+      *reinterpret_cast<uint32_t*>(tile + r * (D / 2) + 4 * l) = codes4(q[0], q[1], q[2], q[3], q[4], q[5], q[6], q[7]);
+      if (l % 2 == 0) tile[L::kKs + r * (D / kKv4Group) + l / 2] = (uint8_t)s.code;
     }
   }
 #pragma unroll
@@ -208,22 +240,24 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_store_kernel(const __grid_con
     const int j = it * kPer + sub, r = 2 * j;
     const bool in0 = r >= t.lo && r < t.hi, in1 = r + 1 >= t.lo && r + 1 < t.hi;
     if (!__any_sync(0xffffffffu, in0 || in1)) continue;
-    uint32_t s0, s1;
-    const uint32_t c0 = quantize8<T>(rv[it][0], v_inv, s0), c1 = quantize8<T>(rv[it][1], v_inv, s1);
+    const auto s0 = scale_of(rv[it][0], v_inv), s1 = scale_of(rv[it][1], v_inv);
+    float q0[8], q1[8];
+    quotients(rv[it][0], v_inv, s0, q0);
+    quotients(rv[it][1], v_inv, s1, q1);
     if (!in0 && !in1) continue;
     const int chunk = 8 * l / L::kChunk, at = 8 * l % L::kChunk;
     uint2* p = reinterpret_cast<uint2*>(tile + L::kV + j * D + (chunk ^ kv4_swizzle<D>(j)) * L::kChunk + at);
-    uint2 w = make_uint2(nibbles_to_bytes(c0) | nibbles_to_bytes(c1) << 4,
-                         nibbles_to_bytes(c0 >> 16) | nibbles_to_bytes(c1 >> 16) << 4);
+    const uint2 w = make_uint2(codes4(q0[0], q1[0], q0[1], q1[1], q0[2], q1[2], q0[3], q1[3]),
+                               codes4(q0[4], q1[4], q0[5], q1[5], q0[6], q1[6], q0[7], q1[7]));
     uint8_t* sc = tile + L::kVs + j * (D / 8) + l / 2 * 2;
     if (in0 && in1) {
       *p = w;
-      if (l % 2 == 0) *reinterpret_cast<uint16_t*>(sc) = (uint16_t)(s0 | s1 << 8);
+      if (l % 2 == 0) *reinterpret_cast<uint16_t*>(sc) = (uint16_t)(s0.code | s1.code << 8);
     } else {  // the pair's other token stays
       const uint32_t mine = in0 ? 0x0F0F0F0Fu : 0xF0F0F0F0u;
       const uint2 old = *p;
       *p = make_uint2((w.x & mine) | (old.x & ~mine), (w.y & mine) | (old.y & ~mine));
-      if (l % 2 == 0) sc[in0 ? 0 : 1] = (uint8_t)(in0 ? s0 : s1);
+      if (l % 2 == 0) sc[in0 ? 0 : 1] = (uint8_t)(in0 ? s0.code : s1.code);
     }
   }
 }

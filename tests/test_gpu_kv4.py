@@ -721,3 +721,24 @@ def test_both_forms_in_many_parts(q_len, lens, hq, hk, dtype):
     """Long units in hundreds of shares, short ones in a CTA each."""
     run(q_len, lens, hq, hk, 128, 64, dtype, True)
     run(q_len, lens, hq, hk, 128, 16, dtype, False)
+
+
+def test_every_largest_value_and_its_borders():
+    """Groups of every positive bf16 largest value, their other values the borders between codes and their neighbours."""
+    bits = np.arange(1, 0x7F80, dtype=np.uint16)
+    bits = bits[:len(bits) // 8 * 8]
+    amax = torch.from_numpy(bits.view(np.int16)).view(BF)
+    s = F.nearest((amax.float().numpy() / np.float32(6)).astype(np.float64), F.E4M3)
+    border = torch.from_numpy(s)[:, None] * torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], dtype=torch.float64)
+    near = border.to(BF)
+    assert bool((near.double() == border)[s > 2.0 ** -9].all())
+    pad = near[:, :1] * 0
+    up, down = (torch.where(near > 0, (near.view(torch.int16) + d).view(BF), near) for d in (1, -1))
+    for other, dtype in ((up, BF), (down, BF), (up, F32), (down, F32)):
+        x = torch.cat([amax[:, None], near, -other, pad], 1).reshape(-1, 1, 128).to(dtype).cuda()
+        n = x.shape[0]
+        cache, table = make([n], 64, 1, 128)
+        cache.store(x, x.flip(0), table, [0], [n])
+        k, v = cache.load(table, [0], [n], dtype=F32)
+        assert same(k, F.held(x)) and same(v, F.held(x.flip(0)))
+    ok()
