@@ -8,7 +8,7 @@
 // passes over 8 bits of an order-keeping integer of the weight narrow the last
 // weight that stays (histograms in shared memory, added up over the cluster), a
 // count by warp slices gives every slice its first place, and the places go out in
-// order.  The second moves the tokens, a warp to a tile of 16 of them.
+// order.  The second moves the tokens, a warp to two tiles of 16 of them.
 #include <algorithm>
 #include <memory>
 #include <new>
@@ -31,7 +31,7 @@ constexpr int kMoveWarps = 4;
 
 struct EvictSeg {
   int32_t k_len;
-  int32_t task_base;  // first task of the moving kernel: tile * kv_heads + head
+  int32_t task_base;  // first task of the moving kernel: tiles * kv_heads + head
   int32_t table_row;  // of the first launch's tables, weights and outputs
 };
 
@@ -57,7 +57,7 @@ __device__ __forceinline__ uint32_t weight_key(float w) { return w != w ? 0xFFFF
 template <bool SHARED>
 __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const __grid_constant__ EvictParams P) {
   pdl_start();
-  extern __shared__ uint32_t keys[];
+  extern __shared__ __align__(16) uint32_t keys[];
   __shared__ uint32_t hist[4][256];
   __shared__ uint2 counts[kSelWarps];  // (above the last weight that stays, equal to it) of a warp's slice
   __shared__ uint32_t sh_digit, sh_left;
@@ -91,32 +91,42 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const __grid_co
   }
   const int lo = P.sink, hi = n - P.recent, want = keep - P.sink - P.recent;  // want < hi - lo
   if (want == 0) return;
-  const int warps = C * kSelWarps, per = ((hi - lo + warps - 1) / warps + 31) & ~31;  // a warp's slice
+  const int warps = C * kSelWarps, per = ((hi - lo + warps - 1) / warps + 127) & ~127;  // a warp's slice
   const int a = min(hi, lo + (rank * kSelWarps + warp) * per), b = min(hi, a + per);
   for (int i = tid; i < 4 * 256; i += kSelThreads) (&hist[0][0])[i] = 0;
   __syncthreads();
-  uint32_t* mine_keys = keys + warp * per;  // key of weight i: [i - a]
-  auto key_at = [&](int i) { return SHARED ? mine_keys[i - a] : weight_key(w[i]); };
+  // The keys of weights i .. i + 3; 0, which is no weight's, behind the slice.
+  uint32_t* slice = keys + warp * per;
+  auto keys_at = [&](int i) {
+    if constexpr (SHARED) return *reinterpret_cast<const uint4*>(slice + (i - a));
+    return make_uint4(i < b ? weight_key(w[i]) : 0u, i + 1 < b ? weight_key(w[i + 1]) : 0u, i + 2 < b ? weight_key(w[i + 2]) : 0u,
+                      i + 3 < b ? weight_key(w[i + 3]) : 0u);
+  };
+  if (SHARED) {
+#pragma unroll 1
+    for (int i0 = a; i0 < b; i0 += 256) {
+      float x[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) x[u] = i0 + 32 * u + lane < b ? w[i0 + 32 * u + lane] : 0.0f;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int i = i0 + 32 * u + lane;
+        if (i < a + per) slice[i - a] = i < b ? weight_key(x[u]) : 0u;
+      }
+    }
+    __syncwarp();
+  }
   uint32_t prefix = 0, left = want;
 #pragma unroll 1
   for (int pass = 0; pass < 4; ++pass) {
     const int shift = 24 - 8 * pass;
-    // eight weights to a lane at a time
-#pragma unroll 1
-    for (int i0 = a; i0 < b; i0 += 256) {
-      uint32_t key[8];
+#pragma unroll 2
+    for (int i = a + 4 * lane; i < b; i += 128) {
+      const uint4 k = keys_at(i);
+      const uint32_t key[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int i = i0 + 32 * u + lane;
-        key[u] = i < b ? (SHARED && pass == 0 ? __float_as_uint(w[i]) : key_at(i)) : 0u;
-      }
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int i = i0 + 32 * u + lane;
-        if (i >= b) continue;
-        if (SHARED && pass == 0) mine_keys[i - a] = key[u] = weight_key(__uint_as_float(key[u]));
-        if (pass == 0 || key[u] >> (shift + 8) == prefix) atomicAdd(&hist[pass][key[u] >> shift & 255], 1u);
-      }
+      for (int u = 0; u < 4; ++u)
+        if (key[u] != 0 && (pass == 0 || key[u] >> (shift + 8) == prefix)) atomicAdd(&hist[pass][key[u] >> shift & 255], 1u);
     }
     cluster.sync();
     // counts from the largest digit down: thread i holds digit 255 - i
@@ -146,11 +156,11 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const __grid_co
   }
   // `prefix` is the key of the last weight that stays, `left` how many of those equal to it do
   uint2 mine = make_uint2(0, 0);
-#pragma unroll 8
-  for (int i = a + lane; i < b; i += 32) {
-    const uint32_t key = key_at(i);
-    mine.x += key > prefix;
-    mine.y += key == prefix;
+#pragma unroll 2
+  for (int i = a + 4 * lane; i < b; i += 128) {
+    const uint4 k = keys_at(i);
+    mine.x += (k.x > prefix) + (k.y > prefix) + (k.z > prefix) + (k.w > prefix);
+    mine.y += (k.x == prefix) + (k.y == prefix) + (k.z == prefix) + (k.w == prefix);
   }
   mine.x = __reduce_add_sync(0xffffffffu, mine.x);
   mine.y = __reduce_add_sync(0xffffffffu, mine.y);
@@ -164,28 +174,45 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const __grid_co
   }
   above = __reduce_add_sync(0xffffffffu, above);
   equal = __reduce_add_sync(0xffffffffu, equal);
-#pragma unroll 4
-  for (int i0 = a; i0 < b; i0 += 32) {
-    const int i = i0 + lane;
-    const uint32_t key = i < b ? key_at(i) : 0u;
-    const uint32_t gt = __ballot_sync(0xffffffffu, i < b && key > prefix), eq = __ballot_sync(0xffffffffu, i < b && key == prefix);
-    const uint32_t below = (1u << lane) - 1;
-    const uint32_t e = equal + __popc(eq & below);
-    if ((gt >> lane & 1) || ((eq >> lane & 1) && e < left)) {
-      const int to = P.sink + above + __popc(gt & below) + min(e, left);
-      index[to] = i;
-      if (ow) ow[to] = w[i];
+#pragma unroll 1
+  for (int i0 = a; i0 < b; i0 += 128) {
+    const int i = i0 + 4 * lane;
+    const uint4 k = i < b ? keys_at(i) : make_uint4(0, 0, 0, 0);
+    const uint32_t key[4] = {k.x, k.y, k.z, k.w};
+    uint32_t here = 0;  // above (low half) and equal (high half)
+#pragma unroll
+    for (int u = 0; u < 4; ++u) here += (key[u] > prefix ? 1u : 0u) + (key[u] == prefix ? 1u << 16 : 0u);
+    uint32_t up = here;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, up, off);
+      if (lane >= off) up += y;
     }
-    above += __popc(gt);
-    equal += __popc(eq);
+    uint32_t n_above = above + ((up - here) & 0xFFFF), n_equal = equal + ((up - here) >> 16);
+    const uint32_t total = __shfl_sync(0xffffffffu, up, 31);
+    above += total & 0xFFFF;
+    equal += total >> 16;
+    if (here == 0) continue;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const bool gt = key[u] > prefix, eq = key[u] == prefix;
+      if (gt || (eq && n_equal < left)) {
+        const int to = P.sink + n_above + min(n_equal, left);
+        index[to] = i + u;
+        if (ow) ow[to] = w[i + u];
+      }
+      n_above += gt;
+      n_equal += eq;
+    }
   }
   cluster.sync();  // no CTA ends while another one reads its counts
 }
 
-// A warp moves a tile of 16 tokens of one head.
+// A warp moves two tiles of 16 tokens of one head, one after the other: their
+// places are looked up at once.
+constexpr int kMoveTiles = 2;
 template <int D>
 __global__ void __launch_bounds__(kMoveWarps * 32) kv4_move_kernel(const __grid_constant__ EvictParams P) {
-  pdl_start();
   using L = Kv4Tile<D>;
   const int task = blockIdx.x * kMoveWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (task >= P.n_tasks) return;
@@ -196,26 +223,32 @@ __global__ void __launch_bounds__(kMoveWarps * 32) kv4_move_kernel(const __grid_
     else hi = mid - 1;
   }
   const EvictSeg& S = P.segs[lo];
-  const int head = (task - S.task_base) % P.c.kv_heads, tile = (task - S.task_base) / P.c.kv_heads;
-  const int n = min(kKv4Tile, min(S.k_len, P.keep) - tile * kKv4Tile);
+  const int head = (task - S.task_base) % P.c.kv_heads, tile0 = (task - S.task_base) / P.c.kv_heads * kMoveTiles;
+  const int left = min(S.k_len, P.keep) - tile0 * kKv4Tile;  // tokens from there on (at least one)
   Kv4Cache to = P.c;
   to.table = P.out_table;
   to.table_stride = P.out_stride;
-  const int to_id = kv4_page(to, S.table_row, tile);
-  if (to_id < 0) return;
-  uint8_t* dst = P.c.pages + kv4_tile_offset<D>(P.c, to_id, head, tile);
-  // lane r (of 16): the place of token r of the tile; a bad page id reads as zeros
+  const int to_tile = tile0 + lane / kKv4Tile;
+  const int to_id = lane / kKv4Tile * kKv4Tile < left ? kv4_page(to, S.table_row, to_tile) : -1;
+  const int64_t to_off = to_id < 0 ? -1 : kv4_tile_offset<D>(P.c, to_id, head, to_tile);
+  // lane r: the place of token r of the tiles; a bad page id reads as zeros
   int64_t off = -1;
   int slot = 0;
-  if (lane < n) {
-    const int t = P.index[((int64_t)S.table_row * P.c.kv_heads + head) * P.keep + tile * kKv4Tile + lane];
+  if (lane < left) {
+    const int t = P.index[((int64_t)S.table_row * P.c.kv_heads + head) * P.keep + tile0 * kKv4Tile + lane];
     slot = t % kKv4Tile;
     const int id = kv4_page(P.c, S.table_row, t / kKv4Tile);
     if (id >= 0) off = kv4_tile_offset<D>(P.c, id, head, t / kKv4Tile);
   }
-  auto off_of = [&](int r) { return __shfl_sync(0xffffffffu, off, r); };
-  auto slot_of = [&](int r) { return __shfl_sync(0xffffffffu, slot, r); };
   const uint8_t* pages = P.c.pages;
+#pragma unroll 1
+  for (int y0 = 0; y0 < kMoveTiles; ++y0) {
+  const int n = min(kKv4Tile, left - y0 * kKv4Tile);
+  const int64_t dst_off = __shfl_sync(0xffffffffu, to_off, y0 * kKv4Tile);
+  if (dst_off < 0) continue;  // (no such tile, or a bad page: the whole warp)
+  uint8_t* dst = P.c.pages + dst_off;
+  auto off_of = [&](int r) { return __shfl_sync(0xffffffffu, off, y0 * kKv4Tile + r); };
+  auto slot_of = [&](int r) { return __shfl_sync(0xffffffffu, slot, y0 * kKv4Tile + r); };
   // all loads first (nothing that is written is read)
   constexpr int KI = D / 64;  // 16-byte pieces of keys to a lane
   uint4 k[KI];
@@ -229,8 +262,12 @@ __global__ void __launch_bounds__(kMoveWarps * 32) kv4_move_kernel(const __grid_
   // scales: of token `lane`'s keys (8 or 4 bytes), of pair `lane`'s values (16 or 8: two tokens' bytes alternate)
   constexpr int G = D / kKv4Group, SW = G / 4;
   uint32_t ks[SW], vs[2 * SW];
+  {
+    const int64_t o = off_of(lane % kKv4Tile);
+    const int sl = slot_of(lane % kKv4Tile);
 #pragma unroll
-  for (int i = 0; i < SW; ++i) ks[i] = off >= 0 ? reinterpret_cast<const uint32_t*>(pages + off + L::kKs + slot * G)[i] : 0;
+    for (int i = 0; i < SW; ++i) ks[i] = o >= 0 ? reinterpret_cast<const uint32_t*>(pages + o + L::kKs + sl * G)[i] : 0;
+  }
   {
     const int j = lane % 8;
     const int64_t o0 = off_of(2 * j), o1 = off_of(2 * j + 1);
@@ -292,6 +329,7 @@ __global__ void __launch_bounds__(kMoveWarps * 32) kv4_move_kernel(const __grid_
       p[z] = x;
     }
   }
+  }
 }
 
 int check_args(const kvpool_kv4_evict_args* a, int32_t n, const int64_t* k_len, int64_t* most) {
@@ -349,14 +387,14 @@ cudaError_t launch_select(const EvictParams& P, int64_t slice, cudaStream_t s) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * (int)kMaxShared);
     if (e != cudaSuccess) return e;
   }
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = P.cluster;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  // not before the kernel ahead has ended: CTAs that wait hold the threads and the
+  // shared memory that it needs (a loop of evictions of 4 x 131,072 tokens 87 us a call instead of 79.5; the kernel that moves likewise)
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = P.cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, P);
 }
 
@@ -390,13 +428,13 @@ extern "C" int kvpool_kv4_evict(const kvpool_kv4_evict_args* a, int32_t n, const
     P->cluster *= 2;
   // keys of the longest segment's slice, as the kernel cuts it
   const int64_t warps = (int64_t)P->cluster * kSelWarps, between = std::max<int64_t>(0, most - a->n_sink - a->n_recent);
-  const int64_t slice = (((between + warps - 1) / warps + 31) & ~(int64_t)31) * kSelWarps;
+  const int64_t slice = (((between + warps - 1) / warps + 127) & ~(int64_t)127) * kSelWarps;
   for (int32_t i = 0; i < n;) {
     const int32_t first = i;
     P->n_segs = 0;
     int64_t tasks = 0;
     for (; i < n && P->n_segs < kKv4MaxSegs; ++i) {
-      const int64_t tiles = (std::min<int64_t>(h_k_len[i], a->keep) + kKv4Tile - 1) / kKv4Tile;
+      const int64_t tiles = (std::min<int64_t>(h_k_len[i], a->keep) + kMoveTiles * kKv4Tile - 1) / (kMoveTiles * kKv4Tile);
       if (tiles * hk > (1 << 30)) return KVPOOL_ERR_INVALID_ARG;
       if (tasks > 0 && tasks + tiles * hk > (1 << 30)) break;
       EvictSeg& S = P->segs[P->n_segs++];
@@ -414,8 +452,8 @@ extern "C" int kvpool_kv4_evict(const kvpool_kv4_evict_args* a, int32_t n, const
     cudaError_t e = slice <= kMaxShared ? launch_select<true>(*P, slice, s) : launch_select<false>(*P, slice, s);
     if (e == cudaSuccess && P->n_tasks > 0) {
       const dim3 grid((unsigned)((P->n_tasks + kMoveWarps - 1) / kMoveWarps)), block(kMoveWarps * 32);
-      e = a->cache.head_dim == 128 ? launch_kernel(true, kv4_move_kernel<128>, grid, block, 0, s, *P)
-                                   : launch_kernel(true, kv4_move_kernel<64>, grid, block, 0, s, *P);
+      e = a->cache.head_dim == 128 ? launch_kernel(false, kv4_move_kernel<128>, grid, block, 0, s, *P)
+                                   : launch_kernel(false, kv4_move_kernel<64>, grid, block, 0, s, *P);
     }
     if (e != cudaSuccess) return KVPOOL_ERR_CUDA;
   }
