@@ -51,6 +51,8 @@ struct EvictParams {
 
 // A larger weight has a larger key; -0 and +0 are alike and a NaN is the largest.
 __device__ __forceinline__ uint32_t weight_key(float w) { return w != w ? 0xFFFFFFFFu : score_key(w); }
+// the weight again (a NaN for any NaN, +0 for -0)
+__device__ __forceinline__ float key_weight(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k); }
 
 // SHARED: a CTA's slice of the weights stays in shared memory as keys (up to
 // kMaxShared of them), otherwise every pass reads it again.
@@ -104,12 +106,12 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const __grid_co
   };
   if (SHARED) {
 #pragma unroll 1
-    for (int i0 = a; i0 < b; i0 += 256) {
-      float x[8];
+    for (int i0 = a; i0 < b; i0 += 512) {
+      float x[16];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) x[u] = i0 + 32 * u + lane < b ? w[i0 + 32 * u + lane] : 0.0f;
+      for (int u = 0; u < 16; ++u) x[u] = i0 + 32 * u + lane < b ? w[i0 + 32 * u + lane] : 0.0f;
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
+      for (int u = 0; u < 16; ++u) {
         const int i = i0 + 32 * u + lane;
         if (i < a + per) slice[i - a] = i < b ? weight_key(x[u]) : 0u;
       }
@@ -199,7 +201,7 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const __grid_co
       if (gt || (eq && n_equal < left)) {
         const int to = P.sink + n_above + min(n_equal, left);
         index[to] = i + u;
-        if (ow) ow[to] = w[i + u];
+        if (ow) ow[to] = key_weight(key[u]);
       }
       n_above += gt;
       n_equal += eq;

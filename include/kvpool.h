@@ -592,8 +592,8 @@ int kvpool_kv4_attend(const kvpool_kv4_args* args, int32_t n, const int64_t* h_q
  * pages that are no row's of d_table (those stay as they were, so they may be
  * shared): its codes and scales are copied.  d_index: [n][kv_heads][keep], the
  * places the tokens had, -1 behind the last.  d_out_weights: NULL, or the weights of
- * what stays, zeros behind up to out_weight_width (at least keep); it lies apart
- * from d_weights.  Errors: INVALID_ARG, CUDA. */
+ * what stays (a zero's sign and a NaN's bits may change), zeros behind up to
+ * out_weight_width (at least keep); it lies apart from d_weights.  Errors: INVALID_ARG, CUDA. */
 typedef struct kvpool_kv4_evict_args {
   kvpool_kv4 cache;
   const int32_t* d_out_table;
