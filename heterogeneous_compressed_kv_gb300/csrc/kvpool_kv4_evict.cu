@@ -10,6 +10,7 @@
 // count by warp slices gives every slice its first place, and the places go out in
 // order.  The second moves the tokens, a warp to two tiles of 16 of them.
 #include <algorithm>
+#include <atomic>
 #include <memory>
 #include <new>
 
@@ -386,7 +387,13 @@ cudaError_t launch_select(const EvictParams& P, int64_t slice, cudaStream_t s) {
   cfg.stream = s;
   if (SHARED) {
     cfg.dynamicSmemBytes = 4 * slice;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * (int)kMaxShared);
+    static std::atomic<uint64_t> told;  // the devices (of 64) that know of the kernel's shared memory
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && !(told.load(std::memory_order_relaxed) >> dev & 1)) {
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * (int)kMaxShared);
+      if (e == cudaSuccess) told.fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
     if (e != cudaSuccess) return e;
   }
   // not before the kernel ahead has ended: CTAs that wait hold the threads and the

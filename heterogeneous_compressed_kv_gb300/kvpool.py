@@ -565,6 +565,9 @@ class Kv4Cache:
         self.index, self.device = pages.get_device(), pages.device
         self._at = pages.data_ptr(), pages.shape[0]
         self._kind = kv_heads, head_dim, page_tokens, k_scale, v_scale, 0
+        self._torch, self._lib = torch, lib()
+        self._device_now, self._stream_now = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+        self._types = {torch.bfloat16: BF16, torch.float32: F32}
 
     def _pack(self, table, n: int) -> bytes:
         ptr, stride, rows, width = _table(table, "table", self.index)
@@ -586,51 +589,59 @@ class Kv4Cache:
         """Store the next n_new[i] rows of k and v ([rows][key heads][dim],
         float32 or bfloat16) as the tokens of segment i from place start[i] on.
         See kvpool_kv4_store in include/kvpool.h."""
-        import torch
-        if torch._C._cuda_getDevice() != self.index:
-            with torch.cuda.device(self.index):
+        if self._device_now() != self.index:
+            with self._torch.cuda.device(self.index):
                 return self.store(k, v, table, start, n_new, stream)
         start, n_new = self._two(start, n_new, "store")
-        self._move(lib().kvpool_kv4_store, "store", k, v, table, start, n_new, False, stream)
+        like = _like(k)
+        if like[2] != self.index or like[1] != self.head_dim or k.shape != v.shape:
+            raise ValueError("store: k and v must be CUDA tensors alike, of the cache's head dim and on its device")
+        self._move(self._lib.kvpool_kv4_store, "store", like[0], k.shape[0], _rows(k, "k", like), _rows(v, "v", like), table,
+                   start, n_new, stream)
 
     def load(self, table, start, length, dtype=None, out_k=None, out_v=None, stream=None) -> tuple:
         """(k, v): segment i's length[i] tokens from place start[i] on, as the
         values that they stand for (bfloat16 unless dtype or out_k says float32).
         See kvpool_kv4_load in include/kvpool.h."""
-        import torch
-        if torch._C._cuda_getDevice() != self.index:
-            with torch.cuda.device(self.index):
+        if self._device_now() != self.index:
+            with self._torch.cuda.device(self.index):
                 return self.load(table, start, length, dtype, out_k, out_v, stream)
         start, length = self._two(start, length, "load")
-        if out_k is None or out_v is None:
-            given = out_k if out_k is not None else out_v
-            dtype = dtype if dtype is not None else torch.bfloat16 if given is None else given.dtype
-            shape = (sum(length.tolist()), self.kv_heads, self.head_dim)
-            if out_k is None:
-                out_k = self._empty(shape, dtype, stream)
-            if out_v is None:
-                out_v = self._empty(shape, dtype, stream)
-        self._move(lib().kvpool_kv4_load, "load", out_k, out_v, table, start, length, True, stream)
+        if out_k is None and out_v is None:
+            n, H, D = sum(length.tolist()), self.kv_heads, self.head_dim
+            if dtype is None:
+                dtype = self._torch.bfloat16
+            out_k, out_v = self._empty((n, H, D), dtype, stream), self._empty((n, H, D), dtype, stream)
+            k, v = (out_k.data_ptr(), H * D, D, H, 0), (out_v.data_ptr(), H * D, D, H, 0)
+        else:
+            if out_k is None or out_v is None:
+                o = out_k if out_k is not None else out_v
+                made = self._empty((sum(length.tolist()), self.kv_heads, self.head_dim), o.dtype if dtype is None else dtype, stream)
+                out_k, out_v = (made, o) if out_k is None else (o, made)
+            like = _like(out_k)
+            if like[2] != self.index or like[1] != self.head_dim or out_k.shape != out_v.shape:
+                raise ValueError("load: out_k and out_v must be CUDA tensors alike, of the cache's head dim and on its device")
+            dtype, n, k, v = like[0], out_k.shape[0], _rows(out_k, "out_k", like, True), _rows(out_v, "out_v", like, True)
+        self._move(self._lib.kvpool_kv4_load, "load", dtype, n, k, v, table, start, length, stream)
         return out_k, out_v
 
     def _empty(self, shape, dtype, stream):
         """A tensor whose memory belongs to the stream that will write it."""
-        import torch
+        torch = self._torch
         if stream is None:
             return torch.empty(shape, dtype=dtype, device=self.device)
         raw = _stream(stream)
-        if raw == torch._C._cuda_getCurrentRawStream(self.index):
+        if raw == self._stream_now(self.index):
             return torch.empty(shape, dtype=dtype, device=self.device)
         with torch.cuda.stream(torch.cuda.ExternalStream(raw, device=self.device)):
             return torch.empty(shape, dtype=dtype, device=self.device)
 
-    def _move(self, call, what, k, v, table, start, length, out, stream) -> None:
-        like = _like(k)
-        if like[2] != self.index or like[1] != self.head_dim or k.shape != v.shape:
-            raise ValueError("k and v must be CUDA tensors alike, of the cache's head dim and on its device")
-        rc = call(self._pack(table, start.size), _dtype(k), _HEADS.pack(*_rows(k, "k", like, out)),
-                  _HEADS.pack(*_rows(v, "v", like, out)), k.shape[0], start.size, start.tobytes(), length.tobytes(),
-                  _stream_of(stream, self.index))
+    def _move(self, call, what, dtype, n, k, v, table, start, length, stream) -> None:
+        kind = self._types.get(dtype)
+        if kind is None:
+            raise ValueError("tensors must be float32 or bfloat16")
+        rc = call(self._pack(table, start.size), kind, _HEADS.pack(*k), _HEADS.pack(*v), n, start.size, start.tobytes(),
+                  length.tobytes(), self._stream_now(self.index) if stream is None else _stream(stream))
         if rc != OK:
             self._done(rc, what)
 
@@ -644,13 +655,12 @@ class Kv4Cache:
         token got from its head's queries.  workspace: a uint8 CUDA tensor of
         workspace() bytes (one is allocated when None).  No gradients flow through.
         See kvpool_kv4_attend in include/kvpool.h."""
-        import torch
-        if torch._C._cuda_getDevice() != self.index:
-            with torch.cuda.device(self.index):
+        if self._device_now() != self.index:
+            with self._torch.cuda.device(self.index):
                 return self.attend(q, table, q_len, k_len, scale, out, lse, weights, decay, workspace, stream)
         if not q.is_cuda:
             raise ValueError("attend: q must be a CUDA tensor")
-        raw = _stream_of(stream, self.index)
+        raw = self._stream_now(self.index) if stream is None else _stream(stream)
         like = _like(q)
         rows = _rows(q, "q", like)
         if out is None:
@@ -660,7 +670,7 @@ class Kv4Cache:
         else:
             o = _rows(out, "out", like, True)
         call = self._call(q, like, rows, table, q_len, k_len, scale, out, o, lse, weights, decay)
-        L = lib()
+        L = self._lib
         rc = L.kvpool_kv4_workspace(*call)
         if rc >= 0:
             nbytes = 0
@@ -670,7 +680,7 @@ class Kv4Cache:
                 nbytes = workspace.numel() * workspace.element_size()
             elif rc > 0:
                 nbytes = rc
-                workspace = self._empty((rc,), torch.uint8, stream)
+                workspace = self._empty((rc,), self._torch.uint8, stream)
             rc = L.kvpool_kv4_attend(*call, workspace.data_ptr() if nbytes else None, nbytes, raw)
         if rc != OK:
             self._done(rc, "attend")
@@ -690,17 +700,18 @@ class Kv4Cache:
         return rc
 
     def _call(self, q, like, q_rows, table, q_len, k_len, scale, out, out_rows, lse, weights, decay):
-        import torch
-        if like[1] != self.head_dim or like[2] != self.index or out.shape != q.shape:
+        shape, kind = q.shape, self._types.get(like[0])
+        if kind is None:
+            raise ValueError("tensors must be float32 or bfloat16")
+        if like[1] != self.head_dim or like[2] != self.index or out.shape != shape:
             raise ValueError("attend: q and out must be alike, of the cache's head dim and on its device")
         ql, kl = self._two(q_len, k_len, "attend")
-        z = 0 if lse is None else _need(lse, "lse", torch.float32, q.shape[:2], self.index)
+        z = 0 if lse is None else _need(lse, "lse", self._torch.float32, shape[:2], self.index)
         w = (0, 0, 0)
         if weights is not None:
             w = _weights(weights, "weights", ql.size, self.kv_heads, max(kl.tolist(), default=0), self.index)
         try:
-            a = _KV4_ARGS.pack(_dtype(q), self.head_dim ** -0.5 if scale is None else scale, *q_rows, *out_rows, q.shape[0], z,
-                               *w, decay, 0)
+            a = _KV4_ARGS.pack(kind, self.head_dim ** -0.5 if scale is None else scale, *q_rows, *out_rows, shape[0], z, *w, decay, 0)
         except (struct.error, OverflowError) as e:
             raise ValueError(f"attend: {e}") from None
         return self._pack(table, ql.size) + a, ql.size, ql.tobytes(), kl.tobytes()
@@ -713,8 +724,8 @@ class Kv4Cache:
         out_weights): the places they had ([segments][key heads][keep] int32, -1
         behind the last) and their weights (zeros behind).  See kvpool_kv4_evict in
         include/kvpool.h."""
-        import torch
-        if torch._C._cuda_getDevice() != self.index:
+        torch = self._torch
+        if self._device_now() != self.index:
             with torch.cuda.device(self.index):
                 return self.evict(table, k_len, weights, keep, out_table, n_sink, n_recent, index, out_weights, stream)
         kl = _i64(k_len)
@@ -731,7 +742,7 @@ class Kv4Cache:
             a = _KV4_EVICT.pack(*ot, *w, *ow, at, out_weights.shape[2], keep, n_sink, n_recent)
         except (struct.error, OverflowError) as e:
             raise ValueError(f"evict: {e}") from None
-        self._done(lib().kvpool_kv4_evict(self._pack(table, n) + a, n, kl.tobytes(), _stream_of(stream, self.index)), "evict")
+        self._done(self._lib.kvpool_kv4_evict(self._pack(table, n) + a, n, kl.tobytes(), _stream_of(stream, self.index)), "evict")
         return index, out_weights
 
 
