@@ -3,7 +3,15 @@
 // Of 16 neighbouring values x of a head the cache holds s = e4m3(amax / 6), amax
 // their largest magnitude, and the nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6 to x / s
 // (ties to the even code); s times such a number has at most 6 bits, so what is
-// read back is exact in bf16 and fp16.
+// read back is exact in bf16.
+//
+// Bound: memory, at sizes that fill the GPU; the smallest call is one launch.  A
+// warp takes a tile of 16 tokens of one head, so that no two warps share a byte
+// (two tokens' values do), and asks for all of it before it needs the first row.
+// Measured (bf16, 16 heads of 128): 6,656 tokens stored 13.4 us (69.9 MB, 0.77 of
+// the copy rate; a value takes 8 instructions, the integer pipe is the next bound),
+// read back 9.3 us (the cache and much of the output stay in L2); 65,536 tokens of
+// 8 heads read back 53.9 us, 6.4 TB/s (0.94); 32 tokens 3.1 and 2.6 us.
 #include <algorithm>
 #include <cmath>
 #include <memory>

@@ -25,6 +25,20 @@
 // the largest so far, so that small ones are off by 2^-31 of that at most.  The
 // unit changes only when a weight passes 2^14 (a running maximum kept exactly
 // takes three shuffles and a rescaling test of every tile).
+//
+// Measured (heads of 128): one request behind 1,048,576 tokens of 16 heads 352 us
+// for 2.42 GB, 6.9 TB/s (1.01 of the measured copy); an eighth of it 57 us a call,
+// 49 inside the kernel.  64 requests of 1 to 16,384 tokens, 16 heads on 4, 69 us
+// (311 MB), with the tokens' weights 85 (their scores are 34 MB, written and read
+// again); 32 of 1 to 8,192 24 us for 76 MB, of which the kernel takes 16.6, 3.4
+// before its first data, and the merging launch after it 5.  A tile takes a warp
+// 260 instructions (64 conversions of codes, 64 products with scales, 16 matrix
+// instructions); issue slots 54% busy, the integer pipe 49%, the tensor pipe 30%.
+// Measured and not kept: a running maximum kept exactly (333 instructions to a
+// tile, 465 us for the million tokens); a CTA of four warps to a part of equal
+// length (ragged lengths leave 20% of a wave idle: 69 us where shares took 62) or
+// several waves of them (68); a CTA's share over several units (the ring drains at
+// each: 79 to 101 us); an exact division of rounds between warps by barriers.
 #include <algorithm>
 #include <atomic>
 #include <cmath>

@@ -9,6 +9,16 @@
 // weight that stays (histograms in shared memory, added up over the cluster), a
 // count by warp slices gives every slice its first place, and the places go out in
 // order.  The second moves the tokens, a warp to two tiles of 16 of them.
+//
+// Measured: 4 segments of 65,536 to 131,072 tokens x 8 heads of 128 cut to 16,384
+// 74 us: 29 the selection (of it 6 the weights' way in, 3.5 and three times 2.9 the
+// passes -- cluster barriers and remote sums --, 5 the places' way out), 43 the
+// moving (75 MB each way, of which reads fetch whole 64-byte pieces for a token's
+// 8 and 16 bytes of scales and every other nibble of its values: about 240 MB in
+// all).  16 of 2,048 to 4,096 tokens x 4 heads cut to 1,024 15 us (11 and 4), one
+// round of latencies after the other.
+// Measured and not kept: eight histograms of the first pass, one to every eighth
+// lane (33.8 us where one took 32.2).
 #include <algorithm>
 #include <atomic>
 #include <memory>

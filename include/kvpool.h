@@ -501,7 +501,7 @@ int kvpool_window_attend(const kvpool_window_args* args, int32_t n, const int64_
  * s = e4m3(amax / 6), amax their largest magnitude (the fp32 quotient, to the
  * nearest, at most 448); a value is held as the nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6
  * to x / s (ties to the even code) with its sign, and stands for s times that
- * times k_scale, which fp16 and bf16 hold exactly.  Values whose group has s = 0
+ * times k_scale, which bf16 holds exactly.  Values whose group has s = 0
  * (amax <= 6 * 2^-10) are zeros, larger ones than 2688 are 2688; a group that holds
  * a NaN or an infinity stands for NaNs.  k_scale, v_scale: powers of two, 2^-16 to 2^16.
  * head_dim 64 or 128; up to 1024 key heads; a segment has at most 2^30 tokens.
