@@ -151,7 +151,7 @@ __device__ __forceinline__ Scale<KVPOOL_F32> scale_of(const Raw8<KVPOOL_F32>& ra
 // number (8 bits) is 6 times a border between two scales (5 bits), or a border
 // between two codes times a scale (7 bits), or at least 2^-8 of it away, where the
 // product is off by 2^-22 of it and the rounding (to fp16's 11 bits; to multiples of
-// 2^-11 beside borders from 0.25 to 5) by less than 2^-10.  (With quotients 6,144
+// 2^-11 beside borders from 0.25 to 5) by less than 2^-10.  (With quotients 6,656
 // tokens of 16 heads x 128 took 30.9 us.)
 __device__ __forceinline__ Scale<KVPOOL_BF16> scale_of(const Raw8<KVPOOL_BF16>& raw, float inv_scale) {
   constexpr uint32_t kAbs = 0x7FFF7FFFu;

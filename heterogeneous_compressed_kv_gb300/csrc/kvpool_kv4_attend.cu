@@ -6,9 +6,9 @@
 //   weights[t] = decay * weights[t] + sum over the key head's query rows of
 //   exp(scale <q, k_t> - lse).
 //
-// A segment with at most 64 query rows to a key head (single tokens, drafts)
-// goes through the kernel below; a longer one's tokens are read back to bf16
-// (exact) or fp32 rows and go through window attention.
+// Single tokens, drafts and all fp32 queries go through the kernel below; the
+// tokens of longer bf16 segments are read back to bf16 rows (exact) and go through
+// window attention where that pays.
 //
 // Bound: reading the cache, 1.125 bytes for a key's and a value's number.  The
 // whole list of keys, across segments and heads, is cut into equal shares, one to
@@ -38,7 +38,9 @@
 // tile, 465 us for the million tokens); a CTA of four warps to a part of equal
 // length (ragged lengths leave 20% of a wave idle: 69 us where shares took 62) or
 // several waves of them (68); a CTA's share over several units (the ring drains at
-// each: 79 to 101 us); an exact division of rounds between warps by barriers.
+// each: 79 to 101 us); barriers that keep a CTA's warps together; skipping pairs
+// that no row of a tile sees (fp32 prompts among their own tokens 81 -> 72 us, but
+// the registers it takes cost single tokens 3 to 8%).
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -55,9 +57,9 @@
 namespace kvp {
 namespace {
 
-constexpr int kMaxGroup = 16;   // query heads per key head
-constexpr int kMaxRows = 64;    // query rows per key head of this file's kernel
-constexpr int kPair = 2;        // tiles of a stage
+constexpr int kMaxGroup = 16;  // query heads per key head
+constexpr int kMaxRows = 64;   // query rows per key head whose weights are summed; bf16 rows that are no prompt
+constexpr int kPair = 2;       // tiles of a stage
 constexpr float kUp = 6.0f, kMost = 14.0f;  // see the kernel's c
 
 // A launch is one list of pairs of tiles: segments in order, of each its units
@@ -275,7 +277,7 @@ __global__ void __launch_bounds__(kv4_warps(NT, F32) * 32, 1) kv4_attend_kernel(
     if (lane != 0) return;
     uint64_t* mb = &sm.bar[to];
     uint8_t* dst = sm.ring[to];
-    if (p0 < 0) {  // (a segment without tokens)
+    if (p0 < 0) {  // a segment without tokens: its scores are all masked
       mbar_arrive(mb);
     } else if (P.c.page_shift > 0) {  // both tiles in one page
       mbar_arrive_expect_tx(mb, kPair * L::kBytes);
@@ -292,349 +294,351 @@ __global__ void __launch_bounds__(kv4_warps(NT, F32) * 32, 1) kv4_attend_kernel(
   int done = 0;
 #pragma unroll 1
   do {  // (a share has a pair at least; a CTA's warp may have none of its unit)
-  // ---- a part: the share's keys of a unit ----
-  if (!UNIT)
-    while (seg + 1 < P.n_segs && P.segs[seg + 1].pair_base <= x_first + done) ++seg;
-  const Kv4Seg& S = P.segs[seg];
-  const int pairs = seg_pairs(S), unit = UNIT ? blockIdx.x - S.unit_base : unit_of(S, pairs, x_first + done);
-  const int a = (int)(x_first + done - S.pair_base - (int64_t)unit * pairs);  // the part's pairs of the unit: a .. b - 1
-  const int b = min(pairs, a + (n_my - done));
-  const bool first_unit = done == 0, whole_unit = b - a == pairs;
-  done += b - a;
-  const int n_rows = S.q_len * P.group;
-  const int head = unit % P.c.kv_heads, row0 = unit / P.c.kv_heads * P.tile_rows;
-  const int rows = min(P.tile_rows, n_rows - row0);
-  const int pos0 = S.k_len - S.q_len + row0 / P.group;  // the first row's place
+    // ---- a part: the share's keys of a unit ----
+    if (!UNIT)
+      while (seg + 1 < P.n_segs && P.segs[seg + 1].pair_base <= x_first + done) ++seg;
+    const Kv4Seg& S = P.segs[seg];
+    const int pairs = seg_pairs(S), unit = UNIT ? blockIdx.x - S.unit_base : unit_of(S, pairs, x_first + done);
+    const int a = (int)(x_first + done - S.pair_base - (int64_t)unit * pairs);  // the part's pairs of the unit: a .. b - 1
+    const int b = min(pairs, a + (n_my - done));
+    const bool first_unit = done == 0, whole_unit = b - a == pairs;
+    done += b - a;
+    const int n_rows = S.q_len * P.group;
+    const int head = unit % P.c.kv_heads, row0 = unit / P.c.kv_heads * P.tile_rows;
+    const int rows = min(P.tile_rows, n_rows - row0);
+    const int pos0 = S.k_len - S.q_len + row0 / P.group;  // the first row's place
 
-  // ---- queries: row 8n + g, dims D / 4 * t .. as fp16 pieces ----
-  constexpr int vb = F32 ? 4 : 2;
-  uint32_t q[kPieces][NT][2 * KS];
-  float mul[NT][2];  // score scale of rows 8n + 2t, + 1
-  int pos[NT][2];
+    // ---- queries: row 8n + g, dims D / 4 * t .. as fp16 pieces ----
+    constexpr int vb = F32 ? 4 : 2;
+    uint32_t q[kPieces][NT][2 * KS];
+    float mul[NT][2];  // score scale of rows 8n + 2t, + 1
+    int pos[NT][2];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    float x[4 * KS];
-    const int row = row0 + 8 * n + g;
-    const uint8_t* p = P.q + vb * ((S.q_row0 + row / P.group) * P.q_tok +
-                                   (int64_t)(head * P.group + row % P.group) * P.q_head + 4 * KS * t);
-    uint32_t amax = 0;
+    for (int n = 0; n < NT; ++n) {
+      float x[4 * KS];
+      const int row = row0 + 8 * n + g;
+      const uint8_t* p = P.q + vb * ((S.q_row0 + row / P.group) * P.q_tok +
+                                     (int64_t)(head * P.group + row % P.group) * P.q_head + 4 * KS * t);
+      uint32_t amax = 0;
 #pragma unroll
-    for (int i = 0; i < 4 * KS; i += 16 / vb) {
-      uint4 w = make_uint4(0, 0, 0, 0);
-      if (8 * n + g < rows) w = *reinterpret_cast<const uint4*>(p + vb * i);
-      const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if constexpr (F32) {
-          x[i + j] = __uint_as_float(v[j]);
-        } else {
-          x[i + 2 * j] = __uint_as_float(v[j] << 16);
-          x[i + 2 * j + 1] = __uint_as_float(v[j] & 0xFFFF0000u);
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 4 * KS; ++i) amax = max(amax, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    // 2^(14 - e), e the exponent of the largest value (at least -110)
-    const int e = max((int)(amax >> 23) - 127, -110);
-    const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23), down = __uint_as_float((uint32_t)(127 - 14 + e) << 23);
-#pragma unroll
-    for (int i = 0; i < 2 * KS; ++i) {
-      const float x0 = x[2 * i] * up, x1 = x[2 * i + 1] * up;
-      q[0][n][i] = pack_f16(x0, x1);
-      if constexpr (F32) {
-        const float2 h = unpack_f16(q[0][n][i]);
-        q[1][n][i] = pack_f16(x0 - h.x, x1 - h.y);
-      }
-    }
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      mul[n][c] = P.scale_log2 * __shfl_sync(0xffffffffu, down, 4 * (2 * t + c));
-      pos[n][c] = min(S.k_len - 1, S.k_len - S.q_len + (row0 + 8 * n + 2 * t + c) / P.group);
-    }
-  }
-
-  // A row's weights are 2^(score + c): c is such that the largest score seen when
-  // it was last set gave 2^kUp, and is set anew when one passes 2^kMost (`most`;
-  // -inf before the row's first score).
-  float c[NT][2], most[NT][2], l[NT][2], o[NT][D / 16][4];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    c[n][0] = c[n][1] = 0.0f;
-    most[n][0] = most[n][1] = -INFINITY;
-    l[n][0] = l[n][1] = 0.0f;
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) o[n][i][j] = 0.0f;
-  }
-  float* scores = nullptr;
-  const int pitch = score_pitch(S.k_len);
-  if (P.scores) scores = P.scores + S.score_base + ((int64_t)head * n_rows + row0) * pitch;
-
-  // ---- pairs of tiles ----
-#pragma unroll 1
-  for (int i = a; i < b; ++i) {
-    if (!warp_wait(&sm.bar[stage], phase, P.c.err)) {  // (flagged) the copies on their way, then the end
-      for (int j = done - b + i + 1; j < issued; ++j) {
-        if (++stage == kStages) stage = 0, phase ^= 1;
-        warp_wait(&sm.bar[stage], phase, P.c.err);
-      }
-      if (!UNIT) return;
-      break;
-    }
-    const uint8_t* ring = sm.ring[stage];
-    const int u0 = i * kPair * kKv4Tile;
-    float s[kPair][NT][4];  // [2i + c]: key g + 8i of the tile, row 8n + 2t + c
-#pragma unroll
-    for (int y = 0; y < kPair; ++y) {
-      Kv4Keys<D> K;
-      K.load(ring + y * L::kBytes, lane);
-      float s2[NT][4];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s[y][n][j] = s2[n][j] = 0.0f;
-#pragma unroll
-      for (int w = 0; w < D / 32; ++w) {
-        uint32_t k0[4], k1[4];
-        e2m1x8_to_f16x2x4(K.k0[w], k0);
-        e2m1x8_to_f16x2x4(K.k1[w], k1);
+      for (int i = 0; i < 4 * KS; i += 16 / vb) {
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (8 * n + g < rows) w = *reinterpret_cast<const uint4*>(p + vb * i);
+        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          k0[j] = mul_f16x2(k0[j], K.sc[0][w / 2]);
-          k1[j] = mul_f16x2(k1[j], K.sc[1][w / 2]);
-        }
-#pragma unroll
-        for (int x = kPieces - 1; x >= 0; --x)
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            mma_f16(s[y][n], k0[0], k1[0], k0[1], k1[1], q[x][n][4 * w], q[x][n][4 * w + 1]);
-            mma_f16(s2[n], k0[2], k1[2], k0[3], k1[3], q[x][n][4 * w + 2], q[x][n][4 * w + 3]);
+          if constexpr (F32) {
+            x[i + j] = __uint_as_float(v[j]);
+          } else {
+            x[i + 2 * j] = __uint_as_float(v[j] << 16);
+            x[i + 2 * j + 1] = __uint_as_float(v[j] & 0xFFFF0000u);
           }
+        }
       }
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int i = 0; i < 4 * KS; ++i) amax = max(amax, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      // 2^(14 - e), e the exponent of the largest value (at least -110)
+      const int e = max((int)(amax >> 23) - 127, -110);
+      const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23), down = __uint_as_float((uint32_t)(127 - 14 + e) << 23);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[y][n][j] += s2[n][j];
+      for (int i = 0; i < 2 * KS; ++i) {
+        const float x0 = x[2 * i] * up, x1 = x[2 * i + 1] * up;
+        q[0][n][i] = pack_f16(x0, x1);
+        if constexpr (F32) {
+          const float2 h = unpack_f16(q[0][n][i]);
+          q[1][n][i] = pack_f16(x0 - h.x, x1 - h.y);
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        mul[n][c] = P.scale_log2 * __shfl_sync(0xffffffffu, down, 4 * (2 * t + c));
+        pos[n][c] = min(S.k_len - 1, S.k_len - S.q_len + (row0 + 8 * n + 2 * t + c) / P.group);
+      }
     }
-    if (scores) {
+
+    // A row's weights are 2^(score + c): c is such that the largest score seen when
+    // it was last set gave 2^kUp, and is set anew when one passes 2^kMost (`most`;
+    // -inf before the row's first score).
+    float c[NT][2], most[NT][2], l[NT][2], o[NT][D / 16][4];
 #pragma unroll
-      for (int y = 0; y < kPair; ++y)
+    for (int n = 0; n < NT; ++n) {
+      c[n][0] = c[n][1] = 0.0f;
+      most[n][0] = most[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[n][i][j] = 0.0f;
+    }
+    float* scores = nullptr;
+    const int pitch = score_pitch(S.k_len);
+    if (P.scores) scores = P.scores + S.score_base + ((int64_t)head * n_rows + row0) * pitch;
+
+    // ---- pairs of tiles ----
+#pragma unroll 1
+    for (int i = a; i < b; ++i) {
+      if (!warp_wait(&sm.bar[stage], phase, P.c.err)) {  // (flagged) the copies on their way, then the end
+        for (int j = done - b + i + 1; j < issued; ++j) {
+          if (++stage == kStages) stage = 0, phase ^= 1;
+          warp_wait(&sm.bar[stage], phase, P.c.err);
+        }
+        if (!UNIT) return;
+        break;
+      }
+      const uint8_t* ring = sm.ring[stage];
+      const int u0 = i * kPair * kKv4Tile;
+      float s[kPair][NT][4];  // [2i + c]: key g + 8i of the tile, row 8n + 2t + c
+#pragma unroll
+      for (int y = 0; y < kPair; ++y) {
+        Kv4Keys<D> K;
+        K.load(ring + y * L::kBytes, lane);
+        float s2[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[y][n][j] = s2[n][j] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) {
+          uint32_t k0[4], k1[4];
+          e2m1x8_to_f16x2x4(K.k0[w], k0);
+          e2m1x8_to_f16x2x4(K.k1[w], k1);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const int row = 8 * n + 2 * t + (j & 1), u = u0 + kKv4Tile * y + g + 8 * (j >> 1);
-            if (row < rows && u < S.k_len)
-              scores[(int64_t)row * pitch + u] = u <= pos[n][j & 1] ? s[y][n][j] * mul[n][j & 1] : -INFINITY;
+            k0[j] = mul_f16x2(k0[j], K.sc[0][w / 2]);
+            k1[j] = mul_f16x2(k1[j], K.sc[1][w / 2]);
           }
-    }
-    bool high = false;
 #pragma unroll
-    for (int y = 0; y < kPair; ++y)
+          for (int x = kPieces - 1; x >= 0; --x)
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+            for (int n = 0; n < NT; ++n) {
+              mma_f16(s[y][n], k0[0], k1[0], k0[1], k1[1], q[x][n][4 * w], q[x][n][4 * w + 1]);
+              mma_f16(s2[n], k0[2], k1[2], k0[3], k1[3], q[x][n][4 * w + 2], q[x][n][4 * w + 3]);
+            }
+        }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[y][n][j] = fmaf(s[y][n][j], mul[n][j & 1], c[n][j & 1]);
-    if (u0 + kPair * kKv4Tile - 1 > pos0) {  // some row does not see some key
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[y][n][j] += s2[n][j];
+      }
+      if (scores) {
+#pragma unroll
+        for (int y = 0; y < kPair; ++y)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int row = 8 * n + 2 * t + (j & 1), u = u0 + kKv4Tile * y + g + 8 * (j >> 1);
+              if (row < rows && u < S.k_len)
+                scores[(int64_t)row * pitch + u] = u <= pos[n][j & 1] ? s[y][n][j] * mul[n][j & 1] : -INFINITY;
+            }
+      }
+      bool high = false;
 #pragma unroll
       for (int y = 0; y < kPair; ++y)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (u0 + kKv4Tile * y + g + 8 * (j >> 1) > pos[n][j & 1]) s[y][n][j] = -INFINITY;
-    }
-    float mx[NT][2];
+          for (int j = 0; j < 4; ++j) s[y][n][j] = fmaf(s[y][n][j], mul[n][j & 1], c[n][j & 1]);
+      if (u0 + kPair * kKv4Tile - 1 > pos0) {  // some row does not see some key
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+        for (int y = 0; y < kPair; ++y)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        mx[n][e] = fmaxf(fmaxf(s[0][n][e], s[0][n][2 + e]), fmaxf(s[1][n][e], s[1][n][2 + e]));
-        high |= mx[n][e] > most[n][e];
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (u0 + kKv4Tile * y + g + 8 * (j >> 1) > pos[n][j & 1]) s[y][n][j] = -INFINITY;
       }
-    if (__any_sync(0xffffffffu, high)) {
+      float mx[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-#pragma unroll
-          for (int off = 4; off < 32; off <<= 1) mx[n][e] = fmaxf(mx[n][e], __shfl_xor_sync(0xffffffffu, mx[n][e], off));
-          if (!(mx[n][e] > most[n][e])) continue;
-          const float d = kUp - mx[n][e], f = ex2f(d);  // (the first time, l and o are zeros or NaN)
-          c[n][e] += d;
-          most[n][e] = kMost;
-          l[n][e] = l[n][e] == 0.0f ? 0.0f : l[n][e] * f;
-#pragma unroll
-          for (int y = 0; y < kPair; ++y) s[y][n][e] += d, s[y][n][2 + e] += d;
-#pragma unroll
-          for (int x = 0; x < D / 16; ++x) {
-            o[n][x][e] = o[n][x][e] == 0.0f ? 0.0f : o[n][x][e] * f;
-            o[n][x][2 + e] = o[n][x][2 + e] == 0.0f ? 0.0f : o[n][x][2 + e] * f;
-          }
+          mx[n][e] = fmaxf(fmaxf(s[0][n][e], s[0][n][2 + e]), fmaxf(s[1][n][e], s[1][n][2 + e]));
+          high |= mx[n][e] > most[n][e];
         }
-    }
+      if (__any_sync(0xffffffffu, high)) {
 #pragma unroll
-    for (int y = 0; y < kPair; ++y) {
-      uint32_t pt[kPieces][NT][2];  // [keys 0 - 7, 8 - 15]
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
+          for (int e = 0; e < 2; ++e) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[y][n][j] = ex2f(s[y][n][j]);
-        l[n][0] += s[y][n][0] + s[y][n][2];  // this lane's keys only
-        l[n][1] += s[y][n][1] + s[y][n][3];
+            for (int off = 4; off < 32; off <<= 1) mx[n][e] = fmaxf(mx[n][e], __shfl_xor_sync(0xffffffffu, mx[n][e], off));
+            if (!(mx[n][e] > most[n][e])) continue;
+            const float d = kUp - mx[n][e], f = ex2f(d);  // (the first time, l and o are zeros or NaN)
+            c[n][e] += d;
+            most[n][e] = kMost;
+            l[n][e] = l[n][e] == 0.0f ? 0.0f : l[n][e] * f;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint32_t pk = pack_f16(s[y][n][2 * j], s[y][n][2 * j + 1]);
-          if constexpr (F32) {
-            const float2 h = unpack_f16(pk);
-            pt[1][n][j] = transpose8x8(pack_f16(s[y][n][2 * j] - h.x, s[y][n][2 * j + 1] - h.y));
-          }
-          pt[0][n][j] = transpose8x8(pk);  // row g, keys 2t, 2t + 1 (+ 8)
-        }
-      }
-      // values: lane's dims D / 8 * g and on of the token pairs t and t + 4
-      constexpr int W = D / 32;  // words of 4 dims
-      uint32_t v0[W], v1[W];
-      const uint8_t* tile = ring + y * L::kBytes;
-      const uint8_t* p = tile + L::kV + t * D + (g ^ kv4_swizzle<D>(t)) * L::kChunk;  // (t and t + 4 swizzle alike)
-      if constexpr (D == 128) {
-        const uint4 x = *reinterpret_cast<const uint4*>(p), z = *reinterpret_cast<const uint4*>(p + 4 * D);
-        v0[0] = x.x, v0[1] = x.y, v0[2] = x.z, v0[3] = x.w;
-        v1[0] = z.x, v1[1] = z.y, v1[2] = z.z, v1[3] = z.w;
-      } else {
-        const uint2 x = *reinterpret_cast<const uint2*>(p), z = *reinterpret_cast<const uint2*>(p + 4 * D);
-        v0[0] = x.x, v0[1] = x.y;
-        v1[0] = z.x, v1[1] = z.y;
-      }
-      const int grp = g * L::kChunk / kKv4Group;
-      uint32_t e0 = *reinterpret_cast<const uint16_t*>(tile + L::kVs + t * (D / 8) + 2 * grp);
-      uint32_t e1 = *reinterpret_cast<const uint16_t*>(tile + L::kVs + (t + 4) * (D / 8) + 2 * grp);
-      if (u0 + kKv4Tile * (y + 1) > S.k_len) {  // places behind the last token may hold anything
-        const int left = S.k_len - u0 - kKv4Tile * y - 2 * t;
-        e0 &= left >= 2 ? 0xFFFFu : left == 1 ? 0xFFu : 0u;
-        e1 &= left >= 10 ? 0xFFFFu : left == 9 ? 0xFFu : 0u;
-      }
-      const uint32_t f0 = e4m3x2_to_f16x2((uint16_t)e0), f1 = e4m3x2_to_f16x2((uint16_t)e1);
+            for (int y = 0; y < kPair; ++y) s[y][n][e] += d, s[y][n][2 + e] += d;
 #pragma unroll
-      for (int w = 0; w < W; ++w) {
-        uint32_t x[4], z[4];
-        e2m1x8_to_f16x2x4(v0[w], x);
-        e2m1x8_to_f16x2x4(v1[w], z);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          x[j] = mul_f16x2(x[j], f0);
-          z[j] = mul_f16x2(z[j], f1);
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            if constexpr (F32) {  // a tile's own sum, added with rounding (the tensor core cuts a running sum off)
-              float d[4] = {0.f, 0.f, 0.f, 0.f};
-              mma_f16(d, x[2 * j], x[2 * j + 1], z[2 * j], z[2 * j + 1], pt[1][n][0], pt[1][n][1]);
-              mma_f16(d, x[2 * j], x[2 * j + 1], z[2 * j], z[2 * j + 1], pt[0][n][0], pt[0][n][1]);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) o[n][2 * w + j][k] += d[k];
-            } else {
-              mma_f16(o[n][2 * w + j], x[2 * j], x[2 * j + 1], z[2 * j], z[2 * j + 1], pt[0][n][0], pt[0][n][1]);
+            for (int x = 0; x < D / 16; ++x) {
+              o[n][x][e] = o[n][x][e] == 0.0f ? 0.0f : o[n][x][e] * f;
+              o[n][x][2 + e] = o[n][x][2 + e] == 0.0f ? 0.0f : o[n][x][2 + e] * f;
             }
           }
       }
-    }
-    __syncwarp();  // the pair is read
-    if (issued < n_my) issue(stage);
-    if (++stage == kStages) stage = 0, phase ^= 1;
-  }
-
-  // ---- the part's rows: dims D / 8 * g and on of rows 8n + 2t, + 1 ----
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
+      for (int y = 0; y < kPair; ++y) {
+        uint32_t pt[kPieces][NT][2];  // [keys 0 - 7, 8 - 15]
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float sum = l[n][e];
+        for (int n = 0; n < NT; ++n) {
 #pragma unroll
-      for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-      const float m = sum == 0.0f ? -INFINITY : -c[n][e];  // the exponent of the weights' unit
-      const int row = 8 * n + 2 * t + e, gr = row0 + row;
-      float y[D / 8];
+          for (int j = 0; j < 4; ++j) s[y][n][j] = ex2f(s[y][n][j]);
+          l[n][0] += s[y][n][0] + s[y][n][2];  // this lane's keys only
+          l[n][1] += s[y][n][1] + s[y][n][3];
 #pragma unroll
-      for (int x = 0; x < D / 16; ++x) y[2 * x] = o[n][x][e], y[2 * x + 1] = o[n][x][2 + e];
-      if constexpr (UNIT) {
-#pragma unroll
-        for (int x = 0; x < D / 8; x += 4)
-          *reinterpret_cast<float4*>(&sm.o[row][L::kChunk * g + x]) = make_float4(y[x], y[x + 1], y[x + 2], y[x + 3]);
-        if (g == 0) sm.ml[row] = make_float2(m, sum);
-        continue;
-      }
-      if (row >= rows) continue;
-      if (!whole_unit) {
-        const int64_t pr = (2 * (int64_t)share + (first_unit ? 0 : 1)) * P.tile_rows + row;
-#pragma unroll
-        for (int x = 0; x < D / 8; x += 4)
-          *reinterpret_cast<float4*>(P.part_o + pr * D + L::kChunk * g + x) = make_float4(y[x], y[x + 1], y[x + 2], y[x + 3]);
-        if (g == 0) P.part_ml[pr] = make_float2(m, sum);
-        continue;
-      }
-      const float inv = sum > 0.0f ? P.c.v_scale / sum : sum == 0.0f ? 0.0f : sum;  // (a NaN stays one)
-      const int64_t tok = S.q_row0 + gr / P.group;
-      const int h = head * P.group + gr % P.group;
-      const int64_t at = tok * P.o_tok + h * P.o_head + L::kChunk * g;
-#pragma unroll
-      for (int x = 0; x < D / 8; x += 8) {
-        if constexpr (F32) {
-          *reinterpret_cast<float4*>(P.out + 4 * (at + x)) = make_float4(y[x] * inv, y[x + 1] * inv, y[x + 2] * inv, y[x + 3] * inv);
-          *reinterpret_cast<float4*>(P.out + 4 * (at + x + 4)) =
-              make_float4(y[x + 4] * inv, y[x + 5] * inv, y[x + 6] * inv, y[x + 7] * inv);
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t pk = pack_f16(s[y][n][2 * j], s[y][n][2 * j + 1]);
+            if constexpr (F32) {
+              const float2 h = unpack_f16(pk);
+              pt[1][n][j] = transpose8x8(pack_f16(s[y][n][2 * j] - h.x, s[y][n][2 * j + 1] - h.y));
+            }
+            pt[0][n][j] = transpose8x8(pk);  // row g, keys 2t, 2t + 1 (+ 8)
+          }
+        }
+        // values: lane's dims D / 8 * g and on of the token pairs t and t + 4
+        constexpr int W = D / 32;  // words of 4 dims
+        uint32_t v0[W], v1[W];
+        const uint8_t* tile = ring + y * L::kBytes;
+        const uint8_t* p = tile + L::kV + t * D + (g ^ kv4_swizzle<D>(t)) * L::kChunk;  // (t and t + 4 swizzle alike)
+        if constexpr (D == 128) {
+          const uint4 x = *reinterpret_cast<const uint4*>(p), z = *reinterpret_cast<const uint4*>(p + 4 * D);
+          v0[0] = x.x, v0[1] = x.y, v0[2] = x.z, v0[3] = x.w;
+          v1[0] = z.x, v1[1] = z.y, v1[2] = z.z, v1[3] = z.w;
         } else {
-          *reinterpret_cast<uint4*>(P.out + 2 * (at + x)) =
-              make_uint4(pack_bf16(y[x] * inv, y[x + 1] * inv), pack_bf16(y[x + 2] * inv, y[x + 3] * inv),
-                         pack_bf16(y[x + 4] * inv, y[x + 5] * inv), pack_bf16(y[x + 6] * inv, y[x + 7] * inv));
+          const uint2 x = *reinterpret_cast<const uint2*>(p), z = *reinterpret_cast<const uint2*>(p + 4 * D);
+          v0[0] = x.x, v0[1] = x.y;
+          v1[0] = z.x, v1[1] = z.y;
+        }
+        const int grp = g * L::kChunk / kKv4Group;
+        uint32_t e0 = *reinterpret_cast<const uint16_t*>(tile + L::kVs + t * (D / 8) + 2 * grp);
+        uint32_t e1 = *reinterpret_cast<const uint16_t*>(tile + L::kVs + (t + 4) * (D / 8) + 2 * grp);
+        if (u0 + kKv4Tile * (y + 1) > S.k_len) {  // places behind the last token may hold anything
+          const int left = S.k_len - u0 - kKv4Tile * y - 2 * t;
+          e0 &= left >= 2 ? 0xFFFFu : left == 1 ? 0xFFu : 0u;
+          e1 &= left >= 10 ? 0xFFFFu : left == 9 ? 0xFFu : 0u;
+        }
+        const uint32_t f0 = e4m3x2_to_f16x2((uint16_t)e0), f1 = e4m3x2_to_f16x2((uint16_t)e1);
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          uint32_t x[4], z[4];
+          e2m1x8_to_f16x2x4(v0[w], x);
+          e2m1x8_to_f16x2x4(v1[w], z);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            x[j] = mul_f16x2(x[j], f0);
+            z[j] = mul_f16x2(z[j], f1);
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              if constexpr (F32) {  // a tile's own sum, added with rounding (the tensor core cuts a running sum off)
+                float d[4] = {0.f, 0.f, 0.f, 0.f};
+                mma_f16(d, x[2 * j], x[2 * j + 1], z[2 * j], z[2 * j + 1], pt[1][n][0], pt[1][n][1]);
+                mma_f16(d, x[2 * j], x[2 * j + 1], z[2 * j], z[2 * j + 1], pt[0][n][0], pt[0][n][1]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[n][2 * w + j][k] += d[k];
+              } else {
+                mma_f16(o[n][2 * w + j], x[2 * j], x[2 * j + 1], z[2 * j], z[2 * j + 1], pt[0][n][0], pt[0][n][1]);
+              }
+            }
         }
       }
-      if (g == 0) {
-        const float z = lse2_of(m, sum);
-        if (P.lse) P.lse[tok * (P.c.kv_heads * P.group) + h] = z * 0.69314718055994531f;
-        if (P.lse2) P.lse2[S.row_base + head * n_rows + gr] = z;
-      }
+      __syncwarp();  // the pair is read
+      if (issued < n_my) issue(stage);
+      if (++stage == kStages) stage = 0, phase ^= 1;
     }
-  if constexpr (UNIT) {
-    __syncthreads();
-    const Kv4Smem<D>* all = reinterpret_cast<const Kv4Smem<D>*>(smem_raw);
-    const int warps = blockDim.x >> 5;
-    for (int i = threadIdx.x; i < rows * (D / 4); i += blockDim.x) {
-      const int row = i / (D / 4), x = 4 * (i % (D / 4)), gr = row0 + row;
-      float mx = -INFINITY;
-      for (int k = 0; k < warps; ++k) mx = fmaxf(mx, all[k].ml[row].x);
-      const float base = mx == -INFINITY ? 0.0f : mx;
-      float sum = 0.0f;
-      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+
+    // ---- the part's rows: dims D / 8 * g and on of rows 8n + 2t, + 1 ----
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float sum = l[n][e];
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        const float m = sum == 0.0f ? -INFINITY : -c[n][e];  // the exponent of the weights' unit
+        const int row = 8 * n + 2 * t + e, gr = row0 + row;
+        float y[D / 8];
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) y[2 * x] = o[n][x][e], y[2 * x + 1] = o[n][x][2 + e];
+        if constexpr (UNIT) {
+#pragma unroll
+          for (int x = 0; x < D / 8; x += 4)
+            *reinterpret_cast<float4*>(&sm.o[row][L::kChunk * g + x]) = make_float4(y[x], y[x + 1], y[x + 2], y[x + 3]);
+          if (g == 0) sm.ml[row] = make_float2(m, sum);
+          continue;
+        }
+        if (row >= rows) continue;
+        if (!whole_unit) {
+          const int64_t pr = (2 * (int64_t)share + (first_unit ? 0 : 1)) * P.tile_rows + row;
+#pragma unroll
+          for (int x = 0; x < D / 8; x += 4)
+            *reinterpret_cast<float4*>(P.part_o + pr * D + L::kChunk * g + x) = make_float4(y[x], y[x + 1], y[x + 2], y[x + 3]);
+          if (g == 0) P.part_ml[pr] = make_float2(m, sum);
+          continue;
+        }
+        const float inv = sum > 0.0f ? P.c.v_scale / sum : sum == 0.0f ? 0.0f : sum;  // (a NaN stays one)
+        const int64_t tok = S.q_row0 + gr / P.group;
+        const int h = head * P.group + gr % P.group;
+        const int64_t at = tok * P.o_tok + h * P.o_head + L::kChunk * g;
+#pragma unroll
+        for (int x = 0; x < D / 8; x += 8) {
+          if constexpr (F32) {
+            *reinterpret_cast<float4*>(P.out + 4 * (at + x)) =
+                make_float4(y[x] * inv, y[x + 1] * inv, y[x + 2] * inv, y[x + 3] * inv);
+            *reinterpret_cast<float4*>(P.out + 4 * (at + x + 4)) =
+                make_float4(y[x + 4] * inv, y[x + 5] * inv, y[x + 6] * inv, y[x + 7] * inv);
+          } else {
+            *reinterpret_cast<uint4*>(P.out + 2 * (at + x)) =
+                make_uint4(pack_bf16(y[x] * inv, y[x + 1] * inv), pack_bf16(y[x + 2] * inv, y[x + 3] * inv),
+                           pack_bf16(y[x + 4] * inv, y[x + 5] * inv), pack_bf16(y[x + 6] * inv, y[x + 7] * inv));
+          }
+        }
+        if (g == 0) {
+          const float z = lse2_of(m, sum);
+          if (P.lse) P.lse[tok * (P.c.kv_heads * P.group) + h] = z * 0.69314718055994531f;
+          if (P.lse2) P.lse2[S.row_base + head * n_rows + gr] = z;
+        }
+      }
+    if constexpr (UNIT) {
+      __syncthreads();
+      const Kv4Smem<D>* all = reinterpret_cast<const Kv4Smem<D>*>(smem_raw);
+      const int warps = blockDim.x >> 5;
+      for (int i = threadIdx.x; i < rows * (D / 4); i += blockDim.x) {
+        const int row = i / (D / 4), x = 4 * (i % (D / 4)), gr = row0 + row;
+        float mx = -INFINITY;
+        for (int k = 0; k < warps; ++k) mx = fmaxf(mx, all[k].ml[row].x);
+        const float base = mx == -INFINITY ? 0.0f : mx;
+        float sum = 0.0f;
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-      for (int k = 0; k < warps; ++k) {
-        const float2 ml = all[k].ml[row];
-        const float f = ex2f(ml.x - base);
-        const float4 z = *reinterpret_cast<const float4*>(&all[k].o[row][x]);
-        sum = fmaf(ml.y, f, sum);
-        y.x = fmaf(z.x, f, y.x), y.y = fmaf(z.y, f, y.y), y.z = fmaf(z.z, f, y.z), y.w = fmaf(z.w, f, y.w);
-      }
-      const float inv = sum > 0.0f ? P.c.v_scale / sum : sum == 0.0f ? 0.0f : sum;  // (a NaN stays one)
-      const int64_t tok = S.q_row0 + gr / P.group;
-      const int h = head * P.group + gr % P.group;
-      const int64_t at = tok * P.o_tok + h * P.o_head + x;
-      if constexpr (F32)
-        *reinterpret_cast<float4*>(P.out + 4 * at) = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
-      else
-        *reinterpret_cast<uint2*>(P.out + 2 * at) = make_uint2(pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv));
-      if (x == 0) {
-        const float z = lse2_of(mx, sum);
-        if (P.lse) P.lse[tok * (P.c.kv_heads * P.group) + h] = z * 0.69314718055994531f;
-        if (P.lse2) P.lse2[S.row_base + head * n_rows + gr] = z;
+        for (int k = 0; k < warps; ++k) {
+          const float2 ml = all[k].ml[row];
+          const float f = ex2f(ml.x - base);
+          const float4 z = *reinterpret_cast<const float4*>(&all[k].o[row][x]);
+          sum = fmaf(ml.y, f, sum);
+          y.x = fmaf(z.x, f, y.x), y.y = fmaf(z.y, f, y.y), y.z = fmaf(z.z, f, y.z), y.w = fmaf(z.w, f, y.w);
+        }
+        const float inv = sum > 0.0f ? P.c.v_scale / sum : sum == 0.0f ? 0.0f : sum;  // (a NaN stays one)
+        const int64_t tok = S.q_row0 + gr / P.group;
+        const int h = head * P.group + gr % P.group;
+        const int64_t at = tok * P.o_tok + h * P.o_head + x;
+        if constexpr (F32)
+          *reinterpret_cast<float4*>(P.out + 4 * at) = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+        else
+          *reinterpret_cast<uint2*>(P.out + 2 * at) =
+              make_uint2(pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv));
+        if (x == 0) {
+          const float z = lse2_of(mx, sum);
+          if (P.lse) P.lse[tok * (P.c.kv_heads * P.group) + h] = z * 0.69314718055994531f;
+          if (P.lse2) P.lse2[S.row_base + head * n_rows + gr] = z;
+        }
       }
     }
-  }
   } while (!UNIT && done < n_my);
 }
 
@@ -807,7 +811,25 @@ __global__ void __launch_bounds__(kFinishThreads) kv4_finish_kernel(const __grid
 }
 
 // ---- host -------------------------------------------------------------------
-bool is_prompt(const kvpool_kv4_args* a, int64_t q_len) { return q_len * (a->q.heads / a->cache.kv_heads) > kMaxRows; }
+int64_t group_rows(const kvpool_kv4_args* a, int64_t q_len) { return q_len * (a->q.heads / a->cache.kv_heads); }
+
+// Do segments of more than kMaxRows bf16 rows to a key head go through window
+// attention (5th-generation products, after reading their tokens back)?  Its
+// launches take 10 to 20 us before the first product; the kernel above takes 1.8
+// us for every 1,216 pairs of tiles and 16 rows beside 8.  (200 queries of 16 heads
+// on 4 among their own 200 tokens 9.3 us here and 17.0 there, 1,024 among theirs
+// 61 and 27, 2 x 128 behind 8,000 tokens 83 and 36.)  fp32 rows never do: window
+// attention's FMAs take 2.3 to 5.6 times as long (1,024 queries among their own
+// tokens 189 us and 81, 256 behind 16,384 1,421 and 253).
+bool prompts_pay(const kvpool_kv4_args* a, int32_t n, const int64_t* q_len, const int64_t* k_len) {
+  if (a->dtype == KVPOOL_F32) return false;
+  double pairs = 0;
+  for (int32_t i = 0; i < n; ++i)
+    if (group_rows(a, q_len[i]) > kMaxRows)
+      pairs += (double)((group_rows(a, q_len[i]) + 15) / 16) * a->cache.kv_heads * (double)(k_len[i] / (kPair * kKv4Tile) + 1);
+  return pairs > 8192;
+}
+bool is_prompt(const kvpool_kv4_args* a, bool prompts, int64_t q_len) { return prompts && group_rows(a, q_len) > kMaxRows; }
 
 int check_args(const kvpool_kv4_args* a, int32_t n, const int64_t* q_len, const int64_t* k_len, int64_t* total_q) {
   if (!a || n < 0) return KVPOOL_ERR_INVALID_ARG;
@@ -828,7 +850,7 @@ int check_args(const kvpool_kv4_args* a, int32_t n, const int64_t* q_len, const 
   for (int i = 0; i < n; ++i) {
     if (q_len[i] < 0 || q_len[i] > (1 << 30) || k_len[i] < 0 || k_len[i] > kv4_tokens(&a->cache)) return KVPOOL_ERR_INVALID_ARG;
     if (q_len[i] == 0) continue;
-    if (a->d_weights && is_prompt(a, q_len[i])) return KVPOOL_ERR_INVALID_ARG;
+    if (a->d_weights && group_rows(a, q_len[i]) > kMaxRows) return KVPOOL_ERR_INVALID_ARG;
     q += q_len[i];
     most = std::max(most, k_len[i]);
     keys |= k_len[i] > 0;
@@ -876,14 +898,14 @@ int unit_warps(int64_t units, int64_t most_pairs, int64_t pairs, int64_t rows, i
 
 // Segments [i0, n) of one launch (at most kKv4MaxSegs that are no prompts);
 // returns the next segment, or -1 (too large for one launch).
-int32_t plan(const kvpool_kv4_args* a, int32_t i0, int32_t n, const int64_t* q_len, const int64_t* k_len, int64_t* q_row,
+int32_t plan(const kvpool_kv4_args* a, bool prompts, int32_t i0, int32_t n, const int64_t* q_len, const int64_t* k_len, int64_t* q_row,
              int n_sms, Kv4Params* P, Space* w) {
   const int hk = a->cache.kv_heads, group = a->q.heads / hk;
   int32_t i = i0;
   int64_t row = *q_row, most_rows = 0, rows = 0, blocks = 0, scores = 0;
   P->n_segs = 0;
   for (; i < n && P->n_segs < kKv4MaxSegs; ++i) {
-    if (q_len[i] > 0 && !is_prompt(a, q_len[i])) {
+    if (q_len[i] > 0 && !is_prompt(a, prompts, q_len[i])) {
       Kv4Seg& S = P->segs[P->n_segs++];
       S.q_row0 = row;
       S.q_len = (int32_t)q_len[i];
@@ -947,12 +969,12 @@ struct Run {
   int32_t first, end;
   int64_t q_row, q_rows, kv_rows, bytes;  // bytes: keys' and values' rows
 };
-bool next_run(const kvpool_kv4_args* a, int32_t* i, int64_t* q_row, int32_t n, const int64_t* q_len, const int64_t* k_len,
+bool next_run(const kvpool_kv4_args* a, bool prompts, int32_t* i, int64_t* q_row, int32_t n, const int64_t* q_len, const int64_t* k_len,
               Run* run) {
-  while (*i < n && (q_len[*i] == 0 || !is_prompt(a, q_len[*i]))) *q_row += q_len[(*i)++];
+  while (*i < n && (q_len[*i] == 0 || !is_prompt(a, prompts, q_len[*i]))) *q_row += q_len[(*i)++];
   if (*i >= n) return false;
   *run = Run{*i, *i, *q_row, 0, 0, 0};
-  for (; *i < n && (q_len[*i] == 0 || is_prompt(a, q_len[*i])); ++*i) {
+  for (; *i < n && (q_len[*i] == 0 || is_prompt(a, prompts, q_len[*i])); ++*i) {
     run->q_rows += q_len[*i];
     if (q_len[*i] > 0) run->kv_rows += k_len[*i];
   }
@@ -1053,16 +1075,17 @@ namespace {
 
 // Bytes that the call's launches take, one after the other (a negative error code).
 int64_t space_of(const kvpool_kv4_args* a, int32_t n, const int64_t* q_len, const int64_t* k_len, int n_sms, Kv4Params* P) {
+  const bool prompts = prompts_pay(a, n, q_len, k_len);
   Space w;
   int64_t row = 0, most = 0;
   for (int32_t i = 0; i < n;) {
-    i = plan(a, i, n, q_len, k_len, &row, n_sms, P, &w);
+    i = plan(a, prompts, i, n, q_len, k_len, &row, n_sms, P, &w);
     if (i < 0) return KVPOOL_ERR_INVALID_ARG;
     most = std::max(most, w.total);
   }
   Run run;
   row = 0;
-  for (int32_t i = 0; next_run(a, &i, &row, n, q_len, k_len, &run);) {
+  for (int32_t i = 0; next_run(a, prompts, &i, &row, n, q_len, k_len, &run);) {
     WindowCall call;
     if (!window_call(a, run, q_len, k_len, nullptr, &call)) return KVPOOL_ERR_INVALID_ARG;
     call.args.k.data = call.args.v.data = reinterpret_cast<const void*>((uintptr_t)16);  // (sizes only)
@@ -1103,11 +1126,12 @@ extern "C" int kvpool_kv4_attend(const kvpool_kv4_args* a, int32_t n, const int6
   if (!dev) return KVPOOL_ERR_CUDA;
   std::unique_ptr<Kv4Params> P(new (std::nothrow) Kv4Params);
   if (!P) return KVPOOL_ERR_INVALID_ARG;
+  const bool prompts = prompts_pay(a, n, h_q_len, h_k_len);
   Space w;
   int64_t row = 0;
-  int32_t next = plan(a, 0, n, h_q_len, h_k_len, &row, dev->sms, P.get(), &w);
+  const int32_t next = plan(a, prompts, 0, n, h_q_len, h_k_len, &row, dev->sms, P.get(), &w);
   bool whole = next == n;  // one launch is the whole call
-  for (int32_t i = 0; whole && i < n; ++i) whole = !is_prompt(a, h_q_len[i]);
+  for (int32_t i = 0; whole && i < n; ++i) whole = !is_prompt(a, prompts, h_q_len[i]);
   const int64_t need = whole ? w.total : space_of(a, n, h_q_len, h_k_len, dev->sms, P.get());
   if (need < 0) return (int)need;
   if (need > 0 && (!d_workspace || workspace_bytes < need || reinterpret_cast<uintptr_t>(d_workspace) % 16 != 0))
@@ -1129,7 +1153,7 @@ extern "C" int kvpool_kv4_attend(const kvpool_kv4_args* a, int32_t n, const int6
   row = 0;
   for (int32_t i = 0; i < n;) {
     const int32_t first = i;
-    i = whole ? n : plan(a, i, n, h_q_len, h_k_len, &row, dev->sms, P.get(), &w);
+    i = whole ? n : plan(a, prompts, i, n, h_q_len, h_k_len, &row, dev->sms, P.get(), &w);
     if (P->n_segs == 0) continue;
     P->c = kv4_cache(&a->cache, first, dev->err);
     P->weights = a->d_weights ? a->d_weights + first * a->weight_stride : nullptr;
@@ -1144,7 +1168,7 @@ extern "C" int kvpool_kv4_attend(const kvpool_kv4_args* a, int32_t n, const int6
   }
   Run run;
   row = 0;
-  for (int32_t i = 0; !whole && next_run(a, &i, &row, n, h_q_len, h_k_len, &run);) {
+  for (int32_t i = 0; !whole && next_run(a, prompts, &i, &row, n, h_q_len, h_k_len, &run);) {
     WindowCall call;
     if (!window_call(a, run, h_q_len, h_k_len, space, &call)) return KVPOOL_ERR_INVALID_ARG;
     const int32_t m = run.end - run.first;

@@ -256,92 +256,92 @@ __global__ void __launch_bounds__(kMoveWarps * 32) kv4_move_kernel(const __grid_
   const uint8_t* pages = P.c.pages;
 #pragma unroll 1
   for (int y0 = 0; y0 < kMoveTiles; ++y0) {
-  const int n = min(kKv4Tile, left - y0 * kKv4Tile);
-  const int64_t dst_off = __shfl_sync(0xffffffffu, to_off, y0 * kKv4Tile);
-  if (dst_off < 0) continue;  // (no such tile, or a bad page: the whole warp)
-  uint8_t* dst = P.c.pages + dst_off;
-  auto off_of = [&](int r) { return __shfl_sync(0xffffffffu, off, y0 * kKv4Tile + r); };
-  auto slot_of = [&](int r) { return __shfl_sync(0xffffffffu, slot, y0 * kKv4Tile + r); };
-  // all loads first (nothing that is written is read)
-  constexpr int KI = D / 64;  // 16-byte pieces of keys to a lane
-  uint4 k[KI];
+    const int n = min(kKv4Tile, left - y0 * kKv4Tile);
+    const int64_t dst_off = __shfl_sync(0xffffffffu, to_off, y0 * kKv4Tile);
+    if (dst_off < 0) continue;  // (no such tile, or a bad page: the whole warp)
+    uint8_t* dst = P.c.pages + dst_off;
+    auto off_of = [&](int r) { return __shfl_sync(0xffffffffu, off, y0 * kKv4Tile + r); };
+    auto slot_of = [&](int r) { return __shfl_sync(0xffffffffu, slot, y0 * kKv4Tile + r); };
+    // all loads first (nothing that is written is read)
+    constexpr int KI = D / 64;  // 16-byte pieces of keys to a lane
+    uint4 k[KI];
 #pragma unroll
-  for (int i = 0; i < KI; ++i) {
-    const int x = i * 32 + lane, r = x / (D / 32), c = x % (D / 32);
-    const int64_t o = off_of(r);
-    const int sl = slot_of(r);
-    k[i] = o >= 0 ? *reinterpret_cast<const uint4*>(pages + o + sl * (D / 2) + 16 * c) : make_uint4(0, 0, 0, 0);
-  }
-  // scales: of token `lane`'s keys (8 or 4 bytes), of pair `lane`'s values (16 or 8: two tokens' bytes alternate)
-  constexpr int G = D / kKv4Group, SW = G / 4;
-  uint32_t ks[SW], vs[2 * SW];
-  {
-    const int64_t o = off_of(lane % kKv4Tile);
-    const int sl = slot_of(lane % kKv4Tile);
-#pragma unroll
-    for (int i = 0; i < SW; ++i) ks[i] = o >= 0 ? reinterpret_cast<const uint32_t*>(pages + o + L::kKs + sl * G)[i] : 0;
-  }
-  {
-    const int j = lane % 8;
-    const int64_t o0 = off_of(2 * j), o1 = off_of(2 * j + 1);
-    const int s0 = slot_of(2 * j), s1 = slot_of(2 * j + 1);
-#pragma unroll
-    for (int i = 0; i < 2 * SW; ++i) {
-      const uint32_t x = o0 >= 0 ? reinterpret_cast<const uint32_t*>(pages + o0 + L::kVs + (s0 >> 1) * 2 * G)[i] : 0;
-      const uint32_t y = o1 >= 0 ? reinterpret_cast<const uint32_t*>(pages + o1 + L::kVs + (s1 >> 1) * 2 * G)[i] : 0;
-      vs[i] = (x >> 8 * (s0 & 1) & 0x00FF00FFu) | (y >> 8 * (s1 & 1) & 0x00FF00FFu) << 8;
+    for (int i = 0; i < KI; ++i) {
+      const int x = i * 32 + lane, r = x / (D / 32), c = x % (D / 32);
+      const int64_t o = off_of(r);
+      const int sl = slot_of(r);
+      k[i] = o >= 0 ? *reinterpret_cast<const uint4*>(pages + o + sl * (D / 2) + 16 * c) : make_uint4(0, 0, 0, 0);
     }
-  }
-  constexpr int VW = D / 64;  // 8-byte words of a V chunk
-  uint2 v[2][VW];             // pairs lane / 8 and + 4, chunk lane % 8
+    // scales: of token `lane`'s keys (8 or 4 bytes), of pair `lane`'s values (16 or 8: two tokens' bytes alternate)
+    constexpr int G = D / kKv4Group, SW = G / 4;
+    uint32_t ks[SW], vs[2 * SW];
+    {
+      const int64_t o = off_of(lane % kKv4Tile);
+      const int sl = slot_of(lane % kKv4Tile);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int j = lane / 8 + 4 * i, c = lane % 8;
+      for (int i = 0; i < SW; ++i) ks[i] = o >= 0 ? reinterpret_cast<const uint32_t*>(pages + o + L::kKs + sl * G)[i] : 0;
+    }
+    {
+      const int j = lane % 8;
+      const int64_t o0 = off_of(2 * j), o1 = off_of(2 * j + 1);
+      const int s0 = slot_of(2 * j), s1 = slot_of(2 * j + 1);
 #pragma unroll
-    for (int y = 0; y < VW; ++y) v[i][y] = make_uint2(0, 0);
+      for (int i = 0; i < 2 * SW; ++i) {
+        const uint32_t x = o0 >= 0 ? reinterpret_cast<const uint32_t*>(pages + o0 + L::kVs + (s0 >> 1) * 2 * G)[i] : 0;
+        const uint32_t y = o1 >= 0 ? reinterpret_cast<const uint32_t*>(pages + o1 + L::kVs + (s1 >> 1) * 2 * G)[i] : 0;
+        vs[i] = (x >> 8 * (s0 & 1) & 0x00FF00FFu) | (y >> 8 * (s1 & 1) & 0x00FF00FFu) << 8;
+      }
+    }
+    constexpr int VW = D / 64;  // 8-byte words of a V chunk
+    uint2 v[2][VW];             // pairs lane / 8 and + 4, chunk lane % 8
 #pragma unroll
-    for (int y = 0; y < 2; ++y) {
-      const int64_t o = off_of(2 * j + y);
-      const int sl = slot_of(2 * j + y), p = sl >> 1;
-      if (o < 0) continue;
-      const uint8_t* src = pages + o + L::kV + p * D + (c ^ kv4_swizzle<D>(p)) * L::kChunk;
+    for (int i = 0; i < 2; ++i) {
+      const int j = lane / 8 + 4 * i, c = lane % 8;
+#pragma unroll
+      for (int y = 0; y < VW; ++y) v[i][y] = make_uint2(0, 0);
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int64_t o = off_of(2 * j + y);
+        const int sl = slot_of(2 * j + y), p = sl >> 1;
+        if (o < 0) continue;
+        const uint8_t* src = pages + o + L::kV + p * D + (c ^ kv4_swizzle<D>(p)) * L::kChunk;
+#pragma unroll
+        for (int z = 0; z < VW; ++z) {
+          const uint2 x = *reinterpret_cast<const uint2*>(src + 8 * z);
+          v[i][z].x |= (x.x >> 4 * (sl & 1) & 0x0F0F0F0Fu) << 4 * y;
+          v[i][z].y |= (x.y >> 4 * (sl & 1) & 0x0F0F0F0Fu) << 4 * y;
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < KI; ++i) {
+      const int x = i * 32 + lane, r = x / (D / 32), c = x % (D / 32);
+      if (r < n) *reinterpret_cast<uint4*>(dst + r * (D / 2) + 16 * c) = k[i];
+    }
+    if (lane < n) {
+#pragma unroll
+      for (int i = 0; i < SW; ++i) reinterpret_cast<uint32_t*>(dst + L::kKs + lane * G)[i] = ks[i];
+    }
+    if (lane < 8 && 2 * lane < n) {
+      uint32_t* p = reinterpret_cast<uint32_t*>(dst + L::kVs + lane * 2 * G);
+#pragma unroll
+      for (int i = 0; i < 2 * SW; ++i) p[i] = 2 * lane + 1 < n ? vs[i] : (vs[i] & 0x00FF00FFu) | (p[i] & 0xFF00FF00u);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int j = lane / 8 + 4 * i, c = lane % 8;
+      if (2 * j >= n) continue;
+      uint2* p = reinterpret_cast<uint2*>(dst + L::kV + j * D + (c ^ kv4_swizzle<D>(j)) * L::kChunk);
 #pragma unroll
       for (int z = 0; z < VW; ++z) {
-        const uint2 x = *reinterpret_cast<const uint2*>(src + 8 * z);
-        v[i][z].x |= (x.x >> 4 * (sl & 1) & 0x0F0F0F0Fu) << 4 * y;
-        v[i][z].y |= (x.y >> 4 * (sl & 1) & 0x0F0F0F0Fu) << 4 * y;
+        uint2 x = v[i][z];
+        if (2 * j + 1 >= n) {  // the place of the pair's second token stays
+          const uint2 old = p[z];
+          x = make_uint2((x.x & 0x0F0F0F0Fu) | (old.x & 0xF0F0F0F0u), (x.y & 0x0F0F0F0Fu) | (old.y & 0xF0F0F0F0u));
+        }
+        p[z] = x;
       }
     }
-  }
-#pragma unroll
-  for (int i = 0; i < KI; ++i) {
-    const int x = i * 32 + lane, r = x / (D / 32), c = x % (D / 32);
-    if (r < n) *reinterpret_cast<uint4*>(dst + r * (D / 2) + 16 * c) = k[i];
-  }
-  if (lane < n) {
-#pragma unroll
-    for (int i = 0; i < SW; ++i) reinterpret_cast<uint32_t*>(dst + L::kKs + lane * G)[i] = ks[i];
-  }
-  if (lane < 8 && 2 * lane < n) {
-    uint32_t* p = reinterpret_cast<uint32_t*>(dst + L::kVs + lane * 2 * G);
-#pragma unroll
-    for (int i = 0; i < 2 * SW; ++i) p[i] = 2 * lane + 1 < n ? vs[i] : (vs[i] & 0x00FF00FFu) | (p[i] & 0xFF00FF00u);
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int j = lane / 8 + 4 * i, c = lane % 8;
-    if (2 * j >= n) continue;
-    uint2* p = reinterpret_cast<uint2*>(dst + L::kV + j * D + (c ^ kv4_swizzle<D>(j)) * L::kChunk);
-#pragma unroll
-    for (int z = 0; z < VW; ++z) {
-      uint2 x = v[i][z];
-      if (2 * j + 1 >= n) {  // the place of the pair's second token stays
-        const uint2 old = p[z];
-        x = make_uint2((x.x & 0x0F0F0F0Fu) | (old.x & 0xF0F0F0F0u), (x.y & 0x0F0F0F0Fu) | (old.y & 0xF0F0F0F0u));
-      }
-      p[z] = x;
-    }
-  }
   }
 }
 

@@ -734,15 +734,22 @@ class Kv4Cache:
         ot = _table(out_table, "out_table", self.index)
         if index is None:
             index = self._empty((n, H, max(keep, 0)), torch.int32, stream)
+            at = index.data_ptr()
+        else:
+            at = _need(index, "index", torch.int32, torch.Size((n, H, keep)), self.index)
         if out_weights is None:
             out_weights = self._empty((n, H, max(keep, 0)), torch.float32, stream)
-        at = _need(index, "index", torch.int32, torch.Size((n, H, keep)), self.index)
-        ow = _weights(out_weights, "out_weights", n, H, keep, self.index)
+            ow, width = (out_weights.data_ptr(), H * keep, keep), keep
+        else:
+            ow, width = _weights(out_weights, "out_weights", n, H, keep, self.index), out_weights.shape[2]
         try:
-            a = _KV4_EVICT.pack(*ot, *w, *ow, at, out_weights.shape[2], keep, n_sink, n_recent)
+            a = _KV4_EVICT.pack(*ot, *w, *ow, at, width, keep, n_sink, n_recent)
         except (struct.error, OverflowError) as e:
             raise ValueError(f"evict: {e}") from None
-        self._done(self._lib.kvpool_kv4_evict(self._pack(table, n) + a, n, kl.tobytes(), _stream_of(stream, self.index)), "evict")
+        rc = self._lib.kvpool_kv4_evict(self._pack(table, n) + a, n, kl.tobytes(),
+                                        self._stream_now(self.index) if stream is None else _stream(stream))
+        if rc != OK:
+            self._done(rc, "evict")
         return index, out_weights
 
 

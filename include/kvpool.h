@@ -554,13 +554,13 @@ int kvpool_kv4_load(const kvpool_kv4* cache, int32_t dtype, const kvpool_heads* 
  * NaNs of them.  Places from h_k_len[i] on and segments without queries stay as
  * they were.  With d_weights a segment has at most 64 query rows per key head.
  * dtype: KVPOOL_F32 or KVPOOL_BF16 (of q and out).  Scores, softmax statistics and
- * sums are fp32.  Where a segment has at most 64 query rows per key head (h_q_len *
- * group), products are of fp16 numbers: keys and values exactly, bf16 queries
- * exactly and fp32 ones to 2^-22 of each (or 2^-39 of their row's largest, where
- * that is more), softmax weights to 2^-11 of each for bf16 outputs and to 2^-22 for
- * fp32 ones (or 2^-31 of their row's largest).  Longer segments
- * are read back to rows in the workspace and go through window attention with
- * everything visible, as kvpool_window_attend says.
+ * sums are fp32.  Products are of fp16 numbers: keys and values exactly, bf16
+ * queries exactly and fp32 ones to 2^-22 of each (or 2^-39 of their row's largest,
+ * where that is more), softmax weights to 2^-11 of each for bf16 outputs and to
+ * 2^-22 for fp32 ones (or 2^-31 of their row's largest).  Long segments of bf16
+ * queries (more than 64 rows per key head, h_q_len * group) may be read back to
+ * rows in the workspace and go through window attention with everything visible,
+ * as kvpool_window_attend says.
  * d_workspace: kvpool_kv4_workspace bytes (16-byte aligned, may be NULL when that is
  * 0); calls that overlap on the GPU need one each.  It, d_lse and d_weights lie
  * apart from everything else.  The lengths are read during the call: a captured

@@ -742,3 +742,27 @@ def test_every_largest_value_and_its_borders():
         k, v = cache.load(table, [0], [n], dtype=F32)
         assert same(k, F.held(x)) and same(v, F.held(x.flip(0)))
     ok()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("q_len,k_len,hq,hk,d", [([200], [200], 4, 1, 64), ([33, 1, 150], [40, 900, 333], 4, 2, 128), ([300], [1500], 2, 2, 64)])
+def test_prompts_that_are_not_read_back(q_len, k_len, hq, hk, d, dtype):
+    """Short enough for the kernel of single tokens (fp32 ones always go there)."""
+    run(q_len, k_len, hq, hk, d, 16, dtype)
+    run(q_len, k_len, hq, hk, d, 128, dtype, strided=True)
+
+
+def test_long_prompts_of_bf16_are_read_back():
+    g, d, hk = gen(97), 64, 1
+    cache, table = make([9000], 64, hk, d)
+    k, v = fill(cache, table, [9000], BF, g)
+    q, lse = randn((600, 8, d), BF, g), torch.empty((600, 8), device="cuda")
+    assert cache.workspace(q, table, [600], [9000]) >= 2 * 9000 * hk * d * 2
+    out = cache.attend(q, table, [600], [9000], lse=lse)
+    # the last 40 queries alone, by the other kernel
+    want_lse = torch.empty((40, 8), device="cuda")
+    want = cache.attend(q[-40:], table, [40], [9000], lse=want_lse)
+    # weights rounded to bf16 (2^-8 of each) against fp16's, both outputs rounded
+    assert float((out[-40:].double() - want.double()).norm() / want.double().norm()) < 2.0 ** -7
+    assert float((lse[-40:] - want_lse).abs().max()) < 1e-4
+    ok()
