@@ -1055,7 +1055,10 @@ cudaError_t launch_all(const Kv4Params& P, int n_sms, cudaStream_t s) {
   // us a call with 512 threads, 23.5 with 128)
   constexpr int kRows = kWeightThreads / (D / 4);  // or slices of 128 threads
   int slices = 1;
-  if (parts && P.n_shares / 16 >= P.n_units && P.n_rows <= n_sms) {
+  // Where weights are summed as well, one launch for both is worth more until 64 parts (4 requests of 4,000 tokens, 4 key
+  // heads: 10.9 us against 15.6); behind them the sides change with the case (16,000 tokens, 150 parts: 25.8 against
+  // 22.0 at a head of 128, 16.4 against 17.8 at 64; one request of 60,000: 62 against 34).
+  if (parts && P.n_shares / (P.n_blocks > 0 ? 64 : 16) >= P.n_units && P.n_rows <= n_sms) {
     if (e == cudaSuccess)
       e = launch_kernel(true, kern, dim3(P.n_rows), dim3(kFinishThreads), 0, s, P, P.n_rows, kFinishThreads / (D / 4));
   } else if (parts) {
