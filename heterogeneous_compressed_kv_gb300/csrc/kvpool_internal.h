@@ -229,6 +229,9 @@ struct OpsDevice {
   uint32_t* err;  // the device error word of such calls
 };
 const OpsDevice* ops_device();
+// Do prompts of a window call go through its tensor-core form?  (Type, scale,
+// strides; the others are left to fp32 multiply-adds.)
+bool window_tc_able(const kvpool_window_args* a);
 // kvpool_window_workspace and kvpool_window_attend.  even: key lists are cut into
 // parts that fill the multiprocessors evenly (no window, long lists).
 int64_t window_space(const kvpool_window_args* a, int32_t n, const int64_t* h_q_len, const int64_t* h_k_start,

@@ -813,6 +813,12 @@ __global__ void __launch_bounds__(kFinishThreads) kv4_finish_kernel(const __grid
 // ---- host -------------------------------------------------------------------
 int64_t group_rows(const kvpool_kv4_args* a, int64_t q_len) { return q_len * (a->q.heads / a->cache.kv_heads); }
 
+// Rows that tokens are read back to: a token's heads one after the other.
+kvpool_heads read_back_rows(const kvpool_kv4_args* a, void* space) {
+  const int32_t d = a->cache.head_dim, hk = a->cache.kv_heads;
+  return kvpool_heads{space, (int64_t)hk * d, d, hk, 0};
+}
+
 // Do segments of more than kMaxRows bf16 rows to a key head go through window
 // attention (5th-generation products, after reading their tokens back)?  Its
 // launches take 10 to 20 us before the first product; the kernel above takes 1.8
@@ -821,15 +827,29 @@ int64_t group_rows(const kvpool_kv4_args* a, int64_t q_len) { return q_len * (a-
 // 61 and 27, 2 x 128 behind 8,000 tokens 83 and 36.)  fp32 rows never do: window
 // attention's FMAs take 2.3 to 5.6 times as long (1,024 queries among their own
 // tokens 189 us and 81, 256 behind 16,384 1,421 and 253).
+//
+// Nor do calls whose scale or strides its tensor-core form does not take (a scale
+// that is not positive, queries alike over an axis: 300 queries of 8 heads on 2
+// behind 6,000 tokens 191 us by its multiply-adds, 25 here), and
+// segments without tokens have nothing to read back.
 bool prompts_pay(const kvpool_kv4_args* a, int32_t n, const int64_t* q_len, const int64_t* k_len) {
   if (a->dtype == KVPOOL_F32) return false;
   double pairs = 0;
   for (int32_t i = 0; i < n; ++i)
-    if (group_rows(a, q_len[i]) > kMaxRows)
+    if (group_rows(a, q_len[i]) > kMaxRows && k_len[i] > 0)
       pairs += (double)((group_rows(a, q_len[i]) + 15) / 16) * a->cache.kv_heads * (double)(k_len[i] / (kPair * kKv4Tile) + 1);
-  return pairs > 8192;
+  if (!(pairs > 8192)) return false;
+  kvpool_window_args w{};
+  w.dtype = a->dtype;
+  w.scale = a->scale;
+  w.q = a->q;
+  w.q_rows = a->q_rows;
+  w.k = w.v = read_back_rows(a, nullptr);
+  return window_tc_able(&w);
 }
-bool is_prompt(const kvpool_kv4_args* a, bool prompts, int64_t q_len) { return prompts && group_rows(a, q_len) > kMaxRows; }
+bool is_prompt(const kvpool_kv4_args* a, bool prompts, int64_t q_len, int64_t k_len) {
+  return prompts && group_rows(a, q_len) > kMaxRows && k_len > 0;
+}
 
 int check_args(const kvpool_kv4_args* a, int32_t n, const int64_t* q_len, const int64_t* k_len, int64_t* total_q) {
   if (!a || n < 0) return KVPOOL_ERR_INVALID_ARG;
@@ -905,7 +925,7 @@ int32_t plan(const kvpool_kv4_args* a, bool prompts, int32_t i0, int32_t n, cons
   int64_t row = *q_row, most_rows = 0, rows = 0, blocks = 0, scores = 0;
   P->n_segs = 0;
   for (; i < n && P->n_segs < kKv4MaxSegs; ++i) {
-    if (q_len[i] > 0 && !is_prompt(a, prompts, q_len[i])) {
+    if (q_len[i] > 0 && !is_prompt(a, prompts, q_len[i], k_len[i])) {
       Kv4Seg& S = P->segs[P->n_segs++];
       S.q_row0 = row;
       S.q_len = (int32_t)q_len[i];
@@ -971,10 +991,10 @@ struct Run {
 };
 bool next_run(const kvpool_kv4_args* a, bool prompts, int32_t* i, int64_t* q_row, int32_t n, const int64_t* q_len, const int64_t* k_len,
               Run* run) {
-  while (*i < n && (q_len[*i] == 0 || !is_prompt(a, prompts, q_len[*i]))) *q_row += q_len[(*i)++];
+  while (*i < n && (q_len[*i] == 0 || !is_prompt(a, prompts, q_len[*i], k_len[*i]))) *q_row += q_len[(*i)++];
   if (*i >= n) return false;
   *run = Run{*i, *i, *q_row, 0, 0, 0};
-  for (; *i < n && (q_len[*i] == 0 || is_prompt(a, prompts, q_len[*i])); ++*i) {
+  for (; *i < n && (q_len[*i] == 0 || is_prompt(a, prompts, q_len[*i], k_len[*i])); ++*i) {
     run->q_rows += q_len[*i];
     if (q_len[*i] > 0) run->kv_rows += k_len[*i];
   }
@@ -1010,9 +1030,7 @@ bool window_call(const kvpool_kv4_args* a, const Run& run, const int64_t* q_len,
   x.out = a->out;
   x.q.data = static_cast<const uint8_t*>(a->q.data) + vb * run.q_row * a->q.token_stride;
   x.out.data = static_cast<const uint8_t*>(a->out.data) + vb * run.q_row * a->out.token_stride;
-  const int64_t row = (int64_t)a->cache.kv_heads * a->cache.head_dim;
-  x.k = kvpool_heads{space, row, a->cache.head_dim, a->cache.kv_heads, 0};
-  x.v = x.k;
+  x.k = x.v = read_back_rows(a, space);
   x.v.data = static_cast<uint8_t*>(space) + run.bytes;
   x.q_rows = run.q_rows;
   x.kv_rows = run.kv_rows;
@@ -1134,7 +1152,7 @@ extern "C" int kvpool_kv4_attend(const kvpool_kv4_args* a, int32_t n, const int6
   int64_t row = 0;
   const int32_t next = plan(a, prompts, 0, n, h_q_len, h_k_len, &row, dev->sms, P.get(), &w);
   bool whole = next == n;  // one launch is the whole call
-  for (int32_t i = 0; whole && i < n; ++i) whole = !is_prompt(a, prompts, h_q_len[i]);
+  for (int32_t i = 0; whole && i < n; ++i) whole = !is_prompt(a, prompts, h_q_len[i], h_k_len[i]);
   const int64_t need = whole ? w.total : space_of(a, n, h_q_len, h_k_len, dev->sms, P.get());
   if (need < 0) return (int)need;
   if (need > 0 && (!d_workspace || workspace_bytes < need || reinterpret_cast<uintptr_t>(d_workspace) % 16 != 0))

@@ -435,9 +435,7 @@ const OpsDevice* ops_device() {
   return &d;
 }
 
-}  // namespace kvp
-
-namespace kvp {
+bool window_tc_able(const kvpool_window_args* a) { return tc_able(a); }
 
 int64_t window_space(const kvpool_window_args* a, int32_t n, const int64_t* h_q_len, const int64_t* h_k_start,
                      const int64_t* h_k_len, bool even) {
