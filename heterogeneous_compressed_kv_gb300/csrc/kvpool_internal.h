@@ -233,7 +233,8 @@ const OpsDevice* ops_device();
 // strides; the others are left to fp32 multiply-adds.)
 bool window_tc_able(const kvpool_window_args* a);
 // kvpool_window_workspace and kvpool_window_attend.  even: key lists are cut into
-// parts that fill the multiprocessors evenly (no window, long lists).
+// parts that fill the multiprocessors evenly (no window, long lists), and a query
+// that is infinite gives NaN whatever the signs of the keys are.
 int64_t window_space(const kvpool_window_args* a, int32_t n, const int64_t* h_q_len, const int64_t* h_k_start,
                      const int64_t* h_k_len, bool even);
 int window_run(const kvpool_window_args* a, int32_t n, const int64_t* h_q_len, const int64_t* h_k_start,

@@ -341,7 +341,9 @@ __global__ void __launch_bounds__(kv4_warps(NT, F32) * 32, 1) kv4_attend_kernel(
       amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
       // 2^(14 - e), e the exponent of the largest value (at least -110)
       const int e = max((int)(amax >> 23) - 127, -110);
-      const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23), down = __uint_as_float((uint32_t)(127 - 14 + e) << 23);
+      const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+      // an infinity makes NaNs of all the row's scores (an infinite product with keys of one sign might be -inf alone)
+      const float down = amax >= 0x7F800000u ? NAN : __uint_as_float((uint32_t)(127 - 14 + e) << 23);
 #pragma unroll
       for (int i = 0; i < 2 * KS; ++i) {
         const float x0 = x[2 * i] * up, x1 = x[2 * i + 1] * up;

@@ -182,7 +182,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) window_merge_kernel(const __
     for (int i = 0; i < V; ++i) acc[i] = acc[i] * fa + x[i] * fb;
     m = mx;
   }
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  l = win_sum(P, w.pos0 + row / P.group, l);
+  const float inv = l > 0.0f ? 1.0f / l : l;  // (a NaN stays one)
   const int64_t tok = S.q_row0 + w.tok0 + row / P.group;
   const int h = w.hk * P.group + row % P.group;
   const int64_t at = tok * P.o_tok + h * P.o_head + lane * V;
@@ -478,6 +479,7 @@ int window_run(const kvpool_window_args* a, int32_t n, const int64_t* h_q_len, c
   if (!P) return KVPOOL_ERR_INVALID_ARG;
   fill_params(a, P.get());
   P->err = dev->err;
+  P->nan_rows = even;
   const bool tc = tc_able(a);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   for (int f = 0; f < kForms; ++f)

@@ -35,6 +35,7 @@ struct WinParams {
   int32_t tile_tokens, tile_rows;
   int32_t n_segs, n_items;
   int32_t n_merge, merge_rows;  // (tile, key head)s to merge, the most rows that one has
+  int32_t nan_rows;  // does a row whose scores are -inf alone give NaN?  (0: zeros, as one that sees nothing)
   float* part_o;    // [slots][tile_rows][head_dim]
   float2* part_ml;  // [slots][tile_rows]: (max in the log2 domain, sum)
   uint32_t* err;
@@ -90,6 +91,12 @@ __device__ __forceinline__ bool win_sees(const WinParams& P, int p, int t) {
 // nothing, NaN where its sum is one (a NaN or an infinity among its scores)
 __device__ __forceinline__ float win_lse(float m, float l) {
   return l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+}
+
+// A row's sum of weights, at its position: NaN where it sees tokens, got nothing
+// from them and the call says so (a query that is infinite)
+__device__ __forceinline__ float win_sum(const WinParams& P, int pos, float l) {
+  return P.nan_rows && l == 0.0f && pos >= 0 ? NAN : l;
 }
 
 // Single-token form: at most 16 query rows per key head, the whole segment in

@@ -546,7 +546,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
       const bool mine = r_tok < q.n && row < tt * P.group;
       const int64_t tok = w.q_row + t * tt + r_tok;
       const int head = w.hk * P.group + r_head;
-      const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+      if (w.n_split == 1) l = win_sum(P, pos, l);
+      const float inv = l > 0.0f ? 1.0f / l : l;  // (a NaN stays one)
       if (!first) {
         if (!warp_wait(&o_full[t], n_o & 1, P.err)) break;
         ++n_o;

@@ -30,3 +30,35 @@ def test_prompts_that_the_tensor_copies_cannot_take(case):
     cache.attend(q, table, [n], [T], scale=scale, out=out, lse=lse)
     check(q, *held(cache, table, [T]), [n], [T], scale, out, lse)
     ok()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("q_len,k_len,hq,hk,d,weigh", [
+    (1, 1, 4, 1, 64, True), (1, 1, 1, 1, 128, False), (3, 40, 4, 2, 128, True), (1, 9000, 8, 1, 64, True), (4, 3, 2, 1, 64, True),
+    (5, 9000, 16, 1, 128, False), (100, 300, 2, 1, 64, False), (300, 4000, 8, 2, 128, False), (310, 300, 8, 8, 64, False)])
+def test_infinite_queries(q_len, k_len, hq, hk, d, weigh, sign, dtype):
+    """A query that is infinite in a dim in which every key has the same sign gives NaN, and no other query does; one that
+    sees no token gives zeros."""
+    g = gen(q_len + k_len)
+    cache, table = make([k_len], 32, hk, d)
+    k, v = randn((k_len, hk, d), dtype, g), randn((k_len, hk, d), dtype, g)
+    k[..., 3] = k[..., 3].abs() + 4  # (no scale makes a zero of it)
+    cache.store(k, v, table, [0], [k_len])
+    q, lse = randn((q_len, hq, d), dtype, g), torch.empty((q_len, hq), device="cuda")
+    w = torch.zeros((1, hk, k_len), device="cuda") if weigh else None
+    at = sorted({0, q_len // 2, q_len - 1})
+    for i, j in enumerate(at):
+        q[j, (i + 1) % hq, 3] = sign * math.inf
+    out = cache.attend(q, table, [q_len], [k_len], lse=lse, weights=w, decay=0.0)
+    bad = torch.zeros((q_len, hq), dtype=torch.bool, device="cuda")
+    nothing = max(0, q_len - k_len)
+    for i, j in enumerate(at):
+        bad[j, (i + 1) % hq] = j >= nothing
+    assert torch.equal(out.isnan().all(-1), bad) and torch.equal(out.isnan().any(-1), bad)
+    assert torch.equal(lse.isnan(), bad)
+    assert bool((out[:nothing] == 0).all()) and bool((lse[:nothing] == -math.inf).all())
+    if weigh:  # a row of NaN makes NaNs of its head's weights, and of no other's
+        heads = bad.any(0).view(hk, -1).any(-1)
+        assert torch.equal(w[0].isnan().all(-1), heads) and torch.equal(w[0].isnan().any(-1), heads)
+    ok()
