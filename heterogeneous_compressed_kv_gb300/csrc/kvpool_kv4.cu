@@ -140,8 +140,8 @@ __device__ __forceinline__ Scale<KVPOOL_F32> scale_of(const Raw8<KVPOOL_F32>& ra
 #pragma unroll
   for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(x[i]) & 0x7FFFFFFFu);
   amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-  const float top = __uint_as_float(amax) * inv_scale;  // (a power of two)
-  if (!(top < INFINITY)) return {0x7F, 0.0f};
+  if (amax >= 0x7F800000u) return {0x7F, 0.0f};
+  const float top = __uint_as_float(amax) * inv_scale;  // (a power of two; past fp32's range: the largest scale)
   const uint32_t s = f32x2_to_e4m3x2(__fdiv_rn(top, 6.0f), 0.0f) & 0xFFu;
   return {s, e4m3x2_to_f32x2((uint16_t)s).x};
 }
@@ -157,8 +157,9 @@ __device__ __forceinline__ Scale<KVPOOL_BF16> scale_of(const Raw8<KVPOOL_BF16>& 
   constexpr uint32_t kAbs = 0x7FFF7FFFu;
   uint32_t m = max_abs_bf16x2(max_abs_bf16x2(raw.r.x & kAbs, raw.r.y & kAbs), max_abs_bf16x2(raw.r.z & kAbs, raw.r.w & kAbs));
   m = max_abs_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  const float top = __uint_as_float(max(m << 16, m & 0xFFFF0000u)) * inv_scale;  // (a power of two; NaN is the largest)
-  if (!(top < INFINITY)) return {0x7F, 0.0f};
+  const uint32_t amax = max(m << 16, m & 0xFFFF0000u);  // (NaN is the largest)
+  if (amax >= 0x7F800000u) return {0x7F, 0.0f};
+  const float top = __uint_as_float(amax) * inv_scale;  // (a power of two; past fp32's range: the largest scale)
   uint16_t s;
   asm("{.reg .b32 h;\n\tcvt.rn.f16x2.f32 h, %1, %1;\n\tcvt.rn.satfinite.e4m3x2.f16x2 %0, h;}" : "=h"(s) : "f"(top * (1.0f / 6.0f)));
   const float f = e4m3x2_to_f32x2(s).x;

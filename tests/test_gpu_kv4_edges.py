@@ -62,3 +62,23 @@ def test_infinite_queries(q_len, k_len, hq, hk, d, weigh, sign, dtype):
         heads = bad.any(0).view(hk, -1).any(-1)
         assert torch.equal(w[0].isnan().all(-1), heads) and torch.equal(w[0].isnan().any(-1), heads)
     ok()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("ks,vs", [(2.0 ** -16, 2.0 ** -3), (2.0 ** -12, 1.0), (1.0, 2.0 ** -16), (2.0 ** 16, 2.0 ** -16)])
+def test_values_too_large_for_a_scale(ks, vs, dtype):
+    """Finite values of any size are held as 2688 scales at most: where x / k_scale is past fp32's range as well."""
+    x = torch.zeros((1, 1, 128))
+    for i, big in enumerate((3e38, -1e35, 2e34, 1e30, 3e5, -3.3e38, 1.0, 1e-3)):
+        x[0, 0, 16 * i:16 * i + 16] = torch.linspace(-1, 1, 16)
+        x[0, 0, 16 * i + i] = big
+        x[0, 0, 16 * i + 15 - i] = -big / 2
+    x = x.to(dtype).cuda()
+    cache, table = make([3], 16, 1, 128, ks=ks, vs=vs)
+    cache.store(x, x, table, [1], [1])
+    got = cache.load(table, [1], [1], dtype=F32)
+    for y, s in zip(got, (ks, vs)):
+        # what is past 2688 scales is held as that, so a smaller number past it has the same codes
+        top = 2.0 ** 20 * s
+        assert same(y, F.held(x.float().clamp(-top, top), s)) and not bool(y.isnan().any())
+    ok()
