@@ -460,6 +460,11 @@ bool kv4_meets(const kvpool_kv4* c, const void* p, __int128 bytes) {
   return touch(c->d_pages, page_bytes(c)) || touch(c->d_table, table_bytes(c));
 }
 
+bool kv4_meets(const kvpool_kv4* c, const float* w, int64_t n, int64_t seg_stride, int64_t head_stride, int64_t len) {
+  return runs_touch(w, n, seg_stride, c->kv_heads, head_stride, len, c->d_pages, page_bytes(c)) ||
+         runs_touch(w, n, seg_stride, c->kv_heads, head_stride, len, c->d_table, table_bytes(c));
+}
+
 Kv4Cache kv4_cache(const kvpool_kv4* c, int64_t row0, uint32_t* err) {
   Kv4Cache C{};
   C.pages = static_cast<uint8_t*>(c->d_pages);

@@ -69,6 +69,8 @@ Kv4Cache kv4_cache(const kvpool_kv4* c, int64_t row0, uint32_t* err);
 // Do n tokens' rows of h lie on the cache's pages or its table?
 bool kv4_meets(const kvpool_kv4* c, const kvpool_heads& h, int64_t n, int64_t vb);
 bool kv4_meets(const kvpool_kv4* c, const void* p, __int128 bytes);
+// The same for n segments' weights (fp32 runs of len places, per segment and head).
+bool kv4_meets(const kvpool_kv4* c, const float* w, int64_t n, int64_t seg_stride, int64_t head_stride, int64_t len);
 inline int64_t kv4_tokens(const kvpool_kv4* c) { return (int64_t)c->table_width * c->page_tokens; }
 
 // Read the tokens [0, len[i]) of table rows row0 + i into rows of k and v

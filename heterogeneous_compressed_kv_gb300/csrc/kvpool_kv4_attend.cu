@@ -1142,9 +1142,24 @@ extern "C" int kvpool_kv4_attend(const kvpool_kv4_args* a, int32_t n, const int6
   if (bad != KVPOOL_OK || total == 0) return bad;
   const int64_t vb = a->dtype == KVPOOL_BF16 ? 2 : 4;
   if (!rows_same(a->out, a->q, total) && rows_meet(a->out, total, a->q, total, a->cache.head_dim, vb)) return KVPOOL_ERR_INVALID_ARG;
-  if (kv4_meets(&a->cache, a->out, total, vb) || kv4_meets(&a->cache, a->d_lse, (__int128)4 * total * a->q.heads) ||
-      kv4_meets(&a->cache, d_workspace, workspace_bytes))
+  if (kv4_meets(&a->cache, a->out, total, vb) || kv4_meets(&a->cache, d_workspace, workspace_bytes)) return KVPOOL_ERR_INVALID_ARG;
+  // the log-sum-exps, the weights and (below) the workspace lie apart from all else
+  int64_t most = 0;  // places of a segment's weights
+  for (int32_t i = 0; a->d_weights && i < n; ++i)
+    if (h_q_len[i] > 0) most = std::max(most, h_k_len[i]);
+  auto on_rows = [&](const void* p, __int128 bytes) {
+    return rows_touch(a->q, total, a->cache.head_dim, vb, p, bytes) || rows_touch(a->out, total, a->cache.head_dim, vb, p, bytes);
+  };
+  auto on_weights = [&](const void* p, __int128 bytes) {
+    return runs_touch(a->d_weights, n, a->weight_stride, a->cache.kv_heads, a->weight_head_stride, most, p, bytes);
+  };
+  const __int128 lse_bytes = a->d_lse ? (__int128)4 * total * a->q.heads : 0;
+  if (kv4_meets(&a->cache, a->d_lse, lse_bytes) || on_rows(a->d_lse, lse_bytes) || on_weights(a->d_lse, lse_bytes) ||
+      kv4_meets(&a->cache, a->d_weights, n, a->weight_stride, a->weight_head_stride, most))
     return KVPOOL_ERR_INVALID_ARG;
+  for (const kvpool_heads& h : {a->q, a->out})
+    if (on_weights(h.data, (__int128)vb * ((__int128)(total - 1) * h.token_stride + (__int128)(h.heads - 1) * h.head_stride + a->cache.head_dim)))
+      return KVPOOL_ERR_INVALID_ARG;
   const OpsDevice* dev = ops_device();
   if (!dev) return KVPOOL_ERR_CUDA;
   std::unique_ptr<Kv4Params> P(new (std::nothrow) Kv4Params);
@@ -1158,6 +1173,9 @@ extern "C" int kvpool_kv4_attend(const kvpool_kv4_args* a, int32_t n, const int6
   const int64_t need = whole ? w.total : space_of(a, n, h_q_len, h_k_len, dev->sms, P.get());
   if (need < 0) return (int)need;
   if (need > 0 && (!d_workspace || workspace_bytes < need || reinterpret_cast<uintptr_t>(d_workspace) % 16 != 0))
+    return KVPOOL_ERR_INVALID_ARG;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(d_workspace), lse = reinterpret_cast<uintptr_t>(a->d_lse);
+  if (need > 0 && (on_rows(d_workspace, need) || on_weights(d_workspace, need) || (lse_bytes > 0 && lse < at + need && at < lse + lse_bytes)))
     return KVPOOL_ERR_INVALID_ARG;
   uint8_t* space = static_cast<uint8_t*>(d_workspace);
   P->q = static_cast<const uint8_t*>(a->q.data);

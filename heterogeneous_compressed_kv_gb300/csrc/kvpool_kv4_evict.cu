@@ -371,9 +371,16 @@ int check_args(const kvpool_kv4_evict_args* a, int32_t n, const int64_t* k_len, 
     if (!out) return true;
     return runs_apart(n, seg, c.kv_heads, head, width);
   };
-  const __int128 index_bytes = (__int128)4 * n * c.kv_heads * a->keep;
-  if (kv4_meets(&c, a->d_index, index_bytes)) return KVPOOL_ERR_INVALID_ARG;
   if (!strides(a->d_weights, a->weight_stride, a->weight_head_stride, len, false)) return KVPOOL_ERR_INVALID_ARG;
+  const __int128 index_bytes = (__int128)4 * n * c.kv_heads * a->keep,
+                 out_table_bytes = a->out_table_width > 0 ? 4 * ((__int128)(n - 1) * a->out_table_stride + a->out_table_width) : 0;
+  auto touch = [](const void* p, __int128 np, const void* q, __int128 nq) {
+    const __int128 x = reinterpret_cast<uintptr_t>(p), y = reinterpret_cast<uintptr_t>(q);
+    return p && q && np > 0 && nq > 0 && x < y + nq && y < x + np;
+  };
+  if (kv4_meets(&c, a->d_index, index_bytes) || touch(a->d_index, index_bytes, a->d_out_table, out_table_bytes) ||
+      runs_touch(a->d_weights, n, a->weight_stride, c.kv_heads, a->weight_head_stride, len, a->d_index, index_bytes))
+    return KVPOOL_ERR_INVALID_ARG;
   if (a->d_out_weights) {
     if (a->out_weight_width < a->keep ||
         !strides(a->d_out_weights, a->out_weight_stride, a->out_weight_head_stride, a->out_weight_width, true))
@@ -383,6 +390,12 @@ int check_args(const kvpool_kv4_evict_args* a, int32_t n, const int64_t* k_len, 
     };
     if (len > 0 && reinterpret_cast<uintptr_t>(a->d_weights) < end(a->d_out_weights, a->out_weight_stride, a->out_weight_head_stride, a->out_weight_width) &&
         reinterpret_cast<uintptr_t>(a->d_out_weights) < end(a->d_weights, a->weight_stride, a->weight_head_stride, len))
+      return KVPOOL_ERR_INVALID_ARG;
+    auto on = [&](const void* p, __int128 bytes) {
+      return runs_touch(a->d_out_weights, n, a->out_weight_stride, c.kv_heads, a->out_weight_head_stride, a->out_weight_width, p, bytes);
+    };
+    if (kv4_meets(&c, a->d_out_weights, n, a->out_weight_stride, a->out_weight_head_stride, a->out_weight_width) ||
+        on(a->d_out_table, out_table_bytes) || on(a->d_index, index_bytes))
       return KVPOOL_ERR_INVALID_ARG;
   }
   return KVPOOL_OK;

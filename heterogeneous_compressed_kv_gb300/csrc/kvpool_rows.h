@@ -81,4 +81,18 @@ inline bool runs_apart(int64_t n1, int64_t s1, int64_t n2, int64_t s2, int64_t l
   return lo >= len && (hi - len) / (n - 1) >= lo;
 }
 
+// Does one of n1 x n2 runs of `len` 4-byte values, s1 and s2 values apart, share a
+// byte with [p, p + bytes)?
+inline bool runs_touch(const void* runs, int64_t n1, int64_t s1, int64_t n2, int64_t s2, int64_t len, const void* p, __int128 bytes) {
+  if (!runs || !p || n1 <= 0 || n2 <= 0 || len <= 0 || bytes <= 0) return false;
+  const __int128 a = reinterpret_cast<uintptr_t>(runs), b = reinterpret_cast<uintptr_t>(p);
+  if (a >= b + bytes || b >= a + 4 * ((__int128)(n1 - 1) * s1 + (__int128)(n2 - 1) * s2 + len)) return false;
+  for (int64_t i = 0; i < n1; ++i)  // (hardly ever: it lies among them)
+    for (int64_t j = 0; j < n2; ++j) {
+      const __int128 x = a + 4 * ((__int128)i * s1 + (__int128)j * s2);
+      if (x < b + bytes && b < x + 4 * (__int128)len) return true;
+    }
+  return false;
+}
+
 }  // namespace kvp

@@ -506,7 +506,8 @@ int kvpool_window_attend(const kvpool_window_args* args, int32_t n, const int64_
  * a NaN or an infinity stands for NaNs.  k_scale, v_scale: powers of two, 2^-16 to 2^16.
  * head_dim 64 or 128; up to 1024 key heads; a segment has at most 2^30 tokens.
  * Nothing is kept between calls but the pages.  Inputs and the table lie apart
- * from what a call writes. */
+ * from what a call writes (calls where they meet are refused; which pages a table
+ * names is not looked at). */
 typedef struct kvpool_kv4 {
   void* d_pages;
   int64_t n_pages;
@@ -593,7 +594,8 @@ int kvpool_kv4_attend(const kvpool_kv4_args* args, int32_t n, const int64_t* h_q
  * shared): its codes and scales are copied.  d_index: [n][kv_heads][keep], the
  * places the tokens had, -1 behind the last.  d_out_weights: NULL, or the weights of
  * what stays (a zero's sign and a NaN's bits may change), zeros behind up to
- * out_weight_width (at least keep); it lies apart from d_weights.  Errors: INVALID_ARG, CUDA. */
+ * out_weight_width (at least keep); it lies apart from d_weights (not between its
+ * rows).  Errors: INVALID_ARG, CUDA. */
 typedef struct kvpool_kv4_evict_args {
   kvpool_kv4 cache;
   const int32_t* d_out_table;
