@@ -601,7 +601,8 @@ class Kv4Cache:
 
     def load(self, table, start, length, dtype=None, out_k=None, out_v=None, stream=None) -> tuple:
         """(k, v): segment i's length[i] tokens from place start[i] on, as the
-        values that they stand for (bfloat16 unless dtype or out_k says float32).
+        values that they stand for (bfloat16 unless dtype or a given output says
+        float32).  Where one output is given the other one is made like it.
         See kvpool_kv4_load in include/kvpool.h."""
         if self._device_now() != self.index:
             with self._torch.cuda.device(self.index):
@@ -616,7 +617,7 @@ class Kv4Cache:
         else:
             if out_k is None or out_v is None:
                 o = out_k if out_k is not None else out_v
-                made = self._empty((sum(length.tolist()), self.kv_heads, self.head_dim), o.dtype if dtype is None else dtype, stream)
+                made = self._empty(o.shape, o.dtype if dtype is None else dtype, stream)
                 out_k, out_v = (made, o) if out_k is None else (o, made)
             like = _like(out_k)
             if like[2] != self.index or like[1] != self.head_dim or out_k.shape != out_v.shape:

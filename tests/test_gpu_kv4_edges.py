@@ -82,3 +82,19 @@ def test_values_too_large_for_a_scale(ks, vs, dtype):
         top = 2.0 ** 20 * s
         assert same(y, F.held(x.float().clamp(-top, top), s)) and not bool(y.isnan().any())
     ok()
+
+
+def test_load_into_one_given_output():
+    """Either output of load may be given, with rows behind the tokens."""
+    g, T = gen(13), 40
+    cache, table = make([T], 16, 2, 64)
+    k, v = fill(cache, table, [T], BF, g)
+    for dtype in (BF, F32):
+        o = torch.full((T + 3, 2, 64), 9.0, dtype=dtype, device="cuda")
+        a, b = cache.load(table, [0], [T], out_k=o)
+        assert a is o and b.dtype is dtype and b.shape == o.shape and same(o[:T], k) and same(b[:T], v) and bool((o[T:] == 9).all())
+        a, b = cache.load(table, [0], [T], out_v=o)
+        assert b is o and a.dtype is dtype and same(o[:T], v) and same(a[:T], k) and bool((o[T:] == 9).all())
+    with pytest.raises(ValueError):
+        cache.load(table, [0], [T], dtype=BF, out_k=o)
+    ok()
