@@ -248,6 +248,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
     const int item = tc_nth(P, threadIdx.x - 32);
     if (item >= 0) table[threadIdx.x - 32] = tc_make(P, item);
   }
+  // Where the group does not divide 128 the query tiles' last rows are nobody's, and no copy writes them: zeros, since a
+  // score of theirs may make their warp rescale, which is another rounding of its rows
+  const int q_rows = P.tile_rows / 2;
+  for (int i = threadIdx.x; i < 2 * (D / 64) * (128 - q_rows) * 8; i += kTcThreads) {
+    const int run = i / ((128 - q_rows) * 8);  // 64 dims of a tile, 128 bytes a row
+    reinterpret_cast<uint4*>(q_tile + run * 16384 + q_rows * 128)[i % ((128 - q_rows) * 8)] = make_uint4(0, 0, 0, 0);
+  }
+  fence_proxy_async();
   if (warp == 9) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
   __syncthreads();
