@@ -232,13 +232,24 @@ const OpsDevice* ops_device();
 // Do prompts of a window call go through its tensor-core form?  (Type, scale,
 // strides; the others are left to fp32 multiply-adds.)
 bool window_tc_able(const kvpool_window_args* a);
-// kvpool_window_workspace and kvpool_window_attend.  even: key lists are cut into
-// parts that fill the multiprocessors evenly (no window, long lists), and a query
-// that is infinite gives NaN whatever the signs of the keys are.
+// How the 4-bit cache calls window attention: all of its prompts in the tensor-core
+// form, nothing hidden, key lists cut into parts that fill the multiprocessors
+// evenly, and NaN for a query that is infinite whatever the signs of the keys are.
+// pieces: one segment, of whose keys this call has some; its rows' states (sums of
+// outputs; largest score and sum) are kept in acc_o [q_rows][q_heads][head_dim] and
+// acc_ml [q_rows][q_heads] from the call with `begin` to the one with `end`, which
+// writes the outputs.
+struct WinDense {
+  bool pieces = false, begin = false, end = false;
+  int64_t behind = 0;  // the place of the last query behind the last key given
+  float* acc_o = nullptr;
+  float2* acc_ml = nullptr;
+};
+// kvpool_window_workspace and kvpool_window_attend (dense: null)
 int64_t window_space(const kvpool_window_args* a, int32_t n, const int64_t* h_q_len, const int64_t* h_k_start,
-                     const int64_t* h_k_len, bool even);
+                     const int64_t* h_k_len, const WinDense* dense);
 int window_run(const kvpool_window_args* a, int32_t n, const int64_t* h_q_len, const int64_t* h_k_start,
-               const int64_t* h_k_len, bool even, void* d_workspace, int64_t workspace_bytes, void* stream);
+               const int64_t* h_k_len, const WinDense* dense, void* d_workspace, int64_t workspace_bytes, void* stream);
 int attend_max_split_len();  // the longest split of a request's sources
 // the first n_entries HCA entries of every request of the launch (the same
 // blocks in all of them), cut into n_split runs: partials in the slots behind

@@ -53,6 +53,7 @@
 #include "kvpool_kv4.h"
 #include "kvpool_mma.cuh"
 #include "kvpool_rows.h"
+#include "kvpool_window.h"
 
 namespace kvp {
 namespace {
@@ -986,61 +987,119 @@ int32_t plan(const kvpool_kv4_args* a, bool prompts, int32_t i0, int32_t n, cons
 }
 
 // The prompts: runs of segments that are prompts (or have no queries), whose
-// tokens are read back to rows of the queries' type.
+// tokens are read back to bf16 rows.  A run's rows take up to kRunBytes of the
+// workspace; a segment of more tokens is a run by itself, taken in pieces: of so
+// many keys, and of queries whose running states take up to kStateBytes.  Measured
+// with 2^26, 2^28, 2^29, 2^30 and 2^31 bytes of rows, and all at once: 1,024 queries
+// of 16 heads behind 1,048,576 tokens 10.7, 8.7, 8.0, 7.6, 7.5 and 7.4 ms (8.6 GB of
+// rows); 64 drafts of 5 tokens, 64 heads on 4, behind 65,536 6.2, 3.8, 3.5, 3.3, 3.1
+// and 3.1 ms (8.6 GB); 8 x 512 queries, 16 heads on 8, behind 131,072 5.2, 4.7, 4.2,
+// 3.7, 3.8 and 4.0 ms (4.3 GB).
+constexpr int64_t kRunBytes = 1ll << 31, kStateBytes = 1ll << 26;
+int64_t token_bytes(const kvpool_kv4_args* a) { return 4LL * a->cache.kv_heads * a->cache.head_dim; }  // of a key's and a value's rows
+
 struct Run {
   int32_t first, end;
-  int64_t q_row, q_rows, kv_rows, bytes;  // bytes: keys' and values' rows
+  int64_t q_row, q_rows, kv_rows;
 };
 bool next_run(const kvpool_kv4_args* a, bool prompts, int32_t* i, int64_t* q_row, int32_t n, const int64_t* q_len, const int64_t* k_len,
               Run* run) {
   while (*i < n && (q_len[*i] == 0 || !is_prompt(a, prompts, q_len[*i], k_len[*i]))) *q_row += q_len[(*i)++];
   if (*i >= n) return false;
-  *run = Run{*i, *i, *q_row, 0, 0, 0};
+  *run = Run{*i, *i, *q_row, 0, 0};
   for (; *i < n && (q_len[*i] == 0 || is_prompt(a, prompts, q_len[*i], k_len[*i])); ++*i) {
+    const int64_t keys = q_len[*i] > 0 ? k_len[*i] : 0;
+    if (run->kv_rows > 0 && (run->kv_rows + keys) * token_bytes(a) > kRunBytes) break;
     run->q_rows += q_len[*i];
-    if (q_len[*i] > 0) run->kv_rows += k_len[*i];
+    run->kv_rows += keys;
   }
   *q_row += run->q_rows;
   run->end = *i;
-  run->bytes = run->kv_rows * a->cache.kv_heads * a->cache.head_dim * (a->dtype == KVPOOL_BF16 ? 2 : 4);
   return true;
 }
 
-// The window call of a run: everything up to the query is visible.
-struct WindowCall {
-  kvpool_window_args args;
-  std::unique_ptr<int64_t[]> start, len;  // [segments of the run], keys read back
+// A run's workspace: keys' rows, values' rows, states of a segment in pieces, and
+// what window attention asks for.
+struct RunSpace {
+  int64_t rows;           // bytes of the keys' rows
+  int64_t state_o, state_ml;
+  int64_t queries, keys;  // the most of a piece (0: no pieces)
+  int64_t window() const { return 2 * rows + state_o + state_ml; }  // where that starts
 };
-bool window_call(const kvpool_kv4_args* a, const Run& run, const int64_t* q_len, const int64_t* k_len, void* space,
-                 WindowCall* w) {
-  const int32_t n = run.end - run.first;
-  w->start.reset(new (std::nothrow) int64_t[n]);
-  w->len.reset(new (std::nothrow) int64_t[n]);
-  if (!w->start || !w->len) return false;
-  int64_t at = 0;
-  for (int32_t i = 0; i < n; ++i) {
-    w->len[i] = q_len[run.first + i] > 0 ? k_len[run.first + i] : 0;
-    w->start[i] = at;
-    at += w->len[i];
-  }
-  const int64_t vb = a->dtype == KVPOOL_BF16 ? 2 : 4;
-  kvpool_window_args& x = w->args;
-  x = kvpool_window_args{};
+RunSpace run_space(const kvpool_kv4_args* a, const Run& run, const int64_t* q_len, const int64_t* k_len) {
+  RunSpace s{};
+  s.rows = run.kv_rows * token_bytes(a) / 2;
+  if (2 * s.rows <= kRunBytes) return s;
+  const int64_t tile = 2 * (kTcTileRows / (a->q.heads / a->cache.kv_heads));
+  const int64_t state = (int64_t)a->q.heads * (a->cache.head_dim + 2) * 4;
+  const int64_t most = kStateBytes / state;
+  s.queries = std::min(q_len[run.first], most < tile ? most : most / tile * tile);
+  s.keys = kRunBytes / token_bytes(a) / 128 * 128;
+  s.rows = s.keys * token_bytes(a) / 2;
+  s.state_o = s.queries * a->q.heads * a->cache.head_dim * 4;
+  s.state_ml = (s.queries * a->q.heads * 8 + 15) / 16 * 16;
+  return s;
+}
+
+// The window call of query rows `row` .. row + queries - 1 over `keys` rows read
+// back: everything up to the query is visible.
+kvpool_window_args window_call(const kvpool_kv4_args* a, const RunSpace& s, uint8_t* space, int64_t row, int64_t queries, int64_t keys) {
+  kvpool_window_args x{};
   x.dtype = a->dtype;
   x.head_dim = a->cache.head_dim;
   x.q = a->q;
   x.out = a->out;
-  x.q.data = static_cast<const uint8_t*>(a->q.data) + vb * run.q_row * a->q.token_stride;
-  x.out.data = static_cast<const uint8_t*>(a->out.data) + vb * run.q_row * a->out.token_stride;
-  x.k = x.v = read_back_rows(a, space);
-  x.v.data = static_cast<uint8_t*>(space) + run.bytes;
-  x.q_rows = run.q_rows;
-  x.kv_rows = run.kv_rows;
-  x.d_lse = a->d_lse ? a->d_lse + run.q_row * a->q.heads : nullptr;
+  x.q.data = static_cast<const uint8_t*>(a->q.data) + 2 * row * a->q.token_stride;
+  x.out.data = static_cast<const uint8_t*>(a->out.data) + 2 * row * a->out.token_stride;
+  x.k = read_back_rows(a, space);
+  x.v = read_back_rows(a, space + s.rows);
+  x.q_rows = queries;
+  x.kv_rows = keys;
+  x.d_lse = a->d_lse ? a->d_lse + row * a->q.heads : nullptr;
   x.window = 1 << 30;
   x.scale = a->scale;
-  return true;
+  return x;
 }
+
+// Call f(first query, queries, first key, keys, dense) for every piece of a
+// segment, in order; it returns a KVPOOL_ code, of which the first that is none ends this.
+template <typename F>
+int each_piece(const RunSpace& s, int64_t q_len, int64_t k_len, F f) {
+  for (int64_t q0 = 0; q0 < q_len; q0 += s.queries) {
+    const int64_t nq = std::min(s.queries, q_len - q0), last = k_len - q_len + q0 + nq;  // keys up to the last query
+    const int64_t keys = std::max<int64_t>(1, last);  // (queries at places below 0 see none of one key)
+    for (int64_t k0 = 0; k0 < keys; k0 += s.keys) {
+      const int64_t nk = std::min(s.keys, keys - k0);
+      WinDense d;
+      d.pieces = true;
+      d.begin = k0 == 0;
+      d.end = k0 + nk == keys;
+      d.behind = last - (k0 + nk);
+      const int rc = f(q0, nq, k0, nk, d);
+      if (rc != KVPOOL_OK) return rc;
+    }
+  }
+  return KVPOOL_OK;
+}
+
+// The segments of a run as window attention takes them: keys read back, one after the other.
+struct RunKeys {
+  std::unique_ptr<int64_t[]> start, len, zero;
+  bool fill(const Run& run, const int64_t* q_len, const int64_t* k_len) {
+    const int32_t n = run.end - run.first;
+    start.reset(new (std::nothrow) int64_t[n]);
+    len.reset(new (std::nothrow) int64_t[n]);
+    zero.reset(new (std::nothrow) int64_t[n]());
+    if (!start || !len || !zero) return false;
+    int64_t at = 0;
+    for (int32_t i = 0; i < n; ++i) {
+      len[i] = q_len[run.first + i] > 0 ? k_len[run.first + i] : 0;
+      start[i] = at;
+      at += len[i];
+    }
+    return true;
+  }
+};
 
 template <int D, int NT, bool F32, bool UNIT>
 cudaError_t launch_attend(const Kv4Params& P, int n_sms, cudaStream_t s) {
@@ -1108,13 +1167,31 @@ int64_t space_of(const kvpool_kv4_args* a, int32_t n, const int64_t* q_len, cons
   }
   Run run;
   row = 0;
+  uint8_t* const none = reinterpret_cast<uint8_t*>((uintptr_t)16);  // (sizes only)
   for (int32_t i = 0; next_run(a, prompts, &i, &row, n, q_len, k_len, &run);) {
-    WindowCall call;
-    if (!window_call(a, run, q_len, k_len, nullptr, &call)) return KVPOOL_ERR_INVALID_ARG;
-    call.args.k.data = call.args.v.data = reinterpret_cast<const void*>((uintptr_t)16);  // (sizes only)
-    const int64_t x = window_space(&call.args, run.end - run.first, q_len + run.first, call.start.get(), call.len.get(), true);
-    if (x < 0) return x;
-    most = std::max(most, 2 * run.bytes + x);
+    const RunSpace s = run_space(a, run, q_len, k_len);
+    int64_t window = 0;
+    if (s.queries > 0) {
+      const int64_t zero = 0;
+      int64_t known[2] = {0, 0};  // (a piece like the one before asks for as much)
+      const int rc = each_piece(s, q_len[run.first], k_len[run.first], [&](int64_t q0, int64_t nq, int64_t, int64_t nk, const WinDense& d) {
+        if (nq == known[0] && nk == known[1]) return (int)KVPOOL_OK;
+        known[0] = nq, known[1] = nk;
+        const kvpool_window_args x = window_call(a, s, none, run.q_row + q0, nq, nk);
+        const int64_t y = window_space(&x, 1, &nq, &zero, &nk, &d);
+        window = std::max(window, y);
+        return y < 0 ? (int)y : (int)KVPOOL_OK;
+      });
+      if (rc != KVPOOL_OK) return rc;
+    } else {
+      RunKeys keys;
+      if (!keys.fill(run, q_len, k_len)) return KVPOOL_ERR_INVALID_ARG;
+      const kvpool_window_args x = window_call(a, s, none, run.q_row, run.q_rows, run.kv_rows);
+      const WinDense d;
+      window = window_space(&x, run.end - run.first, q_len + run.first, keys.start.get(), keys.len.get(), &d);
+      if (window < 0) return window;
+    }
+    most = std::max(most, s.window() + window);
   }
   return most;
 }
@@ -1210,16 +1287,27 @@ extern "C" int kvpool_kv4_attend(const kvpool_kv4_args* a, int32_t n, const int6
   Run run;
   row = 0;
   for (int32_t i = 0; !whole && next_run(a, prompts, &i, &row, n, h_q_len, h_k_len, &run);) {
-    WindowCall call;
-    if (!window_call(a, run, h_q_len, h_k_len, space, &call)) return KVPOOL_ERR_INVALID_ARG;
-    const int32_t m = run.end - run.first;
-    std::unique_ptr<int64_t[]> zero(new (std::nothrow) int64_t[m]());
-    if (!zero) return KVPOOL_ERR_INVALID_ARG;
-    int rc = kv4_load_rows(&a->cache, a->dtype, call.args.k, call.args.v, m, run.first, zero.get(), call.len.get(), dev->err,
-                           stream);
-    if (rc != KVPOOL_OK) return rc;
-    rc = window_run(&call.args, m, h_q_len + run.first, call.start.get(), call.len.get(), true, space + 2 * run.bytes,
-                    workspace_bytes - 2 * run.bytes, stream);
+    const RunSpace r = run_space(a, run, h_q_len, h_k_len);
+    // keys and values of m segments from table row `first` on are read back and attended to
+    auto part = [&](int32_t first, int32_t m, const int64_t* start, const int64_t* q_len, const int64_t* at, const int64_t* len,
+                    const kvpool_window_args& x, const WinDense& d) {
+      const int rc = kv4_load_rows(&a->cache, a->dtype, x.k, x.v, m, first, start, len, dev->err, stream);
+      return rc != KVPOOL_OK ? rc : window_run(&x, m, q_len, at, len, &d, space + r.window(), workspace_bytes - r.window(), stream);
+    };
+    int rc;
+    if (r.queries > 0) {
+      const int64_t zero = 0;
+      rc = each_piece(r, h_q_len[run.first], h_k_len[run.first], [&](int64_t q0, int64_t nq, int64_t k0, int64_t nk, WinDense d) {
+        d.acc_o = reinterpret_cast<float*>(space + 2 * r.rows);
+        d.acc_ml = reinterpret_cast<float2*>(space + 2 * r.rows + r.state_o);
+        return part(run.first, 1, &k0, &nq, &zero, &nk, window_call(a, r, space, run.q_row + q0, nq, nk), d);
+      });
+    } else {
+      RunKeys keys;
+      if (!keys.fill(run, h_q_len, h_k_len)) return KVPOOL_ERR_INVALID_ARG;
+      rc = part(run.first, run.end - run.first, keys.zero.get(), h_q_len + run.first, keys.start.get(), keys.len.get(),
+                window_call(a, r, space, run.q_row, run.q_rows, run.kv_rows), WinDense{});
+    }
     if (rc != KVPOOL_OK) return rc;
   }
   return KVPOOL_OK;

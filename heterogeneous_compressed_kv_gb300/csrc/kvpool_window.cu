@@ -139,7 +139,8 @@ __global__ void __launch_bounds__(kFmaThreads) window_fma_kernel(const __grid_co
 
 // ---- merge of the splits ------------------------------------------------------
 // One warp per row of a tile whose keys were split: out = sum_s 2^(m_s - M)
-// o_s / sum_s 2^(m_s - M) l_s, splits in order (the same sum on every run).
+// o_s / sum_s 2^(m_s - M) l_s, splits in order (the same sum on every run).  With a
+// segment in pieces the sums go on where those of the piece before ended.
 constexpr int kMergeWarps = 8;
 template <int T, int D>
 __global__ void __launch_bounds__(kMergeWarps * 32) window_merge_kernel(const __grid_constant__ WinParams P) {
@@ -164,9 +165,18 @@ __global__ void __launch_bounds__(kMergeWarps * 32) window_merge_kernel(const __
   if (row >= w.n_tok * P.group) return;
   const WinSeg& S = P.segs[w.seg];
   constexpr int V = D / 32;
+  const int64_t tok = S.q_row0 + w.tok0 + row / P.group;
+  const int h = w.hk * P.group + row % P.group;
+  const int64_t state = tok * P.q_heads + h;  // (pieces)
   float m = -INFINITY, l = 0.0f, acc[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+  if (P.pieces && !P.acc_begin) {
+    const float2 ml = P.acc_ml[state];
+    m = ml.x, l = ml.y;
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = P.acc_o[state * D + lane * V + i];
+  }
 #pragma unroll 4
   for (int s = 0; s < w.n_split; ++s) {
     const int64_t pr = ((int64_t)w.slot + (int64_t)s * P.kv_heads) * P.tile_rows + row;
@@ -182,10 +192,14 @@ __global__ void __launch_bounds__(kMergeWarps * 32) window_merge_kernel(const __
     for (int i = 0; i < V; ++i) acc[i] = acc[i] * fa + x[i] * fb;
     m = mx;
   }
+  if (P.pieces && !P.acc_end) {
+    if (lane == 0) P.acc_ml[state] = make_float2(m, l);
+#pragma unroll
+    for (int i = 0; i < V; ++i) P.acc_o[state * D + lane * V + i] = acc[i];
+    return;
+  }
   l = win_sum(P, w.pos0 + row / P.group, l);
   const float inv = l > 0.0f ? 1.0f / l : l;  // (a NaN stays one)
-  const int64_t tok = S.q_row0 + w.tok0 + row / P.group;
-  const int h = w.hk * P.group + row % P.group;
   const int64_t at = tok * P.o_tok + h * P.o_head + lane * V;
   if constexpr (T == KVPOOL_F32) {
 #pragma unroll
@@ -265,9 +279,9 @@ bool tc_able(const kvpool_window_args* a) {
          ok(a->v.head_stride, a->v.heads);
 }
 
-Form form_of(const kvpool_window_args* a, bool tc, int64_t q_len, int64_t k_len) {
+Form form_of(const kvpool_window_args* a, bool tc, const WinDense* dense, int64_t q_len, int64_t k_len) {
   const int64_t rows = q_len * (a->q.heads / a->k.heads);
-  return rows <= kTokRows ? kFormTok : tc && k_len > 0 ? kFormTc : kFormFma;
+  return rows <= kTokRows && !dense ? kFormTok : tc && k_len > 0 ? kFormTc : kFormFma;
 }
 
 // the most keys that a tile of the segment sees
@@ -309,14 +323,14 @@ int64_t even_part(const kvpool_window_args* a, const WinParams& P, int n_sms) {
 // Fill segments [i0, n) of one launch (at most kMaxWinSegs with queries);
 // returns the next segment.  A launch with few tiles cuts each tile's keys
 // into parts (merged by a second kernel) so that the GPU is filled.
-int plan_launch(const kvpool_window_args* a, Form form, bool tc, bool even, int32_t i0, int32_t n, const int64_t* q_len,
-                const int64_t* k_start, const int64_t* k_len, int64_t q_row0, int n_sms, WinParams* P, int64_t* next_row,
+int plan_launch(const kvpool_window_args* a, Form form, bool tc, const WinDense* dense, int32_t i0, int32_t n,
+                const int64_t* q_len, const int64_t* k_start, const int64_t* k_len, int64_t q_row0, int n_sms, WinParams* P, int64_t* next_row,
                 int64_t* slots) {
   const int Hk = a->k.heads;
   int64_t most = 1;  // queries of a single-token segment
   if (form == kFormTok)
     for (int j = i0, m = 0; j < n && m < kMaxWinSegs; ++j)
-      if (q_len[j] > 0 && form_of(a, tc, q_len[j], k_len[j]) == form) most = std::max(most, q_len[j]), ++m;
+      if (q_len[j] > 0 && form_of(a, tc, dense, q_len[j], k_len[j]) == form) most = std::max(most, q_len[j]), ++m;
   P->tile_tokens = form == kFormTok  ? (int32_t)most
                    : form == kFormTc ? 2 * (kTcTileRows / P->group)
                                      : kFmaRows / P->group;
@@ -325,7 +339,7 @@ int plan_launch(const kvpool_window_args* a, Form form, bool tc, bool even, int3
   P->n_segs = 0;
   int64_t tiles = 0;
   for (; i < n && P->n_segs < kMaxWinSegs; ++i) {
-    if (q_len[i] > 0 && form_of(a, tc, q_len[i], k_len[i]) == form) {
+    if (q_len[i] > 0 && form_of(a, tc, dense, q_len[i], k_len[i]) == form) {
       WinSeg& S = P->segs[P->n_segs++];
       S = WinSeg{};
       S.q_row0 = q_row0;
@@ -344,7 +358,7 @@ int plan_launch(const kvpool_window_args* a, Form form, bool tc, bool even, int3
   const int64_t min_keys = form == kFormTok ? 256 : form == kFormTc ? 128 : kFmaKeys;
   const int64_t want = n_sms * (form == kFormTc ? 1LL : 4LL);
   const int64_t fill = tiles == 0 ? 1 : form == kFormFma ? (want + tiles - 1) / tiles : std::max<int64_t>(1, want / tiles);
-  const int64_t part = even && form == kFormTc && tiles > 0 ? even_part(a, *P, n_sms) : 0;
+  const int64_t part = dense && form == kFormTc && tiles > 0 ? even_part(a, *P, n_sms) : 0;
   int64_t items = 0, slot = 0, merge = 0, rows = 0;
   for (int s = 0; s < P->n_segs; ++s) {
     WinSeg& S = P->segs[s];
@@ -356,7 +370,7 @@ int plan_launch(const kvpool_window_args* a, Form form, bool tc, bool even, int3
     S.part_base = (int32_t)slot;
     S.merge_base = (int32_t)merge;
     items += st * split;
-    if (split > 1) {
+    if (split > 1 || P->pieces) {
       slot += st * split;
       merge += st;
       rows = std::max<int64_t>(rows, std::min<int64_t>(S.q_len, P->tile_tokens) * P->group);
@@ -369,7 +383,15 @@ int plan_launch(const kvpool_window_args* a, Form form, bool tc, bool even, int3
   return i;
 }
 
-void fill_params(const kvpool_window_args* a, WinParams* P) {
+void fill_params(const kvpool_window_args* a, const WinDense* dense, WinParams* P) {
+  const WinDense d = dense ? *dense : WinDense{};
+  P->pieces = d.pieces;
+  P->acc_begin = d.begin;
+  P->acc_end = d.end;
+  P->behind = (int32_t)d.behind;
+  P->acc_o = d.acc_o;
+  P->acc_ml = d.acc_ml;
+  P->nan_rows = dense != nullptr;
   P->q = static_cast<const uint8_t*>(a->q.data);
   P->k = static_cast<const uint8_t*>(a->k.data);
   P->v = static_cast<const uint8_t*>(a->v.data);
@@ -439,7 +461,7 @@ const OpsDevice* ops_device() {
 bool window_tc_able(const kvpool_window_args* a) { return tc_able(a); }
 
 int64_t window_space(const kvpool_window_args* a, int32_t n, const int64_t* h_q_len, const int64_t* h_k_start,
-                     const int64_t* h_k_len, bool even) {
+                     const int64_t* h_k_len, const WinDense* dense) {
   int64_t total = 0;
   const int rc = check_args(a, n, h_q_len, h_k_start, h_k_len, &total);
   if (rc != KVPOOL_OK) return rc;
@@ -449,12 +471,12 @@ int64_t window_space(const kvpool_window_args* a, int32_t n, const int64_t* h_q_
   const int sms = dev->sms;
   std::unique_ptr<WinParams> P(new (std::nothrow) WinParams);
   if (!P) return KVPOOL_ERR_INVALID_ARG;
-  fill_params(a, P.get());
+  fill_params(a, dense, P.get());
   const bool tc = tc_able(a);
   int64_t most = 0;
   for (int f = 0; f < kForms; ++f)
     for (int64_t i = 0, row = 0, slots = 0; i < n;) {
-      i = plan_launch(a, (Form)f, tc, even, (int32_t)i, n, h_q_len, h_k_start, h_k_len, row, sms, P.get(), &row, &slots);
+      i = plan_launch(a, (Form)f, tc, dense, (int32_t)i, n, h_q_len, h_k_start, h_k_len, row, sms, P.get(), &row, &slots);
       if (P->n_items < 0) return KVPOOL_ERR_INVALID_ARG;
       most = std::max(most, slots * slot_bytes(*P, a->head_dim));
     }
@@ -462,13 +484,13 @@ int64_t window_space(const kvpool_window_args* a, int32_t n, const int64_t* h_q_
 }
 
 int window_run(const kvpool_window_args* a, int32_t n, const int64_t* h_q_len, const int64_t* h_k_start,
-               const int64_t* h_k_len, bool even, void* d_workspace, int64_t workspace_bytes, void* stream) {
+               const int64_t* h_k_len, const WinDense* dense, void* d_workspace, int64_t workspace_bytes, void* stream) {
   int64_t total = 0;
   const int rc = check_args(a, n, h_q_len, h_k_start, h_k_len, &total);
   if (rc != KVPOOL_OK) return rc;
   if (total == 0) return KVPOOL_OK;
   if (out_meets_inputs(a, n, h_q_len, h_k_start, h_k_len, total)) return KVPOOL_ERR_INVALID_ARG;
-  const int64_t need = window_space(a, n, h_q_len, h_k_start, h_k_len, even);
+  const int64_t need = window_space(a, n, h_q_len, h_k_start, h_k_len, dense);
   if (need < 0) return (int)need;
   if (need > 0 && (!d_workspace || workspace_bytes < need || reinterpret_cast<uintptr_t>(d_workspace) % 16 != 0))
     return KVPOOL_ERR_INVALID_ARG;
@@ -477,14 +499,13 @@ int window_run(const kvpool_window_args* a, int32_t n, const int64_t* h_q_len, c
   const int sms = dev->sms;
   std::unique_ptr<WinParams> P(new (std::nothrow) WinParams);
   if (!P) return KVPOOL_ERR_INVALID_ARG;
-  fill_params(a, P.get());
+  fill_params(a, dense, P.get());
   P->err = dev->err;
-  P->nan_rows = even;
   const bool tc = tc_able(a);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   for (int f = 0; f < kForms; ++f)
     for (int64_t i = 0, row = 0, slots = 0; i < n;) {
-      i = plan_launch(a, (Form)f, tc, even, (int32_t)i, n, h_q_len, h_k_start, h_k_len, row, sms, P.get(), &row, &slots);
+      i = plan_launch(a, (Form)f, tc, dense, (int32_t)i, n, h_q_len, h_k_start, h_k_len, row, sms, P.get(), &row, &slots);
       if (P->n_segs == 0) continue;
       P->part_o = static_cast<float*>(d_workspace);
       P->part_ml = reinterpret_cast<float2*>(P->part_o + slots * P->tile_rows * a->head_dim);
@@ -510,13 +531,13 @@ int window_run(const kvpool_window_args* a, int32_t n, const int64_t* h_q_len, c
 
 extern "C" int64_t kvpool_window_workspace(const kvpool_window_args* a, int32_t n, const int64_t* h_q_len,
                                            const int64_t* h_k_start, const int64_t* h_k_len) {
-  return kvp::window_space(a, n, h_q_len, h_k_start, h_k_len, false);
+  return kvp::window_space(a, n, h_q_len, h_k_start, h_k_len, nullptr);
 }
 
 extern "C" int kvpool_window_attend(const kvpool_window_args* a, int32_t n, const int64_t* h_q_len,
                                     const int64_t* h_k_start, const int64_t* h_k_len, void* d_workspace,
                                     int64_t workspace_bytes, void* stream) {
-  return kvp::window_run(a, n, h_q_len, h_k_start, h_k_len, false, d_workspace, workspace_bytes, stream);
+  return kvp::window_run(a, n, h_q_len, h_k_start, h_k_len, nullptr, d_workspace, workspace_bytes, stream);
 }
 
 extern "C" int kvpool_window_check(void* stream, uint32_t* h_flags) {

@@ -35,6 +35,10 @@ struct WinParams {
   int32_t tile_tokens, tile_rows;
   int32_t n_segs, n_items;
   int32_t n_merge, merge_rows;  // (tile, key head)s to merge, the most rows that one has
+  // one segment in pieces (see WinDense):
+  int32_t pieces, acc_begin, acc_end, behind;
+  float* acc_o;
+  float2* acc_ml;
   int32_t nan_rows;  // does a row whose scores are -inf alone give NaN?  (0: zeros, as one that sees nothing)
   float* part_o;    // [slots][tile_rows][head_dim]
   float2* part_ml;  // [slots][tile_rows]: (max in the log2 domain, sum)
@@ -73,8 +77,8 @@ __device__ __forceinline__ WinItem win_item(const WinParams& P, int item) {
   w.split = r % S.n_split;
   w.tok0 = (r / S.n_split) * P.tile_tokens;
   w.n_tok = min(P.tile_tokens, S.q_len - w.tok0);
-  w.pos0 = S.k_len - S.q_len + w.tok0;
-  const int hi = w.pos0 + w.n_tok - 1;  // the last query's own position
+  w.pos0 = S.k_len - S.q_len + w.tok0 + P.behind;
+  const int hi = min(w.pos0 + w.n_tok, S.k_len) - 1;  // the last query's own position, or the last key's
   w.lo = max(0, w.pos0 - P.window + 1);
   // a window of 0: of these, only the first tokens are anybody's
   w.n_w = max(0, (P.window > 0 ? hi : min(hi, P.n_sink - 1)) - w.lo + 1);

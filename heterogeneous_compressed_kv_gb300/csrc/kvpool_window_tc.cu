@@ -74,7 +74,7 @@ struct TcMaps {
 // A work item as the roles take it: its keys are the first n_s tokens and n_w
 // from lo on, in steps [a, b) of 128.
 struct TcItem {
-  int hk, q_row, k_row, n_tok, pos0, n_split, slot, k_len;
+  int hk, q_row, k_row, n_tok, pos0, part, slot, k_len;  // part: its rows are partials
   int n_s, lo, n_w, a, b;
   int pad[3];
 };
@@ -150,7 +150,7 @@ __device__ __forceinline__ TcItem tc_make(const WinParams& P, int item) {
   x.k_row = (int)S.k_start;
   x.n_tok = w.n_tok;
   x.pos0 = w.pos0;
-  x.n_split = w.n_split;
+  x.part = w.n_split > 1 || P.pieces;
   x.slot = w.slot;
   x.k_len = S.k_len;
   x.n_s = w.n_s;
@@ -554,7 +554,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
       const bool mine = r_tok < q.n && row < tt * P.group;
       const int64_t tok = w.q_row + t * tt + r_tok;
       const int head = w.hk * P.group + r_head;
-      if (w.n_split == 1) l = win_sum(P, pos, l);
+      if (!w.part) l = win_sum(P, pos, l);
       const float inv = l > 0.0f ? 1.0f / l : l;  // (a NaN stays one)
       if (!first) {
         if (!warp_wait(&o_full[t], n_o & 1, P.err)) break;
@@ -578,7 +578,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
           __syncwarp();
           if (lane == 0) mbar_arrive(&o_free[t]);
         }
-        if (mine && w.n_split > 1) {
+        if (mine && w.part) {
           float4* dst = reinterpret_cast<float4*>(P.part_o + pr * D + 32 * i);
 #pragma unroll
           for (int j = 0; j < 8; ++j)
@@ -600,7 +600,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
         }
       }
       if (mine) {
-        if (w.n_split > 1) P.part_ml[pr] = make_float2(l > 0.0f ? m : -INFINITY, l);
+        if (w.part) P.part_ml[pr] = make_float2(l > 0.0f ? m : -INFINITY, l);
         else if (P.lse) P.lse[tok * P.q_heads + head] = win_lse(m, l);
       }
     }

@@ -563,7 +563,8 @@ int kvpool_kv4_load(const kvpool_kv4* cache, int32_t dtype, const kvpool_heads* 
  * rows in the workspace and go through window attention with everything visible,
  * as kvpool_window_attend says.
  * d_workspace: kvpool_kv4_workspace bytes (16-byte aligned, may be NULL when that is
- * 0); calls that overlap on the GPU need one each.  It, d_lse and d_weights lie
+ * 0), 9 * 2^28 at most, and 4 for every query head of a row, with every token of its
+ * segment, where d_weights is given; calls that overlap on the GPU need one each.  It, d_lse and d_weights lie
  * apart from everything else.  The lengths are read during the call: a captured
  * call replays with the same ones.  Errors: INVALID_ARG, CUDA. */
 typedef struct kvpool_kv4_args {

@@ -98,3 +98,61 @@ def test_load_into_one_given_output():
     with pytest.raises(ValueError):
         cache.load(table, [0], [T], dtype=BF, out_k=o)
     ok()
+
+
+SPACE = 9 << 28  # bytes that a call without weights asks for at most
+
+
+@pytest.mark.parametrize("q_len,k_len,hq,hk,d", [
+    ([1024], [1 << 20], 16, 16, 128), ([5] * 64, [131072] * 64, 64, 4, 128), ([4096] * 4, [1 << 18] * 4, 64, 64, 128), ([2048], [1 << 24], 16, 1, 64),
+    ([1 << 20], [1 << 20], 16, 4, 128), ([512], [1 << 16], 1024, 1024, 128), ([80] * 500, [40000] * 500, 8, 8, 64)])
+def test_a_prompt_s_workspace_is_bounded(q_len, k_len, hq, hk, d):
+    """However many tokens are read back, their rows do not lie in the workspace all at once.  (Sizes only.)"""
+    cache = K.Kv4Cache(torch.zeros((1, K.kv4_page_bytes(hk, d, 1024)), dtype=torch.uint8, device="cuda"), hk, d, 1024)
+    table = torch.zeros((len(k_len), max(k_len) // 1024 + 1), dtype=torch.int32, device="cuda")
+    q = torch.empty((sum(q_len), hq, d), dtype=BF, device="cuda")
+    assert cache.workspace(q, table, q_len, k_len) <= SPACE
+
+
+@pytest.mark.parametrize("q_len,k_len,hq,hk,d,page", [
+    ([40], [70001], 128, 64, 128, 64), ([1, 70, 200, 2], [300, 66000, 3000, 70], 256, 128, 64, 16),
+    ([9001], [66003], 64, 64, 128, 1024), ([70100], [66010], 64, 64, 128, 256), ([300, 300], [65536, 131073], 64, 64, 128, 64),
+    ([128], [100000], 192, 64, 128, 128)])
+def test_prompts_behind_more_tokens_than_are_read_back_at_once(q_len, k_len, hq, hk, d, page):
+    """Segments of more than 65,536 tokens at these heads are attended to a piece at a time (of queries too, where there are
+    many), their running sums kept in between: beside others, over their own queries, and with an infinite query."""
+    from tests.test_gpu_kv4_prompts import check, held
+    g = gen(sum(q_len) + hk)
+    cache, table = make(k_len, page, hk, d)
+    fill_in_parts(cache, table, k_len, g)
+    rows = sum(q_len) + 2
+    buf = randn((rows, hq + 1, d), BF, g)
+    q = buf[:, :hq]
+    lse = torch.full((rows, hq), 7.0, device="cuda")
+    out = torch.full((rows, hq, d), 7.0, dtype=BF, device="cuda")
+    assert cache.workspace(q, table, q_len, k_len) <= SPACE
+    cache.attend(q, table, q_len, k_len, out=out, lse=lse)
+    k, v = held(cache, table, k_len)
+    check(q, k, v, q_len, k_len, d ** -0.5, out, lse)
+    assert bool((out[-2:] == 7).all()) and bool((lse[-2:] == 7).all())
+    # An infinite query makes its own row NaN.  The rows of its warp may be rescaled at another step than before (one row's
+    # larger maximum rescales them all), which moves their roundings: they are held to the formula again, not to the same bits.
+    row, finite, want = sum(q_len) - 1, q.clone(), out.clone()
+    q[row, 1, 0] = math.inf
+    cache.attend(q, table, q_len, k_len, out=want)
+    assert bool(want[row, 1].isnan().all())
+    other = want.clone()
+    other[row, 1] = out[row, 1]
+    check(finite, k, v, q_len, k_len, d ** -0.5, other, lse)
+    last, behind = buf[:, hq].clone(), q[-2:].clone()
+    cache.attend(q, table, q_len, k_len, out=q)
+    assert same(q[:-2], want[:-2]) and torch.equal(buf[:, hq], last) and torch.equal(q[-2:], behind)
+    ok()
+
+
+def fill_in_parts(cache, table, lens, g):
+    for i, n in enumerate(lens):
+        for t in range(0, n, 1 << 15):
+            m = min(1 << 15, n - t)
+            k, v = (randn((m, cache.kv_heads, cache.head_dim), BF, g) for _ in range(2))
+            cache.store(k, v, table[i:i + 1], [t], [m])
