@@ -235,12 +235,15 @@ bool window_tc_able(const kvpool_window_args* a);
 // How the 4-bit cache calls window attention: all of its prompts in the tensor-core
 // form, nothing hidden, key lists cut into parts that fill the multiprocessors
 // evenly, and NaN for a query that is infinite whatever the signs of the keys are.
+// V holds fp16 numbers, of which v_scale times are the values, and softmax weights go
+// into their product as fp16 numbers.
 // pieces: one segment, of whose keys this call has some; its rows' states (sums of
 // outputs; largest score and sum) are kept in acc_o [q_rows][q_heads][head_dim] and
 // acc_ml [q_rows][q_heads] from the call with `begin` to the one with `end`, which
 // writes the outputs.
 struct WinDense {
   bool pieces = false, begin = false, end = false;
+  float v_scale = 1.0f;
   int64_t behind = 0;  // the place of the last query behind the last key given
   float* acc_o = nullptr;
   float2* acc_ml = nullptr;

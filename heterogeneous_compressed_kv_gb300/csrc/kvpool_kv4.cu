@@ -277,7 +277,9 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
 }
 __device__ __forceinline__ float2 f16x2_to_f32x2(uint32_t a) { return __half22float2(*reinterpret_cast<const __half2*>(&a)); }
 
-template <int T, int D>
+// HALVES: values as fp16 numbers and without v_scale (codes times their scale are
+// exact in fp16, and then in a product of fp16 numbers)
+template <int T, int D, bool HALVES>
 __global__ void __launch_bounds__(kWarps * 32) kv4_load_kernel(const __grid_constant__ MoveParams P) {
   pdl_start();
   using L = Kv4Tile<D>;
@@ -332,15 +334,28 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_load_kernel(const __grid_cons
     uint32_t h[8];
     e2m1x8_to_f16x2x4(vc[it].x, h);
     e2m1x8_to_f16x2x4(vc[it].y, h + 4);
-    float x0[8], x1[8];
+    const bool in0 = r >= t.lo && r < t.hi, in1 = r + 1 >= t.lo && r + 1 < t.hi;
+    if constexpr (HALVES) {
+      uint32_t x[2][4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 f = f16x2_to_f32x2(mul_f16x2(h[i], s2));
-      x0[i] = f.x * P.c.v_scale;
-      x1[i] = f.y * P.c.v_scale;
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t a = mul_f16x2(h[2 * i], s2), b = mul_f16x2(h[2 * i + 1], s2);
+        x[0][i] = __byte_perm(a, b, 0x5410);
+        x[1][i] = __byte_perm(a, b, 0x7632);
+      }
+      if (in0) *reinterpret_cast<uint4*>(v + r * P.v_tok) = make_uint4(x[0][0], x[0][1], x[0][2], x[0][3]);
+      if (in1) *reinterpret_cast<uint4*>(v + (r + 1) * P.v_tok) = make_uint4(x[1][0], x[1][1], x[1][2], x[1][3]);
+    } else {
+      float x0[8], x1[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 f = f16x2_to_f32x2(mul_f16x2(h[i], s2));
+        x0[i] = f.x * P.c.v_scale;
+        x1[i] = f.y * P.c.v_scale;
+      }
+      if (in0) store8<T>(v + r * P.v_tok, x0);
+      if (in1) store8<T>(v + (r + 1) * P.v_tok, x1);
     }
-    if (r >= t.lo && r < t.hi) store8<T>(v + r * P.v_tok, x0);
-    if (r + 1 >= t.lo && r + 1 < t.hi) store8<T>(v + (r + 1) * P.v_tok, x1);
   }
 }
 
@@ -349,14 +364,17 @@ bool power_of_two(float x) {
   return x > 0.0f && std::isfinite(x) && std::frexp(x, &e) == 0.5f && e - 1 >= -16 && e - 1 <= 16;
 }
 
+enum Move { kStore, kLoad, kLoadHalves };
 template <int T, int D>
-cudaError_t launch_move(bool store, const MoveParams& P, cudaStream_t s) {
+cudaError_t launch_move(Move what, const MoveParams& P, cudaStream_t s) {
   const dim3 grid((unsigned)((P.n_tasks + kWarps - 1) / kWarps)), block(kWarps * 32);
-  return store ? launch_kernel(true, kv4_store_kernel<T, D>, grid, block, 0, s, P)
-               : launch_kernel(true, kv4_load_kernel<T, D>, grid, block, 0, s, P);
+  if constexpr (T == KVPOOL_BF16)
+    if (what == kLoadHalves) return launch_kernel(true, kv4_load_kernel<T, D, true>, grid, block, 0, s, P);
+  return what == kStore ? launch_kernel(true, kv4_store_kernel<T, D>, grid, block, 0, s, P)
+                        : launch_kernel(true, kv4_load_kernel<T, D, false>, grid, block, 0, s, P);
 }
 
-int move_rows(bool store, const kvpool_kv4* c, int32_t dtype, const kvpool_heads& k, const kvpool_heads& v, int32_t n,
+int move_rows(Move what, const kvpool_kv4* c, int32_t dtype, const kvpool_heads& k, const kvpool_heads& v, int32_t n,
               int64_t row0, const int64_t* start, const int64_t* len, uint32_t* err, void* stream) {
   std::unique_ptr<MoveParams> P(new (std::nothrow) MoveParams);
   if (!P) return KVPOOL_ERR_INVALID_ARG;
@@ -392,9 +410,9 @@ int move_rows(bool store, const kvpool_kv4* c, int32_t dtype, const kvpool_heads
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (dtype == KVPOOL_F32)
-      e = c->head_dim == 128 ? launch_move<KVPOOL_F32, 128>(store, *P, s) : launch_move<KVPOOL_F32, 64>(store, *P, s);
+      e = c->head_dim == 128 ? launch_move<KVPOOL_F32, 128>(what, *P, s) : launch_move<KVPOOL_F32, 64>(what, *P, s);
     else
-      e = c->head_dim == 128 ? launch_move<KVPOOL_BF16, 128>(store, *P, s) : launch_move<KVPOOL_BF16, 64>(store, *P, s);
+      e = c->head_dim == 128 ? launch_move<KVPOOL_BF16, 128>(what, *P, s) : launch_move<KVPOOL_BF16, 64>(what, *P, s);
     if (e != cudaSuccess) return KVPOOL_ERR_CUDA;
   }
   return KVPOOL_OK;
@@ -479,9 +497,9 @@ Kv4Cache kv4_cache(const kvpool_kv4* c, int64_t row0, uint32_t* err) {
   return C;
 }
 
-int kv4_load_rows(const kvpool_kv4* c, int32_t dtype, const kvpool_heads& k, const kvpool_heads& v, int32_t n,
-                  int64_t row0, const int64_t* start, const int64_t* len, uint32_t* err, void* stream) {
-  return move_rows(false, c, dtype, k, v, n, row0, start, len, err, stream);
+int kv4_load_rows(const kvpool_kv4* c, const kvpool_heads& k, const kvpool_heads& v, int32_t n, int64_t row0,
+                  const int64_t* start, const int64_t* len, uint32_t* err, void* stream) {
+  return move_rows(kLoadHalves, c, KVPOOL_BF16, k, v, n, row0, start, len, err, stream);
 }
 
 }  // namespace kvp
@@ -501,7 +519,7 @@ extern "C" int kvpool_kv4_store(const kvpool_kv4* c, int32_t dtype, const kvpool
   if (rc != KVPOOL_OK || total == 0) return rc;
   const OpsDevice* dev = ops_device();
   if (!dev) return KVPOOL_ERR_CUDA;
-  return move_rows(true, c, dtype, *k, *v, n, 0, h_start, h_n_new, dev->err, stream);
+  return move_rows(kStore, c, dtype, *k, *v, n, 0, h_start, h_n_new, dev->err, stream);
 }
 
 extern "C" int kvpool_kv4_load(const kvpool_kv4* c, int32_t dtype, const kvpool_heads* k, const kvpool_heads* v,
@@ -517,5 +535,5 @@ extern "C" int kvpool_kv4_load(const kvpool_kv4* c, int32_t dtype, const kvpool_
   if (total == 0) return KVPOOL_OK;
   const OpsDevice* dev = ops_device();
   if (!dev) return KVPOOL_ERR_CUDA;
-  return move_rows(false, c, dtype, *k, *v, n, 0, h_start, h_len, dev->err, stream);
+  return move_rows(kLoad, c, dtype, *k, *v, n, 0, h_start, h_len, dev->err, stream);
 }

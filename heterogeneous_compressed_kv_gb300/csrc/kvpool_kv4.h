@@ -73,9 +73,10 @@ bool kv4_meets(const kvpool_kv4* c, const void* p, __int128 bytes);
 bool kv4_meets(const kvpool_kv4* c, const float* w, int64_t n, int64_t seg_stride, int64_t head_stride, int64_t len);
 inline int64_t kv4_tokens(const kvpool_kv4* c) { return (int64_t)c->table_width * c->page_tokens; }
 
-// Read the tokens [0, len[i]) of table rows row0 + i into rows of k and v
-// (contiguous segments).  Returns a KVPOOL_ code.
-int kv4_load_rows(const kvpool_kv4* c, int32_t dtype, const kvpool_heads& k, const kvpool_heads& v, int32_t n,
-                  int64_t row0, const int64_t* start, const int64_t* len, uint32_t* err, void* stream);
+// Read len[i] tokens from place start[i] on of table rows row0 + i into rows of k
+// (bf16) and v (fp16, not multiplied by v_scale), one segment after the other.
+// Returns a KVPOOL_ code.
+int kv4_load_rows(const kvpool_kv4* c, const kvpool_heads& k, const kvpool_heads& v, int32_t n, int64_t row0,
+                  const int64_t* start, const int64_t* len, uint32_t* err, void* stream);
 
 }  // namespace kvp

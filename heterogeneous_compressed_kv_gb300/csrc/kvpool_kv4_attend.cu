@@ -7,8 +7,8 @@
 //   exp(scale <q, k_t> - lse).
 //
 // Single tokens, drafts and all fp32 queries go through the kernel below; the
-// tokens of longer bf16 segments are read back to bf16 rows (exact) and go through
-// window attention where that pays.
+// tokens of longer bf16 segments are read back to rows (keys in bf16, values in
+// fp16, exact) and go through window attention where that pays.
 //
 // Bound: reading the cache, 1.125 bytes for a key's and a value's number.  The
 // whole list of keys, across segments and heads, is cut into equal shares, one to
@@ -987,7 +987,7 @@ int32_t plan(const kvpool_kv4_args* a, bool prompts, int32_t i0, int32_t n, cons
 }
 
 // The prompts: runs of segments that are prompts (or have no queries), whose
-// tokens are read back to bf16 rows.  A run's rows take up to kRunBytes of the
+// tokens are read back to rows of 16-bit numbers.  A run's rows take up to kRunBytes of the
 // workspace; a segment of more tokens is a run by itself, taken in pieces: of so
 // many keys, and of queries whose running states take up to kStateBytes.  Measured
 // with 2^26, 2^28, 2^29, 2^30 and 2^31 bytes of rows, and all at once: 1,024 queries
@@ -1290,8 +1290,9 @@ extern "C" int kvpool_kv4_attend(const kvpool_kv4_args* a, int32_t n, const int6
     const RunSpace r = run_space(a, run, h_q_len, h_k_len);
     // keys and values of m segments from table row `first` on are read back and attended to
     auto part = [&](int32_t first, int32_t m, const int64_t* start, const int64_t* q_len, const int64_t* at, const int64_t* len,
-                    const kvpool_window_args& x, const WinDense& d) {
-      const int rc = kv4_load_rows(&a->cache, a->dtype, x.k, x.v, m, first, start, len, dev->err, stream);
+                    const kvpool_window_args& x, WinDense d) {
+      d.v_scale = a->cache.v_scale;
+      const int rc = kv4_load_rows(&a->cache, x.k, x.v, m, first, start, len, dev->err, stream);
       return rc != KVPOOL_OK ? rc : window_run(&x, m, q_len, at, len, &d, space + r.window(), workspace_bytes - r.window(), stream);
     };
     int rc;

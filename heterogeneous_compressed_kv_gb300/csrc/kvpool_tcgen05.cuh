@@ -91,9 +91,9 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead) {
          (1ull << 46) | (2ull << 61);
 }
 
-// bf16 x bf16 -> fp32, M x N; trans_b: B's rows run along K
-constexpr uint32_t bf16_idesc(int m, int n, bool trans_b) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | ((trans_b ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
+// bf16 x bf16 -> fp32, M x N (f16: fp16 x fp16); trans_b: B's rows run along K
+constexpr uint32_t bf16_idesc(int m, int n, bool trans_b, bool f16 = false) {
+  return (1u << 4) | (f16 ? 0u : (1u << 7) | (1u << 10)) | ((trans_b ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
          ((uint32_t)(m >> 4) << 24);
 }
 

@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) window_merge_kernel(const __
     return;
   }
   l = win_sum(P, w.pos0 + row / P.group, l);
-  const float inv = l > 0.0f ? 1.0f / l : l;  // (a NaN stays one)
+  const float inv = l > 0.0f ? P.v_scale / l : l;  // (a NaN stays one)
   const int64_t at = tok * P.o_tok + h * P.o_head + lane * V;
   if constexpr (T == KVPOOL_F32) {
 #pragma unroll
@@ -391,7 +391,8 @@ void fill_params(const kvpool_window_args* a, const WinDense* dense, WinParams* 
   P->behind = (int32_t)d.behind;
   P->acc_o = d.acc_o;
   P->acc_ml = d.acc_ml;
-  P->nan_rows = dense != nullptr;
+  P->dense = dense != nullptr;
+  P->v_scale = d.v_scale;
   P->q = static_cast<const uint8_t*>(a->q.data);
   P->k = static_cast<const uint8_t*>(a->k.data);
   P->v = static_cast<const uint8_t*>(a->v.data);

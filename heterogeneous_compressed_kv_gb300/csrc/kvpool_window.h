@@ -39,7 +39,8 @@ struct WinParams {
   int32_t pieces, acc_begin, acc_end, behind;
   float* acc_o;
   float2* acc_ml;
-  int32_t nan_rows;  // does a row whose scores are -inf alone give NaN?  (0: zeros, as one that sees nothing)
+  int32_t dense;     // V and the weights are fp16, and a row whose scores are -inf alone gives NaN (0: zeros, as one that sees nothing)
+  float v_scale;     // of the outputs (1: none)
   float* part_o;    // [slots][tile_rows][head_dim]
   float2* part_ml;  // [slots][tile_rows]: (max in the log2 domain, sum)
   uint32_t* err;
@@ -100,7 +101,7 @@ __device__ __forceinline__ float win_lse(float m, float l) {
 // A row's sum of weights, at its position: NaN where it sees tokens, got nothing
 // from them and the call says so (a query that is infinite)
 __device__ __forceinline__ float win_sum(const WinParams& P, int pos, float l) {
-  return P.nan_rows && l == 0.0f && pos >= 0 ? NAN : l;
+  return P.dense && l == 0.0f && pos >= 0 ? NAN : l;
 }
 
 // Single-token form: at most 16 query rows per key head, the whole segment in

@@ -19,6 +19,11 @@
 // outputs are off by 2.0e-3 to 2.3e-3 of their norm, where their own rounding
 // alone leaves 1.5e-3 to 1.7e-3.
 //
+// The 4-bit cache's values are exact in fp16 (F16): their tiles and the weights are
+// fp16 then (2^-11 of a weight), in units of 2^-6 of the row's maximum or older
+// maximum, so that the largest is 2^6 to 2^14 and what fp16's smallest step takes
+// from small ones is 2^-31 of it.
+//
 // The outputs are rescaled only when a row's maximum grows by more than 2^8:
 // until then its weights are taken against the older maximum (bf16 keeps its
 // relative precision up to 2^8, the sums are fp32), so the read-modify-write
@@ -57,6 +62,7 @@ constexpr int kTcKeys = 128;
 constexpr int kTcThreads = 320;
 constexpr int kTcTable = 96;  // items of a CTA that are worked out at its start
 constexpr float kRescale = 8.0f;  // log2 growth of the maximum that rescales O
+constexpr float kF16Up = 6.0f;    // log2 of the maximum's weight, F16
 
 template <int D>
 struct TcShape {
@@ -172,8 +178,9 @@ __device__ __forceinline__ float tc_max32(const uint32_t* x, float mx) {
 }
 __device__ __forceinline__ float tc_max64(const uint32_t* x, float mx) { return tc_max32(x + 32, tc_max32(x, mx)); }
 
-// weights 2^(x scale - base) of 32 scores as bf16 to 16 words of tensor
+// weights 2^(x scale - base) of 32 scores as bf16 or fp16 to 16 words of tensor
 // memory, and their fp32 sums (packed pairs)
+template <bool F16>
 __device__ __forceinline__ void tc_weights32(const uint32_t* x, float scale, float base, uint64_t* sum, uint32_t addr) {
   const uint64_t scale2 = pack2(scale, scale), base2 = pack2(-base, -base);
   uint32_t pk[16];
@@ -182,8 +189,13 @@ __device__ __forceinline__ void tc_weights32(const uint32_t* x, float scale, flo
     const float2 y = unpack2(fma2(pack2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), scale2, base2));
     const float p0 = ex2f(y.x), p1 = ex2f(y.y);
     sum[j & 1] = add2(sum[j & 1], pack2(p0, p1));
-    const __nv_bfloat162 z = __floats2bfloat162_rn(p0, p1);
-    pk[j] = *reinterpret_cast<const uint32_t*>(&z);
+    if constexpr (F16) {
+      const __half2 z = __floats2half2_rn(p0, p1);
+      pk[j] = *reinterpret_cast<const uint32_t*>(&z);
+    } else {
+      const __nv_bfloat162 z = __floats2bfloat162_rn(p0, p1);
+      pk[j] = *reinterpret_cast<const uint32_t*>(&z);
+    }
   }
   tmem_st16(addr, pk);
 }
@@ -211,7 +223,7 @@ __device__ __forceinline__ void tc_maximum(float mn, bool& first, float& m, floa
   }
 }
 
-template <int D>
+template <int D, bool F16>
 __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_constant__ WinParams P,
                                                                   const __grid_constant__ TcMaps M) {
   using Sh = TcShape<D>;
@@ -347,7 +359,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
   } else if (warp == 9) {
     // ---- matrix products (one thread) ----
     if (elect_one()) {
-      constexpr uint32_t kIdQK = bf16_idesc(128, kTcKeys, false), kIdPV = bf16_idesc(128, D, true);
+      constexpr uint32_t kIdQK = bf16_idesc(128, kTcKeys, false), kIdPV = bf16_idesc(128, D, true, F16);
       const uint64_t q_desc = smem_desc(smem_addr(q_tile), 16), k_desc = smem_desc(smem_addr(ring), 16),
                      v_desc = smem_desc(smem_addr(ring), 16384);
       int stage = 0;
@@ -464,6 +476,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
     const int r_tok = row / P.group, r_head = row % P.group;
     const int tt = P.tile_tokens / 2;
     const float scale = P.scale_log2;
+    constexpr float kUp = F16 ? kF16Up : 0.0f;  // (m - 0 is m: the bf16 form's bits are without it)
     int n_s = 0, n_o = 0;
     bool ok = true;
 #pragma unroll 1
@@ -501,9 +514,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
           for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, x + 32 * i);
           tmem_wait_ld();
           tc_maximum<D>(tc_max64(x + 64, tc_max64(x, -INFINITY)) * scale, first, m, l, to);
-          const float base = m == -INFINITY ? 0.0f : m;
+          const float base = m == -INFINITY ? 0.0f : m - kUp;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) tc_weights32(x + 32 * i, scale, base, sum, ts + 16 * i);
+          for (int i = 0; i < 4; ++i) tc_weights32<F16>(x + 32 * i, scale, base, sum, ts + 16 * i);
         } else {
           // 32 scores at a time, twice (little code: it is run through cold);
           // a quarter that none of the warp's rows sees is skipped
@@ -529,12 +542,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
           for (int i = 0; i < 4; ++i)
             if (quarter(i)) mx = tc_max32(x, mx);
           tc_maximum<D>(mx * scale, first, m, l, to);
-          const float base = m == -INFINITY ? 0.0f : m;
+          const float base = m == -INFINITY ? 0.0f : m - kUp;
           // weights of columns 32 i .. 32 i + 31 go to words 16 i .. 16 i + 15: over scores that have been read by then
 #pragma unroll 1
           for (int i = 0; i < 4; ++i) {
             if (quarter(i)) {
-              tc_weights32(x, scale, base, sum, ts + 16 * i);
+              tc_weights32<F16>(x, scale, base, sum, ts + 16 * i);
             } else {
 #pragma unroll
               for (int j = 0; j < 16; ++j) x[j] = 0u;
@@ -555,7 +568,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
       const int64_t tok = w.q_row + t * tt + r_tok;
       const int head = w.hk * P.group + r_head;
       if (!w.part) l = win_sum(P, pos, l);
-      const float inv = l > 0.0f ? 1.0f / l : l;  // (a NaN stays one)
+      const float inv = l > 0.0f ? P.v_scale / l : l;  // (a NaN stays one)
       if (!first) {
         if (!warp_wait(&o_full[t], n_o & 1, P.err)) break;
         ++n_o;
@@ -600,8 +613,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
         }
       }
       if (mine) {
-        if (w.part) P.part_ml[pr] = make_float2(l > 0.0f ? m : -INFINITY, l);
-        else if (P.lse) P.lse[tok * P.q_heads + head] = win_lse(m, l);
+        if (w.part) P.part_ml[pr] = make_float2(l > 0.0f ? m - kUp : -INFINITY, l);
+        else if (P.lse) P.lse[tok * P.q_heads + head] = win_lse(m - kUp, l);
       }
     }
   }
@@ -639,9 +652,9 @@ bool encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, 
 // a stride in bytes; an axis of length 1 takes any legal one
 cuuint64_t stride_bytes(int64_t values, int64_t extent) { return extent > 1 ? (cuuint64_t)values * 2 : 16; }
 
-template <int D>
+template <int D, bool F16>
 cudaError_t launch_tc(const WinParams& P, const TcMaps& M, int ctas, cudaStream_t s) {
-  auto* kern = window_tc_kernel<D>;
+  auto* kern = window_tc_kernel<D, F16>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TcShape<D>::kSmem);
   if (e != cudaSuccess) return e;
   return launch_kernel(true, kern, dim3(ctas), dim3(kTcThreads), TcShape<D>::kSmem, s, P, M);
@@ -665,7 +678,8 @@ int launch_window_tc(const WinParams& P, int head_dim, int64_t q_rows, int64_t k
     return (int)cudaErrorInvalidValue;
   const int ctas = P.n_items < n_sms ? P.n_items : n_sms;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return (int)(head_dim == 128 ? launch_tc<128>(P, M, ctas, s) : launch_tc<64>(P, M, ctas, s));
+  if (P.dense) return (int)(head_dim == 128 ? launch_tc<128, true>(P, M, ctas, s) : launch_tc<64, true>(P, M, ctas, s));
+  return (int)(head_dim == 128 ? launch_tc<128, false>(P, M, ctas, s) : launch_tc<64, false>(P, M, ctas, s));
 }
 
 }  // namespace kvp

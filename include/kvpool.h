@@ -560,8 +560,8 @@ int kvpool_kv4_load(const kvpool_kv4* cache, int32_t dtype, const kvpool_heads* 
  * where that is more), softmax weights to 2^-11 of each for bf16 outputs and to
  * 2^-22 for fp32 ones (or 2^-31 of their row's largest).  Long segments of bf16
  * queries (more than 64 rows per key head, h_q_len * group) may be read back to
- * rows in the workspace and go through window attention with everything visible,
- * as kvpool_window_attend says.
+ * rows in the workspace and go through window attention's products; their roundings
+ * are these as well.
  * d_workspace: kvpool_kv4_workspace bytes (16-byte aligned, may be NULL when that is
  * 0), 9 * 2^28 at most, and 4 for every query head of a row, with every token of its
  * segment, where d_weights is given; calls that overlap on the GPU need one each.  It, d_lse and d_weights lie

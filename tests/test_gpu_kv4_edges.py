@@ -150,9 +150,27 @@ def test_prompts_behind_more_tokens_than_are_read_back_at_once(q_len, k_len, hq,
     ok()
 
 
-def fill_in_parts(cache, table, lens, g):
+def fill_in_parts(cache, table, lens, g, v_size=1.0):
     for i, n in enumerate(lens):
         for t in range(0, n, 1 << 15):
             m = min(1 << 15, n - t)
             k, v = (randn((m, cache.kv_heads, cache.head_dim), BF, g) for _ in range(2))
-            cache.store(k, v, table[i:i + 1], [t], [m])
+            cache.store(k, v * v_size, table[i:i + 1], [t], [m])
+
+
+@pytest.mark.parametrize("q_len,k_len,hq,hk,d,scale", [
+    ([1, 300, 0, 200, 1, 150], [50, 4000, 30, 2500, 700, 150], 8, 2, 128, 1.0), ([100, 5], [8000, 8000], 16, 1, 64, 0.5),
+    ([700], [6000], 6, 2, 64, 2.0), ([600], [60000], 4, 4, 128, None), ([128], [66000], 64, 64, 128, 0.3)])
+def test_weights_of_prompts_that_are_read_back_have_eleven_bits(q_len, k_len, hq, hk, d, scale):
+    """However a segment is attended to, softmax weights go into their products with half an fp16 step each (2^-11): scales
+    that make a few of them large show it."""
+    from tests.test_gpu_kv4_prompts import check, held, rows_read_back
+    g = gen(hq + d)
+    scale = d ** -0.5 if scale is None else scale
+    cache, table = make(k_len, 64, hk, d, vs=2.0 ** -14)
+    fill_in_parts(cache, table, k_len, g, 2.0 ** -14)
+    q, lse = randn((sum(q_len), hq, d), BF, g), torch.empty((sum(q_len), hq), device="cuda")
+    assert rows_read_back(cache, q, table, q_len, k_len, 2000, scale=scale)
+    out = cache.attend(q, table, q_len, k_len, scale=scale, lse=lse)
+    check(q, *held(cache, table, k_len), q_len, k_len, scale, out, lse, r=2.0 ** -11)
+    ok()
