@@ -271,12 +271,6 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_store_kernel(const __grid_con
   }
 }
 
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-__device__ __forceinline__ float2 f16x2_to_f32x2(uint32_t a) { return __half22float2(*reinterpret_cast<const __half2*>(&a)); }
-
 // HALVES: values as fp16 numbers and without v_scale (codes times their scale are
 // exact in fp16, and then in a product of fp16 numbers)
 template <int T, int D, bool HALVES>
@@ -321,7 +315,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_load_kernel(const __grid_cons
     float x[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 f = f16x2_to_f32x2(mul_f16x2(h[i], s2));
+      const float2 f = unpack_f16(mul_f16x2(h[i], s2));
       x[2 * i] = f.x * P.c.k_scale;
       x[2 * i + 1] = f.y * P.c.k_scale;
     }
@@ -349,7 +343,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_load_kernel(const __grid_cons
       float x0[8], x1[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float2 f = f16x2_to_f32x2(mul_f16x2(h[i], s2));
+        const float2 f = unpack_f16(mul_f16x2(h[i], s2));
         x0[i] = f.x * P.c.v_scale;
         x1[i] = f.y * P.c.v_scale;
       }

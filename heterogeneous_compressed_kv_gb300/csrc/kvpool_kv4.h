@@ -50,6 +50,12 @@ __device__ __forceinline__ int kv4_swizzle(int pair) {
   return D == 128 ? 2 * (pair & 3) : 4 * ((pair >> 1) & 1);
 }
 
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ float2 unpack_f16(uint32_t a) { return __half22float2(*reinterpret_cast<const __half2*>(&a)); }
+
 // The page id of a tile of table row `row`, or -1 (and a flag) if it is none.
 __device__ __forceinline__ int kv4_page(const Kv4Cache& C, int64_t row, int tile) {
   const int id = C.table[row * C.table_stride + (tile >> C.page_shift)];

@@ -152,20 +152,24 @@ __device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
   const __half2 r = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&r);
 }
-__device__ __forceinline__ float2 unpack_f16(uint32_t a) { return __half22float2(*reinterpret_cast<const __half2*>(&a)); }
 __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                    smem_addr(dst)),
                "l"(src), "r"(bytes), "r"(smem_addr(bar))
                : "memory");
+}
+
+// four neighbouring values of an output, times inv
+template <bool F32>
+__device__ __forceinline__ void put4(uint8_t* out, int64_t at, float4 y, float inv) {
+  if constexpr (F32)
+    *reinterpret_cast<float4*>(out + 4 * at) = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+  else
+    *reinterpret_cast<uint2*>(out + 2 * at) = make_uint2(pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv));
 }
 
 constexpr int kStages = 3;
@@ -630,11 +634,7 @@ __global__ void __launch_bounds__(kv4_warps(NT, F32) * 32, 1) kv4_attend_kernel(
         const int64_t tok = S.q_row0 + gr / P.group;
         const int h = head * P.group + gr % P.group;
         const int64_t at = tok * P.o_tok + h * P.o_head + x;
-        if constexpr (F32)
-          *reinterpret_cast<float4*>(P.out + 4 * at) = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
-        else
-          *reinterpret_cast<uint2*>(P.out + 2 * at) =
-              make_uint2(pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv));
+        put4<F32>(P.out, at, y, inv);
         if (x == 0) {
           const float z = lse2_of(mx, sum);
           if (P.lse) P.lse[tok * (P.c.kv_heads * P.group) + h] = z * 0.69314718055994531f;
@@ -718,10 +718,7 @@ __device__ void kv4_merge_row(const Kv4Params& P, int id, int slices) {
   const int64_t tok = S.q_row0 + gr / P.group;
   const int h = head * P.group + gr % P.group;
   const int64_t at = tok * P.o_tok + h * P.o_head + 4 * lane;
-  if constexpr (F32)
-    *reinterpret_cast<float4*>(P.out + 4 * at) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-  else
-    *reinterpret_cast<uint2*>(P.out + 2 * at) = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  put4<F32>(P.out, at, acc, inv);
   if (lane == 0 && P.lse) P.lse[tok * (P.c.kv_heads * P.group) + h] = lse2_of(m, l) * 0.69314718055994531f;
 }
 
