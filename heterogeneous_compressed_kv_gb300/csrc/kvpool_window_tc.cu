@@ -204,7 +204,7 @@ __device__ __forceinline__ void tc_weights32(const uint32_t* x, float scale, flo
 template <int D>
 __device__ __forceinline__ void tc_maximum(float mn, bool& first, float& m, float& l, uint32_t to) {
   if (first) {
-    m = mn;
+    m = fmaxf(m, mn);
     first = false;
   } else if (__any_sync(0xffffffffu, mn > m + kRescale)) {
     const float m2 = fmaxf(m, mn);
@@ -260,14 +260,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
     const int item = tc_nth(P, threadIdx.x - 32);
     if (item >= 0) table[threadIdx.x - 32] = tc_make(P, item);
   }
-  // Where the group does not divide 128 the query tiles' last rows are nobody's, and no copy writes them: zeros, since a
-  // score of theirs may make their warp rescale, which is another rounding of its rows
-  const int q_rows = P.tile_rows / 2;
-  for (int i = threadIdx.x; i < 2 * (D / 64) * (128 - q_rows) * 8; i += kTcThreads) {
-    const int run = i / ((128 - q_rows) * 8);  // 64 dims of a tile, 128 bytes a row
-    reinterpret_cast<uint4*>(q_tile + run * 16384 + q_rows * 128)[i % ((128 - q_rows) * 8)] = make_uint4(0, 0, 0, 0);
-  }
-  fence_proxy_async();
   if (warp == 9) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
   __syncthreads();
@@ -487,7 +479,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
       const TcTile q = tc_tile(P, w, t);
       const TcNeed need = tc_need(P, w, q);
       const int pos = q.p0 + r_tok;
-      float m = -INFINITY, l = 0.0f;  // m: of the scaled scores (log2)
+      const bool mine = r_tok < q.n && row < tt * P.group;
+      // m: of the scaled scores (log2).  A row that is not the tile's has no say in when its warp rescales, since its scores
+      // are of other segments' queries (or of outputs that are written over them meanwhile), or of what shared memory held:
+      // it starts where nothing is larger.
+      float m = mine ? -INFINITY : INFINITY, l = 0.0f;
       bool first = true;
 #pragma unroll 1
       for (int st = w.a; st < w.b; ++st) {
@@ -564,7 +560,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
       }
       if (!ok) break;
       // ---- outputs of the tile ----
-      const bool mine = r_tok < q.n && row < tt * P.group;
       const int64_t tok = w.q_row + t * tt + r_tok;
       const int head = w.hk * P.group + r_head;
       if (!w.part) l = win_sum(P, pos, l);

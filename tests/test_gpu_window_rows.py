@@ -32,3 +32,25 @@ def test_the_same_bits_whatever_ran_before(group, d):
     for out, lse in runs[1:]:
         assert torch.equal(out, runs[0][0]) and torch.equal(lse, runs[0][1])
     assert K.window_check() == (K.OK, 0)
+
+
+@pytest.mark.parametrize("group,d,n", [(1, 128, 130), (2, 64, 70), (4, 128, 33), (3, 64, 50)])
+def test_the_same_bits_whatever_lies_behind_a_segment(group, d, n):
+    """A query tile that ends inside the next segments' rows: a segment's bits do not depend on those, which outputs written
+    over the queries may have replaced by then."""
+    g = torch.Generator(device="cuda").manual_seed(group)
+    segs, T, hk = 80, 2000, 8
+    size = 1 + torch.arange(T, device="cuda") / 300  # later keys are larger: maxima keep growing
+    k = (torch.randn((T, hk, d), device="cuda", generator=g) * size[:, None, None]).to(BF)
+    v = torch.randn((T, hk, d), device="cuda", generator=g).to(BF)
+    q = torch.randn((segs * n, hk * group, d), device="cuda", generator=g).to(BF)
+    args = ([n] * segs, [0] * segs, [T] * segs, 1 << 20)
+    want = K.window_attend(q, k, v, *args)
+    for _ in range(3):
+        over = q.clone()
+        K.window_attend(over, k, v, *args, out=over)
+        assert torch.equal(over, want)
+    q.view(segs, n, hk * group, d)[1::2] *= 40  # every other segment's queries
+    again = K.window_attend(q, k, v, *args)
+    assert torch.equal(again.view(segs, -1)[0::2], want.view(segs, -1)[0::2])
+    assert K.window_check() == (K.OK, 0)
