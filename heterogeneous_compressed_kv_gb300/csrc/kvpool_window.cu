@@ -376,6 +376,13 @@ int plan_launch(const kvpool_window_args* a, Form form, bool tc, const WinDense*
       rows = std::max<int64_t>(rows, std::min<int64_t>(S.q_len, P->tile_tokens) * P->group);
     }
   }
+  // the longest sum, in steps (first tokens and window apart)
+  int64_t steps = 0;
+  for (int s = 0; form == kFormTc && s < P->n_segs; ++s) {
+    const int64_t all = tile_keys(a, P->segs[s].q_len, P->segs[s].k_len, P->tile_tokens) / 128 + 2;
+    steps = std::max(steps, (all + P->segs[s].n_split - 1) / P->segs[s].n_split);
+  }
+  P->long_sums = steps > kTcSumSteps;
   P->n_items = items <= (1 << 30) ? (int32_t)items : -1;
   P->n_merge = (int32_t)merge;
   P->merge_rows = (int32_t)rows;
@@ -414,7 +421,18 @@ void fill_params(const kvpool_window_args* a, const WinDense* dense, WinParams* 
   P->scale_log2 = a->scale * 1.4426950408889634f;
 }
 
-int64_t slot_bytes(const WinParams& P, int head_dim) { return (int64_t)P.tile_rows * (head_dim + 2) * 4; }
+// A launch's workspace: partial outputs, their maxima and sums, and the tensor-core form's sums.
+struct WinSpace {
+  int64_t part_ml, sums, total;
+};
+WinSpace win_space(const WinParams& P, int head_dim, int64_t slots, int n_sms) {
+  WinSpace w;
+  w.part_ml = slots * P.tile_rows * head_dim * 4;
+  w.sums = (w.part_ml + slots * P.tile_rows * 8 + 15) / 16 * 16;
+  const int64_t ctas = P.long_sums ? std::min<int64_t>(P.n_items, n_sms) : 0;
+  w.total = w.sums + ctas * 2 * kTcTileRows * (head_dim + 1) * 4;
+  return w;
+}
 
 template <int T, int D>
 cudaError_t launch_fma(const WinParams& P, cudaStream_t s) {
@@ -479,7 +497,7 @@ int64_t window_space(const kvpool_window_args* a, int32_t n, const int64_t* h_q_
     for (int64_t i = 0, row = 0, slots = 0; i < n;) {
       i = plan_launch(a, (Form)f, tc, dense, (int32_t)i, n, h_q_len, h_k_start, h_k_len, row, sms, P.get(), &row, &slots);
       if (P->n_items < 0) return KVPOOL_ERR_INVALID_ARG;
-      most = std::max(most, slots * slot_bytes(*P, a->head_dim));
+      if (P->n_segs > 0) most = std::max(most, win_space(*P, a->head_dim, slots, sms).total);
     }
   return most;
 }
@@ -508,8 +526,11 @@ int window_run(const kvpool_window_args* a, int32_t n, const int64_t* h_q_len, c
     for (int64_t i = 0, row = 0, slots = 0; i < n;) {
       i = plan_launch(a, (Form)f, tc, dense, (int32_t)i, n, h_q_len, h_k_start, h_k_len, row, sms, P.get(), &row, &slots);
       if (P->n_segs == 0) continue;
-      P->part_o = static_cast<float*>(d_workspace);
-      P->part_ml = reinterpret_cast<float2*>(P->part_o + slots * P->tile_rows * a->head_dim);
+      const WinSpace w = win_space(*P, a->head_dim, slots, sms);
+      uint8_t* space = static_cast<uint8_t*>(d_workspace);
+      P->part_o = reinterpret_cast<float*>(space);
+      P->part_ml = reinterpret_cast<float2*>(space + w.part_ml);
+      P->sums = reinterpret_cast<float*>(space + w.sums);
       cudaError_t e = cudaSuccess;
       if (f == kFormTok) e = (cudaError_t)launch_window_tok(*P, a->dtype, a->head_dim, stream);
       else if (f == kFormTc) e = (cudaError_t)launch_window_tc(*P, a->head_dim, a->q_rows, a->kv_rows, sms, stream);

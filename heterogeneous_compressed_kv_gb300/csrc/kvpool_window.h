@@ -43,6 +43,10 @@ struct WinParams {
   float v_scale;     // of the outputs (1: none)
   float* part_o;    // [slots][tile_rows][head_dim]
   float2* part_ml;  // [slots][tile_rows]: (max in the log2 domain, sum)
+  // tensor-core form, items of more than kTcSumSteps steps of keys: the rows' sums of
+  // outputs, [CTA][2][128] rows of head_dim + 1 numbers (null: no such items)
+  float* sums;
+  int32_t long_sums;
   uint32_t* err;
   WinSeg segs[kMaxWinSegs];
 };
@@ -112,6 +116,7 @@ int launch_window_tok(const WinParams& P, int dtype, int head_dim, void* stream)
 // Tensor-core form of a launch of prompts (bf16); tiles of two times
 // tile_tokens / 2 tokens.  Returns a cudaError_t.
 constexpr int kTcTileRows = 128;
+constexpr int kTcSumSteps = 128;  // (a power of two)
 int launch_window_tc(const WinParams& P, int head_dim, int64_t q_rows, int64_t kv_rows, int n_sms, void* stream);
 
 }  // namespace kvp

@@ -29,6 +29,18 @@
 // relative precision up to 2^8, the sums are fp32), so the read-modify-write
 // of O leaves the critical path.
 //
+// The tensor core cuts its sums off instead of rounding them: 65,536 additions of 16
+// keys' products in a row left outputs 0.7% too small (4,096 queries behind 1,048,576
+// tokens, values of one sign; error 7.2e-3 of their norm, their rounding alone is
+// 1.7e-3).  So a sum in tensor memory is 16,384 keys long at most; a thread then adds
+// its row's to fp32 sums in the workspace (20 MB, L2), with rounding (1.68e-3
+// there).  Calls without such items run a kernel without this.  With it, heads of
+// 128 take 0 to 1.5% longer (16,384 queries of 16 heads on 4 behind 262,144 tokens
+// 23.3 ms, 23.7 without), heads of 64 5 to 9% (1.29 -> 1.36 ms for 4,096 queries
+// behind 65,536, of which the sums take a third; the loop's registers the rest).
+// Measured and not kept: vector atomics instead of reading the sums (D = 64 7.99
+// ms where this takes 7.71), the same in a function of its own (8.0).
+//
 // Rows of K and V behind a segment, or between the first tokens and the window,
 // never count: scores are masked, and such V rows are not copied (boxes of 16
 // and of 1 row up to the last one that holds values, zeros behind it).
@@ -123,6 +135,7 @@ __device__ __forceinline__ TcTile tc_tile(const WinParams& P, const TcItem& w, i
 struct TcNeed {
   int sink, lo, hi;
   __device__ __forceinline__ bool operator()(int st) const { return st < sink || (st >= lo && st < hi); }
+  __device__ __forceinline__ bool more(int st) const { return st + 1 < sink || max(st + 1, lo) < hi; }
   __device__ __forceinline__ int last(int a) const { return hi > lo ? hi - 1 : sink > a ? sink - 1 : -1; }
 };
 __device__ __forceinline__ TcNeed tc_need(const WinParams& P, const TcItem& w, const TcTile& q) {
@@ -223,7 +236,29 @@ __device__ __forceinline__ void tc_maximum(float mn, bool& first, float& m, floa
   }
 }
 
-template <int D, bool F16>
+// A row's sums outside tensor memory, and the maximum that they were taken against.
+struct TcSums {
+  uint4* o;  // four numbers, the next four 128 further
+  float* m;
+  // the sums, times f, to x
+  __device__ __forceinline__ void add(int i, float f, uint32_t* x) const {
+    const uint4 z = __ldcg(o + i * 128);
+    x[0] = __float_as_uint(fmaf(__uint_as_float(z.x), f, __uint_as_float(x[0])));
+    x[1] = __float_as_uint(fmaf(__uint_as_float(z.y), f, __uint_as_float(x[1])));
+    x[2] = __float_as_uint(fmaf(__uint_as_float(z.z), f, __uint_as_float(x[2])));
+    x[3] = __float_as_uint(fmaf(__uint_as_float(z.w), f, __uint_as_float(x[3])));
+  }
+};
+// what a number taken against the maximum `then` is worth against the one now
+__device__ __forceinline__ float tc_factor(float then, float now) { return then == -INFINITY ? 0.0f : ex2f(then - now); }
+template <int D>
+__device__ __forceinline__ TcSums tc_sums(const WinParams& P, int t, int row) {
+  float* base = P.sums + (int64_t)(2 * blockIdx.x + t) * 128 * (D + 1);
+  return TcSums{reinterpret_cast<uint4*>(base) + row, base + 128 * D + row};
+}
+
+// F16: weights and V in fp16; SUMS: some items have more than kTcSumSteps steps
+template <int D, bool F16, bool SUMS>
 __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_constant__ WinParams P,
                                                                   const __grid_constant__ TcMaps M) {
   using Sh = TcShape<D>;
@@ -420,7 +455,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
         const TcTile q[2] = {tc_tile(P, w, 0), tc_tile(P, w, 1)};
         const TcNeed need[2] = {tc_need(P, w, q[0]), tc_need(P, w, q[1])};
         const int last[2] = {need[0].last(a), need[1].last(a)};
-        bool seen_q[2] = {false, false}, seen_pv[2] = {false, false};
+        bool seen_q[2] = {false, false};
+        bool seen_pv[2] = {false, false};
+        if (SUMS) n_p[0] &= 1, n_p[1] &= 1;
         int vs = 0, v16 = 0;  // of the step before: V's stage and its groups of 16 keys
         // round st: outputs of step st - 1, then scores of step st
 #pragma unroll 1
@@ -431,8 +468,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             if (ok && st > a && need[t](st - 1)) {
-              outputs(t, vs, v16, seen_pv[t], st - 1 == last[t]);
-              seen_pv[t] = true;
+              const bool end = st - 1 == last[t] || (SUMS && (n_p[t] + 1) % kTcSumSteps == 0);
+              outputs(t, vs, v16, seen_pv[t], end);
+              seen_pv[t] = !SUMS || !end;
             }
             if (ok && st < b && need[t](st)) {
               scores(t, ks, seen_q[t], st == last[t]);
@@ -485,6 +523,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
       // it starts where nothing is larger.
       float m = mine ? -INFINITY : INFINITY, l = 0.0f;
       bool first = true;
+      // SUMS: the item's steps are counted from the barrier's parity on (0 or 1), here and where the products are issued
+      if (SUMS) n_s &= 1;
 #pragma unroll 1
       for (int st = w.a; st < w.b; ++st) {
         if (!need(st)) continue;
@@ -557,12 +597,38 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_ready[t]);
+        if constexpr (SUMS) {
+          if (n_s % kTcSumSteps == 0 && need.more(st)) {
+            if (!warp_wait(&o_full[t], n_o & 1, P.err)) {
+              ok = false;
+              break;
+            }
+            ++n_o;
+            tc_fence_after();
+            uint32_t o[D];
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) tmem_ld32(to + 32 * i, o + 32 * i);
+            tmem_wait_ld();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&o_free[t]);  // (the next sum may begin)
+            const TcSums sums = tc_sums<D>(P, t, row);
+            if (n_s > kTcSumSteps) {
+              const float f = tc_factor(*sums.m, m);
+#pragma unroll
+              for (int i = 0; i < D / 4; ++i) sums.add(i, f, o + 4 * i);
+            }
+            *sums.m = m;
+#pragma unroll
+            for (int i = 0; i < D / 4; ++i) __stcg(sums.o + i * 128, make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]));
+          }
+        }
       }
       if (!ok) break;
       // ---- outputs of the tile ----
       const int64_t tok = w.q_row + t * tt + r_tok;
       const int head = w.hk * P.group + r_head;
-      if (!w.part) l = win_sum(P, pos, l);
+      if (F16 && !w.part) l = win_sum(P, pos, l);
       const float inv = l > 0.0f ? P.v_scale / l : l;  // (a NaN stays one)
       if (!first) {
         if (!warp_wait(&o_full[t], n_o & 1, P.err)) break;
@@ -585,6 +651,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&o_free[t]);
+        }
+        if (SUMS && n_s > kTcSumSteps) {
+          const TcSums sums = tc_sums<D>(P, t, row);
+          const float f = tc_factor(*sums.m, m);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) sums.add(8 * i + j, f, o + 4 * j);
         }
         if (mine && w.part) {
           float4* dst = reinterpret_cast<float4*>(P.part_o + pr * D + 32 * i);
@@ -647,12 +719,18 @@ bool encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, 
 // a stride in bytes; an axis of length 1 takes any legal one
 cuuint64_t stride_bytes(int64_t values, int64_t extent) { return extent > 1 ? (cuuint64_t)values * 2 : 16; }
 
-template <int D, bool F16>
+template <int D, bool F16, bool SUMS>
 cudaError_t launch_tc(const WinParams& P, const TcMaps& M, int ctas, cudaStream_t s) {
-  auto* kern = window_tc_kernel<D, F16>;
+  auto* kern = window_tc_kernel<D, F16, SUMS>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TcShape<D>::kSmem);
   if (e != cudaSuccess) return e;
   return launch_kernel(true, kern, dim3(ctas), dim3(kTcThreads), TcShape<D>::kSmem, s, P, M);
+}
+
+template <int D>
+cudaError_t launch_dim(const WinParams& P, const TcMaps& M, int ctas, cudaStream_t s) {
+  if (P.long_sums) return P.dense ? launch_tc<D, true, true>(P, M, ctas, s) : launch_tc<D, false, true>(P, M, ctas, s);
+  return P.dense ? launch_tc<D, true, false>(P, M, ctas, s) : launch_tc<D, false, false>(P, M, ctas, s);
 }
 
 }  // namespace
@@ -673,8 +751,7 @@ int launch_window_tc(const WinParams& P, int head_dim, int64_t q_rows, int64_t k
     return (int)cudaErrorInvalidValue;
   const int ctas = P.n_items < n_sms ? P.n_items : n_sms;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (P.dense) return (int)(head_dim == 128 ? launch_tc<128, true>(P, M, ctas, s) : launch_tc<64, true>(P, M, ctas, s));
-  return (int)(head_dim == 128 ? launch_tc<128, false>(P, M, ctas, s) : launch_tc<64, false>(P, M, ctas, s));
+  return (int)(head_dim == 128 ? launch_dim<128>(P, M, ctas, s) : launch_dim<64>(P, M, ctas, s));
 }
 
 }  // namespace kvp

@@ -1,0 +1,61 @@
+"""Prompts behind a million tokens: a sum of outputs over so many keys is not cut off step by step."""
+import pytest
+import torch
+
+from heterogeneous_compressed_kv_gb300 import kvpool as K
+from tests.test_gpu_kv4 import gen, make
+from tests.test_gpu_kv4_prompts import rows64
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def inputs(n, T, hq, hk, d, g):
+    """Values of one sign, of another size in every dim: a sum that loses a little of each addition loses it everywhere."""
+    k = (0.3 * torch.randn((T, hk, d), device="cuda", generator=g)).to(BF)
+    v = torch.randn((T, hk, d), device="cuda", generator=g).abs_()
+    v = (v * (1 + torch.rand((hk, d), device="cuda", generator=g))).to(BF)
+    return torch.randn((n, hq, d), device="cuda", generator=g).to(BF), k, v
+
+
+def close(out, q, k, v, n, T):
+    """The mean relative error of the last 16 queries' outputs.  What the outputs' rounding (2^-8 of each at most, of no sign)
+    leaves of it in hq * d places of unlike sizes, 16 times the same ones: 2^-8 / sqrt(3) / sqrt(hq * d) = 2^-13.3 at 512,
+    three times that 2^-11.7; the weights' rounding, over a million of them, 2^-17.  A sum over 16,384 keys loses 2^-23 of
+    itself in each of 1,024 additions at most: 2^-13.  Together less than 2^-11."""
+    o = rows64(q[n - 16:], torch.arange(T - 16, T, device="cuda"), k, v, q.shape[2] ** -0.5)[0]
+    assert abs(float(((out[n - 16:].double() - o) / o).mean())) < 2.0 ** -11
+
+
+@pytest.mark.parametrize("n,T,hq,hk,d", [(4096, 1 << 20, 16, 4, 128), (1024, 1 << 20, 16, 4, 128), (8192, 600_001, 8, 8, 64), (600, 1 << 20, 12, 4, 128)])
+def test_prompts_over_the_4_bit_cache(n, T, hq, hk, d):
+    q, k, v = inputs(n, T, hq, hk, d, gen(n))
+    cache, table = make([T], 256, hk, d)
+    cache.store(k, v, table, [0], [T])
+    out = cache.attend(q, table, [n], [T])
+    k, v = cache.load(table, [0], [T], dtype=F32)
+    close(out, q, k.double(), v.double(), n, T)
+    assert K.window_check() == (K.OK, 0)
+
+
+@pytest.mark.parametrize("n,T,hq,hk,d,window", [(2500, 1 << 20, 16, 4, 128, 1 << 20), (2500, 1 << 20, 16, 4, 128, 500_000), (5000, 600_001, 8, 8, 64, 1 << 22)])
+def test_window_attention(n, T, hq, hk, d, window):
+    q, k, v = inputs(n, T, hq, hk, d, gen(n + 1))
+    want = torch.full((n + 1, hq), 7.0, device="cuda")
+    out = K.window_attend(q, k, v, [n], [0], [T], window, lse=want[:-1])
+    lo = max(0, T - 15 - window)  # (what the last 16 queries see differs by a few keys of many: they are cut alike)
+    if lo == 0:
+        close(out, q, k.double(), v.double(), n, T)
+    else:
+        q16 = q[n - 1:].double()
+        for h in range(hq):
+            kh, vh = k[T - window:, h // (hq // hk)].double(), v[T - window:, h // (hq // hk)].double()
+            p = torch.softmax(q16[:, h] @ kh.T * d ** -0.5, -1)
+            if h == 0:
+                err = []
+            err.append(((out[n - 1:, h].double() - p @ vh) / (p @ vh)).mean())
+        assert abs(float(torch.stack(err).mean())) < 2.0 ** -11
+    assert K.window_check() == (K.OK, 0)
+    # queries over themselves, and in a second call: the same bits
+    again = K.window_attend(q, k, v, [n], [0], [T], window)
+    assert torch.equal(again, out) and torch.equal(K.window_attend(q, k, v, [n], [0], [T], window, out=q), out)
