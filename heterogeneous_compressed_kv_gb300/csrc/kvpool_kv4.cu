@@ -11,7 +11,9 @@
 // Measured (bf16, 16 heads of 128): 6,656 tokens stored 13.4 us (69.9 MB, 0.77 of
 // the copy rate; a value takes 8 instructions, the integer pipe is the next bound),
 // read back 9.3 us (the cache and much of the output stay in L2); 65,536 tokens of
-// 8 heads read back 53.9 us, 6.4 TB/s (0.94); 32 tokens 3.1 and 2.6 us.
+// 8 heads read back 53.9 us, 6.4 TB/s (0.94); 32 tokens 3.9 and 2.4 us.  fp32, the
+// same 6,656 tokens: stored 48.5 us (124 MB, 0.38; a division for every value bounds
+// it), read back 32.0 (0.57).
 #include <algorithm>
 #include <cmath>
 #include <memory>

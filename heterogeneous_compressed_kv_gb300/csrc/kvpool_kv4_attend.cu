@@ -899,7 +899,9 @@ struct Space {
 // warp, a wave of unit CTAs 3.5 beside its rounds, shares 8.5 and up to 0.004 for
 // every row to merge.  (152 requests of 256 tokens, 4 key heads: 8.9 us as units,
 // 13.9 as shares; 32 of 4,096 18.7 and 22.2; 256 of 1 to 2,048 43.6 and 51; 32 of
-// 1 to 8,192 30.4 and 23.2; one of 16,384 55 and 12.4.)
+// 1 to 8,192 30.4 and 23.2; one of 16,384 55 and 12.4.)  The batches were of 16 bf16
+// heads on 4 of 128; with heads of 64, fp32, 16 heads on one and 4 on 4, ten batches
+// each, the rule's form is the quickest or within 5% of it, but for three (11 to 15%).
 int unit_warps(int64_t units, int64_t most_pairs, int64_t pairs, int64_t rows, int64_t shares, int n_sms, int64_t warps_per_sm) {
   auto round_us = [](double warps) { return 0.55 + 0.0625 * warps; };
   const double rounds = (double)pairs / (double)shares;

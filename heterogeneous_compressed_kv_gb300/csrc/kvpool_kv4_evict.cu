@@ -16,7 +16,9 @@
 // moving (75 MB each way, of which reads fetch whole 64-byte pieces for a token's
 // 8 and 16 bytes of scales and every other nibble of its values: about 240 MB in
 // all).  16 of 2,048 to 4,096 tokens x 4 heads cut to 1,024 15 us (11 and 4), one
-// round of latencies after the other.
+// round of latencies after the other.  One segment of 1,048,576 tokens cut to 16,384,
+// whose slices do not fit shared memory (every pass reads the weights again, 8 CTAs to
+// a head): 192 us with 1 head, 223 with 8.
 // Measured and not kept: eight histograms of the first pass, one to every eighth
 // lane (33.8 us where one took 32.2).
 #include <algorithm>

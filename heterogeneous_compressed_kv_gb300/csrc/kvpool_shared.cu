@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kFmaThreads) shared_fma_kernel(const __grid_co
 // 32-dim piece; O^T = V^T P^T with V's pairs along the keys from byte permutes.
 //
 // The outputs are fp32 and the cache is bf16, so a bf16 weight would be the one
-// rounding that shows (2^-9): each weight is taken apart into three bf16 numbers
+// rounding that shows (2^-8): each weight is taken apart into three bf16 numbers
 // whose sum holds its 24 bits, and O^T takes three products.  Scores are exact
 // products summed in fp32.  Each group of keys has products of its own that are
 // then added to the outputs with rounding: 30 requests of 64 heads x 64 behind

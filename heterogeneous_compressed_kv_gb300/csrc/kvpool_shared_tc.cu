@@ -10,7 +10,7 @@
 // the weights of this one are (two score tiles in tensor memory).
 //
 // The outputs are fp32 and the cache is bf16, so a bf16 weight would be the one
-// rounding that shows (2^-9): each weight is taken apart into three bf16 numbers
+// rounding that shows (2^-8): each weight is taken apart into three bf16 numbers
 // whose sum holds its 24 bits, and O += P V takes three products.  Two of the
 // weights' pieces lie over the scores, the third beside them.
 // Measured: 64 requests behind 8,192 entries of 16 heads x 128 24 us.  The first

@@ -12,7 +12,7 @@
 // the products of the other tile run, so the tensor core and the exponentials
 // (both about 1,024 cycles per 128 x 128 x 128 tile pair and side) overlap.
 //
-// The bf16 weights are the one rounding besides the output's own (2^-9 of a
+// The bf16 weights are the one rounding besides the output's own (2^-8 of a
 // weight, against sums of the unrounded ones).  A second piece of each, and a
 // second product with V, was measured: 32,768 tokens under a window of 4,096
 // 1,075 us against 770, 4 x 2,048 under 128 44.3 against 38.6.  Against 64 bits the

@@ -16,7 +16,7 @@
 // 8 x 8 transposition of bf16 pairs (movmatrix).  The 5th-generation products
 // (128 rows) would do the same with 8 to 128 times the padding.
 // A weight goes into the product as two bf16 numbers whose sum holds 16 of its
-// bits (off by 2^-18 of it at most): one alone would be off by 2^-9, as much as
+// bits (off by 2^-17 of it at most): one alone would be off by 2^-8, as much as
 // the output's own rounding.  The second product takes 0 to 4% of the time
 // (most with 16 rows to a key head).
 // fp32: FMAs; four lanes per key, each lane its own running softmax per row.

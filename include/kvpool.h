@@ -463,7 +463,7 @@ int kvpool_qk_norm_rope_axes(int32_t dtype, int32_t head_dim, int64_t n_tokens, 
  * statistics, sums and d_lse in fp32, one rounding of the outputs, and one of
  * the softmax weights before their product with the values -- to 16 bits where
  * a segment has at most 16 query rows per key head (h_q_len * group), to bf16
- * (2^-9 of each weight) in longer ones.  Callers that need a prompt's weights
+ * (2^-8 of each weight) in longer ones.  Callers that need a prompt's weights
  * unrounded pass fp32 tensors.  head_dim 64 or 128; window and n_sink >= 0.
  * d_workspace: kvpool_window_workspace bytes (16-byte aligned, may be NULL
  * when that is 0); calls that overlap on the GPU need one each.  It and d_lse
@@ -592,7 +592,7 @@ int kvpool_kv4_attend(const kvpool_kv4_args* args, int32_t n, const int64_t* h_q
  * all -- every one where there are no more than that.  What stays goes, in its
  * order, to places 0 .. min(h_k_len[i], keep) - 1 of row i of d_out_table, in
  * pages that are no row's of d_table (those stay as they were, so they may be
- * shared): its codes and scales are copied.  d_index: [n][kv_heads][keep], the
+ * shared) nor another row's of d_out_table: its codes and scales are copied.  d_index: [n][kv_heads][keep], the
  * places the tokens had, -1 behind the last.  d_out_weights: NULL, or the weights of
  * what stays (a zero's sign and a NaN's bits may change), zeros behind up to
  * out_weight_width (at least keep); it lies apart from d_weights (not between its
