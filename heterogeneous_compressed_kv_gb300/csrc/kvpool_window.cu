@@ -320,6 +320,14 @@ int64_t even_part(const kvpool_window_args* a, const WinParams& P, int n_sms) {
   return best;
 }
 
+// Keys of a bf16 single-token item at most: the tensor core cuts its sums off instead
+// of rounding them (about 2^-23 of the sum each time), and a warp's outputs are one
+// sum of two products for every 64 keys of the item.  160 requests behind 1,048,576
+// tokens, uncut: outputs 0.18% too small (values of one sign; error 2.4e-3 of their
+// norm, their rounding alone 1.69e-3), in parts of it 1.69e-3 (50.1 -> 39.6 ms: more
+// items, evener waves).
+constexpr int64_t kTokSumKeys = 65536;
+
 // Fill segments [i0, n) of one launch (at most kMaxWinSegs with queries);
 // returns the next segment.  A launch with few tiles cuts each tile's keys
 // into parts (merged by a second kernel) so that the GPU is filled.
@@ -364,7 +372,8 @@ int plan_launch(const kvpool_window_args* a, Form form, bool tc, const WinDense*
     WinSeg& S = P->segs[s];
     const int64_t st = (int64_t)((S.q_len + P->tile_tokens - 1) / P->tile_tokens) * Hk;
     const int64_t keys = tile_keys(a, S.q_len, S.k_len, P->tile_tokens);
-    const int64_t split = std::max<int64_t>(1, part > 0 ? (keys + part - 1) / part : std::min(fill, (keys + min_keys - 1) / min_keys));
+    int64_t split = std::max<int64_t>(1, part > 0 ? (keys + part - 1) / part : std::min(fill, (keys + min_keys - 1) / min_keys));
+    if (form == kFormTok && a->dtype == KVPOOL_BF16) split = std::max(split, (keys + kTokSumKeys - 1) / kTokSumKeys);
     S.n_split = (int32_t)split;
     S.item_base = (int32_t)items;
     S.part_base = (int32_t)slot;

@@ -59,3 +59,14 @@ def test_window_attention(n, T, hq, hk, d, window):
     # queries over themselves, and in a second call: the same bits
     again = K.window_attend(q, k, v, [n], [0], [T], window)
     assert torch.equal(again, out) and torch.equal(K.window_attend(q, k, v, [n], [0], [T], window, out=q), out)
+
+
+@pytest.mark.parametrize("n,T,hq,hk,d,q_len", [(160, 1 << 20, 16, 4, 128, 1), (200, 700_003, 8, 8, 64, 2)])
+def test_single_tokens_and_drafts(n, T, hq, hk, d, q_len):
+    """More requests than the GPU holds work items of, all behind the same rows: no request's keys are cut for the GPU's sake."""
+    q, k, v = inputs(n * q_len, T, hq, hk, d, gen(n))
+    out = K.window_attend(q, k, v, [q_len] * n, [0] * n, [T] * n, 1 << 20)
+    last = out.view(n, q_len, hq, d)[:16, -1].contiguous()  # (the last query of 16 requests sees all)
+    o = rows64(q.view(n, q_len, hq, d)[:16, -1], torch.full((16,), T - 1, device="cuda"), k.double(), v.double(), d ** -0.5)[0]
+    assert abs(float(((last.double() - o) / o).mean())) < 2.0 ** -11
+    assert K.window_check() == (K.OK, 0)
