@@ -886,6 +886,13 @@ int check_args(const kvpool_kv4_args* a, int32_t n, const int64_t* q_len, const 
 }
 
 constexpr int64_t kMinPairs = 2;  // of a share
+// The most pairs of a bf16 share or of a warp's part of a unit, and the rounds of
+// shares that this may take: the tensor core cuts its running sums of outputs off,
+// up to 2^-23 of the sum at every tile.  (One share to a warp left outputs 0.11% too
+// small for 1,500 requests behind the same 1,048,576 tokens, 8 heads on 2, and 0.033%
+// for 160 requests, 16 heads on 4; these 0.013% there.  15.8 -> 13.6 ms for those, 5.42
+// -> 5.48 for 64 of them.  fp32 outputs are summed with rounding.)
+constexpr int64_t kMaxPairs = 1024, kMaxRounds = 16;
 
 // Where a launch's workspace lies, in bytes from its start.
 struct Space {
@@ -902,13 +909,14 @@ struct Space {
 // 1 to 8,192 30.4 and 23.2; one of 16,384 55 and 12.4.)  The batches were of 16 bf16
 // heads on 4 of 128; with heads of 64, fp32, 16 heads on one and 4 on 4, ten batches
 // each, the rule's form is the quickest or within 5% of it, but for three (11 to 15%).
-int unit_warps(int64_t units, int64_t most_pairs, int64_t pairs, int64_t rows, int64_t shares, int n_sms, int64_t warps_per_sm) {
+int unit_warps(int64_t units, int64_t most_pairs, int64_t pairs, int64_t rows, int64_t shares, int n_sms, int64_t warps_per_sm, bool f32) {
   auto round_us = [](double warps) { return 0.55 + 0.0625 * warps; };
   const double rounds = (double)pairs / (double)shares;
   double best = 8.5 + rounds * round_us(std::min((double)warps_per_sm, (double)shares / n_sms) + 3.0) +
                 0.004 * (double)rows * std::min(1.0, rounds / 8);
   int answer = 0;
   for (int w = 4; w <= warps_per_sm; w *= 2) {
+    if (!f32 && most_pairs > w * kMaxPairs) continue;
     const double waves = (double)units * w / (double)(n_sms * warps_per_sm);
     const double round = round_us((double)std::min<int64_t>(warps_per_sm, (units + n_sms - 1) / n_sms * w));
     const double longest = (double)((most_pairs + w - 1) / w) * round + 3.5, mean = (double)pairs / (double)units / w * round + 3.5;
@@ -968,13 +976,16 @@ int32_t plan(const kvpool_kv4_args* a, bool prompts, int32_t i0, int32_t n, cons
     P->n_pairs += (int64_t)units * pairs;
   }
   P->n_units = (int32_t)n_units;
-  // a share to each warp that the GPU holds, of kMinPairs pairs at least
-  const int64_t warps = (int64_t)n_sms * kv4_warps(P->tile_rows / 8, a->dtype == KVPOOL_F32);
-  P->n_shares = (int32_t)std::max<int64_t>(1, std::min(warps, P->n_pairs / kMinPairs));
+  // a share to each warp that the GPU holds, of kMinPairs pairs at least, or several
+  const bool f32 = a->dtype == KVPOOL_F32;
+  const int64_t warps = (int64_t)n_sms * kv4_warps(P->tile_rows / 8, f32);
+  const int64_t shares = std::max<int64_t>(1, std::min(warps, P->n_pairs / kMinPairs));
+  const int64_t rounds = f32 ? 1 : std::min(kMaxRounds, std::max<int64_t>(1, (P->n_pairs / shares + kMaxPairs - 1) / kMaxPairs));
+  P->n_shares = (int32_t)(shares * rounds);
   P->share = P->n_pairs / P->n_shares;
   if (P->share > (1 << 30)) return -1;
   P->longer = (int32_t)(P->n_pairs % P->n_shares);
-  P->unit_warps = unit_warps(P->n_units, most, P->n_pairs, rows, P->n_shares, n_sms, warps / n_sms);
+  P->unit_warps = unit_warps(P->n_units, most, P->n_pairs, rows, shares, n_sms, warps / n_sms, f32);
   P->n_rows = (int32_t)rows;
   P->n_blocks = (int32_t)blocks;
   const int64_t parts = P->unit_warps == 0 && P->n_shares > 1 ? 2 * (int64_t)P->n_shares * P->tile_rows : 0;
@@ -1113,7 +1124,8 @@ cudaError_t launch_attend(const Kv4Params& P, int n_sms, cudaStream_t s) {
   }
   if (e != cudaSuccess) return e;
   // neighbouring shares go to different multiprocessors: few of them still use all
-  const int ctas = UNIT ? P.n_units : std::min(n_sms, P.n_shares);
+  const int held = n_sms * kv4_warps(NT, F32), rounds = (P.n_shares + held - 1) / held;
+  const int ctas = UNIT ? P.n_units : std::min(n_sms * rounds, P.n_shares);
   const int warps = UNIT ? P.unit_warps : (P.n_shares + ctas - 1) / ctas;
   return launch_kernel(true, kern, dim3(ctas), dim3(warps * 32), smem * warps, s, P);
 }

@@ -70,3 +70,18 @@ def test_single_tokens_and_drafts(n, T, hq, hk, d, q_len):
     o = rows64(q.view(n, q_len, hq, d)[:16, -1], torch.full((16,), T - 1, device="cuda"), k.double(), v.double(), d ** -0.5)[0]
     assert abs(float(((last.double() - o) / o).mean())) < 2.0 ** -11
     assert K.window_check() == (K.OK, 0)
+
+
+@pytest.mark.parametrize("n,T,hq,hk,d,q_len", [(500, 1 << 20, 16, 4, 128, 1), (1500, 1 << 20, 8, 2, 128, 1), (900, 700_003, 8, 4, 128, 2)])
+def test_single_tokens_over_the_4_bit_cache(n, T, hq, hk, d, q_len):
+    """Requests that share their pages, so many that every warp of the GPU has more than a unit's keys of them."""
+    q, k, v = inputs(n * q_len, T, hq, hk, d, gen(n))
+    cache, table = make([T], 256, hk, d)
+    cache.store(k, v, table, [0], [T])
+    out = cache.attend(q, table.expand(n, table.shape[1]), [q_len] * n, [T] * n)
+    k, v = cache.load(table, [0], [T], dtype=F32)
+    at = slice(n // 2, n // 2 + 16)
+    last = out.view(n, q_len, hq, d)[at, -1]
+    o = rows64(q.view(n, q_len, hq, d)[at, -1].contiguous(), torch.full((16,), T - 1, device="cuda"), k.double(), v.double(), d ** -0.5)[0]
+    assert abs(float(((last.double() - o) / o).mean())) < 2.0 ** -11
+    assert K.window_check() == (K.OK, 0)
