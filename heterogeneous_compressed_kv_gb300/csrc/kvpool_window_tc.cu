@@ -34,12 +34,11 @@
 // tokens, values of one sign; error 7.2e-3 of their norm, their rounding alone is
 // 1.7e-3).  So a sum in tensor memory is 16,384 keys long at most; a thread then adds
 // its row's to fp32 sums in the workspace (20 MB, L2), with rounding (1.68e-3
-// there).  Calls without such items run a kernel without this.  With it, heads of
-// 128 take 0 to 1.5% longer (16,384 queries of 16 heads on 4 behind 262,144 tokens
-// 23.3 ms, 23.7 without), heads of 64 5 to 9% (1.29 -> 1.36 ms for 4,096 queries
-// behind 65,536, of which the sums take a third; the loop's registers the rest).
-// Measured and not kept: vector atomics instead of reading the sums (D = 64 7.99
-// ms where this takes 7.71), the same in a function of its own (8.0).
+// there).  Calls without such items run a kernel without this.  With it, prompts over
+// the 4-bit cache take 1% longer with heads of 128 (65,536 queries of 16 heads on 4
+// behind their own 11.4 -> 11.5 ms) and 3% with 64, others no longer (16,384 queries,
+// 16 heads on 8 of 64, window 100,000 7.08 -> 7.03 ms).  Measured and not kept: vector
+// atomics instead of reading the sums, the same in a function of its own (12% there).
 //
 // Rows of K and V behind a segment, or between the first tokens and the window,
 // never count: scores are masked, and such V rows are not copied (boxes of 16
@@ -517,7 +516,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
       const TcTile q = tc_tile(P, w, t);
       const TcNeed need = tc_need(P, w, q);
       const int pos = q.p0 + r_tok;
-      const bool mine = r_tok < q.n && row < tt * P.group;
+      bool mine = r_tok < q.n && row < tt * P.group;
       // m: of the scaled scores (log2).  A row that is not the tile's has no say in when its warp rescales, since its scores
       // are of other segments' queries (or of outputs that are written over them meanwhile), or of what shared memory held:
       // it starts where nothing is larger.
@@ -525,107 +524,117 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
       bool first = true;
       // SUMS: the item's steps are counted from the barrier's parity on (0 or 1), here and where the products are issued
       if (SUMS) n_s &= 1;
+      // (two loops: what is done once in kTcSumSteps steps stays out of the inner one's registers)
+      int st = w.a;
 #pragma unroll 1
-      for (int st = w.a; st < w.b; ++st) {
-        if (!need(st)) continue;
-        const TcStep c = tc_step(w, st);
-        if (!warp_wait(&s_full[t], n_s & 1, P.err)) {
+      while (true) {
+#pragma unroll 1
+        for (; st < w.b; ++st) {
+          if (!need(st)) continue;
+          const TcStep c = tc_step(w, st);
+          if (!warp_wait(&s_full[t], n_s & 1, P.err)) {
+            ok = false;
+            break;
+          }
+          ++n_s;
+          tc_fence_after();
+          // a tile in the middle: every row of the query tile sees all of it
+          const bool whole = c.t0 + kTcKeys <= c.end &&
+                             (c.sink || (c.t0 + kTcKeys - 1 <= q.p0 &&
+                                         (c.t0 > q.p1 - P.window || c.t0 + kTcKeys <= P.n_sink)));
+          const int hi = min(c.sink ? c.end - 1 : pos, c.end - 1) - c.t0;  // last column that the row sees
+          const int lo = c.sink ? 0 : pos - P.window + 1 - c.t0;            // first of the window
+          const int sk = c.sink ? 0 : P.n_sink - c.t0;                     // columns before it: first tokens
+          uint64_t sum[2] = {0, 0};
+          if (whole) {
+            // the row's 128 scores in registers: maximum, weights
+            uint32_t x[128];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, x + 32 * i);
+            tmem_wait_ld();
+            tc_maximum<D>(tc_max64(x + 64, tc_max64(x, -INFINITY)) * scale, first, m, l, to);
+            const float base = m == -INFINITY ? 0.0f : m - kUp;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tc_weights32<F16>(x + 32 * i, scale, base, sum, ts + 16 * i);
+          } else {
+            // 32 scores at a time, twice (little code: it is run through cold);
+            // a quarter that none of the warp's rows sees is skipped
+            uint32_t x[32];
+            auto quarter = [&](int i) {  // false: nobody sees it
+              const int h = hi - 32 * i, g = lo - 32 * i, f = sk - 32 * i;
+              const uint32_t le = h < 0 ? 0u : h >= 31 ? ~0u : (2u << h) - 1u;
+              const uint32_t ge = g <= 0 ? ~0u : g >= 32 ? 0u : ~((1u << g) - 1u);
+              const uint32_t lt = f <= 0 ? 0u : f >= 32 ? ~0u : (1u << f) - 1u;
+              const uint32_t see = le & (ge | lt);
+              if (!__any_sync(0xffffffffu, see != 0u)) return false;
+              tmem_ld32(ts + 32 * i, x);
+              tmem_wait_ld();
+              if (!__all_sync(0xffffffffu, see == ~0u)) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  if (!((see >> j) & 1u)) x[j] = 0xFF800000u;  // -inf
+              }
+              return true;
+            };
+            float mx = -INFINITY;
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i)
+              if (quarter(i)) mx = tc_max32(x, mx);
+            tc_maximum<D>(mx * scale, first, m, l, to);
+            const float base = m == -INFINITY ? 0.0f : m - kUp;
+            // weights of columns 32 i .. 32 i + 31 go to words 16 i .. 16 i + 15: over scores that have been read by then
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+              if (quarter(i)) {
+                tc_weights32<F16>(x, scale, base, sum, ts + 16 * i);
+              } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) x[j] = 0u;
+                tmem_st16(ts + 16 * i, x);
+              }
+            }
+          }
+          const float2 sa = unpack2(sum[0]), sb = unpack2(sum[1]);
+          l += (sa.x + sa.y) + (sb.x + sb.y);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_ready[t]);
+          if (SUMS && n_s % kTcSumSteps == 0 && need.more(st)) break;
+        }
+        if (!SUMS || !ok || st >= w.b) break;
+        // a sum is full, and more steps follow: it joins the row's outside tensor memory
+        if (!warp_wait(&o_full[t], n_o & 1, P.err)) {
           ok = false;
           break;
         }
-        ++n_s;
+        ++n_o;
         tc_fence_after();
-        // a tile in the middle: every row of the query tile sees all of it
-        const bool whole = c.t0 + kTcKeys <= c.end &&
-                           (c.sink || (c.t0 + kTcKeys - 1 <= q.p0 &&
-                                       (c.t0 > q.p1 - P.window || c.t0 + kTcKeys <= P.n_sink)));
-        const int hi = min(c.sink ? c.end - 1 : pos, c.end - 1) - c.t0;  // last column that the row sees
-        const int lo = c.sink ? 0 : pos - P.window + 1 - c.t0;            // first of the window
-        const int sk = c.sink ? 0 : P.n_sink - c.t0;                     // columns before it: first tokens
-        uint64_t sum[2] = {0, 0};
-        if (whole) {
-          // the row's 128 scores in registers: maximum, weights
-          uint32_t x[128];
+        uint32_t o[D];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, x + 32 * i);
-          tmem_wait_ld();
-          tc_maximum<D>(tc_max64(x + 64, tc_max64(x, -INFINITY)) * scale, first, m, l, to);
-          const float base = m == -INFINITY ? 0.0f : m - kUp;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) tc_weights32<F16>(x + 32 * i, scale, base, sum, ts + 16 * i);
-        } else {
-          // 32 scores at a time, twice (little code: it is run through cold);
-          // a quarter that none of the warp's rows sees is skipped
-          uint32_t x[32];
-          auto quarter = [&](int i) {  // false: nobody sees it
-            const int h = hi - 32 * i, g = lo - 32 * i, f = sk - 32 * i;
-            const uint32_t le = h < 0 ? 0u : h >= 31 ? ~0u : (2u << h) - 1u;
-            const uint32_t ge = g <= 0 ? ~0u : g >= 32 ? 0u : ~((1u << g) - 1u);
-            const uint32_t lt = f <= 0 ? 0u : f >= 32 ? ~0u : (1u << f) - 1u;
-            const uint32_t see = le & (ge | lt);
-            if (!__any_sync(0xffffffffu, see != 0u)) return false;
-            tmem_ld32(ts + 32 * i, x);
-            tmem_wait_ld();
-            if (!__all_sync(0xffffffffu, see == ~0u)) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (!((see >> j) & 1u)) x[j] = 0xFF800000u;  // -inf
-            }
-            return true;
-          };
-          float mx = -INFINITY;
-#pragma unroll 1
-          for (int i = 0; i < 4; ++i)
-            if (quarter(i)) mx = tc_max32(x, mx);
-          tc_maximum<D>(mx * scale, first, m, l, to);
-          const float base = m == -INFINITY ? 0.0f : m - kUp;
-          // weights of columns 32 i .. 32 i + 31 go to words 16 i .. 16 i + 15: over scores that have been read by then
-#pragma unroll 1
-          for (int i = 0; i < 4; ++i) {
-            if (quarter(i)) {
-              tc_weights32<F16>(x, scale, base, sum, ts + 16 * i);
-            } else {
-#pragma unroll
-              for (int j = 0; j < 16; ++j) x[j] = 0u;
-              tmem_st16(ts + 16 * i, x);
-            }
-          }
-        }
-        const float2 sa = unpack2(sum[0]), sb = unpack2(sum[1]);
-        l += (sa.x + sa.y) + (sb.x + sb.y);
-        tmem_wait_st();
+        for (int i = 0; i < D / 32; ++i) tmem_ld32(to + 32 * i, o + 32 * i);
+        tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_ready[t]);
-        if constexpr (SUMS) {
-          if (n_s % kTcSumSteps == 0 && need.more(st)) {
-            if (!warp_wait(&o_full[t], n_o & 1, P.err)) {
-              ok = false;
-              break;
-            }
-            ++n_o;
-            tc_fence_after();
-            uint32_t o[D];
+        if (lane == 0) mbar_arrive(&o_free[t]);  // (the next sum may begin)
+        const TcSums sums = tc_sums<D>(P, t, row);
+        if (n_s > kTcSumSteps) {
+          const float f = tc_factor(*sums.m, m);
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) tmem_ld32(to + 32 * i, o + 32 * i);
-            tmem_wait_ld();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&o_free[t]);  // (the next sum may begin)
-            const TcSums sums = tc_sums<D>(P, t, row);
-            if (n_s > kTcSumSteps) {
-              const float f = tc_factor(*sums.m, m);
-#pragma unroll
-              for (int i = 0; i < D / 4; ++i) sums.add(i, f, o + 4 * i);
-            }
-            *sums.m = m;
-#pragma unroll
-            for (int i = 0; i < D / 4; ++i) __stcg(sums.o + i * 128, make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]));
-          }
+          for (int i = 0; i < D / 4; ++i) sums.add(i, f, o + 4 * i);
         }
+        *sums.m = m;
+#pragma unroll
+        for (int i = 0; i < D / 4; ++i) __stcg(sums.o + i * 128, make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]));
+        ++st;
       }
       if (!ok) break;
       // ---- outputs of the tile ----
+      if constexpr (SUMS) {  // worked out again, not kept over the loops (heads of 64 took 3% longer)
+        int own = row;
+        asm volatile("" : "+r"(own));
+        mine = r_tok < q.n && own < tt * P.group;
+      }
       const int64_t tok = w.q_row + t * tt + r_tok;
       const int head = w.hk * P.group + r_head;
       if (F16 && !w.part) l = win_sum(P, pos, l);
