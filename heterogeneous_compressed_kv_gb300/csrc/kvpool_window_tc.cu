@@ -630,7 +630,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) window_tc_kernel(const __grid_c
       }
       if (!ok) break;
       // ---- outputs of the tile ----
-      if constexpr (SUMS) {  // worked out again, not kept over the loops (heads of 64 took 3% longer)
+      if constexpr (SUMS || !F16) {  // worked out again, not kept over the loops (SUMS with heads of 64 took 3% longer, 4 x 2,048
+                                     // queries under a window of 128 2%; the other form is the quicker one with it kept)
         int own = row;
         asm volatile("" : "+r"(own));
         mine = r_tok < q.n && own < tt * P.group;
