@@ -174,3 +174,20 @@ def test_weights_of_prompts_that_are_read_back_have_eleven_bits(q_len, k_len, hq
     out = cache.attend(q, table, q_len, k_len, scale=scale, lse=lse)
     check(q, *held(cache, table, k_len), q_len, k_len, scale, out, lse, r=2.0 ** -11)
     ok()
+
+
+def test_a_segment_in_pieces_in_a_graph():
+    g, q_len, k_len = gen(9), [40, 5], [70000, 300]
+    cache, table = make(k_len, 64, 64, 128)
+    fill_in_parts(cache, table, k_len, g)
+    q = randn((45, 128, 128), BF, g)
+    out, space = torch.zeros_like(q), torch.empty(cache.workspace(q, table, q_len, k_len), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cache.attend(q, table, q_len, k_len, out=out, workspace=space)
+    for _ in range(2):
+        q.copy_(randn(q.shape, BF, g))
+        graph.replay()
+        assert torch.equal(out, cache.attend(q, table, q_len, k_len))
+    ok()

@@ -85,3 +85,46 @@ def test_single_tokens_over_the_4_bit_cache(n, T, hq, hk, d, q_len):
     o = rows64(q.view(n, q_len, hq, d)[at, -1].contiguous(), torch.full((16,), T - 1, device="cuda"), k.double(), v.double(), d ** -0.5)[0]
     assert abs(float(((last.double() - o) / o).mean())) < 2.0 ** -11
     assert K.window_check() == (K.OK, 0)
+
+
+def test_weights_where_shares_take_several_rounds():
+    n, T, h, d = 160, 1 << 20, 4, 128
+    q, k, v = inputs(n, T, h, h, d, gen(7))
+    cache, table = make([T], 256, h, d)
+    cache.store(k, v, table, [0], [T])
+    k = cache.load(table, [0], [T], dtype=F32)[0].double()
+    w, lse = torch.full((n, h, T), 3.0, device="cuda"), torch.empty((n, h), device="cuda")
+    cache.attend(q, table.expand(n, table.shape[1]), [1] * n, [T] * n, lse=lse, weights=w, decay=0.5)
+    for i in (0, 77, 159):
+        for j in range(h):
+            s = q[i, j].double() @ k[:, j].T * d ** -0.5
+            z = torch.logsumexp(s, -1)
+            assert float((lse[i, j] - z).abs()) < 1e-5  # (2^-17 of sums of |q k|, about 0.3)
+            # a half step of numbers from 1 to 2, and 2^-17 of weights that are below 1e-4
+            assert float((w[i, j].double() - 1.5 - torch.exp(s - z)).abs().max()) < 2.0 ** -23
+    assert K.window_check() == (K.OK, 0)
+
+
+@pytest.mark.parametrize("n,T,hk,group,d,window,sink", [
+    (600, 90_001, 2, 3, 64, 33_000, 17_001), (2500, 60_000, 1, 4, 128, 17_000, 40_000), (2500, 90_001, 4, 8, 64, 1 << 20, 130),
+    (300, 40_000, 4, 2, 128, 20_000, 3), (1, 90_001, 2, 8, 128, 70_000, 17_001), (3, 200_003, 1, 1, 64, 1 << 20, 0)])
+def test_first_tokens_before_long_windows(n, T, hk, group, d, window, sink):
+    """Steps over the first tokens and over the window in one item, against 64 bits: weights are rounded to 2^-8 of each,
+    outputs once more, scores are off by less than 1e-4 (2^-17 of sums of |q k| scale, below 10)."""
+    g = gen(T + n)
+    q, k, v = (torch.randn(s, device="cuda", generator=g).to(BF) for s in ((n, hk * group, d), (T, hk, d), (T, hk, d)))
+    lse = torch.empty((n, hk * group), device="cuda")
+    out = K.window_attend(q, k, v, [n], [0], [T], window, sink, lse=lse)
+    j = torch.unique(torch.tensor([0, n // 3, n // 2, n - 2, n - 1], device="cuda").clamp(0))
+    pos, t = T - n + j, torch.arange(T, device="cuda")
+    hidden = ~((t[None] <= pos[:, None]) & ((t[None] > pos[:, None] - window) | (t[None] < sink)))
+    for h in range(hk * group):
+        s = (q[j, h].double() @ k[:, h // group].double().T * d ** -0.5).masked_fill(hidden, -float("inf"))
+        z = torch.logsumexp(s, -1)
+        p, x = torch.exp(s - z[:, None]), v[:, h // group].double()
+        o = p @ x
+        assert bool(((out[j, h].double() - o).abs() <= 2.0 ** -8 * o.abs() + (2.0 ** -8 + 3e-4) * (p @ x.abs()) + 1e-9).all())
+        assert float((lse[j, h] - z).abs().max()) < 1e-4
+    over = q.clone()
+    assert torch.equal(K.window_attend(over, k, v, [n], [0], [T], window, sink, out=over), out)
+    assert K.window_check() == (K.OK, 0)
