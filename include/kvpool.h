@@ -463,7 +463,9 @@ int kvpool_qk_norm_rope_axes(int32_t dtype, int32_t head_dim, int64_t n_tokens, 
  * statistics, sums and d_lse in fp32, one rounding of the outputs, and one of
  * the softmax weights before their product with the values -- to 16 bits where
  * a segment has at most 16 query rows per key head (h_q_len * group), to bf16
- * (2^-8 of each weight) in longer ones.  Callers that need a prompt's weights
+ * (2^-8 of each weight) in longer ones.  The tensor core cuts its sums of bf16
+ * outputs off instead of rounding them: by less than 2^-12 of the sum of their terms'
+ * sizes, however many keys there are.  Callers that need a prompt's weights
  * unrounded pass fp32 tensors.  head_dim 64 or 128; window and n_sink >= 0.
  * d_workspace: kvpool_window_workspace bytes (16-byte aligned, may be NULL
  * when that is 0); calls that overlap on the GPU need one each.  It and d_lse
@@ -558,13 +560,15 @@ int kvpool_kv4_load(const kvpool_kv4* cache, int32_t dtype, const kvpool_heads* 
  * sums are fp32.  Products are of fp16 numbers: keys and values exactly, bf16
  * queries exactly and fp32 ones to 2^-22 of each (or 2^-39 of their row's largest,
  * where that is more), softmax weights to 2^-11 of each for bf16 outputs and to
- * 2^-22 for fp32 ones (or 2^-31 of their row's largest).  Long segments of bf16
+ * 2^-22 for fp32 ones (or 2^-31 of their row's largest); the tensor core's sums of
+ * bf16 outputs are cut off by less than 2^-12 of the sum of their terms' sizes.  Long segments of bf16
  * queries (more than 64 rows per key head, h_q_len * group) may be read back to
  * rows in the workspace and go through window attention's products; their roundings
  * are these as well.
  * d_workspace: kvpool_kv4_workspace bytes (16-byte aligned, may be NULL when that is
- * 0), 9 * 2^28 at most, and 4 for every query head of a row, with every token of its
- * segment, where d_weights is given; calls that overlap on the GPU need one each.  It, d_lse and d_weights lie
+ * 0), 9 * 2^28 at most, and 4 more for every query head of a row, with every token of
+ * its segment, where d_weights is given; calls that overlap on the GPU need one
+ * each.  It, d_lse and d_weights lie
  * apart from everything else.  The lengths are read during the call: a captured
  * call replays with the same ones.  Errors: INVALID_ARG, CUDA. */
 typedef struct kvpool_kv4_args {
@@ -592,7 +596,8 @@ int kvpool_kv4_attend(const kvpool_kv4_args* args, int32_t n, const int64_t* h_q
  * all -- every one where there are no more than that.  What stays goes, in its
  * order, to places 0 .. min(h_k_len[i], keep) - 1 of row i of d_out_table, in
  * pages that are no row's of d_table (those stay as they were, so they may be
- * shared) nor another row's of d_out_table: its codes and scales are copied.  d_index: [n][kv_heads][keep], the
+ * shared) nor another row's of d_out_table: its codes and scales are copied.
+ * d_index: [n][kv_heads][keep], the
  * places the tokens had, -1 behind the last.  d_out_weights: NULL, or the weights of
  * what stays (a zero's sign and a NaN's bits may change), zeros behind up to
  * out_weight_width (at least keep); it lies apart from d_weights (not between its
